@@ -22,6 +22,14 @@
  *   tv_select_topn    best children of the frontier) and its subtree
  *                     selection (the n best nodes of the candidate tree)
  *
+ * and the same pass over a paged KV cache, with ragged batches (a tree, a
+ * chunk of a prompt or a single token per sequence):
+ *
+ *   tv_page_map       block tables and slot maps from the sequences' lengths
+ *   tv_paged_append   new K/V rows into their slots
+ *   tv_attn_paged     attention of every new token over its sequence's pages
+ *   tv_commit_paged   the accepted branch's K/V rows to consecutive positions
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Every pointer argument is a DEVICE pointer owned by the caller, unless
@@ -68,7 +76,8 @@ typedef enum {
   TV_ERR_CUDA = 4,          /* a CUDA runtime call or kernel launch failed */
   TV_ERR_TIMEOUT = 5,       /* reserved: a bounded device wait gave up */
   TV_ERR_INVALID_TOKEN = 6, /* a draft token outside [0, V) */
-  TV_ERR_WORKSPACE = 7      /* workspace missing or smaller than required */
+  TV_ERR_WORKSPACE = 7,     /* workspace missing or smaller than required */
+  TV_ERR_NO_PAGES = 8       /* the page pool cannot serve the sequence */
 } tv_status;
 
 /* Maximum tree size (nodes per sequence) handled by every entry point. */
@@ -340,7 +349,8 @@ tv_status tv_debug_set_wait_limit(long long cycles);
  *                       (always 0 in the regular build), and clears the
  *                       record.  Units: 1 tree, 2 greedy, 3 sample,
  *                       4 expand, 5 attention, 6 commit, 7 expected,
- *                       8 top-n selection, 9 library.  Host call; it must not
+ *                       8 top-n selection, 9 library, 10 pages,
+ *                     11 paged attention.  Host call; it must not
  *                       overlap a launch of this library on the device.
  *                       TV_ERR_INVALID_ARG if site is NULL, TV_ERR_CUDA if
  *                       the device reports an error.
@@ -522,6 +532,161 @@ tv_status tv_select_topn(const int32_t* parent, const int32_t* token, const floa
                          const int32_t* n_nodes, int B, int M, int n, int32_t* out_parent,
                          int32_t* out_token, float* out_logscore, int32_t* out_src,
                          float* expected, int32_t* status, cudaStream_t stream);
+
+/*
+ * Paged KV cache
+ * --------------
+ * K and V live in pages of `page_size` token rows; page p holds, for every kv
+ * head h, rows r = 0 .. page_size - 1 of D elements at element offset
+ *   p * page_stride + h * head_stride + r * row_stride
+ * of k (and of v: both have the same strides).  Strides are in elements and
+ * let one call serve [pages, heads, rows, D] and [pages, rows, heads, D]
+ * caches, and K and V interleaved in one allocation.  The stride of a dimension of
+ * extent one is not read.  The D elements of a row are contiguous.
+ * Row `pos` of sequence b (its pos-th token, from 0) is row pos % page_size of
+ * page block_table[b, pos / page_size]; its slot is
+ * block_table[b, pos / page_size] * page_size + pos % page_size.
+ *
+ * New tokens come packed: q_start int32 [B + 1] holds the first token of each
+ * sequence (q_start[0] >= 0, ascending, q_start[B] <= T), so sequence b has n_b =
+ * q_start[b + 1] - q_start[b] new tokens (none is allowed) and token t of it
+ * sits at position kv_len[b] + t - q_start[b].  T is the length of the token
+ * arrays; tokens outside every sequence (rows behind the last one, as in a
+ * captured graph of fixed T) belong to nobody.  Where a q_start that descends gives a
+ * token to two sequences, either's slot or output row is written.
+ */
+typedef enum { TV_BF16 = 0, TV_FP16 = 1 } tv_dtype;
+
+typedef struct {
+  void* k;             /* device, 16-byte aligned */
+  void* v;             /* device, 16-byte aligned */
+  int64_t page_stride; /* elements; multiples of 8 */
+  int64_t head_stride;
+  int64_t row_stride;
+  int32_t num_pages;
+  int32_t page_size;   /* a power of two from 8 to 256 */
+  int32_t Hkv;
+  int32_t D;
+  int32_t dtype;       /* tv_dtype of k, v and of the tensors that go with them */
+} tv_paged_cache;
+
+/*
+ * tv_page_map -- bring block tables to the sequences' lengths and give every
+ * new token its slot (the paged form of "the caller writes the tree's keys to
+ * the cache at slots kv_len .. kv_len + N - 1").
+ *
+ *   q_start      int32 [B + 1]   new tokens per sequence, see above.
+ *   kv_len       int32 [B]       cached tokens of each sequence.
+ *   block_table  int32 [B, P] in/out, n_pages int32 [B] in/out: the pages each
+ *                sequence holds are block_table[b, 0 .. n_pages[b] - 1].
+ *   free_list    int32 [num_pages] in/out, n_free int32 [1] in/out: a stack of
+ *                the free pages, its top at free_list[n_free - 1].
+ *   slots        int64 [T] out   slot of each new token; -1 for tokens outside
+ *                every sequence and for sequences with a status.
+ *   status       int32 [B] out
+ * Sequence b is to hold target = ceil((kv_len[b] + n_b) / page_size) pages.
+ * Pages past the target go back first: pushed in (sequence, index) order.
+ * Then missing pages are popped, in (sequence, index) order, freed ones among
+ * them; a sequence gets its pages iff the sum of the missing pages up to and
+ * including its own is at most what is free, else it keeps what it held and
+ * reports TV_ERR_NO_PAGES.  So a step's call after a commit returns what
+ * the rejected branches held, and kv_len[b] = n_b = 0 releases a sequence.
+ * Table entries past n_pages[b] and list entries past n_free keep their values.
+ * status[b] = TV_ERR_INVALID_ARG for a malformed q_start, kv_len[b] < 0,
+ * n_pages[b] outside [0, P] or a target above P; the sequence then keeps its
+ * pages.  An n_free outside [0, num_pages], or one that would pass num_pages with the pages
+ * that come back, gives every sequence that status and changes nothing.
+ * Requires 0 <= B <= 4096, B * P and T below 2^31.  One launch for up to 8192 tokens,
+ * else two.  Sums are integers: the result depends on the inputs only.
+ */
+tv_status tv_page_map(const int32_t* q_start, const int32_t* kv_len, int B, int T, int P,
+                      int page_size, int num_pages, int32_t* block_table, int32_t* n_pages,
+                      int32_t* free_list, int32_t* n_free, int64_t* slots, int32_t* status,
+                      cudaStream_t stream);
+
+/*
+ * tv_paged_append -- write new K and V rows into their cache slots.
+ *   k, v    [T, Hkv, D] of the cache's type, 16-byte aligned; element strides
+ *           token_stride and head_stride (multiples of 8, the same for both;
+ *           views of a fused projection are fine), D contiguous.
+ *   slots   int64 [T]  from tv_page_map.  A negative slot writes nothing.
+ *           Slots must be distinct (of two tokens with one slot, either's
+ *           16-byte pieces may stay).
+ *   status  int32 [T] out, may be NULL: 0, or TV_ERR_INVALID_ARG for a slot
+ *           at or past num_pages * page_size (nothing is written).
+ * D a multiple of 8 up to 1024.  k and v must not overlap the cache.
+ */
+tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, int64_t head_stride,
+                          const int64_t* slots, int T, const tv_paged_cache* cache,
+                          int32_t* status, cudaStream_t stream);
+
+/*
+ * tv_attn_paged -- one attention layer for a ragged batch of new tokens over
+ * a paged cache: a decode token, a chunk of a prompt or a draft tree per
+ * sequence.  The new tokens' own K and V rows are in the cache already.
+ *
+ * For token t of sequence b (i = t - q_start[b]), query head h and its kv head
+ * h / (Hq / Hkv), over the visible key rows j of the sequence:
+ *   x_j = scale * q . k_j;  with softcap > 0: x_j = softcap * tanh(x_j / softcap)
+ *   with slopes: x_j -= slopes[h] * (pos(t) - pos(j))
+ *   out[t, h, :] = sum_j softmax_j(x) v_j;   lse[t, h] = log(sum_j exp(x_j))
+ * Causal (anc_mask NULL): pos is the row's index and rows j <= kv_len[b] + i
+ * are visible.  Tree (anc_mask given): prefix rows j < kv_len[b] and rows
+ * kv_len[b] + a for the set bits a of the token's mask are visible, and a
+ * node's pos is kv_len[b] + its depth (the number of its mask bits less one; masks are
+ * those of tv_tree_build).  With window > 0 only rows with pos(t) - pos(j) < window
+ * are visible.  A token that sees nothing gets out = 0, lse = -inf.
+ *
+ *   q           [T, Hq, D] of the cache's type, 16-byte aligned; element strides
+ *               q_token_stride, q_head_stride (multiples of 8), D contiguous.
+ *   cache       host pointer; read before the call returns.
+ *   block_table int32 [B, P]; q_start int32 [B + 1]; kv_len int32 [B].
+ *   anc_mask    uint64 [T, W], W = ceil(max_q / 64), or NULL.
+ *   slopes      float [Hq], or NULL.
+ *   max_q       the largest n_b, as the host knows it.  It picks the kernel; larger
+ *               chunks are served too, only more slowly (with anc_mask up to 64 W
+ *               tokens).
+ *   scale       0 selects 1/sqrt(D).
+ *   out         [T, Hq, D], contiguous, 16-byte aligned; lse float [T, Hq], may be NULL.
+ *               Rows of tokens outside every sequence are left as they were.
+ *   status      int32 [B] out, may be NULL: 0, or TV_ERR_INVALID_ARG for
+ *               - a malformed q_start (the sequence's rows are left as they were);
+ *               - kv_len[b] < 0, kv_len[b] + n_b > P * page_size, or with anc_mask
+ *                 n_b > 64 W (its rows are zeroed, lse too);
+ *               - a page id outside [0, num_pages) among the sequence's pages that
+ *                 the window reaches (its keys count as hidden).
+ *   workspace   tv_attn_paged_workspace_size() bytes, 256-byte aligned, any
+ *               contents; calls that share one must not run concurrently.
+ * Cache rows that no token sees may hold anything, NaN included; a row of V seen
+ * by one token of a chunk and not by another must be finite.
+ * Supported: D 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 128, B <= 4096, T * Hq and
+ * B * P below 2^31; max_q <= TV_MAX_NODES with anc_mask.
+ */
+size_t tv_attn_paged_workspace_size(int max_q, int Hq, int Hkv, int D);
+tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                        const tv_paged_cache* cache, const int32_t* block_table,
+                        const int32_t* q_start, const int32_t* kv_len, const uint64_t* anc_mask,
+                        const float* slopes, int B, int T, int P, int Hq, int max_q, float scale,
+                        float softcap, int window, void* out, float* lse, int32_t* status,
+                        void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * tv_commit_paged -- tv_commit_path over a paged cache: the accepted branch's
+ * K and V rows move to positions kv_len[b] + 1 .. kv_len[b] + accept_len[b] of
+ * their sequence (pages may be any, source and destination may share one).
+ *   block_table int32 [B, P]; the other arguments as for tv_commit_path.
+ *   status      int32 [B] out: as tv_commit_path's (kv_len[b] + path[b, a] against
+ *               P * page_size), and TV_ERR_INVALID_ARG for a page id
+ *               outside [0, num_pages) among the rows that move; the sequence's cache is
+ *               then left as it was and new_kv_len[b] = kv_len[b].
+ * The pages past the new length stay with the sequence until tv_page_map.
+ * Pages of the moved rows must belong to one sequence only.  D a multiple of 8 up
+ * to 1024.
+ */
+tv_status tv_commit_paged(const tv_paged_cache* cache, const int32_t* block_table,
+                          const int32_t* kv_len, const int32_t* path, const int32_t* accept_len,
+                          int B, int N, int P, int32_t* new_kv_len, int32_t* status,
+                          cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,6 +19,9 @@ TV_ERR_CUDA = 4
 TV_ERR_TIMEOUT = 5
 TV_ERR_INVALID_TOKEN = 6
 TV_ERR_WORKSPACE = 7
+TV_ERR_NO_PAGES = 8
+TV_BF16 = 0
+TV_FP16 = 1
 TV_MAX_NODES = 512
 TV_WAIT_LIMIT_DEFAULT = -1
 
@@ -46,6 +49,15 @@ _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _U64 = ctypes.c_uint64
+_I64 = ctypes.c_int64
+
+
+class PagedCache(ctypes.Structure):
+    """tv_paged_cache."""
+    _fields_ = [("k", _P), ("v", _P), ("page_stride", _I64), ("head_stride", _I64),
+                ("row_stride", _I64), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
 
 _SIGS = {
     "tv_status_string": (ctypes.c_char_p, [_I]),
@@ -75,6 +87,12 @@ _SIGS = {
     "tv_debug_check_selftest": (_I, [_P, _I, _I, _P]),
     "tv_attn_verify_tree": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _P,
                                  _P, _P, _SZ, _P]),
+    "tv_page_map": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
+    "tv_paged_append": (_I, [_P, _P, _I64, _I64, _P, _I, _P, _P, _P]),
+    "tv_attn_paged_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "tv_attn_paged": (_I, [_P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _I,
+                           _P, _P, _P, _P, _SZ, _P]),
+    "tv_commit_paged": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
 }
 
 for _name, (_res, _args) in _SIGS.items():

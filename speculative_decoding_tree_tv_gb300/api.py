@@ -1,15 +1,17 @@
 """Torch-tensor front end of libtreeverify (argument marshalling only)."""
 from __future__ import annotations
 
+import ctypes
 from typing import Callable, Optional
 
 import torch
 
-from ._lib import TV_MAX_NODES, check, lib
+from ._lib import TV_BF16, TV_FP16, TV_MAX_NODES, PagedCache, check, lib
 
 __all__ = ["tree_build", "attn_verify", "accept_greedy", "accept_sample", "expand_gated",
            "expand_tree", "commit_path", "expected_accept", "build_spine_tree", "spine_ratio_update", "workspace", "attn_workspace_size", "attn_plan", "greedy_workspace_size",
-           "sample_workspace_size", "expand_workspace_size"]
+           "sample_workspace_size", "expand_workspace_size", "page_map", "paged_append", "attn_paged",
+           "commit_paged", "attn_paged_workspace_size"]
 
 _workspaces: dict = {}
 
@@ -56,7 +58,6 @@ def attn_workspace_size(B, N, Hq, Hkv, D, Lcap) -> int:
 
 def attn_plan(B, N, Hq, Hkv, D, Lcap) -> dict:
     """The launch plan tv_attn_verify takes for this shape on the current device."""
-    import ctypes
     info = (ctypes.c_int32 * 4)()
     check("tv_attn_plan", lib.tv_attn_plan(B, N, Hq, Hkv, D, Lcap, info))
     return {"rows_per_cta": info[0], "node_tiles": info[1], "splits": info[2], "ctas": info[3]}
@@ -459,3 +460,200 @@ def expand_tree(draft_rows: Callable, root_key, child_key: Callable, topk: int, 
         layer += 1
     return dict(parent=par[:n].cpu(), token=tok[:n].cpu(), logscore=ls[:n].cpu(), n=n,
                 layers=layer - 1)
+
+
+# ---------------------------------------------------------------------------
+# Paged KV cache
+# ---------------------------------------------------------------------------
+_CACHE_DTYPES = {torch.bfloat16: TV_BF16, torch.float16: TV_FP16}
+
+
+def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> PagedCache:
+    """tv_paged_cache of k_pages, v_pages [num_pages, Hkv, page_size, D]: any
+    strides with D contiguous, the same for both (a [num_pages, page_size, Hkv, D]
+    cache goes in as its .transpose(1, 2))."""
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    dtype = _CACHE_DTYPES.get(k_pages.dtype)
+    if dtype is None:
+        raise TypeError(f"k_pages must be torch.bfloat16 or torch.float16, got {k_pages.dtype}")
+    if v_pages.dtype != k_pages.dtype:
+        raise TypeError(f"v_pages must be {k_pages.dtype}, got {v_pages.dtype}")
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must both be [num_pages, Hkv, page_size, D]")
+    strides = k_pages.stride()
+    if strides != v_pages.stride():
+        raise ValueError("k_pages and v_pages must have the same strides")
+    if strides[3] != 1:
+        raise ValueError("the last dimension of k_pages and v_pages must be contiguous")
+    if v_pages.device != k_pages.device:
+        raise ValueError(f"v_pages is on {v_pages.device}, expected {k_pages.device}")
+    n, Hkv, page, D = k_pages.shape
+    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), strides[0], strides[1], strides[2], n,
+                      page, Hkv, D, dtype)
+
+
+def _need_rows(t: torch.Tensor, name: str, dtype, shape, device):
+    """A [tokens, heads, D] tensor of the cache's type, any token and head stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(2) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _call(fn: str, dev: torch.device, *args) -> None:
+    """Call the library's `fn` on dev's current stream, with dev the current device."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        check(fn, getattr(lib, fn)(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn, getattr(lib, fn)(*args, _stream(dev)))
+
+
+def attn_paged_workspace_size(max_q, Hq, Hkv, D) -> int:
+    return int(lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D))
+
+
+def page_map(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor,
+             n_pages: torch.Tensor, free_list: torch.Tensor, n_free: torch.Tensor, page_size: int,
+             tokens: int, slots: Optional[torch.Tensor] = None,
+             status: Optional[torch.Tensor] = None):
+    """Bring the block tables to the sequences' lengths, in place: pages past
+    ceil((kv_len + new) / page_size) go back to the free list, missing ones are
+    taken from its end.  q_start int32 [B+1] (first new token of each
+    sequence); kv_len, n_pages int32 [B]; block_table int32 [B, P]; free_list
+    int32 [num_pages]; n_free int32 [1]; tokens = length of the slot map.
+    Returns (slots int64 [tokens], status int32 [B])."""
+    _need(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have shape [B, P]")
+    B, P = block_table.shape
+    dev = block_table.device
+    _need(q_start, "q_start", torch.int32, (B + 1,), dev)
+    _need(kv_len, "kv_len", torch.int32, (B,), dev)
+    _need(n_pages, "n_pages", torch.int32, (B,), dev)
+    _need(free_list, "free_list", torch.int32, (free_list.numel(),), dev)
+    _need(n_free, "n_free", torch.int32, (1,), dev)
+    slots = torch.empty(tokens, dtype=torch.int64, device=dev) if slots is None else slots
+    _need(slots, "slots", torch.int64, (tokens,), dev)
+    status = torch.empty(B, dtype=torch.int32, device=dev) if status is None else status
+    _need(status, "status", torch.int32, (B,), dev)
+    _call(
+        "tv_page_map", dev, q_start.data_ptr(), kv_len.data_ptr(), B, int(tokens), P, int(page_size),
+        free_list.numel(), block_table.data_ptr(), n_pages.data_ptr(), free_list.data_ptr(), n_free.data_ptr(),
+        slots.data_ptr(), status.data_ptr())
+    return slots, status
+
+
+def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor,
+                 v_pages: torch.Tensor, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Write k, v [T, Hkv, D] (views of a fused projection are fine) into the
+    cache rows slots int64 [T] name; negative slots write nothing.  k_pages,
+    v_pages [num_pages, Hkv, page_size, D] bf16 or fp16.  Returns status int32 [T]."""
+    cache = _cache(k_pages, v_pages)
+    dev = k_pages.device
+    _need(slots, "slots", torch.int64, None, dev)
+    if slots.dim() != 1:
+        raise ValueError("slots must have shape [T]")
+    T = slots.numel()
+    shape = (T, cache.Hkv, cache.D)
+    _need_rows(k, "k", k_pages.dtype, shape, dev)
+    _need_rows(v, "v", k_pages.dtype, shape, dev)
+    if k.stride() != v.stride():
+        raise ValueError("k and v must have the same strides")
+    status = torch.empty(T, dtype=torch.int32, device=dev) if status is None else status
+    _need(status, "status", torch.int32, (T,), dev)
+    _call(
+        "tv_paged_append", dev, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
+        slots.data_ptr(), T, ctypes.addressof(cache), status.data_ptr())
+    return status
+
+
+def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+               block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor, max_q: int,
+               anc_mask: Optional[torch.Tensor] = None, scale: float = 0.0, softcap: float = 0.0,
+               window: int = 0, slopes: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None, want_lse: bool = True,
+               ws: Optional[torch.Tensor] = None):
+    """Attention of packed new tokens q [T, Hq, D] over their sequences' pages:
+    causal, or a draft tree where anc_mask int64 [T, W] is given; one token a
+    sequence is a decode step.  k_pages, v_pages [num_pages, Hkv, page_size, D] (bf16
+    or fp16, like q); block_table int32 [B, P]; q_start int32 [B+1]; kv_len
+    int32 [B]; max_q = the largest chunk.  softcap caps the scores by a tanh,
+    slopes float32 [Hq] subtracts slope * distance, window hides keys that far
+    back.  Returns (out [T, Hq, D], lse float32 [T, Hq], status int32 [B])."""
+    cache = _cache(k_pages, v_pages)
+    dev = k_pages.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [T, Hq, D]")
+    T, Hq, D = q.shape
+    _need_rows(q, "q", k_pages.dtype, (T, Hq, cache.D), dev)
+    _need(block_table, "block_table", torch.int32, None, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have shape [B, P]")
+    B, P = block_table.shape
+    _need(q_start, "q_start", torch.int32, (B + 1,), dev)
+    _need(kv_len, "kv_len", torch.int32, (B,), dev)
+    if anc_mask is not None:
+        _need(anc_mask, "anc_mask", torch.int64, None, dev)
+        W = (int(max_q) + 63) // 64
+        if anc_mask.numel() != T * W:
+            raise ValueError(f"anc_mask must have shape {(T, W)}, got {tuple(anc_mask.shape)}")
+    if slopes is not None:
+        _need(slopes, "slopes", torch.float32, (Hq,), dev)
+    out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
+    _need(out, "out", q.dtype, (T, Hq, D), dev)
+    if want_lse and lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, Hq), dev)
+    status = torch.empty(B, dtype=torch.int32, device=dev) if status is None else status
+    _need(status, "status", torch.int32, (B,), dev)
+    if ws is None:  # from torch's allocator: ordered by stream, and a captured graph's own
+        ws = torch.empty(attn_paged_workspace_size(int(max_q), Hq, cache.Hkv, D), dtype=torch.uint8,
+                         device=dev)
+    _call(
+        "tv_attn_paged", dev, q.data_ptr(), q.stride(0), q.stride(1), ctypes.addressof(cache),
+        block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), _ptr(anc_mask), _ptr(slopes),
+        B, T, P, Hq, int(max_q), float(scale), float(softcap), int(window), out.data_ptr(), _ptr(lse), status.data_ptr(),
+        ws.data_ptr(), ws.numel())
+    return out, lse, status
+
+
+def commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+                 kv_len: torch.Tensor, path: torch.Tensor, accept_len: torch.Tensor,
+                 new_kv_len: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None):
+    """Move each sequence's accepted branch to consecutive positions of its
+    pages, in place.  k_pages, v_pages [num_pages, Hkv, page_size, D]; block_table
+    int32 [B, P]; kv_len, accept_len int32 [B]; path int32 [B, N].
+    Returns (new_kv_len int32 [B], status int32 [B])."""
+    cache = _cache(k_pages, v_pages)
+    dev = k_pages.device
+    _need(block_table, "block_table", torch.int32, None, dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have shape [B, P]")
+    B, P = block_table.shape
+    _need(path, "path", torch.int32, None, dev)
+    if path.dim() != 2 or path.shape[0] != B:
+        raise ValueError(f"path must have shape [B, N] with B = {B}")
+    _need(kv_len, "kv_len", torch.int32, (B,), dev)
+    _need(accept_len, "accept_len", torch.int32, (B,), dev)
+    new_kv_len = torch.empty(B, dtype=torch.int32, device=dev) if new_kv_len is None else new_kv_len
+    _need(new_kv_len, "new_kv_len", torch.int32, (B,), dev)
+    status = torch.empty(B, dtype=torch.int32, device=dev) if status is None else status
+    _need(status, "status", torch.int32, (B,), dev)
+    _call(
+        "tv_commit_paged", dev, ctypes.addressof(cache), block_table.data_ptr(), kv_len.data_ptr(),
+        path.data_ptr(), accept_len.data_ptr(), B, path.shape[1], P, new_kv_len.data_ptr(), status.data_ptr())
+    return new_kv_len, status

@@ -56,6 +56,7 @@ extern "C" const char* tv_status_string(tv_status s) {
     case TV_ERR_TIMEOUT: return "TV_ERR_TIMEOUT";
     case TV_ERR_INVALID_TOKEN: return "TV_ERR_INVALID_TOKEN";
     case TV_ERR_WORKSPACE: return "TV_ERR_WORKSPACE";
+    case TV_ERR_NO_PAGES: return "TV_ERR_NO_PAGES";
   }
   return "TV_ERR_UNKNOWN";
 }

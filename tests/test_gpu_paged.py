@@ -1,0 +1,600 @@
+"""The paged KV cache on the GPU: page map, append, attention and commit against
+plain implementations in integers and 64-bit floats, their refusals, and a
+verify step of all of them together."""
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from _gpu_util import i32, np_
+from _paged_util import DTYPES, attn_ref, check_attn, make, page_map_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tv():
+    import speculative_decoding_tree_tv_gb300 as m
+    return m
+
+
+def starts(new):
+    return [0] + list(np.cumsum(new))
+
+
+# ------------------------------------------------------------------ page map
+class Pool:
+    """Tables of a serving loop, on the GPU and as python lists."""
+
+    def __init__(self, seed, B, P, pool, page):
+        rng = random.Random(seed)
+        self.page = page
+        self.free = list(range(pool))
+        rng.shuffle(self.free)
+        self.table, self.held, self.n_free = [[-1] * P for _ in range(B)], [0] * B, pool
+        self.gpu = dict(table=i32(self.table), held=i32(self.held), free=i32(self.free), n_free=i32([pool]))
+
+    def step(self, tv, q_start, kv_len, T):
+        g = self.gpu
+        slots, status = tv.page_map(i32(q_start), i32(kv_len), g["table"], g["held"], g["free"], g["n_free"],
+                                    self.page, T)
+        ref_slots, ref_status, self.n_free = page_map_ref(q_start, kv_len, self.table, self.held, self.free,
+                                                          self.n_free, self.page, T)
+        assert np_(status).tolist() == ref_status
+        owners = [1] * T
+        if sorted(q_start) != list(q_start):
+            owners = [sum(a <= t < b for a, b in zip(q_start, q_start[1:])) for t in range(T)]
+        got = np_(slots).tolist()  # a descending q_start gives some tokens two owners: either's slot
+        assert [s for s, n in zip(got, owners) if n < 2] == [s for s, n in zip(ref_slots, owners) if n < 2]
+        assert int(g["n_free"]) == self.n_free
+        assert np_(g["held"]).tolist() == self.held
+        assert np_(g["table"]).tolist() == self.table
+        assert np_(g["free"]).tolist() == self.free
+        return ref_status
+
+
+@pytest.mark.parametrize("B,P,page,scarce", [(1, 1, 8, 1.0), (1, 40, 16, 1.0), (7, 12, 8, 0.5), (64, 20, 16, 0.6),
+                                             (300, 9, 32, 0.9), (600, 5, 256, 0.4), (1030, 3, 64, 0.7),
+                                             (4096, 4, 8, 0.5)])
+def test_page_map_follows_the_plain_one(tv, B, P, page, scarce):
+    rng = random.Random(B)
+    pool = Pool(B, B, P, max(1, int(B * P * scarce)), page)
+    seen = set()
+    for it in range(6):
+        kv = [rng.randint(0, P * page) for _ in range(B)]
+        most = [P * page, 3, 40, 1, page, 0][it]
+        new = [rng.randint(0, min(most, P * page - L)) for L in kv]
+        if B > 1000 and it == 0:
+            new = [min(n, 60) for n in new]
+        seen |= set(pool.step(tv, starts(new), kv, sum(new) + rng.choice([0, 5])))
+    assert 0 in seen
+    pool.step(tv, [0] * (B + 1), [0] * B, 0)
+    assert pool.n_free == len(pool.free)
+
+
+def test_page_map_many_tokens(tv):
+    """More tokens than one cluster maps (the wide slot launch)."""
+    B, P, page = 40, 70, 16
+    pool = Pool(3, B, P, B * P - 100, page)
+    rng = random.Random(5)
+    new = [rng.randint(0, P * page) for _ in range(B)]
+    st = pool.step(tv, starts(new), [0] * B, sum(new) + 1500)
+    assert set(st) <= {0, 8}
+
+
+def test_page_map_bad_sequences(tv):
+    """Malformed ranges, lengths and page counts are reported and left alone; their
+    neighbours are served."""
+    B, P, page = 6, 4, 16
+    pool = Pool(1, B, P, 30, page)
+    pool.step(tv, starts([20] * B), [0] * B, 120)
+    pool.step(tv, starts([10, 10, 0, 10, 10, 10]), [20, -3, 20, 100, 20, 60], 50)   # negative, above P pages
+    pool.step(tv, [0, 5, 10, 8, 20, 30, 70], [20] * B, 60)      # descending; past T
+    pool.step(tv, [-4, 5, 10, 12, 20, 30, 40], [20] * B, 60)    # negative start
+    pool.held[2] = -1
+    pool.held[3] = P + 1
+    pool.gpu["held"].copy_(i32(pool.held))
+    pool.step(tv, starts([5] * B), [20] * B, 30)
+
+
+@pytest.mark.parametrize("n_free", [-1, 31, 29])
+def test_page_map_bad_free_count_changes_nothing(tv, n_free):
+    B, P, page = 3, 4, 16
+    pool = Pool(1, B, P, 30, page)
+    pool.step(tv, starts([40] * B), [0] * B, 120)  # 9 pages out, 21 free
+    pool.n_free = n_free                           # 29 + the 9 that would come back pass 30
+    pool.gpu["n_free"].fill_(n_free)
+    assert pool.step(tv, [0] * (B + 1), [0] * B, 4) == [1] * B
+
+
+def test_page_map_empty_batch(tv):
+    z = torch.zeros(0, dtype=torch.int32, device="cuda:0")
+    slots, status = tv.page_map(i32([0]), z, z.reshape(0, 4), z, i32([0, 1]), i32([2]), 16, 7)
+    assert np_(slots).tolist() == [-1] * 7 and status.numel() == 0
+
+
+def test_page_map_in_a_graph(tv):
+    """A captured step replayed on new lengths in the same buffers."""
+    B, P, page, T = 5, 8, 16, 64
+    pool = Pool(2, B, P, 30, page)
+    g = pool.gpu
+    q, kv = i32([0] * (B + 1)), i32([0] * B)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        tv.page_map(q, kv, g["table"], g["held"], g["free"], g["n_free"], page, T)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        slots, status = tv.page_map(q, kv, g["table"], g["held"], g["free"], g["n_free"], page, T)
+    rng = random.Random(9)
+    for _ in range(4):
+        kv_h = [rng.randint(0, 90) for _ in range(B)]
+        q_h = starts([rng.randint(0, 12) for _ in range(B)])
+        q.copy_(i32(q_h))
+        kv.copy_(i32(kv_h))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        ref, st, pool.n_free = page_map_ref(q_h, kv_h, pool.table, pool.held, pool.free, pool.n_free, page, T)
+        assert np_(slots).tolist() == ref and np_(status).tolist() == st
+        assert np_(g["table"]).tolist() == pool.table and int(g["n_free"]) == pool.n_free
+
+
+# -------------------------------------------------------------------- append
+@pytest.mark.parametrize("T,Hkv,D,page,dtype,layout", [
+    (1, 1, 64, 8, "bf16", "heads"), (33, 8, 128, 16, "fp16", "rows"), (700, 3, 64, 32, "bf16", "both"),
+    (5, 5, 40, 16, "bf16", "heads"), (3000, 8, 128, 64, "bf16", "rows"), (9, 2, 1024, 256, "fp16", "heads")])
+@pytest.mark.parametrize("fused", [False, True])
+def test_append_writes_the_slots_and_nothing_else(tv, T, Hkv, D, page, dtype, layout, fused):
+    dt, g = DTYPES[dtype], torch.Generator().manual_seed(T)
+    pool = -(-T // page) + 3
+    kv = torch.randn(2, pool, Hkv, page, D, generator=g).to(dt).to("cuda:0")
+    if layout == "heads":
+        k, v = kv[0], kv[1]
+    elif layout == "rows":
+        kv = kv.view(2, pool, page, Hkv, D)
+        k, v = kv[0].transpose(1, 2), kv[1].transpose(1, 2)
+    else:
+        kv = kv.view(pool, 2, Hkv, page, D)
+        k, v = kv[:, 0], kv[:, 1]
+    x = torch.randn(T, 3 * Hkv if fused else 2 * Hkv, D, generator=g).to(dt).to("cuda:0")
+    nk, nv = x[:, -2 * Hkv:-Hkv], x[:, -Hkv:]
+    if not fused:
+        nk, nv = nk.contiguous(), nv.contiguous()
+    slots = torch.randperm(pool * page, generator=g)[:T]
+    bad = torch.rand(T, generator=g)
+    slots[bad < 0.1] = -1
+    slots[bad > 0.95] = pool * page + (slots[bad > 0.95] % 3) * 2**33
+    ek, ev = k.clone(), v.clone()
+    for t, s in enumerate(slots.tolist()):
+        if 0 <= s < pool * page:
+            ek[s // page, :, s % page] = nk[t]
+            ev[s // page, :, s % page] = nv[t]
+    status = tv.paged_append(nk, nv, slots.to("cuda:0"), k, v)
+    torch.cuda.synchronize()
+    assert torch.equal(k, ek) and torch.equal(v, ev)
+    assert np_(status).tolist() == [1 if s >= pool * page else 0 for s in slots.tolist()]
+
+
+def test_append_without_tokens(tv):
+    k = torch.ones(2, 1, 16, 64, dtype=torch.bfloat16, device="cuda:0")
+    x = torch.zeros(0, 1, 64, dtype=torch.bfloat16, device="cuda:0")
+    assert tv.paged_append(x, x, torch.zeros(0, dtype=torch.int64, device="cuda:0"), k, k.clone()).numel() == 0
+    assert bool((k == 1).all())
+
+
+# -------------------------------------------------------------------- commit
+@pytest.mark.parametrize("B,N,Hkv,D,page,dtype,layout", [
+    (1, 2, 1, 64, 8, "bf16", "heads"), (5, 60, 8, 128, 16, "bf16", "rows"), (3, 512, 2, 128, 64, "fp16", "both"),
+    (4, 33, 3, 40, 32, "bf16", "heads"), (2, 100, 1, 1024, 256, "bf16", "heads")])
+def test_commit_moves_the_branch(tv, B, N, Hkv, D, page, dtype, layout):
+    rng = random.Random(N)
+    lens = [(rng.randint(0, 3 * page), N) for _ in range(B)]
+    c = make(N, lens, Hkv, Hkv, D, page, dtype, layout=layout)
+    acc = [rng.randint(0, min(N - 1, 40)) for _ in range(B)]
+    if B > 1:
+        acc[0], acc[1] = 0, N - 1
+    paths = [[0] + sorted(rng.sample(range(1, N), a)) for a in acc]
+    path = [p + [-1] * (N - len(p)) for p in paths]
+    ek, ev = c["k"].clone(), c["v"].clone()
+    table = np_(c["table"]).tolist()
+    for x in (ek, ev):
+        for b, (L, _) in enumerate(lens):
+            at = lambda i: (table[b][(L + i) // page], slice(None), (L + i) % page)  # noqa: E731
+            rows = [x[at(p)].clone() for p in paths[b]]
+            for d, r in enumerate(rows):
+                x[at(d)] = r
+    new_len, status = tv.commit_paged(c["k"], c["v"], c["table"], c["kv_len"], i32(path), i32(acc))
+    torch.cuda.synchronize()
+    assert np_(status).tolist() == [0] * B
+    assert np_(new_len).tolist() == [L + a + 1 for (L, _), a in zip(lens, acc)]
+    for got, want in ((c["k"], ek), (c["v"], ev)):
+        assert torch.equal(got.contiguous().view(torch.int16), want.contiguous().view(torch.int16))
+
+
+def test_commit_bad_sequences_move_nothing(tv):
+    N, page = 8, 8
+    lens = [(5, N)] * 9
+    c = make(3, lens, 2, 2, 64, page)
+    good = [0, 2, 3, 5] + [-1] * 4
+    path = [list(good) for _ in lens]
+    acc, kv = [3] * 9, [5] * 9
+    path[0][0] = 1                    # not from node 0
+    path[1][2] = 2                    # not ascending
+    path[2][3] = N                    # outside the tree
+    acc[3], acc[4] = -1, N            # outside [0, N)
+    kv[5], kv[6] = -2, 10**9          # a negative length, one past the table
+    table = c["table"].clone()
+    table[7, 1] = table[7, 1] + 10**6  # the page of rows 8 and up
+    before = c["k"].clone().view(torch.int16), c["v"].clone().view(torch.int16)
+    new_len, status = tv.commit_paged(c["k"], c["v"], table, i32(kv), i32(path), i32(acc))
+    torch.cuda.synchronize()
+    assert np_(status).tolist() == [1] * 8 + [0]
+    assert np_(new_len).tolist() == kv[:8] + [9]
+    mine = set(np_(c["table"])[8].tolist())
+    for got, was in zip((c["k"], c["v"]), before):
+        for p in range(got.shape[0]):
+            if p not in mine:
+                assert torch.equal(got[p].view(torch.int16), was[p])
+    assert not torch.equal(c["k"].view(torch.int16), before[0])
+
+
+# ----------------------------------------------------------------- attention
+def run(tv, c, pad=0, **kw):
+    T, Hq, D = c["q"].shape
+    out = torch.full((T, Hq, D), 7.0, dtype=c["q"].dtype, device="cuda:0")
+    lse = torch.full((T, Hq), 7.0, device="cuda:0")
+    out, lse, status = tv.attn_paged(c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_len"], c["max_q"],
+                                     anc_mask=c["anc"], out=out, lse=lse, **kw)
+    torch.cuda.synchronize()
+    n = c["T"]
+    assert bool((out[n:] == 7).all()) and bool((lse[n:] == 7).all())  # rows of nobody
+    return out[:n], lse[:n], np_(status).tolist()
+
+
+def agree(tv, c, Hq, Hkv, D, dtype, what="", **kw):
+    out, lse, status = run(tv, c, **kw)
+    assert status == [0] * len(c["lens"])
+    check_attn(out, lse, attn_ref(c, Hq, Hkv, D, **kw), dtype, what)
+    return out, lse
+
+
+DECODE = [[(0, 1)], [(1, 1)], [(63, 1), (64, 1), (65, 1), (0, 1)], [(2500, 1), (3, 1), (0, 1), (700, 1)],
+          [(127, 1), (128, 1), (4100, 1)]]
+
+
+@pytest.mark.parametrize("lens", DECODE)
+@pytest.mark.parametrize("Hq,Hkv,D,page,dtype", [(8, 2, 128, 16, "bf16"), (4, 4, 64, 8, "fp16"),
+                                                 (7, 1, 128, 256, "bf16"), (16, 1, 64, 64, "bf16"),
+                                                 (32, 1, 128, 32, "fp16"), (100, 2, 64, 128, "bf16")])
+def test_decode(tv, lens, Hq, Hkv, D, page, dtype):
+    c = make(len(lens), lens, Hq, Hkv, D, page, dtype)
+    agree(tv, c, Hq, Hkv, D, dtype)
+
+
+CHUNKS = [[(0, 2)], [(0, 129)], [(200, 33), (0, 0), (5, 64), (130, 1)], [(64, 200), (700, 3)],
+          [(1000, 5), (1, 4), (33, 8)], [(0, 1), (0, 0), (2000, 127)]]
+
+
+@pytest.mark.parametrize("lens", CHUNKS)
+@pytest.mark.parametrize("Hq,Hkv,D,page,dtype", [(8, 2, 128, 16, "bf16"), (3, 3, 64, 8, "bf16"),
+                                                 (10, 2, 128, 128, "fp16"), (7, 1, 64, 256, "bf16"),
+                                                 (64, 1, 128, 32, "bf16")])
+def test_causal_chunks(tv, lens, Hq, Hkv, D, page, dtype):
+    c = make(len(lens) + 10, lens, Hq, Hkv, D, page, dtype, pad=3)
+    agree(tv, c, Hq, Hkv, D, dtype)
+
+
+TREES = [[(0, 1)], [(100, 4), (0, 3)], [(300, 64), (17, 60), (0, 5), (64, 1)], [(190, 65)], [(40, 300), (0, 7)]]
+
+
+@pytest.mark.parametrize("lens", TREES)
+@pytest.mark.parametrize("Hq,Hkv,D,page,dtype", [(8, 2, 128, 16, "bf16"), (4, 4, 64, 64, "fp16"),
+                                                 (8, 1, 64, 8, "bf16")])
+def test_trees(tv, lens, Hq, Hkv, D, page, dtype):
+    c = make(len(lens) + 20, lens, Hq, Hkv, D, page, dtype, tree=True, pad=2)
+    agree(tv, c, Hq, Hkv, D, dtype)
+
+
+def slopes_of(Hq):
+    return torch.tensor([2.0 ** (-8.0 * (h + 1) / Hq) for h in range(Hq)], device="cuda:0")
+
+
+KINDS = [dict(softcap=5.0), dict(softcap=50.0, scale=0.7), dict(window=1), dict(window=70), dict(window=10**6),
+         dict(slopes=True), dict(slopes=True, softcap=20.0, window=150)]
+
+
+@pytest.mark.parametrize("kw", KINDS)
+@pytest.mark.parametrize("lens,tree", [([(900, 1), (0, 1), (150, 1)], False), ([(300, 200), (0, 40), (77, 1)], False),
+                                       ([(260, 70), (0, 9), (129, 1)], True), ([(500, 3), (64, 4)], True)])
+@pytest.mark.parametrize("Hq,Hkv,D,page,dtype", [(8, 2, 128, 16, "bf16"), (4, 4, 64, 32, "fp16")])
+def test_score_kinds(tv, kw, lens, tree, Hq, Hkv, D, page, dtype):
+    kw = dict(kw)
+    if kw.get("slopes"):
+        kw["slopes"] = slopes_of(Hq)
+    c = make(5, lens, Hq, Hkv, D, page, dtype, tree=tree, q_mag=3.0)
+    agree(tv, c, Hq, Hkv, D, dtype, **kw)
+
+
+@pytest.mark.parametrize("layout", ["heads", "rows", "both"])
+@pytest.mark.parametrize("lens", [[(700, 1), (90, 1)], [(300, 90), (20, 5)]])
+def test_cache_layouts(tv, layout, lens):
+    """[pages, heads, rows, D], [pages, rows, heads, D] and K, V side by side."""
+    c = make(1, lens, 8, 2, 128, 16, layout=layout)
+    agree(tv, c, 8, 2, 128, "bf16")
+
+
+@pytest.mark.parametrize("lens", [[(3000, 1)] * 3, [(2900, 90), (1, 2)], [(0, 1500)]])
+def test_same_result_every_time(tv, lens):
+    """The split of the key ranges depends on the lengths alone and nothing is added
+    in an order that can change."""
+    c = make(8, lens, 8, 2, 128, 16)
+    a = run(tv, c)
+    for _ in range(3):
+        b = run(tv, c)
+        assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
+def test_lengths_do_not_depend_on_the_hint(tv):
+    """Chunks longer than max_q says are served too."""
+    c = make(4, [(100, 70), (0, 3), (40, 200)], 8, 2, 128, 16)
+    want = attn_ref(c, 8, 2, 128)
+    for hint in (1, 3, 8, 64, 4000):
+        c["max_q"] = hint
+        out, lse, status = run(tv, c)
+        assert status == [0, 0, 0]
+        check_attn(out, lse, want, "bf16", f"max_q {hint}")
+
+
+def test_large_scores(tv):
+    """Rows whose scores differ by hundreds: the running maximum moves far and often."""
+    for lens in ([(1500, 1)], [(700, 100)]):
+        c = make(6, lens, 4, 1, 128, 16, q_mag=30.0)
+        agree(tv, c, 4, 1, 128, "bf16")
+
+
+def test_values_of_the_types_edge(tv):
+    """V near the largest half: sums of weights times values stay in 32 bits."""
+    c = make(6, [(300, 40), (500, 1)], 4, 1, 64, 16, "fp16")
+    for x in c["rows"]:
+        x[1].mul_(8000.0)
+    c["v"].mul_(8000.0)
+    agree(tv, c, 4, 1, 64, "fp16")
+
+
+def test_bad_sequences(tv):
+    """Lengths that do not fit are reported and zeroed, malformed ranges left alone;
+    their neighbours are served."""
+    lens = [(40, 3), (20, 3), (60, 3), (10, 3)]
+    for extra in (0, 60):  # single-token and many-token kernels
+        lens = [(L, n + extra) for L, n in lens]
+        c = make(2, lens, 8, 2, 128, 16)
+        ref = attn_ref(c, 8, 2, 128)
+        n = lens[0][1]
+        c["kv_len"][0] = -1
+        c["kv_len"][2] = 10**6
+        out, lse, status = run(tv, c)
+        assert status == [1, 0, 1, 0]
+        for b in (0, 2):
+            assert bool((out[b * n:(b + 1) * n] == 0).all()) and bool((lse[b * n:(b + 1) * n] == 0).all())
+        for b in (1, 3):
+            part = tuple(r[b * n:(b + 1) * n] for r in ref)
+            check_attn(out[b * n:(b + 1) * n], lse[b * n:(b + 1) * n], part, "bf16")
+        c = make(2, lens, 8, 2, 128, 16)
+        c["q_start"][2] = c["q_start"][1] - 1   # sequence 1 descends, sequence 2 overlaps sequence 0
+        out, lse, status = run(tv, c)
+        assert status[1] == 1
+        last = tuple(r[3 * n:] for r in ref)
+        check_attn(out[3 * n:], lse[3 * n:], last, "bf16")
+        c = make(2, lens, 8, 2, 128, 16)
+        c["q_start"][4] += 1                    # past T
+        out, lse, status = run(tv, c)
+        assert status == [0, 0, 0, 1] and bool((out[3 * n:] == 7).all())
+
+
+@pytest.mark.parametrize("new", [1, 50])
+@pytest.mark.parametrize("page", [8, 32, 128, 256])
+def test_bad_pages_are_hidden_and_reported(tv, new, page):
+    lens = [(600, new), (600, new), (90, new)]
+    c = make(3, lens, 8, 2, 128, page)
+    c["table"][0, 1] = -5
+    c["table"][2, 0] = 10**7
+    hidden = {0: set(range(page, min(2 * page, 600 + new))), 2: set(range(min(page, 90 + new)))}
+    out, lse, status = run(tv, c)
+    assert status == [1, 0, 1]
+    ref = attn_ref(c, 8, 2, 128, hidden=hidden)
+    check_attn(out, lse, ref, "bf16")
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_pages_behind_the_window_may_be_gone(tv, new):
+    c = make(3, [(500, new), (100, new)], 4, 2, 64, 16)
+    ref = attn_ref(c, 4, 2, 64, window=100)
+    gone = (500 - 100 + 1) // 16
+    ids = np_(c["table"])[0, :gone].tolist()
+    c["table"][0, :gone] = -1
+    c["k"][ids] = float("nan")
+    c["v"][ids] = float("inf")
+    edge = int(c["table"][0, gone])           # rows in front of the window, in its first page
+    front = (500 - 100 + 1) % 16
+    c["k"][edge, :, :front] = float("nan")
+    c["v"][edge, :, :front] = float("nan")
+    out, lse, status = run(tv, c, window=100)
+    assert status == [0, 0]
+    check_attn(out, lse, ref, "bf16")
+
+
+def test_empty_masks(tv):
+    """The masks of an invalid tree: nothing of the tree is seen."""
+    c = make(3, [(0, 6), (30, 6)], 4, 2, 64, 16, tree=True)
+    c["anc"].zero_()
+    out, lse, status = run(tv, c)
+    assert status == [0, 0]
+    assert bool((out[:6] == 0).all()) and bool((lse[:6] == -math.inf).all())
+    assert bool(torch.isfinite(lse[6:]).all()) and bool((out[6:] != 0).any())
+    for i in range(6):  # the same prefix for every node: only its query differs
+        d = make(3, [(0, 6), (30, 6)], 4, 2, 64, 16)
+        q = d["q"][6 + i:7 + i].clone()
+        one, lse1, _ = tv.attn_paged(q, d["k"], d["v"], d["table"][1:], i32([0, 1]), i32([29]), 1)
+        assert (one.float() - out[6 + i:7 + i].float()).abs().max() <= 2 * 2.0**-8 * 4
+        assert (lse1 - lse[6 + i:7 + i]).abs().max() <= 1e-4
+
+
+def test_no_tokens(tv):
+    c = make(3, [(40, 0), (0, 0)], 4, 2, 64, 16, pad=4)
+    out, lse, status = run(tv, c)
+    assert status == [0, 0] and out.numel() == 0
+    q = c["q"][:0]
+    out, lse, status = tv.attn_paged(q, c["k"], c["v"], c["table"], c["q_start"], c["kv_len"], 1)
+    torch.cuda.synchronize()
+    assert out.shape == (0, 4, 64) and np_(status).tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("lens", [[(300, 1), (2000, 1)], [(300, 80), (2000, 9)]])
+def test_other_stream_and_graphs(tv, lens):
+    """On a stream of its own, and two captured calls replayed at the same time on new
+    inputs in the same buffers."""
+    cs = [make(s, lens, 8, 2, 128, 16) for s in (1, 2)]
+    refs = [attn_ref(c, 8, 2, 128) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    graphs, outs = [], []
+    for c, s in zip(cs, streams):
+        with torch.cuda.stream(s):
+            got = tv.attn_paged(c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_len"], c["max_q"])
+        s.synchronize()
+        check_attn(got[0], got[1], refs[len(graphs)], "bf16")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(tv.attn_paged(c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_len"], c["max_q"]))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for o in outs:
+            o[0].zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, r in zip(outs, refs):
+            check_attn(o[0], o[1], r, "bf16")
+
+
+def test_refusals_of_the_binding(tv):
+    c = make(1, [(40, 3)], 4, 2, 64, 16)
+    ok = (c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_len"], 3)
+
+    def bad(i, x, err, **kw):
+        a = list(ok)
+        a[i] = x
+        with pytest.raises(err):
+            tv.attn_paged(*a, **kw)
+    bad(0, c["q"].float(), TypeError)
+    bad(0, c["q"].half(), TypeError)
+    bad(0, c["q"][..., :32], ValueError)
+    bad(0, c["q"].transpose(1, 2).contiguous().transpose(1, 2), ValueError)
+    bad(0, c["q"][0], ValueError)
+    bad(1, c["k"].float(), TypeError)
+    bad(2, c["v"].half(), TypeError)
+    bad(2, c["v"][:-1], ValueError)
+    bad(2, c["v"].transpose(1, 2).contiguous().transpose(1, 2), ValueError)
+    bad(3, c["table"].long(), TypeError)
+    bad(3, c["table"][0], ValueError)
+    bad(4, c["q_start"][:1], ValueError)
+    bad(5, c["kv_len"].cpu(), ValueError)
+    bad(6, 0, tv.TVError)
+    bad(6, 3, ValueError, anc_mask=torch.zeros(2, 1, dtype=torch.int64, device="cuda:0"))
+    bad(6, 3, ValueError, slopes=torch.zeros(3, device="cuda:0"))
+    bad(6, 3, tv.TVError, softcap=-1.0)
+    bad(6, 3, tv.TVError, window=-1)
+    bad(6, 3, TypeError, out=torch.zeros(3, 4, 64, device="cuda:0"))
+    odd = torch.zeros(c["q"].numel() + 1, dtype=torch.bfloat16, device="cuda:0")[1:].view(c["q"].shape)
+    bad(0, odd, tv.TVError)
+    torch.cuda.synchronize()
+
+
+# ------------------------------------------------------------------ together
+def test_verify_steps_of_a_paged_batch_equal_the_dense_ones(tv):
+    """Speculative steps over the paged cache (page map, append, tree attention,
+    greedy acceptance, commit) against the dense entry points on the same rows."""
+    B, N, Hq, Hkv, D, page, V = 3, 20, 8, 2, 128, 16, 500
+    rng, g = random.Random(4), torch.Generator().manual_seed(4)
+    prompt = [37, 5, 130]
+    Lcap, P = 320, 20
+    pool = Pool(6, B, P, 2 * B * P // 3, page)
+    t = pool.gpu
+    kp, vp = (torch.full((len(pool.free), Hkv, page, D), float("nan"), dtype=torch.bfloat16, device="cuda:0")
+              for _ in range(2))
+    kd, vd = (torch.zeros(B, Hkv, Lcap, D, dtype=torch.bfloat16, device="cuda:0") for _ in range(2))
+    randn = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to("cuda:0")  # noqa: E731
+
+    def write(kv_len, new, k, v, q_start):
+        slots, status = tv.page_map(i32(q_start), kv_len, t["table"], t["held"], t["free"], t["n_free"], page,
+                                    q_start[-1])
+        assert np_(status).tolist() == [0] * B
+        assert int(tv.paged_append(k, v, slots, kp, vp).sum()) == 0
+        for b, L in enumerate(np_(kv_len).tolist()):
+            kd[b, :, L:L + new[b]] = k[q_start[b]:q_start[b + 1]].transpose(0, 1)
+            vd[b, :, L:L + new[b]] = v[q_start[b]:q_start[b + 1]].transpose(0, 1)
+
+    def close(a, b, u):
+        a, b = a.float(), b.float()
+        assert (a - b).abs().max() <= 2 * u * b.abs().max().clamp_min(1.0)
+
+    # the prompts in one ragged chunk: each token against its causal prefix
+    q0 = starts(prompt)
+    kv_len = i32([0] * B)
+    write(kv_len, prompt, randn(q0[-1], Hkv, D), randn(q0[-1], Hkv, D), q0)
+    q = randn(q0[-1], Hq, D)
+    out, lse, status = tv.attn_paged(q, kp, vp, t["table"], i32(q0), kv_len, max(prompt))
+    assert np_(status).tolist() == [0] * B
+    for b in range(B):
+        for i in {0, prompt[b] // 2, prompt[b] - 1}:
+            one = torch.ones(1, 1, 1, dtype=torch.int64, device="cuda:0")
+            do, dl, _ = tv.attn_verify(q[q0[b] + i].view(1, 1, Hq, D), kd[b:b + 1], vd[b:b + 1], i32([i]), one)
+            close(out[q0[b] + i], do[0, 0], 2.0**-8)
+            assert (lse[q0[b] + i] - dl[0, 0]).abs().max() <= 1e-4
+    kv_len = i32(prompt)
+    for step in range(3):
+        parent = i32([[-1] + [rng.randrange(max(0, i - 6), i) for i in range(1, N)] for _ in range(B)])
+        depth, anc, st = tv.tree_build(parent)
+        q1 = starts([N] * B)
+        write(kv_len, [N] * B, randn(B * N, Hkv, D), randn(B * N, Hkv, D), q1)
+        q = randn(B * N, Hq, D)
+        out, lse, status = tv.attn_paged(q, kp, vp, t["table"], i32(q1), kv_len, N, anc_mask=anc.view(B * N, -1))
+        dout, dlse, _ = tv.attn_verify(q.view(B, N, Hq, D), kd, vd, kv_len, anc)
+        close(out.view(B, N, Hq, D), dout, 2.0**-8)
+        assert (lse.view(B, N, Hq) - dlse).abs().max() <= 1e-4
+        tokens = torch.randint(0, V, (B, N), generator=g, dtype=torch.int32).to("cuda:0")
+        logits = torch.randn(B, N, V, generator=g).to("cuda:0")
+        for b in range(B):      # the target agrees with a branch
+            node = rng.randrange(N // 2, N)
+            while node > 0:
+                up = int(parent[b, node])
+                logits[b, up, int(tokens[b, node])] = 50.0
+                node = up
+        acc = tv.accept_greedy(logits, tokens, parent, depth)
+        dnew, _ = tv.commit_path(kd, vd, kv_len, acc["path"], acc["accept_len"])
+        pnew, status = tv.commit_paged(kp, vp, t["table"], kv_len, acc["path"], acc["accept_len"])
+        assert np_(status).tolist() == [0] * B
+        assert torch.equal(dnew, pnew) and int(acc["accept_len"].max()) > 0
+        kv_len = pnew
+        table, lens = np_(t["table"]).tolist(), np_(kv_len).tolist()
+        for b in range(B):
+            for pos in range(lens[b]):
+                p, r = table[b][pos // page], pos % page
+                assert torch.equal(kp[p, :, r], kd[b, :, pos]) and torch.equal(vp[p, :, r], vd[b, :, pos])
+    # one plain decode token each, then everything is released
+    q1 = starts([1] * B)
+    write(kv_len, [1] * B, randn(B, Hkv, D), randn(B, Hkv, D), q1)
+    q = randn(B, Hq, D)
+    out, lse, _ = tv.attn_paged(q, kp, vp, t["table"], i32(q1), kv_len, 1)
+    one = torch.ones(B, 1, 1, dtype=torch.int64, device="cuda:0")
+    dout, dlse, _ = tv.attn_verify(q.view(B, 1, Hq, D), kd, vd, kv_len, one)
+    close(out, dout[:, 0], 2.0**-8)
+    assert (lse - dlse[:, 0]).abs().max() <= 1e-4
+    tv.page_map(i32([0] * (B + 1)), i32([0] * B), t["table"], t["held"], t["free"], t["n_free"], page, 0)
+    assert int(t["n_free"]) == len(pool.free)
+    assert sorted(np_(t["free"]).tolist()) == list(range(len(pool.free)))
