@@ -350,7 +350,7 @@ tv_status tv_debug_set_wait_limit(long long cycles);
  *                       record.  Units: 1 tree, 2 greedy, 3 sample,
  *                       4 expand, 5 attention, 6 commit, 7 expected,
  *                       8 top-n selection, 9 library, 10 pages,
- *                     11 paged attention.  Host call; it must not
+ *                     11 to 13 paged attention.  Host call; it must not
  *                       overlap a launch of this library on the device.
  *                       TV_ERR_INVALID_ARG if site is NULL, TV_ERR_CUDA if
  *                       the device reports an error.

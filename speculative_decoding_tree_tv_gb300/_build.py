@@ -18,7 +18,7 @@ CHECKED_LIB_PATH = os.path.join(PKG, "libtreeverify_checked.so")
 
 SOURCES = ["tv_api.cu", "tv_tree.cu", "tv_greedy.cu", "tv_sample.cu", "tv_expand.cu",
            "tv_attn.cu", "tv_commit.cu", "tv_expected.cu", "tv_topn.cu", "tv_spine.cpp",
-           "tv_pages.cu", "tv_attn_paged.cu"]
+           "tv_pages.cu", "tv_attn_paged.cu", "tv_attn_paged_rows.cu", "tv_attn_paged_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE,
               "-I" + CSRC, "--expt-relaxed-constexpr"]

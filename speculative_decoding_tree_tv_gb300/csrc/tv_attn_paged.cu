@@ -1,158 +1,190 @@
-// tv_attn_paged: attention of a ragged batch of new tokens over a paged cache.
+// tv_attn_paged: the merge of split units, the plan and the entry point (tv_attn_paged.cuh
+// says how the work is shared).
 #define TV_UNIT 11
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
-#include "tv_paged.cuh"
+#include "tv_attn_paged.cuh"
 
 namespace tv {
+namespace paged {
 namespace {
 
-struct PagedAttnParams {
-  const uint16_t* q;
-  const uint16_t* k;
-  const uint16_t* v;
-  long long q_token_stride, q_head_stride;
-  PagedCache c;
-  const int32_t* table;
-  const int32_t* q_start;
-  const int32_t* kv_len;
-  const uint64_t* anc;
-  const float* slopes;
-  uint16_t* out;
-  float* lse;
-  int32_t* status;
-  int B, T, P, Hq, Hkv, G, W, window;
-  float scale, softcap;
-};
+// Joins the parts of the split units.  Block (i, y): the unit that CTA i's
+// share ends inside, if any; its parts are slots 2 i + 1, 2 (i + 1), 2 (i + 2), ..
+// Rows of the tcgen05 kernel lie chunk by chunk (TC: [D / 4][rows] of four floats, the
+// order its threads write), the others row by row.
+constexpr int kMergeThreads = 256, kMergeBatch = 4;
 
-template <bool F16>
-__device__ __forceinline__ float to_f(uint16_t x) {
-  if (F16) return __half2float(__ushort_as_half(x));
-  return __uint_as_float((uint32_t)x << 16);
-}
-template <bool F16>
-__device__ __forceinline__ uint16_t from_f(float x) {
-  if (F16) return __half_as_ushort(__float2half_rn(x));
-  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-}
-
-// One warp per (token, query head); a lane scores one key of 32, the warp
-// then adds the 32 value rows.
-template <int D, bool F16>
-__global__ void __launch_bounds__(128) attn_simple_kernel(const PagedAttnParams p) {
+template <int D, bool F16, bool TC>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnParams p, int slot_rows,
+                                                                    int nb) {
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const long long items = (long long)p.T * p.Hq;
-  if (item >= items) {  // one warp per sequence: its status
-    const long long b = item - items;
-    if (b >= p.B || !p.status) return;
-    int t0, n;
-    int bad = !seq_range(p.q_start, (int)b, p.T, t0, n);
-    const int L = __ldg(p.kv_len + b);
-    if (!bad) bad = L < 0 || (long long)L + n > ((long long)p.P << p.c.page_shift) ||
-                    (p.anc && n > 64 * p.W);
-    if (!bad) {
-      const int lo = p.window > 0 ? max(0, L - p.window + 1) : 0;
-      for (int j = (lo >> p.c.page_shift) + lane; n > 0 && ((long long)j << p.c.page_shift) < L + n; j += 32) {
-        const int page = __ldg(p.table + (size_t)b * p.P + j);
-        bad |= page < 0 || page >= p.c.num_pages;
-      }
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    if (lane == 0) p.status[b] = bad ? TV_ERR_INVALID_ARG : TV_OK;
-    return;
-  }
-  const int t = (int)(item / p.Hq), h = (int)(item % p.Hq), kvh = h / p.G;
-  int b = -1, t0 = 0, n = 0;
-  for (int x = 0; x < p.B; ++x) {
-    int f, m;
-    if (seq_range(p.q_start, x, p.T, f, m) && t >= f && t < f + m) {
-      b = x;
-      t0 = f;
-      n = m;
-    }
-  }
-  if (b < 0) return;
-  const int L = __ldg(p.kv_len + b), i = t - t0;
-  float acc[D / 32];
+  const int i = blockIdx.x;
+  const int4 d = p.desc[i];
+  if (d.w == 0 || !TV_IN(d.x, p.B)) return;
+  const Seq s = load_seq(p, d.x);
+  const int first = d.z * p.tq, ntok = min(p.tq, s.n - first);
+  constexpr int kChunks = D / 4;
+  const int items = slot_rows * kChunks;
+  for (int k = blockIdx.y * kMergeThreads + threadIdx.x; k < items; k += gridDim.y * kMergeThreads) {
+    const int row = TC ? k % slot_rows : k / kChunks, c = TC ? k / slot_rows : k % kChunks;
+    // a row block of the tcgen05 kernel holds nb tokens in its 128 rows
+    const int rl = TC ? row & 127 : row;
+    const int tl = (TC ? (row >> 7) * nb : 0) + rl / p.G;
+    if (tl >= ntok || (TC && rl / p.G >= nb)) continue;
+    const int h = d.y * p.G + rl % p.G;
+    float M = -INFINITY, l = 0.0f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < d.w; j0 += kMergeBatch) {
+      float2 ml[kMergeBatch];
+      float4 v[kMergeBatch];
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) acc[e] = 0.0f;
-  float m_run = -INFINITY, l_run = 0.0f;
-  const bool bad = L < 0 || (long long)L + n > ((long long)p.P << p.c.page_shift) ||
-                   (p.anc && n > 64 * p.W);
-  if (!bad) {
-    const uint64_t* anc = p.anc ? p.anc + (size_t)t * p.W : nullptr;
-    int pos = L + i;
-    if (anc) {
-      int c = 0;
-      for (int w = 0; w < p.W; ++w) c += __popcll(anc[w]);
-      pos = L + c - 1;
-    }
-    const float slope = p.slopes ? p.slopes[h] : 0.0f;
-    const uint16_t* q = p.q + t * p.q_token_stride + h * p.q_head_stride;
-    const int keys = anc ? L + n : L + i + 1;
-    for (int j0 = 0; j0 < keys; j0 += 32) {
-      const int j = j0 + lane;
-      float x = -INFINITY;
-      long long row = -1;
-      if (j < keys) {
-        int kpos = j;
-        bool see = true;
-        if (anc && j >= L) {
-          const int a = j - L;
-          see = (anc[a >> 6] >> (a & 63)) & 1;
-          int c = 0;
-          for (int w = 0; w <= (a >> 6); ++w)
-            c += __popcll(w < (a >> 6) ? anc[w] : anc[w] & (~0ull >> (63 - (a & 63))));
-          kpos = L + c - 1;
-        }
-        if (p.window > 0) see = see && pos - kpos < p.window;
-        if (see) {
-          const int page = p.table[(size_t)b * p.P + (j >> p.c.page_shift)];
-          if (page >= 0 && page < p.c.num_pages) {
-            row = page * p.c.page_stride + kvh * p.c.head_stride +
-                  (j & ((1 << p.c.page_shift) - 1)) * p.c.row_stride;
-            float s = 0.0f;
-            for (int e = 0; e < D; ++e) s += to_f<F16>(q[e]) * to_f<F16>(p.k[row + e]);
-            x = s * p.scale;
-            if (p.softcap > 0.0f) x = p.softcap * tanhf(x / p.softcap);
-            x -= slope * (float)(pos - kpos);
-          }
+      for (int j = 0; j < kMergeBatch; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.0f);
+        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j0 + j < d.w && TV_CHECK(i + j0 + j < (int)gridDim.x)) {
+          const size_t slot = j0 + j == 0 ? 2 * i + 1 : 2 * (i + j0 + j);
+          ml[j] = p.part_ml[slot * slot_rows + row];
+          v[j] = *reinterpret_cast<const float4*>(p.part + slot * slot_rows * D +
+                                                  (TC ? ((size_t)c * slot_rows + row) * 4
+                                                      : (size_t)row * D + 4 * c));
         }
       }
-      const float m_new = fmaxf(m_run, warp_max(x));
-      if (m_new == -INFINITY) continue;
-      const float corr = expf(m_run - m_new), w = expf(x - m_new);
-      m_run = m_new;
-      l_run = l_run * corr + warp_sum(w);
+      float mx = M;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] *= corr;
-      for (int s = 0; s < 32; ++s) {
-        const long long r = __shfl_sync(0xffffffffu, row, s);
-        const float ws = __shfl_sync(0xffffffffu, w, s);
-        if (r < 0) continue;
+      for (int j = 0; j < kMergeBatch; ++j) mx = fmaxf(mx, ml[j].x);
+      if (mx == -INFINITY) continue;
+      const float f = M == -INFINITY ? 0.0f : ex2(M - mx);
+      M = mx;
+      l *= f;
+      a.x *= f;
+      a.y *= f;
+      a.z *= f;
+      a.w *= f;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[e] += ws * to_f<F16>(p.v[r + 32 * e + lane]);
+      for (int j = 0; j < kMergeBatch; ++j) {
+        if (ml[j].x == -INFINITY) continue;  // (a part whose keys are all hidden: select, do not multiply)
+        const float e = ex2(ml[j].x - M);
+        l = fmaf(e, ml[j].y, l);
+        a.x = fmaf(e, v[j].x, a.x);
+        a.y = fmaf(e, v[j].y, a.y);
+        a.z = fmaf(e, v[j].z, a.z);
+        a.w = fmaf(e, v[j].w, a.w);
       }
     }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const size_t oidx = (size_t)(s.t0 + first + tl) * p.Hq + h;
+    if (!TV_CHECK(oidx < (size_t)p.T * p.Hq)) continue;
+    *reinterpret_cast<uint2*>(p.out + oidx * D + 4 * c) =
+        make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
+    if (c == 0 && p.lse) p.lse[oidx] = l > 0.0f ? (M + log2f(l)) * kLn2 : -INFINITY;
   }
-  const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e)
-    p.out[((size_t)t * p.Hq + h) * D + 32 * e + lane] = from_f<F16>(acc[e] * inv);
-  if (p.lse && lane == 0)
-    p.lse[(size_t)t * p.Hq + h] = bad ? 0.0f : (l_run > 0.0f ? m_run + logf(l_run) : -INFINITY);
+}
+
+// --------------------------------------------------------------------- host
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 f = fn.load(std::memory_order_acquire);
+  if (!f) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      return nullptr;
+    }
+    f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    fn.store(f, std::memory_order_release);
+  }
+  return f;
+}
+
+// The outer dimensions of a tensor map in the order of their strides, which a map wants
+// to be multiples of one another; a dimension of extent one takes a stride that fits.
+// order[i] = which dimension comes i-th.
+bool order_strides(const long long (&extent)[3], long long (&stride)[3], int D, int (&order)[3]) {
+  long long most = D;
+  for (int i = 0; i < 3; ++i)
+    if (extent[i] > 1) most = stride[i] > most ? stride[i] : most;
+  for (int i = 0; i < 3; ++i)
+    if (extent[i] == 1) stride[i] = most;
+  for (int i = 0; i < 3; ++i) order[i] = i;
+  for (int i = 1; i < 3; ++i)
+    for (int j = i; j > 0 && stride[order[j]] < stride[order[j - 1]]; --j) {
+      const int x = order[j];
+      order[j] = order[j - 1];
+      order[j - 1] = x;
+    }
+  const long long a = stride[order[0]], b = stride[order[1]], c = stride[order[2]];
+  return a > 0 && a % 8 == 0 && b % a == 0 && c % b == 0 && c < (1ll << 39);
+}
+
+// A cache side: D by rows, heads and pages; a box is 64 dims of `rows` rows of one
+// page and head.
+bool map_cache(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void* base,
+               const tv_paged_cache* cache, const long long (&stride)[3], const int (&order)[3],
+               int rows) {
+  const cuuint64_t extent[3] = {(cuuint64_t)cache->page_size, (cuuint64_t)cache->Hkv,
+                                (cuuint64_t)cache->num_pages};
+  cuuint64_t dims[4] = {(cuuint64_t)cache->D}, strides[3];
+  cuuint32_t box[4] = {64};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = extent[order[i]];
+    strides[i] = (cuuint64_t)stride[order[i]] * 2;
+    box[i + 1] = order[i] == 0 ? (cuuint32_t)rows : 1u;
+  }
+  return encode(map, cache->dtype == TV_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Which kernel runs, by the rows of the largest unit.
+PagedPlan paged_plan(int max_q, int G, int D) {
+  PagedPlan pl;
+  const long long rows = (long long)max_q * G;
+  pl.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
+  if (pl.mt) {
+    pl.rows = 16 * pl.mt;
+    pl.nb = pl.tq = pl.rows / G;
+    pl.ctas = 2 * device_sm_count();
+    pl.min_share = 6;
+  } else {
+    pl.rows = 256;
+    pl.nb = 128 / G;
+    pl.tq = 2 * pl.nb;
+    pl.ctas = device_sm_count();
+    pl.min_share = 4;
+  }
+  const size_t r = 2 * (size_t)pl.ctas * pl.rows;
+  pl.part_bytes = align_up(r * D * 4, 256);
+  pl.ml_bytes = align_up(r * 8, 256);
+  pl.desc_bytes = align_up((size_t)pl.ctas * 16, 256);
+  return pl;
+}
+
+template <int D, bool F16>
+cudaError_t launch_merge(const PagedPlan& pl, const PagedAttnParams& p, cudaStream_t stream) {
+  if (pl.mt)
+    return launch_pdl(paged_merge_kernel<D, F16, false>, dim3(pl.ctas, 1), dim3(kMergeThreads), 0,
+                      stream, p, pl.rows, pl.nb);
+  return launch_pdl(paged_merge_kernel<D, F16, true>, dim3(pl.ctas, 8), dim3(kMergeThreads), 0, stream,
+                    p, pl.rows, pl.nb);
 }
 
 }  // namespace
+}  // namespace paged
 }  // namespace tv
 
 extern "C" size_t tv_attn_paged_workspace_size(int max_q, int Hq, int Hkv, int D) {
-  (void)max_q, (void)Hq, (void)Hkv, (void)D;
-  return 0;
+  if (max_q < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128))
+    return 0;
+  return tv::paged::paged_plan(max_q, Hq / Hkv, D).bytes();
 }
 
 extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -166,27 +198,62 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   if (B < 0 || T < 0 || P < 1 || Hq < 1 || max_q < 1 || window < 0) return TV_ERR_INVALID_ARG;
   if (!(scale >= 0.0f) || !isfinite(scale) || !(softcap >= 0.0f) || !isfinite(softcap))
     return TV_ERR_INVALID_ARG;
-  tv::PagedAttnParams p;
-  const tv_status st = tv::check_cache(cache, &p.c);
+  tv::paged::PagedAttnParams p;
+  tv::PagedCache c;
+  const tv_status st = tv::check_cache(cache, &c);
   if (st != TV_OK) return st;
   const int Hkv = cache->Hkv, D = cache->D;
   if (Hq % Hkv != 0) return TV_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || Hq / Hkv > 128 || B > 4096) return TV_ERR_UNSUPPORTED;
+  if ((D != 64 && D != 128) || Hq / Hkv > 128 || B > tv::paged::kMaxSeqs) return TV_ERR_UNSUPPORTED;
   if (anc_mask && max_q > TV_MAX_NODES) return TV_ERR_UNSUPPORTED;
   if ((long long)T * Hq > 0x7fffffffll || (long long)B * P > 0x7fffffffll ||
-      ((long long)P << p.c.page_shift) > 0x7fffffffll)
+      ((long long)P << c.page_shift) > 0x7fffffffll - 512)
     return TV_ERR_UNSUPPORTED;
   if (B == 0) return TV_OK;
   if (!block_table || !q_start || !kv_len || (T > 0 && (!q || !out))) return TV_ERR_INVALID_ARG;
-  p.q_token_stride = tv::stride_or(q_token_stride, T, 8);
-  p.q_head_stride = tv::stride_or(q_head_stride, Hq, 8);
+  p.q_head_stride = tv::stride_or(q_head_stride, Hq, D);
+  p.q_token_stride = tv::stride_or(q_token_stride, T, Hq * p.q_head_stride);
   if (p.q_token_stride < 0 || p.q_head_stride < 0 || ((p.q_token_stride | p.q_head_stride) & 7))
     return TV_ERR_INVALID_ARG;
+  if (p.q_head_stride == 0 || p.q_token_stride == 0) return TV_ERR_UNSUPPORTED;
+  if (Hq == 1) p.q_head_stride = p.q_token_stride;
+  if (p.q_token_stride % p.q_head_stride != 0 || p.q_token_stride >= (1ll << 39))
+    return TV_ERR_UNSUPPORTED;
+  const long long extent[3] = {cache->page_size, Hkv, cache->num_pages};
+  long long stride[3] = {c.row_stride, c.head_stride, c.page_stride};
+  int order[3];
+  if (!tv::paged::order_strides(extent, stride, D, order)) return TV_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15)
     return TV_ERR_INVALID_ARG;
+  const tv::paged::PagedPlan pl = tv::paged::paged_plan(max_q, Hq / Hkv, D);
+  if (!workspace || ws_bytes < pl.bytes() || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return TV_ERR_WORKSPACE;
+  auto encode = tv::paged::tensor_map_encoder();
+  if (!encode) return TV_ERR_CUDA;
+  CUtensorMap tmQ, tmK, tmV;
+  const int rows = min(cache->page_size, pl.mt ? tv::paged::kRowsKeys : tv::paged::kTcKeys);
+  if (!tv::paged::map_cache(encode, &tmK, cache->k, cache, stride, order, rows) ||
+      !tv::paged::map_cache(encode, &tmV, cache->v, cache, stride, order, rows))
+    return TV_ERR_INVALID_ARG;
+  if (!pl.mt && T > 0) {
+    // q as [tokens][heads][D]; a box is 64 dims of the group's heads of nb tokens
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.q_head_stride * 2, (cuuint64_t)p.q_token_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)(Hq / Hkv), (cuuint32_t)pl.nb}, estr[3] = {1, 1, 1};
+    if (encode(&tmQ, cache->dtype == TV_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+               3, const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return TV_ERR_INVALID_ARG;
+  } else {
+    tmQ = tmK;  // not read
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part = reinterpret_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + pl.part_bytes);
+  p.desc = reinterpret_cast<int4*>(ws + pl.part_bytes + pl.ml_bytes);
   p.q = static_cast<const uint16_t*>(q);
-  p.k = static_cast<const uint16_t*>(cache->k);
-  p.v = static_cast<const uint16_t*>(cache->v);
   p.table = block_table;
   p.q_start = q_start;
   p.kv_len = kv_len;
@@ -203,14 +270,29 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   p.G = Hq / Hkv;
   p.W = (max_q + 63) / 64;
   p.window = window;
-  p.scale = scale == 0.0f ? 1.0f / sqrtf((float)D) : scale;
-  p.softcap = softcap;
+  p.num_pages = c.num_pages;
+  p.page_shift = c.page_shift;
+  for (int i = 0; i < 3; ++i) {
+    if (order[i] == 0) p.row_dim = i + 1;
+    if (order[i] == 1) p.head_dim = i + 1;
+  }
+  p.tq = pl.tq;
+  p.min_share = pl.min_share;
+  const float sc = scale == 0.0f ? 1.0f / sqrtf((float)D) : scale;
+  p.scale_log2 = sc * tv::paged::kLog2e;
+  p.softcap_log2 = softcap * tv::paged::kLog2e;
+  p.cap_in = softcap > 0.0f ? 2.0f * tv::paged::kLog2e * sc / softcap : 0.0f;
+  // scores that need more than a scale, or tree rows whose distances the window can reach
+  const bool mod = softcap > 0.0f || slopes || (anc_mask && window > 0 && window < 64 * p.W);
   const bool f16 = cache->dtype == TV_FP16;
-  auto kernel = D == 128 ? (f16 ? tv::attn_simple_kernel<128, true> : tv::attn_simple_kernel<128, false>)
-                         : (f16 ? tv::attn_simple_kernel<64, true> : tv::attn_simple_kernel<64, false>);
-  const long long warps = (long long)T * Hq + B;
-  if (tv::launch_pdl(kernel, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, stream, p) !=
-      cudaSuccess) {
+  cudaError_t e = pl.mt ? tv::paged::launch_rows(pl, D, f16, mod, tmK, tmV, p, stream)
+                        : tv::paged::launch_tc(pl, D, f16, mod, tmQ, tmK, tmV, p, stream);
+  if (e == cudaSuccess)
+    e = D == 128 ? (f16 ? tv::paged::launch_merge<128, true>(pl, p, stream)
+                        : tv::paged::launch_merge<128, false>(pl, p, stream))
+                 : (f16 ? tv::paged::launch_merge<64, true>(pl, p, stream)
+                        : tv::paged::launch_merge<64, false>(pl, p, stream));
+  if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return TV_ERR_CUDA;
   }

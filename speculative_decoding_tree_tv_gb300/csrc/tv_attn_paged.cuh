@@ -1,0 +1,383 @@
+// tv_attn_paged: attention of a ragged batch of new tokens over a paged cache -- what its
+// kernels share.
+//
+// Work.  A unit is (sequence, kv head, query tile): the tile's rows are the
+// (token, head) pairs of the GQA group, token-major, and they share every K/V
+// tile.  Its keys are the tiles of [lo, hi): from the first key the window
+// leaves to the last one that the tile's last token sees.  The units, in the
+// order sequence, head, query tile, are laid end to end on one line, each as
+// long as its key tiles plus kUnitCost (what starting and finishing a unit costs,
+// in tiles), and the line is cut into equal shares, one per resident CTA.
+// So a ragged batch is balanced whatever its lengths are, without the host
+// knowing them: every CTA finds its share from q_start and kv_len alone.  A unit
+// that a cut splits leaves 32-bit partial rows (running maximum, sum, unnormalised
+// output) in the workspace: at most one per CTA for the unit its share begins in
+// and one for the unit it ends in; the merge kernel, chained by programmatic
+// dependent launch, joins them.  The cuts depend on the lengths alone, so
+// results do not vary from run to run.
+//
+// Two kernels take units: paged_rows_kernel (tv_attn_paged_rows.cu) those of at most 32 rows
+// (decode tokens and small trees: HBM-bound, warp-level mma), and
+// paged_tc_kernel (tv_attn_paged_tc.cu, tcgen05) larger ones.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "tv_paged.cuh"
+#include "tv_sm100.cuh"
+
+namespace tv {
+namespace paged {
+
+using namespace sm100;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kRescaleLog2 = 8.0f;  // keep a stale maximum while within 2^8
+constexpr int kMaxSeqs = 4096;
+
+struct PagedAttnParams {
+  const uint16_t* q;
+  long long q_token_stride, q_head_stride;
+  const int32_t* table;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const uint64_t* anc;
+  const float* slopes;
+  uint16_t* out;
+  float* lse;
+  int32_t* status;
+  float* part;      // [2 * CTAs] slots of partial rows
+  float2* part_ml;  // their (running maximum, log2 domain; running sum)
+  int4* desc;       // [CTAs]: the unit a CTA's share ends inside (b, kvh, qt, parts)
+  int B, T, P, Hq, Hkv, G, W, window;
+  int num_pages, page_shift;
+  int row_dim, head_dim;  // which of a cache map's dimensions 1, 2, 3 they are (the pages: the third)
+  int tq;           // tokens per query tile
+  int min_share;    // least cost of a share
+  float scale_log2, softcap_log2, cap_in;  // cap_in: 2 log2(e) scale / softcap
+};
+
+// ------------------------------------------------------------ small helpers
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (F16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
+        "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+// 2^x on the special-function unit (flush-to-zero); 2^-inf = +0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  return fmaxf(fmaxf(a, b), c);
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                            int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+// One box of a cache map: 64 dims from d0 of the rows from `row` of (page, head).  The map's
+// outer dimensions lie in the order of their strides.
+__device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map, uint64_t* bar, int d0,
+                                              int row, int head, int page, int row_dim, int head_dim) {
+  const int c1 = row_dim == 1 ? row : head_dim == 1 ? head : page;
+  const int c2 = row_dim == 2 ? row : head_dim == 2 ? head : page;
+  const int c3 = row_dim == 3 ? row : head_dim == 3 ? head : page;
+  tma_load_4d(dst, map, bar, d0, c1, c2, c3);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// The score in the log2 domain behind the cap: cap tanh(y) with y = scale s / cap, as
+// cap (1 - 2 / (1 + e^2y)).  The subtraction leaves an absolute error of a few
+// 2^-24 cap, which is what a probability feels; tanh.approx is off by 2^-11.
+__device__ __forceinline__ float capped(float s, float cap_in, float cap) {
+  return fmaf(-2.0f * cap, rcp(1.0f + ex2(s * cap_in)), cap);
+}
+
+// Bits [a, b) of a 32-bit word (a, b any integers).
+__device__ __forceinline__ uint32_t range_bits(int a, int b) {
+  const uint32_t hi = b >= 32 ? 0xffffffffu : (b <= 0 ? 0u : (1u << b) - 1u);
+  const uint32_t lo = a >= 32 ? 0xffffffffu : (a <= 0 ? 0u : (1u << a) - 1u);
+  return hi & ~lo;
+}
+// 32 bits of the mask row starting at bit `pos` (-32 < pos < 64 W); 0 beyond it.
+__device__ __forceinline__ uint32_t anc_bits32(const uint64_t* anc, int W, int pos) {
+  if (pos < 0) return (uint32_t)anc[0] << -pos;
+  const int wi = pos >> 6, sh = pos & 63;
+  if (!TV_IN(wi, W)) return 0;
+  const uint64_t lo = anc[wi], hi = (sh > 32 && wi + 1 < W) ? anc[wi + 1] : 0ull;
+  return (uint32_t)((lo >> sh) | (sh ? hi << (64 - sh) : 0ull));
+}
+// Number of mask bits below bit `pos` (pos <= 64 W): a visible node a is at depth
+// count(a + 1) - 1, as the mask's bits up to a are a and its own ancestors.
+__device__ __forceinline__ int anc_count(const uint64_t* anc, int W, int pos) {
+  int c = 0;
+  for (int w = 0; w < W && 64 * w < pos; ++w)
+    c += __popcll(pos - 64 * w >= 64 ? anc[w] : anc[w] & ((1ull << (pos - 64 * w)) - 1ull));
+  return c;
+}
+
+// ------------------------------------------------------- shares of the work
+constexpr int kUnitCost = 2;
+
+struct Seq {
+  int t0, n, L;
+  bool bad;  // rows are zeroed
+};
+
+__device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
+  Seq s;
+  s.L = __ldg(p.kv_len + b);
+  if (!seq_range(p.q_start, b, p.T, s.t0, s.n)) s.n = 0;
+  s.bad = s.L < 0 || (long long)s.L + s.n > ((long long)p.P << p.page_shift) ||
+          (p.anc && s.n > 64 * p.W);
+  return s;
+}
+
+// Keys [lo, hi) that some token of query tile qt sees.
+__device__ __forceinline__ void key_range(const PagedAttnParams& p, const Seq& s, int qt, int& lo,
+                                          int& hi) {
+  const int first = qt * p.tq;
+  hi = p.anc ? s.L + s.n : s.L + min(s.n, first + p.tq);
+  // (a node whose mask is empty counts as one before the root)
+  lo = p.window > 0 ? max(0, (p.anc ? s.L - 1 : s.L + first) - p.window + 1) : 0;
+}
+template <int KT>
+__device__ __forceinline__ int key_tiles(const PagedAttnParams& p, const Seq& s, int qt) {
+  if (s.bad) return 0;
+  int lo, hi;
+  key_range(p, s, qt, lo, hi);
+  return (hi + KT - 1) / KT - lo / KT;
+}
+
+struct Part {
+  Seq s;
+  int b, kvh, qt;
+  int first, ntok;   // the query tile's tokens: first, count
+  int lo, hi;        // its keys
+  int begin, end;    // key tiles of this part
+  int tiles;         // the unit's key tiles
+  int slot;          // partial slot, or -1: the whole unit is here
+};
+
+// A CTA's walk over its share [x, x1) of the line.
+template <int KT>
+struct Cursor {
+  long long x, x1, share;
+  int b, kvh, qt, pos;
+  Seq s;
+
+  __device__ __forceinline__ bool next(const PagedAttnParams& p, Part& o, int4* desc) {
+    const int cta = blockIdx.x;
+    while (x < x1) {
+      const int tiles = key_tiles<KT>(p, s, qt), cost = tiles + kUnitCost;
+      const int take = (int)min((long long)(cost - pos), x1 - x);
+      const int a = max(0, pos - kUnitCost), e = max(0, pos + take - kUnitCost);
+      const bool ends = pos + take == cost;
+      const bool emit = e > a || (tiles == 0 && ends);
+      if (emit) {
+        key_range(p, s, qt, o.lo, o.hi);
+        o.s = s;
+        o.b = b;
+        o.kvh = kvh;
+        o.qt = qt;
+        o.first = qt * p.tq;
+        o.ntok = min(p.tq, s.n - o.first);
+        o.tiles = tiles;
+        o.begin = o.lo / KT + a;
+        o.end = o.lo / KT + e;
+        o.slot = (a == 0 && e == tiles) ? -1 : 2 * cta + (a == 0);
+        if (desc && o.slot >= 0 && a == 0) {
+          const long long xu = x - pos;
+          *desc = make_int4(b, kvh, qt, (int)((xu + cost - 1) / share - (xu + kUnitCost) / share) + 1);
+        }
+      }
+      x += take;
+      pos += take;
+      if (ends) {
+        pos = 0;
+        if (++qt * (long long)p.tq >= s.n) {
+          qt = 0;
+          if (++kvh == p.Hkv) {
+            kvh = 0;
+            do {
+              if (++b >= p.B) break;
+              s = load_seq(p, b);
+            } while (s.n == 0);
+            if (b >= p.B) x = x1;
+          }
+        }
+      }
+      if (emit) return true;
+    }
+    return false;
+  }
+};
+
+// Finds this CTA's share.  All THREADS threads call it; ends with a barrier.
+template <int KT, int THREADS>
+__device__ __forceinline__ Cursor<KT> find_share(const PagedAttnParams& p) {
+  __shared__ long long s_warp[THREADS / 32];
+  __shared__ Cursor<KT> s_cur;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = ceil_div(p.B, THREADS), b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Seq s = load_seq(p, b);
+    long long c = 0;
+    for (int qt = 0; qt * (long long)p.tq < s.n; ++qt) c += key_tiles<KT>(p, s, qt) + kUnitCost;
+    sum += c * p.Hkv;
+  }
+  long long inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  if (tid == 0) s_cur.x = s_cur.x1 = 0;
+  __syncthreads();
+  long long base = inc - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) base += s_warp[w];
+    total += s_warp[w];
+  }
+  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_share);
+  const long long x0 = blockIdx.x * share, x1 = min(total, x0 + share);
+  if (x0 < x1 && x0 >= base && x0 < base + sum) {  // this thread's sequences hold the share's start
+    Cursor<KT> c;
+    c.x = x0;
+    c.x1 = x1;
+    c.share = share;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = load_seq(p, b);
+      long long one = 0;
+      for (int qt = 0; qt * (long long)p.tq < s.n; ++qt) one += key_tiles<KT>(p, s, qt) + kUnitCost;
+      const long long r = x0 - base;
+      base += one * p.Hkv;
+      if (x0 >= base) continue;
+      c.b = b;
+      c.s = s;
+      c.kvh = (int)(r / one);
+      long long left = r - c.kvh * one;
+      c.qt = 0;
+      for (;;) {
+        const int cost = key_tiles<KT>(p, s, c.qt) + kUnitCost;
+        if (left < cost) break;
+        left -= cost;
+        ++c.qt;
+      }
+      c.pos = (int)left;
+      break;
+    }
+    s_cur = c;
+  }
+  __syncthreads();
+  return s_cur;
+}
+
+// status[b] of the sequences b = CTA, CTA + grid, ..: lengths, and every page id
+// that the window reaches.  `threads` consecutive threads from 0 take part.
+__device__ __forceinline__ void write_status(const PagedAttnParams& p, int threads, int bar) {
+  if (!p.status) return;
+  __shared__ int s_bad;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const Seq s = load_seq(p, b);
+    int t0, n;
+    const bool bad = !seq_range(p.q_start, b, p.T, t0, n) || s.bad;
+    if (!bad && s.n > 0) {
+      int lo, hi;
+      key_range(p, s, 0, lo, hi);
+      hi = s.L + s.n;
+      if (threadIdx.x == 0) s_bad = 0;
+      named_sync(bar, threads);
+      int any = 0;
+      const int32_t* row = p.table + (size_t)b * p.P;
+#pragma unroll 4
+      for (int j = (lo >> p.page_shift) + threadIdx.x; j <= (hi - 1) >> p.page_shift; j += threads) {
+        const int page = TV_IN(j, p.P) ? __ldg(row + j) : 0;
+        any |= page < 0 || page >= p.num_pages;
+      }
+      if (any) s_bad = 1;
+      named_sync(bar, threads);
+      if (threadIdx.x == 0) p.status[b] = s_bad ? TV_ERR_INVALID_ARG : TV_OK;
+      named_sync(bar, threads);
+    } else if (threadIdx.x == 0) {
+      p.status[b] = bad ? TV_ERR_INVALID_ARG : TV_OK;
+    }
+  }
+}
+
+// The page of key position `key` if the unit needs it, else (or where the table holds
+// no page) num_pages, which a tensor map reads as zeros.  bad: needed and no page.
+__device__ __forceinline__ int page_at(const PagedAttnParams& p, const Part& w, int key, int rows,
+                                       bool& bad) {
+  bad = false;
+  if (key >= w.hi || key + rows <= w.lo) return p.num_pages;
+  const int j = key >> p.page_shift;
+  const int page = TV_IN(j, p.P) ? __ldg(p.table + (size_t)w.b * p.P + j) : -1;
+  bad = page < 0 || page >= p.num_pages;
+  return bad ? p.num_pages : page;
+}
+
+// How a call runs: the kernel, its CTAs, and the layout of the workspace.
+struct PagedPlan {
+  int mt;    // 16-row tiles of the small-unit kernel (1 or 2); 0: the tcgen05 kernel
+  int rows;  // rows of a unit
+  int tq, nb, ctas, min_share;
+  size_t part_bytes, ml_bytes, desc_bytes;
+  size_t bytes() const { return part_bytes + ml_bytes + desc_bytes; }
+};
+
+constexpr int kRowsKeys = 64, kTcKeys = 128;  // keys of a tile of either kernel
+
+// mod: scores that need more than a scale (a cap, a bias, tree distances that the window reaches)
+cudaError_t launch_rows(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmK,
+                        const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
+cudaError_t launch_tc(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmQ,
+                      const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
+                      cudaStream_t stream);
+
+}  // namespace paged
+}  // namespace tv

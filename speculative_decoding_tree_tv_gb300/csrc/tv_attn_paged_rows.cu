@@ -1,0 +1,396 @@
+// paged_rows_kernel: units of at most 16 MT rows.  HBM-bound: per 64-key stage a CTA reads 64 D * 4
+// bytes and issues 8 MT D/16 warp mma.  Four consumer warps take 16 keys of a stage each
+// and keep a running maximum, sum and output of their own (no barrier
+// between them until the unit's end); a fifth warp issues the TMA loads, one box
+// per lane (64 dims x the rows of a page).
+#define TV_UNIT 12
+#include "tv_attn_paged.cuh"
+
+namespace tv {
+namespace paged {
+namespace {
+
+constexpr int kRowsWarps = 4;
+constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
+
+template <int D>
+struct RowsLayout {
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kAtom = kRowsKeys * 128;           // bytes of one 64-dim atom of a stage
+  static constexpr int kSide = kAtoms * kAtom;            // K or V of a stage
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kScratch = kRowsWarps * 16 * 32 * 4;  // [warp][row][32 dims]
+  static constexpr int kDyn = 2 * kStages * kSide + kScratch + 1024;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                 "{%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+                 "{%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, bool F16, int MT, bool MOD>
+__global__ void __launch_bounds__(kRowsThreads, 2)
+paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const PagedAttnParams p) {
+  using Lay = RowsLayout<D>;
+  constexpr int kRows = 16 * MT, kSteps = D / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + Lay::kStages * Lay::kSide;
+  float* s_acc = reinterpret_cast<float*>(smem + 2 * Lay::kStages * Lay::kSide);
+  __shared__ __align__(8) uint64_t bar_full[Lay::kStages], bar_empty[Lay::kStages];
+  __shared__ uint32_t s_bad_pages[Lay::kStages];  // bit g: keys 8 g .. 8 g + 7 have no page
+  __shared__ float2 s_ml[kRowsWarps][kRows];
+  __shared__ volatile int s_abort;  // a consumer's wait ran out
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  if (tid == 0) {
+    s_abort = 0;
+    for (int s = 0; s < Lay::kStages; ++s) {
+      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_empty[s], kRowsWarps);
+    }
+    mbar_fence_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  pdl_wait();
+  Cursor<kRowsKeys> cur = find_share<kRowsKeys, kRowsThreads>(p);
+  const int rows_page = min(1 << p.page_shift, kRowsKeys);  // rows of one box
+  Part w;
+  uint32_t it = 0;  // stages used so far
+
+  if (warp == kRowsWarps) {
+    // ------------------------------------------------------------ producer
+    if (tid == kRowsWarps * 32) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    const int npg = kRowsKeys / rows_page;
+    const int pg = lane % npg, atom = (lane / npg) % Lay::kAtoms, side = lane / (npg * Lay::kAtoms);
+    const bool issues = side < 2;
+    const int row0 = pg * rows_page;
+    bool ok = true;
+    while (ok && cur.next(p, w, lane == 0 ? p.desc + blockIdx.x : nullptr)) {
+      bool bad;
+      int page = w.begin < w.end ? page_at(p, w, w.begin * kRowsKeys + row0, rows_page, bad) : 0;
+      for (int t = w.begin; t < w.end; ++t, ++it) {
+        const int st = it % Lay::kStages;
+        const int key = t * kRowsKeys + row0;
+        bool bad_next = false;
+        int page_next = 0;
+        if (t + 1 < w.end) page_next = page_at(p, w, key + kRowsKeys, rows_page, bad_next);
+        ok = warp_wait(&bar_empty[st], ((it / Lay::kStages) & 1) ^ 1);
+        if (!ok) break;
+        const uint32_t bad_pages = __ballot_sync(0xffffffffu, bad && lane < npg);
+        if (lane == 0) {
+          uint32_t m = 0;
+          if (bad_pages)
+            for (int g = 0; g < kRowsKeys / 8; ++g) m |= ((bad_pages >> (8 * g / rows_page)) & 1u) << g;
+          s_bad_pages[st] = m;
+          mbar_expect_tx(&bar_full[st], 2 * Lay::kSide);
+        }
+        __syncwarp();
+        if (issues)
+          tma_load_rows((side ? sV : sK) + st * Lay::kSide + atom * Lay::kAtom + row0 * 128,
+                        side ? &tmV : &tmK, &bar_full[st], atom * 64, key & ((1 << p.page_shift) - 1),
+                        w.kvh, page, p.row_dim, p.head_dim);
+        page = page_next;
+        bad = bad_next;
+      }
+    }
+    // no copy may be in flight when the CTA leaves
+    for (uint32_t i = it > (uint32_t)Lay::kStages ? it - Lay::kStages : 0; i < it; ++i)
+      mbar_wait(&bar_full[i % Lay::kStages], (i / Lay::kStages) & 1);
+    if (!ok && lane == 0 && p.status) atomicMax(p.status + w.b, (int)TV_ERR_TIMEOUT);
+    return;
+  }
+
+  // ---------------------------------------------------------------- consumers
+  write_status(p, kRowsWarps * 32, 1);
+  const int g = lane >> 2, c2 = (lane & 3) * 2;  // fragment row and first column of this lane
+  while (cur.next(p, w, nullptr)) {
+    const int rows = w.ntok * p.G;
+    uint32_t qf[MT][kSteps][4];
+    int pos[2 * MT], limit[2 * MT];
+    const uint64_t* anc[2 * MT];
+    float slope[2 * MT];
+    float m[2 * MT], l[2 * MT], o[MT][D / 8][4];
+#pragma unroll
+    for (int r = 0; r < 2 * MT; ++r) {
+      const int row = min((r >> 1) * 16 + (r & 1) * 8 + g, rows - 1);  // rows past the unit repeat its last
+      const int i = w.first + row / p.G, t = w.s.t0 + i, h = w.kvh * p.G + row % p.G;
+      const uint16_t* qr = p.q + t * p.q_token_stride + h * p.q_head_stride;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) {
+        qf[r >> 1][k][(r & 1)] = __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + c2));
+        qf[r >> 1][k][(r & 1) + 2] = __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8 + c2));
+      }
+      anc[r] = p.anc ? p.anc + (size_t)t * p.W : nullptr;
+      pos[r] = w.s.L + (p.anc ? anc_count(anc[r], p.W, 64 * p.W) - 1 : i);
+      limit[r] = p.anc ? w.s.L : w.s.L + i + 1;  // keys below it are visible, the window apart
+      slope[r] = (MOD && p.slopes) ? __ldg(p.slopes + h) * kLog2e : 0.0f;
+      m[r] = -INFINITY;
+      l[r] = 0.0f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.0f;
+    const int all_below = p.anc ? w.s.L : w.s.L + w.first + 1;  // keys below it are visible to every row
+    const int all_from = p.window > 0
+                             ? (p.anc ? w.s.L + w.s.n : w.s.L + w.first + w.ntok) - p.window : -1;
+
+    for (int t = w.begin; t < w.end; ++t, ++it) {
+      const int st = it % Lay::kStages;
+      const int j0 = t * kRowsKeys + 16 * warp;
+      // (a warp that gives up still joins the others at the unit's end, where all see it)
+      if (!warp_wait(&bar_full[st], (it / Lay::kStages) & 1)) {
+        s_abort = 1;
+        break;
+      }
+      if (j0 < w.hi && j0 + 16 > w.lo) {
+        float s[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[mt][e >> 2][e & 3] = 0.0f;
+        {
+          const int key = 16 * warp + (lane >> 4) * 8 + (lane & 7);
+          const uint32_t base = smem_u32(sK) + st * Lay::kSide + key * 128;
+          const int kc = (lane >> 3) & 1, sw = key & 7;
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t b[4];
+            ldsm4(base + (k >> 2) * Lay::kAtom + ((((k & 3) * 2 + kc) ^ sw) << 4), b);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16816<F16>(s[mt][0], qf[mt][k], b[0], b[1]);
+              mma16816<F16>(s[mt][1], qf[mt][k], b[2], b[3]);
+            }
+          }
+        }
+        const uint32_t bad8 = (s_bad_pages[st] >> (2 * warp)) & 3u;
+        const bool plain = j0 + 16 <= all_below && j0 > all_from && j0 >= w.lo && bad8 == 0;
+        uint32_t vkeep[2] = {0xffffffffu, 0xffffffffu};  // V pairs of keys that some row sees
+        if (!plain) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int j = j0 + 8 * nt + c2 + e;
+              if (j < w.lo || j >= w.hi) vkeep[nt] &= e ? 0x0000ffffu : 0xffff0000u;
+            }
+        }
+        // scores in the log2 domain, hidden keys at -inf
+#pragma unroll
+        for (int r = 0; r < 2 * MT; ++r)
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& x = s[r >> 1][nt][(r & 1) * 2 + e];
+              const int j = j0 + 8 * nt + c2 + e;
+              x = (MOD && p.softcap_log2 > 0.0f) ? capped(x, p.cap_in, p.softcap_log2) : x * p.scale_log2;
+              int kpos = j;
+              if (!plain) {
+                bool see = j < limit[r];
+                if (p.anc && j >= w.s.L && j < w.hi) {
+                  const int a = j - w.s.L;
+                  see = (__ldg(reinterpret_cast<const unsigned long long*>(anc[r]) + (a >> 6)) >> (a & 63)) & 1;
+                  if (MOD) kpos = w.s.L + anc_count(anc[r], p.W, a + 1) - 1;
+                }
+                if (p.window > 0) see = see && pos[r] - kpos < p.window;
+                if ((bad8 >> nt) & 1) see = false;
+                if (MOD) x = fmaf(slope[r], (float)(kpos - pos[r]), x);
+                if (!see) x = -INFINITY;
+              } else if (MOD) {
+                x = fmaf(slope[r], (float)(kpos - pos[r]), x);
+              }
+            }
+        // running maximum (lazily moved), probabilities, sums
+        uint32_t pf[MT][4];
+        float corr[2 * MT];
+        bool move = false;
+#pragma unroll
+        for (int r = 0; r < 2 * MT; ++r) {
+          float (&a)[4] = s[r >> 1][0];
+          float (&b)[4] = s[r >> 1][1];
+          const int e = (r & 1) * 2;
+          float mx = fmaxf(fmaxf(a[e], a[e + 1]), fmaxf(b[e], b[e + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          corr[r] = 1.0f;
+          if (m[r] == -INFINITY) {
+            m[r] = mx;
+          } else if (mx > m[r] + kRescaleLog2) {
+            corr[r] = ex2(m[r] - mx);
+            m[r] = mx;
+            move = true;
+          }
+          const float mm = m[r] == -INFINITY ? 0.0f : m[r];  // 2^(-inf - 0) = 0
+          const float p0 = ex2(a[e] - mm), p1 = ex2(a[e + 1] - mm);
+          const float p2 = ex2(b[e] - mm), p3 = ex2(b[e + 1] - mm);
+          l[r] = fmaf(l[r], corr[r], (p0 + p1) + (p2 + p3));
+          pf[r >> 1][(r & 1)] = pack2<F16>(p0, p1);
+          pf[r >> 1][(r & 1) + 2] = pack2<F16>(p2, p3);
+        }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[mt][n][e] *= corr[2 * mt + (e >> 1)];
+        }
+        {
+          const int key = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7);
+          const uint32_t base = smem_u32(sV) + st * Lay::kSide + key * 128;
+          const int dc = lane >> 4, sw = key & 7;
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            uint32_t b[4];
+            ldsm4_t(base + (n >> 2) * Lay::kAtom + ((((n & 3) * 2 + dc) ^ sw) << 4), b);
+            if (!plain) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) b[q] &= vkeep[q & 1];
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16816<F16>(o[mt][2 * n], pf[mt], b[0], b[1]);
+              mma16816<F16>(o[mt][2 * n + 1], pf[mt], b[2], b[3]);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_empty[st]);
+    }
+
+    // the four warps' rows joined in shared memory, 32 dims at a time
+#pragma unroll
+    for (int r = 0; r < 2 * MT; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if ((lane & 3) == 0) s_ml[warp][(r >> 1) * 16 + (r & 1) * 8 + g] = make_float2(m[r], l[r]);
+    }
+    named_sync(1, kRowsWarps * 32);
+    const bool abort = s_abort;
+    float f[2 * MT];
+#pragma unroll
+    for (int r = 0; r < 2 * MT; ++r) {
+      const int row = (r >> 1) * 16 + (r & 1) * 8 + g;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][row].x);
+      f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mm);
+    }
+    const int orow = tid >> 3, od = (tid & 7) * 4;  // this thread's row and dims of a joined piece
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int row = mt * 16 + orow;
+      float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][row].x);
+#pragma unroll
+      for (int x = 0; x < kRowsWarps; ++x) {
+        const float2 v = s_ml[x][row];
+        if (v.x != -INFINITY) ll = fmaf(ex2(v.x - mm), v.y, ll);
+      }
+      const bool mine = row < rows;
+      const int tok = w.s.t0 + w.first + row / p.G, h = w.kvh * p.G + row % p.G;
+      const size_t oidx = (size_t)tok * p.Hq + h;
+      const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float fr = f[2 * mt + half];
+            // (fr = 0: nothing seen by this warp, its sums are 0)
+            *reinterpret_cast<float2*>(s_acc + (warp * 16 + half * 8 + g) * 32 + 8 * n + c2) =
+                make_float2(o[mt][4 * c + n][2 * half] * fr, o[mt][4 * c + n][2 * half + 1] * fr);
+          }
+        named_sync(1, kRowsWarps * 32);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < kRowsWarps; ++x) {
+          const float4 v = *reinterpret_cast<const float4*>(s_acc + (x * 16 + orow) * 32 + od);
+          a.x += v.x;
+          a.y += v.y;
+          a.z += v.z;
+          a.w += v.w;
+        }
+        if (mine) {
+          if (w.slot >= 0)
+            *reinterpret_cast<float4*>(p.part + ((size_t)w.slot * kRows + row) * D + 32 * c + od) = a;
+          else if (TV_CHECK(tok < p.T && h < p.Hq))
+            *reinterpret_cast<uint2*>(p.out + oidx * D + 32 * c + od) =
+                make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
+        }
+        named_sync(1, kRowsWarps * 32);
+      }
+      if (mine && (tid & 7) == 0) {
+        if (w.slot >= 0) p.part_ml[(size_t)w.slot * kRows + row] = make_float2(mm, ll);
+        else if (p.lse)
+          p.lse[oidx] = w.s.bad ? 0.0f : (ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY);
+      }
+    }
+    if (abort) {
+      if (tid == 0 && p.status) atomicMax(p.status + w.b, (int)TV_ERR_TIMEOUT);
+      break;
+    }
+  }
+}
+
+template <int D, bool F16, int MT, bool MOD>
+cudaError_t launch(const PagedPlan& pl, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                   const PagedAttnParams& p, cudaStream_t stream) {
+  if (!set_dyn_smem(paged_rows_kernel<D, F16, MT, MOD>, RowsLayout<D>::kDyn)) return cudaErrorUnknown;
+  return launch_pdl(paged_rows_kernel<D, F16, MT, MOD>, dim3(pl.ctas), dim3(kRowsThreads),
+                    (size_t)RowsLayout<D>::kDyn, stream, tmK, tmV, p);
+}
+template <int D, bool F16>
+cudaError_t launch_kind(const PagedPlan& pl, bool mod, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                        const PagedAttnParams& p, cudaStream_t stream) {
+  if (pl.mt == 1)
+    return mod ? launch<D, F16, 1, true>(pl, tmK, tmV, p, stream)
+               : launch<D, F16, 1, false>(pl, tmK, tmV, p, stream);
+  return mod ? launch<D, F16, 2, true>(pl, tmK, tmV, p, stream)
+             : launch<D, F16, 2, false>(pl, tmK, tmV, p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rows(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmK,
+                        const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream) {
+  if (D == 128)
+    return f16 ? launch_kind<128, true>(pl, mod, tmK, tmV, p, stream)
+               : launch_kind<128, false>(pl, mod, tmK, tmV, p, stream);
+  return f16 ? launch_kind<64, true>(pl, mod, tmK, tmV, p, stream)
+             : launch_kind<64, false>(pl, mod, tmK, tmV, p, stream);
+}
+
+}  // namespace paged
+}  // namespace tv

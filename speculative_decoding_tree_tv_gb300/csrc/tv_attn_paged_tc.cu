@@ -1,0 +1,505 @@
+// paged_tc_kernel: units of up to 256 rows (two row blocks of 128 TMEM lanes, each nb =
+// floor(128 / G) whole tokens) on the 5th-generation tensor cores.
+//
+// A CTA (one per SM) walks its share of the units.  Warp roles:
+//   warps 0-3, 4-7  softmax of row block 0, 1: one thread per row (TMEM lane), 128 scores a
+//                   tile, online softmax in the log2 domain with lazy rescaling;
+//   warp 8, 10      K and V tiles of 128 keys by TMA (a lane per box: 64 dims of the rows of
+//                   one page), each into a ring of its own;
+//   warp 9          the products: S_r = Q_r K^T and O_r += P_r V (tcgen05.mma, operands in
+//                   shared memory but P, which is read from TMEM where it overlays S_r);
+//   warp 11         the unit's Q rows.
+// The products are issued in the order PV_0(t), S_0(t + 1), PV_1(t), S_1(t + 1): while one row
+// block's softmax runs, the tensor core works on the other's.  S_r(t + 1) may
+// overwrite P_r(t), as products retire in issue order.  The next unit's first S
+// is issued while this one's epilogue still reads O: its first PV needs P, which the same
+// threads write after the epilogue.  Every wait is bounded.
+#define TV_UNIT 13
+#include "tv_attn_paged.cuh"
+
+namespace tv {
+namespace paged {
+namespace {
+
+constexpr int kTcThreads = 384;
+constexpr int kRB = 128;           // rows of a row block
+constexpr int kAtomBytes = 16384;  // 128 rows x 128 bytes
+constexpr int kKStages = 2, kVStages = 3;
+constexpr int kBadRing = 8;        // page flags outlive their K stage by two tiles at most
+
+template <int D>
+struct TcLayout {
+  static constexpr int A = D / 64;
+  static constexpr int kTile = A * kAtomBytes;  // one K or V tile, one row block of Q
+  static constexpr int kK = 2 * kTile;
+  static constexpr int kV = kK + kKStages * kTile;
+  static constexpr int kDyn = kV + kVStages * kTile + 1024;
+};
+
+// kind::f16 with fp32 accumulators: c_format F32, a/b_format F16 (0) or BF16 (1), b_major
+constexpr uint32_t idesc(bool f16, int N, int b_mn) {
+  return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRB >> 4) << 24);
+}
+
+// What one row sees.
+struct Row {
+  const uint64_t* anc;  // mask row, or nullptr (causal)
+  int limit;            // causal and prefix keys below it are visible ..
+  int from;             // .. and at or past this one (the window)
+  int pos;
+};
+
+// Visibility of keys j .. j + 31 for a row (the window's reach inside a tree is
+// taken in tree_scores).
+__device__ __forceinline__ uint32_t see32(const PagedAttnParams& p, const Row& r, int j, int L, int hi) {
+  uint32_t v = range_bits(r.from - j, r.limit - j);
+  const int x = j - L;  // tree index of the first key
+  if (r.anc && x > -32 && j < hi) v |= anc_bits32(r.anc, p.W, x) & range_bits(0, hi - j);
+  return v;
+}
+
+template <int D, bool F16, bool MOD>
+__global__ void __launch_bounds__(kTcThreads, 1)
+paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const PagedAttnParams p, const int nb) {
+  using Lay = TcLayout<D>;
+  constexpr int A = Lay::A;
+  constexpr uint32_t kTmemCols = 512, kOCol = 256;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + Lay::kK;
+  uint8_t* sV = smem + Lay::kV;
+  __shared__ __align__(8) uint64_t bar_q_full, bar_q_empty, bar_drain;
+  __shared__ __align__(8) uint64_t bar_k_full[kKStages], bar_k_empty[kKStages];
+  __shared__ __align__(8) uint64_t bar_v_full[kVStages], bar_v_empty[kVStages];
+  __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_full[2], bar_o_done[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile uint32_t s_bad_pages[kBadRing];  // bit g: keys 8 g .. 8 g + 7 have no page
+  __shared__ volatile int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  if (tid == 0) {
+    mbar_init(&bar_q_full, 1);
+    mbar_init(&bar_q_empty, 1);
+    mbar_init(&bar_drain, 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&bar_k_full[i], 1);
+      mbar_init(&bar_k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&bar_v_full[i], 1);
+      mbar_init(&bar_v_empty[i], 1);
+    }
+    for (int r = 0; r < 2; ++r) {
+      mbar_init(&bar_s_full[r], 1);
+      mbar_init(&bar_p_full[r], kRB);
+      mbar_init(&bar_o_done[r], 1);
+    }
+    mbar_fence_init();
+    s_abort = 0;
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
+  pdl_wait();
+  tc_fence_before();
+  Cursor<kTcKeys> cur = find_share<kTcKeys, kTcThreads>(p);
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  Part w;
+  bool ok = true;
+
+  if (warp == 8 || warp == 10) {
+    // ------------------------------------------------------- K, V producers
+    const bool isV = warp == 10;
+    const CUtensorMap* map = isV ? &tmV : &tmK;
+    uint8_t* ring = isV ? sV : sK;
+    uint64_t* full = isV ? bar_v_full : bar_k_full;
+    uint64_t* empty = isV ? bar_v_empty : bar_k_empty;
+    const uint32_t stages = isV ? kVStages : kKStages;
+    if (!isV && lane == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    const int rows_page = min(1 << p.page_shift, kTcKeys), npg = kTcKeys / rows_page;
+    const int pg = lane % npg, atom = lane / npg, row0 = pg * rows_page;
+    const bool issues = atom < A;
+    uint32_t it = 0;
+    while (ok && cur.next(p, w, !isV && lane == 0 ? p.desc + blockIdx.x : nullptr)) {
+      bool bad = false;
+      int page = w.begin < w.end ? page_at(p, w, w.begin * kTcKeys + row0, rows_page, bad) : 0;
+      for (int t = w.begin; t < w.end; ++t, ++it) {
+        const uint32_t st = it % stages;
+        const int key = t * kTcKeys + row0;
+        bool bad_next = false;
+        int page_next = 0;
+        if (t + 1 < w.end) page_next = page_at(p, w, key + kTcKeys, rows_page, bad_next);
+        ok = warp_wait(&empty[st], ((it / stages) & 1) ^ 1) && !s_abort;
+        if (!ok) break;
+        const uint32_t bad_pages = __ballot_sync(0xffffffffu, bad && lane < npg);
+        if (lane == 0) {
+          if (!isV) {
+            uint32_t m = 0;
+            if (bad_pages)
+              for (int g = 0; g < kTcKeys / 8; ++g) m |= ((bad_pages >> (8 * g / rows_page)) & 1u) << g;
+            s_bad_pages[it % kBadRing] = m;
+          }
+          mbar_expect_tx(&full[st], Lay::kTile);
+        }
+        __syncwarp();
+        if (issues)
+          tma_load_rows(ring + st * Lay::kTile + atom * kAtomBytes + row0 * 128, map, &full[st],
+                        atom * 64, key & ((1 << p.page_shift) - 1), w.kvh, page, p.row_dim, p.head_dim);
+        page = page_next;
+        bad = bad_next;
+      }
+    }
+    // no copy may be in flight when the CTA leaves
+    for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
+      mbar_wait(&full[i % stages], (i / stages) & 1);
+  } else if (warp == 11) {
+    // ----------------------------------------------------------- Q producer
+    uint32_t parts = 0;
+    while (ok && cur.next(p, w, nullptr)) {
+      if (w.begin == w.end) continue;
+      ok = warp_wait(&bar_q_empty, (parts & 1) ^ 1) && !s_abort;
+      if (!ok) break;
+      if (lane == 0) {
+        const int nrb = w.ntok > nb ? 2 : 1;
+        mbar_expect_tx(&bar_q_full, (uint32_t)(nrb * A * 64 * p.G * nb * 2));
+        for (int r = 0; r < nrb; ++r)
+#pragma unroll
+          for (int a = 0; a < A; ++a)
+            tma_load_3d(sQ + (r * A + a) * kAtomBytes, &tmQ, &bar_q_full, a * 64, w.kvh * p.G,
+                        w.s.t0 + w.first + r * nb);
+      }
+      __syncwarp();
+      ++parts;
+    }
+    if (parts > 0) mbar_wait(&bar_q_full, (parts - 1) & 1);
+  } else if (warp == 9) {
+    // ------------------------------------------------------------- products
+    constexpr uint32_t idS = idesc(F16, kTcKeys, 0), idO = idesc(F16, D, 1);
+    const uint64_t dQ = sw128_desc(smem_u32(sQ), 16, 1024);
+    const uint64_t dK = sw128_desc(smem_u32(sK), 16, 1024);
+    const uint64_t dV = sw128_desc(smem_u32(sV), kAtomBytes, 1024);
+    uint32_t kt = 0, vt = 0, parts = 0, pc[2] = {0, 0};
+    // S_r = Q_r K^T (one thread)
+    auto issue_s = [&](int r, uint32_t st) {
+      const uint64_t q = dQ + (uint64_t)(r * (Lay::kTile >> 4)), k = dK + (uint64_t)(st * (Lay::kTile >> 4));
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = ((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4;
+        mma_bf16(tmem + 128 * r, q + off, k + off, idS, kk > 0);
+      }
+      mma_commit(&bar_s_full[r]);
+    };
+    // O_r (+)= P_r V (one thread)
+    auto issue_pv = [&](int r, uint32_t st, bool first) {
+      const uint64_t v = dV + (uint64_t)(st * (Lay::kTile >> 4));
+      mma_bf16_ts(tmem + kOCol + 128 * r, tmem + 128 * r, v, idO, !first);
+#pragma unroll
+      for (int kk = 1; kk < kTcKeys / 16; ++kk)
+        mma_bf16_ts(tmem + kOCol + 128 * r, tmem + 128 * r + 8 * kk, v + (uint64_t)(kk * 128), idO, 1);
+    };
+    while (ok && cur.next(p, w, nullptr)) {
+      const int T = w.end - w.begin, nrb = w.ntok > nb ? 2 : 1;
+      if (T == 0) continue;
+      ok = warp_wait(&bar_q_full, parts & 1) && warp_wait(&bar_k_full[kt % kKStages], (kt / kKStages) & 1);
+      if (!ok) break;
+      ++parts;
+      tc_fence_after();
+      if (elect_one()) {
+        for (int r = 0; r < nrb; ++r) issue_s(r, kt % kKStages);
+        mma_commit(&bar_k_empty[kt % kKStages]);
+        if (T == 1) mma_commit(&bar_q_empty);
+      }
+      __syncwarp();
+      for (int t = 0; t < T; ++t, ++kt, ++vt) {
+        const uint32_t vst = vt % kVStages, kst = (kt + 1) % kKStages;
+        const int j0 = (w.begin + t) * kTcKeys;
+        ok = warp_wait(&bar_v_full[vst], (vt / kVStages) & 1);
+        if (!ok) break;
+        if (w.lo > j0 || w.hi < j0 + kTcKeys) {
+          // rows that no token of the unit sees may hold anything: cleared
+          const int z0 = max(0, w.lo - j0), z1 = min(kTcKeys, w.hi - j0);
+          for (int zr = lane >> 3; zr < kTcKeys; zr += 4)
+            if (zr < z0 || zr >= z1)
+#pragma unroll
+              for (int a = 0; a < A; ++a)
+                *reinterpret_cast<uint4*>(sV + vst * Lay::kTile + a * kAtomBytes + zr * 128 +
+                                          ((lane & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+          __syncwarp();
+        }
+        const bool more = t + 1 < T;
+        for (int r = 0; r < nrb; ++r) {
+          ok = warp_wait(&bar_p_full[r], pc[r] & 1);
+          if (ok && more && r == 0) ok = warp_wait(&bar_k_full[kst], ((kt + 1) / kKStages) & 1);
+          if (!ok) break;
+          ++pc[r];
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(r, vst, t == 0);
+            if (more) issue_s(r, kst);
+            else mma_commit(&bar_o_done[r]);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) {
+          mma_commit(&bar_v_empty[vst]);
+          if (more) mma_commit(&bar_k_empty[kst]);
+          if (t + 2 == T) mma_commit(&bar_q_empty);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) {
+      (void)TV_CHECK(false);
+      s_abort = 1;
+    }
+    if (lane == 0) {  // everything issued retires before TMEM is released
+      mma_commit(&bar_drain);
+      if (!mbar_wait(&bar_drain, 0)) s_abort = 1;
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- softmax
+    write_status(p, 256, 1);
+    const int rb = warp >> 2, row = tid & (kRB - 1);
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + 128 * rb, tO = tmem + kOCol + 128 * rb;
+    const int tl = row / p.G, h_in = row % p.G;
+    const bool warp_in_block = (warp & 3) * 32 < nb * p.G;
+    uint32_t sc = 0, oc = 0, kt = 0;
+    while (ok && cur.next(p, w, nullptr)) {
+      const int T = w.end - w.begin, tile_tok = rb * nb + tl;
+      const bool mine = tl < nb && tile_tok < w.ntok;
+      const int h = w.kvh * p.G + h_in;
+      const size_t oidx = (size_t)(w.s.t0 + w.first + tile_tok) * p.Hq + h;
+      if (T == 0) {  // a sequence with a status
+        if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq)) {
+          uint4* orow = reinterpret_cast<uint4*>(p.out + oidx * D);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) orow[c] = make_uint4(0, 0, 0, 0);
+          if (p.lse) p.lse[oidx] = 0.0f;
+        }
+        continue;
+      }
+      if (rb * nb >= w.ntok) {  // no second row block
+        kt += T;
+        continue;
+      }
+      // rows past the unit take the last token's mask: computed, never written
+      const int i = w.first + min(rb * nb + min(tl, nb - 1), w.ntok - 1);
+      const bool warp_works = warp_in_block && rb * nb + (warp & 3) * 32 / p.G < w.ntok;
+      Row r;
+      r.anc = p.anc ? p.anc + (size_t)(w.s.t0 + i) * p.W : nullptr;
+      r.pos = w.s.L + (p.anc ? anc_count(r.anc, p.W, 64 * p.W) - 1 : i);
+      r.limit = p.anc ? w.s.L : w.s.L + i + 1;
+      r.from = p.window > 0 ? r.pos - p.window + 1 : 0;
+      const float slope = (MOD && p.slopes) ? __ldg(p.slopes + h) * kLog2e : 0.0f;
+      const float scale = MOD ? 1.0f : p.scale_log2;
+      float m_run = -INFINITY, l_run = 0.0f;
+      for (int t = 0; t < T; ++t, ++kt, ++sc) {
+        const int j0 = (w.begin + t) * kTcKeys;
+        uint32_t vis[4];
+        if (j0 + kTcKeys <= r.limit && j0 >= r.from) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) vis[c] = 0xffffffffu;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) vis[c] = see32(p, r, j0 + 32 * c, w.s.L, w.hi);
+        }
+        ok = warp_wait(&bar_s_full[rb], sc & 1);
+        if (!ok) break;
+        if (!warp_works) {
+          mbar_arrive(&bar_p_full[rb]);
+          continue;
+        }
+        const uint32_t bad = s_bad_pages[kt % kBadRing];
+        tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + lane_base + 32 * c, sr[c]);
+        tmem_wait_ld();
+        if (bad) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if ((bad >> (4 * c + g)) & 1u) vis[c] &= ~(0xffu << (8 * g));
+        }
+        if (MOD) {  // to the log2 domain: scale, cap, bias
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float s = __uint_as_float(sr[c][e]);
+              sr[c][e] = __float_as_uint(p.softcap_log2 > 0.0f ? capped(s, p.cap_in, p.softcap_log2)
+                                                               : s * p.scale_log2);
+            }
+          if (!r.anc || j0 + kTcKeys <= w.s.L) {
+            if (p.slopes) {
+              const float d0 = (float)(j0 - r.pos);
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  sr[c][e] = __float_as_uint(fmaf(slope, d0 + (float)(32 * c + e), __uint_as_float(sr[c][e])));
+            }
+          } else {  // the tile reaches the tree: a node's position is its depth's
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int x = j0 + 32 * c - w.s.L;  // tree index of the chunk's first key
+              const int before = x > 0 ? anc_count(r.anc, p.W, min(x, 64 * p.W)) : 0;
+              const uint32_t tree = vis[c] & range_bits(-x, 32);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int kpos = x + e < 0 ? j0 + 32 * c + e
+                                           : w.s.L + before + __popc(tree & (0xffffffffu >> (31 - e))) - 1;
+                if (p.window > 0 && r.pos - kpos >= p.window) vis[c] &= ~(1u << e);
+                sr[c][e] = __float_as_uint(fmaf(slope, (float)(kpos - r.pos), __uint_as_float(sr[c][e])));
+              }
+            }
+          }
+        }
+        if ((vis[0] & vis[1] & vis[2] & vis[3]) != 0xffffffffu) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!((vis[c] >> e) & 1u)) sr[c][e] = __float_as_uint(-INFINITY);
+        }
+        __syncwarp();
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(sr[c][0]);
+#pragma unroll
+          for (int e = 1; e < 31; e += 2)
+            mx[c] = max3(mx[c], __uint_as_float(sr[c][e]), __uint_as_float(sr[c][e + 1]));
+          mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][31]));
+        }
+        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        float corr = 1.0f;
+        bool need = false;
+        if (m_run == -INFINITY) {
+          m_run = tmax;
+        } else if (tmax > m_run + kRescaleLog2) {
+          corr = ex2(m_run - tmax);
+          m_run = tmax;
+          need = true;
+        }
+        const float mm = m_run == -INFINITY ? 0.0f : m_run;  // nothing seen yet: 2^-inf = 0
+        const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(-mm, -mm);
+        float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                        make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = ffma2(make_float2(__uint_as_float(sr[c][2 * e]),
+                                               __uint_as_float(sr[c][2 * e + 1])), sc2, nm2);
+            const float2 x = make_float2(ex2(y.x), ex2(y.y));
+            ps[e & 3] = fadd2(ps[e & 3], x);
+            pw[e] = pack2<F16>(x.x, x.y);
+          }
+          tmem_st16(tS + lane_base + 16 * c, pw);
+        }
+        tmem_wait_st();
+        const float2 pa = fadd2(fadd2(ps[0], ps[1]), fadd2(ps[2], ps[3]));
+        l_run = fmaf(l_run, corr, pa.x + pa.y);
+        if (__any_sync(0xffffffffu, need)) {
+          // O holds every tile up to t - 1: S(t) was issued after PV(t - 1) and has completed
+#pragma unroll
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(tO + lane_base + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+            tmem_st32(tO + lane_base + c, o);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&bar_p_full[rb]);
+      }
+      if (ok) ok = warp_wait(&bar_o_done[rb], oc & 1);
+      if (!ok) break;
+      ++oc;
+      tc_fence_after();
+      if (!warp_works) continue;
+      // ------------------------------------------------------- epilogue
+      const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
+      const int crow = rb * kRB + row;
+      if (w.slot >= 0 && mine) p.part_ml[(size_t)w.slot * 256 + crow] = make_float2(m_run, l_run);
+      float4* dst = reinterpret_cast<float4*>(p.part) + (size_t)max(w.slot, 0) * (D / 4) * 256 + crow;
+      uint4* orow = reinterpret_cast<uint4*>(p.out + oidx * D);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + lane_base + 32 * c, o);
+        tmem_wait_ld();
+        if (mine && w.slot >= 0) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            dst[(size_t)(8 * c + q) * 256] =
+                make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                            __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+        } else if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            orow[4 * c + q] = make_uint4(
+                pack2<F16>(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv),
+                pack2<F16>(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv),
+                pack2<F16>(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv),
+                pack2<F16>(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv));
+        }
+        __syncwarp();
+      }
+      if (w.slot < 0 && mine && p.lse)
+        p.lse[oidx] = l_run > 0.0f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+      tc_fence_before();
+    }
+  }
+  if (!ok) {
+    s_abort = 1;
+    if (lane == 0 && p.status) atomicMax(p.status + w.b, (int)TV_ERR_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();  // every role is done; TMA and MMA work has retired
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D, bool F16, bool MOD>
+cudaError_t launch(const PagedPlan& pl, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                   const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream) {
+  if (!set_dyn_smem(paged_tc_kernel<D, F16, MOD>, TcLayout<D>::kDyn)) return cudaErrorUnknown;
+  return launch_pdl(paged_tc_kernel<D, F16, MOD>, dim3(pl.ctas), dim3(kTcThreads),
+                    (size_t)TcLayout<D>::kDyn, stream, tmQ, tmK, tmV, p, pl.nb);
+}
+
+}  // namespace
+
+cudaError_t launch_tc(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmQ,
+                      const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
+                      cudaStream_t stream) {
+  if (D == 128) {
+    if (f16) return mod ? launch<128, true, true>(pl, tmQ, tmK, tmV, p, stream)
+                        : launch<128, true, false>(pl, tmQ, tmK, tmV, p, stream);
+    return mod ? launch<128, false, true>(pl, tmQ, tmK, tmV, p, stream)
+               : launch<128, false, false>(pl, tmQ, tmK, tmV, p, stream);
+  }
+  if (f16) return mod ? launch<64, true, true>(pl, tmQ, tmK, tmV, p, stream)
+                      : launch<64, true, false>(pl, tmQ, tmK, tmV, p, stream);
+  return mod ? launch<64, false, true>(pl, tmQ, tmK, tmV, p, stream)
+             : launch<64, false, false>(pl, tmQ, tmK, tmV, p, stream);
+}
+
+}  // namespace paged
+}  // namespace tv
