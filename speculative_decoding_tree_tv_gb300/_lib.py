@@ -50,14 +50,9 @@ _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _U64 = ctypes.c_uint64
 _I64 = ctypes.c_int64
-
-
-class PagedCache(ctypes.Structure):
-    """tv_paged_cache."""
-    _fields_ = [("k", _P), ("v", _P), ("page_stride", _I64), ("head_stride", _I64),
-                ("row_stride", _I64), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32)]
-
+# tv_paged_cache for struct.pack: k, v; page, head and row strides; num_pages,
+# page_size, Hkv, D, dtype (a bytes object passes as a pointer argument)
+PAGED_CACHE_FORMAT = "PPqqqiiiii"
 
 _SIGS = {
     "tv_status_string": (ctypes.c_char_p, [_I]),

@@ -2,11 +2,12 @@
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Callable, Optional
 
 import torch
 
-from ._lib import TV_BF16, TV_FP16, TV_MAX_NODES, PagedCache, check, lib
+from ._lib import PAGED_CACHE_FORMAT, TV_BF16, TV_FP16, TV_MAX_NODES, TVError, check, lib
 
 __all__ = ["tree_build", "attn_verify", "accept_greedy", "accept_sample", "expand_gated",
            "expand_tree", "commit_path", "expected_accept", "build_spine_tree", "spine_ratio_update", "workspace", "attn_workspace_size", "attn_plan", "greedy_workspace_size",
@@ -464,36 +465,64 @@ def expand_tree(draft_rows: Callable, root_key, child_key: Callable, topk: int, 
 
 # ---------------------------------------------------------------------------
 # Paged KV cache
+#
+# These calls run once per layer or per step of a serving loop and take a few
+# microseconds on the GPU, so what the host does for each counts.  Arguments
+# are checked in one expression; only when it fails are they checked
+# one by one, for the error that names the argument.
 # ---------------------------------------------------------------------------
 _CACHE_DTYPES = {torch.bfloat16: TV_BF16, torch.float16: TV_FP16}
+_pack_cache = struct.Struct(PAGED_CACHE_FORMAT).pack
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 
-def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> PagedCache:
+def _call(fn, name: str, dev: torch.device, *args) -> None:
+    """fn(*args, stream) on dev's current stream, with dev the current device."""
+    index = dev.index
+    if index == _current_device():
+        code = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, _raw_stream(index))
+    if code:
+        raise TVError(name, code)
+
+
+def _is(t: torch.Tensor, dtype, shape, dev) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()
+
+
+def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> bytes:
     """tv_paged_cache of k_pages, v_pages [num_pages, Hkv, page_size, D]: any
     strides with D contiguous, the same for both (a [num_pages, page_size, Hkv, D]
     cache goes in as its .transpose(1, 2))."""
+    try:
+        n, Hkv, page, D = shape = k_pages.shape
+        s0, s1, s2, s3 = strides = k_pages.stride()
+        if (k_pages.is_cuda and s3 == 1 and v_pages.shape == shape and v_pages.stride() == strides
+                and v_pages.dtype is k_pages.dtype and v_pages.device == k_pages.device):
+            return _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), s0, s1, s2, n, page, Hkv, D,
+                               _CACHE_DTYPES[k_pages.dtype])
+    except (AttributeError, KeyError, TypeError, ValueError):
+        pass
     for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    dtype = _CACHE_DTYPES.get(k_pages.dtype)
-    if dtype is None:
-        raise TypeError(f"k_pages must be torch.bfloat16 or torch.float16, got {k_pages.dtype}")
+        if t.dtype not in _CACHE_DTYPES:
+            raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
     if v_pages.dtype != k_pages.dtype:
         raise TypeError(f"v_pages must be {k_pages.dtype}, got {v_pages.dtype}")
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must both be [num_pages, Hkv, page_size, D]")
-    strides = k_pages.stride()
-    if strides != v_pages.stride():
+    if k_pages.stride() != v_pages.stride():
         raise ValueError("k_pages and v_pages must have the same strides")
-    if strides[3] != 1:
-        raise ValueError("the last dimension of k_pages and v_pages must be contiguous")
     if v_pages.device != k_pages.device:
         raise ValueError(f"v_pages is on {v_pages.device}, expected {k_pages.device}")
-    n, Hkv, page, D = k_pages.shape
-    return PagedCache(k_pages.data_ptr(), v_pages.data_ptr(), strides[0], strides[1], strides[2], n,
-                      page, Hkv, D, dtype)
+    raise ValueError("the last dimension of k_pages and v_pages must be contiguous")
 
 
 def _need_rows(t: torch.Tensor, name: str, dtype, shape, device):
@@ -510,13 +539,11 @@ def _need_rows(t: torch.Tensor, name: str, dtype, shape, device):
         raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
-def _call(fn: str, dev: torch.device, *args) -> None:
-    """Call the library's `fn` on dev's current stream, with dev the current device."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        check(fn, getattr(lib, fn)(*args, _stream(dev)))
-    else:
-        with torch.cuda.device(dev):
-            check(fn, getattr(lib, fn)(*args, _stream(dev)))
+def _table_shape(block_table: torch.Tensor):
+    _need(block_table, "block_table", _I32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have shape [B, P]")
+    return block_table.shape
 
 
 def attn_paged_workspace_size(max_q, Hq, Hkv, D) -> int:
@@ -533,49 +560,62 @@ def page_map(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Ten
     sequence); kv_len, n_pages int32 [B]; block_table int32 [B, P]; free_list
     int32 [num_pages]; n_free int32 [1]; tokens = length of the slot map.
     Returns (slots int64 [tokens], status int32 [B])."""
-    _need(block_table, "block_table", torch.int32)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have shape [B, P]")
-    B, P = block_table.shape
+    B, P = _table_shape(block_table)
     dev = block_table.device
-    _need(q_start, "q_start", torch.int32, (B + 1,), dev)
-    _need(kv_len, "kv_len", torch.int32, (B,), dev)
-    _need(n_pages, "n_pages", torch.int32, (B,), dev)
-    _need(free_list, "free_list", torch.int32, (free_list.numel(),), dev)
-    _need(n_free, "n_free", torch.int32, (1,), dev)
-    slots = torch.empty(tokens, dtype=torch.int64, device=dev) if slots is None else slots
-    _need(slots, "slots", torch.int64, (tokens,), dev)
-    status = torch.empty(B, dtype=torch.int32, device=dev) if status is None else status
-    _need(status, "status", torch.int32, (B,), dev)
-    _call(
-        "tv_page_map", dev, q_start.data_ptr(), kv_len.data_ptr(), B, int(tokens), P, int(page_size),
-        free_list.numel(), block_table.data_ptr(), n_pages.data_ptr(), free_list.data_ptr(), n_free.data_ptr(),
-        slots.data_ptr(), status.data_ptr())
+    if slots is None:
+        slots = torch.empty(tokens, dtype=_I64, device=dev)
+    if status is None:
+        status = torch.empty(B, dtype=_I32, device=dev)
+    try:
+        pool = free_list.numel()
+        good = (_is(q_start, _I32, (B + 1,), dev) and _is(kv_len, _I32, (B,), dev)
+                and _is(n_pages, _I32, (B,), dev) and _is(free_list, _I32, (pool,), dev)
+                and _is(n_free, _I32, (1,), dev) and _is(slots, _I64, (tokens,), dev)
+                and _is(status, _I32, (B,), dev))
+    except AttributeError:
+        good = False
+    if not good:
+        _need(q_start, "q_start", _I32, (B + 1,), dev)
+        _need(kv_len, "kv_len", _I32, (B,), dev)
+        _need(n_pages, "n_pages", _I32, (B,), dev)
+        _need(free_list, "free_list", _I32, (free_list.numel(),), dev)
+        _need(n_free, "n_free", _I32, (1,), dev)
+        _need(slots, "slots", _I64, (tokens,), dev)
+        _need(status, "status", _I32, (B,), dev)
+    _call(lib.tv_page_map, "tv_page_map", dev, q_start.data_ptr(), kv_len.data_ptr(), B, int(tokens),
+          P, int(page_size), pool, block_table.data_ptr(), n_pages.data_ptr(),
+          free_list.data_ptr(), n_free.data_ptr(), slots.data_ptr(), status.data_ptr())
     return slots, status
 
 
 def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor,
-                 v_pages: torch.Tensor, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+                 v_pages: torch.Tensor, status: Optional[torch.Tensor] = None) -> None:
     """Write k, v [T, Hkv, D] (views of a fused projection are fine) into the
-    cache rows slots int64 [T] name; negative slots write nothing.  k_pages,
-    v_pages [num_pages, Hkv, page_size, D] bf16 or fp16.  Returns status int32 [T]."""
+    cache rows slots int64 [T] name; negative slots, and slots past the cache, write
+    nothing.  k_pages, v_pages [num_pages, Hkv, page_size, D] bf16 or fp16.  status int32
+    [T], if given, tells of slots past the cache."""
     cache = _cache(k_pages, v_pages)
-    dev = k_pages.device
-    _need(slots, "slots", torch.int64, None, dev)
-    if slots.dim() != 1:
-        raise ValueError("slots must have shape [T]")
-    T = slots.numel()
-    shape = (T, cache.Hkv, cache.D)
-    _need_rows(k, "k", k_pages.dtype, shape, dev)
-    _need_rows(v, "v", k_pages.dtype, shape, dev)
-    if k.stride() != v.stride():
+    dev, dtype = k_pages.device, k_pages.dtype
+    _, Hkv, _, D = k_pages.shape
+    try:
+        T = slots.numel()
+        shape, strides = (T, Hkv, D), k.stride()
+        good = (_is(slots, _I64, (T,), dev) and k.shape == shape and v.shape == shape
+                and k.dtype is dtype and v.dtype is dtype and k.device == dev and v.device == dev
+                and v.stride() == strides and strides[2] == 1)
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _need(slots, "slots", _I64, None, dev)
+        if slots.dim() != 1:
+            raise ValueError("slots must have shape [T]")
+        _need_rows(k, "k", dtype, (T, Hkv, D), dev)
+        _need_rows(v, "v", dtype, (T, Hkv, D), dev)
         raise ValueError("k and v must have the same strides")
-    status = torch.empty(T, dtype=torch.int32, device=dev) if status is None else status
-    _need(status, "status", torch.int32, (T,), dev)
-    _call(
-        "tv_paged_append", dev, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1),
-        slots.data_ptr(), T, ctypes.addressof(cache), status.data_ptr())
-    return status
+    if status is not None:
+        _need(status, "status", _I32, (T,), dev)
+    _call(lib.tv_paged_append, "tv_paged_append", dev, k.data_ptr(), v.data_ptr(), strides[0],
+          strides[1], slots.data_ptr(), T, cache, _ptr(status))
 
 
 def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -593,40 +633,51 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     slopes float32 [Hq] subtracts slope * distance, window hides keys that far
     back.  Returns (out [T, Hq, D], lse float32 [T, Hq], status int32 [B])."""
     cache = _cache(k_pages, v_pages)
-    dev = k_pages.device
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a tensor [T, Hq, D]")
-    T, Hq, D = q.shape
-    _need_rows(q, "q", k_pages.dtype, (T, Hq, cache.D), dev)
-    _need(block_table, "block_table", torch.int32, None, dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have shape [B, P]")
-    B, P = block_table.shape
-    _need(q_start, "q_start", torch.int32, (B + 1,), dev)
-    _need(kv_len, "kv_len", torch.int32, (B,), dev)
+    dev, dtype = k_pages.device, k_pages.dtype
+    _, Hkv, _, Dc = k_pages.shape
+    B, P = _table_shape(block_table)
+    max_q = int(max_q)
+    try:
+        T, Hq, D = shape = q.shape
+        strides = q.stride()
+        good = (D == Dc and q.dtype is dtype and q.device == dev and strides[2] == 1
+                and block_table.device == dev and _is(q_start, _I32, (B + 1,), dev)
+                and _is(kv_len, _I32, (B,), dev))
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a tensor [T, Hq, D]")
+        _need_rows(q, "q", dtype, (T, Hq, Dc), dev)
+        _need(block_table, "block_table", _I32, None, dev)
+        _need(q_start, "q_start", _I32, (B + 1,), dev)
+        _need(kv_len, "kv_len", _I32, (B,), dev)
     if anc_mask is not None:
-        _need(anc_mask, "anc_mask", torch.int64, None, dev)
-        W = (int(max_q) + 63) // 64
+        _need(anc_mask, "anc_mask", _I64, None, dev)
+        W = (max_q + 63) // 64
         if anc_mask.numel() != T * W:
             raise ValueError(f"anc_mask must have shape {(T, W)}, got {tuple(anc_mask.shape)}")
     if slopes is not None:
-        _need(slopes, "slopes", torch.float32, (Hq,), dev)
-    out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out
-    _need(out, "out", q.dtype, (T, Hq, D), dev)
-    if want_lse and lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        _need(slopes, "slopes", _F32, (Hq,), dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(out, "out", dtype, shape, dev)
     if lse is not None:
-        _need(lse, "lse", torch.float32, (T, Hq), dev)
-    status = torch.empty(B, dtype=torch.int32, device=dev) if status is None else status
-    _need(status, "status", torch.int32, (B,), dev)
+        _need(lse, "lse", _F32, (T, Hq), dev)
+    elif want_lse:
+        lse = torch.empty((T, Hq), dtype=_F32, device=dev)
+    if status is None:
+        status = torch.empty(B, dtype=_I32, device=dev)
+    else:
+        _need(status, "status", _I32, (B,), dev)
     if ws is None:  # from torch's allocator: ordered by stream, and a captured graph's own
-        ws = torch.empty(attn_paged_workspace_size(int(max_q), Hq, cache.Hkv, D), dtype=torch.uint8,
+        ws = torch.empty(lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D), dtype=torch.uint8,
                          device=dev)
-    _call(
-        "tv_attn_paged", dev, q.data_ptr(), q.stride(0), q.stride(1), ctypes.addressof(cache),
-        block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), _ptr(anc_mask), _ptr(slopes),
-        B, T, P, Hq, int(max_q), float(scale), float(softcap), int(window), out.data_ptr(), _ptr(lse), status.data_ptr(),
-        ws.data_ptr(), ws.numel())
+    _call(lib.tv_attn_paged, "tv_attn_paged", dev, q.data_ptr(), strides[0], strides[1], cache,
+          block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), _ptr(anc_mask),
+          _ptr(slopes), B, T, P, Hq, max_q, scale, softcap, window, out.data_ptr(), _ptr(lse),
+          status.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse, status
 
 
@@ -640,20 +691,28 @@ def commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torc
     Returns (new_kv_len int32 [B], status int32 [B])."""
     cache = _cache(k_pages, v_pages)
     dev = k_pages.device
-    _need(block_table, "block_table", torch.int32, None, dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must have shape [B, P]")
-    B, P = block_table.shape
-    _need(path, "path", torch.int32, None, dev)
-    if path.dim() != 2 or path.shape[0] != B:
-        raise ValueError(f"path must have shape [B, N] with B = {B}")
-    _need(kv_len, "kv_len", torch.int32, (B,), dev)
-    _need(accept_len, "accept_len", torch.int32, (B,), dev)
-    new_kv_len = torch.empty(B, dtype=torch.int32, device=dev) if new_kv_len is None else new_kv_len
-    _need(new_kv_len, "new_kv_len", torch.int32, (B,), dev)
-    status = torch.empty(B, dtype=torch.int32, device=dev) if status is None else status
-    _need(status, "status", torch.int32, (B,), dev)
-    _call(
-        "tv_commit_paged", dev, ctypes.addressof(cache), block_table.data_ptr(), kv_len.data_ptr(),
-        path.data_ptr(), accept_len.data_ptr(), B, path.shape[1], P, new_kv_len.data_ptr(), status.data_ptr())
+    B, P = _table_shape(block_table)
+    if new_kv_len is None:
+        new_kv_len = torch.empty(B, dtype=_I32, device=dev)
+    if status is None:
+        status = torch.empty(B, dtype=_I32, device=dev)
+    try:
+        N = path.shape[1]
+        good = (block_table.device == dev and _is(path, _I32, (B, N), dev)
+                and _is(kv_len, _I32, (B,), dev) and _is(accept_len, _I32, (B,), dev)
+                and _is(new_kv_len, _I32, (B,), dev) and _is(status, _I32, (B,), dev))
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _need(block_table, "block_table", _I32, None, dev)
+        _need(path, "path", _I32, None, dev)
+        if path.dim() != 2 or path.shape[0] != B:
+            raise ValueError(f"path must have shape [B, N] with B = {B}")
+        _need(kv_len, "kv_len", _I32, (B,), dev)
+        _need(accept_len, "accept_len", _I32, (B,), dev)
+        _need(new_kv_len, "new_kv_len", _I32, (B,), dev)
+        _need(status, "status", _I32, (B,), dev)
+    _call(lib.tv_commit_paged, "tv_commit_paged", dev, cache, block_table.data_ptr(),
+          kv_len.data_ptr(), path.data_ptr(), accept_len.data_ptr(), B, N, P,
+          new_kv_len.data_ptr(), status.data_ptr())
     return new_kv_len, status

@@ -2,6 +2,7 @@
 plain page map of the GPU tests pinned by its own invariants."""
 import ctypes
 import random
+import struct
 
 import pytest
 
@@ -21,15 +22,12 @@ ODD = ctypes.c_void_p(0x1008)
 
 
 def cache(tv, **kw):
-    from speculative_decoding_tree_tv_gb300._lib import PagedCache
+    from speculative_decoding_tree_tv_gb300._lib import PAGED_CACHE_FORMAT
     f = dict(k=0x1000, v=0x1000, page_stride=16 * 64 * 2, head_stride=16 * 64, row_stride=64, num_pages=10,
              page_size=16, Hkv=2, D=64, dtype=0)
     f.update(kw)
-    return PagedCache(**f)
-
-
-def addr(c):
-    return ctypes.addressof(c)
+    f["k"] = f["k"] or 0
+    return struct.pack(PAGED_CACHE_FORMAT, *f.values())
 
 
 BAD_CACHES = [(dict(num_pages=0), 1), (dict(Hkv=0), 1), (dict(D=0), 1), (dict(dtype=2), 3),
@@ -41,8 +39,8 @@ BAD_CACHES = [(dict(num_pages=0), 1), (dict(Hkv=0), 1), (dict(D=0), 1), (dict(dt
 @pytest.mark.parametrize("kw,code", BAD_CACHES)
 def test_bad_caches_are_refused(tvlib, kw, code):
     lib, c = tvlib.lib, cache(tvlib, **kw)
-    assert lib.tv_paged_append(D, D, 128, 64, D, 4, addr(c), D, None) == code
-    assert lib.tv_commit_paged(addr(c), D, D, D, D, 1, 4, 4, D, D, None) == code
+    assert lib.tv_paged_append(D, D, 128, 64, D, 4, c, D, None) == code
+    assert lib.tv_commit_paged(c, D, D, D, D, 1, 4, 4, D, D, None) == code
     assert attn(lib, c) == code
     assert lib.tv_paged_append(D, D, 128, 64, D, 4, None, D, None) == 1
 
@@ -51,7 +49,7 @@ def attn(lib, c, **kw):
     a = dict(q=D, qt=256, qh=64, table=D, q_start=D, kv_len=D, anc=None, slopes=None, B=1, T=4, P=4, Hq=4,
              max_q=4, scale=0.0, softcap=0.0, window=0, out=D, lse=None, status=None, ws=D, n=0)
     a.update(kw)
-    return lib.tv_attn_paged(a["q"], a["qt"], a["qh"], addr(c), a["table"], a["q_start"], a["kv_len"], a["anc"],
+    return lib.tv_attn_paged(a["q"], a["qt"], a["qh"], c, a["table"], a["q_start"], a["kv_len"], a["anc"],
                              a["slopes"], a["B"], a["T"], a["P"], a["Hq"], a["max_q"], a["scale"], a["softcap"],
                              a["window"], a["out"], a["lse"], a["status"], a["ws"], a["n"], None)
 
@@ -91,7 +89,7 @@ def test_page_map_arguments_are_checked(tvlib):
 def test_append_and_commit_arguments_are_checked(tvlib):
     lib, c = tvlib.lib, cache(tvlib)
     ap = lambda **k: lib.tv_paged_append(k.get("k", D), k.get("v", D), k.get("t", 128), k.get("h", 64),  # noqa: E731
-                                         k.get("slots", D), k.get("T", 4), addr(k.get("c", c)), None, None)
+                                         k.get("slots", D), k.get("T", 4), k.get("c", c), None, None)
     for kw in (dict(T=-1), dict(k=None), dict(v=None), dict(slots=None), dict(t=3), dict(h=-8), dict(k=ODD)):
         assert ap(**kw) == tvlib.TV_ERR_INVALID_ARG, kw
     for kw in (dict(c=cache(tvlib, D=12)), dict(c=cache(tvlib, D=1032)), dict(T=2**30)):
@@ -100,7 +98,7 @@ def test_append_and_commit_arguments_are_checked(tvlib):
     other = ctypes.c_void_p(0x2000)
 
     def cm(c=c, table=D, kv=D, path=D, acc=D, B=1, N=4, P=4, new=other, st=D):
-        return lib.tv_commit_paged(addr(c), table, kv, path, acc, B, N, P, new, st, None)
+        return lib.tv_commit_paged(c, table, kv, path, acc, B, N, P, new, st, None)
     for kw in (dict(B=-1), dict(N=0), dict(N=513), dict(P=0), dict(table=None), dict(kv=None), dict(path=None),
                dict(acc=None), dict(new=None), dict(st=None), dict(new=D)):
         assert cm(**kw) == tvlib.TV_ERR_INVALID_ARG, kw
