@@ -42,6 +42,19 @@ constexpr uint32_t idesc(bool f16, int N, int b_mn) {
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRB >> 4) << 24);
 }
 
+// 8 consecutive 32-bit TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // What one row sees.
 struct Row {
   const uint64_t* anc;  // mask row, or nullptr (causal)
@@ -75,7 +88,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   __shared__ __align__(8) uint64_t bar_q_full, bar_q_empty, bar_drain;
   __shared__ __align__(8) uint64_t bar_k_full[kKStages], bar_k_empty[kKStages];
   __shared__ __align__(8) uint64_t bar_v_full[kVStages], bar_v_empty[kVStages];
-  __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_full[2], bar_o_done[2];
+  // (one per stage: the loads run up to three tiles ahead, and a barrier that is two phases
+  // ahead of its reader cannot be told from one that is not ready)
+  __shared__ __align__(8) uint64_t bar_v_zero[kVStages];
+  __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_full[2][2], bar_o_done[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_bad_pages[kBadRing];  // bit g: keys 8 g .. 8 g + 7 have no page
   __shared__ volatile int s_abort;
@@ -92,10 +108,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(&bar_v_full[i], 1);
       mbar_init(&bar_v_empty[i], 1);
+      mbar_init(&bar_v_zero[i], 1);
     }
     for (int r = 0; r < 2; ++r) {
       mbar_init(&bar_s_full[r], 1);
-      mbar_init(&bar_p_full[r], kRB);
+      mbar_init(&bar_p_full[r][0], 4);  // one arrival a warp: those of 128 threads queue up
+      mbar_init(&bar_p_full[r][1], 4);  // for some 400 cycles
       mbar_init(&bar_o_done[r], 1);
     }
     mbar_fence_init();
@@ -112,7 +130,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   const uint32_t tmem = s_tmem;
   Part w;
   bool ok = true;
-
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------------- K, V producers
     const bool isV = warp == 10;
@@ -126,6 +143,27 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int pg = lane % npg, atom = lane / npg, row0 = pg * rows_page;
     const bool issues = atom < A;
     uint32_t it = 0;
+    // Rows of V before lo and from hi on may hold anything (NaN times a probability of 0 is
+    // NaN): cleared in the tiles that have them (a unit's first and last at most), once the
+    // tile after them is on its way.
+    uint32_t z_it = 0;
+    int z0 = 0, z1 = kTcKeys;
+    auto clear_rows = [&]() {
+      if (z0 == 0 && z1 == kTcKeys) return;
+      const uint32_t st = z_it % stages;
+      ok = warp_wait(&full[st], (z_it / stages) & 1);
+      for (int zr = lane >> 3; zr < kTcKeys; zr += 4)
+        if (zr < z0 || zr >= z1)
+#pragma unroll
+          for (int a = 0; a < A; ++a)
+            *reinterpret_cast<uint4*>(ring + st * Lay::kTile + a * kAtomBytes + zr * 128 +
+                                      ((lane & 7) << 4)) = make_uint4(0, 0, 0, 0);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_v_zero[st]);
+      z0 = 0;
+      z1 = kTcKeys;
+    };
     while (ok && cur.next(p, w, !isV && lane == 0 ? p.desc + blockIdx.x : nullptr)) {
       bool bad = false;
       int page = w.begin < w.end ? page_at(p, w, w.begin * kTcKeys + row0, rows_page, bad) : 0;
@@ -153,8 +191,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         atom * 64, key & ((1 << p.page_shift) - 1), w.kvh, page, p.row_dim, p.head_dim);
         page = page_next;
         bad = bad_next;
+        if (isV) {
+          clear_rows();
+          if (!ok) break;
+          z_it = it;
+          z0 = max(0, w.lo - t * kTcKeys);
+          z1 = min(kTcKeys, w.hi - t * kTcKeys);
+        }
       }
     }
+    if (isV && ok) clear_rows();
     // no copy may be in flight when the CTA leaves
     for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
       mbar_wait(&full[i % stages], (i / stages) & 1);
@@ -180,91 +226,90 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     if (parts > 0) mbar_wait(&bar_q_full, (parts - 1) & 1);
   } else if (warp == 9) {
     // ------------------------------------------------------------- products
-    constexpr uint32_t idS = idesc(F16, kTcKeys, 0), idO = idesc(F16, D, 1);
-    const uint64_t dQ = sw128_desc(smem_u32(sQ), 16, 1024);
-    const uint64_t dK = sw128_desc(smem_u32(sK), 16, 1024);
-    const uint64_t dV = sw128_desc(smem_u32(sV), kAtomBytes, 1024);
-    uint32_t kt = 0, vt = 0, parts = 0, pc[2] = {0, 0};
-    // S_r = Q_r K^T (one thread)
-    auto issue_s = [&](int r, uint32_t st) {
-      const uint64_t q = dQ + (uint64_t)(r * (Lay::kTile >> 4)), k = dK + (uint64_t)(st * (Lay::kTile >> 4));
+    // One thread waits and issues: what it does between two products is on the critical
+    // path of both row blocks (with the whole warp waiting and voting, a barrier that
+    // had completed already cost some 150 cycles).
+    if (elect_one()) {
+      constexpr uint32_t idS = idesc(F16, kTcKeys, 0), idO = idesc(F16, D, 1);
+      const uint64_t dQ = sw128_desc(smem_u32(sQ), 16, 1024);
+      const uint64_t dK = sw128_desc(smem_u32(sK), 16, 1024);
+      const uint64_t dV = sw128_desc(smem_u32(sV), kAtomBytes, 1024);
+      uint32_t kst = 0, kph = 0, vst = 0, vph = 0, qph = 0, zph = 0, pph[2] = {0, 0};
+      // S_r = Q_r K^T
+      auto issue_s = [&](int r) {
+        const uint64_t q = dQ + (uint64_t)(r * (Lay::kTile >> 4)), k = dK + (uint64_t)(kst * (Lay::kTile >> 4));
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t off = ((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4;
-        mma_bf16(tmem + 128 * r, q + off, k + off, idS, kk > 0);
-      }
-      mma_commit(&bar_s_full[r]);
-    };
-    // O_r (+)= P_r V (one thread)
-    auto issue_pv = [&](int r, uint32_t st, bool first) {
-      const uint64_t v = dV + (uint64_t)(st * (Lay::kTile >> 4));
-      mma_bf16_ts(tmem + kOCol + 128 * r, tmem + 128 * r, v, idO, !first);
-#pragma unroll
-      for (int kk = 1; kk < kTcKeys / 16; ++kk)
-        mma_bf16_ts(tmem + kOCol + 128 * r, tmem + 128 * r + 8 * kk, v + (uint64_t)(kk * 128), idO, 1);
-    };
-    while (ok && cur.next(p, w, nullptr)) {
-      const int T = w.end - w.begin, nrb = w.ntok > nb ? 2 : 1;
-      if (T == 0) continue;
-      ok = warp_wait(&bar_q_full, parts & 1) && warp_wait(&bar_k_full[kt % kKStages], (kt / kKStages) & 1);
-      if (!ok) break;
-      ++parts;
-      tc_fence_after();
-      if (elect_one()) {
-        for (int r = 0; r < nrb; ++r) issue_s(r, kt % kKStages);
-        mma_commit(&bar_k_empty[kt % kKStages]);
-        if (T == 1) mma_commit(&bar_q_empty);
-      }
-      __syncwarp();
-      for (int t = 0; t < T; ++t, ++kt, ++vt) {
-        const uint32_t vst = vt % kVStages, kst = (kt + 1) % kKStages;
-        const int j0 = (w.begin + t) * kTcKeys;
-        ok = warp_wait(&bar_v_full[vst], (vt / kVStages) & 1);
-        if (!ok) break;
-        if (w.lo > j0 || w.hi < j0 + kTcKeys) {
-          // rows that no token of the unit sees may hold anything: cleared
-          const int z0 = max(0, w.lo - j0), z1 = min(kTcKeys, w.hi - j0);
-          for (int zr = lane >> 3; zr < kTcKeys; zr += 4)
-            if (zr < z0 || zr >= z1)
-#pragma unroll
-              for (int a = 0; a < A; ++a)
-                *reinterpret_cast<uint4*>(sV + vst * Lay::kTile + a * kAtomBytes + zr * 128 +
-                                          ((lane & 7) << 4)) = make_uint4(0, 0, 0, 0);
-          fence_async_smem();
-          __syncwarp();
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = ((kk >> 2) * kAtomBytes + (kk & 3) * 32) >> 4;
+          mma_bf16(tmem + 128 * r, q + off, k + off, idS, kk > 0);
         }
-        const bool more = t + 1 < T;
-        for (int r = 0; r < nrb; ++r) {
-          ok = warp_wait(&bar_p_full[r], pc[r] & 1);
-          if (ok && more && r == 0) ok = warp_wait(&bar_k_full[kst], ((kt + 1) / kKStages) & 1);
-          if (!ok) break;
-          ++pc[r];
-          tc_fence_after();
-          if (elect_one()) {
-            issue_pv(r, vst, t == 0);
-            if (more) issue_s(r, kst);
+        mma_commit(&bar_s_full[r]);
+      };
+      // O_r (+)= P_r V over the tile's first or last 64 keys
+      auto issue_pv = [&](int r, int half, bool first) {
+        const uint64_t v = dV + (uint64_t)(vst * (Lay::kTile >> 4) + half * 512);
+        const uint32_t tP = tmem + 128 * r + 32 * half;
+        mma_bf16_ts(tmem + kOCol + 128 * r, tP, v, idO, !first);
+#pragma unroll
+        for (int kk = 1; kk < kTcKeys / 32; ++kk)
+          mma_bf16_ts(tmem + kOCol + 128 * r, tP + 8 * kk, v + (uint64_t)(kk * 128), idO, 1);
+      };
+      auto next_k = [&]() {
+        kph ^= kst == kKStages - 1;
+        kst = kst == kKStages - 1 ? 0 : kst + 1;
+      };
+      while (ok && cur.next(p, w, nullptr)) {
+        const int T = w.end - w.begin, nrb = w.ntok > nb ? 2 : 1;
+        if (T == 0) continue;
+        ok = mbar_wait(&bar_q_full, qph) && mbar_wait(&bar_k_full[kst], kph);
+        if (!ok) break;
+        qph ^= 1;
+        tc_fence_after();
+        for (int r = 0; r < nrb; ++r) issue_s(r);
+        mma_commit(&bar_k_empty[kst]);
+        next_k();
+        if (T == 1) mma_commit(&bar_q_empty);
+        for (int t = 0; t < T; ++t) {
+          const int j0 = (w.begin + t) * kTcKeys;
+          const bool more = t + 1 < T;
+          ok = mbar_wait(&bar_v_full[vst], vph);
+          if (w.lo > j0 || w.hi < j0 + kTcKeys) {  // the V producer clears rows of this tile
+            ok = ok && mbar_wait(&bar_v_zero[vst], (zph >> vst) & 1);
+            zph ^= 1u << vst;
+          }
+          if (more) ok = ok && mbar_wait(&bar_k_full[kst], kph);
+          for (int r = 0; ok && r < nrb; ++r) {
+            ok = mbar_wait(&bar_p_full[r][0], pph[r]);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(r, 0, t == 0);
+            ok = mbar_wait(&bar_p_full[r][1], pph[r]);
+            if (!ok) break;
+            pph[r] ^= 1;
+            tc_fence_after();
+            issue_pv(r, 1, false);
+            if (more) issue_s(r);
             else mma_commit(&bar_o_done[r]);
           }
-          __syncwarp();
-        }
-        if (!ok) break;
-        if (elect_one()) {
+          if (!ok) break;
           mma_commit(&bar_v_empty[vst]);
-          if (more) mma_commit(&bar_k_empty[kst]);
+          vph ^= vst == kVStages - 1;
+          vst = vst == kVStages - 1 ? 0 : vst + 1;
+          if (more) {
+            mma_commit(&bar_k_empty[kst]);
+            next_k();
+          }
           if (t + 2 == T) mma_commit(&bar_q_empty);
         }
-        __syncwarp();
       }
-    }
-    if (!ok) {
-      (void)TV_CHECK(false);
-      s_abort = 1;
-    }
-    if (lane == 0) {  // everything issued retires before TMEM is released
-      mma_commit(&bar_drain);
+      if (!ok) {
+        (void)TV_CHECK(false);
+        s_abort = 1;
+      }
+      mma_commit(&bar_drain);  // everything issued retires before TMEM is released
       if (!mbar_wait(&bar_drain, 0)) s_abort = 1;
     }
-    __syncwarp();
+    ok = __all_sync(0xffffffffu, ok);
   } else {
     // -------------------------------------------------------------- softmax
     write_status(p, 256, 1);
@@ -316,7 +361,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         ok = warp_wait(&bar_s_full[rb], sc & 1);
         if (!ok) break;
         if (!warp_works) {
-          mbar_arrive(&bar_p_full[rb]);
+          if (lane == 0) {
+            mbar_arrive(&bar_p_full[rb][0]);
+            mbar_arrive(&bar_p_full[rb][1]);
+          }
           continue;
         }
         const uint32_t bad = s_bad_pages[kt % kBadRing];
@@ -374,6 +422,20 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               if (!((vis[c] >> e) & 1u)) sr[c][e] = __float_as_uint(-INFINITY);
         }
         __syncwarp();
+        // Probabilities of 32 keys against the maximum m: their sums into ps, packed pairs to pw.
+        float2 ps[4] = {};
+        const float2 sc2 = make_float2(scale, scale);
+        auto probs = [&](int c, float m, uint32_t (&pw)[16]) {
+          const float2 nm2 = make_float2(-m, -m);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = ffma2(make_float2(__uint_as_float(sr[c][2 * e]),
+                                               __uint_as_float(sr[c][2 * e + 1])), sc2, nm2);
+            const float2 x = make_float2(ex2(y.x), ex2(y.y));
+            ps[e & 3] = fadd2(ps[e & 3], x);
+            pw[e] = pack2<F16>(x.x, x.y);
+          }
+        };
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -384,50 +446,40 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][31]));
         }
         const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-        float corr = 1.0f;
-        bool need = false;
-        if (m_run == -INFINITY) {
-          m_run = tmax;
-        } else if (tmax > m_run + kRescaleLog2) {
-          corr = ex2(m_run - tmax);
-          m_run = tmax;
-          need = true;
+        const bool moves = m_run == -INFINITY || tmax > m_run + kRescaleLog2;
+        if (__any_sync(0xffffffffu, moves)) {
+          const float m_new = moves ? tmax : m_run;
+          const float corr = moves && m_run != -INFINITY ? ex2(m_run - m_new) : 1.0f;
+          m_run = m_new;
+          l_run *= corr;
+          if (t > 0) {
+            // O holds every tile up to t - 1: S(t) was issued after PV(t - 1) and has completed
+#pragma unroll 1
+            for (int c = 0; c < D; c += 8) {  // (few at a time: the scores hold the registers)
+              uint32_t o[8];
+              tmem_ld8(tO + lane_base + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              tmem_st8(tO + lane_base + c, o);
+            }
+          }
         }
         const float mm = m_run == -INFINITY ? 0.0f : m_run;  // nothing seen yet: 2^-inf = 0
-        const float2 sc2 = make_float2(scale, scale), nm2 = make_float2(-mm, -mm);
-        float2 ps[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                        make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pw[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 y = ffma2(make_float2(__uint_as_float(sr[c][2 * e]),
-                                               __uint_as_float(sr[c][2 * e + 1])), sc2, nm2);
-            const float2 x = make_float2(ex2(y.x), ex2(y.y));
-            ps[e & 3] = fadd2(ps[e & 3], x);
-            pw[e] = pack2<F16>(x.x, x.y);
-          }
+          probs(c, mm, pw);
           tmem_st16(tS + lane_base + 16 * c, pw);
-        }
-        tmem_wait_st();
-        const float2 pa = fadd2(fadd2(ps[0], ps[1]), fadd2(ps[2], ps[3]));
-        l_run = fmaf(l_run, corr, pa.x + pa.y);
-        if (__any_sync(0xffffffffu, need)) {
-          // O holds every tile up to t - 1: S(t) was issued after PV(t - 1) and has completed
-#pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + lane_base + c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-            tmem_st32(tO + lane_base + c, o);
+          if (c & 1) {  // 64 keys are there: their product may start
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_p_full[rb][c >> 1]);
           }
-          tmem_wait_st();
         }
-        tc_fence_before();
-        mbar_arrive(&bar_p_full[rb]);
+        const float2 pa = fadd2(fadd2(ps[0], ps[1]), fadd2(ps[2], ps[3]));
+        l_run += pa.x + pa.y;
       }
       if (ok) ok = warp_wait(&bar_o_done[rb], oc & 1);
       if (!ok) break;

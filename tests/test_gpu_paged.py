@@ -320,6 +320,15 @@ def test_score_kinds(tv, kw, lens, tree, Hq, Hkv, D, page, dtype):
     agree(tv, c, Hq, Hkv, D, dtype, **kw)
 
 
+@pytest.mark.parametrize("window", [33, 128, 300, 700])
+@pytest.mark.parametrize("tree", [False, True])
+def test_windows_over_many_units(tv, window, tree):
+    """Units whose first and last key tiles both hold rows that nobody sees, many to a CTA."""
+    lens = [(1500, 90), (130, 250), (0, 400), (777, 40), (255, 129), (5, 33)] * 3
+    c = make(window, lens, 16, 8, 64, 16, tree=tree)
+    agree(tv, c, 16, 8, 64, "bf16", window=window)
+
+
 @pytest.mark.parametrize("layout", ["heads", "rows", "both"])
 @pytest.mark.parametrize("lens", [[(700, 1), (90, 1)], [(300, 90), (20, 5)]])
 def test_cache_layouts(tv, layout, lens):
