@@ -281,7 +281,16 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   const float sc = scale == 0.0f ? 1.0f / sqrtf((float)D) : scale;
   p.scale_log2 = sc * tv::paged::kLog2e;
   p.softcap_log2 = softcap * tv::paged::kLog2e;
-  p.cap_in = softcap > 0.0f ? 2.0f * tv::paged::kLog2e * sc / softcap : 0.0f;
+  p.cap_in = softcap > 0.0f ? sc / softcap : 0.0f;
+  // the cubic's coefficients for products as they are, in the log2 domain; not where their
+  // powers would leave the 32-bit range
+  p.cap_top = -1.0f;
+  if (p.cap_in >= 1e-5f && p.cap_in <= 1e5f) {
+    const float a2 = p.cap_in * p.cap_in;
+    float f = p.scale_log2;
+    for (int i = 0; i < 4; ++i, f *= a2) p.cap_q[i] = f * tv::paged::kTanhC[i];
+    p.cap_top = tv::paged::kTanhSmall * tv::paged::kTanhSmall / a2;
+  }
   // scores that need more than a scale, or tree rows whose distances the window can reach
   const bool mod = softcap > 0.0f || slopes || (anc_mask && window > 0 && window < 64 * p.W);
   const bool f16 = cache->dtype == TV_FP16;

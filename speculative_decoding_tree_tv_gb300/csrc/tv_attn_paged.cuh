@@ -57,7 +57,8 @@ struct PagedAttnParams {
   int row_dim, head_dim;  // which of a cache map's dimensions 1, 2, 3 they are (the pages: the third)
   int tq;           // tokens per query tile
   int min_share;    // least cost of a share
-  float scale_log2, softcap_log2, cap_in;  // cap_in: 2 log2(e) scale / softcap
+  float scale_log2, softcap_log2, cap_in;  // cap_in: scale / softcap
+  float cap_q[4], cap_top;  // capped scores s of s^2 <= cap_top: s (q0 + q1 s^2 + q2 s^4 + q3 s^6)
 };
 
 // ------------------------------------------------------------ small helpers
@@ -76,6 +77,13 @@ __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
       : "=l"(d)
       : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)),
         "l"(*reinterpret_cast<const uint64_t*>(&c)));
+  return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
   return *reinterpret_cast<const float2*>(&d);
 }
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
@@ -97,7 +105,9 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
-  return fmaxf(fmaxf(a, b), c);
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -127,12 +137,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-// The score in the log2 domain behind the cap: cap tanh(y) with y = scale s / cap, as
-// cap (1 - 2 / (1 + e^2y)).  The subtraction leaves an absolute error of a few
-// 2^-24 cap, which is what a probability feels; tanh.approx is off by 2^-11.
-__device__ __forceinline__ float capped(float s, float cap_in, float cap) {
-  return fmaf(-2.0f * cap, rcp(1.0f + ex2(s * cap_in)), cap);
-}
+// tanh(y) as 1 - 2 / (1 + e^2y), y2 = 2 log2(e) y.  The subtraction leaves an
+// absolute error of a few 2^-24, times the cap what a probability feels; tanh.approx is off by
+// 2^-11 of the value.
+__device__ __forceinline__ float tanh_any(float y2) { return fmaf(-2.0f, rcp(1.0f + ex2(y2)), 1.0f); }
+// For |y| <= kTanhSmall tanh(y) / y is a cubic in y^2, fitted at Chebyshev nodes (relative
+// error 2^-22 in 32-bit arithmetic), on the FMA pipe where the function above takes
+// two special-function instructions.
+constexpr float kTanhSmall = 0.4f;
+constexpr float kTanhC[4] = {0.999999903f, -0.333313733f, 0.132711566f, -0.047561077f};
 
 // Bits [a, b) of a 32-bit word (a, b any integers).
 __device__ __forceinline__ uint32_t range_bits(int a, int b) {

@@ -126,6 +126,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
   // ---------------------------------------------------------------- consumers
   write_status(p, kRowsWarps * 32, 1);
+  const float cap_in2 = 2.0f * kLog2e * p.cap_in;
   const int g = lane >> 2, c2 = (lane & 3) * 2;  // fragment row and first column of this lane
   while (cur.next(p, w, nullptr)) {
     const int rows = w.ntok * p.G;
@@ -211,7 +212,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             for (int e = 0; e < 2; ++e) {
               float& x = s[r >> 1][nt][(r & 1) * 2 + e];
               const int j = j0 + 8 * nt + c2 + e;
-              x = (MOD && p.softcap_log2 > 0.0f) ? capped(x, p.cap_in, p.softcap_log2) : x * p.scale_log2;
+              x = (MOD && p.softcap_log2 > 0.0f) ? p.softcap_log2 * tanh_any(x * cap_in2) : x * p.scale_log2;
               int kpos = j;
               if (!plain) {
                 bool see = j < limit[r];

@@ -72,6 +72,35 @@ __device__ __forceinline__ uint32_t see32(const PagedAttnParams& p, const Row& r
   return v;
 }
 
+// x, scaled, less slope times distance; b0: the first key's bias.
+__device__ __forceinline__ void bias_chunk(float b0, float slope, float in_scale, uint32_t (&x)[32]) {
+  const float2 in2 = make_float2(in_scale, in_scale), slope2 = make_float2(slope, slope);
+  const float2 b2 = make_float2(b0, b0);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const float2 y = ffma2(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), in2,
+                           ffma2(slope2, make_float2((float)e, (float)(e + 1)), b2));
+    x[e] = __float_as_uint(y.x);
+    x[e + 1] = __float_as_uint(y.y);
+  }
+}
+
+// 32 keys from j that reach the tree: a node's position is its depth's.  Clears v where the
+// window does not reach, and adds the bias.
+__device__ __forceinline__ void tree_chunk(const PagedAttnParams& p, const Row& r, int j, int L,
+                                           float in_scale, float slope, uint32_t& v, uint32_t (&x)[32]) {
+  const int a = j - L;  // tree index of the first key
+  const int before = a > 0 ? anc_count(r.anc, p.W, min(a, 64 * p.W)) : 0;
+  const uint32_t tree = v & range_bits(-a, 32);
+#pragma unroll
+  for (int e = 0; e < 32; ++e) {
+    const int kpos = a + e < 0 ? j + e : L + before + __popc(tree & (0xffffffffu >> (31 - e))) - 1;
+    if (p.window > 0 && r.pos - kpos >= p.window) v &= ~(1u << e);
+    if (p.slopes)
+      x[e] = __float_as_uint(fmaf(slope, (float)(kpos - r.pos), __uint_as_float(x[e]) * in_scale));
+  }
+}
+
 template <int D, bool F16, bool MOD>
 __global__ void __launch_bounds__(kTcThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -346,7 +375,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       r.limit = p.anc ? w.s.L : w.s.L + i + 1;
       r.from = p.window > 0 ? r.pos - p.window + 1 : 0;
       const float slope = (MOD && p.slopes) ? __ldg(p.slopes + h) * kLog2e : 0.0f;
-      const float scale = MOD ? 1.0f : p.scale_log2;
+      // what turns a score into the log2 domain; capped scores are there already, and with
+      // slopes it comes with the bias
+      const float in_scale = (MOD && p.softcap_log2 > 0.0f) ? 1.0f : p.scale_log2;
+      const float scale = (MOD && p.slopes) ? 1.0f : in_scale;
       float m_run = -INFINITY, l_run = 0.0f;
       for (int t = 0; t < T; ++t, ++kt, ++sc) {
         const int j0 = (w.begin + t) * kTcKeys;
@@ -380,39 +412,79 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             for (int g = 0; g < 4; ++g)
               if ((bad >> (4 * c + g)) & 1u) vis[c] &= ~(0xffu << (8 * g));
         }
-        if (MOD) {  // to the log2 domain: scale, cap, bias
+        if (MOD && p.softcap_log2 > 0.0f) {
+          float top = 0.0f;
+          const float2 q0 = make_float2(p.cap_q[0], p.cap_q[0]), q1 = make_float2(p.cap_q[1], p.cap_q[1]);
+          const float2 q2 = make_float2(p.cap_q[2], p.cap_q[2]), q3 = make_float2(p.cap_q[3], p.cap_q[3]);
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float s = __uint_as_float(sr[c][e]);
-              sr[c][e] = __float_as_uint(p.softcap_log2 > 0.0f ? capped(s, p.cap_in, p.softcap_log2)
-                                                               : s * p.scale_log2);
-            }
-          if (!r.anc || j0 + kTcKeys <= w.s.L) {
-            if (p.slopes) {
-              const float d0 = (float)(j0 - r.pos);
+            for (int e = 0; e < 32; e += 8) {  // four pairs step by step, so that their chains overlap
+              float2 s[4], w[4], f[4];
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+              for (int b = 0; b < 4; ++b) {
+                s[b] = make_float2(__uint_as_float(sr[c][e + 2 * b]), __uint_as_float(sr[c][e + 2 * b + 1]));
+                w[b] = fmul2(s[b], s[b]);
+              }
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  sr[c][e] = __float_as_uint(fmaf(slope, d0 + (float)(32 * c + e), __uint_as_float(sr[c][e])));
-            }
-          } else {  // the tile reaches the tree: a node's position is its depth's
+              for (int b = 0; b < 4; ++b) f[b] = ffma2(q3, w[b], q2);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int x = j0 + 32 * c - w.s.L;  // tree index of the chunk's first key
-              const int before = x > 0 ? anc_count(r.anc, p.W, min(x, 64 * p.W)) : 0;
-              const uint32_t tree = vis[c] & range_bits(-x, 32);
+              for (int b = 0; b < 4; ++b) f[b] = ffma2(f[b], w[b], q1);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int kpos = x + e < 0 ? j0 + 32 * c + e
-                                           : w.s.L + before + __popc(tree & (0xffffffffu >> (31 - e))) - 1;
-                if (p.window > 0 && r.pos - kpos >= p.window) vis[c] &= ~(1u << e);
-                sr[c][e] = __float_as_uint(fmaf(slope, (float)(kpos - r.pos), __uint_as_float(sr[c][e])));
+              for (int b = 0; b < 4; ++b) f[b] = ffma2(f[b], w[b], q0);
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                top = max3(top, w[b].x, w[b].y);
+                f[b] = fmul2(s[b], f[b]);
+                sr[c][e + 2 * b] = __float_as_uint(f[b].x);
+                sr[c][e + 2 * b + 1] = __float_as_uint(f[b].y);
               }
             }
+          // a warp with a score past the cubic's range takes all again, through TMEM (which
+          // still holds them), to keep the code of this rare way small
+          if (__any_sync(0xffffffffu, top > p.cap_top)) {
+            const float in = 2.0f * kLog2e * p.cap_in;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 8) {
+              uint32_t x[8];
+              tmem_ld8(tS + lane_base + c, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                x[e] = __float_as_uint(p.softcap_log2 * tanh_any(__uint_as_float(x[e]) * in));
+              tmem_st8(tS + lane_base + c, x);
+            }
+            tmem_wait_st();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + lane_base + 32 * c, sr[c]);
+            tmem_wait_ld();
           }
+        }
+        if (MOD && r.anc && j0 + kTcKeys > w.s.L) {
+          // the tile reaches the tree: also through TMEM
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_st32(tS + lane_base + 32 * c, sr[c]);
+          tmem_wait_st();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32], v = c == 0 ? vis[0] : c == 1 ? vis[1] : c == 2 ? vis[2] : vis[3];
+            tmem_ld32(tS + lane_base + 32 * c, x);
+            tmem_wait_ld();
+            tree_chunk(p, r, j0 + 32 * c, w.s.L, in_scale, slope, v, x);
+            tmem_st32(tS + lane_base + 32 * c, x);
+            if (c == 0) vis[0] = v;
+            if (c == 1) vis[1] = v;
+            if (c == 2) vis[2] = v;
+            if (c == 3) vis[3] = v;
+          }
+          tmem_wait_st();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + lane_base + 32 * c, sr[c]);
+          tmem_wait_ld();
+        } else if (MOD && p.slopes) {
+          const float b0 = slope * (float)(j0 - r.pos);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) bias_chunk(fmaf(slope, 32.0f * c, b0), slope, in_scale, sr[c]);
         }
         if ((vis[0] & vis[1] & vis[2] & vis[3]) != 0xffffffffu) {
 #pragma unroll
