@@ -291,11 +291,10 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
     for (int i = 0; i < 4; ++i, f *= a2) p.cap_q[i] = f * tv::paged::kTanhC[i];
     p.cap_top = tv::paged::kTanhSmall * tv::paged::kTanhSmall / a2;
   }
-  // scores that need more than a scale, or tree rows whose distances the window can reach
-  const bool mod = softcap > 0.0f || slopes || (anc_mask && window > 0 && window < 64 * p.W);
+  const bool bias = slopes || (anc_mask && window > 0 && window < 64 * p.W);
   const bool f16 = cache->dtype == TV_FP16;
-  cudaError_t e = pl.mt ? tv::paged::launch_rows(pl, D, f16, mod, tmK, tmV, p, stream)
-                        : tv::paged::launch_tc(pl, D, f16, mod, tmQ, tmK, tmV, p, stream);
+  cudaError_t e = pl.mt ? tv::paged::launch_rows(pl, D, f16, bias || softcap > 0.0f, tmK, tmV, p, stream)
+                        : tv::paged::launch_tc(pl, D, f16, bias, tmQ, tmK, tmV, p, stream);
   if (e == cudaSuccess)
     e = D == 128 ? (f16 ? tv::paged::launch_merge<128, true>(pl, p, stream)
                         : tv::paged::launch_merge<128, false>(pl, p, stream))

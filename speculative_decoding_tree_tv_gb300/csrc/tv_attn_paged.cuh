@@ -385,10 +385,10 @@ struct PagedPlan {
 
 constexpr int kRowsKeys = 64, kTcKeys = 128;  // keys of a tile of either kernel
 
-// mod: scores that need more than a scale (a cap, a bias, tree distances that the window reaches)
+// bias: slopes, or tree distances that the window reaches (mod: those or a cap)
 cudaError_t launch_rows(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmK,
                         const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
-cudaError_t launch_tc(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmQ,
+cudaError_t launch_tc(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
                       const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
                       cudaStream_t stream);
 

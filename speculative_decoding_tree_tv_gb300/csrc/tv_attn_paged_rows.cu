@@ -91,13 +91,13 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     bool ok = true;
     while (ok && cur.next(p, w, lane == 0 ? p.desc + blockIdx.x : nullptr)) {
       bool bad;
-      int page = w.begin < w.end ? page_at(p, w, w.begin * kRowsKeys + row0, rows_page, bad) : 0;
-      for (int t = w.begin; t < w.end; ++t, ++it) {
+      int page = w.begin < w.end ? page_at(p, w, (w.end - 1) * kRowsKeys + row0, rows_page, bad) : 0;
+      for (int t = w.end - 1; t >= w.begin; --t, ++it) {
         const int st = it % Lay::kStages;
         const int key = t * kRowsKeys + row0;
         bool bad_next = false;
         int page_next = 0;
-        if (t + 1 < w.end) page_next = page_at(p, w, key + kRowsKeys, rows_page, bad_next);
+        if (t > w.begin) page_next = page_at(p, w, key - kRowsKeys, rows_page, bad_next);
         ok = warp_wait(&bar_empty[st], ((it / Lay::kStages) & 1) ^ 1);
         if (!ok) break;
         const uint32_t bad_pages = __ballot_sync(0xffffffffu, bad && lane < npg);
@@ -162,7 +162,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const int all_from = p.window > 0
                              ? (p.anc ? w.s.L + w.s.n : w.s.L + w.first + w.ntok) - p.window : -1;
 
-    for (int t = w.begin; t < w.end; ++t, ++it) {
+    for (int t = w.end - 1; t >= w.begin; --t, ++it) {  // (last first: see paged_tc_kernel)
       const int st = it % Lay::kStages;
       const int j0 = t * kRowsKeys + 16 * warp;
       // (a warp that gives up still joins the others at the unit's end, where all see it)

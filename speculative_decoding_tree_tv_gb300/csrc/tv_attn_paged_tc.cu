@@ -1,7 +1,10 @@
 // paged_tc_kernel: units of up to 256 rows (two row blocks of 128 TMEM lanes, each nb =
 // floor(128 / G) whole tokens) on the 5th-generation tensor cores.
 //
-// A CTA (one per SM) walks its share of the units.  Warp roles:
+// A CTA (one per SM) walks its share of the units, and a unit's keys from its last tile to
+// its first: with a distance bias the scores fall that way, and the running maximum
+// stays (the other way it moves with every tile, and O is scaled each time: a chunk of 2048 behind 6,100
+// keys with slopes took 269 instead of ALIBI us).  Warp roles:
 //   warps 0-3, 4-7  softmax of row block 0, 1: one thread per row (TMEM lane), 128 scores a
 //                   tile, online softmax in the log2 domain with lazy rescaling;
 //   warp 8, 10      K and V tiles of 128 keys by TMA (a lane per box: 64 dims of the rows of
@@ -101,7 +104,10 @@ __device__ __forceinline__ void tree_chunk(const PagedAttnParams& p, const Row& 
   }
 }
 
-template <int D, bool F16, bool MOD>
+// CAP: a softcap; BIAS: slopes, or tree distances that the window reaches.  Variants of
+// their own, and rolled loops wherever a warp does not wait for them: a loop over the tiles that is
+// larger than the instruction cache (some 32 KB) runs at half the speed.
+template <int D, bool F16, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kTcThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const PagedAttnParams p, const int nb) {
@@ -195,13 +201,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     };
     while (ok && cur.next(p, w, !isV && lane == 0 ? p.desc + blockIdx.x : nullptr)) {
       bool bad = false;
-      int page = w.begin < w.end ? page_at(p, w, w.begin * kTcKeys + row0, rows_page, bad) : 0;
-      for (int t = w.begin; t < w.end; ++t, ++it) {
+      int page = w.begin < w.end ? page_at(p, w, (w.end - 1) * kTcKeys + row0, rows_page, bad) : 0;
+      for (int t = w.end - 1; t >= w.begin; --t, ++it) {
         const uint32_t st = it % stages;
         const int key = t * kTcKeys + row0;
         bool bad_next = false;
         int page_next = 0;
-        if (t + 1 < w.end) page_next = page_at(p, w, key + kTcKeys, rows_page, bad_next);
+        if (t > w.begin) page_next = page_at(p, w, key - kTcKeys, rows_page, bad_next);
         ok = warp_wait(&empty[st], ((it / stages) & 1) ^ 1) && !s_abort;
         if (!ok) break;
         const uint32_t bad_pages = __ballot_sync(0xffffffffu, bad && lane < npg);
@@ -299,7 +305,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         next_k();
         if (T == 1) mma_commit(&bar_q_empty);
         for (int t = 0; t < T; ++t) {
-          const int j0 = (w.begin + t) * kTcKeys;
+          const int j0 = (w.end - 1 - t) * kTcKeys;
           const bool more = t + 1 < T;
           ok = mbar_wait(&bar_v_full[vst], vph);
           if (w.lo > j0 || w.hi < j0 + kTcKeys) {  // the V producer clears rows of this tile
@@ -374,21 +380,24 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       r.pos = w.s.L + (p.anc ? anc_count(r.anc, p.W, 64 * p.W) - 1 : i);
       r.limit = p.anc ? w.s.L : w.s.L + i + 1;
       r.from = p.window > 0 ? r.pos - p.window + 1 : 0;
-      const float slope = (MOD && p.slopes) ? __ldg(p.slopes + h) * kLog2e : 0.0f;
+      const float slope = (BIAS && p.slopes) ? __ldg(p.slopes + h) * kLog2e : 0.0f;
       // what turns a score into the log2 domain; capped scores are there already, and with
       // slopes it comes with the bias
-      const float in_scale = (MOD && p.softcap_log2 > 0.0f) ? 1.0f : p.scale_log2;
-      const float scale = (MOD && p.slopes) ? 1.0f : in_scale;
+      const float in_scale = CAP ? 1.0f : p.scale_log2;
+      const float scale = (BIAS && p.slopes) ? 1.0f : in_scale;
       float m_run = -INFINITY, l_run = 0.0f;
       for (int t = 0; t < T; ++t, ++kt, ++sc) {
-        const int j0 = (w.begin + t) * kTcKeys;
-        uint32_t vis[4];
-        if (j0 + kTcKeys <= r.limit && j0 >= r.from) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) vis[c] = 0xffffffffu;
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) vis[c] = see32(p, r, j0 + 32 * c, w.s.L, w.hi);
+        const int j0 = (w.end - 1 - t) * kTcKeys;
+        uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (j0 + kTcKeys > r.limit || j0 < r.from) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t v = see32(p, r, j0 + 32 * c, w.s.L, w.hi);
+            if (c == 0) vis[0] = v;
+            if (c == 1) vis[1] = v;
+            if (c == 2) vis[2] = v;
+            if (c == 3) vis[3] = v;
+          }
         }
         ok = warp_wait(&bar_s_full[rb], sc & 1);
         if (!ok) break;
@@ -412,7 +421,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             for (int g = 0; g < 4; ++g)
               if ((bad >> (4 * c + g)) & 1u) vis[c] &= ~(0xffu << (8 * g));
         }
-        if (MOD && p.softcap_log2 > 0.0f) {
+        if (CAP) {
           float top = 0.0f;
           const float2 q0 = make_float2(p.cap_q[0], p.cap_q[0]), q1 = make_float2(p.cap_q[1], p.cap_q[1]);
           const float2 q2 = make_float2(p.cap_q[2], p.cap_q[2]), q3 = make_float2(p.cap_q[3], p.cap_q[3]);
@@ -460,7 +469,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             tmem_wait_ld();
           }
         }
-        if (MOD && r.anc && j0 + kTcKeys > w.s.L) {
+        if (BIAS && r.anc && j0 + kTcKeys > w.s.L) {
           // the tile reaches the tree: also through TMEM
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_st32(tS + lane_base + 32 * c, sr[c]);
@@ -481,7 +490,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + lane_base + 32 * c, sr[c]);
           tmem_wait_ld();
-        } else if (MOD && p.slopes) {
+        } else if (BIAS && p.slopes) {
           const float b0 = slope * (float)(j0 - r.pos);
 #pragma unroll
           for (int c = 0; c < 4; ++c) bias_chunk(fmaf(slope, 32.0f * c, b0), slope, in_scale, sr[c]);
@@ -564,7 +573,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (w.slot >= 0 && mine) p.part_ml[(size_t)w.slot * 256 + crow] = make_float2(m_run, l_run);
       float4* dst = reinterpret_cast<float4*>(p.part) + (size_t)max(w.slot, 0) * (D / 4) * 256 + crow;
       uint4* orow = reinterpret_cast<uint4*>(p.out + oidx * D);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(tO + lane_base + 32 * c, o);
@@ -600,29 +609,33 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool F16, bool MOD>
+template <int D, bool F16, bool CAP, bool BIAS>
 cudaError_t launch(const PagedPlan& pl, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                    const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream) {
-  if (!set_dyn_smem(paged_tc_kernel<D, F16, MOD>, TcLayout<D>::kDyn)) return cudaErrorUnknown;
-  return launch_pdl(paged_tc_kernel<D, F16, MOD>, dim3(pl.ctas), dim3(kTcThreads),
+  if (!set_dyn_smem(paged_tc_kernel<D, F16, CAP, BIAS>, TcLayout<D>::kDyn)) return cudaErrorUnknown;
+  return launch_pdl(paged_tc_kernel<D, F16, CAP, BIAS>, dim3(pl.ctas), dim3(kTcThreads),
                     (size_t)TcLayout<D>::kDyn, stream, tmQ, tmK, tmV, p, pl.nb);
+}
+template <int D, bool F16>
+cudaError_t launch_kind(const PagedPlan& pl, bool bias, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                        const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream) {
+  if (p.softcap_log2 > 0.0f)
+    return bias ? launch<D, F16, true, true>(pl, tmQ, tmK, tmV, p, stream)
+                : launch<D, F16, true, false>(pl, tmQ, tmK, tmV, p, stream);
+  return bias ? launch<D, F16, false, true>(pl, tmQ, tmK, tmV, p, stream)
+              : launch<D, F16, false, false>(pl, tmQ, tmK, tmV, p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_tc(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmQ,
+cudaError_t launch_tc(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
                       const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
                       cudaStream_t stream) {
-  if (D == 128) {
-    if (f16) return mod ? launch<128, true, true>(pl, tmQ, tmK, tmV, p, stream)
-                        : launch<128, true, false>(pl, tmQ, tmK, tmV, p, stream);
-    return mod ? launch<128, false, true>(pl, tmQ, tmK, tmV, p, stream)
-               : launch<128, false, false>(pl, tmQ, tmK, tmV, p, stream);
-  }
-  if (f16) return mod ? launch<64, true, true>(pl, tmQ, tmK, tmV, p, stream)
-                      : launch<64, true, false>(pl, tmQ, tmK, tmV, p, stream);
-  return mod ? launch<64, false, true>(pl, tmQ, tmK, tmV, p, stream)
-             : launch<64, false, false>(pl, tmQ, tmK, tmV, p, stream);
+  if (D == 128)
+    return f16 ? launch_kind<128, true>(pl, bias, tmQ, tmK, tmV, p, stream)
+               : launch_kind<128, false>(pl, bias, tmQ, tmK, tmV, p, stream);
+  return f16 ? launch_kind<64, true>(pl, bias, tmQ, tmK, tmV, p, stream)
+             : launch_kind<64, false>(pl, bias, tmQ, tmK, tmV, p, stream);
 }
 
 }  // namespace paged
