@@ -148,9 +148,12 @@ bool map_cache(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void*
 PagedPlan paged_plan(int max_q, int G, int D) {
   PagedPlan pl;
   const long long rows = (long long)max_q * G;
-  pl.mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
-  if (pl.mt) {
-    pl.rows = 16 * pl.mt;
+  // 64 decode sequences of 512 to 8,192 keys, 8 kv heads, D 128: 4 rows a unit 188 us here and RULE4 us on the
+  // tcgen05 kernel, 16 rows RULE16A and RULE16B us; 32 rows took 430 us with two row tiles a warp here
+  // (its registers spill) and RULE32 us there.
+  pl.small = rows <= 16;
+  if (pl.small) {
+    pl.rows = 16;
     pl.nb = pl.tq = pl.rows / G;
     pl.ctas = 2 * device_sm_count();
     pl.min_share = 6;
@@ -170,7 +173,7 @@ PagedPlan paged_plan(int max_q, int G, int D) {
 
 template <int D, bool F16>
 cudaError_t launch_merge(const PagedPlan& pl, const PagedAttnParams& p, cudaStream_t stream) {
-  if (pl.mt)
+  if (pl.small)
     return launch_pdl(paged_merge_kernel<D, F16, false>, dim3(pl.ctas, 1), dim3(kMergeThreads), 0,
                       stream, p, pl.rows, pl.nb);
   return launch_pdl(paged_merge_kernel<D, F16, true>, dim3(pl.ctas, 8), dim3(kMergeThreads), 0, stream,
@@ -231,11 +234,11 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   auto encode = tv::paged::tensor_map_encoder();
   if (!encode) return TV_ERR_CUDA;
   CUtensorMap tmQ, tmK, tmV;
-  const int rows = min(cache->page_size, pl.mt ? tv::paged::kRowsKeys : tv::paged::kTcKeys);
+  const int rows = min(cache->page_size, pl.small ? tv::paged::kRowsKeys : tv::paged::kTcKeys);
   if (!tv::paged::map_cache(encode, &tmK, cache->k, cache, stride, order, rows) ||
       !tv::paged::map_cache(encode, &tmV, cache->v, cache, stride, order, rows))
     return TV_ERR_INVALID_ARG;
-  if (!pl.mt && T > 0) {
+  if (!pl.small && T > 0) {
     // q as [tokens][heads][D]; a box is 64 dims of the group's heads of nb tokens
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)p.q_head_stride * 2, (cuuint64_t)p.q_token_stride * 2};
@@ -293,7 +296,7 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   }
   const bool bias = slopes || (anc_mask && window > 0 && window < 64 * p.W);
   const bool f16 = cache->dtype == TV_FP16;
-  cudaError_t e = pl.mt ? tv::paged::launch_rows(pl, D, f16, bias || softcap > 0.0f, tmK, tmV, p, stream)
+  cudaError_t e = pl.small ? tv::paged::launch_rows(pl, D, f16, bias || softcap > 0.0f, tmK, tmV, p, stream)
                         : tv::paged::launch_tc(pl, D, f16, bias, tmQ, tmK, tmV, p, stream);
   if (e == cudaSuccess)
     e = D == 128 ? (f16 ? tv::paged::launch_merge<128, true>(pl, p, stream)

@@ -16,7 +16,7 @@
 // dependent launch, joins them.  The cuts depend on the lengths alone, so
 // results do not vary from run to run.
 //
-// Two kernels take units: paged_rows_kernel (tv_attn_paged_rows.cu) those of at most 32 rows
+// Two kernels take units: paged_rows_kernel (tv_attn_paged_rows.cu) those of at most 16 rows
 // (decode tokens and small trees: HBM-bound, warp-level mma), and
 // paged_tc_kernel (tv_attn_paged_tc.cu, tcgen05) larger ones.
 #pragma once
@@ -376,7 +376,7 @@ __device__ __forceinline__ int page_at(const PagedAttnParams& p, const Part& w, 
 
 // How a call runs: the kernel, its CTAs, and the layout of the workspace.
 struct PagedPlan {
-  int mt;    // 16-row tiles of the small-unit kernel (1 or 2); 0: the tcgen05 kernel
+  bool small;  // units of at most 16 rows: paged_rows_kernel
   int rows;  // rows of a unit
   int tq, nb, ctas, min_share;
   size_t part_bytes, ml_bytes, desc_bytes;

@@ -1,5 +1,5 @@
-// paged_rows_kernel: units of at most 16 MT rows.  HBM-bound: per 64-key stage a CTA reads 64 D * 4
-// bytes and issues 8 MT D/16 warp mma.  Four consumer warps take 16 keys of a stage each
+// paged_rows_kernel: units of at most 16 rows.  HBM-bound: per 64-key stage a CTA reads 64 D * 4
+// bytes and issues 4 D warp mma.  Four consumer warps take 16 keys of a stage each
 // and keep a running maximum, sum and output of their own (no barrier
 // between them until the unit's end); a fifth warp issues the TMA loads, one box
 // per lane (64 dims x the rows of a page).
@@ -10,6 +10,7 @@ namespace tv {
 namespace paged {
 namespace {
 
+constexpr int kUnitRows = 16;
 constexpr int kRowsWarps = 4;
 constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
 
@@ -47,21 +48,23 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, bool F16, int MT, bool MOD>
+template <int D, bool F16, bool MOD>
 __global__ void __launch_bounds__(kRowsThreads, 2)
 paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const PagedAttnParams p) {
   using Lay = RowsLayout<D>;
-  constexpr int kRows = 16 * MT, kSteps = D / 16;
+  constexpr int kSteps = D / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sK = smem;
   uint8_t* sV = smem + Lay::kStages * Lay::kSide;
-  float* s_acc = reinterpret_cast<float*>(smem + 2 * Lay::kStages * Lay::kSide);
+  // the unit's Q rows; at its end the warps' outputs (32 dims at a time)
+  uint4* s_q = reinterpret_cast<uint4*>(smem + 2 * Lay::kStages * Lay::kSide);
+  float* s_acc = reinterpret_cast<float*>(s_q);
   __shared__ __align__(8) uint64_t bar_full[Lay::kStages], bar_empty[Lay::kStages];
   __shared__ uint32_t s_bad_pages[Lay::kStages];  // bit g: keys 8 g .. 8 g + 7 have no page
-  __shared__ float2 s_ml[kRowsWarps][kRows];
+  __shared__ float2 s_ml[kRowsWarps][kUnitRows];
   __shared__ volatile int s_abort;  // a consumer's wait ran out
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
@@ -130,34 +133,39 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   const int g = lane >> 2, c2 = (lane & 3) * 2;  // fragment row and first column of this lane
   while (cur.next(p, w, nullptr)) {
     const int rows = w.ntok * p.G;
-    uint32_t qf[MT][kSteps][4];
-    int pos[2 * MT], limit[2 * MT];
-    const uint64_t* anc[2 * MT];
-    float slope[2 * MT];
-    float m[2 * MT], l[2 * MT], o[MT][D / 8][4];
+    // the unit's Q rows to shared memory (rows past the unit repeat its last one); 16-byte
+    // chunk c of row r lies at c ^ (r & 7)
+    for (int x = tid; x < kUnitRows * (D / 8); x += kRowsWarps * 32) {
+      const int r = x / (D / 8), c = x % (D / 8), row = min(r, rows - 1);
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (w.s.t0 + w.first + row / p.G) * p.q_token_stride +
+          (w.kvh * p.G + row % p.G) * p.q_head_stride);
+      s_q[r * (D / 8) + (c ^ (r & 7))] = __ldg(src + c);
+    }
+    named_sync(1, kRowsWarps * 32);
+    uint32_t qf[kSteps][4];
+    {
+      const uint32_t base = smem_u32(s_q) + ((lane & 7) + ((lane >> 3) & 1) * 8) * (D * 2);
 #pragma unroll
-    for (int r = 0; r < 2 * MT; ++r) {
-      const int row = min((r >> 1) * 16 + (r & 1) * 8 + g, rows - 1);  // rows past the unit repeat its last
+      for (int k = 0; k < kSteps; ++k) ldsm4(base + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4), qf[k]);
+    }
+    int pos[2], tok[2];
+    float slope[2];
+    float m[2], l[2], o[D / 8][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = min(r * 8 + g, rows - 1);  // rows past the unit repeat its last
       const int i = w.first + row / p.G, t = w.s.t0 + i, h = w.kvh * p.G + row % p.G;
-      const uint16_t* qr = p.q + t * p.q_token_stride + h * p.q_head_stride;
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        qf[r >> 1][k][(r & 1)] = __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + c2));
-        qf[r >> 1][k][(r & 1) + 2] = __ldg(reinterpret_cast<const uint32_t*>(qr + 16 * k + 8 + c2));
-      }
-      anc[r] = p.anc ? p.anc + (size_t)t * p.W : nullptr;
-      pos[r] = w.s.L + (p.anc ? anc_count(anc[r], p.W, 64 * p.W) - 1 : i);
-      limit[r] = p.anc ? w.s.L : w.s.L + i + 1;  // keys below it are visible, the window apart
+      tok[r] = t;
+      pos[r] = w.s.L + (p.anc ? anc_count(p.anc + (size_t)t * p.W, p.W, 64 * p.W) - 1 : i);
       slope[r] = (MOD && p.slopes) ? __ldg(p.slopes + h) * kLog2e : 0.0f;
       m[r] = -INFINITY;
       l[r] = 0.0f;
     }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
     const int all_below = p.anc ? w.s.L : w.s.L + w.first + 1;  // keys below it are visible to every row
     const int all_from = p.window > 0
                              ? (p.anc ? w.s.L + w.s.n : w.s.L + w.first + w.ntok) - p.window : -1;
@@ -171,11 +179,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         break;
       }
       if (j0 < w.hi && j0 + 16 > w.lo) {
-        float s[MT][2][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s[mt][e >> 2][e & 3] = 0.0f;
+        float s[2][4] = {};  // [8 keys][row g: two keys, row g + 8: two keys]
         {
           const int key = 16 * warp + (lane >> 4) * 8 + (lane & 7);
           const uint32_t base = smem_u32(sK) + st * Lay::kSide + key * 128;
@@ -184,11 +188,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           for (int k = 0; k < kSteps; ++k) {
             uint32_t b[4];
             ldsm4(base + (k >> 2) * Lay::kAtom + ((((k & 3) * 2 + kc) ^ sw) << 4), b);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma16816<F16>(s[mt][0], qf[mt][k], b[0], b[1]);
-              mma16816<F16>(s[mt][1], qf[mt][k], b[2], b[3]);
-            }
+            mma16816<F16>(s[0], qf[k], b[0], b[1]);
+            mma16816<F16>(s[1], qf[k], b[2], b[3]);
           }
         }
         const uint32_t bad8 = (s_bad_pages[st] >> (2 * warp)) & 3u;
@@ -204,22 +205,39 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             }
         }
         // scores in the log2 domain, hidden keys at -inf
+        if (MOD && p.softcap_log2 > 0.0f) {
+          float f[8], top = 0.0f;
 #pragma unroll
-        for (int r = 0; r < 2 * MT; ++r)
+          for (int e = 0; e < 8; ++e) {
+            const float x = s[e >> 2][e & 3], w2 = x * x;
+            top = fmaxf(top, w2);
+            f[e] = x * fmaf(fmaf(fmaf(p.cap_q[3], w2, p.cap_q[2]), w2, p.cap_q[1]), w2, p.cap_q[0]);
+          }
+          const bool far = __any_sync(0xffffffffu, top > p.cap_top);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            s[e >> 2][e & 3] = far ? p.softcap_log2 * tanh_any(s[e >> 2][e & 3] * cap_in2) : f[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] *= p.scale_log2;
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float& x = s[r >> 1][nt][(r & 1) * 2 + e];
+              float& x = s[nt][r * 2 + e];
               const int j = j0 + 8 * nt + c2 + e;
-              x = (MOD && p.softcap_log2 > 0.0f) ? p.softcap_log2 * tanh_any(x * cap_in2) : x * p.scale_log2;
               int kpos = j;
               if (!plain) {
-                bool see = j < limit[r];
+                // (causal: up to its own position; a tree's: the prefix and its mask)
+                bool see = j < (p.anc ? w.s.L : pos[r] + 1);
                 if (p.anc && j >= w.s.L && j < w.hi) {
                   const int a = j - w.s.L;
-                  see = (__ldg(reinterpret_cast<const unsigned long long*>(anc[r]) + (a >> 6)) >> (a & 63)) & 1;
-                  if (MOD) kpos = w.s.L + anc_count(anc[r], p.W, a + 1) - 1;
+                  const uint64_t* anc = p.anc + (size_t)tok[r] * p.W;
+                  see = (__ldg(reinterpret_cast<const unsigned long long*>(anc) + (a >> 6)) >> (a & 63)) & 1;
+                  if (MOD) kpos = w.s.L + anc_count(anc, p.W, a + 1) - 1;
                 }
                 if (p.window > 0) see = see && pos[r] - kpos < p.window;
                 if ((bad8 >> nt) & 1) see = false;
@@ -230,14 +248,14 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
               }
             }
         // running maximum (lazily moved), probabilities, sums
-        uint32_t pf[MT][4];
-        float corr[2 * MT];
+        uint32_t pf[4];
+        float corr[2];
         bool move = false;
 #pragma unroll
-        for (int r = 0; r < 2 * MT; ++r) {
-          float (&a)[4] = s[r >> 1][0];
-          float (&b)[4] = s[r >> 1][1];
-          const int e = (r & 1) * 2;
+        for (int r = 0; r < 2; ++r) {
+          float (&a)[4] = s[0];
+          float (&b)[4] = s[1];
+          const int e = r * 2;
           float mx = fmaxf(fmaxf(a[e], a[e + 1]), fmaxf(b[e], b[e + 1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -253,16 +271,14 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           const float p0 = ex2(a[e] - mm), p1 = ex2(a[e + 1] - mm);
           const float p2 = ex2(b[e] - mm), p3 = ex2(b[e + 1] - mm);
           l[r] = fmaf(l[r], corr[r], (p0 + p1) + (p2 + p3));
-          pf[r >> 1][(r & 1)] = pack2<F16>(p0, p1);
-          pf[r >> 1][(r & 1) + 2] = pack2<F16>(p2, p3);
+          pf[r] = pack2<F16>(p0, p1);
+          pf[r + 2] = pack2<F16>(p2, p3);
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[mt][n][e] *= corr[2 * mt + (e >> 1)];
+            for (int e = 0; e < 4; ++e) o[n][e] *= corr[e >> 1];
         }
         {
           const int key = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7);
@@ -276,11 +292,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
               for (int q = 0; q < 4; ++q) b[q] &= vkeep[q & 1];
             }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma16816<F16>(o[mt][2 * n], pf[mt], b[0], b[1]);
-              mma16816<F16>(o[mt][2 * n + 1], pf[mt], b[2], b[3]);
-            }
+            mma16816<F16>(o[2 * n], pf, b[0], b[1]);
+            mma16816<F16>(o[2 * n + 1], pf, b[2], b[3]);
           }
         }
       }
@@ -290,73 +303,64 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
     // the four warps' rows joined in shared memory, 32 dims at a time
 #pragma unroll
-    for (int r = 0; r < 2 * MT; ++r) {
+    for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if ((lane & 3) == 0) s_ml[warp][(r >> 1) * 16 + (r & 1) * 8 + g] = make_float2(m[r], l[r]);
+      if ((lane & 3) == 0) s_ml[warp][r * 8 + g] = make_float2(m[r], l[r]);
     }
     named_sync(1, kRowsWarps * 32);
     const bool abort = s_abort;
-    float f[2 * MT];
+    float f[2];
 #pragma unroll
-    for (int r = 0; r < 2 * MT; ++r) {
-      const int row = (r >> 1) * 16 + (r & 1) * 8 + g;
+    for (int r = 0; r < 2; ++r) {
       float mm = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][row].x);
-      f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mm);
+      for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][r * 8 + g].x);
+      f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mm);  // (0: nothing seen by this warp, its sums are 0)
     }
-    const int orow = tid >> 3, od = (tid & 7) * 4;  // this thread's row and dims of a joined piece
+    const int row = tid >> 3, od = (tid & 7) * 4;  // this thread's row and dims of a joined piece
+    float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int row = mt * 16 + orow;
-      float mm = -INFINITY, ll = 0.0f;
+    for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][row].x);
 #pragma unroll
-      for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][row].x);
+    for (int x = 0; x < kRowsWarps; ++x) {
+      const float2 v = s_ml[x][row];
+      if (v.x != -INFINITY) ll = fmaf(ex2(v.x - mm), v.y, ll);
+    }
+    const bool mine = row < rows;
+    const int out_tok = w.s.t0 + w.first + row / p.G, h = w.kvh * p.G + row % p.G;
+    const size_t oidx = (size_t)out_tok * p.Hq + h;
+    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          *reinterpret_cast<float2*>(s_acc + (warp * 16 + r * 8 + g) * 32 + 8 * n + c2) =
+              make_float2(o[4 * c + n][2 * r] * f[r], o[4 * c + n][2 * r + 1] * f[r]);
+      named_sync(1, kRowsWarps * 32);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < kRowsWarps; ++x) {
-        const float2 v = s_ml[x][row];
-        if (v.x != -INFINITY) ll = fmaf(ex2(v.x - mm), v.y, ll);
+        const float4 v = *reinterpret_cast<const float4*>(s_acc + (x * 16 + row) * 32 + od);
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
       }
-      const bool mine = row < rows;
-      const int tok = w.s.t0 + w.first + row / p.G, h = w.kvh * p.G + row % p.G;
-      const size_t oidx = (size_t)tok * p.Hq + h;
-      const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float fr = f[2 * mt + half];
-            // (fr = 0: nothing seen by this warp, its sums are 0)
-            *reinterpret_cast<float2*>(s_acc + (warp * 16 + half * 8 + g) * 32 + 8 * n + c2) =
-                make_float2(o[mt][4 * c + n][2 * half] * fr, o[mt][4 * c + n][2 * half + 1] * fr);
-          }
-        named_sync(1, kRowsWarps * 32);
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int x = 0; x < kRowsWarps; ++x) {
-          const float4 v = *reinterpret_cast<const float4*>(s_acc + (x * 16 + orow) * 32 + od);
-          a.x += v.x;
-          a.y += v.y;
-          a.z += v.z;
-          a.w += v.w;
-        }
-        if (mine) {
-          if (w.slot >= 0)
-            *reinterpret_cast<float4*>(p.part + ((size_t)w.slot * kRows + row) * D + 32 * c + od) = a;
-          else if (TV_CHECK(tok < p.T && h < p.Hq))
-            *reinterpret_cast<uint2*>(p.out + oidx * D + 32 * c + od) =
-                make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
-        }
-        named_sync(1, kRowsWarps * 32);
+      if (mine) {
+        if (w.slot >= 0)
+          *reinterpret_cast<float4*>(p.part + ((size_t)w.slot * kUnitRows + row) * D + 32 * c + od) = a;
+        else if (TV_CHECK(out_tok < p.T && h < p.Hq))
+          *reinterpret_cast<uint2*>(p.out + oidx * D + 32 * c + od) =
+              make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
       }
-      if (mine && (tid & 7) == 0) {
-        if (w.slot >= 0) p.part_ml[(size_t)w.slot * kRows + row] = make_float2(mm, ll);
-        else if (p.lse)
-          p.lse[oidx] = w.s.bad ? 0.0f : (ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY);
-      }
+      named_sync(1, kRowsWarps * 32);
+    }
+    if (mine && (tid & 7) == 0) {
+      if (w.slot >= 0) p.part_ml[(size_t)w.slot * kUnitRows + row] = make_float2(mm, ll);
+      else if (p.lse) p.lse[oidx] = w.s.bad ? 0.0f : (ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY);
     }
     if (abort) {
       if (tid == 0 && p.status) atomicMax(p.status + w.b, (int)TV_ERR_TIMEOUT);
@@ -365,32 +369,28 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   }
 }
 
-template <int D, bool F16, int MT, bool MOD>
+template <int D, bool F16, bool MOD>
 cudaError_t launch(const PagedPlan& pl, const CUtensorMap& tmK, const CUtensorMap& tmV,
                    const PagedAttnParams& p, cudaStream_t stream) {
-  if (!set_dyn_smem(paged_rows_kernel<D, F16, MT, MOD>, RowsLayout<D>::kDyn)) return cudaErrorUnknown;
-  return launch_pdl(paged_rows_kernel<D, F16, MT, MOD>, dim3(pl.ctas), dim3(kRowsThreads),
+  if (!set_dyn_smem(paged_rows_kernel<D, F16, MOD>, RowsLayout<D>::kDyn)) return cudaErrorUnknown;
+  return launch_pdl(paged_rows_kernel<D, F16, MOD>, dim3(pl.ctas), dim3(kRowsThreads),
                     (size_t)RowsLayout<D>::kDyn, stream, tmK, tmV, p);
-}
-template <int D, bool F16>
-cudaError_t launch_kind(const PagedPlan& pl, bool mod, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                        const PagedAttnParams& p, cudaStream_t stream) {
-  if (pl.mt == 1)
-    return mod ? launch<D, F16, 1, true>(pl, tmK, tmV, p, stream)
-               : launch<D, F16, 1, false>(pl, tmK, tmV, p, stream);
-  return mod ? launch<D, F16, 2, true>(pl, tmK, tmV, p, stream)
-             : launch<D, F16, 2, false>(pl, tmK, tmV, p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rows(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmK,
                         const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream) {
-  if (D == 128)
-    return f16 ? launch_kind<128, true>(pl, mod, tmK, tmV, p, stream)
-               : launch_kind<128, false>(pl, mod, tmK, tmV, p, stream);
-  return f16 ? launch_kind<64, true>(pl, mod, tmK, tmV, p, stream)
-             : launch_kind<64, false>(pl, mod, tmK, tmV, p, stream);
+  if (D == 128) {
+    if (f16) return mod ? launch<128, true, true>(pl, tmK, tmV, p, stream)
+                        : launch<128, true, false>(pl, tmK, tmV, p, stream);
+    return mod ? launch<128, false, true>(pl, tmK, tmV, p, stream)
+               : launch<128, false, false>(pl, tmK, tmV, p, stream);
+  }
+  if (f16) return mod ? launch<64, true, true>(pl, tmK, tmV, p, stream)
+                      : launch<64, true, false>(pl, tmK, tmV, p, stream);
+  return mod ? launch<64, false, true>(pl, tmK, tmV, p, stream)
+             : launch<64, false, false>(pl, tmK, tmV, p, stream);
 }
 
 }  // namespace paged
