@@ -14,73 +14,96 @@ namespace {
 // share ends inside, if any; its parts are slots 2 i + 1, 2 (i + 1), 2 (i + 2), ..
 // Rows of the tcgen05 kernel lie chunk by chunk (TC: [D / 4][rows] of four floats, the
 // order its threads write), the others row by row.
-constexpr int kMergeThreads = 256, kMergeBatch = 4;
+constexpr int kMergeThreads = 256, kMergeBatch = 2;
 
+// The merge's blocks also write the sequences' status: it costs nothing here, while a scan of
+// a long block table held up the attention kernel's first tiles by some 1.5 us.
+__device__ __forceinline__ void merge_status(const PagedAttnParams& p) {
+  if (!p.status) return;
+  for (int b = blockIdx.y * gridDim.x + blockIdx.x; b < p.B; b += gridDim.x * gridDim.y) {
+    bool late = false;
+    for (int c = threadIdx.x; c < gridDim.x; c += kMergeThreads) late |= p.timeout[c] == b + 1;
+    const bool bad = !seq_ok(p, b, threadIdx.x, kMergeThreads);
+    const int any_late = __syncthreads_or(late), any_bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0)
+      p.status[b] = any_late ? TV_ERR_TIMEOUT : any_bad ? TV_ERR_INVALID_ARG : TV_OK;
+  }
+}
+
+// A thread joins kC chunks (of four floats) of one row, all its loads of a batch of parts
+// in flight.
 template <int D, bool F16, bool TC>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnParams p, int slot_rows,
-                                                                    int nb) {
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnParams p, int nb) {
+  constexpr int kChunks = D / 4, kRows = TC ? 256 : 16;
+  constexpr int kC = TC ? 4 : kChunks * kRows / kMergeThreads;  // a small unit: one block
   pdl_trigger();
   pdl_wait();
   const int i = blockIdx.x;
   const int4 d = p.desc[i];
-  if (d.w == 0 || !TV_IN(d.x, p.B)) return;
-  const Seq s = load_seq(p, d.x);
-  const int first = d.z * p.tq, ntok = min(p.tq, s.n - first);
-  constexpr int kChunks = D / 4;
-  const int items = slot_rows * kChunks;
-  for (int k = blockIdx.y * kMergeThreads + threadIdx.x; k < items; k += gridDim.y * kMergeThreads) {
-    const int row = TC ? k % slot_rows : k / kChunks, c = TC ? k / slot_rows : k % kChunks;
-    // a row block of the tcgen05 kernel holds nb tokens in its 128 rows
-    const int rl = TC ? row & 127 : row;
-    const int tl = (TC ? (row >> 7) * nb : 0) + rl / p.G;
-    if (tl >= ntok || (TC && rl / p.G >= nb)) continue;
-    const int h = d.y * p.G + rl % p.G;
-    float M = -INFINITY, l = 0.0f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < d.w; j0 += kMergeBatch) {
-      float2 ml[kMergeBatch];
-      float4 v[kMergeBatch];
+  merge_status(p);
+  if (d.w == 0) return;
+  const int row = TC ? threadIdx.x : threadIdx.x / (kChunks / kC);
+  const int c0 = TC ? blockIdx.y * kC : (threadIdx.x % (kChunks / kC)) * kC;
+  // a row block of the tcgen05 kernel holds nb tokens in its 128 rows
+  const int rl = TC ? row & 127 : row, tr = rl / p.G;
+  const int tl = (TC ? (row >> 7) * nb : 0) + tr;
+  if (tl >= d.y || (TC && tr >= nb)) return;
+  const int h = d.z * p.G + rl - tr * p.G;
+  const size_t oidx = (size_t)(d.x + tl) * p.Hq + h;
+  if (!TV_CHECK(oidx < (size_t)p.T * p.Hq)) return;
+  float M = -INFINITY, l = 0.0f;
+  float4 a[kC];
 #pragma unroll
-      for (int j = 0; j < kMergeBatch; ++j) {
-        ml[j] = make_float2(-INFINITY, 0.0f);
-        v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j0 + j < d.w && TV_CHECK(i + j0 + j < (int)gridDim.x)) {
-          const size_t slot = j0 + j == 0 ? 2 * i + 1 : 2 * (i + j0 + j);
-          ml[j] = p.part_ml[slot * slot_rows + row];
-          v[j] = *reinterpret_cast<const float4*>(p.part + slot * slot_rows * D +
-                                                  (TC ? ((size_t)c * slot_rows + row) * 4
-                                                      : (size_t)row * D + 4 * c));
-        }
-      }
-      float mx = M;
+  for (int c = 0; c < kC; ++c) a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = 0; j0 < d.w; j0 += kMergeBatch) {
+    float2 ml[kMergeBatch];
+    float4 v[kMergeBatch][kC];
 #pragma unroll
-      for (int j = 0; j < kMergeBatch; ++j) mx = fmaxf(mx, ml[j].x);
-      if (mx == -INFINITY) continue;
-      const float f = M == -INFINITY ? 0.0f : ex2(M - mx);
-      M = mx;
-      l *= f;
-      a.x *= f;
-      a.y *= f;
-      a.z *= f;
-      a.w *= f;
+    for (int j = 0; j < kMergeBatch; ++j) {
+      ml[j] = make_float2(-INFINITY, 0.0f);
+      if (j0 + j < d.w && TV_CHECK(i + j0 + j < (int)gridDim.x)) {
+        const size_t slot = j0 + j == 0 ? 2 * i + 1 : 2 * (i + j0 + j);
+        ml[j] = p.part_ml[slot * kRows + row];
+        const float4* src = reinterpret_cast<const float4*>(p.part) + slot * kRows * kChunks;
 #pragma unroll
-      for (int j = 0; j < kMergeBatch; ++j) {
-        if (ml[j].x == -INFINITY) continue;  // (a part whose keys are all hidden: select, do not multiply)
-        const float e = ex2(ml[j].x - M);
-        l = fmaf(e, ml[j].y, l);
-        a.x = fmaf(e, v[j].x, a.x);
-        a.y = fmaf(e, v[j].y, a.y);
-        a.z = fmaf(e, v[j].z, a.z);
-        a.w = fmaf(e, v[j].w, a.w);
+        for (int c = 0; c < kC; ++c)
+          v[j][c] = src[TC ? (c0 + c) * kRows + row : row * kChunks + c0 + c];
       }
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const size_t oidx = (size_t)(s.t0 + first + tl) * p.Hq + h;
-    if (!TV_CHECK(oidx < (size_t)p.T * p.Hq)) continue;
-    *reinterpret_cast<uint2*>(p.out + oidx * D + 4 * c) =
-        make_uint2(pack2<F16>(a.x * inv, a.y * inv), pack2<F16>(a.z * inv, a.w * inv));
-    if (c == 0 && p.lse) p.lse[oidx] = l > 0.0f ? (M + log2f(l)) * kLn2 : -INFINITY;
+    float mx = M;
+#pragma unroll
+    for (int j = 0; j < kMergeBatch; ++j) mx = fmaxf(mx, ml[j].x);
+    if (mx == -INFINITY) continue;
+    const float f = M == -INFINITY ? 0.0f : ex2(M - mx);
+    M = mx;
+    l *= f;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      a[c].x *= f;
+      a[c].y *= f;
+      a[c].z *= f;
+      a[c].w *= f;
+    }
+#pragma unroll
+    for (int j = 0; j < kMergeBatch; ++j) {
+      if (ml[j].x == -INFINITY) continue;  // (a part whose keys are all hidden: select, do not multiply)
+      const float e = ex2(ml[j].x - M);
+      l = fmaf(e, ml[j].y, l);
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        a[c].x = fmaf(e, v[j][c].x, a[c].x);
+        a[c].y = fmaf(e, v[j][c].y, a[c].y);
+        a[c].z = fmaf(e, v[j][c].z, a[c].z);
+        a[c].w = fmaf(e, v[j][c].w, a[c].w);
+      }
+    }
   }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  uint2* out = reinterpret_cast<uint2*>(p.out + oidx * D) + c0;
+#pragma unroll
+  for (int c = 0; c < kC; ++c)
+    out[c] = make_uint2(pack2<F16>(a[c].x * inv, a[c].y * inv), pack2<F16>(a[c].z * inv, a[c].w * inv));
+  if (c0 == 0 && p.lse) p.lse[oidx] = l > 0.0f ? (M + log2f(l)) * kLn2 : -INFINITY;
 }
 
 // --------------------------------------------------------------------- host
@@ -144,8 +167,10 @@ bool map_cache(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void*
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr long long kWholeRowsKeys = 1024, kWholeTcKeys = 512;
+
 // Which kernel runs, by the rows of the largest unit.
-PagedPlan paged_plan(int max_q, int G, int D) {
+PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long keys) {
   PagedPlan pl;
   const long long rows = (long long)max_q * G;
   // 64 decode sequences of 512 to 8,192 keys, 8 kv heads, D 128: 4 rows a unit 188 us here and RULE4 us on the
@@ -164,10 +189,16 @@ PagedPlan paged_plan(int max_q, int G, int D) {
     pl.ctas = device_sm_count();
     pl.min_share = 4;
   }
+  // Units short enough for a CTA each (keys: the most a sequence can have) are not split, and
+  // the merge is not launched.
+  pl.whole = keys <= (pl.small ? kWholeRowsKeys : kWholeTcKeys) &&
+             (long long)Hkv * (T / pl.tq + B) <= device_sm_count();
+  if (pl.whole) pl.min_share = 1;
   const size_t r = 2 * (size_t)pl.ctas * pl.rows;
   pl.part_bytes = align_up(r * D * 4, 256);
   pl.ml_bytes = align_up(r * 8, 256);
   pl.desc_bytes = align_up((size_t)pl.ctas * 16, 256);
+  pl.timeout_bytes = align_up((size_t)pl.ctas * 4, 256);
   return pl;
 }
 
@@ -175,9 +206,9 @@ template <int D, bool F16>
 cudaError_t launch_merge(const PagedPlan& pl, const PagedAttnParams& p, cudaStream_t stream) {
   if (pl.small)
     return launch_pdl(paged_merge_kernel<D, F16, false>, dim3(pl.ctas, 1), dim3(kMergeThreads), 0,
-                      stream, p, pl.rows, pl.nb);
-  return launch_pdl(paged_merge_kernel<D, F16, true>, dim3(pl.ctas, 8), dim3(kMergeThreads), 0, stream,
-                    p, pl.rows, pl.nb);
+                      stream, p, pl.nb);
+  return launch_pdl(paged_merge_kernel<D, F16, true>, dim3(pl.ctas, D / 16), dim3(kMergeThreads), 0,
+                    stream, p, pl.nb);
 }
 
 }  // namespace
@@ -187,7 +218,7 @@ cudaError_t launch_merge(const PagedPlan& pl, const PagedAttnParams& p, cudaStre
 extern "C" size_t tv_attn_paged_workspace_size(int max_q, int Hq, int Hkv, int D) {
   if (max_q < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128))
     return 0;
-  return tv::paged::paged_plan(max_q, Hq / Hkv, D).bytes();
+  return tv::paged::paged_plan(max_q, Hkv, Hq / Hkv, D, 0, 0, 0).bytes();  // (whatever B, T and keys are)
 }
 
 extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -228,7 +259,8 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   if (!tv::paged::order_strides(extent, stride, D, order)) return TV_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15)
     return TV_ERR_INVALID_ARG;
-  const tv::paged::PagedPlan pl = tv::paged::paged_plan(max_q, Hq / Hkv, D);
+  const tv::paged::PagedPlan pl =
+      tv::paged::paged_plan(max_q, Hkv, Hq / Hkv, D, B, T, (long long)P << c.page_shift);
   if (!workspace || ws_bytes < pl.bytes() || (reinterpret_cast<uintptr_t>(workspace) & 255))
     return TV_ERR_WORKSPACE;
   auto encode = tv::paged::tensor_map_encoder();
@@ -256,6 +288,7 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.part_bytes);
   p.desc = reinterpret_cast<int4*>(ws + pl.part_bytes + pl.ml_bytes);
+  p.timeout = reinterpret_cast<int*>(ws + pl.part_bytes + pl.ml_bytes + pl.desc_bytes);
   p.q = static_cast<const uint16_t*>(q);
   p.table = block_table;
   p.q_start = q_start;
@@ -281,6 +314,7 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   }
   p.tq = pl.tq;
   p.min_share = pl.min_share;
+  p.whole = pl.whole;
   const float sc = scale == 0.0f ? 1.0f / sqrtf((float)D) : scale;
   p.scale_log2 = sc * tv::paged::kLog2e;
   p.softcap_log2 = softcap * tv::paged::kLog2e;
@@ -298,7 +332,7 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   const bool f16 = cache->dtype == TV_FP16;
   cudaError_t e = pl.small ? tv::paged::launch_rows(pl, D, f16, bias || softcap > 0.0f, tmK, tmV, p, stream)
                         : tv::paged::launch_tc(pl, D, f16, bias, tmQ, tmK, tmV, p, stream);
-  if (e == cudaSuccess)
+  if (e == cudaSuccess && !pl.whole)
     e = D == 128 ? (f16 ? tv::paged::launch_merge<128, true>(pl, p, stream)
                         : tv::paged::launch_merge<128, false>(pl, p, stream))
                  : (f16 ? tv::paged::launch_merge<64, true>(pl, p, stream)

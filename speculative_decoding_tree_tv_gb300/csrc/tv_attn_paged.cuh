@@ -51,12 +51,14 @@ struct PagedAttnParams {
   int32_t* status;
   float* part;      // [2 * CTAs] slots of partial rows
   float2* part_ml;  // their (running maximum, log2 domain; running sum)
-  int4* desc;       // [CTAs]: the unit a CTA's share ends inside (b, kvh, qt, parts)
+  int4* desc;       // [CTAs]: the unit a CTA's share ends inside (first token, tokens, kv head, parts)
+  int* timeout;     // [CTAs]: 1 + a sequence whose waits gave up, or 0
   int B, T, P, Hq, Hkv, G, W, window;
   int num_pages, page_shift;
   int row_dim, head_dim;  // which of a cache map's dimensions 1, 2, 3 they are (the pages: the third)
   int tq;           // tokens per query tile
   int min_share;    // least cost of a share
+  int whole;        // one unit a CTA, none is split: no merge follows
   float scale_log2, softcap_log2, cap_in;  // cap_in: scale / softcap
   float cap_q[4], cap_top;  // capped scores s of s^2 <= cap_top: s (q0 + q1 s^2 + q2 s^4 + q3 s^6)
 };
@@ -205,27 +207,32 @@ __device__ __forceinline__ int key_tiles(const PagedAttnParams& p, const Seq& s,
 
 struct Part {
   Seq s;
-  int b, kvh, qt;
+  int b;             // its sequence; -1: the share is at its end
+  int kvh;
   int first, ntok;   // the query tile's tokens: first, count
   int lo, hi;        // its keys
   int begin, end;    // key tiles of this part
-  int tiles;         // the unit's key tiles
   int slot;          // partial slot, or -1: the whole unit is here
+  int parts;         // a unit that this part begins: how many parts it has
 };
 
-// A CTA's walk over its share [x, x1) of the line.
+// A CTA's walk over its share of the line.
 template <int KT>
 struct Cursor {
-  long long x, x1, share;
-  int b, kvh, qt, pos;
+  long long rest, share;  // cost left, cost of a share
+  long long at;           // cost behind the share's start
+  int b, kvh, qt, pos;    // unit, and cost of it that lies behind
   Seq s;
 
-  __device__ __forceinline__ bool next(const PagedAttnParams& p, Part& o, int4* desc) {
-    const int cta = blockIdx.x;
-    while (x < x1) {
-      const int tiles = key_tiles<KT>(p, s, qt), cost = tiles + kUnitCost;
-      const int take = (int)min((long long)(cost - pos), x1 - x);
-      const int a = max(0, pos - kUnitCost), e = max(0, pos + take - kUnitCost);
+  __device__ __forceinline__ int cost_of(const PagedAttnParams& p, int tiles) const {
+    return p.whole ? 1 : tiles + kUnitCost;
+  }
+  __device__ __forceinline__ bool next(const PagedAttnParams& p, Part& o) {
+    while (rest > 0) {
+      const int tiles = key_tiles<KT>(p, s, qt), cost = cost_of(p, tiles);
+      const int take = (int)min((long long)(cost - pos), rest);
+      const int a = p.whole ? 0 : max(0, pos - kUnitCost);
+      const int e = p.whole ? tiles : max(0, pos + take - kUnitCost);
       const bool ends = pos + take == cost;
       const bool emit = e > a || (tiles == 0 && ends);
       if (emit) {
@@ -233,19 +240,15 @@ struct Cursor {
         o.s = s;
         o.b = b;
         o.kvh = kvh;
-        o.qt = qt;
         o.first = qt * p.tq;
         o.ntok = min(p.tq, s.n - o.first);
-        o.tiles = tiles;
         o.begin = o.lo / KT + a;
         o.end = o.lo / KT + e;
-        o.slot = (a == 0 && e == tiles) ? -1 : 2 * cta + (a == 0);
-        if (desc && o.slot >= 0 && a == 0) {
-          const long long xu = x - pos;
-          *desc = make_int4(b, kvh, qt, (int)((xu + cost - 1) / share - (xu + kUnitCost) / share) + 1);
-        }
+        o.slot = (a == 0 && e == tiles) ? -1 : 2 * (int)blockIdx.x + (a == 0);
+        o.parts = (o.slot >= 0 && a == 0) ? (int)((at - pos + cost - 1) / share) + 1 : 0;
       }
-      x += take;
+      rest -= take;
+      at += take;
       pos += take;
       if (ends) {
         pos = 0;
@@ -257,15 +260,35 @@ struct Cursor {
               if (++b >= p.B) break;
               s = load_seq(p, b);
             } while (s.n == 0);
-            if (b >= p.B) x = x1;
+            if (b >= p.B) rest = 0;
           }
         }
       }
       if (emit) return true;
     }
+    o.b = -1;
     return false;
   }
 };
+
+// (64-bit division costs some hundred cycles; the quotients here are small)
+__device__ __forceinline__ long long div_fast(long long a, long long b) {
+  if (((a | b) >> 31) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+
+// Lines of the lengths and of the block table into the L2, shared out over the CTAs, while
+// the previous kernel finishes: a hint, which changes no result if that kernel writes them.
+template <int THREADS>
+__device__ __forceinline__ void prefetch_lengths(const PagedAttnParams& p) {
+  const int first = (blockIdx.x * THREADS + threadIdx.x) * 32, step = gridDim.x * THREADS * 32;
+  for (int i = first; i < p.B; i += step) {
+    line_prefetch_l2(p.q_start + i);
+    line_prefetch_l2(p.kv_len + i);
+  }
+  const long long words = min((long long)p.B * p.P, (long long)step);  // (one line a thread)
+  if (first < words) line_prefetch_l2(p.table + first);
+}
 
 // Finds this CTA's share.  All THREADS threads call it; ends with a barrier.
 template <int KT, int THREADS>
@@ -274,12 +297,17 @@ __device__ __forceinline__ Cursor<KT> find_share(const PagedAttnParams& p) {
   __shared__ Cursor<KT> s_cur;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = ceil_div(p.B, THREADS), b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  long long sum = 0;
+  Cursor<KT> c;
+  auto head_cost = [&](const Seq& s) {  // of one kv head's units
+    long long v = 0;
+    for (int qt = 0; qt * (long long)p.tq < s.n; ++qt) v += c.cost_of(p, key_tiles<KT>(p, s, qt));
+    return v;
+  };
+  long long sum = 0, one = 0;
   for (int b = b0; b < b1; ++b) {
-    const Seq s = load_seq(p, b);
-    long long c = 0;
-    for (int qt = 0; qt * (long long)p.tq < s.n; ++qt) c += key_tiles<KT>(p, s, qt) + kUnitCost;
-    sum += c * p.Hkv;
+    c.s = load_seq(p, b);
+    one = head_cost(c.s);
+    sum += one * p.Hkv;
   }
   long long inc = sum;
 #pragma unroll
@@ -288,7 +316,7 @@ __device__ __forceinline__ Cursor<KT> find_share(const PagedAttnParams& p) {
     if (lane >= o) inc += v;
   }
   if (lane == 31) s_warp[warp] = inc;
-  if (tid == 0) s_cur.x = s_cur.x1 = 0;
+  if (tid == 0) s_cur.rest = 0;
   __syncthreads();
   long long base = inc - sum, total = 0;
 #pragma unroll
@@ -296,70 +324,98 @@ __device__ __forceinline__ Cursor<KT> find_share(const PagedAttnParams& p) {
     if (w < warp) base += s_warp[w];
     total += s_warp[w];
   }
-  const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_share);
-  const long long x0 = blockIdx.x * share, x1 = min(total, x0 + share);
-  if (x0 < x1 && x0 >= base && x0 < base + sum) {  // this thread's sequences hold the share's start
-    Cursor<KT> c;
-    c.x = x0;
-    c.x1 = x1;
-    c.share = share;
-    for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq(p, b);
-      long long one = 0;
-      for (int qt = 0; qt * (long long)p.tq < s.n; ++qt) one += key_tiles<KT>(p, s, qt) + kUnitCost;
-      const long long r = x0 - base;
-      base += one * p.Hkv;
-      if (x0 >= base) continue;
-      c.b = b;
-      c.s = s;
-      c.kvh = (int)(r / one);
-      long long left = r - c.kvh * one;
-      c.qt = 0;
-      for (;;) {
-        const int cost = key_tiles<KT>(p, s, c.qt) + kUnitCost;
-        if (left < cost) break;
-        left -= cost;
-        ++c.qt;
+  c.share = max(div_fast(total + gridDim.x - 1, gridDim.x), (long long)p.min_share);
+  const long long x0 = blockIdx.x * c.share;
+  c.rest = min(total - x0, c.share);
+  if (c.rest > 0 && x0 >= base && x0 < base + sum) {  // this thread's sequences hold the share's start
+    c.b = b0;
+    if (per > 1) {
+      for (;; ++c.b) {
+        c.s = load_seq(p, c.b);
+        one = head_cost(c.s);
+        if (x0 < base + one * p.Hkv) break;
+        base += one * p.Hkv;
       }
-      c.pos = (int)left;
-      break;
     }
+    c.at = 0;
+    c.kvh = (int)div_fast(x0 - base, one);
+    long long left = x0 - base - c.kvh * one;
+    for (c.qt = 0;; ++c.qt) {
+      const int cost = c.cost_of(p, key_tiles<KT>(p, c.s, c.qt));
+      if (left < cost) break;
+      left -= cost;
+    }
+    c.pos = (int)left;
     s_cur = c;
   }
   __syncthreads();
   return s_cur;
 }
 
-// status[b] of the sequences b = CTA, CTA + grid, ..: lengths, and every page id
-// that the window reaches.  `threads` consecutive threads from 0 take part.
-__device__ __forceinline__ void write_status(const PagedAttnParams& p, int threads, int bar) {
-  if (!p.status) return;
-  __shared__ int s_bad;
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const Seq s = load_seq(p, b);
-    int t0, n;
-    const bool bad = !seq_range(p.q_start, b, p.T, t0, n) || s.bad;
-    if (!bad && s.n > 0) {
-      int lo, hi;
-      key_range(p, s, 0, lo, hi);
-      hi = s.L + s.n;
-      if (threadIdx.x == 0) s_bad = 0;
-      named_sync(bar, threads);
-      int any = 0;
-      const int32_t* row = p.table + (size_t)b * p.P;
-#pragma unroll 4
-      for (int j = (lo >> p.page_shift) + threadIdx.x; j <= (hi - 1) >> p.page_shift; j += threads) {
-        const int page = TV_IN(j, p.P) ? __ldg(row + j) : 0;
-        any |= page < 0 || page >= p.num_pages;
-      }
-      if (any) s_bad = 1;
-      named_sync(bar, threads);
-      if (threadIdx.x == 0) p.status[b] = s_bad ? TV_ERR_INVALID_ARG : TV_OK;
-      named_sync(bar, threads);
-    } else if (threadIdx.x == 0) {
-      p.status[b] = bad ? TV_ERR_INVALID_ARG : TV_OK;
+// The parts of a CTA's share, published by the one warp that walks it: the other
+// warps read a part from shared memory when they come to it.
+constexpr int kPartRing = 4;
+struct PartRing {
+  Part part[kPartRing];
+  uint64_t full[kPartRing], empty[kPartRing];
+
+  __device__ __forceinline__ void init(int readers) {  // one thread
+    for (int i = 0; i < kPartRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], readers);
     }
   }
+  // (a whole warp)
+  __device__ __forceinline__ bool publish(uint32_t n, const Part& w) {
+    const uint32_t i = n % kPartRing;
+    if (!__all_sync(0xffffffffu, mbar_wait(&empty[i], ((n / kPartRing) & 1) ^ 1))) return false;
+    if ((threadIdx.x & 31) == 0) {
+      part[i] = w;
+      mbar_arrive(&full[i]);
+    }
+    __syncwarp();
+    return true;
+  }
+  __device__ __forceinline__ bool ready(uint32_t n) {
+    return mbar_wait(&full[n % kPartRing], (n / kPartRing) & 1);
+  }
+  __device__ __forceinline__ const Part& at(uint32_t n) const { return part[n % kPartRing]; }
+  __device__ __forceinline__ void done(uint32_t n) { mbar_arrive(&empty[n % kPartRing]); }  // one thread
+};
+
+// Whether sequence b's lengths fit and its pages are pages, as far as the window reaches;
+// `lane` of `lanes` threads looks at its share of the pages.
+__device__ __forceinline__ bool seq_ok(const PagedAttnParams& p, int b, int lane, int lanes) {
+  int t0, n;
+  if (!seq_range(p.q_start, b, p.T, t0, n)) return false;
+  const Seq s = load_seq(p, b);
+  if (s.bad) return false;
+  if (n == 0) return true;
+  int lo, hi, any = 0;
+  key_range(p, s, 0, lo, hi);
+  hi = s.L + n;
+  const int32_t* row = p.table + (size_t)b * p.P;
+#pragma unroll 8
+  for (int j = (lo >> p.page_shift) + lane; j <= (hi - 1) >> p.page_shift; j += lanes) {
+    const int page = TV_IN(j, p.P) ? __ldg(row + j) : 0;
+    any |= page < 0 || page >= p.num_pages;
+  }
+  return any == 0;
+}
+// status[b] of the sequences b = CTA, CTA + grid, .., by one warp, where no merge kernel follows
+// to write it.
+__device__ __forceinline__ void write_status(const PagedAttnParams& p) {
+  if (!p.status) return;
+  const int lane = threadIdx.x & 31;
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const bool ok = __all_sync(0xffffffffu, seq_ok(p, b, lane, 32));
+    if (lane == 0) p.status[b] = ok ? TV_OK : TV_ERR_INVALID_ARG;
+  }
+}
+// A wait of this CTA gave up (one thread).
+__device__ __forceinline__ void report_timeout(const PagedAttnParams& p, int b) {
+  if (!p.whole) p.timeout[blockIdx.x] = b + 1;
+  else if (p.status && b >= 0) atomicMax(p.status + b, (int)TV_ERR_TIMEOUT);
 }
 
 // The page of key position `key` if the unit needs it, else (or where the table holds
@@ -379,8 +435,9 @@ struct PagedPlan {
   bool small;  // units of at most 16 rows: paged_rows_kernel
   int rows;  // rows of a unit
   int tq, nb, ctas, min_share;
-  size_t part_bytes, ml_bytes, desc_bytes;
-  size_t bytes() const { return part_bytes + ml_bytes + desc_bytes; }
+  int whole;  // units are not split: one launch
+  size_t part_bytes, ml_bytes, desc_bytes, timeout_bytes;
+  size_t bytes() const { return part_bytes + ml_bytes + desc_bytes + timeout_bytes; }
 };
 
 constexpr int kRowsKeys = 64, kTcKeys = 128;  // keys of a tile of either kernel

@@ -19,9 +19,10 @@ struct RowsLayout {
   static constexpr int kAtoms = D / 64;
   static constexpr int kAtom = kRowsKeys * 128;           // bytes of one 64-dim atom of a stage
   static constexpr int kSide = kAtoms * kAtom;            // K or V of a stage
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  // stages: half the shared memory of an SM, or all of it where a CTA has the SM to itself
+  static constexpr int kStages = D == 128 ? 3 : 6, kMaxStages = 2 * kStages;
   static constexpr int kScratch = kRowsWarps * 16 * 32 * 4;  // [warp][row][32 dims]
-  static constexpr int kDyn = 2 * kStages * kSide + kScratch + 1024;
+  static constexpr int dyn(int stages) { return 2 * stages * kSide + kScratch + 1024; }
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -58,19 +59,22 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sK = smem;
-  uint8_t* sV = smem + Lay::kStages * Lay::kSide;
+  const uint32_t stages = p.whole ? Lay::kMaxStages : Lay::kStages;
+  uint8_t* sV = smem + stages * Lay::kSide;
   // the unit's Q rows; at its end the warps' outputs (32 dims at a time)
-  uint4* s_q = reinterpret_cast<uint4*>(smem + 2 * Lay::kStages * Lay::kSide);
+  uint4* s_q = reinterpret_cast<uint4*>(smem + 2 * stages * Lay::kSide);
   float* s_acc = reinterpret_cast<float*>(s_q);
-  __shared__ __align__(8) uint64_t bar_full[Lay::kStages], bar_empty[Lay::kStages];
-  __shared__ uint32_t s_bad_pages[Lay::kStages];  // bit g: keys 8 g .. 8 g + 7 have no page
+  __shared__ __align__(8) uint64_t bar_full[Lay::kMaxStages], bar_empty[Lay::kMaxStages];
+  __shared__ uint32_t s_bad_pages[Lay::kMaxStages];  // bit g: keys 8 g .. 8 g + 7 have no page
   __shared__ float2 s_ml[kRowsWarps][kUnitRows];
   __shared__ volatile int s_abort;  // a consumer's wait ran out
+  __shared__ PartRing s_ring;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   if (tid == 0) {
     s_abort = 0;
-    for (int s = 0; s < Lay::kStages; ++s) {
+    s_ring.init(kRowsWarps);
+    for (int s = 0; s < Lay::kMaxStages; ++s) {
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_empty[s], kRowsWarps);
     }
@@ -78,30 +82,39 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
+  prefetch_lengths<kRowsThreads>(p);
   pdl_wait();
   Cursor<kRowsKeys> cur = find_share<kRowsKeys, kRowsThreads>(p);
   const int rows_page = min(1 << p.page_shift, kRowsKeys);  // rows of one box
-  Part w;
-  uint32_t it = 0;  // stages used so far
+  uint32_t it = 0, np = 0;  // stages and parts so far
 
   if (warp == kRowsWarps) {
     // ------------------------------------------------------------ producer
-    if (tid == kRowsWarps * 32) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    Part w;
+    if (!p.whole && lane == 0) {
+      p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+      p.timeout[blockIdx.x] = 0;
+    }
     const int npg = kRowsKeys / rows_page;
     const int pg = lane % npg, atom = (lane / npg) % Lay::kAtoms, side = lane / (npg * Lay::kAtoms);
     const bool issues = side < 2;
     const int row0 = pg * rows_page;
     bool ok = true;
-    while (ok && cur.next(p, w, lane == 0 ? p.desc + blockIdx.x : nullptr)) {
+    for (;; ++np) {
+      const bool more = cur.next(p, w);
+      ok = s_ring.publish(np, w);
+      if (!ok || !more) break;
+      if (w.parts && lane == 0)
+        p.desc[blockIdx.x] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
       bool bad;
       int page = w.begin < w.end ? page_at(p, w, (w.end - 1) * kRowsKeys + row0, rows_page, bad) : 0;
       for (int t = w.end - 1; t >= w.begin; --t, ++it) {
-        const int st = it % Lay::kStages;
+        const int st = it % stages;
         const int key = t * kRowsKeys + row0;
         bool bad_next = false;
         int page_next = 0;
         if (t > w.begin) page_next = page_at(p, w, key - kRowsKeys, rows_page, bad_next);
-        ok = warp_wait(&bar_empty[st], ((it / Lay::kStages) & 1) ^ 1);
+        ok = warp_wait(&bar_empty[st], ((it / stages) & 1) ^ 1);
         if (!ok) break;
         const uint32_t bad_pages = __ballot_sync(0xffffffffu, bad && lane < npg);
         if (lane == 0) {
@@ -119,19 +132,31 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         page = page_next;
         bad = bad_next;
       }
+      if (!ok) break;
     }
+    if (p.whole) write_status(p);
     // no copy may be in flight when the CTA leaves
-    for (uint32_t i = it > (uint32_t)Lay::kStages ? it - Lay::kStages : 0; i < it; ++i)
-      mbar_wait(&bar_full[i % Lay::kStages], (i / Lay::kStages) & 1);
-    if (!ok && lane == 0 && p.status) atomicMax(p.status + w.b, (int)TV_ERR_TIMEOUT);
+    for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
+      mbar_wait(&bar_full[i % stages], (i / stages) & 1);
+    if (!ok && lane == 0) report_timeout(p, w.b);
     return;
   }
 
   // ---------------------------------------------------------------- consumers
-  write_status(p, kRowsWarps * 32, 1);
   const float cap_in2 = 2.0f * kLog2e * p.cap_in;
   const int g = lane >> 2, c2 = (lane & 3) * 2;  // fragment row and first column of this lane
-  while (cur.next(p, w, nullptr)) {
+  int b = 0;
+  for (;; ++np) {
+    // (a warp that gives up still joins the others at the unit's end, where all see it)
+    if (!__all_sync(0xffffffffu, s_ring.ready(np))) s_abort = 1;
+    named_sync(1, kRowsWarps * 32);
+    if (s_abort) {
+      if (tid == 0) report_timeout(p, b);
+      break;
+    }
+    const Part w = s_ring.at(np);
+    if (w.b < 0) break;
+    b = w.b;
     const int rows = w.ntok * p.G;
     // the unit's Q rows to shared memory (rows past the unit repeat its last one); 16-byte
     // chunk c of row r lies at c ^ (r & 7)
@@ -171,10 +196,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
                              ? (p.anc ? w.s.L + w.s.n : w.s.L + w.first + w.ntok) - p.window : -1;
 
     for (int t = w.end - 1; t >= w.begin; --t, ++it) {  // (last first: see paged_tc_kernel)
-      const int st = it % Lay::kStages;
+      const int st = it % stages;
       const int j0 = t * kRowsKeys + 16 * warp;
-      // (a warp that gives up still joins the others at the unit's end, where all see it)
-      if (!warp_wait(&bar_full[st], (it / Lay::kStages) & 1)) {
+      if (!warp_wait(&bar_full[st], (it / stages) & 1)) {
         s_abort = 1;
         break;
       }
@@ -362,8 +386,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (w.slot >= 0) p.part_ml[(size_t)w.slot * kUnitRows + row] = make_float2(mm, ll);
       else if (p.lse) p.lse[oidx] = w.s.bad ? 0.0f : (ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY);
     }
+    if (lane == 0) s_ring.done(np);
     if (abort) {
-      if (tid == 0 && p.status) atomicMax(p.status + w.b, (int)TV_ERR_TIMEOUT);
+      if (tid == 0) report_timeout(p, w.b);
       break;
     }
   }
@@ -372,9 +397,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 template <int D, bool F16, bool MOD>
 cudaError_t launch(const PagedPlan& pl, const CUtensorMap& tmK, const CUtensorMap& tmV,
                    const PagedAttnParams& p, cudaStream_t stream) {
-  if (!set_dyn_smem(paged_rows_kernel<D, F16, MOD>, RowsLayout<D>::kDyn)) return cudaErrorUnknown;
+  using Lay = RowsLayout<D>;
+  if (!set_dyn_smem(paged_rows_kernel<D, F16, MOD>, Lay::dyn(Lay::kMaxStages))) return cudaErrorUnknown;
   return launch_pdl(paged_rows_kernel<D, F16, MOD>, dim3(pl.ctas), dim3(kRowsThreads),
-                    (size_t)RowsLayout<D>::kDyn, stream, tmK, tmV, p);
+                    (size_t)Lay::dyn(pl.whole ? Lay::kMaxStages : Lay::kStages), stream, tmK, tmV, p);
 }
 
 }  // namespace

@@ -11,7 +11,7 @@
 //                   one page), each into a ring of its own;
 //   warp 9          the products: S_r = Q_r K^T and O_r += P_r V (tcgen05.mma, operands in
 //                   shared memory but P, which is read from TMEM where it overlays S_r);
-//   warp 11         the unit's Q rows.
+//   warp 11         walks the share and publishes its parts; the parts' Q rows.
 // The products are issued in the order PV_0(t), S_0(t + 1), PV_1(t), S_1(t + 1): while one row
 // block's softmax runs, the tensor core works on the other's.  S_r(t + 1) may
 // overwrite P_r(t), as products retire in issue order.  The next unit's first S
@@ -130,6 +130,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_bad_pages[kBadRing];  // bit g: keys 8 g .. 8 g + 7 have no page
   __shared__ volatile int s_abort;
+  __shared__ PartRing s_ring;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   if (tid == 0) {
@@ -153,17 +154,20 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     }
     mbar_fence_init();
     s_abort = 0;
+    s_ring.init(11);  // K, V, products, eight softmax warps
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
   if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
+  prefetch_lengths<kTcThreads>(p);
   pdl_wait();
   tc_fence_before();
   Cursor<kTcKeys> cur = find_share<kTcKeys, kTcThreads>(p);
   tc_fence_after();
   const uint32_t tmem = s_tmem;
-  Part w;
+  uint32_t n = 0;  // parts so far
+  int b = 0;       // their sequence
   bool ok = true;
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------------- K, V producers
@@ -173,7 +177,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint64_t* full = isV ? bar_v_full : bar_k_full;
     uint64_t* empty = isV ? bar_v_empty : bar_k_empty;
     const uint32_t stages = isV ? kVStages : kKStages;
-    if (!isV && lane == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
     const int rows_page = min(1 << p.page_shift, kTcKeys), npg = kTcKeys / rows_page;
     const int pg = lane % npg, atom = lane / npg, row0 = pg * rows_page;
     const bool issues = atom < A;
@@ -199,7 +202,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       z0 = 0;
       z1 = kTcKeys;
     };
-    while (ok && cur.next(p, w, !isV && lane == 0 ? p.desc + blockIdx.x : nullptr)) {
+    for (; ok; ++n) {
+      ok = __all_sync(0xffffffffu, s_ring.ready(n));
+      if (!ok) break;
+      const Part w = s_ring.at(n);
+      if (w.b < 0) break;
+      b = w.b;
       bool bad = false;
       int page = w.begin < w.end ? page_at(p, w, (w.end - 1) * kTcKeys + row0, rows_page, bad) : 0;
       for (int t = w.end - 1; t >= w.begin; --t, ++it) {
@@ -234,15 +242,27 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           z1 = min(kTcKeys, w.hi - t * kTcKeys);
         }
       }
+      if (lane == 0) s_ring.done(n);
     }
     if (isV && ok) clear_rows();
     // no copy may be in flight when the CTA leaves
     for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
       mbar_wait(&full[i % stages], (i / stages) & 1);
   } else if (warp == 11) {
-    // ----------------------------------------------------------- Q producer
+    // ------------------------------ the share's parts, and their Q rows
     uint32_t parts = 0;
-    while (ok && cur.next(p, w, nullptr)) {
+    Part w;
+    if (!p.whole && lane == 0) {
+      p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+      p.timeout[blockIdx.x] = 0;
+    }
+    for (;; ++n) {
+      const bool more = cur.next(p, w);
+      ok = s_ring.publish(n, w);
+      if (!ok || !more) break;
+      b = w.b;
+      if (w.parts && lane == 0)
+        p.desc[blockIdx.x] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
       if (w.begin == w.end) continue;
       ok = warp_wait(&bar_q_empty, (parts & 1) ^ 1) && !s_abort;
       if (!ok) break;
@@ -258,6 +278,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       __syncwarp();
       ++parts;
     }
+    if (p.whole) write_status(p);
     if (parts > 0) mbar_wait(&bar_q_full, (parts - 1) & 1);
   } else if (warp == 9) {
     // ------------------------------------------------------------- products
@@ -293,7 +314,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         kph ^= kst == kKStages - 1;
         kst = kst == kKStages - 1 ? 0 : kst + 1;
       };
-      while (ok && cur.next(p, w, nullptr)) {
+      for (; ok; ++n) {
+        ok = s_ring.ready(n);
+        if (!ok) break;
+        const Part w = s_ring.at(n);
+        s_ring.done(n);
+        if (w.b < 0) break;
+        b = w.b;
         const int T = w.end - w.begin, nrb = w.ntok > nb ? 2 : 1;
         if (T == 0) continue;
         ok = mbar_wait(&bar_q_full, qph) && mbar_wait(&bar_k_full[kst], kph);
@@ -345,16 +372,23 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (!mbar_wait(&bar_drain, 0)) s_abort = 1;
     }
     ok = __all_sync(0xffffffffu, ok);
+    b = __reduce_max_sync(0xffffffffu, b);
   } else {
     // -------------------------------------------------------------- softmax
-    write_status(p, 256, 1);
     const int rb = warp >> 2, row = tid & (kRB - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128 * rb, tO = tmem + kOCol + 128 * rb;
     const int tl = row / p.G, h_in = row % p.G;
     const bool warp_in_block = (warp & 3) * 32 < nb * p.G;
     uint32_t sc = 0, oc = 0, kt = 0;
-    while (ok && cur.next(p, w, nullptr)) {
+    for (; ok; ++n) {
+      ok = __all_sync(0xffffffffu, s_ring.ready(n));
+      if (!ok) break;
+      const Part w = s_ring.at(n);
+      __syncwarp();
+      if (lane == 0) s_ring.done(n);
+      if (w.b < 0) break;
+      b = w.b;
       const int T = w.end - w.begin, tile_tok = rb * nb + tl;
       const bool mine = tl < nb && tile_tok < w.ntok;
       const int h = w.kvh * p.G + h_in;
@@ -602,7 +636,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   }
   if (!ok) {
     s_abort = 1;
-    if (lane == 0 && p.status) atomicMax(p.status + w.b, (int)TV_ERR_TIMEOUT);
+    if (lane == 0) report_timeout(p, b);
   }
   tc_fence_before();
   __syncthreads();  // every role is done; TMA and MMA work has retired
