@@ -266,7 +266,7 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   auto encode = tv::paged::tensor_map_encoder();
   if (!encode) return TV_ERR_CUDA;
   CUtensorMap tmQ, tmK, tmV;
-  const int rows = min(cache->page_size, pl.small ? tv::paged::kRowsKeys : tv::paged::kTcKeys);
+  const int rows = min(cache->page_size, pl.small && !pl.whole ? 64 : 128);
   if (!tv::paged::map_cache(encode, &tmK, cache->k, cache, stride, order, rows) ||
       !tv::paged::map_cache(encode, &tmV, cache->v, cache, stride, order, rows))
     return TV_ERR_INVALID_ARG;

@@ -430,6 +430,50 @@ __device__ __forceinline__ int page_at(const PagedAttnParams& p, const Part& w, 
   return bad ? p.num_pages : page;
 }
 
+// The page ids of a part's tiles, last tile first, for a warp that issues their loads: one
+// coalesced read of the block table covers 32 pages, and the next is on its way
+// (a read per tile held the loads to a tile per memory latency).
+template <int KT>
+struct PageFeed {
+  int rows, per_tile, tiles;  // rows of a box; pages of a tile; tiles of a read
+  int page, page_next;
+  uint32_t bad, bad_next;     // bit l: lane l's page is needed and is none
+
+  __device__ __forceinline__ void read(const PagedAttnParams& p, const Part& w, int t0, int& pg,
+                                       uint32_t& bits) const {
+    const int lane = threadIdx.x & 31, back = lane / per_tile, t = t0 - back;
+    bool b = false;
+    pg = p.num_pages;
+    if (back < tiles && t >= w.begin)
+      pg = page_at(p, w, t * KT + (lane - back * per_tile) * rows, rows, b);
+    bits = __ballot_sync(0xffffffffu, b);
+  }
+  __device__ __forceinline__ void start(const PagedAttnParams& p, const Part& w) {
+    rows = min(1 << p.page_shift, KT);
+    per_tile = KT / rows;
+    tiles = 32 / per_tile;
+    read(p, w, w.end - 1, page, bad);
+    read(p, w, w.end - 1 - tiles, page_next, bad_next);
+  }
+  // For tile t (they come in order): the page of the box at row `pg` * rows, and bits of 8
+  // keys each that have no page.
+  __device__ __forceinline__ int get(const PagedAttnParams& p, const Part& w, int t, int pg,
+                                     uint32_t& bad8) {
+    const int i = w.end - 1 - t, off = i % tiles;
+    if (off == 0 && i > 0) {
+      page = page_next;
+      bad = bad_next;
+      read(p, w, t - tiles, page_next, bad_next);
+    }
+    bad8 = 0;
+    if (bad) {
+      const uint32_t b = bad >> (off * per_tile);
+      for (int g = 0; g < KT / 8; ++g) bad8 |= ((b >> (8 * g / rows)) & 1u) << g;
+    }
+    return __shfl_sync(0xffffffffu, page, off * per_tile + pg);
+  }
+};
+
 // How a call runs: the kernel, its CTAs, and the layout of the workspace.
 struct PagedPlan {
   bool small;  // units of at most 16 rows: paged_rows_kernel
@@ -440,7 +484,7 @@ struct PagedPlan {
   size_t bytes() const { return part_bytes + ml_bytes + desc_bytes + timeout_bytes; }
 };
 
-constexpr int kRowsKeys = 64, kTcKeys = 128;  // keys of a tile of either kernel
+constexpr int kTcKeys = 128;  // keys of a tile of the tcgen05 kernel
 
 // bias: slopes, or tree distances that the window reaches (mod: those or a cap)
 cudaError_t launch_rows(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmK,

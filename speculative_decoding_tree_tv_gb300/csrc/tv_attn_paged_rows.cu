@@ -11,18 +11,18 @@ namespace paged {
 namespace {
 
 constexpr int kUnitRows = 16;
-constexpr int kRowsWarps = 4;
-constexpr int kRowsThreads = 32 * (kRowsWarps + 1);
 
-template <int D>
+// NW consumer warps, 16 keys of a stage each: 4 and two CTAs an SM, which fill it when there is work
+// for all, or 8 and one CTA where every unit has an SM to itself (p.whole).
+template <int D, int NW>
 struct RowsLayout {
+  static constexpr int kKeys = 16 * NW;
   static constexpr int kAtoms = D / 64;
-  static constexpr int kAtom = kRowsKeys * 128;           // bytes of one 64-dim atom of a stage
-  static constexpr int kSide = kAtoms * kAtom;            // K or V of a stage
-  // stages: half the shared memory of an SM, or all of it where a CTA has the SM to itself
-  static constexpr int kStages = D == 128 ? 3 : 6, kMaxStages = 2 * kStages;
-  static constexpr int kScratch = kRowsWarps * 16 * 32 * 4;  // [warp][row][32 dims]
-  static constexpr int dyn(int stages) { return 2 * stages * kSide + kScratch + 1024; }
+  static constexpr int kAtom = kKeys * 128;         // bytes of one 64-dim atom of a stage
+  static constexpr int kSide = kAtoms * kAtom;      // K or V of a stage
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kScratch = NW * 16 * 32 * 4;  // [warp][row][32 dims]
+  static constexpr int kDyn = 2 * kStages * kSide + kScratch + 1024;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -49,23 +49,23 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, bool F16, bool MOD>
-__global__ void __launch_bounds__(kRowsThreads, 2)
+template <int D, bool F16, bool MOD, int NW>
+__global__ void __launch_bounds__(32 * (NW + 1), NW == 4 ? 2 : 1)
 paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const PagedAttnParams p) {
-  using Lay = RowsLayout<D>;
-  constexpr int kSteps = D / 16;
+  using Lay = RowsLayout<D, NW>;
+  constexpr int kSteps = D / 16, kRowsWarps = NW, kRowsKeys = 16 * NW, kRowsThreads = 32 * (NW + 1);
+  constexpr int kStages = Lay::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sK = smem;
-  const uint32_t stages = p.whole ? Lay::kMaxStages : Lay::kStages;
-  uint8_t* sV = smem + stages * Lay::kSide;
+  uint8_t* sV = smem + kStages * Lay::kSide;
   // the unit's Q rows; at its end the warps' outputs (32 dims at a time)
-  uint4* s_q = reinterpret_cast<uint4*>(smem + 2 * stages * Lay::kSide);
+  uint4* s_q = reinterpret_cast<uint4*>(smem + 2 * kStages * Lay::kSide);
   float* s_acc = reinterpret_cast<float*>(s_q);
-  __shared__ __align__(8) uint64_t bar_full[Lay::kMaxStages], bar_empty[Lay::kMaxStages];
-  __shared__ uint32_t s_bad_pages[Lay::kMaxStages];  // bit g: keys 8 g .. 8 g + 7 have no page
+  __shared__ __align__(8) uint64_t bar_full[kStages], bar_empty[kStages];
+  __shared__ uint32_t s_bad_pages[kStages];  // bit g: keys 8 g .. 8 g + 7 have no page
   __shared__ float2 s_ml[kRowsWarps][kUnitRows];
   __shared__ volatile int s_abort;  // a consumer's wait ran out
   __shared__ PartRing s_ring;
@@ -74,7 +74,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   if (tid == 0) {
     s_abort = 0;
     s_ring.init(kRowsWarps);
-    for (int s = 0; s < Lay::kMaxStages; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&bar_full[s], 1);
       mbar_init(&bar_empty[s], kRowsWarps);
     }
@@ -85,8 +85,11 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   prefetch_lengths<kRowsThreads>(p);
   pdl_wait();
   Cursor<kRowsKeys> cur = find_share<kRowsKeys, kRowsThreads>(p);
-  const int rows_page = min(1 << p.page_shift, kRowsKeys);  // rows of one box
-  uint32_t it = 0, np = 0;  // stages and parts so far
+  uint32_t st = 0, phase = 0, np = 0;  // stage, its ring's phase; parts so far
+  auto next_stage = [&]() {
+    phase ^= st == kStages - 1;
+    st = st == kStages - 1 ? 0 : st + 1;
+  };
 
   if (warp == kRowsWarps) {
     // ------------------------------------------------------------ producer
@@ -95,10 +98,12 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
       p.timeout[blockIdx.x] = 0;
     }
+    PageFeed<kRowsKeys> feed;
+    const int rows_page = min(1 << p.page_shift, kRowsKeys);  // rows of one box
+    uint32_t issued = 0;
     const int npg = kRowsKeys / rows_page;
-    const int pg = lane % npg, atom = (lane / npg) % Lay::kAtoms, side = lane / (npg * Lay::kAtoms);
-    const bool issues = side < 2;
-    const int row0 = pg * rows_page;
+    const int pg = lane % npg, atom = lane / npg, row0 = pg * rows_page;
+    const bool issues = atom < Lay::kAtoms;
     bool ok = true;
     for (;; ++np) {
       const bool more = cur.next(p, w);
@@ -106,38 +111,32 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (!ok || !more) break;
       if (w.parts && lane == 0)
         p.desc[blockIdx.x] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
-      bool bad;
-      int page = w.begin < w.end ? page_at(p, w, (w.end - 1) * kRowsKeys + row0, rows_page, bad) : 0;
-      for (int t = w.end - 1; t >= w.begin; --t, ++it) {
-        const int st = it % stages;
-        const int key = t * kRowsKeys + row0;
-        bool bad_next = false;
-        int page_next = 0;
-        if (t > w.begin) page_next = page_at(p, w, key - kRowsKeys, rows_page, bad_next);
-        ok = warp_wait(&bar_empty[st], ((it / stages) & 1) ^ 1);
+      feed.start(p, w);
+      for (int t = w.end - 1; t >= w.begin; --t) {
+        const int row = (t * kRowsKeys + row0) & ((1 << p.page_shift) - 1);
+        uint32_t bad8;
+        const int page = feed.get(p, w, t, pg, bad8);
+        ok = warp_wait(&bar_empty[st], phase ^ 1);
         if (!ok) break;
-        const uint32_t bad_pages = __ballot_sync(0xffffffffu, bad && lane < npg);
         if (lane == 0) {
-          uint32_t m = 0;
-          if (bad_pages)
-            for (int g = 0; g < kRowsKeys / 8; ++g) m |= ((bad_pages >> (8 * g / rows_page)) & 1u) << g;
-          s_bad_pages[st] = m;
+          s_bad_pages[st] = bad8;
           mbar_expect_tx(&bar_full[st], 2 * Lay::kSide);
         }
         __syncwarp();
-        if (issues)
-          tma_load_rows((side ? sV : sK) + st * Lay::kSide + atom * Lay::kAtom + row0 * 128,
-                        side ? &tmV : &tmK, &bar_full[st], atom * 64, key & ((1 << p.page_shift) - 1),
-                        w.kvh, page, p.row_dim, p.head_dim);
-        page = page_next;
-        bad = bad_next;
+        if (issues) {
+          const int at = st * Lay::kSide + atom * Lay::kAtom + row0 * 128;
+          tma_load_rows(sK + at, &tmK, &bar_full[st], atom * 64, row, w.kvh, page, p.row_dim, p.head_dim);
+          tma_load_rows(sV + at, &tmV, &bar_full[st], atom * 64, row, w.kvh, page, p.row_dim, p.head_dim);
+        }
+        next_stage();
+        ++issued;
       }
       if (!ok) break;
     }
     if (p.whole) write_status(p);
     // no copy may be in flight when the CTA leaves
-    for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
-      mbar_wait(&bar_full[i % stages], (i / stages) & 1);
+    for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+      mbar_wait(&bar_full[i % kStages], (i / kStages) & 1);
     if (!ok && lane == 0) report_timeout(p, w.b);
     return;
   }
@@ -195,10 +194,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const int all_from = p.window > 0
                              ? (p.anc ? w.s.L + w.s.n : w.s.L + w.first + w.ntok) - p.window : -1;
 
-    for (int t = w.end - 1; t >= w.begin; --t, ++it) {  // (last first: see paged_tc_kernel)
-      const int st = it % stages;
+    for (int t = w.end - 1; t >= w.begin; --t) {  // (last first: see paged_tc_kernel)
       const int j0 = t * kRowsKeys + 16 * warp;
-      if (!warp_wait(&bar_full[st], (it / stages) & 1)) {
+      if (!warp_wait(&bar_full[st], phase)) {
         s_abort = 1;
         break;
       }
@@ -323,6 +321,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_empty[st]);
+      next_stage();
     }
 
     // the four warps' rows joined in shared memory, 32 dims at a time
@@ -342,7 +341,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][r * 8 + g].x);
       f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mm);  // (0: nothing seen by this warp, its sums are 0)
     }
-    const int row = tid >> 3, od = (tid & 7) * 4;  // this thread's row and dims of a joined piece
+    const int row = (tid >> 3) & 15, od = (tid & 7) * 4;  // this thread's row and dims of a joined piece
     float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
     for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][row].x);
@@ -351,7 +350,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       const float2 v = s_ml[x][row];
       if (v.x != -INFINITY) ll = fmaf(ex2(v.x - mm), v.y, ll);
     }
-    const bool mine = row < rows;
+    const bool mine = tid < 128 && row < rows;
     const int out_tok = w.s.t0 + w.first + row / p.G, h = w.kvh * p.G + row % p.G;
     const size_t oidx = (size_t)out_tok * p.Hq + h;
     const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
@@ -397,10 +396,11 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 template <int D, bool F16, bool MOD>
 cudaError_t launch(const PagedPlan& pl, const CUtensorMap& tmK, const CUtensorMap& tmV,
                    const PagedAttnParams& p, cudaStream_t stream) {
-  using Lay = RowsLayout<D>;
-  if (!set_dyn_smem(paged_rows_kernel<D, F16, MOD>, Lay::dyn(Lay::kMaxStages))) return cudaErrorUnknown;
-  return launch_pdl(paged_rows_kernel<D, F16, MOD>, dim3(pl.ctas), dim3(kRowsThreads),
-                    (size_t)Lay::dyn(pl.whole ? Lay::kMaxStages : Lay::kStages), stream, tmK, tmV, p);
+  auto kernel = pl.whole ? paged_rows_kernel<D, F16, MOD, 8> : paged_rows_kernel<D, F16, MOD, 4>;
+  const int smem = pl.whole ? RowsLayout<D, 8>::kDyn : RowsLayout<D, 4>::kDyn;
+  if (!set_dyn_smem(kernel, smem)) return cudaErrorUnknown;
+  return launch_pdl(kernel, dim3(pl.whole ? device_sm_count() : pl.ctas), dim3(pl.whole ? 288 : 160),
+                    (size_t)smem, stream, tmK, tmV, p);
 }
 
 }  // namespace

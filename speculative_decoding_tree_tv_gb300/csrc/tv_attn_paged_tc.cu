@@ -177,6 +177,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint64_t* full = isV ? bar_v_full : bar_k_full;
     uint64_t* empty = isV ? bar_v_empty : bar_k_empty;
     const uint32_t stages = isV ? kVStages : kKStages;
+    PageFeed<kTcKeys> feed;
     const int rows_page = min(1 << p.page_shift, kTcKeys), npg = kTcKeys / rows_page;
     const int pg = lane % npg, atom = lane / npg, row0 = pg * rows_page;
     const bool issues = atom < A;
@@ -208,32 +209,22 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const Part w = s_ring.at(n);
       if (w.b < 0) break;
       b = w.b;
-      bool bad = false;
-      int page = w.begin < w.end ? page_at(p, w, (w.end - 1) * kTcKeys + row0, rows_page, bad) : 0;
+      feed.start(p, w);
       for (int t = w.end - 1; t >= w.begin; --t, ++it) {
         const uint32_t st = it % stages;
         const int key = t * kTcKeys + row0;
-        bool bad_next = false;
-        int page_next = 0;
-        if (t > w.begin) page_next = page_at(p, w, key - kTcKeys, rows_page, bad_next);
+        uint32_t bad8;
+        const int page = feed.get(p, w, t, pg, bad8);
         ok = warp_wait(&empty[st], ((it / stages) & 1) ^ 1) && !s_abort;
         if (!ok) break;
-        const uint32_t bad_pages = __ballot_sync(0xffffffffu, bad && lane < npg);
         if (lane == 0) {
-          if (!isV) {
-            uint32_t m = 0;
-            if (bad_pages)
-              for (int g = 0; g < kTcKeys / 8; ++g) m |= ((bad_pages >> (8 * g / rows_page)) & 1u) << g;
-            s_bad_pages[it % kBadRing] = m;
-          }
+          if (!isV) s_bad_pages[it % kBadRing] = bad8;
           mbar_expect_tx(&full[st], Lay::kTile);
         }
         __syncwarp();
         if (issues)
           tma_load_rows(ring + st * Lay::kTile + atom * kAtomBytes + row0 * 128, map, &full[st],
                         atom * 64, key & ((1 << p.page_shift) - 1), w.kvh, page, p.row_dim, p.head_dim);
-        page = page_next;
-        bad = bad_next;
         if (isV) {
           clear_rows();
           if (!ok) break;
