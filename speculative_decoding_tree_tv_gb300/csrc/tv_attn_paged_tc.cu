@@ -375,26 +375,29 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     for (; ok; ++n) {
       ok = __all_sync(0xffffffffu, s_ring.ready(n));
       if (!ok) break;
-      const Part w = s_ring.at(n);
-      __syncwarp();
-      if (lane == 0) s_ring.done(n);
+      const Part& w = s_ring.at(n);  // (stays in shared memory: the tiles need the registers)
       if (w.b < 0) break;
       b = w.b;
-      const int T = w.end - w.begin, tile_tok = rb * nb + tl;
-      const bool mine = tl < nb && tile_tok < w.ntok;
-      const int h = w.kvh * p.G + h_in;
-      const size_t oidx = (size_t)(w.s.t0 + w.first + tile_tok) * p.Hq + h;
+      const int T = w.end - w.begin;
+      const int L = w.s.L, hi = w.hi, j_last = (w.end - 1) * kTcKeys;
       if (T == 0) {  // a sequence with a status
+        const int tile_tok = rb * nb + tl;
+        const bool mine = tl < nb && tile_tok < w.ntok;
+        const size_t oidx = (size_t)(w.s.t0 + w.first + tile_tok) * p.Hq + w.kvh * p.G + h_in;
         if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq)) {
           uint4* orow = reinterpret_cast<uint4*>(p.out + oidx * D);
 #pragma unroll
           for (int c = 0; c < D / 8; ++c) orow[c] = make_uint4(0, 0, 0, 0);
           if (p.lse) p.lse[oidx] = 0.0f;
         }
+        __syncwarp();
+        if (lane == 0) s_ring.done(n);
         continue;
       }
       if (rb * nb >= w.ntok) {  // no second row block
         kt += T;
+        __syncwarp();
+        if (lane == 0) s_ring.done(n);
         continue;
       }
       // rows past the unit take the last token's mask: computed, never written
@@ -405,19 +408,19 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       r.pos = w.s.L + (p.anc ? anc_count(r.anc, p.W, 64 * p.W) - 1 : i);
       r.limit = p.anc ? w.s.L : w.s.L + i + 1;
       r.from = p.window > 0 ? r.pos - p.window + 1 : 0;
-      const float slope = (BIAS && p.slopes) ? __ldg(p.slopes + h) * kLog2e : 0.0f;
+      const float slope = (BIAS && p.slopes) ? __ldg(p.slopes + w.kvh * p.G + h_in) * kLog2e : 0.0f;
       // what turns a score into the log2 domain; capped scores are there already, and with
       // slopes it comes with the bias
       const float in_scale = CAP ? 1.0f : p.scale_log2;
       const float scale = (BIAS && p.slopes) ? 1.0f : in_scale;
       float m_run = -INFINITY, l_run = 0.0f;
       for (int t = 0; t < T; ++t, ++kt, ++sc) {
-        const int j0 = (w.end - 1 - t) * kTcKeys;
+        const int j0 = j_last - t * kTcKeys;
         uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (j0 + kTcKeys > r.limit || j0 < r.from) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            const uint32_t v = see32(p, r, j0 + 32 * c, w.s.L, w.hi);
+            const uint32_t v = see32(p, r, j0 + 32 * c, L, hi);
             if (c == 0) vis[0] = v;
             if (c == 1) vis[1] = v;
             if (c == 2) vis[2] = v;
@@ -494,7 +497,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             tmem_wait_ld();
           }
         }
-        if (BIAS && r.anc && j0 + kTcKeys > w.s.L) {
+        if (BIAS && r.anc && j0 + kTcKeys > L) {
           // the tile reaches the tree: also through TMEM
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_st32(tS + lane_base + 32 * c, sr[c]);
@@ -504,7 +507,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             uint32_t x[32], v = c == 0 ? vis[0] : c == 1 ? vis[1] : c == 2 ? vis[2] : vis[3];
             tmem_ld32(tS + lane_base + 32 * c, x);
             tmem_wait_ld();
-            tree_chunk(p, r, j0 + 32 * c, w.s.L, in_scale, slope, v, x);
+            tree_chunk(p, r, j0 + 32 * c, L, in_scale, slope, v, x);
             tmem_st32(tS + lane_base + 32 * c, x);
             if (c == 0) vis[0] = v;
             if (c == 1) vis[1] = v;
@@ -591,8 +594,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (!ok) break;
       ++oc;
       tc_fence_after();
-      if (!warp_works) continue;
+      if (!warp_works) {
+        if (lane == 0) s_ring.done(n);
+        continue;
+      }
       // ------------------------------------------------------- epilogue
+      const int tile_tok = rb * nb + tl;
+      const bool mine = tl < nb && tile_tok < w.ntok;
+      const size_t oidx = (size_t)(w.s.t0 + w.first + tile_tok) * p.Hq + w.kvh * p.G + h_in;
       const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
       const int crow = rb * kRB + row;
       if (w.slot >= 0 && mine) p.part_ml[(size_t)w.slot * 256 + crow] = make_float2(m_run, l_run);
@@ -623,6 +632,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (w.slot < 0 && mine && p.lse)
         p.lse[oidx] = l_run > 0.0f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) s_ring.done(n);
     }
   }
   if (!ok) {
