@@ -4,16 +4,17 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <chrono>
+
 #include "tv_attn_paged.cuh"
 
 namespace tv {
 namespace paged {
 namespace {
 
-// Joins the parts of the split units.  Block (i, y): the unit that CTA i's
-// share ends inside, if any; its parts are slots 2 i + 1, 2 (i + 1), 2 (i + 2), ..
-// Rows of the tcgen05 kernel lie chunk by chunk (TC: [D / 4][rows] of four floats, the
-// order its threads write), the others row by row.
+// Joins the parts of split units.  Block (i, y): the unit that share i ends inside, if any; its
+// parts are slots 2 i + 1, 2 (i + 1), 2 (i + 2), ..  Rows of the tcgen05 kernel (TC) lie chunk by
+// chunk ([D / 4][256] of four floats, the order its threads write), small units' row by row.
 constexpr int kMergeThreads = 256, kMergeBatch = 2;
 
 // The merge's blocks also write the sequences' status: it costs nothing here, while a scan of
@@ -169,6 +170,16 @@ bool map_cache(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void*
 
 constexpr long long kWholeRowsKeys = 1024, kWholeTcKeys = 512;
 
+// A mark of its own for every call, which nothing that a workspace held before is taken for: counted
+// on from a start that differs from process to process.
+unsigned long long next_token() {
+  static std::atomic<unsigned long long> token{
+      ((unsigned long long)std::chrono::system_clock::now().time_since_epoch().count() << 20) ^
+      (unsigned long long)reinterpret_cast<uintptr_t>(&tensor_map_encoder)};
+  return token.fetch_add(1, std::memory_order_relaxed) | 1ull << 63;
+}
+
+
 // Which kernel runs, by the rows of the largest unit.
 PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long keys) {
   PagedPlan pl;
@@ -194,11 +205,19 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
   pl.whole = keys <= (pl.small ? kWholeRowsKeys : kWholeTcKeys) &&
              (long long)Hkv * (T / pl.tq + B) <= device_sm_count();
   if (pl.whole) pl.min_share = 1;
+  // At least Hkv ceil(T / tokens of a unit) units: with two CTAs a unit or fewer the CTAs join
+  // split units themselves (16 trees of 64 nodes 77 us, 82 us with the merge kernel; one tree of 64
+  // behind 32,000 keys, 19 CTAs a unit, 86 and 47 us).  Small units always take the merge kernel:
+  // joining in the CTAs took 199 instead of 187 us for a decode of 64.
+  const int unit_tokens = pl.tq < max_q ? pl.tq : max_q;
+  pl.merge = !pl.whole &&
+             (pl.small || 2ll * Hkv * ((T + unit_tokens - 1) / unit_tokens) < pl.ctas);
   const size_t r = 2 * (size_t)pl.ctas * pl.rows;
   pl.part_bytes = align_up(r * D * 4, 256);
   pl.ml_bytes = align_up(r * 8, 256);
   pl.desc_bytes = align_up((size_t)pl.ctas * 16, 256);
   pl.timeout_bytes = align_up((size_t)pl.ctas * 4, 256);
+  pl.ready_bytes = align_up((size_t)pl.ctas * 64, 256);
   return pl;
 }
 
@@ -315,6 +334,10 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   p.tq = pl.tq;
   p.min_share = pl.min_share;
   p.whole = pl.whole;
+  p.merge = pl.merge;
+  p.ready = reinterpret_cast<unsigned long long*>(ws + pl.part_bytes + pl.ml_bytes + pl.desc_bytes +
+                                                  pl.timeout_bytes);
+  p.token = tv::paged::next_token();
   const float sc = scale == 0.0f ? 1.0f / sqrtf((float)D) : scale;
   p.scale_log2 = sc * tv::paged::kLog2e;
   p.softcap_log2 = softcap * tv::paged::kLog2e;
@@ -332,7 +355,7 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   const bool f16 = cache->dtype == TV_FP16;
   cudaError_t e = pl.small ? tv::paged::launch_rows(pl, D, f16, bias || softcap > 0.0f, tmK, tmV, p, stream)
                         : tv::paged::launch_tc(pl, D, f16, bias, tmQ, tmK, tmV, p, stream);
-  if (e == cudaSuccess && !pl.whole)
+  if (e == cudaSuccess && pl.merge)
     e = D == 128 ? (f16 ? tv::paged::launch_merge<128, true>(pl, p, stream)
                         : tv::paged::launch_merge<128, false>(pl, p, stream))
                  : (f16 ? tv::paged::launch_merge<64, true>(pl, p, stream)

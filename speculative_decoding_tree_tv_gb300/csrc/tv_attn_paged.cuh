@@ -11,10 +11,12 @@
 // So a ragged batch is balanced whatever its lengths are, without the host
 // knowing them: every CTA finds its share from q_start and kv_len alone.  A unit
 // that a cut splits leaves 32-bit partial rows (running maximum, sum, unnormalised
-// output) in the workspace: at most one per CTA for the unit its share begins in
-// and one for the unit it ends in; the merge kernel, chained by programmatic
-// dependent launch, joins them.  The cuts depend on the lengths alone, so
-// results do not vary from run to run.
+// output) in the workspace, and they are joined in one of two ways.  Where units
+// are many, so that one is split over few CTAs, the CTA that a unit begins in (with the
+// last item of its share) joins the rows of those that go on with it (with the
+// first of theirs, so they are there as a rule).  Where few units are split
+// over many CTAs, a merge kernel joins them, chained by programmatic dependent launch.
+// The cuts depend on the lengths alone, so results do not vary from run to run.
 //
 // Two kernels take units: paged_rows_kernel (tv_attn_paged_rows.cu) those of at most 16 rows
 // (decode tokens and small trees: HBM-bound, warp-level mma), and
@@ -58,7 +60,10 @@ struct PagedAttnParams {
   int row_dim, head_dim;  // which of a cache map's dimensions 1, 2, 3 they are (the pages: the third)
   int tq;           // tokens per query tile
   int min_share;    // least cost of a share
-  int whole;        // one unit a CTA, none is split: no merge follows
+  int whole;        // one unit a CTA, none is split
+  int merge;        // a merge kernel joins the parts of split units, else the CTA a unit begins in
+  unsigned long long token;      // this call's mark in `ready`
+  unsigned long long* ready;     // [CTAs][8]: a warp of a share's first part has left its rows
   float scale_log2, softcap_log2, cap_in;  // cap_in: scale / softcap
   float cap_q[4], cap_top;  // capped scores s of s^2 <= cap_top: s (q0 + q1 s^2 + q2 s^4 + q3 s^6)
 };
@@ -205,6 +210,10 @@ __device__ __forceinline__ int key_tiles(const PagedAttnParams& p, const Seq& s,
   return (hi + KT - 1) / KT - lo / KT;
 }
 
+// Shares are handed out against the CTAs' order: a CTA waits for the rows of later shares alone, whose
+// CTAs have started before it.
+__device__ __forceinline__ int share_index() { return (int)(gridDim.x - 1 - blockIdx.x); }
+
 struct Part {
   Seq s;
   int b;             // its sequence; -1: the share is at its end
@@ -244,7 +253,7 @@ struct Cursor {
         o.ntok = min(p.tq, s.n - o.first);
         o.begin = o.lo / KT + a;
         o.end = o.lo / KT + e;
-        o.slot = (a == 0 && e == tiles) ? -1 : 2 * (int)blockIdx.x + (a == 0);
+        o.slot = (a == 0 && e == tiles) ? -1 : p.merge ? 2 * share_index() + (a == 0) : share_index();
         o.parts = (o.slot >= 0 && a == 0) ? (int)((at - pos + cost - 1) / share) + 1 : 0;
       }
       rest -= take;
@@ -325,7 +334,7 @@ __device__ __forceinline__ Cursor<KT> find_share(const PagedAttnParams& p) {
     total += s_warp[w];
   }
   c.share = max(div_fast(total + gridDim.x - 1, gridDim.x), (long long)p.min_share);
-  const long long x0 = blockIdx.x * c.share;
+  const long long x0 = share_index() * c.share;
   c.rest = min(total - x0, c.share);
   if (c.rest > 0 && x0 >= base && x0 < base + sum) {  // this thread's sequences hold the share's start
     c.b = b0;
@@ -414,8 +423,38 @@ __device__ __forceinline__ void write_status(const PagedAttnParams& p) {
 }
 // A wait of this CTA gave up (one thread).
 __device__ __forceinline__ void report_timeout(const PagedAttnParams& p, int b) {
-  if (!p.whole) p.timeout[blockIdx.x] = b + 1;
+  if (p.merge) p.timeout[blockIdx.x] = b + 1;
   else if (p.status && b >= 0) atomicMax(p.status + b, (int)TV_ERR_TIMEOUT);
+}
+
+// Hand-over of partial rows within the launch, warp by warp (a warp holds the same rows of a
+// unit in every CTA).  `ready` needs no clearing: a mark counts only if it is this
+// call's, and a replayed graph, whose calls keep their mark, finds it taken away again.
+__device__ __forceinline__ void leave_rows(const PagedAttnParams& p, int share, int warp) {
+  __threadfence();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p.ready + share * 8 + warp), "l"(p.token) : "memory");
+}
+// False if the rows did not come within the limit.
+__device__ __forceinline__ bool await_rows(const PagedAttnParams& p, int share, int warp) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    unsigned long long* at = p.ready + share * 8 + warp;
+    const long long t0 = clock64();
+    for (;;) {
+      unsigned long long v;
+      asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
+      if (v == p.token) break;
+      if (clock64() - t0 > kWaitLimitCycles) {
+        ok = false;
+        break;
+      }
+      __nanosleep(100);
+    }
+    if (ok) *at = 0;
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 // The page of key position `key` if the unit needs it, else (or where the table holds
@@ -479,9 +518,10 @@ struct PagedPlan {
   bool small;  // units of at most 16 rows: paged_rows_kernel
   int rows;  // rows of a unit
   int tq, nb, ctas, min_share;
-  int whole;  // units are not split: one launch
-  size_t part_bytes, ml_bytes, desc_bytes, timeout_bytes;
-  size_t bytes() const { return part_bytes + ml_bytes + desc_bytes + timeout_bytes; }
+  int whole;  // units are not split
+  int merge;  // the merge kernel follows
+  size_t part_bytes, ml_bytes, desc_bytes, timeout_bytes, ready_bytes;
+  size_t bytes() const { return part_bytes + ml_bytes + desc_bytes + timeout_bytes + ready_bytes; }
 };
 
 constexpr int kTcKeys = 128;  // keys of a tile of the tcgen05 kernel

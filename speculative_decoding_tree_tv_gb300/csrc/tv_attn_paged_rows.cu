@@ -94,8 +94,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   if (warp == kRowsWarps) {
     // ------------------------------------------------------------ producer
     Part w;
-    if (!p.whole && lane == 0) {
-      p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (p.merge && lane == 0) {
+      p.desc[share_index()] = make_int4(0, 0, 0, 0);
       p.timeout[blockIdx.x] = 0;
     }
     PageFeed<kRowsKeys> feed;
@@ -110,7 +110,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       ok = s_ring.publish(np, w);
       if (!ok || !more) break;
       if (w.parts && lane == 0)
-        p.desc[blockIdx.x] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
+        p.desc[share_index()] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
       feed.start(p, w);
       for (int t = w.end - 1; t >= w.begin; --t) {
         const int row = (t * kRowsKeys + row0) & ((1 << p.page_shift) - 1);
@@ -133,7 +133,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       }
       if (!ok) break;
     }
-    if (p.whole) write_status(p);
+    if (!p.merge) write_status(p);
     // no copy may be in flight when the CTA leaves
     for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
       mbar_wait(&bar_full[i % kStages], (i / kStages) & 1);

@@ -243,8 +243,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     // ------------------------------ the share's parts, and their Q rows
     uint32_t parts = 0;
     Part w;
-    if (!p.whole && lane == 0) {
-      p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (p.merge && lane == 0) {
+      p.desc[share_index()] = make_int4(0, 0, 0, 0);
       p.timeout[blockIdx.x] = 0;
     }
     for (;; ++n) {
@@ -252,8 +252,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       ok = s_ring.publish(n, w);
       if (!ok || !more) break;
       b = w.b;
-      if (w.parts && lane == 0)
-        p.desc[blockIdx.x] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
+      if (p.merge && w.parts && lane == 0)
+        p.desc[share_index()] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
       if (w.begin == w.end) continue;
       ok = warp_wait(&bar_q_empty, (parts & 1) ^ 1) && !s_abort;
       if (!ok) break;
@@ -269,7 +269,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       __syncwarp();
       ++parts;
     }
-    if (p.whole) write_status(p);
+    if (!p.merge) write_status(p);
     if (parts > 0) mbar_wait(&bar_q_full, (parts - 1) & 1);
   } else if (warp == 9) {
     // ------------------------------------------------------------- products
@@ -602,35 +602,80 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const int tile_tok = rb * nb + tl;
       const bool mine = tl < nb && tile_tok < w.ntok;
       const size_t oidx = (size_t)(w.s.t0 + w.first + tile_tok) * p.Hq + w.kvh * p.G + h_in;
-      const float inv = l_run > 0.0f ? 1.0f / l_run : 0.0f;
       const int crow = rb * kRB + row;
-      if (w.slot >= 0 && mine) p.part_ml[(size_t)w.slot * 256 + crow] = make_float2(m_run, l_run);
-      float4* dst = reinterpret_cast<float4*>(p.part) + (size_t)max(w.slot, 0) * (D / 4) * 256 + crow;
-      uint4* orow = reinterpret_cast<uint4*>(p.out + oidx * D);
+      const bool leaves = w.slot >= 0 && (p.merge || w.parts == 0);  // rows for another to join
+      float4* part = reinterpret_cast<float4*>(p.part) + crow;       // [slot][D / 4][256]
+      if (leaves) {
+        if (mine) p.part_ml[(size_t)w.slot * 256 + crow] = make_float2(m_run, l_run);
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tO + lane_base + 32 * c, o);
-        tmem_wait_ld();
-        if (mine && w.slot >= 0) {
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + lane_base + 32 * c, o);
+          tmem_wait_ld();
+          if (mine)
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dst[(size_t)(8 * c + q) * 256] =
-                make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
-                            __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
-        } else if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq)) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            orow[4 * c + q] = make_uint4(
-                pack2<F16>(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv),
-                pack2<F16>(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv),
-                pack2<F16>(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv),
-                pack2<F16>(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv));
+            for (int q = 0; q < 8; ++q)
+              part[((size_t)w.slot * (D / 4) + 8 * c + q) * 256] =
+                  make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                              __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+          __syncwarp();
         }
-        __syncwarp();
+        if (!p.merge) leave_rows(p, w.slot, warp);
+      } else {
+        // the rows of the shares that went on with the unit, then the output
+        const int more = w.slot >= 0 ? w.parts - 1 : 0;
+        float m_all = m_run;
+        for (int k = 1; ok && k <= more; ++k) {
+          ok = await_rows(p, w.slot + k, warp);
+          if (ok && mine) m_all = fmaxf(m_all, __ldcg(&p.part_ml[(size_t)(w.slot + k) * 256 + crow].x));
+        }
+        if (!ok) break;
+        const float f0 = m_run == -INFINITY ? 0.0f : ex2(m_run - m_all);
+        float l_all = l_run * f0;
+        for (int k = 1; k <= more; ++k)
+          if (mine) {
+            const float2 ml = __ldcg(&p.part_ml[(size_t)(w.slot + k) * 256 + crow]);
+            if (ml.x != -INFINITY) l_all = fmaf(ex2(ml.x - m_all), ml.y, l_all);
+          }
+        const float inv = l_all > 0.0f ? 1.0f / l_all : 0.0f;
+        uint4* orow = reinterpret_cast<uint4*>(p.out + oidx * D);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + lane_base + 32 * c, o);
+          tmem_wait_ld();
+          if (more) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
+            for (int k = 1; k <= more; ++k)
+              if (mine) {
+                const float m = __ldcg(&p.part_ml[(size_t)(w.slot + k) * 256 + crow].x);
+                float4 v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  v[q] = __ldcg(&part[((size_t)(w.slot + k) * (D / 4) + 8 * c + q) * 256]);
+                const float f = m == -INFINITY ? 0.0f : ex2(m - m_all);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  o[4 * q] = __float_as_uint(fmaf(f, v[q].x, __uint_as_float(o[4 * q])));
+                  o[4 * q + 1] = __float_as_uint(fmaf(f, v[q].y, __uint_as_float(o[4 * q + 1])));
+                  o[4 * q + 2] = __float_as_uint(fmaf(f, v[q].z, __uint_as_float(o[4 * q + 2])));
+                  o[4 * q + 3] = __float_as_uint(fmaf(f, v[q].w, __uint_as_float(o[4 * q + 3])));
+                }
+              }
+          }
+          if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq))
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              orow[4 * c + q] = make_uint4(
+                  pack2<F16>(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv),
+                  pack2<F16>(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv),
+                  pack2<F16>(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv),
+                  pack2<F16>(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv));
+          __syncwarp();
+        }
+        if (mine && p.lse) p.lse[oidx] = l_all > 0.0f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
       }
-      if (w.slot < 0 && mine && p.lse)
-        p.lse[oidx] = l_run > 0.0f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) s_ring.done(n);
