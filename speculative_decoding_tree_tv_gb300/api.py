@@ -490,10 +490,6 @@ def _call(fn, name: str, dev: torch.device, *args) -> None:
         raise TVError(name, code)
 
 
-def _is(t: torch.Tensor, dtype, shape, dev) -> bool:
-    return t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()
-
-
 def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> bytes:
     """tv_paged_cache of k_pages, v_pages [num_pages, Hkv, page_size, D]: any
     strides with D contiguous, the same for both (a [num_pages, page_size, Hkv, D]
@@ -560,27 +556,36 @@ def page_map(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Ten
     sequence); kv_len, n_pages int32 [B]; block_table int32 [B, P]; free_list
     int32 [num_pages]; n_free int32 [1]; tokens = length of the slot map.
     Returns (slots int64 [tokens], status int32 [B])."""
-    B, P = _table_shape(block_table)
-    dev = block_table.device
-    if slots is None:
-        slots = torch.empty(tokens, dtype=_I64, device=dev)
-    if status is None:
-        status = torch.empty(B, dtype=_I32, device=dev)
     try:
-        pool = free_list.numel()
-        good = (_is(q_start, _I32, (B + 1,), dev) and _is(kv_len, _I32, (B,), dev)
-                and _is(n_pages, _I32, (B,), dev) and _is(free_list, _I32, (pool,), dev)
-                and _is(n_free, _I32, (1,), dev) and _is(slots, _I64, (tokens,), dev)
-                and _is(status, _I32, (B,), dev))
-    except AttributeError:
+        (B, P), dev, pool = block_table.shape, block_table.device, free_list.shape[0]
+        row, one = (B,), (1,)
+        good = (block_table.dtype is _I32 and block_table.is_contiguous() and block_table.is_cuda
+                and q_start.dtype is _I32 and q_start.shape == (B + 1,) and q_start.device == dev
+                and q_start.is_contiguous()
+                and kv_len.dtype is _I32 and kv_len.shape == row and kv_len.device == dev
+                and kv_len.is_contiguous()
+                and n_pages.dtype is _I32 and n_pages.shape == row and n_pages.device == dev
+                and n_pages.is_contiguous()
+                and free_list.dtype is _I32 and free_list.dim() == 1 and free_list.device == dev
+                and free_list.is_contiguous()
+                and n_free.dtype is _I32 and n_free.shape == one and n_free.device == dev)
+    except (AttributeError, IndexError, ValueError):
         good = False
     if not good:
+        B, P = _table_shape(block_table)
+        dev = block_table.device
         _need(q_start, "q_start", _I32, (B + 1,), dev)
         _need(kv_len, "kv_len", _I32, (B,), dev)
         _need(n_pages, "n_pages", _I32, (B,), dev)
         _need(free_list, "free_list", _I32, (free_list.numel(),), dev)
         _need(n_free, "n_free", _I32, (1,), dev)
+    if slots is None:
+        slots = torch.empty(tokens, dtype=_I64, device=dev)
+    else:
         _need(slots, "slots", _I64, (tokens,), dev)
+    if status is None:
+        status = torch.empty(B, dtype=_I32, device=dev)
+    else:
         _need(status, "status", _I32, (B,), dev)
     _call(lib.tv_page_map, "tv_page_map", dev, q_start.data_ptr(), kv_len.data_ptr(), B, int(tokens),
           P, int(page_size), pool, block_table.data_ptr(), n_pages.data_ptr(),
@@ -600,7 +605,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
     try:
         T = slots.numel()
         shape, strides = (T, Hkv, D), k.stride()
-        good = (_is(slots, _I64, (T,), dev) and k.shape == shape and v.shape == shape
+        good = (slots.dtype is _I64 and slots.shape == (T,) and slots.device == dev
+                and slots.is_contiguous() and k.shape == shape and v.shape == shape
                 and k.dtype is dtype and v.dtype is dtype and k.device == dev and v.device == dev
                 and v.stride() == strides and strides[2] == 1)
     except (AttributeError, IndexError):
@@ -635,17 +641,20 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     cache = _cache(k_pages, v_pages)
     dev, dtype = k_pages.device, k_pages.dtype
     _, Hkv, _, Dc = k_pages.shape
-    B, P = _table_shape(block_table)
     max_q = int(max_q)
     try:
-        T, Hq, D = shape = q.shape
-        strides = q.stride()
+        (T, Hq, D), (B, P), strides = q.shape, block_table.shape, q.stride()
         good = (D == Dc and q.dtype is dtype and q.device == dev and strides[2] == 1
-                and block_table.device == dev and _is(q_start, _I32, (B + 1,), dev)
-                and _is(kv_len, _I32, (B,), dev))
+                and block_table.dtype is _I32 and block_table.device == dev
+                and block_table.is_contiguous()
+                and q_start.dtype is _I32 and q_start.shape == (B + 1,) and q_start.device == dev
+                and q_start.is_contiguous()
+                and kv_len.dtype is _I32 and kv_len.shape == (B,) and kv_len.device == dev
+                and kv_len.is_contiguous())
     except (AttributeError, ValueError):
         good = False
     if not good:
+        B, P = _table_shape(block_table)
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be a tensor [T, Hq, D]")
         _need_rows(q, "q", dtype, (T, Hq, Dc), dev)
@@ -660,9 +669,9 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     if slopes is not None:
         _need(slopes, "slopes", _F32, (Hq,), dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
     else:
-        _need(out, "out", dtype, shape, dev)
+        _need(out, "out", dtype, (T, Hq, D), dev)
     if lse is not None:
         _need(lse, "lse", _F32, (T, Hq), dev)
     elif want_lse:
@@ -691,26 +700,34 @@ def commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torc
     Returns (new_kv_len int32 [B], status int32 [B])."""
     cache = _cache(k_pages, v_pages)
     dev = k_pages.device
-    B, P = _table_shape(block_table)
-    if new_kv_len is None:
-        new_kv_len = torch.empty(B, dtype=_I32, device=dev)
-    if status is None:
-        status = torch.empty(B, dtype=_I32, device=dev)
     try:
-        N = path.shape[1]
-        good = (block_table.device == dev and _is(path, _I32, (B, N), dev)
-                and _is(kv_len, _I32, (B,), dev) and _is(accept_len, _I32, (B,), dev)
-                and _is(new_kv_len, _I32, (B,), dev) and _is(status, _I32, (B,), dev))
-    except (AttributeError, IndexError):
+        (B, P), N = block_table.shape, path.shape[1]
+        row = (B,)
+        good = (block_table.dtype is _I32 and block_table.device == dev
+                and block_table.is_contiguous()
+                and path.dtype is _I32 and path.shape == (B, N) and path.device == dev
+                and path.is_contiguous()
+                and kv_len.dtype is _I32 and kv_len.shape == row and kv_len.device == dev
+                and kv_len.is_contiguous()
+                and accept_len.dtype is _I32 and accept_len.shape == row
+                and accept_len.device == dev and accept_len.is_contiguous())
+    except (AttributeError, IndexError, ValueError):
         good = False
     if not good:
+        B, P = _table_shape(block_table)
         _need(block_table, "block_table", _I32, None, dev)
         _need(path, "path", _I32, None, dev)
         if path.dim() != 2 or path.shape[0] != B:
             raise ValueError(f"path must have shape [B, N] with B = {B}")
         _need(kv_len, "kv_len", _I32, (B,), dev)
         _need(accept_len, "accept_len", _I32, (B,), dev)
+    if new_kv_len is None:
+        new_kv_len = torch.empty(B, dtype=_I32, device=dev)
+    else:
         _need(new_kv_len, "new_kv_len", _I32, (B,), dev)
+    if status is None:
+        status = torch.empty(B, dtype=_I32, device=dev)
+    else:
         _need(status, "status", _I32, (B,), dev)
     _call(lib.tv_commit_paged, "tv_commit_paged", dev, cache, block_table.data_ptr(),
           kv_len.data_ptr(), path.data_ptr(), accept_len.data_ptr(), B, N, P,
