@@ -660,7 +660,8 @@ tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, in
  * Cache rows that no token sees may hold anything, NaN included; a row of V seen
  * by one token of a chunk and not by another must be finite.
  * Supported: D 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 128, B <= 4096, T * Hq and
- * B * P below 2^31; max_q <= TV_MAX_NODES with anc_mask.
+ * B * P below 2^31; max_q <= TV_MAX_NODES with anc_mask; positive strides, of the cache (in
+ * the order of their size) and of q (token by head) each a multiple of the one before.
  */
 size_t tv_attn_paged_workspace_size(int max_q, int Hq, int Hkv, int D);
 tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_stride,

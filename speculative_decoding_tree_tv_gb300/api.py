@@ -683,6 +683,8 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     if ws is None:  # from torch's allocator: ordered by stream, and a captured graph's own
         ws = torch.empty(lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D), dtype=torch.uint8,
                          device=dev)
+    else:
+        _need(ws, "ws", torch.uint8, None, dev)
     _call(lib.tv_attn_paged, "tv_attn_paged", dev, q.data_ptr(), strides[0], strides[1], cache,
           block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), _ptr(anc_mask),
           _ptr(slopes), B, T, P, Hq, max_q, scale, softcap, window, out.data_ptr(), _ptr(lse),

@@ -211,7 +211,7 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
   // joining in the CTAs took 199 instead of 187 us for a decode of 64.
   const int unit_tokens = pl.tq < max_q ? pl.tq : max_q;
   pl.merge = !pl.whole &&
-             (pl.small || 2ll * Hkv * ((T + unit_tokens - 1) / unit_tokens) < pl.ctas);
+             (pl.small || 2 * Hkv * (((long long)T + unit_tokens - 1) / unit_tokens) < pl.ctas);
   const size_t r = 2 * (size_t)pl.ctas * pl.rows;
   pl.part_bytes = align_up(r * D * 4, 256);
   pl.ml_bytes = align_up(r * 8, 256);

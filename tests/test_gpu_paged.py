@@ -359,6 +359,67 @@ def test_lengths_do_not_depend_on_the_hint(tv):
         check_attn(out, lse, want, "bf16", f"max_q {hint}")
 
 
+@pytest.mark.parametrize("new", [1, 6])
+@pytest.mark.parametrize("B", [33, 700])
+def test_many_short_sequences(tv, B, new):
+    """More sequences than a CTA has threads; some without tokens."""
+    rng = random.Random(B)
+    lens = [(rng.randint(0, 90), new if rng.random() < 0.9 else 0) for _ in range(B)]
+    c = make(B, lens, 8, 2, 64, 16, pad=2)
+    agree(tv, c, 8, 2, 64, "bf16")
+
+
+@pytest.mark.parametrize("lens", [[(70000, 1)], [(30000, 40), (5, 3)]])
+def test_long_contexts(tv, lens):
+    c = make(2, lens, 4, 1, 64, 64)
+    agree(tv, c, 4, 1, 64, "bf16")
+
+
+def test_the_widest_group(tv):
+    """128 query heads of one kv head: a token fills a row block."""
+    c = make(3, [(150, 5), (0, 2), (300, 1)], 128, 1, 64, 32)
+    agree(tv, c, 128, 1, 64, "bf16")
+
+
+def test_one_head_and_one_page(tv):
+    """Dimensions of extent one, with strides that no one reads."""
+    c = make(3, [(3, 2)], 1, 1, 64, 16, spare=0)
+    assert c["k"].shape[:2] == (1, 1)
+    c["k"], c["v"] = (x.as_strided(x.shape, (7, 3, 64, 1)) for x in (c["k"], c["v"]))
+    c["q"] = c["q"].as_strided(c["q"].shape, (c["q"].stride(0), 5, 1))
+    agree(tv, c, 1, 1, 64, "bf16")
+    slots = torch.tensor([3], device="cuda:0")
+    x = torch.randn(1, 1, 64, device="cuda:0").bfloat16().as_strided((1, 1, 64), (9, 11, 1))
+    tv.paged_append(x, x, slots, c["k"], c["v"])
+    torch.cuda.synchronize()
+    assert torch.equal(c["k"][0, 0, 3], x[0, 0]) and torch.equal(c["v"][0, 0, 3], x[0, 0])
+
+
+def test_offsets_past_32_bits(tv):
+    """Pages two billion elements apart."""
+    L, n, page, D, Hkv = 20, 6, 16, 64, 2
+    c = make(9, [(L, n)], 4, Hkv, D, page, spare=0)
+    far = 2**31 + page * D
+    flat = [torch.empty(far + page * Hkv * D, dtype=torch.bfloat16, device="cuda:0") for _ in range(2)]
+    wide = [f.as_strided((2, Hkv, page, D), (far, page * D, D, 1)) for f in flat]
+    for w, x in zip(wide, (c["k"], c["v"])):
+        w.copy_(x)
+    c["k"], c["v"] = wide
+    agree(tv, c, 4, Hkv, D, "bf16")
+    d = dict(c, q=c["q"][:1], lens=[(L, 1)], q_start=i32([0, 1]), max_q=1, T=1,
+             rows=[tuple(r[:L + 1] for r in c["rows"][0])])
+    agree(tv, d, 4, Hkv, D, "bf16")
+    x = torch.randn(1, Hkv, D, device="cuda:0").bfloat16()
+    last = int(c["table"][0, 1])
+    tv.paged_append(x, x, torch.tensor([last * page + 12], device="cuda:0"), *wide)
+    # rows 16 .. : the branch [0, 2] moves row 18 to row 17
+    before = wide[0][last, :, 2].clone()
+    new_len, status = tv.commit_paged(*wide, c["table"], i32([16]), i32([[0, 2, -1]]), i32([1]))
+    torch.cuda.synchronize()
+    assert np_(status).tolist() == [0] and np_(new_len).tolist() == [18]
+    assert torch.equal(wide[0][last, :, 12], x[0]) and torch.equal(wide[0][last, :, 1], before)
+
+
 def test_large_scores(tv):
     """Rows whose scores differ by hundreds: the running maximum moves far and often."""
     for lens in ([(1500, 1)], [(700, 100)]):
@@ -463,7 +524,9 @@ def test_no_tokens(tv):
     assert out.shape == (0, 4, 64) and np_(status).tolist() == [0, 0]
 
 
-@pytest.mark.parametrize("lens", [[(300, 1), (2000, 1)], [(300, 80), (2000, 9)]])
+# (decode tokens; few units, joined by the merge kernel; many, joined by their CTAs; short ones, whole)
+@pytest.mark.parametrize("lens", [[(300, 1), (2000, 1)], [(300, 80), (2000, 9)],
+                                  [(700 + 40 * i, 64) for i in range(45)], [(90, 1), (70, 1)]])
 def test_other_stream_and_graphs(tv, lens):
     """On a stream of its own, and two captured calls replayed at the same time on new
     inputs in the same buffers."""
@@ -520,6 +583,8 @@ def test_refusals_of_the_binding(tv):
     bad(6, 3, ValueError, slopes=torch.zeros(3, device="cuda:0"))
     bad(6, 3, tv.TVError, softcap=-1.0)
     bad(6, 3, tv.TVError, window=-1)
+    bad(6, 3, ValueError, ws=torch.zeros(10, dtype=torch.uint8))
+    bad(6, 3, tv.TVError, ws=torch.zeros(256, dtype=torch.uint8, device="cuda:0"))
     bad(6, 3, TypeError, out=torch.zeros(3, 4, 64, device="cuda:0"))
     odd = torch.zeros(c["q"].numel() + 1, dtype=torch.bfloat16, device="cuda:0")[1:].view(c["q"].shape)
     bad(0, odd, tv.TVError)
