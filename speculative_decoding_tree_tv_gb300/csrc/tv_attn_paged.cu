@@ -334,6 +334,7 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   p.tq = pl.tq;
   p.min_share = pl.min_share;
   p.whole = pl.whole;
+  p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   p.merge = pl.merge;
   p.ready = reinterpret_cast<unsigned long long*>(ws + pl.part_bytes + pl.ml_bytes + pl.desc_bytes +
                                                   pl.timeout_bytes);

@@ -61,6 +61,7 @@ struct PagedAttnParams {
   int tq;           // tokens per query tile
   int min_share;    // least cost of a share
   int whole;        // one unit a CTA, none is split
+  int out_sectors;  // out lies on a 32-byte boundary
   int merge;        // a merge kernel joins the parts of split units, else the CTA a unit begins in
   unsigned long long token;      // this call's mark in `ready`
   unsigned long long* ready;     // [CTAs][8]: a warp of a share's first part has left its rows

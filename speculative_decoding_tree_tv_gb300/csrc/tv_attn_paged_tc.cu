@@ -58,6 +58,18 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
                : "memory");
 }
 
+// 32 bytes of a row in one store where rows lie on sectors (`whole`), else in two.
+__device__ __forceinline__ void store32(uint8_t* at, const uint32_t (&x)[8], int whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(x[0]), "r"(x[1]),
+                 "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(at)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4*>(at)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
 // What one row sees.
 struct Row {
   const uint64_t* anc;  // mask row, or nullptr (causal)
@@ -372,6 +384,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const int tl = row / p.G, h_in = row % p.G;
     const bool warp_in_block = (warp & 3) * 32 < nb * p.G;
     uint32_t sc = 0, oc = 0, kt = 0;
+    // Rows left for an earlier share are announced while the next part's first tile is under way:
+    // the fence before the announcement waits for their stores, some 4,000 cycles right behind them.
+    int left = -1;
+    auto announce = [&]() {
+      if (left >= 0) leave_rows(p, left, warp);
+      left = -1;
+    };
     for (; ok; ++n) {
       ok = __all_sync(0xffffffffu, s_ring.ready(n));
       if (!ok) break;
@@ -380,6 +399,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       b = w.b;
       const int T = w.end - w.begin;
       const int L = w.s.L, hi = w.hi, j_last = (w.end - 1) * kTcKeys;
+      if (T == 0 || rb * nb >= w.ntok || rb * nb + (warp & 3) * 32 / p.G >= w.ntok) announce();  // (no tile of it here)
       if (T == 0) {  // a sequence with a status
         const int tile_tok = rb * nb + tl;
         const bool mine = tl < nb && tile_tok < w.ntok;
@@ -587,6 +607,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (lane == 0) mbar_arrive(&bar_p_full[rb][c >> 1]);
           }
         }
+        announce();
         const float2 pa = fadd2(fadd2(ps[0], ps[1]), fadd2(ps[2], ps[3]));
         l_run += pa.x + pa.y;
       }
@@ -620,58 +641,64 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                               __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
           __syncwarp();
         }
-        if (!p.merge) leave_rows(p, w.slot, warp);
+        if (!p.merge) left = w.slot;
       } else {
         // the rows of the shares that went on with the unit, then the output
         const int more = w.slot >= 0 ? w.parts - 1 : 0;
-        float m_all = m_run;
+        float m_all = m_run, l_all = l_run;
         for (int k = 1; ok && k <= more; ++k) {
           ok = await_rows(p, w.slot + k, warp);
-          if (ok && mine) m_all = fmaxf(m_all, __ldcg(&p.part_ml[(size_t)(w.slot + k) * 256 + crow].x));
+          const float2 ml = ok && mine ? __ldcg(&p.part_ml[(size_t)(w.slot + k) * 256 + crow])
+                                       : make_float2(-INFINITY, 0.0f);
+          if (ml.x != -INFINITY) {
+            const float top = fmaxf(m_all, ml.x);
+            l_all = fmaf(m_all == -INFINITY ? 0.0f : ex2(m_all - top), l_all, ex2(ml.x - top) * ml.y);
+            m_all = top;
+          }
         }
         if (!ok) break;
         const float f0 = m_run == -INFINITY ? 0.0f : ex2(m_run - m_all);
-        float l_all = l_run * f0;
-        for (int k = 1; k <= more; ++k)
-          if (mine) {
-            const float2 ml = __ldcg(&p.part_ml[(size_t)(w.slot + k) * 256 + crow]);
-            if (ml.x != -INFINITY) l_all = fmaf(ex2(ml.x - m_all), ml.y, l_all);
-          }
         const float inv = l_all > 0.0f ? 1.0f / l_all : 0.0f;
-        uint4* orow = reinterpret_cast<uint4*>(p.out + oidx * D);
+        uint8_t* orow = reinterpret_cast<uint8_t*>(p.out + oidx * D);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + lane_base + 32 * c, o);
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t o[2][32];
+          tmem_ld32(tO + lane_base + 64 * c, o[0]);
+          tmem_ld32(tO + lane_base + 64 * c + 32, o[1]);
           tmem_wait_ld();
-          if (more) {
+          if (more && mine) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f0);
-            for (int k = 1; k <= more; ++k)
-              if (mine) {
-                const float m = __ldcg(&p.part_ml[(size_t)(w.slot + k) * 256 + crow].x);
-                float4 v[8];
+            for (int e = 0; e < 64; ++e)
+              o[e >> 5][e & 31] = __float_as_uint(__uint_as_float(o[e >> 5][e & 31]) * f0);
+#pragma unroll 1
+            for (int k = 1; k <= more; ++k) {
+              const float m = __ldcg(&p.part_ml[(size_t)(w.slot + k) * 256 + crow].x);
+              float4 v[16];
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  v[q] = __ldcg(&part[((size_t)(w.slot + k) * (D / 4) + 8 * c + q) * 256]);
-                const float f = m == -INFINITY ? 0.0f : ex2(m - m_all);
+              for (int q = 0; q < 16; ++q)
+                v[q] = __ldcg(&part[((size_t)(w.slot + k) * (D / 4) + 16 * c + q) * 256]);
+              const float f = m == -INFINITY ? 0.0f : ex2(m - m_all);
+              if (f == 0.0f) continue;  // (a part whose keys are all hidden: select, do not multiply)
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                  o[4 * q] = __float_as_uint(fmaf(f, v[q].x, __uint_as_float(o[4 * q])));
-                  o[4 * q + 1] = __float_as_uint(fmaf(f, v[q].y, __uint_as_float(o[4 * q + 1])));
-                  o[4 * q + 2] = __float_as_uint(fmaf(f, v[q].z, __uint_as_float(o[4 * q + 2])));
-                  o[4 * q + 3] = __float_as_uint(fmaf(f, v[q].w, __uint_as_float(o[4 * q + 3])));
-                }
+              for (int q = 0; q < 16; ++q) {
+                uint32_t* x = &o[q >> 3][4 * (q & 7)];
+                x[0] = __float_as_uint(fmaf(f, v[q].x, __uint_as_float(x[0])));
+                x[1] = __float_as_uint(fmaf(f, v[q].y, __uint_as_float(x[1])));
+                x[2] = __float_as_uint(fmaf(f, v[q].z, __uint_as_float(x[2])));
+                x[3] = __float_as_uint(fmaf(f, v[q].w, __uint_as_float(x[3])));
               }
+            }
           }
           if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq))
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              orow[4 * c + q] = make_uint4(
-                  pack2<F16>(__uint_as_float(o[8 * q + 0]) * inv, __uint_as_float(o[8 * q + 1]) * inv),
-                  pack2<F16>(__uint_as_float(o[8 * q + 2]) * inv, __uint_as_float(o[8 * q + 3]) * inv),
-                  pack2<F16>(__uint_as_float(o[8 * q + 4]) * inv, __uint_as_float(o[8 * q + 5]) * inv),
-                  pack2<F16>(__uint_as_float(o[8 * q + 6]) * inv, __uint_as_float(o[8 * q + 7]) * inv));
+            for (int q = 0; q < 4; ++q) {  // 16 columns: 32 bytes, a whole sector at a time
+              uint32_t x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                x[e] = pack2<F16>(__uint_as_float(o[q >> 1][16 * (q & 1) + 2 * e]) * inv,
+                                  __uint_as_float(o[q >> 1][16 * (q & 1) + 2 * e + 1]) * inv);
+              store32(orow + 128 * c + 32 * q, x, p.out_sectors);
+            }
           __syncwarp();
         }
         if (mine && p.lse) p.lse[oidx] = l_all > 0.0f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
@@ -680,6 +707,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       __syncwarp();
       if (lane == 0) s_ring.done(n);
     }
+    announce();
   }
   if (!ok) {
     s_abort = 1;
