@@ -184,9 +184,9 @@ unsigned long long next_token() {
 PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long keys) {
   PagedPlan pl;
   const long long rows = (long long)max_q * G;
-  // 64 decode sequences of 512 to 8,192 keys, 8 kv heads, D 128: 4 rows a unit 188 us here and RULE4 us on the
-  // tcgen05 kernel, 16 rows RULE16A and RULE16B us; 32 rows took 430 us with two row tiles a warp here
-  // (its registers spill) and RULE32 us there.
+  // 64 decode sequences of 512 to 8,192 keys, 8 kv heads: 4 rows a unit 186 us here and 198 us on the
+  // tcgen05 kernel (D 64: 107 and 149 us), 16 rows 171 and 180 us; 32 rows took 430 us with two row
+  // tiles a warp here (its registers spill) and 185 us there.
   pl.small = rows <= 16;
   if (pl.small) {
     pl.rows = 16;

@@ -25,6 +25,10 @@ struct RowsLayout {
   static constexpr int kDyn = 2 * kStages * kSide + kScratch + 1024;
 };
 
+// Column order of a row of s_acc: neither the stores (8 rows of 8 floats) nor the loads (a row) meet
+// in a bank.
+__device__ __forceinline__ int acc_swizzle(int row) { return ((row & 3) << 3) | (row & 4); }
+
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -360,13 +364,13 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int r = 0; r < 2; ++r)
-          *reinterpret_cast<float2*>(s_acc + (warp * 16 + r * 8 + g) * 32 + 8 * n + c2) =
+          *reinterpret_cast<float2*>(s_acc + (warp * 16 + r * 8 + g) * 32 + ((8 * n + c2) ^ acc_swizzle(g))) =
               make_float2(o[4 * c + n][2 * r] * f[r], o[4 * c + n][2 * r + 1] * f[r]);
       named_sync(1, kRowsWarps * 32);
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < kRowsWarps; ++x) {
-        const float4 v = *reinterpret_cast<const float4*>(s_acc + (x * 16 + row) * 32 + od);
+        const float4 v = *reinterpret_cast<const float4*>(s_acc + (x * 16 + row) * 32 + (od ^ acc_swizzle(row)));
         a.x += v.x;
         a.y += v.y;
         a.z += v.z;
