@@ -168,7 +168,7 @@ bool map_cache(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void*
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr long long kWholeRowsKeys = 1024, kWholeTcKeys = 512;
+constexpr long long kWholeRowsKeys = 768, kWholeTcKeys = 512;
 
 // A mark of its own for every call, which nothing that a workspace held before is taken for: counted
 // on from a start that differs from process to process.
@@ -201,7 +201,9 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
     pl.min_share = 4;
   }
   // Units short enough for a CTA each (keys: the most a sequence can have) are not split, and
-  // the merge is not launched.
+  // the merge is not launched: decode of 4 sequences of 100, 500 and 1,000 keys 7.5, 11.0 and 16.4 us,
+  // split 12.4, 13.2 and 13.6 us; 2 trees of 64 behind 200, 440 and 900 keys 14.3, 14.7 and 20.3 us, split 18.1,
+  // 18.9 and 19.5 us.
   pl.whole = keys <= (pl.small ? kWholeRowsKeys : kWholeTcKeys) &&
              (long long)Hkv * (T / pl.tq + B) <= device_sm_count();
   if (pl.whole) pl.min_share = 1;
