@@ -190,7 +190,7 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
   pl.small = rows <= 16;
   if (pl.small) {
     pl.rows = 16;
-    pl.nb = pl.tq = pl.rows / G;
+    pl.nb = pl.tq = (rows <= 8 ? 8 : 16) / G;
     pl.ctas = 2 * device_sm_count();
     pl.min_share = 6;
   } else {

@@ -10,7 +10,7 @@ namespace tv {
 namespace paged {
 namespace {
 
-constexpr int kUnitRows = 16;
+constexpr int kUnitRows = 16;  // rows of a slot
 
 // NW consumer warps, 16 keys of a stage each: 4 and two CTAs an SM, which fill it when there is work
 // for all, or 8 and one CTA where every unit has an SM to itself (p.whole).
@@ -25,9 +25,18 @@ struct RowsLayout {
   static constexpr int kDyn = 2 * kStages * kSide + kScratch + 1024;
 };
 
-// Column order of a row of s_acc: neither the stores (8 rows of 8 floats) nor the loads (a row) meet
-// in a bank.
-__device__ __forceinline__ int acc_swizzle(int row) { return ((row & 3) << 3) | (row & 4); }
+// Column order of a row of s_acc: neither the stores (NR 16: 8 rows of 8 floats, NR 8: every other
+// row, 8 floats) nor the loads (a row) meet in a bank.
+template <int NR>
+__device__ __forceinline__ int acc_swizzle(int row) {
+  return NR == 16 ? ((row & 3) << 3) | (row & 4) : ((row & 6) << 2) | ((row & 1) << 2);
+}
+// An 8x8 matrix of 16-bit values held by a warp, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -53,12 +62,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, bool F16, bool MOD, int NW>
-__global__ void __launch_bounds__(32 * (NW + 1), NW == 4 ? 2 : 1)
+template <int D, bool F16, bool MOD, int NW, int NR>
+__global__ void __launch_bounds__(32 * (NW + 2), NW == 4 ? 2 : 1)
 paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const PagedAttnParams p) {
   using Lay = RowsLayout<D, NW>;
-  constexpr int kSteps = D / 16, kRowsWarps = NW, kRowsKeys = 16 * NW, kRowsThreads = 32 * (NW + 1);
+  constexpr int kSteps = D / 16, kRowsWarps = NW, kRowsKeys = 16 * NW, kRowsThreads = 32 * (NW + 2);
   constexpr int kStages = Lay::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -77,9 +86,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   pdl_trigger();
   if (tid == 0) {
     s_abort = 0;
-    s_ring.init(kRowsWarps);
+    s_ring.init(kRowsWarps + 1);  // V, consumers
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_full[s], 2);
       mbar_init(&bar_empty[s], kRowsWarps);
     }
     mbar_fence_init();
@@ -95,10 +104,14 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     st = st == kStages - 1 ? 0 : st + 1;
   };
 
-  if (warp == kRowsWarps) {
-    // ------------------------------------------------------------ producer
+  if (warp >= kRowsWarps) {
+    // ------------------------------------------------- K, V producers
+    // (K's also walks the share)
+    const bool isV = warp > kRowsWarps;
+    const CUtensorMap* map = isV ? &tmV : &tmK;
+    uint8_t* ring = isV ? sV : sK;
     Part w;
-    if (p.merge && lane == 0) {
+    if (p.merge && !isV && lane == 0) {
       p.desc[share_index()] = make_int4(0, 0, 0, 0);
       p.timeout[blockIdx.x] = 0;
     }
@@ -110,11 +123,20 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const bool issues = atom < Lay::kAtoms;
     bool ok = true;
     for (;; ++np) {
-      const bool more = cur.next(p, w);
-      ok = s_ring.publish(np, w);
-      if (!ok || !more) break;
-      if (w.parts && lane == 0)
-        p.desc[share_index()] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
+      if (isV) {
+        ok = __all_sync(0xffffffffu, s_ring.ready(np));
+        if (!ok) break;
+        w = s_ring.at(np);
+        __syncwarp();
+        if (lane == 0) s_ring.done(np);
+        if (w.b < 0) break;
+      } else {
+        const bool more = cur.next(p, w);
+        ok = s_ring.publish(np, w);
+        if (!ok || !more) break;
+        if (w.parts && lane == 0)
+          p.desc[share_index()] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
+      }
       feed.start(p, w);
       for (int t = w.end - 1; t >= w.begin; --t) {
         const int row = (t * kRowsKeys + row0) & ((1 << p.page_shift) - 1);
@@ -123,21 +145,19 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         ok = warp_wait(&bar_empty[st], phase ^ 1);
         if (!ok) break;
         if (lane == 0) {
-          s_bad_pages[st] = bad8;
-          mbar_expect_tx(&bar_full[st], 2 * Lay::kSide);
+          if (!isV) s_bad_pages[st] = bad8;
+          mbar_expect_tx(&bar_full[st], Lay::kSide);
         }
         __syncwarp();
-        if (issues) {
-          const int at = st * Lay::kSide + atom * Lay::kAtom + row0 * 128;
-          tma_load_rows(sK + at, &tmK, &bar_full[st], atom * 64, row, w.kvh, page, p.row_dim, p.head_dim);
-          tma_load_rows(sV + at, &tmV, &bar_full[st], atom * 64, row, w.kvh, page, p.row_dim, p.head_dim);
-        }
+        if (issues)
+          tma_load_rows(ring + st * Lay::kSide + atom * Lay::kAtom + row0 * 128, map, &bar_full[st],
+                        atom * 64, row, w.kvh, page, p.row_dim, p.head_dim);
         next_stage();
         ++issued;
       }
       if (!ok) break;
     }
-    if (!p.merge) write_status(p);
+    if (!p.merge && !isV) write_status(p);
     // no copy may be in flight when the CTA leaves
     for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
       mbar_wait(&bar_full[i % kStages], (i / kStages) & 1);
@@ -148,6 +168,18 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   // ---------------------------------------------------------------- consumers
   const float cap_in2 = 2.0f * kLog2e * p.cap_in;
   const int g = lane >> 2, c2 = (lane & 3) * 2;  // fragment row and first column of this lane
+  // A lane's two rows, and the kKeys keys of 16 that it holds of both
+  constexpr int kKeys = NR == 16 ? 4 : 2, kScores = 2 * kKeys;
+  constexpr int kQRegs = kSteps * (NR == 16 ? 4 : 2), kAcc = NR == 16 ? D / 8 : D / 16;
+  auto row_of = [&](int r) { return NR == 16 ? r * 8 + g : c2 + r; };
+  auto key_of = [&](int i) { return NR == 16 ? 8 * (i >> 1) + c2 + (i & 1) : 8 * i + g; };
+  auto at = [](int r, int i) { return NR == 16 ? 4 * (i >> 1) + 2 * r + (i & 1) : 2 * i + r; };
+  auto reduce = [](float x, auto op) {  // over the lanes that hold a row's keys
+#pragma unroll
+    for (int o = NR == 16 ? 1 : 4; o < (NR == 16 ? 4 : 32); o *= 2)
+      x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  };
   int b = 0;
   for (;; ++np) {
     // (a warp that gives up still joins the others at the unit's end, where all see it)
@@ -163,7 +195,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const int rows = w.ntok * p.G;
     // the unit's Q rows to shared memory (rows past the unit repeat its last one); 16-byte
     // chunk c of row r lies at c ^ (r & 7)
-    for (int x = tid; x < kUnitRows * (D / 8); x += kRowsWarps * 32) {
+    for (int x = tid; x < NR * (D / 8); x += kRowsWarps * 32) {
       const int r = x / (D / 8), c = x % (D / 8), row = min(r, rows - 1);
       const uint4* src = reinterpret_cast<const uint4*>(
           p.q + (w.s.t0 + w.first + row / p.G) * p.q_token_stride +
@@ -171,18 +203,20 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       s_q[r * (D / 8) + (c ^ (r & 7))] = __ldg(src + c);
     }
     named_sync(1, kRowsWarps * 32);
-    uint32_t qf[kSteps][4];
+    uint32_t qf[kQRegs / 4][4];  // (NR 8: two steps' fragments together)
     {
-      const uint32_t base = smem_u32(s_q) + ((lane & 7) + ((lane >> 3) & 1) * 8) * (D * 2);
+      const int row8 = NR == 16 ? ((lane >> 3) & 1) * 8 : 0, chunk = NR == 16 ? lane >> 4 : lane >> 3;
+      const uint32_t base = smem_u32(s_q) + ((lane & 7) + row8) * (D * 2);
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) ldsm4(base + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4), qf[k]);
+      for (int k = 0; k < kQRegs / 4; ++k)
+        ldsm4(base + (((NR / 8 == 2 ? 2 * k : 4 * k) + chunk) ^ (lane & 7)) * 16, qf[k]);
     }
     int pos[2], tok[2];
     float slope[2];
-    float m[2], l[2], o[D / 8][4];
+    float m[2], l[2], o[kAcc][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int row = min(r * 8 + g, rows - 1);  // rows past the unit repeat its last
+      const int row = min(row_of(r), rows - 1);  // rows past the unit repeat its last
       const int i = w.first + row / p.G, t = w.s.t0 + i, h = w.kvh * p.G + row % p.G;
       tok[r] = t;
       pos[r] = w.s.L + (p.anc ? anc_count(p.anc + (size_t)t * p.W, p.W, 64 * p.W) - 1 : i);
@@ -191,7 +225,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       l[r] = 0.0f;
     }
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int n = 0; n < kAcc; ++n)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
     const int all_below = p.anc ? w.s.L : w.s.L + w.first + 1;  // keys below it are visible to every row
@@ -205,18 +239,32 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         break;
       }
       if (j0 < w.hi && j0 + 16 > w.lo) {
-        float s[2][4] = {};  // [8 keys][row g: two keys, row g + 8: two keys]
-        {
+        float s[8] = {};
+        if (NR == 16) {  // S: [8 keys][row g: two keys, row g + 8: two keys]
           const int key = 16 * warp + (lane >> 4) * 8 + (lane & 7);
           const uint32_t base = smem_u32(sK) + st * Lay::kSide + key * 128;
           const int kc = (lane >> 3) & 1, sw = key & 7;
+          float (&s0)[4] = reinterpret_cast<float (&)[4]>(s[0]), (&s1)[4] = reinterpret_cast<float (&)[4]>(s[4]);
 #pragma unroll
           for (int k = 0; k < kSteps; ++k) {
             uint32_t b[4];
             ldsm4(base + (k >> 2) * Lay::kAtom + ((((k & 3) * 2 + kc) ^ sw) << 4), b);
-            mma16816<F16>(s[0], qf[k], b[0], b[1]);
-            mma16816<F16>(s[1], qf[k], b[2], b[3]);
+            mma16816<F16>(s0, qf[NR == 16 ? k : 0], b[0], b[1]);
+            mma16816<F16>(s1, qf[NR == 16 ? k : 0], b[2], b[3]);
           }
+        } else {  // S^T: [key g: two rows, key g + 8: two rows], even and odd steps apart
+          const int key = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7);
+          const uint32_t base = smem_u32(sK) + st * Lay::kSide + key * 128;
+          const int kc = lane >> 4, sw = key & 7;
+          float (&s0)[4] = reinterpret_cast<float (&)[4]>(s[0]), (&s1)[4] = reinterpret_cast<float (&)[4]>(s[4]);
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t a[4];
+            ldsm4(base + (k >> 2) * Lay::kAtom + ((((k & 3) * 2 + kc) ^ sw) << 4), a);
+            mma16816<F16>(k & 1 ? s1 : s0, a, qf[k / 2][2 * (k & 1)], qf[k / 2][2 * (k & 1) + 1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] += s[4 + e];
         }
         const uint32_t bad8 = (s_bad_pages[st] >> (2 * warp)) & 3u;
         const bool plain = j0 + 16 <= all_below && j0 > all_from && j0 >= w.lo && bad8 == 0;
@@ -232,59 +280,53 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         }
         // scores in the log2 domain, hidden keys at -inf
         if (MOD && p.softcap_log2 > 0.0f) {
-          float f[8], top = 0.0f;
+          float f[kScores], top = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = s[e >> 2][e & 3], w2 = x * x;
+          for (int e = 0; e < kScores; ++e) {
+            const float x = s[e], w2 = x * x;
             top = fmaxf(top, w2);
             f[e] = x * fmaf(fmaf(fmaf(p.cap_q[3], w2, p.cap_q[2]), w2, p.cap_q[1]), w2, p.cap_q[0]);
           }
           const bool far = __any_sync(0xffffffffu, top > p.cap_top);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            s[e >> 2][e & 3] = far ? p.softcap_log2 * tanh_any(s[e >> 2][e & 3] * cap_in2) : f[e];
+          for (int e = 0; e < kScores; ++e) s[e] = far ? p.softcap_log2 * tanh_any(s[e] * cap_in2) : f[e];
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] *= p.scale_log2;
+          for (int e = 0; e < kScores; ++e) s[e] *= p.scale_log2;
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& x = s[nt][r * 2 + e];
-              const int j = j0 + 8 * nt + c2 + e;
-              int kpos = j;
-              if (!plain) {
-                // (causal: up to its own position; a tree's: the prefix and its mask)
-                bool see = j < (p.anc ? w.s.L : pos[r] + 1);
-                if (p.anc && j >= w.s.L && j < w.hi) {
-                  const int a = j - w.s.L;
-                  const uint64_t* anc = p.anc + (size_t)tok[r] * p.W;
-                  see = (__ldg(reinterpret_cast<const unsigned long long*>(anc) + (a >> 6)) >> (a & 63)) & 1;
-                  if (MOD) kpos = w.s.L + anc_count(anc, p.W, a + 1) - 1;
-                }
-                if (p.window > 0) see = see && pos[r] - kpos < p.window;
-                if ((bad8 >> nt) & 1) see = false;
-                if (MOD) x = fmaf(slope[r], (float)(kpos - pos[r]), x);
-                if (!see) x = -INFINITY;
-              } else if (MOD) {
-                x = fmaf(slope[r], (float)(kpos - pos[r]), x);
+          for (int i = 0; i < kKeys; ++i) {
+            float& x = s[at(r, i)];
+            const int j = j0 + key_of(i);
+            int kpos = j;
+            if (!plain) {
+              // (causal: up to its own position; a tree's: the prefix and its mask)
+              bool see = j < (p.anc ? w.s.L : pos[r] + 1);
+              if (p.anc && j >= w.s.L && j < w.hi) {
+                const int a = j - w.s.L;
+                const uint64_t* anc = p.anc + (size_t)tok[r] * p.W;
+                see = (__ldg(reinterpret_cast<const unsigned long long*>(anc) + (a >> 6)) >> (a & 63)) & 1;
+                if (MOD) kpos = w.s.L + anc_count(anc, p.W, a + 1) - 1;
               }
+              if (p.window > 0) see = see && pos[r] - kpos < p.window;
+              if ((bad8 >> (NR == 16 ? i >> 1 : i)) & 1) see = false;
+              if (MOD) x = fmaf(slope[r], (float)(kpos - pos[r]), x);
+              if (!see) x = -INFINITY;
+            } else if (MOD) {
+              x = fmaf(slope[r], (float)(kpos - pos[r]), x);
             }
+          }
         // running maximum (lazily moved), probabilities, sums
-        uint32_t pf[4];
         float corr[2];
         bool move = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float (&a)[4] = s[0];
-          float (&b)[4] = s[1];
-          const int e = r * 2;
-          float mx = fmaxf(fmaxf(a[e], a[e + 1]), fmaxf(b[e], b[e + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          float mx = s[at(r, 0)];
+#pragma unroll
+          for (int i = 1; i < kKeys; ++i) mx = fmaxf(mx, s[at(r, i)]);
+          mx = reduce(mx, [](float a, float b) { return fmaxf(a, b); });
           corr[r] = 1.0f;
           if (m[r] == -INFINITY) {
             m[r] = mx;
@@ -294,19 +336,20 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             move = true;
           }
           const float mm = m[r] == -INFINITY ? 0.0f : m[r];  // 2^(-inf - 0) = 0
-          const float p0 = ex2(a[e] - mm), p1 = ex2(a[e + 1] - mm);
-          const float p2 = ex2(b[e] - mm), p3 = ex2(b[e + 1] - mm);
-          l[r] = fmaf(l[r], corr[r], (p0 + p1) + (p2 + p3));
-          pf[r] = pack2<F16>(p0, p1);
-          pf[r + 2] = pack2<F16>(p2, p3);
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i) sum += s[at(r, i)] = ex2(s[at(r, i)] - mm);
+          l[r] = fmaf(l[r], corr[r], sum);
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-          for (int n = 0; n < D / 8; ++n)
+          for (int n = 0; n < kAcc; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] *= corr[e >> 1];
+            for (int e = 0; e < 4; ++e) o[n][e] *= corr[NR == 16 ? e >> 1 : e & 1];
         }
-        {
+        if (NR == 16) {  // O += P V
+          const uint32_t pf[4] = {pack2<F16>(s[0], s[1]), pack2<F16>(s[2], s[3]), pack2<F16>(s[4], s[5]),
+                                  pack2<F16>(s[6], s[7])};
           const int key = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7);
           const uint32_t base = smem_u32(sV) + st * Lay::kSide + key * 128;
           const int dc = lane >> 4, sw = key & 7;
@@ -318,8 +361,23 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
               for (int q = 0; q < 4; ++q) b[q] &= vkeep[q & 1];
             }
-            mma16816<F16>(o[2 * n], pf, b[0], b[1]);
-            mma16816<F16>(o[2 * n + 1], pf, b[2], b[3]);
+            mma16816<F16>(o[(2 * n) % kAcc], pf, b[0], b[1]);
+            mma16816<F16>(o[(2 * n + 1) % kAcc], pf, b[2], b[3]);
+          }
+        } else {  // O^T += V^T P^T
+          const uint32_t p0 = transpose8(pack2<F16>(s[0], s[1])), p1 = transpose8(pack2<F16>(s[2], s[3]));
+          const int key = 16 * warp + (lane >> 4) * 8 + (lane & 7);
+          const uint32_t base = smem_u32(sV) + st * Lay::kSide + key * 128;
+          const int dc = (lane >> 3) & 1, sw = key & 7;
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            uint32_t a[4];
+            ldsm4_t(base + (n >> 2) * Lay::kAtom + ((((n & 3) * 2 + dc) ^ sw) << 4), a);
+            if (!plain) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) a[q] &= vkeep[q >> 1];
+            }
+            mma16816<F16>(o[n], a, p0, p1);
           }
         }
       }
@@ -331,9 +389,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     // the four warps' rows joined in shared memory, 32 dims at a time
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if ((lane & 3) == 0) s_ml[warp][r * 8 + g] = make_float2(m[r], l[r]);
+      l[r] = reduce(l[r], [](float a, float b) { return a + b; });
+      if (NR == 16 ? (lane & 3) == 0 : lane < 4) s_ml[warp][row_of(r)] = make_float2(m[r], l[r]);
     }
     named_sync(1, kRowsWarps * 32);
     const bool abort = s_abort;
@@ -342,10 +399,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     for (int r = 0; r < 2; ++r) {
       float mm = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][r * 8 + g].x);
+      for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][row_of(r)].x);
       f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mm);  // (0: nothing seen by this warp, its sums are 0)
     }
-    const int row = (tid >> 3) & 15, od = (tid & 7) * 4;  // this thread's row and dims of a joined piece
+    const int row = (tid >> 3) & (NR - 1), od = (tid & 7) * 4;  // this thread's row and dims of a joined piece
     float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
     for (int x = 0; x < kRowsWarps; ++x) mm = fmaxf(mm, s_ml[x][row].x);
@@ -354,23 +411,32 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       const float2 v = s_ml[x][row];
       if (v.x != -INFINITY) ll = fmaf(ex2(v.x - mm), v.y, ll);
     }
-    const bool mine = tid < 128 && row < rows;
+    const bool mine = tid < 8 * NR && row < rows;
     const int out_tok = w.s.t0 + w.first + row / p.G, h = w.kvh * p.G + row % p.G;
     const size_t oidx = (size_t)out_tok * p.Hq + h;
     const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int x = 0; x < kAcc * 32 / D; ++x) {
+        const float(&v)[4] = o[c * (kAcc * 32 / D) + x];
+        if (NR == 16) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          *reinterpret_cast<float2*>(s_acc + (warp * 16 + r * 8 + g) * 32 + ((8 * n + c2) ^ acc_swizzle(g))) =
-              make_float2(o[4 * c + n][2 * r] * f[r], o[4 * c + n][2 * r + 1] * f[r]);
+          for (int r = 0; r < 2; ++r)
+            *reinterpret_cast<float2*>(s_acc + (warp * 16 + r * 8 + g) * 32 + ((8 * x + c2) ^ acc_swizzle<NR>(g))) =
+                make_float2(v[2 * r] * f[r], v[2 * r + 1] * f[r]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            s_acc[(warp * 16 + c2 + (e & 1)) * 32 + ((16 * x + 8 * (e >> 1) + g) ^ acc_swizzle<NR>(c2 + (e & 1)))] =
+                v[e] * f[e & 1];
+        }
+      }
       named_sync(1, kRowsWarps * 32);
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int x = 0; x < kRowsWarps; ++x) {
-        const float4 v = *reinterpret_cast<const float4*>(s_acc + (x * 16 + row) * 32 + (od ^ acc_swizzle(row)));
+        const float4 v = *reinterpret_cast<const float4*>(s_acc + (x * 16 + row) * 32 + (od ^ acc_swizzle<NR>(row)));
         a.x += v.x;
         a.y += v.y;
         a.z += v.z;
@@ -397,14 +463,22 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   }
 }
 
+template <int D, bool F16, bool MOD, int NW, int NR>
+cudaError_t launch(int ctas, const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
+                   cudaStream_t stream) {
+  auto kernel = paged_rows_kernel<D, F16, MOD, NW, NR>;
+  if (!set_dyn_smem(kernel, RowsLayout<D, NW>::kDyn)) return cudaErrorUnknown;
+  return launch_pdl(kernel, dim3(ctas), dim3(32 * (NW + 2)), (size_t)RowsLayout<D, NW>::kDyn, stream, tmK, tmV, p);
+}
 template <int D, bool F16, bool MOD>
-cudaError_t launch(const PagedPlan& pl, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                   const PagedAttnParams& p, cudaStream_t stream) {
-  auto kernel = pl.whole ? paged_rows_kernel<D, F16, MOD, 8> : paged_rows_kernel<D, F16, MOD, 4>;
-  const int smem = pl.whole ? RowsLayout<D, 8>::kDyn : RowsLayout<D, 4>::kDyn;
-  if (!set_dyn_smem(kernel, smem)) return cudaErrorUnknown;
-  return launch_pdl(kernel, dim3(pl.whole ? device_sm_count() : pl.ctas), dim3(pl.whole ? 288 : 160),
-                    (size_t)smem, stream, tmK, tmV, p);
+cudaError_t launch_kind(const PagedPlan& pl, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                        const PagedAttnParams& p, cudaStream_t stream) {
+  const bool few = p.tq * p.G <= 8;
+  if (pl.whole)
+    return few ? launch<D, F16, MOD, 8, 8>(device_sm_count(), tmK, tmV, p, stream)
+               : launch<D, F16, MOD, 8, 16>(device_sm_count(), tmK, tmV, p, stream);
+  return few ? launch<D, F16, MOD, 4, 8>(pl.ctas, tmK, tmV, p, stream)
+             : launch<D, F16, MOD, 4, 16>(pl.ctas, tmK, tmV, p, stream);
 }
 
 }  // namespace
@@ -412,15 +486,15 @@ cudaError_t launch(const PagedPlan& pl, const CUtensorMap& tmK, const CUtensorMa
 cudaError_t launch_rows(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmK,
                         const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream) {
   if (D == 128) {
-    if (f16) return mod ? launch<128, true, true>(pl, tmK, tmV, p, stream)
-                        : launch<128, true, false>(pl, tmK, tmV, p, stream);
-    return mod ? launch<128, false, true>(pl, tmK, tmV, p, stream)
-               : launch<128, false, false>(pl, tmK, tmV, p, stream);
+    if (f16) return mod ? launch_kind<128, true, true>(pl, tmK, tmV, p, stream)
+                        : launch_kind<128, true, false>(pl, tmK, tmV, p, stream);
+    return mod ? launch_kind<128, false, true>(pl, tmK, tmV, p, stream)
+               : launch_kind<128, false, false>(pl, tmK, tmV, p, stream);
   }
-  if (f16) return mod ? launch<64, true, true>(pl, tmK, tmV, p, stream)
-                      : launch<64, true, false>(pl, tmK, tmV, p, stream);
-  return mod ? launch<64, false, true>(pl, tmK, tmV, p, stream)
-             : launch<64, false, false>(pl, tmK, tmV, p, stream);
+  if (f16) return mod ? launch_kind<64, true, true>(pl, tmK, tmV, p, stream)
+                      : launch_kind<64, true, false>(pl, tmK, tmV, p, stream);
+  return mod ? launch_kind<64, false, true>(pl, tmK, tmV, p, stream)
+             : launch_kind<64, false, false>(pl, tmK, tmV, p, stream);
 }
 
 }  // namespace paged
