@@ -168,7 +168,7 @@ bool map_cache(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void*
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr long long kWholeRowsKeys = 768, kWholeTcKeys = 512;
+constexpr long long kWholeRowsKeys = 960, kWholeTcKeys = 512;
 
 // A mark of its own for every call, which nothing that a workspace held before is taken for: counted
 // on from a start that differs from process to process.
@@ -185,7 +185,7 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
   PagedPlan pl;
   const long long rows = (long long)max_q * G;
   // 64 decode sequences of 512 to 8,192 keys, 8 kv heads: 4 rows a unit 186 us here and 198 us on the
-  // tcgen05 kernel (D 64: 107 and 149 us), 16 rows 171 and 180 us; 32 rows took 430 us with two row
+  // tcgen05 kernel (D 64: 102 and 149 us), 16 rows 171 and 180 us; 32 rows took 430 us with two row
   // tiles a warp here (its registers spill) and 185 us there.
   pl.small = rows <= 16;
   if (pl.small) {
@@ -201,9 +201,9 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
     pl.min_share = 4;
   }
   // Units short enough for a CTA each (keys: the most a sequence can have) are not split, and
-  // the merge is not launched: decode of 4 sequences of 100, 500 and 1,000 keys 7.5, 11.0 and 16.4 us,
-  // split 12.4, 13.2 and 13.6 us; 2 trees of 64 behind 200, 440 and 900 keys 14.3, 14.7 and 20.3 us, split 18.1,
-  // 18.9 and 19.5 us.
+  // the merge is not launched: decode of 4 sequences of 500, 1,000 and 1,500 keys 8.9, 12.6 and 16.2 us,
+  // split 11.2, 11.8 and 12.2 us (D 64: 1,000 keys 9.9 and 10.5 us; 16 rows: 13.5 and 14.1 us); 2 trees of 64
+  // behind 200, 440 and 900 keys 14.3, 14.7 and 20.3 us, split 18.1, 18.9 and 19.5 us.
   pl.whole = keys <= (pl.small ? kWholeRowsKeys : kWholeTcKeys) &&
              (long long)Hkv * (T / pl.tq + B) <= device_sm_count();
   if (pl.whole) pl.min_share = 1;

@@ -1,8 +1,10 @@
 // paged_rows_kernel: units of at most 16 rows.  HBM-bound: per 64-key stage a CTA reads 64 D * 4
-// bytes and issues 4 D warp mma.  Four consumer warps take 16 keys of a stage each
-// and keep a running maximum, sum and output of their own (no barrier
-// between them until the unit's end); a fifth warp issues the TMA loads, one box
-// per lane (64 dims x the rows of a page).
+// bytes and issues D warp mma (D / 2 with at most 8 rows).  Four consumer warps take 16 keys of
+// a stage each and keep a running maximum, sum and output of their own (no barrier
+// between them until the unit's end); two more warps issue the TMA loads of K and V, one box
+// per lane (64 dims x the rows of a page): a warp issues a box in some 57 cycles, which with pages of 16
+// rows and one warp for both held 4 short sequences at 13.5 us, now 11.8.
+// A decode of 64 sequences (1.23 GB of cache) takes 186 us, 97 % of what a copy reaches.
 #define TV_UNIT 12
 #include "tv_attn_paged.cuh"
 
@@ -12,6 +14,10 @@ namespace {
 
 constexpr int kUnitRows = 16;  // rows of a slot
 
+// NR: the most rows of a unit.  16: S = Q K^T and O = P V, rows in the mma's 16.  8: S^T = K Q^T and
+// O^T = V^T P^T, keys and dims in its 16 and rows in its 8, so half the products and half the
+// exponentials (4 short sequences 11.8 -> 10.6 us, a decode of 64 at D 64 107 -> 102 us, capped in
+// a window 64 -> 53 us).
 // NW consumer warps, 16 keys of a stage each: 4 and two CTAs an SM, which fill it when there is work
 // for all, or 8 and one CTA where every unit has an SM to itself (p.whole).
 template <int D, int NW>

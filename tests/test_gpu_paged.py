@@ -674,3 +674,17 @@ def test_verify_steps_of_a_paged_batch_equal_the_dense_ones(tv):
     tv.page_map(i32([0] * (B + 1)), i32([0] * B), t["table"], t["held"], t["free"], t["n_free"], page, 0)
     assert int(t["n_free"]) == len(pool.free)
     assert sorted(np_(t["free"]).tolist()) == list(range(len(pool.free)))
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 5, 8])
+@pytest.mark.parametrize("tree,kw", [(False, {}), (True, {}), (True, dict(window=4, slopes=True)),
+                                     (False, dict(window=200, softcap=9.0))])
+@pytest.mark.parametrize("ctx,page", [(150, 16), (1500, 64)])
+def test_small_units_of_either_height(tv, G, tree, kw, ctx, page):
+    """1 to 16 rows a unit: both heights of the small units, whole and split."""
+    kw = dict(kw)
+    if kw.get("slopes"):
+        kw["slopes"] = slopes_of(2 * G)
+    for n in sorted({1, 8 // G, 8 // G + 1, 16 // G}):
+        c = make(G + n, [(ctx, n), (0, max(1, n - 1)), (ctx // 3, n)], 2 * G, 2, 128 if G % 2 else 64, page, tree=tree)
+        agree(tv, c, 2 * G, 2, 128 if G % 2 else 64, "bf16", **kw)
