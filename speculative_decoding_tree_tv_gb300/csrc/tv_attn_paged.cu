@@ -335,6 +335,9 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   }
   p.tq = pl.tq;
   p.min_share = pl.min_share;
+  p.share_lanes = 0;  // (a lane per query tile of the largest chunk, where the kernels' threads suffice)
+  while (p.share_lanes < 5 && (pl.tq << p.share_lanes) < max_q && (B << (p.share_lanes + 1)) <= 192)
+    ++p.share_lanes;
   p.whole = pl.whole;
   p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   p.merge = pl.merge;

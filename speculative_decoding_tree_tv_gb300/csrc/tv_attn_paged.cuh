@@ -60,6 +60,7 @@ struct PagedAttnParams {
   int row_dim, head_dim;  // which of a cache map's dimensions 1, 2, 3 they are (the pages: the third)
   int tq;           // tokens per query tile
   int min_share;    // least cost of a share
+  int share_lanes;  // log2 of the lanes that look at one sequence (1 << share_lanes) * B threads at most
   int whole;        // one unit a CTA, none is split
   int out_sectors;  // out lies on a 32-byte boundary
   int merge;        // a merge kernel joins the parts of split units, else the CTA a unit begins in
@@ -228,6 +229,12 @@ struct Part {
   int parts;         // a unit that this part begins: how many parts it has
 };
 
+// (64-bit division costs some hundred cycles; the quotients here are small)
+__device__ __forceinline__ long long div_fast(long long a, long long b) {
+  if (((a | b) >> 31) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+
 // A CTA's walk over its share of the line.
 template <int KT>
 struct Cursor {
@@ -257,7 +264,7 @@ struct Cursor {
         o.begin = o.lo / KT + a;
         o.end = o.lo / KT + e;
         o.slot = (a == 0 && e == tiles) ? -1 : p.merge ? 2 * share_index() + (a == 0) : share_index();
-        o.parts = (o.slot >= 0 && a == 0) ? (int)((at - pos + cost - 1) / share) + 1 : 0;
+        o.parts = (o.slot >= 0 && a == 0) ? (int)div_fast(at - pos + cost - 1, share) + 1 : 0;
       }
       rest -= take;
       at += take;
@@ -283,12 +290,6 @@ struct Cursor {
   }
 };
 
-// (64-bit division costs some hundred cycles; the quotients here are small)
-__device__ __forceinline__ long long div_fast(long long a, long long b) {
-  if (((a | b) >> 31) == 0) return (unsigned)a / (unsigned)b;
-  return a / b;
-}
-
 // Lines of the lengths and of the block table into the L2, shared out over the CTAs, while
 // the previous kernel finishes: a hint, which changes no result if that kernel writes them.
 template <int THREADS>
@@ -302,23 +303,31 @@ __device__ __forceinline__ void prefetch_lengths(const PagedAttnParams& p) {
   if (first < words) line_prefetch_l2(p.table + first);
 }
 
-// Finds this CTA's share.  All THREADS threads call it; ends with a barrier.
+// Finds this CTA's share.  All THREADS threads call it; ends with a barrier.  Where sequences are few and
+// chunks long, 2^share_lanes lanes share one's query tiles (a lane that walked the 32 of a chunk of 2048
+// alone held up the first tile by some 3,000 cycles).
 template <int KT, int THREADS>
 __device__ __forceinline__ Cursor<KT> find_share(const PagedAttnParams& p) {
   __shared__ long long s_warp[THREADS / 32];
   __shared__ Cursor<KT> s_cur;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = ceil_div(p.B, THREADS), b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  const int lanes = 1 << p.share_lanes;
+  const int per = ceil_div(p.B, THREADS);  // (1 where lanes > 1)
+  const int own = tid >> p.share_lanes, b0 = min(p.B, own * per), b1 = min(p.B, b0 + per);
   Cursor<KT> c;
-  auto head_cost = [&](const Seq& s) {  // of one kv head's units
+  int qt0 = 0, qt1 = 0;  // this lane's query tiles
+  auto tiles_cost = [&](const Seq& s) {  // of one kv head's units among them
+    const int nq = s.n > 0 ? (s.n - 1) / p.tq + 1 : 0, each = (nq + lanes - 1) >> p.share_lanes;
+    qt0 = min(nq, (tid & (lanes - 1)) * each);
+    qt1 = min(nq, qt0 + each);
     long long v = 0;
-    for (int qt = 0; qt * (long long)p.tq < s.n; ++qt) v += c.cost_of(p, key_tiles<KT>(p, s, qt));
+    for (int qt = qt0; qt < qt1; ++qt) v += c.cost_of(p, key_tiles<KT>(p, s, qt));
     return v;
   };
-  long long sum = 0, one = 0;
+  long long sum = 0, one = 0, before = 0;  // (before: of the head's units ahead of this lane's)
   for (int b = b0; b < b1; ++b) {
     c.s = load_seq(p, b);
-    one = head_cost(c.s);
+    one = tiles_cost(c.s);
     sum += one * p.Hkv;
   }
   long long inc = sum;
@@ -336,29 +345,40 @@ __device__ __forceinline__ Cursor<KT> find_share(const PagedAttnParams& p) {
     if (w < warp) base += s_warp[w];
     total += s_warp[w];
   }
+  if (lanes > 1) {  // the sequence's start and cost, from its lanes
+    const int first = lane & ~(lanes - 1), last = first + lanes - 1;
+    const long long end = __shfl_sync(0xffffffffu, base + sum, last);
+    const long long mine = base;
+    base = __shfl_sync(0xffffffffu, base, first);
+    sum = end - base;
+    before = div_fast(mine - base, p.Hkv);
+    one = div_fast(sum, p.Hkv);
+  }
   c.share = max(div_fast(total + gridDim.x - 1, gridDim.x), (long long)p.min_share);
   const long long x0 = share_index() * c.share;
   c.rest = min(total - x0, c.share);
-  if (c.rest > 0 && x0 >= base && x0 < base + sum) {  // this thread's sequences hold the share's start
+  if (c.rest > 0 && x0 >= base && x0 < base + sum) {  // this lane's sequences hold the share's start
     c.b = b0;
     if (per > 1) {
       for (;; ++c.b) {
         c.s = load_seq(p, c.b);
-        one = head_cost(c.s);
+        one = tiles_cost(c.s);
         if (x0 < base + one * p.Hkv) break;
         base += one * p.Hkv;
       }
     }
     c.at = 0;
     c.kvh = (int)div_fast(x0 - base, one);
-    long long left = x0 - base - c.kvh * one;
-    for (c.qt = 0;; ++c.qt) {
+    long long left = x0 - base - c.kvh * one - before;
+    for (c.qt = qt0; left >= 0 && c.qt < qt1; ++c.qt) {
       const int cost = c.cost_of(p, key_tiles<KT>(p, c.s, c.qt));
-      if (left < cost) break;
+      if (left < cost) {
+        c.pos = (int)left;
+        s_cur = c;
+        break;
+      }
       left -= cost;
     }
-    c.pos = (int)left;
-    s_cur = c;
   }
   __syncthreads();
   return s_cur;
