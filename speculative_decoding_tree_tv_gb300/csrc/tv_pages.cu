@@ -319,7 +319,8 @@ commit_paged_kernel(uint16_t* __restrict__ k, uint16_t* __restrict__ v, const Pa
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int pos = L + (e ? d : s_path[d]), j = pos >> c.page_shift;
-          const int page = TV_IN(j, P) ? __ldg(table + (size_t)b * P + j) : -1;
+          // (a path that does not rise may lead past the table before its end is seen)
+          const int page = j < P ? __ldg(table + (size_t)b * P + j) : -1;
           bad |= page < 0 || page >= c.num_pages;
           off[e] = page * c.page_stride + h * c.head_stride +
                    (pos & ((1 << c.page_shift) - 1)) * c.row_stride;

@@ -243,6 +243,20 @@ def test_commit_bad_sequences_move_nothing(tv):
     assert not torch.equal(c["k"].view(torch.int16), before[0])
 
 
+def test_commit_path_that_leaves_the_table_before_it_falls(tv):
+    """A node past the table's end in the middle of a path that then falls: a status, and no entry
+    behind the table is looked at (the checked build records one that is)."""
+    N, page, L = 8, 8, 9
+    c = make(5, [(L, 7)], 2, 2, 64, page)
+    table = c["table"][:, :2].contiguous()
+    before = [c[x].clone().view(torch.int16) for x in "kv"]
+    path = [0, 7, 2] + [-1] * 5
+    new_len, status = tv.commit_paged(c["k"], c["v"], table, i32([L]), i32([path]), i32([2]))
+    torch.cuda.synchronize()
+    assert np_(status).tolist() == [1] and np_(new_len).tolist() == [L]
+    assert all(torch.equal(c[x].view(torch.int16), was) for x, was in zip("kv", before))
+
+
 # ----------------------------------------------------------------- attention
 def run(tv, c, pad=0, **kw):
     T, Hq, D = c["q"].shape
