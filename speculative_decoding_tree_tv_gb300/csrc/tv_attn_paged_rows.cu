@@ -117,6 +117,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const CUtensorMap* map = isV ? &tmV : &tmK;
     uint8_t* ring = isV ? sV : sK;
     Part w;
+    w.b = -1;
     if (p.merge && !isV && lane == 0) {
       p.desc[share_index()] = make_int4(0, 0, 0, 0);
       p.timeout[blockIdx.x] = 0;
