@@ -702,3 +702,41 @@ def test_small_units_of_either_height(tv, G, tree, kw, ctx, page):
     for n in sorted({1, 8 // G, 8 // G + 1, 16 // G}):
         c = make(G + n, [(ctx, n), (0, max(1, n - 1)), (ctx // 3, n)], 2 * G, 2, 128 if G % 2 else 64, page, tree=tree)
         agree(tv, c, 2 * G, 2, 128 if G % 2 else 64, "bf16", **kw)
+
+
+def test_two_calls_at_once(tv):
+    """Calls that overlap on two streams, each with its own workspace, eager and as two replayed graphs:
+    whole, split and joined in the launch, split and merged."""
+    cases = [make(i, lens, 8, 2, 128, 16) for i, lens in enumerate(
+        [[(700, 64)] * 40, [(3000, 64)], [(900, 1)] * 30, [(100, 1)] * 3, [(50, 300), (2000, 90)] * 8, [(2500, 2)] * 2])]
+    call = lambda c: tv.attn_paged(c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_len"],  # noqa: E731
+                                   c["max_q"])
+    bits = lambda r: (r[0].view(torch.int16), r[1])  # noqa: E731
+    want = [bits(call(c)) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def same(i, r):
+        return all(torch.equal(a, b) for a, b in zip(bits(r), want[i])) and not bool(r[2].any())
+
+    for i in range(0, len(cases), 2):
+        got = ([], [])
+        for _ in range(8):
+            for j, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    got[j].append(call(cases[i + j]))
+        torch.cuda.synchronize()
+        for j in range(2):
+            assert all(same(i + j, r) for r in got[j])
+        graphs, outs = [], []
+        for j, s in enumerate(streams):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[j], stream=s):
+                outs.append([call(cases[i + j]) for _ in range(3)])
+        for _ in range(5):
+            for j, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    graphs[j].replay()
+        torch.cuda.synchronize()
+        for j in range(2):
+            assert all(same(i + j, r) for r in outs[j])
