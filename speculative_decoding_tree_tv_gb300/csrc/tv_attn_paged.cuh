@@ -180,8 +180,8 @@ __device__ __forceinline__ int anc_count(const uint64_t* anc, int W, int pos) {
 }
 
 // ------------------------------------------------------- shares of the work
-// (16 trees of 64 nodes, a capped ragged batch and biased prompts of 200 to 1,500: 80.1, 65.2 and 31.4 us at 1;
-// 76.0, 63.2 and 30.3 us at 3; 80.3, 61.9 and 34.4 us at 8)
+// (16 trees of 64 nodes, a capped ragged batch and biased prompts of 200 to 1,500: 79.1, 64.2 and 29.5 us at 1;
+// 75.7, 63.8 and 28.7 us at 3; 80.3, 63.0 and 33.0 us at 8)
 constexpr int kUnitCost = 3;
 
 struct Seq {
