@@ -387,7 +387,9 @@ extern "C" tv_status tv_page_map(const int32_t* q_start, const int32_t* kv_len, 
   if (B > 0 && (!kv_len || !block_table || !n_pages || !status)) return TV_ERR_INVALID_ARG;
   tv::PageMapParams p{q_start, kv_len, block_table, n_pages, free_list, n_free, slots,
                       status,  B,      T,           P,       shift,     num_pages, 1};
-  const bool wide = T > 8192;
+  // (growing by prompts of 40 to 2,000 tokens and back: 16 of them 9.6 us with the slots in the first launch,
+  // 12.2 us with the wide one behind it; 64 of them 21.0 and 17.6 us)
+  const bool wide = T > 16384;
   p.map_slots = !wide;
   const int smem = 5 * B * (int)sizeof(int);
   // The pages that move are known to the device alone; the tables' size bounds them.  Growing by
@@ -395,7 +397,9 @@ extern "C" tv_status tv_page_map(const int32_t* q_start, const int32_t* kv_len, 
   // 16 us on a cluster; a decode step of 64 sequences and its way back 6.6 and 7.8 us.
   const long long most = (long long)B * P;
   const int ctas = (T > 1024 || B > 512 || most > 8192) ? 8 : 1;
-  const int threads = (T > 4096 || B > 1024) ? 1024 : 256;
+  // (a decode step of 64 and its way back 7.8 us with 256 threads a CTA, 8.2 with 512; 200 prompts 17.4,
+  // 15.5 and with 1,024 threads 16.8 us; 4,000 decode sequences 36.7, 24.2 and 21.0 us)
+  const int threads = B > 1024 ? 1024 : (T > 1024 || B > 128) ? 512 : 256;
   if (!tv::set_dyn_smem(tv::page_map_kernel, 5 * tv::kMaxSeqs * (int)sizeof(int)))
     return TV_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -449,7 +453,9 @@ extern "C" tv_status tv_paged_append(const void* k, const void* v, int64_t token
   p.C = D / 8;
   const long long items = 2ll * T * Hkv * p.C;
   const int per = tv::kAppendThreads;
-  if (items <= (long long)per * 8 * tv::device_sm_count())
+  // Rows of 8 heads of 128: 64 and 2,000 tokens take 1.4 and 3.2 us with one chunk a thread, 2.3 and 4.9 us
+  // with four; 8,192 tokens 14.0 and 12.0 us (78 % of what a copy reaches).
+  if (items <= (long long)per * 24 * tv::device_sm_count())
     return tv::launched(tv::launch_pdl(tv::append_kernel<1>, dim3((unsigned)((items + per - 1) / per)),
                                        dim3(per), 0, stream, p));
   return tv::launched(tv::launch_pdl(tv::append_kernel<4>,
