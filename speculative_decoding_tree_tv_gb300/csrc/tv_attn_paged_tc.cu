@@ -199,7 +199,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint32_t it = 0;
     // Rows of V before lo and from hi on may hold anything (NaN times a probability of 0 is
     // NaN): cleared in the tiles that have them (a unit's first and last at most), once the
-    // tile after them is on its way.
+    // tile after them is on its way, or a part without tiles comes (the ring of parts moves on only
+    // with the softmax warps, which wait for the products of that tile).
     uint32_t z_it = 0;
     int z0 = 0, z1 = kTcKeys;
     auto clear_rows = [&]() {
@@ -224,6 +225,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const Part w = s_ring.at(n);
       if (w.b < 0) break;
       b = w.b;
+      if (isV && w.begin == w.end) clear_rows();
       feed.start(p, w);
       for (int t = w.end - 1; t >= w.begin; --t, ++it) {
         const uint32_t st = it % stages;

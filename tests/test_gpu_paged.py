@@ -740,3 +740,35 @@ def test_two_calls_at_once(tv):
         torch.cuda.synchronize()
         for j in range(2):
             assert all(same(i + j, r) for r in outs[j])
+
+
+def tail_ref(c, b, m, Hq, Hkv, D, **kw):
+    """Token range and attn_ref of the last m tokens of sequence b alone."""
+    L, n = c["lens"][b]
+    end = sum(n for _, n in c["lens"][:b + 1])
+    part = dict(c, lens=[(L + n - m, m)], rows=[c["rows"][b]], q=c["q"][end - m:end])
+    return slice(end - m, end), attn_ref(part, Hq, Hkv, D, **kw)
+
+
+# (joined by their CTAs, and by the merge kernel)
+@pytest.mark.parametrize("good,bad,rest", [([(100, 20), (700, 64)] * 20, (0, 64), []),
+                                           ([(300, 9)] * 3, (0, 70), [(20000, 20)])])
+def test_bad_sequences_between_units_of_one_cta(tv, good, bad, rest):
+    """A CTA whose share goes from a unit with rows to clear (a ragged last tile) to the many units
+    without tiles of a sequence that does not fit: its neighbours are served and no wait runs out."""
+    lens = [x for s in good for x in (s, bad)] + rest
+    Hq, Hkv, D = 32, 8, 64
+    c = make(7, lens, Hq, Hkv, D, 16)
+    wrong = set(range(1, 2 * len(good), 2))
+    for b in wrong:
+        c["kv_len"][b] = 10**6
+    out, lse, status = run(tv, c)
+    assert status == [int(b in wrong) for b in range(len(lens))]
+    at = 0
+    for b, (_, n) in enumerate(lens):
+        if b in wrong:
+            assert bool((out[at:at + n] == 0).all()) and bool((lse[at:at + n] == 0).all())
+        elif b < 8 or b >= len(lens) - 2:
+            where, ref = tail_ref(c, b, min(n, 9), Hq, Hkv, D)
+            check_attn(out[where], lse[where], ref, "bf16", f"sequence {b}")
+        at += n
