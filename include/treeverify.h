@@ -633,9 +633,9 @@ tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, in
  * Causal (anc_mask NULL): pos is the row's index and rows j <= kv_len[b] + i
  * are visible.  Tree (anc_mask given): prefix rows j < kv_len[b] and rows
  * kv_len[b] + a for the set bits a of the token's mask are visible, and a
- * node's pos is kv_len[b] + its depth (the number of its mask bits less one; masks are
- * those of tv_tree_build).  With window > 0 only rows with pos(t) - pos(j) < window
- * are visible.  A token that sees nothing gets out = 0, lse = -inf.
+ * node's pos is kv_len[b] + its depth (the number of its mask bits less one, 0 for an
+ * empty mask; masks are those of tv_tree_build).  With window > 0 only rows with
+ * pos(t) - pos(j) < window are visible.  A token that sees nothing gets out = 0, lse = -inf.
  *
  *   q           [T, Hq, D] of the cache's type, 16-byte aligned; element strides
  *               q_token_stride, q_head_stride (multiples of 8), D contiguous.

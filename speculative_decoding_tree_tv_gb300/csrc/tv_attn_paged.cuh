@@ -179,6 +179,12 @@ __device__ __forceinline__ int anc_count(const uint64_t* anc, int W, int pos) {
   return c;
 }
 
+// Depth of the node with this mask row: its ancestors.  A node whose mask is empty (of a tree that
+// was refused) is taken at the root's depth, so that it reaches no further back than a window's pages.
+__device__ __forceinline__ int anc_depth(const uint64_t* anc, int W) {
+  return max(0, anc_count(anc, W, 64 * W) - 1);
+}
+
 // ------------------------------------------------------- shares of the work
 // (16 trees of 64 nodes, a capped ragged batch and biased prompts of 200 to 1,500: 79.1, 64.2 and 29.5 us at 1;
 // 75.7, 63.8 and 28.7 us at 3; 80.3, 63.0 and 33.0 us at 8)
@@ -203,8 +209,8 @@ __device__ __forceinline__ void key_range(const PagedAttnParams& p, const Seq& s
                                           int& hi) {
   const int first = qt * p.tq;
   hi = p.anc ? s.L + s.n : s.L + min(s.n, first + p.tq);
-  // (a node whose mask is empty counts as one before the root)
-  lo = p.window > 0 ? max(0, (p.anc ? s.L - 1 : s.L + first) - p.window + 1) : 0;
+  // (the root of a tree sees furthest back)
+  lo = p.window > 0 ? max(0, (p.anc ? s.L : s.L + first) - p.window + 1) : 0;
 }
 template <int KT>
 __device__ __forceinline__ int key_tiles(const PagedAttnParams& p, const Seq& s, int qt) {

@@ -226,7 +226,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       const int row = min(row_of(r), rows - 1);  // rows past the unit repeat its last
       const int i = w.first + row / p.G, t = w.s.t0 + i, h = w.kvh * p.G + row % p.G;
       tok[r] = t;
-      pos[r] = w.s.L + (p.anc ? anc_count(p.anc + (size_t)t * p.W, p.W, 64 * p.W) - 1 : i);
+      pos[r] = w.s.L + (p.anc ? anc_depth(p.anc + (size_t)t * p.W, p.W) : i);
       slope[r] = (MOD && p.slopes) ? __ldg(p.slopes + h) * kLog2e : 0.0f;
       m[r] = -INFINITY;
       l[r] = 0.0f;

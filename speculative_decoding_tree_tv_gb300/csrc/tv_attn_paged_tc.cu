@@ -430,7 +430,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const bool warp_works = warp_in_block && rb * nb + (warp & 3) * 32 / p.G < w.ntok;
       Row r;
       r.anc = p.anc ? p.anc + (size_t)(w.s.t0 + i) * p.W : nullptr;
-      r.pos = w.s.L + (p.anc ? anc_count(r.anc, p.W, 64 * p.W) - 1 : i);
+      r.pos = w.s.L + (p.anc ? anc_depth(r.anc, p.W) : i);
       r.limit = p.anc ? w.s.L : w.s.L + i + 1;
       r.from = p.window > 0 ? r.pos - p.window + 1 : 0;
       const float slope = (BIAS && p.slopes) ? __ldg(p.slopes + w.kvh * p.G + h_in) * kLog2e : 0.0f;

@@ -772,3 +772,43 @@ def test_bad_sequences_between_units_of_one_cta(tv, good, bad, rest):
             where, ref = tail_ref(c, b, min(n, 9), Hq, Hkv, D)
             check_attn(out[where], lse[where], ref, "bf16", f"sequence {b}")
         at += n
+
+
+@pytest.mark.parametrize("nodes", [1, 3, 40, 100])
+@pytest.mark.parametrize("D,kw", [(64, {}), (128, dict(slopes=True))])
+@pytest.mark.parametrize("last", [True, False])
+def test_pages_behind_a_trees_window_may_be_gone(tv, nodes, D, kw, last):
+    """Row kv_len - window is the first that the root does not see: its page may be gone where it is
+    the page's last row, and it may hold NaN where its page stays."""
+    L, page = 500, 16
+    window = L - (6 * page + 15 if last else 6 * page + 4)
+    kw = dict(kw, window=window)
+    if kw.get("slopes"):
+        kw["slopes"] = slopes_of(4)
+    c = make(nodes, [(L, nodes), (30, 2)], 4, 2, D, page, tree=True)
+    ref = attn_ref(c, 4, 2, D, **kw)
+    ids = np_(c["table"])[0].tolist()
+    whole = 7 if last else 6
+    c["table"][0, :whole] = -1
+    c["k"][ids[:whole]] = float("nan")
+    c["v"][ids[:whole]] = float("inf")
+    if not last:
+        c["k"][ids[6], :, :5] = float("nan")
+        c["v"][ids[6], :, :5] = float("nan")
+    out, lse, status = run(tv, c, **kw)
+    assert status == [0, 0]
+    check_attn(out, lse, ref, "bf16")
+
+
+@pytest.mark.parametrize("nodes", [3, 40])
+def test_empty_masks_reach_as_far_as_the_root(tv, nodes):
+    """A node whose mask is empty sits at the root's depth: what it sees of the prefix under a
+    window is what a token at the prefix's end sees under one that is a row shorter."""
+    L, window = 90, 50
+    c = make(3, [(L, nodes)], 4, 2, 64, 16, tree=True)
+    c["anc"].zero_()
+    out, lse, status = run(tv, c, window=window)
+    assert status == [0]
+    for i in {0, 1, nodes - 1}:
+        part = dict(c, lens=[(L - 1, 1)], rows=[tuple(r[:L] for r in c["rows"][0])], q=c["q"][i:i + 1], anc=None)
+        check_attn(out[i:i + 1], lse[i:i + 1], attn_ref(part, 4, 2, 64, window=window - 1), "bf16")
