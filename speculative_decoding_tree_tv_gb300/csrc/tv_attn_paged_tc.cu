@@ -81,13 +81,16 @@ struct Row {
   int pos;
 };
 
-// Visibility of keys j .. j + 31 for a row (the window's reach inside a tree is
-// taken in tree_scores).
-__device__ __forceinline__ uint32_t see32(const PagedAttnParams& p, const Row& r, int j, int L, int hi) {
-  uint32_t v = range_bits(r.from - j, r.limit - j);
+// The row's mask for keys j .. j + 31.
+__device__ __forceinline__ uint32_t tree32(const PagedAttnParams& p, const Row& r, int j, int L, int hi) {
   const int x = j - L;  // tree index of the first key
-  if (r.anc && x > -32 && j < hi) v |= anc_bits32(r.anc, p.W, x) & range_bits(0, hi - j);
-  return v;
+  return r.anc && x > -32 && j < hi ? anc_bits32(r.anc, p.W, x) & range_bits(0, hi - j) : 0u;
+}
+
+// Visibility of keys j .. j + 31 for a row (the window's reach inside a tree is
+// taken in tree_chunk).
+__device__ __forceinline__ uint32_t see32(const PagedAttnParams& p, const Row& r, int j, int L, int hi) {
+  return range_bits(r.from - j, r.limit - j) | tree32(p, r, j, L, hi);
 }
 
 // x, scaled, less slope times distance; b0: the first key's bias.
@@ -103,13 +106,13 @@ __device__ __forceinline__ void bias_chunk(float b0, float slope, float in_scale
   }
 }
 
-// 32 keys from j that reach the tree: a node's position is its depth's.  Clears v where the
-// window does not reach, and adds the bias.
-__device__ __forceinline__ void tree_chunk(const PagedAttnParams& p, const Row& r, int j, int L,
+// 32 keys from j that reach the tree: a node's position is its depth's, which the mask tells (v
+// lacks the nodes whose page is none).  Clears v where the window does not reach, and adds the bias.
+__device__ __forceinline__ void tree_chunk(const PagedAttnParams& p, const Row& r, int j, int L, int hi,
                                            float in_scale, float slope, uint32_t& v, uint32_t (&x)[32]) {
   const int a = j - L;  // tree index of the first key
   const int before = a > 0 ? anc_count(r.anc, p.W, min(a, 64 * p.W)) : 0;
-  const uint32_t tree = v & range_bits(-a, 32);
+  const uint32_t tree = tree32(p, r, j, L, hi);
 #pragma unroll
   for (int e = 0; e < 32; ++e) {
     const int kpos = a + e < 0 ? j + e : L + before + __popc(tree & (0xffffffffu >> (31 - e))) - 1;
@@ -532,7 +535,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             uint32_t x[32], v = c == 0 ? vis[0] : c == 1 ? vis[1] : c == 2 ? vis[2] : vis[3];
             tmem_ld32(tS + lane_base + 32 * c, x);
             tmem_wait_ld();
-            tree_chunk(p, r, j0 + 32 * c, L, in_scale, slope, v, x);
+            tree_chunk(p, r, j0 + 32 * c, L, hi, in_scale, slope, v, x);
             tmem_st32(tS + lane_base + 32 * c, x);
             if (c == 0) vis[0] = v;
             if (c == 1) vis[1] = v;

@@ -812,3 +812,23 @@ def test_empty_masks_reach_as_far_as_the_root(tv, nodes):
     for i in {0, 1, nodes - 1}:
         part = dict(c, lens=[(L - 1, 1)], rows=[tuple(r[:L] for r in c["rows"][0])], q=c["q"][i:i + 1], anc=None)
         check_attn(out[i:i + 1], lse[i:i + 1], attn_ref(part, 4, 2, 64, window=window - 1), "bf16")
+
+
+@pytest.mark.parametrize("nodes", [20, 90])
+@pytest.mark.parametrize("kw", [dict(slopes=True), dict(window=4), dict(slopes=True, window=6, softcap=9.0)])
+@pytest.mark.parametrize("Hq", [1, 4])
+def test_a_bad_page_inside_a_tree(tv, nodes, kw, Hq):
+    """Hidden nodes still count for the depth of those behind them (both kernels: 20 nodes of one head
+    are handed to the small one by the hint below)."""
+    L, page = 37, 8
+    kw = dict(kw)
+    if kw.get("slopes"):
+        kw["slopes"] = -8 * slopes_of(Hq)  # (what lies far back matters)
+    c = make(nodes, [(L, nodes), (50, 3)], Hq, 1, 64, page, tree=True)
+    W = (nodes + 63) // 64
+    c["max_q"] = min(nodes, 16) if Hq == 1 and W == 1 else nodes
+    c["table"][0, 5] = -1
+    hidden = {0: set(range(5 * page, 6 * page))}
+    out, lse, status = run(tv, c, **kw)
+    assert status == [1, 0]
+    check_attn(out, lse, attn_ref(c, Hq, 1, 64, hidden=hidden, **kw), "bf16")
