@@ -635,7 +635,8 @@ tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, in
  * kv_len[b] + a for the set bits a of the token's mask are visible, and a
  * node's pos is kv_len[b] + its depth (the number of its mask bits less one, 0 for an
  * empty mask; masks are those of tv_tree_build).  With window > 0 only rows with
- * pos(t) - pos(j) < window are visible.  A token that sees nothing gets out = 0, lse = -inf.
+ * pos(t) - pos(j) < window are visible.  A token that sees nothing gets out = 0, lse = -inf;
+ * a NaN in a query row, or in a key that it sees, makes its out and lse NaN.
  *
  *   q           [T, Hq, D] of the cache's type, 16-byte aligned; element strides
  *               q_token_stride, q_head_stride (multiples of 8), D contiguous.

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     float mx = M;
 #pragma unroll
     for (int j = 0; j < kMergeBatch; ++j) mx = fmaxf(mx, ml[j].x);
-    if (mx == -INFINITY) continue;
+    // (maxima leave a NaN out, sums carry it: 0 times NaN is NaN)
     const float f = M == -INFINITY ? 0.0f : ex2(M - mx);
     M = mx;
     l *= f;
@@ -87,9 +87,9 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     }
 #pragma unroll
     for (int j = 0; j < kMergeBatch; ++j) {
-      if (ml[j].x == -INFINITY) continue;  // (a part whose keys are all hidden: select, do not multiply)
-      const float e = ex2(ml[j].x - M);
+      const float e = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - M);
       l = fmaf(e, ml[j].y, l);
+      if (e == 0.0f) continue;  // (a part whose keys are all hidden: select, do not multiply)
 #pragma unroll
       for (int c = 0; c < kC; ++c) {
         a[c].x = fmaf(e, v[j][c].x, a[c].x);
@@ -99,12 +99,12 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
       }
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint2* out = reinterpret_cast<uint2*>(p.out + oidx * D) + c0;
 #pragma unroll
   for (int c = 0; c < kC; ++c)
     out[c] = make_uint2(pack2<F16>(a[c].x * inv, a[c].y * inv), pack2<F16>(a[c].z * inv, a[c].w * inv));
-  if (c0 == 0 && p.lse) p.lse[oidx] = l > 0.0f ? (M + log2f(l)) * kLn2 : -INFINITY;
+  if (c0 == 0 && p.lse) p.lse[oidx] = l == 0.0f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
 // --------------------------------------------------------------------- host

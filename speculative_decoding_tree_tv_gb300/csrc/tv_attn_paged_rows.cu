@@ -416,12 +416,12 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
     for (int x = 0; x < kRowsWarps; ++x) {
       const float2 v = s_ml[x][row];
-      if (v.x != -INFINITY) ll = fmaf(ex2(v.x - mm), v.y, ll);
+      ll = fmaf(v.x == -INFINITY ? 0.0f : ex2(v.x - mm), v.y, ll);  // (a NaN stays: maxima leave it out, sums do not)
     }
     const bool mine = tid < 8 * NR && row < rows;
     const int out_tok = w.s.t0 + w.first + row / p.G, h = w.kvh * p.G + row % p.G;
     const size_t oidx = (size_t)out_tok * p.Hq + h;
-    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
 #pragma unroll
@@ -460,7 +460,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
     if (mine && (tid & 7) == 0) {
       if (w.slot >= 0) p.part_ml[(size_t)w.slot * kUnitRows + row] = make_float2(mm, ll);
-      else if (p.lse) p.lse[oidx] = w.s.bad ? 0.0f : (ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY);
+      else if (p.lse) p.lse[oidx] = w.s.bad ? 0.0f : (ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2);
     }
     if (lane == 0) s_ring.done(np);
     if (abort) {

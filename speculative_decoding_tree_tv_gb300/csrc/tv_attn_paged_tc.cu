@@ -658,15 +658,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           ok = await_rows(p, w.slot + k, warp);
           const float2 ml = ok && mine ? __ldcg(&p.part_ml[(size_t)(w.slot + k) * 256 + crow])
                                        : make_float2(-INFINITY, 0.0f);
-          if (ml.x != -INFINITY) {
-            const float top = fmaxf(m_all, ml.x);
-            l_all = fmaf(m_all == -INFINITY ? 0.0f : ex2(m_all - top), l_all, ex2(ml.x - top) * ml.y);
-            m_all = top;
-          }
+          // (maxima leave a NaN out, sums carry it: 0 times NaN is NaN)
+          const float top = fmaxf(m_all, ml.x);
+          l_all = fmaf(m_all == -INFINITY ? 0.0f : ex2(m_all - top), l_all,
+                       (ml.x == -INFINITY ? 0.0f : ex2(ml.x - top)) * ml.y);
+          m_all = top;
         }
         if (!ok) break;
         const float f0 = m_run == -INFINITY ? 0.0f : ex2(m_run - m_all);
-        const float inv = l_all > 0.0f ? 1.0f / l_all : 0.0f;
+        const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
         uint8_t* orow = reinterpret_cast<uint8_t*>(p.out + oidx * D);
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
@@ -709,7 +709,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
           __syncwarp();
         }
-        if (mine && p.lse) p.lse[oidx] = l_all > 0.0f ? (m_all + log2f(l_all)) * kLn2 : -INFINITY;
+        if (mine && p.lse) p.lse[oidx] = l_all == 0.0f ? -INFINITY : (m_all + log2f(l_all)) * kLn2;
       }
       tc_fence_before();
       __syncwarp();

@@ -832,3 +832,51 @@ def test_a_bad_page_inside_a_tree(tv, nodes, kw, Hq):
     out, lse, status = run(tv, c, **kw)
     assert status == [1, 0]
     check_attn(out, lse, attn_ref(c, Hq, 1, 64, hidden=hidden, **kw), "bf16")
+
+
+# (small units, whole and split; larger ones whole, merged, and joined by their CTAs)
+NAN_LENS = [[(90, 1), (128, 1)], [(300, 1), (2048, 1), (64, 1)], [(50, 40), (120, 9)], [(300, 80), (2040, 9)],
+            [(700 + 40 * i, 64) for i in range(45)]]
+
+
+def same_bits(a, b):
+    return torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
+
+
+@pytest.mark.parametrize("lens", NAN_LENS)
+@pytest.mark.parametrize("kw", [{}, dict(softcap=30.0), dict(window=40)])
+def test_nan_in_a_query_row(tv, lens, kw):
+    """The row's out and lse are NaN, whichever way its unit is cut; no other row changes."""
+    c = make(3, lens, 8, 2, 128, 16)
+    want = run(tv, c, **kw)
+    last = [s - 1 for s in starts([n for _, n in lens])[1:]]
+    c["q"] = c["q"].clone()
+    for b, t in enumerate(last):
+        c["q"][t, b % 8, 5] = float("nan")
+    out, lse, status = run(tv, c, **kw)
+    assert status == [0] * len(lens)
+    for b, t in enumerate(last):
+        assert bool(out[t, b % 8].isnan().all()) and bool(lse[t, b % 8].isnan())
+        out[t, b % 8], lse[t, b % 8] = want[0][t, b % 8], want[1][t, b % 8]
+    assert same_bits(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("lens", NAN_LENS)
+@pytest.mark.parametrize("kw", [{}, dict(softcap=30.0), dict(window=40)])
+@pytest.mark.parametrize("where", ["last", "middle", "first"])
+def test_nan_in_a_key(tv, lens, kw, where):
+    """Tokens that see the key get NaN (alone in its tile or not, in one part of a unit or another);
+    tokens that do not are as they were."""
+    c = make(4, lens, 8, 2, 128, 16)
+    want = run(tv, c, **kw)
+    sees, at = [], 0
+    table = np_(c["table"])
+    for b, (L, n) in enumerate(lens):
+        j = dict(last=L + n - 1, middle=L + n // 2, first=0)[where]
+        c["k"][table[b, j // 16], :, j % 16, 3] = float("nan")
+        sees += [L + i >= j and L + i - j < kw.get("window", 10**9) for i in range(n)]
+    out, lse, status = run(tv, c, **kw)
+    assert status == [0] * len(lens)
+    sees = torch.tensor(sees, device="cuda:0")
+    assert bool(out[sees].isnan().all()) and bool(lse[sees].isnan().all())
+    assert same_bits(out[~sees], want[0][~sees]) and torch.equal(lse[~sees], want[1][~sees])
