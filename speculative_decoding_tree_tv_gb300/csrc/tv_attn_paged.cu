@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <chrono>
 
 #include "tv_attn_paged.cuh"
@@ -349,16 +350,20 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   p.token = tv::paged::next_token();
   const float sc = scale == 0.0f ? 1.0f / sqrtf((float)D) : scale;
   p.scale_log2 = sc * tv::paged::kLog2e;
-  p.softcap_log2 = softcap * tv::paged::kLog2e;
-  p.cap_in = softcap > 0.0f ? sc / softcap : 0.0f;
-  // the cubic's coefficients for products as they are, in the log2 domain; not where their
-  // powers would leave the 32-bit range
+  // (caps at the ends of the 32-bit range: a product of 0 has a score of 0 all the same)
+  p.softcap_log2 = fminf(softcap * tv::paged::kLog2e, FLT_MAX);
+  p.cap_in = softcap > 0.0f ? fminf(sc / softcap, 1e30f) : 0.0f;
+  // The cubic's coefficients for products as they are, in the log2 domain.  For a large cap the higher
+  // ones fade to 0 and nearly every score is taken by it: the function for the others is off by
+  // some 2^-23 of the cap, not of the score.  For caps below 1e-5 of the scale, whose coefficients would
+  // leave the 32-bit range, that is small, and it takes all.
   p.cap_top = -1.0f;
-  if (p.cap_in >= 1e-5f && p.cap_in <= 1e5f) {
+  for (float& c : p.cap_q) c = 0.0f;
+  if (p.cap_in <= 1e5f) {
     const float a2 = p.cap_in * p.cap_in;
     float f = p.scale_log2;
     for (int i = 0; i < 4; ++i, f *= a2) p.cap_q[i] = f * tv::paged::kTanhC[i];
-    p.cap_top = tv::paged::kTanhSmall * tv::paged::kTanhSmall / a2;
+    p.cap_top = fminf(tv::paged::kTanhSmall * tv::paged::kTanhSmall / a2, 1e36f);  // (squares stay finite)
   }
   const bool bias = slopes || (anc_mask && window > 0 && window < 64 * p.W);
   const bool f16 = cache->dtype == TV_FP16;

@@ -880,3 +880,19 @@ def test_nan_in_a_key(tv, lens, kw, where):
     sees = torch.tensor(sees, device="cuda:0")
     assert bool(out[sees].isnan().all()) and bool(lse[sees].isnan().all())
     assert same_bits(out[~sees], want[0][~sees]) and torch.equal(lse[~sees], want[1][~sees])
+
+
+@pytest.mark.parametrize("softcap", [1e-42, 1e-30, 1e-7, 9e3, 1e5, 1e8, 1e30, 3.4e38])
+@pytest.mark.parametrize("lens", [[(300, 1), (5, 1)], [(200, 40)]])
+def test_caps_of_any_size(tv, softcap, lens):
+    """A large cap leaves scores as they are, a small one makes them equal.  attn_ref's bound on a score
+    holds 8 roundings of the cap, which say nothing for a large one: without them it is the bound of the
+    uncapped scores, and the cubic's 2^-22 and its seven roundings of the score (below 8 * 2^-23 of
+    the terms' magnitudes, of which the bound has D + 4 = 68) make it 9 / 8 of that at most."""
+    c = make(3, lens, 4, 1, 64, 16, q_mag=3.0)
+    c["q"] = c["q"].clone()
+    c["q"][0, 0] = 0
+    out, lse, status = run(tv, c, softcap=softcap)
+    assert status == [0] * len(lens)
+    ref, plain = attn_ref(c, 4, 1, 64, softcap=softcap), attn_ref(c, 4, 1, 64)
+    check_attn(out, lse, ref[:3] + (plain[3] * 1.125 if softcap > 1 else ref[3],) + ref[4:], "bf16")
