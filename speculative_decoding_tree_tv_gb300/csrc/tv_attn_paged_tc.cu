@@ -506,8 +506,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               }
             }
           // a warp with a score past the cubic's range takes all again, through TMEM (which
-          // still holds them), to keep the code of this rare way small
-          if (__any_sync(0xffffffffu, top > p.cap_top)) {
+          // still holds them), to keep the code of this rare way small (rows past the unit hold
+          // anything, and have no say in it)
+          if (__any_sync(0xffffffffu, top > p.cap_top && tl < nb && rb * nb + tl < w.ntok)) {
             const float in = 2.0f * kLog2e * p.cap_in;
 #pragma unroll 1
             for (int c = 0; c < 128; c += 8) {

@@ -896,3 +896,18 @@ def test_caps_of_any_size(tv, softcap, lens):
     assert status == [0] * len(lens)
     ref, plain = attn_ref(c, 4, 1, 64, softcap=softcap), attn_ref(c, 4, 1, 64)
     check_attn(out, lse, ref[:3] + (plain[3] * 1.125 if softcap > 1 else ref[3],) + ref[4:], "bf16")
+
+
+@pytest.mark.parametrize("lens", [[(200, 37)], [(500, 35), (0, 33)]])
+@pytest.mark.parametrize("Hq,D", [(8, 64), (10, 128)])
+def test_capped_rows_do_not_depend_on_rows_past_the_unit(tv, lens, Hq, D):
+    """What the rows behind a unit's tokens hold (the query box reaches over them) changes no bit."""
+    got = []
+    for fill in (0.0, 1000.0, float("nan")):
+        c = make(3, lens, Hq, 2, D, 16, pad=40)
+        c["q"] = c["q"].clone()
+        c["q"][c["T"]:] = fill
+        got.append(run(tv, c, softcap=9.0))
+        assert got[-1][2] == [0] * len(lens)
+    for g in got[1:]:
+        assert same_bits(g[0], got[0][0]) and torch.equal(g[1], got[0][1])
