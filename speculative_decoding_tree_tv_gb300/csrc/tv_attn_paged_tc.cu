@@ -247,7 +247,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                         atom * 64, key & ((1 << p.page_shift) - 1), w.kvh, page, p.row_dim, p.head_dim);
         if (isV) {
           clear_rows();
-          if (!ok) break;
+          if (!ok) {
+            ++it;  // (this tile's copy is on its way)
+            break;
+          }
           z_it = it;
           z0 = max(0, w.lo - t * kTcKeys);
           z1 = min(kTcKeys, w.hi - t * kTcKeys);
