@@ -43,8 +43,8 @@
  *  - Errors in device-resident data (a malformed parent[] array, a token
  *    outside [0, V), a kv_len that does not fit the cache) are written to the
  *    per-sequence `status[b]` array (0 = ok) and that sequence's outputs are
- *    set to -1 (indices) or 0 (values).  No kernel traps, asserts or
- *    spin-waits.
+ *    set to -1 (indices) or 0 (values).  No kernel traps or asserts, and
+ *    every wait has a limit.
  *  - Trees: node 0 is the root (the token right after the cached prefix,
  *    always accepted), parent[b*N + 0] = -1 and 0 <= parent[b*N + i] < i for
  *    i > 0, i.e. the nodes are numbered in a topological order.  N <= 512.
@@ -315,13 +315,15 @@ tv_status tv_accept_greedy(const float* logits, const int32_t* tokens, const int
  * no counterpart).  Every wait of a kernel in this library is bounded: when
  * its limit (about a second of SM clock) runs out, the kernel stops waiting,
  * reports TV_ERR_TIMEOUT in status[b] and leaves with no copy in flight.
- * This call sets, for the current device, the limit of one such wait -- the
- * wait of tv_accept_greedy's CTAs for their logit chunks -- so that a test
+ * This call sets, for the current device, the limit of some of them -- the
+ * wait of tv_accept_greedy's CTAs for their logit chunks, and the waits of
+ * the tv_attn_paged calls made (or captured) after it -- so that a test
  * can make it run out without a fault or a hang:
  *   cycles >= 1                 limit in SM cycles;
  *   cycles == 0                 a single non-blocking test of the copies
  *                               (a call then reports TV_ERR_TIMEOUT, since
- *                               its copies have only just been issued);
+ *                               its copies have only just been issued;
+ *                               tv_attn_paged does not issue them);
  *   cycles == TV_WAIT_LIMIT_DEFAULT  restores the regular limit.
  * The second wait that keeps copies from outliving a CTA keeps the regular
  * limit.  Host call, synchronous with respect to the device's default
@@ -655,7 +657,9 @@ tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, in
  *               - kv_len[b] < 0, kv_len[b] + n_b > P * page_size, or with anc_mask
  *                 n_b > 64 W (its rows are zeroed, lse too);
  *               - a page id outside [0, num_pages) among the sequence's pages that
- *                 the window reaches (its keys count as hidden).
+ *                 the window reaches (its keys count as hidden);
+ *               or TV_ERR_TIMEOUT for the sequences with tokens whose rows may be missing, as
+ *               a wait gave up (some beside them in the batch may be named too).
  *   workspace   tv_attn_paged_workspace_size() bytes, 256-byte aligned, any
  *               contents; calls that share one must not run concurrently.  After
  *               TV_ERR_TIMEOUT its contents are to be overwritten before a captured call

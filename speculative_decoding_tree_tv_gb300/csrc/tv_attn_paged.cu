@@ -23,8 +23,7 @@ constexpr int kMergeThreads = 256, kMergeBatch = 2;
 __device__ __forceinline__ void merge_status(const PagedAttnParams& p) {
   if (!p.status) return;
   for (int b = blockIdx.y * gridDim.x + blockIdx.x; b < p.B; b += gridDim.x * gridDim.y) {
-    bool late = false;
-    for (int c = threadIdx.x; c < gridDim.x; c += kMergeThreads) late |= p.timeout[c] == b + 1;
+    const bool late = is_late(p, b, threadIdx.x, kMergeThreads);
     const bool bad = !seq_ok(p, b, threadIdx.x, kMergeThreads);
     const int any_late = __syncthreads_or(late), any_bad = __syncthreads_or(bad);
     if (threadIdx.x == 0)
@@ -181,6 +180,13 @@ unsigned long long next_token() {
 }
 
 
+// Limits of the kernels' waits, less the regular one (so that 0 is that); by device.
+std::atomic<long long> g_wait_limit[kMaxDevicesCached];
+long long wait_limit() {
+  const int dev = current_device();
+  return kWaitLimitCycles + (dev >= 0 && dev < kMaxDevicesCached ? g_wait_limit[dev].load() : 0);
+}
+
 // Which kernel runs, by the rows of the largest unit.
 PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long keys) {
   PagedPlan pl;
@@ -222,7 +228,7 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
   pl.part_bytes = align_up(r * D * 4, 256);
   pl.ml_bytes = align_up(r * 8, 256);
   pl.desc_bytes = align_up((size_t)pl.ctas * 16, 256);
-  pl.timeout_bytes = align_up((size_t)pl.ctas * 4, 256);
+  pl.late_bytes = align_up((size_t)pl.ctas * sizeof(Late) + 8, 256);
   pl.ready_bytes = align_up((size_t)pl.ctas * 64, 256);
   return pl;
 }
@@ -237,6 +243,12 @@ cudaError_t launch_merge(const PagedPlan& pl, const PagedAttnParams& p, cudaStre
 }
 
 }  // namespace
+
+void set_wait_limit(long long cycles) {
+  const int dev = current_device();
+  if (dev >= 0 && dev < kMaxDevicesCached) g_wait_limit[dev] = cycles - kWaitLimitCycles;
+}
+
 }  // namespace paged
 }  // namespace tv
 
@@ -313,7 +325,9 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.part_bytes);
   p.desc = reinterpret_cast<int4*>(ws + pl.part_bytes + pl.ml_bytes);
-  p.timeout = reinterpret_cast<int*>(ws + pl.part_bytes + pl.ml_bytes + pl.desc_bytes);
+  p.late = reinterpret_cast<tv::paged::Late*>(ws + pl.part_bytes + pl.ml_bytes + pl.desc_bytes);
+  p.any_late = reinterpret_cast<unsigned long long*>(p.late + pl.ctas);
+  p.wait_limit = tv::paged::wait_limit();
   p.q = static_cast<const uint16_t*>(q);
   p.table = block_table;
   p.q_start = q_start;
@@ -346,7 +360,7 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   p.merge = pl.merge;
   p.ready = reinterpret_cast<unsigned long long*>(ws + pl.part_bytes + pl.ml_bytes + pl.desc_bytes +
-                                                  pl.timeout_bytes);
+                                                  pl.late_bytes);
   p.token = tv::paged::next_token();
   const float sc = scale == 0.0f ? 1.0f / sqrtf((float)D) : scale;
   p.scale_log2 = sc * tv::paged::kLog2e;

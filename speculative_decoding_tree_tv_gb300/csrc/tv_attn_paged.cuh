@@ -40,6 +40,13 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleLog2 = 8.0f;  // keep a stale maximum while within 2^8
 constexpr int kMaxSeqs = 4096;
 
+// A CTA whose waits gave up: rows of the sequences first .. last with tokens may not be there.  It counts
+// only with this call's token.
+struct Late {
+  unsigned long long token;
+  int first, last;
+};
+
 struct PagedAttnParams {
   const uint16_t* q;
   long long q_token_stride, q_head_stride;
@@ -54,7 +61,9 @@ struct PagedAttnParams {
   float* part;      // [2 * CTAs] slots of partial rows
   float2* part_ml;  // their (running maximum, log2 domain; running sum)
   int4* desc;       // [CTAs]: the unit a CTA's share ends inside (first token, tokens, kv head, parts)
-  int* timeout;     // [CTAs]: 1 + a sequence whose waits gave up, or 0
+  Late* late;       // [CTAs]
+  unsigned long long* any_late;  // this call's token: some CTA is late
+  long long wait_limit;          // SM cycles; 0: the producers of K and V give up before they load anything
   int B, T, P, Hq, Hkv, G, W, window;
   int num_pages, page_shift;
   int row_dim, head_dim;  // which of a cache map's dimensions 1, 2, 3 they are (the pages: the third)
@@ -140,8 +149,17 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map,
   const int c3 = row_dim == 3 ? row : head_dim == 3 ? head : page;
   tma_load_4d(dst, map, bar, d0, c1, c2, c3);
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+// A wait that gives up after `limit` SM cycles.  (The limit is looked at where a barrier is not ready:
+// a branch or another test ahead of it cost a chunk of 2048 6 us and biased prompts 0.7 us.)
+__device__ __forceinline__ bool wait_within(uint64_t* bar, uint32_t parity, long long limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > limit) return false;
+  return true;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long limit) {
+  return __all_sync(0xffffffffu, wait_within(bar, parity, limit));
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -247,6 +265,7 @@ struct Cursor {
   long long rest, share;  // cost left, cost of a share
   long long at;           // cost behind the share's start
   int b, kvh, qt, pos;    // unit, and cost of it that lies behind
+  int last;               // the share's last sequence (or one behind it, where a thread looks at several)
   Seq s;
 
   __device__ __forceinline__ int cost_of(const PagedAttnParams& p, int tiles) const {
@@ -309,13 +328,13 @@ __device__ __forceinline__ void prefetch_lengths(const PagedAttnParams& p) {
   if (first < words) line_prefetch_l2(p.table + first);
 }
 
-// Finds this CTA's share.  All THREADS threads call it; ends with a barrier.  Where sequences are few and
+// Finds this CTA's share (s_cur: shared; rest is 0 where there is none).  All THREADS threads call it;
+// ends with a barrier.  Where sequences are few and
 // chunks long, 2^share_lanes lanes share one's query tiles (a lane that walked the 32 of a chunk of 2048
 // alone held up the first tile by some 3,000 cycles).
 template <int KT, int THREADS>
-__device__ __forceinline__ Cursor<KT> find_share(const PagedAttnParams& p) {
+__device__ __forceinline__ void find_share(const PagedAttnParams& p, Cursor<KT>& s_cur) {
   __shared__ long long s_warp[THREADS / 32];
-  __shared__ Cursor<KT> s_cur;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lanes = 1 << p.share_lanes;
   const int per = ceil_div(p.B, THREADS);  // (1 where lanes > 1)
@@ -360,6 +379,7 @@ __device__ __forceinline__ Cursor<KT> find_share(const PagedAttnParams& p) {
     before = div_fast(mine - base, p.Hkv);
     one = div_fast(sum, p.Hkv);
   }
+  const long long base0 = base;
   c.share = max(div_fast(total + gridDim.x - 1, gridDim.x), (long long)p.min_share);
   const long long x0 = share_index() * c.share;
   c.rest = min(total - x0, c.share);
@@ -380,14 +400,22 @@ __device__ __forceinline__ Cursor<KT> find_share(const PagedAttnParams& p) {
       const int cost = c.cost_of(p, key_tiles<KT>(p, c.s, c.qt));
       if (left < cost) {
         c.pos = (int)left;
-        s_cur = c;
+        s_cur.rest = c.rest;
+        s_cur.share = c.share;
+        s_cur.at = c.at;
+        s_cur.b = c.b;
+        s_cur.kvh = c.kvh;
+        s_cur.qt = c.qt;
+        s_cur.pos = c.pos;
+        s_cur.s = c.s;
         break;
       }
       left -= cost;
     }
   }
+  const long long x1 = x0 + c.rest;  // the share's end, among this lane's sequences?
+  if (c.rest > 0 && x1 > base0 && x1 <= base0 + sum) s_cur.last = b1 - 1;
   __syncthreads();
-  return s_cur;
 }
 
 // The parts of a CTA's share, published by the one warp that walks it: the other
@@ -404,9 +432,9 @@ struct PartRing {
     }
   }
   // (a whole warp)
-  __device__ __forceinline__ bool publish(uint32_t n, const Part& w) {
+  __device__ __forceinline__ bool publish(uint32_t n, const Part& w, long long limit) {
     const uint32_t i = n % kPartRing;
-    if (!__all_sync(0xffffffffu, mbar_wait(&empty[i], ((n / kPartRing) & 1) ^ 1))) return false;
+    if (!warp_wait(&empty[i], ((n / kPartRing) & 1) ^ 1, limit)) return false;
     if ((threadIdx.x & 31) == 0) {
       part[i] = w;
       mbar_arrive(&full[i]);
@@ -414,8 +442,8 @@ struct PartRing {
     __syncwarp();
     return true;
   }
-  __device__ __forceinline__ bool ready(uint32_t n) {
-    return mbar_wait(&full[n % kPartRing], (n / kPartRing) & 1);
+  __device__ __forceinline__ bool ready(uint32_t n, long long limit) {
+    return wait_within(&full[n % kPartRing], (n / kPartRing) & 1, limit);
   }
   __device__ __forceinline__ const Part& at(uint32_t n) const { return part[n % kPartRing]; }
   __device__ __forceinline__ void done(uint32_t n) { mbar_arrive(&empty[n % kPartRing]); }  // one thread
@@ -440,20 +468,50 @@ __device__ __forceinline__ bool seq_ok(const PagedAttnParams& p, int b, int lane
   }
   return any == 0;
 }
+// Whether a CTA that gave up may have left rows of sequence b undone; `lane` of `lanes` threads
+// looks at its share of the CTAs.
+__device__ __forceinline__ bool is_late(const PagedAttnParams& p, int b, int lane, int lanes) {
+  if (*(volatile unsigned long long*)p.any_late != p.token) return false;
+  int t0, n;
+  bool late = false;
+  for (int c = lane; c < gridDim.x; c += lanes) {
+    volatile Late* l = p.late + c;
+    late |= l->token == p.token && b >= l->first && b <= l->last;
+  }
+  return late && seq_range(p.q_start, b, p.T, t0, n) && n > 0;
+}
 // status[b] of the sequences b = CTA, CTA + grid, .., by one warp, where no merge kernel follows
-// to write it.
+// to write it.  A CTA that gives up (report_late) leaves its mark, then the status; here the status comes
+// first, then a look at the marks: with a fence between the two on either side, a look that misses
+// the mark comes before it, and the status here before the one there.
 __device__ __forceinline__ void write_status(const PagedAttnParams& p) {
-  if (!p.status) return;
+  if (!p.status || blockIdx.x >= p.B) return;
   const int lane = threadIdx.x & 31;
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     const bool ok = __all_sync(0xffffffffu, seq_ok(p, b, lane, 32));
-    if (lane == 0) p.status[b] = ok ? TV_OK : TV_ERR_INVALID_ARG;
+    if (lane == 0) *(volatile int32_t*)(p.status + b) = ok ? TV_OK : TV_ERR_INVALID_ARG;
   }
+  __threadfence();
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+    if (__any_sync(0xffffffffu, is_late(p, b, lane, 32)) && lane == 0)
+      *(volatile int32_t*)(p.status + b) = TV_ERR_TIMEOUT;
 }
-// A wait of this CTA gave up (one thread).
-__device__ __forceinline__ void report_timeout(const PagedAttnParams& p, int b) {
-  if (p.merge) p.timeout[blockIdx.x] = b + 1;
-  else if (p.status && b >= 0) atomicMax(p.status + b, (int)TV_ERR_TIMEOUT);
+// A wait of this CTA gave up: the sequences of its share from `first` on may lack rows (one thread).
+template <int KT>
+__device__ __forceinline__ void report_late(const PagedAttnParams& p, const Cursor<KT>& share, int first) {
+  if (share.rest <= 0) return;
+  volatile Late* l = p.late + blockIdx.x;
+  l->first = first;
+  l->last = share.last;
+  __threadfence();
+  l->token = p.token;
+  *(volatile unsigned long long*)p.any_late = p.token;
+  __threadfence();
+  if (p.merge || !p.status) return;  // (the merge kernel looks at the marks)
+  for (int b = first; b <= share.last; ++b) {
+    int t0, n;
+    if (seq_range(p.q_start, b, p.T, t0, n) && n > 0) *(volatile int32_t*)(p.status + b) = TV_ERR_TIMEOUT;
+  }
 }
 
 // Hand-over of partial rows within the launch, warp by warp (a warp holds the same rows of a
@@ -475,7 +533,7 @@ __device__ __forceinline__ bool await_rows(const PagedAttnParams& p, int share, 
       unsigned long long v;
       asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
       if (v == p.token) break;
-      if (clock64() - t0 > kWaitLimitCycles) {
+      if (clock64() - t0 > p.wait_limit) {
         ok = false;
         break;
       }
@@ -539,8 +597,8 @@ struct PagedPlan {
   int tq, nb, ctas, min_share;
   int whole;  // units are not split
   int merge;  // the merge kernel follows
-  size_t part_bytes, ml_bytes, desc_bytes, timeout_bytes, ready_bytes;
-  size_t bytes() const { return part_bytes + ml_bytes + desc_bytes + timeout_bytes + ready_bytes; }
+  size_t part_bytes, ml_bytes, desc_bytes, late_bytes, ready_bytes;
+  size_t bytes() const { return part_bytes + ml_bytes + desc_bytes + late_bytes + ready_bytes; }
 };
 
 constexpr int kTcKeys = 128;  // keys of a tile of the tcgen05 kernel

@@ -88,6 +88,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   __shared__ float2 s_ml[kRowsWarps][kUnitRows];
   __shared__ volatile int s_abort;  // a consumer's wait ran out
   __shared__ PartRing s_ring;
+  __shared__ Cursor<kRowsKeys> s_cur;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   if (tid == 0) {
@@ -103,7 +104,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
   }
   prefetch_lengths<kRowsThreads>(p);
   pdl_wait();
-  Cursor<kRowsKeys> cur = find_share<kRowsKeys, kRowsThreads>(p);
+  find_share<kRowsKeys, kRowsThreads>(p, s_cur);
   uint32_t st = 0, phase = 0, np = 0;  // stage, its ring's phase; parts so far
   auto next_stage = [&]() {
     phase ^= st == kStages - 1;
@@ -117,21 +118,18 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     const CUtensorMap* map = isV ? &tmV : &tmK;
     uint8_t* ring = isV ? sV : sK;
     Part w;
-    w.b = -1;
-    if (p.merge && !isV && lane == 0) {
-      p.desc[share_index()] = make_int4(0, 0, 0, 0);
-      p.timeout[blockIdx.x] = 0;
-    }
+    Cursor<kRowsKeys> cur = s_cur;
+    if (p.merge && !isV && lane == 0) p.desc[share_index()] = make_int4(0, 0, 0, 0);
     PageFeed<kRowsKeys> feed;
     const int rows_page = min(1 << p.page_shift, kRowsKeys);  // rows of one box
     uint32_t issued = 0;
     const int npg = kRowsKeys / rows_page;
     const int pg = lane % npg, atom = lane / npg, row0 = pg * rows_page;
     const bool issues = atom < Lay::kAtoms;
-    bool ok = true;
-    for (;; ++np) {
+    bool ok = p.wait_limit > 0;
+    for (; ok; ++np) {
       if (isV) {
-        ok = __all_sync(0xffffffffu, s_ring.ready(np));
+        ok = __all_sync(0xffffffffu, s_ring.ready(np, p.wait_limit));
         if (!ok) break;
         w = s_ring.at(np);
         __syncwarp();
@@ -139,7 +137,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         if (w.b < 0) break;
       } else {
         const bool more = cur.next(p, w);
-        ok = s_ring.publish(np, w);
+        ok = s_ring.publish(np, w, p.wait_limit);
         if (!ok || !more) break;
         if (w.parts && lane == 0)
           p.desc[share_index()] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
@@ -149,7 +147,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         const int row = (t * kRowsKeys + row0) & ((1 << p.page_shift) - 1);
         uint32_t bad8;
         const int page = feed.get(p, w, t, pg, bad8);
-        ok = warp_wait(&bar_empty[st], phase ^ 1);
+        ok = warp_wait(&bar_empty[st], phase ^ 1, p.wait_limit);
         if (!ok) break;
         if (lane == 0) {
           if (!isV) s_bad_pages[st] = bad8;
@@ -165,11 +163,11 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (!ok) break;
     }
     if (!p.merge && !isV) write_status(p);
-    // no copy may be in flight when the CTA leaves
+    // no copy may be in flight when the CTA leaves (where the other producer gave up, its half of a
+    // stage never comes: this one's has landed long before the limit)
     for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-      mbar_wait(&bar_full[i % kStages], (i / kStages) & 1);
-    if (!ok && lane == 0) report_timeout(p, w.b);
-    return;
+      if (!mbar_wait(&bar_full[i % kStages], (i / kStages) & 1)) break;
+    return;  // (what a producer that gave up did not load, the consumers wait for in vain, and report)
   }
 
   // ---------------------------------------------------------------- consumers
@@ -187,13 +185,13 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
   };
-  int b = 0;
+  int b = s_cur.b;
   for (;; ++np) {
     // (a warp that gives up still joins the others at the unit's end, where all see it)
-    if (!__all_sync(0xffffffffu, s_ring.ready(np))) s_abort = 1;
+    if (!__all_sync(0xffffffffu, s_ring.ready(np, p.wait_limit))) s_abort = 1;
     named_sync(1, kRowsWarps * 32);
     if (s_abort) {
-      if (tid == 0) report_timeout(p, b);
+      if (tid == 0) report_late(p, s_cur, b);
       break;
     }
     const Part w = s_ring.at(np);
@@ -241,7 +239,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 
     for (int t = w.end - 1; t >= w.begin; --t) {  // (last first: see paged_tc_kernel)
       const int j0 = t * kRowsKeys + 16 * warp;
-      if (!warp_wait(&bar_full[st], phase)) {
+      if (!warp_wait(&bar_full[st], phase, p.wait_limit)) {
         s_abort = 1;
         break;
       }
@@ -464,7 +462,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     }
     if (lane == 0) s_ring.done(np);
     if (abort) {
-      if (tid == 0) report_timeout(p, w.b);
+      if (tid == 0) report_late(p, s_cur, b);
       break;
     }
   }

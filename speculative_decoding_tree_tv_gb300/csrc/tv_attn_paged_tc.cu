@@ -21,6 +21,8 @@
 // is issued while this one's epilogue still reads O: its first PV needs P, which the same
 // threads write after the epilogue.  Every wait is bounded.
 #define TV_UNIT 13
+#include <climits>
+
 #include "tv_attn_paged.cuh"
 
 namespace tv {
@@ -149,6 +151,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   __shared__ volatile uint32_t s_bad_pages[kBadRing];  // bit g: keys 8 g .. 8 g + 7 have no page
   __shared__ volatile int s_abort;
   __shared__ PartRing s_ring;
+  __shared__ Cursor<kTcKeys> s_cur;
+  __shared__ int s_late;  // the first sequence that a softmax warp gave up in
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   if (tid == 0) {
@@ -172,6 +176,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     }
     mbar_fence_init();
     s_abort = 0;
+    s_late = INT_MAX;
     s_ring.init(11);  // K, V, products, eight softmax warps
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
@@ -181,11 +186,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   prefetch_lengths<kTcThreads>(p);
   pdl_wait();
   tc_fence_before();
-  Cursor<kTcKeys> cur = find_share<kTcKeys, kTcThreads>(p);
+  find_share<kTcKeys, kTcThreads>(p, s_cur);
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   uint32_t n = 0;  // parts so far
-  int b = 0;       // their sequence
   bool ok = true;
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------------- K, V producers
@@ -209,7 +213,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     auto clear_rows = [&]() {
       if (z0 == 0 && z1 == kTcKeys) return;
       const uint32_t st = z_it % stages;
-      ok = warp_wait(&full[st], (z_it / stages) & 1);
+      ok = warp_wait(&full[st], (z_it / stages) & 1, p.wait_limit);
       for (int zr = lane >> 3; zr < kTcKeys; zr += 4)
         if (zr < z0 || zr >= z1)
 #pragma unroll
@@ -222,12 +226,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       z0 = 0;
       z1 = kTcKeys;
     };
+    ok = p.wait_limit > 0;
     for (; ok; ++n) {
-      ok = __all_sync(0xffffffffu, s_ring.ready(n));
+      ok = __all_sync(0xffffffffu, s_ring.ready(n, p.wait_limit));
       if (!ok) break;
       const Part w = s_ring.at(n);
       if (w.b < 0) break;
-      b = w.b;
       if (isV && w.begin == w.end) clear_rows();
       feed.start(p, w);
       for (int t = w.end - 1; t >= w.begin; --t, ++it) {
@@ -235,7 +239,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const int key = t * kTcKeys + row0;
         uint32_t bad8;
         const int page = feed.get(p, w, t, pg, bad8);
-        ok = warp_wait(&empty[st], ((it / stages) & 1) ^ 1) && !s_abort;
+        ok = warp_wait(&empty[st], ((it / stages) & 1) ^ 1, p.wait_limit) && !s_abort;
         if (!ok) break;
         if (lane == 0) {
           if (!isV) s_bad_pages[it % kBadRing] = bad8;
@@ -266,19 +270,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     // ------------------------------ the share's parts, and their Q rows
     uint32_t parts = 0;
     Part w;
-    if (p.merge && lane == 0) {
-      p.desc[share_index()] = make_int4(0, 0, 0, 0);
-      p.timeout[blockIdx.x] = 0;
-    }
+    Cursor<kTcKeys> cur = s_cur;
+    if (p.merge && lane == 0) p.desc[share_index()] = make_int4(0, 0, 0, 0);
     for (;; ++n) {
       const bool more = cur.next(p, w);
-      ok = s_ring.publish(n, w);
+      ok = s_ring.publish(n, w, p.wait_limit);
       if (!ok || !more) break;
-      b = w.b;
       if (p.merge && w.parts && lane == 0)
         p.desc[share_index()] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
       if (w.begin == w.end) continue;
-      ok = warp_wait(&bar_q_empty, (parts & 1) ^ 1) && !s_abort;
+      ok = warp_wait(&bar_q_empty, (parts & 1) ^ 1, p.wait_limit) && !s_abort;
       if (!ok) break;
       if (lane == 0) {
         const int nrb = w.ntok > nb ? 2 : 1;
@@ -329,15 +330,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         kst = kst == kKStages - 1 ? 0 : kst + 1;
       };
       for (; ok; ++n) {
-        ok = s_ring.ready(n);
+        ok = s_ring.ready(n, p.wait_limit);
         if (!ok) break;
         const Part w = s_ring.at(n);
         s_ring.done(n);
         if (w.b < 0) break;
-        b = w.b;
         const int T = w.end - w.begin, nrb = w.ntok > nb ? 2 : 1;
         if (T == 0) continue;
-        ok = mbar_wait(&bar_q_full, qph) && mbar_wait(&bar_k_full[kst], kph);
+        ok = wait_within(&bar_q_full, qph, p.wait_limit) && wait_within(&bar_k_full[kst], kph, p.wait_limit);
         if (!ok) break;
         qph ^= 1;
         tc_fence_after();
@@ -348,18 +348,18 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         for (int t = 0; t < T; ++t) {
           const int j0 = (w.end - 1 - t) * kTcKeys;
           const bool more = t + 1 < T;
-          ok = mbar_wait(&bar_v_full[vst], vph);
+          ok = wait_within(&bar_v_full[vst], vph, p.wait_limit);
           if (w.lo > j0 || w.hi < j0 + kTcKeys) {  // the V producer clears rows of this tile
-            ok = ok && mbar_wait(&bar_v_zero[vst], (zph >> vst) & 1);
+            ok = ok && wait_within(&bar_v_zero[vst], (zph >> vst) & 1, p.wait_limit);
             zph ^= 1u << vst;
           }
-          if (more) ok = ok && mbar_wait(&bar_k_full[kst], kph);
+          if (more) ok = ok && wait_within(&bar_k_full[kst], kph, p.wait_limit);
           for (int r = 0; ok && r < nrb; ++r) {
-            ok = mbar_wait(&bar_p_full[r][0], pph[r]);
+            ok = wait_within(&bar_p_full[r][0], pph[r], p.wait_limit);
             if (!ok) break;
             tc_fence_after();
             issue_pv(r, 0, t == 0);
-            ok = mbar_wait(&bar_p_full[r][1], pph[r]);
+            ok = wait_within(&bar_p_full[r][1], pph[r], p.wait_limit);
             if (!ok) break;
             pph[r] ^= 1;
             tc_fence_after();
@@ -386,7 +386,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (!mbar_wait(&bar_drain, 0)) s_abort = 1;
     }
     ok = __all_sync(0xffffffffu, ok);
-    b = __reduce_max_sync(0xffffffffu, b);
   } else {
     // -------------------------------------------------------------- softmax
     const int rb = warp >> 2, row = tid & (kRB - 1);
@@ -398,12 +397,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     // Rows left for an earlier share are announced while the next part's first tile is under way:
     // the fence before the announcement waits for their stores, some 4,000 cycles right behind them.
     int left = -1;
+    int b = s_cur.b;
     auto announce = [&]() {
       if (left >= 0) leave_rows(p, left, warp);
       left = -1;
     };
     for (; ok; ++n) {
-      ok = __all_sync(0xffffffffu, s_ring.ready(n));
+      ok = __all_sync(0xffffffffu, s_ring.ready(n, p.wait_limit));
       if (!ok) break;
       const Part& w = s_ring.at(n);  // (stays in shared memory: the tiles need the registers)
       if (w.b < 0) break;
@@ -458,7 +458,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (c == 3) vis[3] = v;
           }
         }
-        ok = warp_wait(&bar_s_full[rb], sc & 1);
+        ok = warp_wait(&bar_s_full[rb], sc & 1, p.wait_limit);
         if (!ok) break;
         if (!warp_works) {
           if (lane == 0) {
@@ -623,7 +623,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const float2 pa = fadd2(fadd2(ps[0], ps[1]), fadd2(ps[2], ps[3]));
         l_run += pa.x + pa.y;
       }
-      if (ok) ok = warp_wait(&bar_o_done[rb], oc & 1);
+      if (ok) ok = warp_wait(&bar_o_done[rb], oc & 1, p.wait_limit);
       if (!ok) break;
       ++oc;
       tc_fence_after();
@@ -720,13 +720,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (lane == 0) s_ring.done(n);
     }
     announce();
+    if (!ok && lane == 0) atomicMin(&s_late, b);  // (what other roles did not do, these warps waited for)
   }
-  if (!ok) {
-    s_abort = 1;
-    if (lane == 0) report_timeout(p, b);
-  }
+  if (!ok) s_abort = 1;
   tc_fence_before();
   __syncthreads();  // every role is done; TMA and MMA work has retired
+  if (tid == 0 && s_late != INT_MAX) report_late(p, s_cur, s_late);
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 

@@ -681,8 +681,13 @@ extern "C" tv_status tv_accept_greedy_noalloc(const float* logits, const int32_t
 }
 
 // ---------------------------------------------------------------------------
-// Test hook: the reporting limit of tv_accept_greedy's chunk-copy waits on the
-// current device (see the header).
+// Test hook: the reporting limit of tv_accept_greedy's chunk-copy waits and of
+// tv_attn_paged's waits on the current device (see the header).
+namespace tv {
+namespace paged {
+void set_wait_limit(long long cycles);  // tv_attn_paged.cu
+}
+}  // namespace tv
 extern "C" tv_status tv_debug_set_wait_limit(long long cycles) {
   if (cycles < 0 && cycles != TV_WAIT_LIMIT_DEFAULT) return TV_ERR_INVALID_ARG;
   const long long v = (cycles == TV_WAIT_LIMIT_DEFAULT) ? tv::sm100::kWaitLimitCycles : cycles;
@@ -690,5 +695,6 @@ extern "C" tv_status tv_debug_set_wait_limit(long long cycles) {
     (void)cudaGetLastError();
     return TV_ERR_CUDA;
   }
+  tv::paged::set_wait_limit(v);
   return TV_OK;
 }

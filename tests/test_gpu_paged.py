@@ -911,3 +911,32 @@ def test_capped_rows_do_not_depend_on_rows_past_the_unit(tv, lens, Hq, D):
         assert got[-1][2] == [0] * len(lens)
     for g in got[1:]:
         assert same_bits(g[0], got[0][0]) and torch.equal(g[1], got[0][1])
+
+
+# (small units, whole and merged; larger ones whole, merged, and joined by their CTAs; more sequences
+# than a CTA has threads)
+@pytest.mark.parametrize("lens", [[(90, 1), (0, 0), (128, 1)], [(300, 1), (0, 0), (2048, 1), (64, 1)],
+                                  [(50, 40), (9, 0), (120, 9)], [(300, 80), (7, 0), (2040, 9)],
+                                  [(700 + 40 * i, 64) for i in range(45)] + [(5, 0)],
+                                  [(60, 2)] * 450 + [(3, 0)], [(40, 20)] * 450])
+def test_a_wait_that_runs_out_is_reported(tv, lens):
+    """Failure detection without a fault: with a limit of 0 the tiles that a CTA waits for never come.
+    Every sequence with tokens says so, and no other; the next call is right."""
+    c = make(5, lens, 8, 2, 64, 16)
+    call = lambda: tv.attn_paged(c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_len"],  # noqa: E731
+                                 c["max_q"])
+    want = call()
+    torch.cuda.synchronize()
+    try:
+        assert tv.lib.tv_debug_set_wait_limit(0) == tv.TV_OK
+        late = call()
+        torch.cuda.synchronize()
+    finally:
+        assert tv.lib.tv_debug_set_wait_limit(tv.TV_WAIT_LIMIT_DEFAULT) == tv.TV_OK
+    assert np_(late[2]).tolist() == [tv.TV_ERR_TIMEOUT if n else 0 for _, n in lens]
+    got = call()
+    torch.cuda.synchronize()
+    assert np_(got[2]).tolist() == [0] * len(lens)
+    assert same_bits(got[0], want[0]) and torch.equal(got[1], want[1])
+    if tv.CHECKED:  # (this build records the site of a wait that gave up)
+        tv.check_take()
