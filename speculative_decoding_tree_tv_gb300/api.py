@@ -473,8 +473,10 @@ def expand_tree(draft_rows: Callable, root_key, child_key: Callable, topk: int, 
 # ---------------------------------------------------------------------------
 _CACHE_DTYPES = {torch.bfloat16: TV_BF16, torch.float16: TV_FP16}
 _pack_cache = struct.Struct(PAGED_CACHE_FORMAT).pack
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (what torch.cuda.current_stream and current_device ask, without the objects that they make of it;
+# a torch without these private names is asked by the public ones)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 
 

@@ -155,3 +155,20 @@ def test_plain_page_map_keeps_every_page_once(seed):
             assert all((s < 0) == (status[b] != 0) for s in mine)
     _, status, n_free = page_map_ref([0] * (B + 1), [0] * B, table, held, free, n_free, page, 0)
     assert n_free == pool and status == [0] * B
+
+
+def test_a_torch_without_the_private_names(tvlib):
+    """The package imports, and takes stream and device by torch's public names."""
+    import os
+    import subprocess
+    import sys
+    code = ("import torch\n"
+            "for name in ('_cuda_getCurrentRawStream', '_cuda_getDevice'):\n"
+            "    if hasattr(torch._C, name): delattr(torch._C, name)\n"
+            "from speculative_decoding_tree_tv_gb300 import api\n"
+            "class Stream: cuda_stream = 77\n"
+            "torch.cuda.current_stream = lambda device=None: Stream\n"
+            "assert api._raw_stream(0) == 77 and api._current_device is torch.cuda.current_device\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))), timeout=300)
+    assert r.returncode == 0, r.stderr
