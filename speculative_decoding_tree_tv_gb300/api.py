@@ -492,6 +492,11 @@ def _call(fn, name: str, dev: torch.device, *args) -> None:
         raise TVError(name, code)
 
 
+def _same_strides(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Of two tensors of one shape; strides of extent-one dimensions say nothing."""
+    return all(n < 2 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride()))
+
+
 def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> bytes:
     """tv_paged_cache of k_pages, v_pages [num_pages, Hkv, page_size, D]: any
     strides with D contiguous, the same for both (a [num_pages, page_size, Hkv, D]
@@ -516,11 +521,15 @@ def _cache(k_pages: torch.Tensor, v_pages: torch.Tensor) -> bytes:
         raise TypeError(f"v_pages must be {k_pages.dtype}, got {v_pages.dtype}")
     if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must both be [num_pages, Hkv, page_size, D]")
-    if k_pages.stride() != v_pages.stride():
+    if not _same_strides(k_pages, v_pages):
         raise ValueError("k_pages and v_pages must have the same strides")
     if v_pages.device != k_pages.device:
         raise ValueError(f"v_pages is on {v_pages.device}, expected {k_pages.device}")
-    raise ValueError("the last dimension of k_pages and v_pages must be contiguous")
+    if k_pages.stride(3) != 1:
+        raise ValueError("the last dimension of k_pages and v_pages must be contiguous")
+    n, Hkv, page, D = k_pages.shape
+    return _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.stride()[:3], n, page, Hkv, D,
+                       _CACHE_DTYPES[k_pages.dtype])
 
 
 def _need_rows(t: torch.Tensor, name: str, dtype, shape, device):
@@ -619,7 +628,8 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
             raise ValueError("slots must have shape [T]")
         _need_rows(k, "k", dtype, (T, Hkv, D), dev)
         _need_rows(v, "v", dtype, (T, Hkv, D), dev)
-        raise ValueError("k and v must have the same strides")
+        if not _same_strides(k, v):
+            raise ValueError("k and v must have the same strides")
     if status is not None:
         _need(status, "status", _I32, (T,), dev)
     _call(lib.tv_paged_append, "tv_paged_append", dev, k.data_ptr(), v.data_ptr(), strides[0],

@@ -940,3 +940,27 @@ def test_a_wait_that_runs_out_is_reported(tv, lens):
     assert same_bits(got[0], want[0]) and torch.equal(got[1], want[1])
     if tv.CHECKED:  # (this build records the site of a wait that gave up)
         tv.check_take()
+
+
+def test_strides_of_extent_one_may_differ(tv):
+    """One token from two projections, and a cache of one page whose K and V are cut from different pools."""
+    g = torch.Generator().manual_seed(2)
+    randn = lambda *s: torch.randn(*s, generator=g).bfloat16().to("cuda:0")  # noqa: E731
+    qkv, v = randn(1, 12, 64), randn(1, 2, 64)
+    k = qkv[:, 8:10]
+    pool = randn(3, 2, 2, 16, 64)
+    kp, vp = pool[1:2, 0], randn(1, 2, 16, 64)
+    assert k.stride() != v.stride() and kp.stride() != vp.stride()
+    tv.paged_append(k, v, torch.tensor([5], device="cuda:0"), kp, vp)
+    out, lse, status = tv.attn_paged(qkv[:, :8], kp, vp, i32([[0]]), i32([0, 1]), i32([5]), 1)
+    c = dict(lens=[(5, 1)], rows=[tuple(x[0, :, :6].transpose(0, 1).cpu() for x in (kp, vp))], q=qkv[:, :8], anc=None)
+    torch.cuda.synchronize()
+    assert torch.equal(kp[0, :, 5], k[0]) and torch.equal(vp[0, :, 5], v[0]) and int(status) == 0
+    check_attn(out, lse, attn_ref(c, 8, 2, 64), "bf16")
+    with pytest.raises(ValueError, match="same strides"):
+        tv.paged_append(qkv.repeat(2, 1, 1)[:, 8:10], v.repeat(2, 1, 1), torch.tensor([5, 6], device="cuda:0"), kp, vp)
+    with pytest.raises(ValueError, match="contiguous"):
+        wide = randn(1, 2, 16, 128)[..., ::2]
+        tv.paged_append(k, v, torch.tensor([5], device="cuda:0"), wide, wide)
+    with pytest.raises(ValueError, match="contiguous"):
+        tv.paged_append(randn(1, 2, 128)[..., ::2], v, torch.tensor([5], device="cuda:0"), kp, vp)
