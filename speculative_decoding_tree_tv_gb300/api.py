@@ -588,7 +588,9 @@ def page_map(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Ten
         _need(q_start, "q_start", _I32, (B + 1,), dev)
         _need(kv_len, "kv_len", _I32, (B,), dev)
         _need(n_pages, "n_pages", _I32, (B,), dev)
-        _need(free_list, "free_list", _I32, (free_list.numel(),), dev)
+        _need(free_list, "free_list", _I32, None, dev)
+        if free_list.dim() != 1:
+            raise ValueError(f"free_list must have shape [num_pages], got {tuple(free_list.shape)}")
         _need(n_free, "n_free", _I32, (1,), dev)
     if slots is None:
         slots = torch.empty(tokens, dtype=_I64, device=dev)

@@ -964,3 +964,11 @@ def test_strides_of_extent_one_may_differ(tv):
         tv.paged_append(k, v, torch.tensor([5], device="cuda:0"), wide, wide)
     with pytest.raises(ValueError, match="contiguous"):
         tv.paged_append(randn(1, 2, 128)[..., ::2], v, torch.tensor([5], device="cuda:0"), kp, vp)
+
+
+def test_page_map_refuses_other_free_lists(tv):
+    z = i32([0])
+    for free, err in (([0, 1], TypeError), (i32([[0, 1]]), ValueError), (torch.zeros(2, device="cuda:0"), TypeError),
+                      (torch.zeros(2, dtype=torch.int32), ValueError)):
+        with pytest.raises(err, match="free_list"):
+            tv.page_map(i32([0, 0]), z, i32([[0]]), z, free, z, 16, 0)
