@@ -660,10 +660,10 @@ tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, in
  *                 the window reaches (its keys count as hidden);
  *               or TV_ERR_TIMEOUT for the sequences with tokens whose rows may be missing, as
  *               a wait gave up (some beside them in the batch may be named too).
- *   workspace   tv_attn_paged_workspace_size() bytes, 256-byte aligned, any
- *               contents; calls that share one must not run concurrently.  After
- *               TV_ERR_TIMEOUT its contents are to be overwritten before a captured call
- *               that uses it is replayed.
+ *   workspace   tv_attn_paged_workspace_size() bytes (which the current device's SMs
+ *               decide), 256-byte aligned, any contents; calls that share one must not
+ *               run concurrently.  After TV_ERR_TIMEOUT its contents are to be overwritten
+ *               before a captured call that uses it is replayed.
  * Cache rows that no token sees may hold anything, NaN included; a row of V seen
  * by one token of a chunk and not by another must be finite.
  * Supported: D 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 128, B <= 4096, T * Hq and

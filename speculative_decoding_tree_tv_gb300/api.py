@@ -553,8 +553,12 @@ def _table_shape(block_table: torch.Tensor):
     return block_table.shape
 
 
-def attn_paged_workspace_size(max_q, Hq, Hkv, D) -> int:
-    return int(lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D))
+def attn_paged_workspace_size(max_q, Hq, Hkv, D, device=None) -> int:
+    """Bytes of attn_paged's workspace on `device` (the current one): it has room for each SM."""
+    if device is None or torch.device(device).index in (None, _current_device()):
+        return int(lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D))
+    with torch.cuda.device(device):
+        return int(lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D))
 
 
 def page_map(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor,
@@ -695,8 +699,9 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     else:
         _need(status, "status", _I32, (B,), dev)
     if ws is None:  # from torch's allocator: ordered by stream, and a captured graph's own
-        ws = torch.empty(lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D), dtype=torch.uint8,
-                         device=dev)
+        size = (lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D) if dev.index == _current_device()
+                else attn_paged_workspace_size(max_q, Hq, Hkv, D, dev))
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
         _need(ws, "ws", torch.uint8, None, dev)
     _call(lib.tv_attn_paged, "tv_attn_paged", dev, q.data_ptr(), strides[0], strides[1], cache,

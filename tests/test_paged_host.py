@@ -172,3 +172,25 @@ def test_a_torch_without_the_private_names(tvlib):
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))), timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+def test_the_workspace_is_sized_for_its_device(tvlib, monkeypatch):
+    import torch
+    from speculative_decoding_tree_tv_gb300 import api
+    inside = []
+
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            inside.append(self.device)
+
+        def __exit__(self, *_):
+            inside.pop()
+
+    monkeypatch.setattr(api, "_current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(api.lib, "tv_attn_paged_workspace_size", lambda *a: 100 + len(inside))
+    assert [tvlib.attn_paged_workspace_size(1, 8, 2, 64, d) for d in (None, "cuda:0", "cuda", "cuda:1")] == \
+        [100, 100, 100, 101]
