@@ -51,6 +51,15 @@ __device__ __forceinline__ int first_above(const int* a, int n, int x) {
   return lo;
 }
 
+// The sequence that token t belongs to, or n: end[b] is one past sequence b's last token (its first
+// where its range is malformed), ascending unless q_start descends somewhere; then all are looked at.
+__device__ __forceinline__ int owner_of(const int* end, const int32_t* q_start, int n, int t, bool descends) {
+  if (!descends) return first_above(end, n, t);
+  int b = 0;
+  while (b < n && !(__ldg(q_start + b) >= 0 && t >= __ldg(q_start + b) && t < end[b])) ++b;
+  return b;
+}
+
 __device__ __forceinline__ long long slot_of(int page, int pos, int shift, int num_pages) {
   return (page >= 0 && page < num_pages)
              ? ((long long)page << shift) + (pos & ((1 << shift) - 1)) : -1ll;
@@ -73,9 +82,11 @@ __global__ void __launch_bounds__(1024) page_map_kernel(const PageMapParams p) {
   if (tid == 0) s_taken = 0;
   const int n_free = *(volatile const int32_t*)p.n_free;
   int2 sum = make_int2(0, 0);
+  bool falls = false;
   for (int b = b0; b < b1; ++b) {
     int t0, n;
     const bool range = seq_range(p.q_start, b, p.T, t0, n);
+    falls |= t0 > __ldg(p.q_start + b + 1);
     const int kv = __ldg(p.kv_len + b), held = *(volatile const int32_t*)(p.n_pages + b);
     const long long want = ((long long)kv + n + (1 << p.shift) - 1) >> p.shift;
     const bool ok = range && kv >= 0 && held >= 0 && held <= p.P && want <= p.P;
@@ -100,7 +111,7 @@ __global__ void __launch_bounds__(1024) page_map_kernel(const PageMapParams p) {
     }
   }
   if (lane == 31) s_warp[warp] = inc;
-  __syncthreads();
+  const bool descends = __syncthreads_or(falls);
   int2 base = make_int2(inc.x - sum.x, inc.y - sum.y), total = make_int2(0, 0);
   for (int w = 0; w < nt / 32; ++w) {
     if (w < warp) {
@@ -180,7 +191,7 @@ __global__ void __launch_bounds__(1024) page_map_kernel(const PageMapParams p) {
   }
   if (!p.map_slots) return;
   for (int t = g0; t < p.T; t += gs) {
-    const int b = first_above(s_end, p.B, t);
+    const int b = owner_of(s_end, p.q_start, p.B, t, descends);
     long long slot = -1;
     if (!bad && b < p.B && s_kv[b] >= 0) {
       const int first = __ldg(p.q_start + b);
@@ -206,17 +217,19 @@ __global__ void __launch_bounds__(kSlotThreads) page_slots_kernel(const PageMapP
   int* s_end = s_dyn;
   pdl_trigger();
   pdl_wait();
+  bool falls = false;
   for (int b = threadIdx.x; b < p.B; b += kSlotThreads) {
     int t0, n;
     s_end[b] = seq_range(p.q_start, b, p.T, t0, n) ? t0 + n : t0;
+    falls |= t0 > __ldg(p.q_start + b + 1);
   }
-  __syncthreads();
+  const bool descends = __syncthreads_or(falls);
   const int base = blockIdx.x * kSlotTokens + threadIdx.x;
 #pragma unroll
   for (int u = 0; u < kSlotTokens / kSlotThreads; ++u) {
     const int t = base + u * kSlotThreads;
     if (t >= p.T) return;
-    const int b = first_above(s_end, p.B, t);
+    const int b = owner_of(s_end, p.q_start, p.B, t, descends);
     long long slot = -1;
     if (b < p.B && __ldg(p.status + b) == TV_OK) {
       const int first = __ldg(p.q_start + b);

@@ -972,3 +972,13 @@ def test_page_map_refuses_other_free_lists(tv):
                       (torch.zeros(2, dtype=torch.int32), ValueError)):
         with pytest.raises(err, match="free_list"):
             tv.page_map(i32([0, 0]), z, i32([[0]]), z, free, z, 16, 0)
+
+
+@pytest.mark.parametrize("T", [40, 20000])
+def test_page_map_serves_sequences_behind_a_descent(tv, T):
+    """Sequence 1 descends; the tokens of those behind it belong to them alone and get their slots."""
+    B, P, page = 6, 8, 16
+    pool = Pool(4, B, P, 44, page)
+    pool.step(tv, starts([20] * B), [0] * B, 120)
+    assert pool.step(tv, [20, 30, 5, 10, 12, 12, 19], [20, 7, 20, 90, 3, 33], T) == [0, 1, 0, 0, 0, 0]
+    assert pool.step(tv, [T - 3, T, 0, 2, 1, 9, 9], [20] * B, T) == [0, 1, 0, 1, 0, 0]
