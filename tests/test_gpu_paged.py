@@ -982,3 +982,65 @@ def test_page_map_serves_sequences_behind_a_descent(tv, T):
     pool.step(tv, starts([20] * B), [0] * B, 120)
     assert pool.step(tv, [20, 30, 5, 10, 12, 12, 19], [20, 7, 20, 90, 3, 33], T) == [0, 1, 0, 0, 0, 0]
     assert pool.step(tv, [T - 3, T, 0, 2, 1, 9, 9], [20] * B, T) == [0, 1, 0, 1, 0, 0]
+
+
+@pytest.mark.parametrize("N", [5, 40])
+def test_verify_steps_as_a_replayed_graph(tv, N):
+    """The whole step (tree, page map, append, attention, acceptance, commit, the next lengths) captured once
+    and replayed on new inputs in the same buffers: every bit as in eager steps."""
+    B, Hq, Hkv, D, page, V, P, pool = 3, 8, 2, 128, 16, 300, 9, 24
+    g, rng = torch.Generator().manual_seed(N), random.Random(N)
+    randn = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to("cuda:0")  # noqa: E731
+    free = list(range(pool))
+    rng.shuffle(free)
+
+    def state():
+        return dict(kp=torch.zeros(pool, Hkv, page, D, dtype=torch.bfloat16, device="cuda:0"),
+                    vp=torch.zeros(pool, Hkv, page, D, dtype=torch.bfloat16, device="cuda:0"),
+                    table=i32([[-1] * P] * B), held=i32([0] * B), free=i32(free), n_free=i32([pool]),
+                    kv_len=i32([0] * B), q_start=i32(starts([N] * B)))
+
+    def inputs():
+        parent = [[-1] + [rng.randrange(max(0, i - 4), i) for i in range(1, N)] for _ in range(B)]
+        logits = torch.randn(B, N, V, generator=g)
+        tokens = torch.randint(0, V, (B, N), generator=g, dtype=torch.int32)
+        for b in range(B):  # the target agrees with a branch
+            node = rng.randrange(N)
+            while node > 0:
+                logits[b, parent[b][node], int(tokens[b, node])] = 50.0
+                node = parent[b][node]
+        return dict(q=randn(B * N, Hq, D), k=randn(B * N, Hkv, D), v=randn(B * N, Hkv, D), parent=i32(parent),
+                    logits=logits.to("cuda:0"), tokens=tokens.to("cuda:0"))
+
+    def step(s, x):
+        depth, anc, st0 = tv.tree_build(x["parent"])
+        slots, st1 = tv.page_map(s["q_start"], s["kv_len"], s["table"], s["held"], s["free"], s["n_free"], page, B * N)
+        tv.paged_append(x["k"], x["v"], slots, s["kp"], s["vp"])
+        out, lse, st2 = tv.attn_paged(x["q"], s["kp"], s["vp"], s["table"], s["q_start"], s["kv_len"], N,
+                                      anc_mask=anc.view(B * N, -1))
+        acc = tv.accept_greedy(x["logits"], x["tokens"], x["parent"], depth)
+        new_len, st3 = tv.commit_paged(s["kp"], s["vp"], s["table"], s["kv_len"], acc["path"], acc["accept_len"])
+        s["kv_len"].copy_(new_len)
+        return out, lse, slots, acc["accept_len"], torch.stack([st0, st1, st2, st3])
+
+    a, b, buf = state(), state(), inputs()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        step(state(), buf)  # (the workspaces that are kept)
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        got = step(b, buf)
+    moved = 0
+    for _ in range(6):
+        x = inputs()
+        want = step(a, x)
+        for name, t in x.items():
+            buf[name].copy_(t)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert not bool(want[4].any()) and all(torch.equal(p, q) for p, q in zip(want, got))
+        assert all(torch.equal(a[n], b[n]) for n in a)
+        moved += int(want[3].sum())
+    assert moved > 0
