@@ -478,6 +478,13 @@ _pack_cache = struct.Struct(PAGED_CACHE_FORMAT).pack
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _stream
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_MOST = 2**31 - 1  # of an int argument: ctypes would pass a larger one's lower 32 bits
+
+
+def _fits(**sizes) -> None:
+    for name, n in sizes.items():
+        if not 0 <= n <= _MOST:
+            raise ValueError(f"{name} must be from 0 to 2^31 - 1, got {n}")
 
 
 def _call(fn, name: str, dev: torch.device, *args) -> None:
@@ -574,7 +581,7 @@ def page_map(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Ten
     try:
         (B, P), dev, pool = block_table.shape, block_table.device, free_list.shape[0]
         row, one = (B,), (1,)
-        good = (block_table.dtype is _I32 and block_table.is_contiguous() and block_table.is_cuda
+        good = (P <= _MOST and 0 <= tokens <= _MOST and 0 <= page_size <= _MOST and block_table.dtype is _I32 and block_table.is_contiguous() and block_table.is_cuda
                 and q_start.dtype is _I32 and q_start.shape == (B + 1,) and q_start.device == dev
                 and q_start.is_contiguous()
                 and kv_len.dtype is _I32 and kv_len.shape == row and kv_len.device == dev
@@ -596,6 +603,7 @@ def page_map(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Ten
         if free_list.dim() != 1:
             raise ValueError(f"free_list must have shape [num_pages], got {tuple(free_list.shape)}")
         _need(n_free, "n_free", _I32, (1,), dev)
+        _fits(tokens=tokens, page_size=page_size, P=P)
     if slots is None:
         slots = torch.empty(tokens, dtype=_I64, device=dev)
     else:
@@ -622,7 +630,7 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
     try:
         T = slots.numel()
         shape, strides = (T, Hkv, D), k.stride()
-        good = (slots.dtype is _I64 and slots.shape == (T,) and slots.device == dev
+        good = (T <= _MOST and slots.dtype is _I64 and slots.shape == (T,) and slots.device == dev
                 and slots.is_contiguous() and k.shape == shape and v.shape == shape
                 and k.dtype is dtype and v.dtype is dtype and k.device == dev and v.device == dev
                 and v.stride() == strides and strides[2] == 1)
@@ -636,6 +644,7 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
         _need_rows(v, "v", dtype, (T, Hkv, D), dev)
         if not _same_strides(k, v):
             raise ValueError("k and v must have the same strides")
+        _fits(T=T)
     if status is not None:
         _need(status, "status", _I32, (T,), dev)
     _call(lib.tv_paged_append, "tv_paged_append", dev, k.data_ptr(), v.data_ptr(), strides[0],
@@ -662,7 +671,7 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     max_q = int(max_q)
     try:
         (T, Hq, D), (B, P), strides = q.shape, block_table.shape, q.stride()
-        good = (D == Dc and q.dtype is dtype and q.device == dev and strides[2] == 1
+        good = (T <= _MOST and P <= _MOST and 0 <= max_q <= _MOST and D == Dc and q.dtype is dtype and q.device == dev and strides[2] == 1
                 and block_table.dtype is _I32 and block_table.device == dev
                 and block_table.is_contiguous()
                 and q_start.dtype is _I32 and q_start.shape == (B + 1,) and q_start.device == dev
@@ -676,9 +685,12 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be a tensor [T, Hq, D]")
         _need_rows(q, "q", dtype, (T, Hq, Dc), dev)
+        _fits(T=T, P=P, max_q=max_q)
         _need(block_table, "block_table", _I32, None, dev)
         _need(q_start, "q_start", _I32, (B + 1,), dev)
         _need(kv_len, "kv_len", _I32, (B,), dev)
+    if window > _MOST:  # (positions are below it: nothing is hidden)
+        window = 0
     if anc_mask is not None:
         _need(anc_mask, "anc_mask", _I64, None, dev)
         W = (max_q + 63) // 64
@@ -724,7 +736,7 @@ def commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torc
     try:
         (B, P), N = block_table.shape, path.shape[1]
         row = (B,)
-        good = (block_table.dtype is _I32 and block_table.device == dev
+        good = (P <= _MOST and N <= _MOST and block_table.dtype is _I32 and block_table.device == dev
                 and block_table.is_contiguous()
                 and path.dtype is _I32 and path.shape == (B, N) and path.device == dev
                 and path.is_contiguous()
@@ -740,6 +752,7 @@ def commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torc
         _need(path, "path", _I32, None, dev)
         if path.dim() != 2 or path.shape[0] != B:
             raise ValueError(f"path must have shape [B, N] with B = {B}")
+        _fits(P=P, N=path.shape[1])
         _need(kv_len, "kv_len", _I32, (B,), dev)
         _need(accept_len, "accept_len", _I32, (B,), dev)
     if new_kv_len is None:

@@ -1044,3 +1044,23 @@ def test_verify_steps_as_a_replayed_graph(tv, N):
         assert all(torch.equal(a[n], b[n]) for n in a)
         moved += int(want[3].sum())
     assert moved > 0
+
+
+def test_sizes_past_an_int_are_not_cut(tv):
+    """No argument loses its upper bits on the way to the library."""
+    c = make(1, [(40, 3)], 4, 2, 64, 16)
+    want = run(tv, c)
+    for window in (2**31, 2**32 + 5, 2**63 - 1):
+        got = run(tv, c, window=window)
+        assert same_bits(got[0], want[0]) and torch.equal(got[1], want[1])
+    wide = torch.zeros((0, 2**32 + 4), dtype=torch.int32, device="cuda:0")
+    z = i32([0])
+    for bad in (lambda: tv.page_map(i32([0, 0]), z, c["table"], z, z, z, 16, 2**32),
+                lambda: tv.page_map(i32([0, 0]), z, c["table"], z, z, z, 16, -1),
+                lambda: tv.page_map(i32([0, 0]), z, c["table"], z, z, z, 2**32 + 16, 0),
+                lambda: tv.page_map(i32([0]), z[:0], wide, z[:0], z, z, 16, 0),
+                lambda: tv.attn_paged(c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_len"], 2**32 + 3),
+                lambda: tv.attn_paged(c["q"], c["k"], c["v"], wide, i32([0]), z[:0], 3),
+                lambda: tv.commit_paged(c["k"], c["v"], wide, z[:0], wide[:, :3].contiguous(), z[:0])):
+        with pytest.raises(ValueError, match="2\\^31"):
+            bad()
