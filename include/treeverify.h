@@ -22,8 +22,8 @@
  *   tv_select_topn    best children of the frontier) and its subtree
  *                     selection (the n best nodes of the candidate tree)
  *
- * and the same pass over a paged KV cache, with ragged batches (a tree, a
- * chunk of a prompt or a single token per sequence):
+ * and the same pass over a paged KV cache, with ragged batches (sequences of
+ * their own lengths, each with a tree, or with a chunk of a prompt or a token):
  *
  *   tv_page_map       block tables and slot maps from the sequences' lengths
  *   tv_paged_append   new K/V rows into their slots
@@ -594,12 +594,14 @@ typedef struct {
  * reports TV_ERR_NO_PAGES.  So a step's call after a commit returns what
  * the rejected branches held, and kv_len[b] = n_b = 0 releases a sequence.
  * Table entries past n_pages[b] and list entries past n_free keep their values.
+ * A page that is held or free must be so once: one that two sequences hold (a
+ * common prefix) would go back twice, and then be handed out twice.
  * status[b] = TV_ERR_INVALID_ARG for a malformed q_start, kv_len[b] < 0,
  * n_pages[b] outside [0, P] or a target above P; the sequence then keeps its
  * pages.  An n_free outside [0, num_pages], or one that would pass num_pages with the pages
  * that come back, gives every sequence that status and changes nothing.
- * Requires 0 <= B <= 4096, B * P and T below 2^31.  One launch for up to 8192 tokens,
- * else two.  Sums are integers: the result depends on the inputs only.
+ * Requires 0 <= B <= 4096, and B * P, P * page_size and T + 1024 below 2^31.  One launch
+ * for up to 16384 tokens, else two.  Sums are integers: the result depends on the inputs only.
  */
 tv_status tv_page_map(const int32_t* q_start, const int32_t* kv_len, int B, int T, int P,
                       int page_size, int num_pages, int32_t* block_table, int32_t* n_pages,
@@ -616,7 +618,8 @@ tv_status tv_page_map(const int32_t* q_start, const int32_t* kv_len, int B, int 
  *           16-byte pieces may stay).
  *   status  int32 [T] out, may be NULL: 0, or TV_ERR_INVALID_ARG for a slot
  *           at or past num_pages * page_size (nothing is written).
- * D a multiple of 8 up to 1024.  k and v must not overlap the cache.
+ * D a multiple of 8 up to 1024, T * Hkv * D / 8 + 4096 at most 2^30.  k and v must
+ * not overlap the cache.
  */
 tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, int64_t head_stride,
                           const int64_t* slots, int T, const tv_paged_cache* cache,
@@ -624,7 +627,7 @@ tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, in
 
 /*
  * tv_attn_paged -- one attention layer for a ragged batch of new tokens over
- * a paged cache: a decode token, a chunk of a prompt or a draft tree per
+ * a paged cache: decode tokens and chunks of prompts in one call, or a draft tree per
  * sequence.  The new tokens' own K and V rows are in the cache already.
  *
  * For token t of sequence b (i = t - q_start[b]), query head h and its kv head
@@ -636,9 +639,10 @@ tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, in
  * are visible.  Tree (anc_mask given): prefix rows j < kv_len[b] and rows
  * kv_len[b] + a for the set bits a of the token's mask are visible, and a
  * node's pos is kv_len[b] + its depth (the number of its mask bits less one, 0 for an
- * empty mask; masks are those of tv_tree_build).  With window > 0 only rows with
- * pos(t) - pos(j) < window are visible.  A token that sees nothing gets out = 0, lse = -inf;
- * a NaN in a query row, or in a key that it sees, makes its out and lse NaN.
+ * empty mask).  Masks are those of tv_tree_build, for every sequence of the call: a decode
+ * token goes with trees as a tree of one node, a chunk as a chain.  With window > 0 only
+ * rows with pos(t) - pos(j) < window are visible.  A token that sees nothing gets out = 0,
+ * lse = -inf; a NaN in a query row, or in a key that it sees, makes its out and lse NaN.
  *
  *   q           [T, Hq, D] of the cache's type, 16-byte aligned; element strides
  *               q_token_stride, q_head_stride (multiples of 8), D contiguous.
@@ -650,7 +654,7 @@ tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, in
  *               chunks are served too, only more slowly (with anc_mask up to 64 W
  *               tokens).
  *   scale       0 selects 1/sqrt(D).
- *   out         [T, Hq, D], contiguous, 16-byte aligned; lse float [T, Hq], may be NULL.
+ *   out         [T, Hq, D], contiguous, 16-byte aligned, apart from q; lse float [T, Hq], may be NULL.
  *               Rows of tokens outside every sequence are left as they were.
  *   status      int32 [B] out, may be NULL: 0, or TV_ERR_INVALID_ARG for
  *               - a malformed q_start (the sequence's rows are left as they were);
@@ -666,8 +670,8 @@ tv_status tv_paged_append(const void* k, const void* v, int64_t token_stride, in
  *               before a captured call that uses it is replayed.
  * Cache rows that no token sees may hold anything, NaN included; a row of V seen
  * by one token of a chunk and not by another must be finite.
- * Supported: D 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 128, B <= 4096, T * Hq and
- * B * P below 2^31; max_q <= TV_MAX_NODES with anc_mask; positive strides, of the cache (in
+ * Supported: D 64 or 128, Hq % Hkv == 0, Hq / Hkv <= 128, B <= 4096, T * Hq, B * P and
+ * P * page_size + 512 below 2^31; max_q <= TV_MAX_NODES with anc_mask; positive strides, of the cache (in
  * the order of their size) and of q (token by head) each a multiple of the one before.
  */
 size_t tv_attn_paged_workspace_size(int max_q, int Hq, int Hkv, int D);
@@ -689,7 +693,7 @@ tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_st
  *               then left as it was and new_kv_len[b] = kv_len[b].
  * The pages past the new length stay with the sequence until tv_page_map.
  * Pages of the moved rows must belong to one sequence only.  D a multiple of 8 up
- * to 1024.
+ * to 1024; B * P, B * Hkv and P * page_size + 512 below 2^31.
  */
 tv_status tv_commit_paged(const tv_paged_cache* cache, const int32_t* block_table,
                           const int32_t* kv_len, const int32_t* path, const int32_t* accept_len,

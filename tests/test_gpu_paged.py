@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from _gpu_util import i32, np_
-from _paged_util import DTYPES, attn_ref, check_attn, make, page_map_ref
+from _paged_util import DTYPES, attn_ref, check_attn, make, page_map_ref, tree_masks
 
 pytestmark = pytest.mark.gpu
 
@@ -1064,3 +1064,32 @@ def test_sizes_past_an_int_are_not_cut(tv):
                 lambda: tv.commit_paged(c["k"], c["v"], wide, z[:0], wide[:, :3].contiguous(), z[:0])):
         with pytest.raises(ValueError, match="2\\^31"):
             bad()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(slopes=True, window=120)])
+def test_chunks_and_tokens_among_trees(tv, kw):
+    """In a call with masks a chunk is a chain and a decode token a tree of one node."""
+    kw = dict(kw)
+    if kw.get("slopes"):
+        kw["slopes"] = slopes_of(8)
+    lens = [(300, 64), (100, 130), (50, 1), (0, 40)]
+    c = make(3, lens, 8, 2, 64, 16, tree=True)
+    c["parents"][1] = list(range(-1, 129))
+    W = (130 + 63) // 64
+    words, c["depth"] = tree_masks(c["parents"], W)
+    c["anc"] = torch.tensor(words, dtype=torch.int64, device="cuda:0")
+    out, lse = agree(tv, c, 8, 2, 64, "bf16", **kw)
+    for b in (1, 2):  # as without masks
+        L, n = lens[b]
+        t = sum(m for _, m in lens[:b])
+        part = dict(c, lens=[lens[b]], rows=[c["rows"][b]], q=c["q"][t:t + n], anc=None)
+        check_attn(out[t:t + n], lse[t:t + n], attn_ref(part, 8, 2, 64, **kw), "bf16")
+
+
+@pytest.mark.parametrize("lens,tree", [([(300, 1), (5, 1), (900, 1)], False), ([(200, 80), (30, 3)], False),
+                                       ([(200, 20), (30, 3)], True)])
+def test_tables_as_wide_as_the_longest_permitted_sequence(tv, lens, tree):
+    """A server's block table: most of a row is never held."""
+    c = make(3, lens, 8, 2, 64, 16, tree=tree)
+    c["table"] = torch.nn.functional.pad(c["table"], (0, 8192), value=-1)
+    agree(tv, c, 8, 2, 64, "bf16")
