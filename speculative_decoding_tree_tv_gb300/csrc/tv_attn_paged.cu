@@ -210,7 +210,8 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
     // (a unit's fixed cost and one tile; one tree of 64 behind 2,000 keys 21.2, 22.2 and 23.1 us at 4, 5 and 6)
     pl.min_share = 4;
   }
-  // Units short enough for a CTA each (keys: the most a sequence can have) are not split, and
+  // Units short enough for a CTA each (keys: the most that the block table has room for, as the
+  // host knows no lengths; short sequences in a wide table are split) are not split, and
   // the merge is not launched: decode of 4 sequences of 500, 1,000 and 1,500 keys 8.9, 12.6 and 16.2 us,
   // split 11.2, 11.8 and 12.2 us (D 64: 1,000 keys 9.9 and 10.5 us; 16 rows: 13.5 and 14.1 us); 2 trees of 64
   // behind 200, 440 and 900 keys 14.3, 14.7 and 20.3 us, split 18.1, 18.9 and 19.5 us.

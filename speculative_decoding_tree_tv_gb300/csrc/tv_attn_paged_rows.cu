@@ -352,6 +352,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][e] *= corr[NR == 16 ? e >> 1 : e & 1];
         }
+        // P is rounded to the cache's type for the product (half a step: 2^-8 or 2^-11 of a probability); the
+        // sums took it as it was
         if (NR == 16) {  // O += P V
           const uint32_t pf[4] = {pack2<F16>(s[0], s[1]), pack2<F16>(s[2], s[3]), pack2<F16>(s[4], s[5]),
                                   pack2<F16>(s[6], s[7])};

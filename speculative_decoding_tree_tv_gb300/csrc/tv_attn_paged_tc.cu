@@ -5,7 +5,7 @@
 // its first: with a distance bias the scores fall that way, and the running maximum
 // stays (the other way it moves with every tile, and O is scaled each time: a chunk of 2048 behind 6,100
 // keys with slopes, now 178 us, went from 269 to 209 us by this alone).  Without slopes it takes
-// 159 us, 78 % of the measured matrix rate: a tile of 256 rows takes some 2,850 cycles, its products
+// 157 us, 79 % of the measured matrix rate: a tile of 256 rows takes some 2,850 cycles, its products
 // 2,550 at that rate, and what a CTA does once (start, changes of unit, joining) some 14 us.
 // 16 trees of 64 nodes stream their pages at 6.4 TB/s in the loop (75.6 us in all).  Warp roles:
 //   warps 0-3, 4-7  softmax of row block 0, 1: one thread per row (TMEM lane), 128 scores a
@@ -609,6 +609,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const float mm = m_run == -INFINITY ? 0.0f : m_run;  // nothing seen yet: 2^-inf = 0
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          // (rounded to the cache's type, the product's operand: half a step, 2^-8 or 2^-11 of a
+          // probability; the sums take them as they were)
           uint32_t pw[16];
           probs(c, mm, pw);
           tmem_st16(tS + lane_base + 16 * c, pw);
