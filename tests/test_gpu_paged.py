@@ -1093,3 +1093,57 @@ def test_tables_as_wide_as_the_longest_permitted_sequence(tv, lens, tree):
     c = make(3, lens, 8, 2, 64, 16, tree=tree)
     c["table"] = torch.nn.functional.pad(c["table"], (0, 8192), value=-1)
     agree(tv, c, 8, 2, 64, "bf16")
+
+
+@pytest.mark.parametrize("lens", [[(300, 1), (20, 1)], [(200, 80), (30, 3)], [(700 + 40 * i, 64) for i in range(45)]])
+def test_output_rows_between_sectors(tv, lens):
+    """out on a 16-byte boundary that is no 32-byte one, written into a larger buffer."""
+    c = make(3, lens, 8, 2, 64, 16)
+    want = tv.attn_paged(c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_len"], c["max_q"])[0]
+    flat = torch.full((want.numel() + 16,), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    out = flat[8:-8].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    tv.attn_paged(c["q"], c["k"], c["v"], c["table"], c["q_start"], c["kv_len"], c["max_q"], out=out)
+    torch.cuda.synchronize()
+    assert same_bits(out, want) and bool((flat[:8] == 7).all()) and bool((flat[-8:] == 7).all())
+
+
+@pytest.mark.parametrize("lens", [[(300, 1), (20, 1)], [(200, 80), (30, 3)]])
+def test_pages_inside_heads(tv, lens):
+    """A [heads, pages, rows, D] cache, the fourth order of the outer dimensions."""
+    c = make(3, lens, 8, 4, 128, 32)
+    for x in "kv":
+        c[x] = c[x].transpose(0, 1).contiguous().transpose(0, 1)
+    assert c["k"].stride(1) > c["k"].stride(0)
+    agree(tv, c, 8, 4, 128, "bf16")
+
+
+@pytest.mark.parametrize("lens", [[(300, 1), (20, 1)], [(200, 80), (30, 3)]])
+def test_tokens_before_the_first_sequence(tv, lens):
+    """q_start need not begin at 0: the tokens in front belong to nobody."""
+    c = make(3, lens, 8, 2, 64, 16)
+    front = 5
+    c["q"] = torch.cat([torch.full_like(c["q"][:1], float("nan")).repeat(front, 1, 1), c["q"]])
+    q_start = c["q_start"] + front
+    out = torch.full(c["q"].shape, 7.0, dtype=torch.bfloat16, device="cuda:0")
+    out, lse, status = tv.attn_paged(c["q"], c["k"], c["v"], c["table"], q_start, c["kv_len"], c["max_q"], out=out)
+    torch.cuda.synchronize()
+    assert np_(status).tolist() == [0] * len(lens) and bool((out[:front] == 7).all())
+    c["q"] = c["q"][front:]
+    check_attn(out[front:], lse[front:], attn_ref(c, 8, 2, 64), "bf16")
+
+
+@pytest.mark.parametrize("lens", [[(1500, 1), (40, 1)], [(700, 100)]])
+def test_negative_slopes(tv, lens):
+    """What lies far back weighs most: the maximum moves with every tile."""
+    c = make(6, lens, 4, 1, 64, 16)
+    agree(tv, c, 4, 1, 64, "bf16", slopes=-slopes_of(4))
+
+
+def test_the_most_sequences(tv):
+    rng = random.Random(1)
+    lens = [(rng.randint(0, 40), int(rng.random() < 0.8)) for _ in range(4096)]
+    c = make(1, lens, 2, 1, 64, 8, pad=3)
+    agree(tv, c, 2, 1, 64, "bf16")
+    pool = Pool(2, 4096, 6, 4096 * 6, 8)
+    pool.step(tv, starts([n for _, n in lens]), [L for L, _ in lens], c["T"])
