@@ -287,11 +287,14 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         if (MOD && p.softcap_log2 > 0.0f) {
           float f[kScores], top = 0.0f;
 #pragma unroll
-          for (int e = 0; e < kScores; ++e) {
-            const float x = s[e], w2 = x * x;
-            top = fmaxf(top, w2);
-            f[e] = x * fmaf(fmaf(fmaf(p.cap_q[3], w2, p.cap_q[2]), w2, p.cap_q[1]), w2, p.cap_q[0]);
-          }
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) {
+              const float x = s[at(r, i)], w2 = x * x;
+              const int j = j0 + key_of(i);  // (keys outside of the unit's range hold anything)
+              if (plain || (j >= w.lo && j < w.hi)) top = fmaxf(top, w2);
+              f[at(r, i)] = x * fmaf(fmaf(fmaf(p.cap_q[3], w2, p.cap_q[2]), w2, p.cap_q[1]), w2, p.cap_q[0]);
+            }
           const bool far = __any_sync(0xffffffffu, top > p.cap_top);
 #pragma unroll
           for (int e = 0; e < kScores; ++e) s[e] = far ? p.softcap_log2 * tanh_any(s[e] * cap_in2) : f[e];

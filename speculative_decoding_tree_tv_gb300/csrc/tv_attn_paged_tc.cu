@@ -509,9 +509,26 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               }
             }
           // a warp with a score past the cubic's range takes all again, through TMEM (which
-          // still holds them), to keep the code of this rare way small (rows past the unit hold
-          // anything, and have no say in it)
-          if (__any_sync(0xffffffffu, top > p.cap_top && tl < nb && rb * nb + tl < w.ntok)) {
+          // still holds them), to keep the code of this rare way small (rows past the unit and keys outside
+          // of its range hold anything, and have no say in it)
+          const bool is_row = tl < nb && rb * nb + tl < w.ntok;
+          bool far = __any_sync(0xffffffffu, top > p.cap_top && is_row);
+          if (far && (j0 < w.lo || j0 + kTcKeys > hi)) {
+            top = 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 8) {
+              uint32_t x[8];
+              tmem_ld8(tS + lane_base + c, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float y = __uint_as_float(x[e]);
+                if (j0 + c + e >= w.lo && j0 + c + e < hi) top = fmaxf(top, y * y);
+              }
+            }
+            far = __any_sync(0xffffffffu, top > p.cap_top && is_row);
+          }
+          if (far) {
             const float in = 2.0f * kLog2e * p.cap_in;
 #pragma unroll 1
             for (int c = 0; c < 128; c += 8) {

@@ -1147,3 +1147,27 @@ def test_the_most_sequences(tv):
     agree(tv, c, 2, 1, 64, "bf16")
     pool = Pool(2, 4096, 6, 4096 * 6, 8)
     pool.step(tv, starts([n for _, n in lens]), [L for L, _ in lens], c["T"])
+
+
+@pytest.mark.parametrize("lens", [[(300, 1), (75, 1), (1000, 1)], [(70, 1), (30, 1)], [(90, 2), (700, 1)],
+                                  [(200, 37), (500, 33)], [(70, 9), (3000, 40)]])
+@pytest.mark.parametrize("Hq,D", [(8, 64), (16, 128)])
+@pytest.mark.parametrize("window", [0, 41])
+def test_capped_rows_do_not_depend_on_rows_nobody_sees(tv, lens, Hq, D, window):
+    """What cache rows behind a sequence's end and in front of its window hold changes no bit."""
+    got = []
+    for fill in (0.0, 1000.0, float("nan")):
+        c = make(3, lens, Hq, 2, D, 16)
+        for x in "kv":
+            c[x] = torch.where(c[x].isnan(), torch.full_like(c[x], fill), c[x])
+        if window:
+            table = np_(c["table"])
+            for b, (L, n) in enumerate(lens):
+                for j in range(max(0, L - window + 1)):
+                    c["k"][table[b, j // 16], :, j % 16] = fill
+                    c["v"][table[b, j // 16], :, j % 16] = fill
+        got.append(run(tv, c, softcap=9.0, window=window))
+        assert got[-1][2] == [0] * len(lens)
+    assert bool(torch.isfinite(got[0][0]).all())
+    for g in got[1:]:
+        assert same_bits(g[0], got[0][0]) and torch.equal(g[1], got[0][1])
