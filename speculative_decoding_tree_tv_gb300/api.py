@@ -581,7 +581,8 @@ def page_map(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Ten
     try:
         (B, P), dev, pool = block_table.shape, block_table.device, free_list.shape[0]
         row, one = (B,), (1,)
-        good = (P <= _MOST and 0 <= tokens <= _MOST and 0 <= page_size <= _MOST and block_table.dtype is _I32 and block_table.is_contiguous() and block_table.is_cuda
+        good = (P <= _MOST and 0 <= tokens <= _MOST and 0 <= page_size <= _MOST
+                and block_table.dtype is _I32 and block_table.is_contiguous() and block_table.is_cuda
                 and q_start.dtype is _I32 and q_start.shape == (B + 1,) and q_start.device == dev
                 and q_start.is_contiguous()
                 and kv_len.dtype is _I32 and kv_len.shape == row and kv_len.device == dev
@@ -671,7 +672,8 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     max_q = int(max_q)
     try:
         (T, Hq, D), (B, P), strides = q.shape, block_table.shape, q.stride()
-        good = (T <= _MOST and P <= _MOST and 0 <= max_q <= _MOST and D == Dc and q.dtype is dtype and q.device == dev and strides[2] == 1
+        good = (T <= _MOST and P <= _MOST and 0 <= max_q <= _MOST
+                and D == Dc and q.dtype is dtype and q.device == dev and strides[2] == 1
                 and block_table.dtype is _I32 and block_table.device == dev
                 and block_table.is_contiguous()
                 and q_start.dtype is _I32 and q_start.shape == (B + 1,) and q_start.device == dev
@@ -736,7 +738,8 @@ def commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torc
     try:
         (B, P), N = block_table.shape, path.shape[1]
         row = (B,)
-        good = (P <= _MOST and N <= _MOST and block_table.dtype is _I32 and block_table.device == dev
+        good = (P <= _MOST and N <= _MOST
+                and block_table.dtype is _I32 and block_table.device == dev
                 and block_table.is_contiguous()
                 and path.dtype is _I32 and path.shape == (B, N) and path.device == dev
                 and path.is_contiguous()

@@ -149,8 +149,8 @@ __device__ __forceinline__ void tma_load_rows(void* dst, const CUtensorMap* map,
   const int c3 = row_dim == 3 ? row : head_dim == 3 ? head : page;
   tma_load_4d(dst, map, bar, d0, c1, c2, c3);
 }
-// A wait that gives up after `limit` SM cycles.  (The limit is looked at where a barrier is not ready:
-// a branch or another test ahead of it cost a chunk of 2048 6 us and biased prompts 0.7 us.)
+// A wait that gives up after `limit` SM cycles.  (The limit is looked at where a barrier is not ready: a
+// chunk of 2048 157 us, with a branch on it ahead of every wait 166.5 us.)
 __device__ __forceinline__ bool wait_within(uint64_t* bar, uint32_t parity, long long limit) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
@@ -329,9 +329,8 @@ __device__ __forceinline__ void prefetch_lengths(const PagedAttnParams& p) {
 }
 
 // Finds this CTA's share (s_cur: shared; rest is 0 where there is none).  All THREADS threads call it;
-// ends with a barrier.  Where sequences are few and
-// chunks long, 2^share_lanes lanes share one's query tiles (a lane that walked the 32 of a chunk of 2048
-// alone held up the first tile by some 3,000 cycles).
+// ends with a barrier.  Where sequences are few and chunks long, 2^share_lanes lanes share one's query tiles
+// (a lane that walked the 32 of a chunk of 2048 alone held up the first tile by some 3,000 cycles).
 template <int KT, int THREADS>
 __device__ __forceinline__ void find_share(const PagedAttnParams& p, Cursor<KT>& s_cur) {
   __shared__ long long s_warp[THREADS / 32];
