@@ -34,38 +34,38 @@ def listed():
     pre = {k: v for k, v in dict(attn, op="prefix").items() if k != "fmt"}
     return [
         # cache write of one decode step
-        dict(name="write, 64 tokens", op="write", fmt="e4m3", dtype="bf16", page=16, tokens=64, Hkv=8, D=128,
+        dict(name="write 64 tokens", op="write", fmt="e4m3", dtype="bf16", page=16, tokens=64, Hkv=8, D=128,
              packed=True),
         # cache write of a prefill chunk, k and v views of one fused projection
-        dict(name="write, 8192 tokens", op="write", fmt="int8", dtype="bf16", page=16, tokens=8192, Hkv=8,
+        dict(name="write 8192 tokens", op="write", fmt="int8", dtype="bf16", page=16, tokens=8192, Hkv=8,
              D=128, packed=True),
         # one short sequence handed to a 16-bit consumer
-        dict(name="read, one of 300", op="read", fmt="int8", dtype="fp16", page=16, B=1, Hkv=8, D=128, ctx_lo=0,
+        dict(name="read one of 300", op="read", fmt="int8", dtype="fp16", page=16, B=1, Hkv=8, D=128, ctx_lo=0,
              ctx_hi=0, new_lo=300, new_hi=300),
         # a batch of sequences leaving the 8-bit cache
-        dict(name="read, 16 sequences", op="read", fmt="e4m3", dtype="bf16", page=16, B=16, Hkv=8, D=128,
+        dict(name="read 16 sequences", op="read", fmt="e4m3", dtype="bf16", page=16, B=16, Hkv=8, D=128,
              ctx_lo=0, ctx_hi=0, new_lo=512, new_hi=8192),
         # the accepted branch of one 60-node spine tree
-        dict(name="commit, spine tree", op="commit", fmt="e4m3", page=16, B=1, N=60, Hkv=8, D=128, acc_lo=12,
+        dict(name="commit spine tree", op="commit", fmt="e4m3", page=16, B=1, N=60, Hkv=8, D=128, acc_lo=12,
              acc_hi=12, ctx_lo=2048, ctx_hi=2048),
         # the accepted branches of a large batch of 64-node trees
-        dict(name="commit, 128 trees", op="commit", fmt="int8", page=32, B=128, N=64, Hkv=8, D=128, acc_lo=0,
+        dict(name="commit 128 trees", op="commit", fmt="int8", page=32, B=128, N=64, Hkv=8, D=128, acc_lo=0,
              acc_hi=8, ctx_lo=500, ctx_hi=2000),
         # decode of a few short sequences: latency
-        dict(attn, name="attn, decode of 4 short", B=4, ctx_lo=300, ctx_hi=700, new_lo=1, new_hi=1),
+        dict(attn, name="attn decode of 4 short", B=4, ctx_lo=300, ctx_hi=700, new_lo=1, new_hi=1),
         # decode of a serving batch: the cache is read once
-        dict(attn, name="attn, decode of 64", B=64, ctx_lo=512, ctx_hi=8192, new_lo=1, new_hi=1),
+        dict(attn, name="attn decode of 64", B=64, ctx_lo=512, ctx_hi=8192, new_lo=1, new_hi=1),
         # tree verification of a ragged batch, 64 nodes a sequence
-        dict(attn, name="attn, 16 trees of 64", fmt="int8", mask="tree", B=16, ctx_lo=512, ctx_hi=8192, new_lo=64,
+        dict(attn, name="attn 16 trees of 64", fmt="int8", mask="tree", B=16, ctx_lo=512, ctx_hi=8192, new_lo=64,
              new_hi=64),
         # a few requests just behind one system prompt: latency
-        dict(pre, name="prefix, decode of 3 short", groups=1, per_lo=3, per_hi=3, pre_lo=500, pre_hi=500,
+        dict(pre, name="prefix decode of 3 short", groups=1, per_lo=3, per_hi=3, pre_lo=500, pre_hi=500,
              ctx_lo=5, ctx_hi=60, new_lo=1, new_hi=1),
         # decode of many requests behind one long document
-        dict(pre, name="prefix, decode of 64", groups=1, per_lo=64, per_hi=64, pre_lo=8000, pre_hi=8000,
+        dict(pre, name="prefix decode of 64", groups=1, per_lo=64, per_hi=64, pre_lo=8000, pre_hi=8000,
              ctx_lo=30, ctx_hi=600, new_lo=1, new_hi=1),
         # draft trees of requests behind several system prompts, narrow heads
-        dict(pre, name="prefix, trees behind 4", dtype="fp16", page=32, Hq=16, Hkv=4, D=64, mask="tree", groups=4,
+        dict(pre, name="prefix trees behind 4", dtype="fp16", page=32, Hq=16, Hkv=4, D=64, mask="tree", groups=4,
              per_lo=3, per_hi=5, pre_lo=1500, pre_hi=5000, ctx_lo=40, ctx_hi=700, new_lo=16, new_hi=48),
     ]
 
