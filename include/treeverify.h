@@ -30,6 +30,12 @@
  *   tv_attn_paged     attention of every new token over its sequence's pages
  *   tv_commit_paged   the accepted branch's K/V rows to consecutive positions
  *
+ * and over an 8-bit paged cache, which holds twice the tokens:
+ *
+ *   tv_paged_append_q8  new K/V rows, quantised, into their slots
+ *   tv_paged_read_q8    cached rows as 16-bit values
+ *   tv_commit_paged_q8  the accepted branch's rows to consecutive positions
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Every pointer argument is a DEVICE pointer owned by the caller, unless
@@ -352,7 +358,7 @@ tv_status tv_debug_set_wait_limit(long long cycles);
  *                       record.  Units: 1 tree, 2 greedy, 3 sample,
  *                       4 expand, 5 attention, 6 commit, 7 expected,
  *                       8 top-n selection, 9 library, 10 pages,
- *                     11 to 13 paged attention.  Host call; it must not
+ *                       11 to 13 paged attention, 14 the 8-bit cache.  Host call; it must not
  *                       overlap a launch of this library on the device.
  *                       TV_ERR_INVALID_ARG if site is NULL, TV_ERR_CUDA if
  *                       the device reports an error.
@@ -699,6 +705,72 @@ tv_status tv_commit_paged(const tv_paged_cache* cache, const int32_t* block_tabl
                           const int32_t* kv_len, const int32_t* path, const int32_t* accept_len,
                           int B, int N, int P, int32_t* new_kv_len, int32_t* status,
                           cudaStream_t stream);
+
+/*
+ * The 8-bit paged cache
+ * ---------------------
+ * A cache row (one token, one kv head, K or V) is D codes of one byte and a scale byte s; its values
+ * are code * 2^(s - 127), and NaN where s is 255.  Codes are e4m3 (TV_E4M3: 4 exponent and 3
+ * mantissa bits, no infinities) or signed whole numbers (TV_INT8).  Written rows have the least exponent
+ * e = s - 127 >= -126 with max |x| <= M 2^e, M = 448 or 127, and the codes nearest to x 2^-e, ties to
+ * even: a value of an e4m3 row is off by at most 2^-4 of itself (or 2^(e - 10), below 2^(e - 6)), one of an int8
+ * row by at most 2^(e - 1), which is below max|x| / 127.  A row with an infinity or a NaN gets s = 255 and codes 0.
+ * The codes are laid out as a tv_paged_cache's elements are (strides in codes, multiples of 16);
+ * scales are [num_pages, Hkv, page_size], contiguous.  D is a multiple of 16 up to 1024 (attention: 64 or
+ * 128).  tv_page_map serves these caches too: tables, slots and positions are the same.
+ */
+typedef enum { TV_E4M3 = 0, TV_INT8 = 1 } tv_q8_format;
+
+typedef struct {
+  void* k;              /* device, 16-byte aligned */
+  void* v;              /* device, 16-byte aligned */
+  uint8_t* k_scale;     /* device, 8-byte aligned */
+  uint8_t* v_scale;     /* device, 8-byte aligned */
+  int64_t page_stride;
+  int64_t head_stride;
+  int64_t row_stride;
+  int32_t num_pages;
+  int32_t page_size;    /* a power of two from 8 to 256 */
+  int32_t Hkv;
+  int32_t D;
+  int32_t format;       /* tv_q8_format */
+  int32_t dtype;        /* tv_dtype of the 16-bit tensors that go with the cache */
+} tv_q8_cache;
+
+/*
+ * tv_paged_append_q8 -- tv_paged_append into an 8-bit cache: K and V rows are quantised as they
+ * are written.  Arguments and status as there; k, v are of cache->dtype.  Of two tokens with one slot, either's
+ * pieces may stay.
+ */
+tv_status tv_paged_append_q8(const void* k, const void* v, int64_t token_stride,
+                             int64_t head_stride, const int64_t* slots, int T,
+                             const tv_q8_cache* cache, int32_t* status, cudaStream_t stream);
+
+/*
+ * tv_paged_read_q8 -- cached rows as 16-bit values, for what takes no 8-bit cache (a 16-bit cache that a
+ * sequence moves to, tv_attn_verify, a host copy).  Row t of sequence b (q_start[b] <= t < q_start[b + 1])
+ * is the row at position start[b] + t - q_start[b].
+ *   block_table int32 [B, P]; q_start int32 [B + 1]; start int32 [B].
+ *   k, v        [T, Hkv, D] of cache->dtype out, contiguous, 16-byte aligned, apart from the cache: the
+ *               value rounded to nearest (a bf16 value from 2^-126 on is exact), past the type's largest
+ *               number that number.  Rows of tokens outside every sequence are left as they were.
+ *   status      int32 [B] out, may be NULL: 0, or TV_ERR_INVALID_ARG for a malformed q_start (the
+ *               sequence's rows are left as they were), start[b] < 0 or start[b] + n_b > P * page_size
+ *               (its rows are zeroed), or a page id outside [0, num_pages) (that page's rows are zeroed).
+ * Requires B <= 4096; B * P below 2^31 and P * page_size at most 2^31 - 1; Hkv * D / 16 at most 2^20.
+ */
+tv_status tv_paged_read_q8(const tv_q8_cache* cache, const int32_t* block_table,
+                           const int32_t* q_start, const int32_t* start, int B, int T, int P, void* k,
+                           void* v, int32_t* status, cudaStream_t stream);
+
+/*
+ * tv_commit_paged_q8 -- tv_commit_paged over an 8-bit cache: codes and scales move as they are.
+ * Arguments, status and limits as there.
+ */
+tv_status tv_commit_paged_q8(const tv_q8_cache* cache, const int32_t* block_table,
+                             const int32_t* kv_len, const int32_t* path, const int32_t* accept_len,
+                             int B, int N, int P, int32_t* new_kv_len, int32_t* status,
+                             cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -22,6 +22,8 @@ TV_ERR_WORKSPACE = 7
 TV_ERR_NO_PAGES = 8
 TV_BF16 = 0
 TV_FP16 = 1
+TV_E4M3 = 0
+TV_INT8 = 1
 TV_MAX_NODES = 512
 TV_WAIT_LIMIT_DEFAULT = -1
 
@@ -53,6 +55,9 @@ _I64 = ctypes.c_int64
 # tv_paged_cache for struct.pack: k, v; page, head and row strides; num_pages,
 # page_size, Hkv, D, dtype (a bytes object passes as a pointer argument)
 PAGED_CACHE_FORMAT = "PPqqqiiiii"
+# tv_q8_cache: k, v, k_scale, v_scale; page, head and row strides; num_pages, page_size, Hkv, D,
+# format, dtype
+Q8_CACHE_FORMAT = "PPPPqqqiiiiii"
 
 _SIGS = {
     "tv_status_string": (ctypes.c_char_p, [_I]),
@@ -87,6 +92,9 @@ _SIGS = {
     "tv_attn_paged_workspace_size": (_SZ, [_I, _I, _I, _I]),
     "tv_attn_paged": (_I, [_P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _I,
                            _P, _P, _P, _P, _SZ, _P]),
+    "tv_paged_append_q8": (_I, [_P, _P, _I64, _I64, _P, _I, _P, _P, _P]),
+    "tv_paged_read_q8": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "tv_commit_paged_q8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
     "tv_commit_paged": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
 }
 

@@ -7,12 +7,13 @@ from typing import Callable, Optional
 
 import torch
 
-from ._lib import PAGED_CACHE_FORMAT, TV_BF16, TV_FP16, TV_MAX_NODES, TVError, check, lib
+from ._lib import (PAGED_CACHE_FORMAT, Q8_CACHE_FORMAT, TV_BF16, TV_E4M3, TV_FP16, TV_INT8, TV_MAX_NODES, TVError,
+                   check, lib)
 
 __all__ = ["tree_build", "attn_verify", "accept_greedy", "accept_sample", "expand_gated",
            "expand_tree", "commit_path", "expected_accept", "build_spine_tree", "spine_ratio_update", "workspace", "attn_workspace_size", "attn_plan", "greedy_workspace_size",
            "sample_workspace_size", "expand_workspace_size", "page_map", "paged_append", "attn_paged",
-           "commit_paged", "attn_paged_workspace_size"]
+           "commit_paged", "attn_paged_workspace_size", "paged_append_q8", "paged_read_q8", "commit_paged_q8"]
 
 _workspaces: dict = {}
 
@@ -625,8 +626,12 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
     cache rows slots int64 [T] name; negative slots, and slots past the cache, write
     nothing.  k_pages, v_pages [num_pages, Hkv, page_size, D] bf16 or fp16.  status int32
     [T], if given, tells of slots past the cache."""
-    cache = _cache(k_pages, v_pages)
-    dev, dtype = k_pages.device, k_pages.dtype
+    _append(lib.tv_paged_append, "tv_paged_append", _cache(k_pages, v_pages), k_pages, k_pages.dtype, k, v, slots,
+            status)
+
+
+def _append(fn, name, cache, k_pages, dtype, k, v, slots, status) -> None:
+    dev = k_pages.device
     _, Hkv, _, D = k_pages.shape
     try:
         T = slots.numel()
@@ -648,7 +653,7 @@ def paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_pages:
         _fits(T=T)
     if status is not None:
         _need(status, "status", _I32, (T,), dev)
-    _call(lib.tv_paged_append, "tv_paged_append", dev, k.data_ptr(), v.data_ptr(), strides[0],
+    _call(fn, name, dev, k.data_ptr(), v.data_ptr(), strides[0],
           strides[1], slots.data_ptr(), T, cache, _ptr(status))
 
 
@@ -733,8 +738,11 @@ def commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torc
     pages, in place.  k_pages, v_pages [num_pages, Hkv, page_size, D]; block_table
     int32 [B, P]; kv_len, accept_len int32 [B]; path int32 [B, N].
     Returns (new_kv_len int32 [B], status int32 [B])."""
-    cache = _cache(k_pages, v_pages)
-    dev = k_pages.device
+    return _commit(lib.tv_commit_paged, "tv_commit_paged", _cache(k_pages, v_pages), k_pages.device, block_table,
+                   kv_len, path, accept_len, new_kv_len, status)
+
+
+def _commit(fn, name, cache, dev, block_table, kv_len, path, accept_len, new_kv_len, status):
     try:
         (B, P), N = block_table.shape, path.shape[1]
         row = (B,)
@@ -766,7 +774,129 @@ def commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torc
         status = torch.empty(B, dtype=_I32, device=dev)
     else:
         _need(status, "status", _I32, (B,), dev)
-    _call(lib.tv_commit_paged, "tv_commit_paged", dev, cache, block_table.data_ptr(),
+    _call(fn, name, dev, cache, block_table.data_ptr(),
           kv_len.data_ptr(), path.data_ptr(), accept_len.data_ptr(), B, N, P,
           new_kv_len.data_ptr(), status.data_ptr())
     return new_kv_len, status
+
+
+# ---------------------------------------------------------------------------
+# 8-bit paged KV cache
+#
+# k_codes, v_codes [num_pages, Hkv, page_size, D] of torch.float8_e4m3fn or torch.int8 (any strides with
+# D contiguous, as the 16-bit caches), k_scale, v_scale uint8 [num_pages, Hkv, page_size]: a row's values are
+# code * 2^(scale - 127).  Block tables and slots are page_map's.
+# ---------------------------------------------------------------------------
+_CODES = {torch.float8_e4m3fn: TV_E4M3, torch.int8: TV_INT8}
+_U8 = torch.uint8
+_pack_q8_cache = struct.Struct(Q8_CACHE_FORMAT).pack
+
+
+def _q8_cache(k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+              dtype) -> bytes:
+    """tv_q8_cache of these tensors; dtype: of the 16-bit tensors that go with it."""
+    try:
+        n, Hkv, page, D = shape = k_codes.shape
+        s0, s1, s2, s3 = strides = k_codes.stride()
+        rows, dev = (n, Hkv, page), k_codes.device
+        if (k_codes.is_cuda and s3 == 1 and v_codes.shape == shape and v_codes.stride() == strides
+                and v_codes.dtype is k_codes.dtype and v_codes.device == dev
+                and k_scale.dtype is _U8 and k_scale.shape == rows and k_scale.device == dev
+                and k_scale.is_contiguous()
+                and v_scale.dtype is _U8 and v_scale.shape == rows and v_scale.device == dev
+                and v_scale.is_contiguous()):
+            return _pack_q8_cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                  s0, s1, s2, n, page, Hkv, D, _CODES[k_codes.dtype], _CACHE_DTYPES[dtype])
+    except (AttributeError, KeyError, TypeError, ValueError):
+        pass
+    if dtype not in _CACHE_DTYPES:
+        raise TypeError(f"rows must be torch.bfloat16 or torch.float16, got {dtype}")
+    for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        if t.dtype not in _CODES:
+            raise TypeError(f"{name} must be torch.float8_e4m3fn or torch.int8, got {t.dtype}")
+    if v_codes.dtype != k_codes.dtype:
+        raise TypeError(f"v_codes must be {k_codes.dtype}, got {v_codes.dtype}")
+    if k_codes.dim() != 4 or v_codes.shape != k_codes.shape:
+        raise ValueError("k_codes and v_codes must both be [num_pages, Hkv, page_size, D]")
+    if not _same_strides(k_codes, v_codes):
+        raise ValueError("k_codes and v_codes must have the same strides")
+    if v_codes.device != k_codes.device:
+        raise ValueError(f"v_codes is on {v_codes.device}, expected {k_codes.device}")
+    if k_codes.stride(3) != 1:
+        raise ValueError("the last dimension of k_codes and v_codes must be contiguous")
+    _need(k_scale, "k_scale", _U8, k_codes.shape[:3], k_codes.device)
+    _need(v_scale, "v_scale", _U8, k_codes.shape[:3], k_codes.device)
+    n, Hkv, page, D = k_codes.shape
+    return _pack_q8_cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                          *k_codes.stride()[:3], n, page, Hkv, D, _CODES[k_codes.dtype], _CACHE_DTYPES[dtype])
+
+
+def paged_append_q8(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor,
+                    v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                    status: Optional[torch.Tensor] = None) -> None:
+    """paged_append into an 8-bit cache: k, v [T, Hkv, D] (bf16 or fp16) are quantised
+    as they are written into the rows that slots int64 [T] name."""
+    if not isinstance(k, torch.Tensor):
+        raise TypeError("k must be a torch.Tensor")
+    _append(lib.tv_paged_append_q8, "tv_paged_append_q8", _q8_cache(k_codes, v_codes, k_scale, v_scale, k.dtype),
+            k_codes, k.dtype, k, v, slots, status)
+
+
+def paged_read_q8(k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                  block_table: torch.Tensor, q_start: torch.Tensor, start: torch.Tensor, tokens: int,
+                  dtype=torch.bfloat16, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None):
+    """Cached rows as bf16 or fp16 values: rows start[b], start[b] + 1, .. of sequence b go to rows
+    q_start[b] .. q_start[b + 1] - 1 of the outputs.  block_table int32 [B, P]; q_start int32
+    [B+1]; start int32 [B]; tokens = rows of the outputs.
+    Returns (k, v [tokens, Hkv, D], status int32 [B])."""
+    if k is not None:
+        dtype = k.dtype
+    cache = _q8_cache(k_codes, v_codes, k_scale, v_scale, dtype)
+    dev = k_codes.device
+    _, Hkv, _, D = k_codes.shape
+    try:
+        B, P = block_table.shape
+        good = (P <= _MOST and 0 <= tokens <= _MOST
+                and block_table.dtype is _I32 and block_table.device == dev and block_table.is_contiguous()
+                and q_start.dtype is _I32 and q_start.shape == (B + 1,) and q_start.device == dev
+                and q_start.is_contiguous()
+                and start.dtype is _I32 and start.shape == (B,) and start.device == dev and start.is_contiguous())
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        B, P = _table_shape(block_table)
+        _need(block_table, "block_table", _I32, None, dev)
+        _need(q_start, "q_start", _I32, (B + 1,), dev)
+        _need(start, "start", _I32, (B,), dev)
+        _fits(tokens=tokens, P=P)
+    shape = (tokens, Hkv, D)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(k, "k", dtype, shape, dev)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _need(v, "v", dtype, shape, dev)
+    if status is None:
+        status = torch.empty(B, dtype=_I32, device=dev)
+    else:
+        _need(status, "status", _I32, (B,), dev)
+    _call(lib.tv_paged_read_q8, "tv_paged_read_q8", dev, cache, block_table.data_ptr(), q_start.data_ptr(),
+          start.data_ptr(), B, int(tokens), P, k.data_ptr(), v.data_ptr(), status.data_ptr())
+    return k, v, status
+
+
+def commit_paged_q8(k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                    block_table: torch.Tensor, kv_len: torch.Tensor, path: torch.Tensor,
+                    accept_len: torch.Tensor, new_kv_len: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None):
+    """commit_paged over an 8-bit cache: codes and scales move as they are."""
+    return _commit(lib.tv_commit_paged_q8, "tv_commit_paged_q8",
+                   _q8_cache(k_codes, v_codes, k_scale, v_scale, torch.bfloat16), k_codes.device, block_table,
+                   kv_len, path, accept_len, new_kv_len, status)

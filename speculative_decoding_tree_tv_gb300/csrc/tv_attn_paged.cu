@@ -276,7 +276,7 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   if (st != TV_OK) return st;
   const int Hkv = cache->Hkv, D = cache->D;
   if (Hq % Hkv != 0) return TV_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || Hq / Hkv > 128 || B > tv::paged::kMaxSeqs) return TV_ERR_UNSUPPORTED;
+  if ((D != 64 && D != 128) || Hq / Hkv > 128 || B > tv::kMaxSeqs) return TV_ERR_UNSUPPORTED;
   if (anc_mask && max_q > TV_MAX_NODES) return TV_ERR_UNSUPPORTED;
   if ((long long)T * Hq > 0x7fffffffll || (long long)B * P > 0x7fffffffll ||
       ((long long)P << c.page_shift) > 0x7fffffffll - 512)

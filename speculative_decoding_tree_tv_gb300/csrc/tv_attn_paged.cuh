@@ -38,7 +38,6 @@ using namespace sm100;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kRescaleLog2 = 8.0f;  // keep a stale maximum while within 2^8
-constexpr int kMaxSeqs = 4096;
 
 // A CTA whose waits gave up: rows of the sequences first .. last with tokens may not be there.  It counts
 // only with this call's token.

@@ -6,6 +6,8 @@
 
 namespace tv {
 
+constexpr int kMaxSeqs = 4096;
+
 struct PagedCache {
   long long page_stride, head_stride, row_stride;  // elements
   int num_pages, page_shift;                       // page_size = 1 << page_shift

@@ -19,13 +19,12 @@
 // read list entries below n_free and table entries at or past a target, while
 // pushes write list entries at or past n_free and tables grow past held_b.
 #define TV_UNIT 10
-#include "tv_paged.cuh"
+#include "tv_commit_paged.cuh"
 #include "tv_sm100.cuh"
 
 namespace tv {
 namespace {
 
-constexpr int kMaxSeqs = 4096;
 
 struct PageMapParams {
   const int32_t* q_start;
@@ -293,87 +292,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     if (dst[u]) *dst[u] = x[u];
 }
 
-// ------------------------------------------------------------------- commit
-// As commit_kernel of the dense cache: one CTA per (sequence, kv head); the
-// path is strictly increasing from 0, so path[d] >= d and a destination never
-// lies past the sources still to be read; a batch reads all its rows before
-// it writes any.  Row addresses come from the block table; every page that
-// a moving row touches is checked before the first row moves.
-constexpr int kCommitThreads = 256;
-constexpr int kCommitChunks = 4;  // 16-byte chunks a thread carries per batch
-
-__global__ void __launch_bounds__(kCommitThreads)
-commit_paged_kernel(uint16_t* __restrict__ k, uint16_t* __restrict__ v, const PagedCache c,
-                    const int32_t* __restrict__ table, const int32_t* __restrict__ kv_len,
-                    const int32_t* __restrict__ path, const int32_t* __restrict__ accept_len, int N,
-                    int Hkv, int C, int P, int32_t* __restrict__ new_kv_len,
-                    int32_t* __restrict__ status) {
-  __shared__ int32_t s_path[kMaxNodes];
-  __shared__ long long s_src[kMaxNodes], s_dst[kMaxNodes];  // element offsets; -1: the row stays
-  pdl_trigger();
-  pdl_wait();
-  const int b = blockIdx.x / Hkv, h = blockIdx.x % Hkv;
-  const int tid = threadIdx.x;
-  const int L = __ldg(kv_len + b), a = __ldg(accept_len + b);
-  int bad = !(L >= 0 && a >= 0 && a < N && TV_CHECK(N <= kMaxNodes));
-  if (!bad)
-    for (int d = tid; d <= a; d += kCommitThreads) {
-      const int p = __ldg(path + (size_t)b * N + d);
-      s_path[d] = p;
-      bad |= (d == 0) ? (p != 0) : (p < d || p >= N);
-    }
-  bad = __syncthreads_or(bad);
-  if (!bad) bad = (long long)L + s_path[a] >= ((long long)P << c.page_shift);
-  if (!bad)
-    for (int d = tid; d <= a; d += kCommitThreads) {
-      if (d > 0) bad |= s_path[d] <= s_path[d - 1];
-      long long off[2] = {-1, -1};
-      if (d > 0 && s_path[d] != d) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int pos = L + (e ? d : s_path[d]), j = pos >> c.page_shift;
-          // (a path that does not rise may lead past the table before its end is seen)
-          const int page = j < P ? __ldg(table + (size_t)b * P + j) : -1;
-          bad |= page < 0 || page >= c.num_pages;
-          off[e] = page * c.page_stride + h * c.head_stride +
-                   (pos & ((1 << c.page_shift) - 1)) * c.row_stride;
-        }
-      }
-      s_src[d] = off[0];
-      s_dst[d] = off[1];
-    }
-  bad = __syncthreads_or(bad);
-  if (h == 0 && tid == 0) {
-    status[b] = bad ? TV_ERR_INVALID_ARG : TV_OK;
-    new_kv_len[b] = bad ? L : L + a + 1;
-  }
-  if (bad) return;
-  const int per_row = 2 * C;  // K and V chunks of a row
-  const int rows_per_batch = max(1, kCommitThreads * kCommitChunks / per_row);
-  for (int d0 = 1; d0 <= a; d0 += rows_per_batch) {
-    const int items = (min(a + 1, d0 + rows_per_batch) - d0) * per_row;
-    uint4 buf[kCommitChunks];
-#pragma unroll
-    for (int u = 0; u < kCommitChunks; ++u) {
-      const int w = tid + u * kCommitThreads;
-      if (w < items) {
-        const int d = d0 + w / per_row, t = (w / C) & 1, x = w % C;
-        if (s_src[d] >= 0) buf[u] = reinterpret_cast<const uint4*>((t ? v : k) + s_src[d])[x];
-      }
-    }
-    __syncthreads();  // every source of the batch is read before any destination is written
-#pragma unroll
-    for (int u = 0; u < kCommitChunks; ++u) {
-      const int w = tid + u * kCommitThreads;
-      if (w < items) {
-        const int d = d0 + w / per_row, t = (w / C) & 1, x = w % C;
-        if (s_dst[d] >= 0) reinterpret_cast<uint4*>((t ? v : k) + s_dst[d])[x] = buf[u];
-      }
-    }
-    __syncthreads();
-  }
-}
-
 tv_status launched(cudaError_t e) {
   if (e == cudaSuccess) return TV_OK;
   (void)cudaGetLastError();
@@ -494,7 +412,7 @@ extern "C" tv_status tv_commit_paged(const tv_paged_cache* cache, const int32_t*
     return TV_ERR_INVALID_ARG;
   if (new_kv_len == kv_len) return TV_ERR_INVALID_ARG;
   return tv::launched(tv::launch_pdl(
-      tv::commit_paged_kernel, dim3((unsigned)(B * cache->Hkv)), dim3(tv::kCommitThreads), 0, stream,
-      static_cast<uint16_t*>(cache->k), static_cast<uint16_t*>(cache->v), c, block_table, kv_len,
-      path, accept_len, N, cache->Hkv, cache->D / 8, P, new_kv_len, status));
+      tv::commit_paged_kernel<uint16_t>, dim3((unsigned)(B * cache->Hkv)), dim3(tv::kCommitThreads), 0, stream,
+      static_cast<uint16_t*>(cache->k), static_cast<uint16_t*>(cache->v), (uint8_t*)nullptr,
+      (uint8_t*)nullptr, c, block_table, kv_len, path, accept_len, N, cache->Hkv, cache->D / 8, P, new_kv_len, status));
 }

@@ -1,0 +1,330 @@
+// The 8-bit paged cache's writes and reads: tv_paged_append_q8 (new K and V rows quantised into their
+// slots), tv_paged_read_q8 (rows of sequences as 16-bit values) and tv_commit_paged_q8 (the accepted
+// branch's rows: Speculative Decoding concept page, "The protocol" step 4; OPT-Tree §2).
+//
+// A row x of D values becomes codes c_i and a scale byte s: with e = s - 127 the least exponent from
+// -126 on with max |x_i| <= M 2^e, c_i = x_i 2^-e to the nearest e4m3 (M = 448) or whole number (M = 127),
+// ties to even.  A power of two costs e4m3 nothing (its step goes with the value, off by at most 2^-4 of
+// it) and int8 up to a bit (a step is at most max|x| / 63.5, half of it the error); in return scaling is
+// exact, so a code is off by one rounding and the same on every machine, and a code's value is a bf16
+// number, so reading back rounds nothing and a row that is written again keeps its codes' values.
+#define TV_UNIT 14
+#include "tv_commit_paged.cuh"
+#include "tv_quant.cuh"
+
+namespace tv {
+namespace {
+
+tv_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return TV_OK;
+  (void)cudaGetLastError();
+  return TV_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------- append
+// A row goes to 1 << row_lanes lanes, C chunks of eight values each, all loads in flight ahead of the
+// row's maximum, which takes row_lanes shuffles.  Bound by HBM (3 D + 1 bytes a row).
+constexpr int kRowThreads = 256;
+
+struct AppendQ8Params {
+  const uint16_t* k;
+  const uint16_t* v;
+  const int64_t* slots;
+  int32_t* status;
+  long long token_stride, head_stride;
+  Q8Cache c;
+  int T, chunks, row_lanes;
+};
+
+template <bool E4M3, bool F16, int C>
+__global__ void __launch_bounds__(kRowThreads) append_q8_kernel(const AppendQ8Params p) {
+  pdl_trigger();
+  pdl_wait();
+  const unsigned item = blockIdx.x * kRowThreads + threadIdx.x, lanes = 1u << p.row_lanes;
+  const unsigned r = item >> p.row_lanes, lane = item & (lanes - 1);
+  const unsigned per_token = 2 * p.c.Hkv, t = r / per_token, w = r - t * per_token;
+  const bool side = w >= (unsigned)p.c.Hkv;
+  const int h = side ? w - p.c.Hkv : w;
+  const bool is_row = t < (unsigned)p.T;
+  const long long slot = is_row ? __ldg(reinterpret_cast<const long long*>(p.slots) + t) : -1;
+  const long long limit = (long long)p.c.num_pages << p.c.page_shift;
+  const bool in = slot >= 0 && slot < limit;
+  if (is_row && w == 0 && lane == 0 && p.status) p.status[t] = slot >= limit ? TV_ERR_INVALID_ARG : TV_OK;
+  uint4 x[C];
+  const uint4* src = reinterpret_cast<const uint4*>((side ? p.v : p.k) + (long long)t * p.token_stride +
+                                                    h * p.head_stride);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int at = lane + c * lanes;
+    x[c] = in && at < p.chunks ? __ldg(src + at) : make_uint4(0, 0, 0, 0);
+  }
+  // the largest magnitude: 16-bit floats without their sign are in the order of their bits
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const uint32_t m = 0x7fff7fffu;
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[c].x & m, x[c].y & m), __vmaxu2(x[c].z & m, x[c].w & m)));
+  }
+  top = max(top & 0xffffu, top >> 16);
+  for (int o = 1; o < (int)lanes; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (!in) return;
+  const int s = q8::scale_of<E4M3>(q8::unpack<F16>(top).x);
+  // (2^-e; rows that are no numbers get codes of 0)
+  const float f = s == q8::kNaN ? 0.0f : __int_as_float((254 - s) << 23);
+  const long long page = slot >> p.c.page_shift;
+  const int row = (int)(slot & ((1ll << p.c.page_shift) - 1));
+  uint2* dst = reinterpret_cast<uint2*>((side ? p.c.v : p.c.k) + p.c.code_at(page, h, row));
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int at = lane + c * lanes;
+    const uint32_t in4[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+    float2 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = q8::unpack<F16>(s == q8::kNaN ? 0u : in4[i]);
+      y[i].x *= f;
+      y[i].y *= f;
+    }
+    if (at < p.chunks) dst[at] = make_uint2(q8::encode4<E4M3>(y[0], y[1]), q8::encode4<E4M3>(y[2], y[3]));
+  }
+  if (lane == 0) (side ? p.c.vs : p.c.ks)[p.c.scale_at(page, h, row)] = (uint8_t)s;
+}
+
+template <bool E4M3, bool F16>
+cudaError_t launch_append(const AppendQ8Params& p, int C, unsigned blocks, cudaStream_t stream) {
+  if (C == 1) return launch_pdl(append_q8_kernel<E4M3, F16, 1>, dim3(blocks), dim3(kRowThreads), 0, stream, p);
+  if (C == 2) return launch_pdl(append_q8_kernel<E4M3, F16, 2>, dim3(blocks), dim3(kRowThreads), 0, stream, p);
+  return launch_pdl(append_q8_kernel<E4M3, F16, 4>, dim3(blocks), dim3(kRowThreads), 0, stream, p);
+}
+
+// --------------------------------------------------------------------- read
+// A CTA takes `tokens` consecutive tokens: a thread each finds its token's sequence (a binary search of
+// the starts) and row, then all stream the rows, 16 codes a step, four steps in flight.
+constexpr int kReadTokens = 32, kReadFlight = 4;
+
+struct ReadQ8Params {
+  Q8Cache c;
+  const int32_t* table;
+  const int32_t* q_start;
+  const int32_t* start;
+  uint16_t* k;
+  uint16_t* v;
+  int32_t* status;
+  int B, T, P, tokens, units;  // units: of 16 codes in a row
+  int blocks;                  // CTAs of tokens; those behind them write the sequences' status
+};
+
+// Whether a sequence's rows lie within the table.
+__device__ __forceinline__ bool read_fits(const ReadQ8Params& p, int start, int n) {
+  return start >= 0 && (long long)start + n <= ((long long)p.P << p.c.page_shift);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t narrow(float2 y, float f) {
+  y.x *= f;
+  y.y *= f;
+  const float most = F16 ? 65504.0f : 3.38953139e38f;  // (a code's value may be past it; a NaN stays)
+  if (fabsf(y.x) > most) y.x = copysignf(most, y.x);
+  if (fabsf(y.y) > most) y.y = copysignf(most, y.y);
+  if (F16) {
+    const __half2 o = __floats2half2_rn(y.x, y.y);
+    return *reinterpret_cast<const uint32_t*>(&o);
+  }
+  const __nv_bfloat162 o = __floats2bfloat162_rn(y.x, y.y);
+  return *reinterpret_cast<const uint32_t*>(&o);
+}
+
+template <bool E4M3, bool F16>
+__global__ void __launch_bounds__(kRowThreads) read_q8_kernel(const ReadQ8Params p) {
+  __shared__ int s_page[kReadTokens], s_row[kReadTokens];  // page -1: zeros, -2: nobody's token
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= p.blocks) {  // a warp per sequence
+    const int b = ((int)blockIdx.x - p.blocks) * (kRowThreads / 32) + (tid >> 5);
+    if (b >= p.B) return;
+    int t0, n;
+    bool ok = seq_range(p.q_start, b, p.T, t0, n);
+    const int start = __ldg(p.start + b);
+    ok = ok && read_fits(p, start, n);
+    if (ok && n > 0)
+      for (int j = (start >> p.c.page_shift) + (tid & 31); j <= (start + n - 1) >> p.c.page_shift; j += 32) {
+        const int page = TV_IN(j, p.P) ? __ldg(p.table + (size_t)b * p.P + j) : -1;
+        ok = ok && page >= 0 && page < p.c.num_pages;
+      }
+    ok = __all_sync(0xffffffffu, ok);
+    if ((tid & 31) == 0 && p.status) p.status[b] = ok ? TV_OK : TV_ERR_INVALID_ARG;
+    return;
+  }
+  const int first = blockIdx.x * p.tokens, count = min(p.tokens, p.T - first);
+  if (tid < count) {
+    const int t = first + tid;
+    int lo = 0, hi = p.B;  // the last sequence that starts at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.q_start + mid) <= t) lo = mid + 1;
+      else hi = mid;
+    }
+    const int b = lo - 1;
+    int page = -2, row = 0, t0, n;
+    if (b >= 0 && seq_range(p.q_start, b, p.T, t0, n) && t >= t0 && t - t0 < n) {
+      const int start = __ldg(p.start + b);
+      page = -1;
+      if (read_fits(p, start, n)) {
+        const int pos = start + t - t0, j = pos >> p.c.page_shift;
+        page = TV_IN(j, p.P) ? __ldg(p.table + (size_t)b * p.P + j) : -1;
+        if (page < 0 || page >= p.c.num_pages) page = -1;
+        row = pos & ((1 << p.c.page_shift) - 1);
+      }
+    }
+    s_page[tid] = page;
+    s_row[tid] = row;
+  }
+  __syncthreads();
+  const int per_side = p.c.Hkv * p.units, per_token = 2 * per_side, items = count * per_token;
+  for (int i0 = tid; i0 < items; i0 += kRowThreads * kReadFlight) {
+    uint4 x[kReadFlight], *dst[kReadFlight];
+    int s[kReadFlight];
+#pragma unroll
+    for (int u = 0; u < kReadFlight; ++u) {
+      const int i = i0 + u * kRowThreads;
+      dst[u] = nullptr;
+      if (i < items) {
+        const int t = i / per_token, w = i - t * per_token;
+        const bool side = w >= per_side;
+        const int r = side ? w - per_side : w, h = r / p.units, c = r - h * p.units;
+        const int page = s_page[t];
+        x[u] = make_uint4(0, 0, 0, 0);
+        s[u] = 1;
+        if (page >= -1)
+          dst[u] = reinterpret_cast<uint4*>((side ? p.v : p.k) +
+                                            ((long long)(first + t) * per_side + r) * 16);
+        if (page >= 0) {
+          x[u] = __ldg(reinterpret_cast<const uint4*>((side ? p.c.v : p.c.k) + p.c.code_at(page, h, s_row[t])) + c);
+          s[u] = __ldg((side ? p.c.vs : p.c.ks) + p.c.scale_at(page, h, s_row[t]));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kReadFlight; ++u) {
+      if (!dst[u]) continue;
+      const float f = q8::factor(s[u]);
+      const uint32_t c4[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 a, b;
+        q8::decode4<E4M3>(c4[i], a, b);
+        o[2 * i] = narrow<F16>(a, f);
+        o[2 * i + 1] = narrow<F16>(b, f);
+      }
+      dst[u][0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[u][1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+  }
+}
+
+}  // namespace
+}  // namespace tv
+
+extern "C" tv_status tv_paged_append_q8(const void* k, const void* v, int64_t token_stride,
+                                        int64_t head_stride, const int64_t* slots, int T,
+                                        const tv_q8_cache* cache, int32_t* status,
+                                        cudaStream_t stream) {
+  TV_NVTX_RANGE("tv_paged_append_q8");
+  if (T < 0) return TV_ERR_INVALID_ARG;
+  tv::AppendQ8Params p;
+  const tv_status st = tv::check_q8_cache(cache, &p.c);
+  if (st != TV_OK) return st;
+  const int Hkv = cache->Hkv, D = cache->D;
+  if ((long long)T * Hkv * (D / 8) > (1ll << 30) - 4096) return TV_ERR_UNSUPPORTED;
+  if (T == 0) return TV_OK;
+  if (!k || !v || !slots) return TV_ERR_INVALID_ARG;
+  p.token_stride = tv::stride_or(token_stride, T, 8);
+  p.head_stride = tv::stride_or(head_stride, Hkv, 8);
+  if (p.token_stride < 0 || p.head_stride < 0 || ((p.token_stride | p.head_stride) & 7))
+    return TV_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
+    return TV_ERR_INVALID_ARG;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.slots = slots;
+  p.status = status;
+  p.T = T;
+  p.chunks = D / 8;
+  const int C = p.chunks > 64 ? 4 : p.chunks >= 4 ? 2 : 1;
+  p.row_lanes = 0;
+  while (p.row_lanes < 5 && (C << p.row_lanes) < p.chunks) ++p.row_lanes;
+  const long long threads = (2ll * T * Hkv) << p.row_lanes;
+  const unsigned blocks = (unsigned)((threads + tv::kRowThreads - 1) / tv::kRowThreads);
+  const bool f16 = cache->dtype == TV_FP16;
+  if (cache->format == TV_E4M3)
+    return tv::launched(f16 ? tv::launch_append<true, true>(p, C, blocks, stream)
+                            : tv::launch_append<true, false>(p, C, blocks, stream));
+  return tv::launched(f16 ? tv::launch_append<false, true>(p, C, blocks, stream)
+                          : tv::launch_append<false, false>(p, C, blocks, stream));
+}
+
+extern "C" tv_status tv_paged_read_q8(const tv_q8_cache* cache, const int32_t* block_table,
+                                      const int32_t* q_start, const int32_t* start, int B, int T, int P,
+                                      void* k, void* v, int32_t* status, cudaStream_t stream) {
+  TV_NVTX_RANGE("tv_paged_read_q8");
+  if (B < 0 || T < 0 || P < 1) return TV_ERR_INVALID_ARG;
+  tv::ReadQ8Params p;
+  const tv_status st = tv::check_q8_cache(cache, &p.c);
+  if (st != TV_OK) return st;
+  const int Hkv = cache->Hkv, D = cache->D;
+  if (B > tv::kMaxSeqs || (long long)B * P > 0x7fffffffll ||
+      ((long long)P << p.c.page_shift) > 0x7fffffffll || (long long)Hkv * (D / 16) > (1 << 20))
+    return TV_ERR_UNSUPPORTED;
+  if (B == 0) return TV_OK;
+  if (!block_table || !q_start || !start || (T > 0 && (!k || !v))) return TV_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
+    return TV_ERR_INVALID_ARG;
+  p.table = block_table;
+  p.q_start = q_start;
+  p.start = start;
+  p.k = static_cast<uint16_t*>(k);
+  p.v = static_cast<uint16_t*>(v);
+  p.status = status;
+  p.B = B;
+  p.T = T;
+  p.P = P;
+  p.units = D / 16;
+  p.tokens = tv::kReadTokens;
+  while (p.tokens > 1 && T / p.tokens < 4 * tv::device_sm_count()) p.tokens /= 2;
+  p.blocks = T / p.tokens + (T % p.tokens != 0);
+  const int per = tv::kRowThreads / 32;
+  const dim3 grid((unsigned)p.blocks + (status ? (B + per - 1) / per : 0));
+  if (grid.x == 0) return TV_OK;
+  const bool f16 = cache->dtype == TV_FP16;
+  if (cache->format == TV_E4M3)
+    return tv::launched(
+        f16 ? tv::launch_pdl(tv::read_q8_kernel<true, true>, grid, dim3(tv::kRowThreads), 0, stream, p)
+            : tv::launch_pdl(tv::read_q8_kernel<true, false>, grid, dim3(tv::kRowThreads), 0, stream, p));
+  return tv::launched(
+      f16 ? tv::launch_pdl(tv::read_q8_kernel<false, true>, grid, dim3(tv::kRowThreads), 0, stream, p)
+          : tv::launch_pdl(tv::read_q8_kernel<false, false>, grid, dim3(tv::kRowThreads), 0, stream, p));
+}
+
+extern "C" tv_status tv_commit_paged_q8(const tv_q8_cache* cache, const int32_t* block_table,
+                                        const int32_t* kv_len, const int32_t* path,
+                                        const int32_t* accept_len, int B, int N, int P,
+                                        int32_t* new_kv_len, int32_t* status, cudaStream_t stream) {
+  TV_NVTX_RANGE("tv_commit_paged_q8");
+  if (B < 0 || N < 1 || N > TV_MAX_NODES || P < 1) return TV_ERR_INVALID_ARG;
+  tv::Q8Cache c;
+  const tv_status st = tv::check_q8_cache(cache, &c);
+  if (st != TV_OK) return st;
+  if ((long long)B * P > 0x7fffffffll || (long long)B * cache->Hkv > 0x7fffffffll ||
+      ((long long)P << c.page_shift) > 0x7fffffffll - TV_MAX_NODES)
+    return TV_ERR_UNSUPPORTED;
+  if (B == 0) return TV_OK;
+  if (!block_table || !kv_len || !path || !accept_len || !new_kv_len || !status)
+    return TV_ERR_INVALID_ARG;
+  if (new_kv_len == kv_len) return TV_ERR_INVALID_ARG;
+  return tv::launched(tv::launch_pdl(
+      tv::commit_paged_kernel<uint8_t>, dim3((unsigned)(B * cache->Hkv)), dim3(tv::kCommitThreads), 0,
+      stream, c.k, c.v, c.ks, c.vs, static_cast<const tv::PagedCache&>(c), block_table, kv_len, path,
+      accept_len, N, cache->Hkv, cache->D / 16, P, new_kv_len, status));
+}

@@ -1,0 +1,90 @@
+"""Plain forms of the 8-bit paged cache (64-bit floats and whole numbers), and its tests' inputs."""
+import numpy as np
+import torch
+
+from _paged_util import make
+
+FORMATS = {"e4m3": (torch.float8_e4m3fn, 448.0), "int8": (torch.int8, 127.0)}
+NAN_SCALE = 255
+
+
+def quantise_ref(x, fmt):
+    """(codes as 64-bit values [.., D], scale bytes [..]) of rows x [.., D], from the definition."""
+    x = x.double().cpu().numpy()
+    most = FORMATS[fmt][1]
+    top = np.abs(x).max(-1)
+    fine = np.isfinite(top)
+    m, e = np.frexp(np.where(fine, top, 1.0) / most)  # (a quotient that is no power of two is 2^-11 from one)
+    e = np.maximum(np.where(top == 0, -126, np.where(m == 0.5, e - 1, e)), -126)
+    y = np.ldexp(np.where(fine[..., None], x, 0.0), -e[..., None])
+    if fmt == "int8":
+        codes = np.rint(y)
+    else:
+        b = np.maximum(np.frexp(y)[1] - 1, -6)  # the code's binade; below 2^-6 steps stay 2^-9
+        codes = np.ldexp(np.rint(np.ldexp(y, 3 - b)), b - 3)
+    return torch.from_numpy(codes + 0.0), torch.from_numpy(np.where(fine, e + 127, NAN_SCALE))
+
+
+def values_ref(codes, scale):
+    """64-bit values of codes (any type) [.., D] and scale bytes [..]."""
+    c, s = codes.cpu().to(torch.float32).double().numpy(), scale.cpu().long().numpy()
+    v = np.ldexp(c, s[..., None] - 127)
+    return torch.from_numpy(np.where((s == NAN_SCALE)[..., None], np.nan, v))
+
+
+def cache(fmt, pool, Hkv, page, D, layout="heads", seed=1, device="cuda:0"):
+    """k, v codes and scales of a cache whose every byte is set (codes of e4m3 NaN and of -128 among them)."""
+    g = torch.Generator().manual_seed(seed)
+    raw = torch.randint(0, 256, (2, pool, Hkv, page, D), generator=g, dtype=torch.uint8).to(device)
+    if layout == "heads":
+        k, v = raw[0], raw[1]
+    elif layout == "rows":
+        raw = raw.view(2, pool, page, Hkv, D)
+        k, v = raw[0].transpose(1, 2), raw[1].transpose(1, 2)
+    else:
+        raw = raw.view(pool, 2, Hkv, page, D)
+        k, v = raw[:, 0], raw[:, 1]
+    s = torch.randint(0, 256, (2, pool, Hkv, page), generator=g, dtype=torch.uint8).to(device)
+    t = FORMATS[fmt][0]
+    return k.view(t), v.view(t), s[0], s[1]
+
+
+def raw(x):
+    return x.contiguous().view(torch.uint8)
+
+
+def make_q8(seed, lens, Hq, Hkv, D, page, fmt, dtype="bf16", layout="heads", spread=2.0, **kw):
+    """_paged_util.make's case over an 8-bit cache: `rows` hold the quantised values (64 bits), and c["q8"] the four
+    cache tensors.  Rows differ in size by powers of two; what no token sees is any byte."""
+    c = make(seed, lens, Hq, Hkv, D, page, dtype, **kw)
+    pool = c["k"].shape[0]
+    g = torch.Generator().manual_seed(seed + 1)
+    sides = [t.cpu() for t in cache(fmt, pool, Hkv, page, D, layout, seed, "cpu")]
+    table = c["table"].cpu().tolist()
+    rows = []
+    for b, both in enumerate(c["rows"]):
+        new = []
+        for side, x in enumerate(both):
+            n = x.shape[0]
+            size = torch.exp2(torch.randn(n, Hkv, 1, generator=g) * spread)
+            codes, scale = quantise_ref((x.float() * size).to(x.dtype), fmt)
+            for p in range(-(-n // page)):
+                m = min(page, n - p * page)
+                at = table[b][p]
+                raw8 = codes[p * page:p * page + m].float().to(FORMATS[fmt][0]).view(torch.uint8)
+                sides[side].view(torch.uint8)[at, :, :m] = raw8.transpose(0, 1)
+                sides[2 + side][at, :, :m] = scale[p * page:p * page + m].to(torch.uint8).T
+            new.append(values_ref(codes, scale))
+        rows.append(tuple(new))
+    dev = c["q"].device
+    c["rows"] = rows
+    moved = []
+    for t in sides[:2]:
+        perm = {"heads": t, "rows": t.transpose(1, 2), "both": t}[layout].contiguous().to(dev)
+        moved.append(perm.transpose(1, 2) if layout == "rows" else perm)
+    if layout == "both":  # K and V interleaved page by page
+        both = torch.stack([raw(m) for m in moved], 1)
+        moved = [both[:, 0].view(FORMATS[fmt][0]), both[:, 1].view(FORMATS[fmt][0])]
+    c["q8"] = (moved[0], moved[1], sides[2].to(dev), sides[3].to(dev))
+    c["fmt"] = fmt
+    return c
