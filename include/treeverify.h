@@ -34,6 +34,7 @@
  *
  *   tv_paged_append_q8  new K/V rows, quantised, into their slots
  *   tv_paged_read_q8    cached rows as 16-bit values
+ *   tv_attn_paged_q8    attention of every new token over its sequence's pages
  *   tv_commit_paged_q8  the accepted branch's rows to consecutive positions
  *
  * Conventions shared by every entry point
@@ -358,7 +359,8 @@ tv_status tv_debug_set_wait_limit(long long cycles);
  *                       record.  Units: 1 tree, 2 greedy, 3 sample,
  *                       4 expand, 5 attention, 6 commit, 7 expected,
  *                       8 top-n selection, 9 library, 10 pages,
- *                       11 to 13 paged attention, 14 the 8-bit cache.  Host call; it must not
+ *                       11 to 13 paged attention, 14 the 8-bit cache,
+ *                       15 and 16 its attention.  Host call; it must not
  *                       overlap a launch of this library on the device.
  *                       TV_ERR_INVALID_ARG if site is NULL, TV_ERR_CUDA if
  *                       the device reports an error.
@@ -762,6 +764,23 @@ tv_status tv_paged_append_q8(const void* k, const void* v, int64_t token_stride,
 tv_status tv_paged_read_q8(const tv_q8_cache* cache, const int32_t* block_table,
                            const int32_t* q_start, const int32_t* start, int B, int T, int P, void* k,
                            void* v, int32_t* status, cudaStream_t stream);
+
+/*
+ * tv_attn_paged_q8 -- tv_attn_paged over an 8-bit cache: keys and values are the rows' values, q, out and
+ * sums as there (q and out of cache->dtype).  Arguments, statuses and limits are tv_attn_paged's, with these
+ * differences:
+ *   - the workspace is tv_attn_paged_q8_workspace_size() bytes;
+ *   - Hq / Hkv is at most 16;
+ *   - a row of V whose scale is 255 makes the outputs of the tokens that see it NaN, and no others';
+ *     codes that tv_paged_append_q8 does not write (the NaNs of e4m3) count as V values that are not finite.
+ */
+size_t tv_attn_paged_q8_workspace_size(int max_q, int Hq, int Hkv, int D);
+tv_status tv_attn_paged_q8(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                           const tv_q8_cache* cache, const int32_t* block_table,
+                           const int32_t* q_start, const int32_t* kv_len, const uint64_t* anc_mask,
+                           const float* slopes, int B, int T, int P, int Hq, int max_q, float scale,
+                           float softcap, int window, void* out, float* lse, int32_t* status,
+                           void* workspace, size_t ws_bytes, cudaStream_t stream);
 
 /*
  * tv_commit_paged_q8 -- tv_commit_paged over an 8-bit cache: codes and scales move as they are.

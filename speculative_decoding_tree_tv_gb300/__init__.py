@@ -16,5 +16,6 @@ from .api import (  # noqa: F401
     tree_build, attn_verify, attn_verify_tree, accept_greedy, accept_sample, expand_gated, expand_tree, expand_topn, select_topn, grow_opt_tree, opt_tree_layer_sizes, commit_path, expected_accept, build_spine_tree, spine_ratio_update,
     workspace, attn_workspace_size, attn_plan, greedy_workspace_size, sample_workspace_size,
     expand_workspace_size, page_map, paged_append, attn_paged, commit_paged,
-    attn_paged_workspace_size, paged_append_q8, paged_read_q8, commit_paged_q8,
+    attn_paged_workspace_size, paged_append_q8, paged_read_q8, commit_paged_q8, attn_paged_q8,
+    attn_paged_q8_workspace_size,
 )

@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 from typing import Callable, Optional
 
@@ -13,7 +14,8 @@ from ._lib import (PAGED_CACHE_FORMAT, Q8_CACHE_FORMAT, TV_BF16, TV_E4M3, TV_FP1
 __all__ = ["tree_build", "attn_verify", "accept_greedy", "accept_sample", "expand_gated",
            "expand_tree", "commit_path", "expected_accept", "build_spine_tree", "spine_ratio_update", "workspace", "attn_workspace_size", "attn_plan", "greedy_workspace_size",
            "sample_workspace_size", "expand_workspace_size", "page_map", "paged_append", "attn_paged",
-           "commit_paged", "attn_paged_workspace_size", "paged_append_q8", "paged_read_q8", "commit_paged_q8"]
+           "commit_paged", "attn_paged_workspace_size", "paged_append_q8", "paged_read_q8", "commit_paged_q8",
+           "attn_paged_q8", "attn_paged_q8_workspace_size"]
 
 _workspaces: dict = {}
 
@@ -563,10 +565,14 @@ def _table_shape(block_table: torch.Tensor):
 
 def attn_paged_workspace_size(max_q, Hq, Hkv, D, device=None) -> int:
     """Bytes of attn_paged's workspace on `device` (the current one): it has room for each SM."""
+    return _ws_size(lib.tv_attn_paged_workspace_size, device, max_q, Hq, Hkv, D)
+
+
+def _ws_size(fn, device, *sizes) -> int:
     if device is None or torch.device(device).index in (None, _current_device()):
-        return int(lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D))
+        return int(fn(*sizes))
     with torch.cuda.device(device):
-        return int(lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D))
+        return int(fn(*sizes))
 
 
 def page_map(q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor,
@@ -671,8 +677,14 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     int32 [B]; max_q = the largest chunk.  softcap caps the scores by a tanh,
     slopes float32 [Hq] subtracts slope * distance, window hides keys that far
     back.  Returns (out [T, Hq, D], lse float32 [T, Hq], status int32 [B])."""
-    cache = _cache(k_pages, v_pages)
-    dev, dtype = k_pages.device, k_pages.dtype
+    return _attn(lib.tv_attn_paged, "tv_attn_paged", lib.tv_attn_paged_workspace_size, _cache(k_pages, v_pages),
+                 k_pages, k_pages.dtype, q, block_table, q_start, kv_len, max_q, anc_mask, scale, softcap, window,
+                 slopes, out, lse, status, want_lse, ws)
+
+
+def _attn(fn, name, ws_size, cache, k_pages, dtype, q, block_table, q_start, kv_len, max_q, anc_mask, scale, softcap,
+          window, slopes, out, lse, status, want_lse, ws):
+    dev = k_pages.device
     _, Hkv, _, Dc = k_pages.shape
     max_q = int(max_q)
     try:
@@ -718,12 +730,12 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     else:
         _need(status, "status", _I32, (B,), dev)
     if ws is None:  # from torch's allocator: ordered by stream, and a captured graph's own
-        size = (lib.tv_attn_paged_workspace_size(max_q, Hq, Hkv, D) if dev.index == _current_device()
-                else attn_paged_workspace_size(max_q, Hq, Hkv, D, dev))
+        size = (ws_size if dev.index == _current_device() else functools.partial(_ws_size, ws_size, dev))(
+            max_q, Hq, Hkv, D)
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
         _need(ws, "ws", torch.uint8, None, dev)
-    _call(lib.tv_attn_paged, "tv_attn_paged", dev, q.data_ptr(), strides[0], strides[1], cache,
+    _call(fn, name, dev, q.data_ptr(), strides[0], strides[1], cache,
           block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), _ptr(anc_mask),
           _ptr(slopes), B, T, P, Hq, max_q, scale, softcap, window, out.data_ptr(), _ptr(lse),
           status.data_ptr(), ws.data_ptr(), ws.numel())
@@ -890,6 +902,26 @@ def paged_read_q8(k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.T
     _call(lib.tv_paged_read_q8, "tv_paged_read_q8", dev, cache, block_table.data_ptr(), q_start.data_ptr(),
           start.data_ptr(), B, int(tokens), P, k.data_ptr(), v.data_ptr(), status.data_ptr())
     return k, v, status
+
+
+def attn_paged_q8_workspace_size(max_q, Hq, Hkv, D, device=None) -> int:
+    """Bytes of attn_paged_q8's workspace on `device` (the current one): it has room for each SM."""
+    return _ws_size(lib.tv_attn_paged_q8_workspace_size, device, max_q, Hq, Hkv, D)
+
+
+def attn_paged_q8(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
+                  v_scale: torch.Tensor, block_table: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                  max_q: int, anc_mask: Optional[torch.Tensor] = None, scale: float = 0.0, softcap: float = 0.0,
+                  window: int = 0, slopes: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, want_lse: bool = True,
+                  ws: Optional[torch.Tensor] = None):
+    """attn_paged over an 8-bit cache.  q [T, Hq, D] bf16 or fp16; the other arguments as
+    attn_paged's.  Returns (out [T, Hq, D], lse float32 [T, Hq], status int32 [B])."""
+    if not isinstance(q, torch.Tensor):
+        raise ValueError("q must be a tensor [T, Hq, D]")
+    return _attn(lib.tv_attn_paged_q8, "tv_attn_paged_q8", lib.tv_attn_paged_q8_workspace_size,
+                 _q8_cache(k_codes, v_codes, k_scale, v_scale, q.dtype), k_codes, q.dtype, q, block_table, q_start,
+                 kv_len, max_q, anc_mask, scale, softcap, window, slopes, out, lse, status, want_lse, ws)
 
 
 def commit_paged_q8(k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,

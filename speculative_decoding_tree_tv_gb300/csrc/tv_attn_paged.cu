@@ -8,6 +8,7 @@
 #include <chrono>
 
 #include "tv_attn_paged.cuh"
+#include "tv_quant.cuh"
 
 namespace tv {
 namespace paged {
@@ -89,7 +90,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     for (int j = 0; j < kMergeBatch; ++j) {
       const float e = ml[j].x == -INFINITY ? 0.0f : ex2(ml[j].x - M);
       l = fmaf(e, ml[j].y, l);
-      if (e == 0.0f) continue;  // (a part whose keys are all hidden: select, do not multiply)
+      // (a part whose keys are all hidden: select, do not multiply; 8-bit rows that are no numbers stay)
+      if (e == 0.0f && (!p.k_scale || ml[j].x == -INFINITY)) continue;
 #pragma unroll
       for (int c = 0; c < kC; ++c) {
         a[c].x = fmaf(e, v[j][c].x, a[c].x);
@@ -146,26 +148,37 @@ bool order_strides(const long long (&extent)[3], long long (&stride)[3], int D, 
   return a > 0 && a % 8 == 0 && b % a == 0 && c % b == 0 && c < (1ll << 39);
 }
 
-// A cache side: D by rows, heads and pages; a box is 64 dims of `rows` rows of one
+// A cache as the entry point sees it, of 16-bit values or of 8-bit codes.
+struct CacheArg {
+  PagedCache c;
+  void* k;
+  void* v;
+  int Hkv, D, dtype;
+  int format;  // tv_q8_format, or -1
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
+};
+
+// A cache side: D by rows, heads and pages; a box is 64 dims (of codes: all) of `rows` rows of one
 // page and head.
-bool map_cache(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void* base,
-               const tv_paged_cache* cache, const long long (&stride)[3], const int (&order)[3],
-               int rows) {
-  const cuuint64_t extent[3] = {(cuuint64_t)cache->page_size, (cuuint64_t)cache->Hkv,
-                                (cuuint64_t)cache->num_pages};
-  cuuint64_t dims[4] = {(cuuint64_t)cache->D}, strides[3];
-  cuuint32_t box[4] = {64};
+bool map_cache(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void* base, const CacheArg& a,
+               const long long (&stride)[3], const int (&order)[3], int rows) {
+  const cuuint64_t extent[3] = {(cuuint64_t)1 << a.c.page_shift, (cuuint64_t)a.Hkv, (cuuint64_t)a.c.num_pages};
+  const bool codes = a.format >= 0;
+  cuuint64_t dims[4] = {(cuuint64_t)a.D}, strides[3];
+  cuuint32_t box[4] = {codes ? (cuuint32_t)a.D : 64u};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   for (int i = 0; i < 3; ++i) {
     dims[i + 1] = extent[order[i]];
-    strides[i] = (cuuint64_t)stride[order[i]] * 2;
+    strides[i] = (cuuint64_t)stride[order[i]] * (codes ? 1 : 2);
     box[i + 1] = order[i] == 0 ? (cuuint32_t)rows : 1u;
   }
-  return encode(map, cache->dtype == TV_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+  return encode(map,
+                codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                      : a.dtype == TV_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                codes && a.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr long long kWholeRowsKeys = 960, kWholeTcKeys = 512;
@@ -188,13 +201,13 @@ long long wait_limit() {
 }
 
 // Which kernel runs, by the rows of the largest unit.
-PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long keys) {
+PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long keys, bool q8) {
   PagedPlan pl;
   const long long rows = (long long)max_q * G;
   // 64 decode sequences of 512 to 8,192 keys, 8 kv heads: 4 rows a unit 186 us here and 198 us on the
   // tcgen05 kernel (D 64: 102 and 149 us), 16 rows 171 and 180 us; 32 rows took 430 us with two row
   // tiles a warp here (its registers spill) and 185 us there.
-  pl.small = rows <= 16;
+  pl.small = rows <= 16 || q8;
   if (pl.small) {
     pl.rows = 16;
     pl.nb = pl.tq = (rows <= 8 ? 8 : 16) / G;
@@ -256,96 +269,116 @@ void set_wait_limit(long long cycles) {
 extern "C" size_t tv_attn_paged_workspace_size(int max_q, int Hq, int Hkv, int D) {
   if (max_q < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128))
     return 0;
-  return tv::paged::paged_plan(max_q, Hkv, Hq / Hkv, D, 0, 0, 0).bytes();  // (whatever B, T and keys are)
+  return tv::paged::paged_plan(max_q, Hkv, Hq / Hkv, D, 0, 0, 0, false).bytes();  // (whatever B, T and keys are)
 }
 
-extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_stride,
-                                   const tv_paged_cache* cache, const int32_t* block_table,
-                                   const int32_t* q_start, const int32_t* kv_len,
-                                   const uint64_t* anc_mask, const float* slopes, int B, int T,
-                                   int P, int Hq, int max_q, float scale, float softcap, int window,
-                                   void* out, float* lse, int32_t* status, void* workspace,
-                                   size_t ws_bytes, cudaStream_t stream) {
-  TV_NVTX_RANGE("tv_attn_paged");
-  if (B < 0 || T < 0 || P < 1 || Hq < 1 || max_q < 1 || window < 0) return TV_ERR_INVALID_ARG;
-  if (!(scale >= 0.0f) || !isfinite(scale) || !(softcap >= 0.0f) || !isfinite(softcap))
+
+namespace tv {
+namespace paged {
+namespace {
+
+// What an attention call is given, whatever the cache.
+struct AttnArgs {
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  const int32_t* block_table;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const uint64_t* anc_mask;
+  const float* slopes;
+  int B, T, P, Hq, max_q;
+  float scale, softcap;
+  int window;
+  void* out;
+  float* lse;
+  int32_t* status;
+  void* workspace;
+  size_t ws_bytes;
+  cudaStream_t stream;
+};
+
+tv_status attend(const AttnArgs& a, const CacheArg& cache) {
+  PagedAttnParams p;
+  const PagedCache& c = cache.c;
+  const int Hkv = cache.Hkv, D = cache.D;
+  const bool q8 = cache.format >= 0, f16 = cache.dtype == TV_FP16;
+  if (a.B < 0 || a.T < 0 || a.P < 1 || a.Hq < 1 || a.max_q < 1 || a.window < 0) return TV_ERR_INVALID_ARG;
+  if (!(a.scale >= 0.0f) || !isfinite(a.scale) || !(a.softcap >= 0.0f) || !isfinite(a.softcap))
     return TV_ERR_INVALID_ARG;
-  tv::paged::PagedAttnParams p;
-  tv::PagedCache c;
-  const tv_status st = tv::check_cache(cache, &c);
-  if (st != TV_OK) return st;
-  const int Hkv = cache->Hkv, D = cache->D;
-  if (Hq % Hkv != 0) return TV_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || Hq / Hkv > 128 || B > tv::kMaxSeqs) return TV_ERR_UNSUPPORTED;
-  if (anc_mask && max_q > TV_MAX_NODES) return TV_ERR_UNSUPPORTED;
-  if ((long long)T * Hq > 0x7fffffffll || (long long)B * P > 0x7fffffffll ||
-      ((long long)P << c.page_shift) > 0x7fffffffll - 512)
+  if (a.Hq % Hkv != 0) return TV_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || a.Hq / Hkv > 128 || a.B > kMaxSeqs) return TV_ERR_UNSUPPORTED;
+  if (q8 && a.Hq / Hkv > 16) return TV_ERR_UNSUPPORTED;
+  if (a.anc_mask && a.max_q > TV_MAX_NODES) return TV_ERR_UNSUPPORTED;
+  if ((long long)a.T * a.Hq > 0x7fffffffll || (long long)a.B * a.P > 0x7fffffffll ||
+      ((long long)a.P << c.page_shift) > 0x7fffffffll - 512)
     return TV_ERR_UNSUPPORTED;
-  if (B == 0) return TV_OK;
-  if (!block_table || !q_start || !kv_len || (T > 0 && (!q || !out))) return TV_ERR_INVALID_ARG;
-  p.q_head_stride = tv::stride_or(q_head_stride, Hq, D);
-  p.q_token_stride = tv::stride_or(q_token_stride, T, Hq * p.q_head_stride);
+  if (a.B == 0) return TV_OK;
+  if (!a.block_table || !a.q_start || !a.kv_len || (a.T > 0 && (!a.q || !a.out))) return TV_ERR_INVALID_ARG;
+  p.q_head_stride = stride_or(a.q_head_stride, a.Hq, D);
+  p.q_token_stride = stride_or(a.q_token_stride, a.T, a.Hq * p.q_head_stride);
   if (p.q_token_stride < 0 || p.q_head_stride < 0 || ((p.q_token_stride | p.q_head_stride) & 7))
     return TV_ERR_INVALID_ARG;
   if (p.q_head_stride == 0 || p.q_token_stride == 0) return TV_ERR_UNSUPPORTED;
-  if (Hq == 1) p.q_head_stride = p.q_token_stride;
+  if (a.Hq == 1) p.q_head_stride = p.q_token_stride;
   if (p.q_token_stride % p.q_head_stride != 0 || p.q_token_stride >= (1ll << 39))
     return TV_ERR_UNSUPPORTED;
-  const long long extent[3] = {cache->page_size, Hkv, cache->num_pages};
+  const long long extent[3] = {1ll << c.page_shift, Hkv, c.num_pages};
   long long stride[3] = {c.row_stride, c.head_stride, c.page_stride};
   int order[3];
-  if (!tv::paged::order_strides(extent, stride, D, order)) return TV_ERR_UNSUPPORTED;
-  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15)
+  if (!order_strides(extent, stride, D, order)) return TV_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.out)) & 15)
     return TV_ERR_INVALID_ARG;
-  const tv::paged::PagedPlan pl =
-      tv::paged::paged_plan(max_q, Hkv, Hq / Hkv, D, B, T, (long long)P << c.page_shift);
-  if (!workspace || ws_bytes < pl.bytes() || (reinterpret_cast<uintptr_t>(workspace) & 255))
+  const PagedPlan pl =
+      paged_plan(a.max_q, Hkv, a.Hq / Hkv, D, a.B, a.T, (long long)a.P << c.page_shift, q8);
+  if (!a.workspace || a.ws_bytes < pl.bytes() || (reinterpret_cast<uintptr_t>(a.workspace) & 255))
     return TV_ERR_WORKSPACE;
-  auto encode = tv::paged::tensor_map_encoder();
+  auto encode = tensor_map_encoder();
   if (!encode) return TV_ERR_CUDA;
   CUtensorMap tmQ, tmK, tmV;
-  const int rows = min(cache->page_size, pl.small && !pl.whole ? 64 : 128);
-  if (!tv::paged::map_cache(encode, &tmK, cache->k, cache, stride, order, rows) ||
-      !tv::paged::map_cache(encode, &tmV, cache->v, cache, stride, order, rows))
+  const int rows = min(1 << c.page_shift, pl.small && !pl.whole && !q8 ? 64 : 128);
+  if (!map_cache(encode, &tmK, cache.k, cache, stride, order, rows) ||
+      !map_cache(encode, &tmV, cache.v, cache, stride, order, rows))
     return TV_ERR_INVALID_ARG;
-  if (!pl.small && T > 0) {
+  if (!pl.small && a.T > 0) {
     // q as [tokens][heads][D]; a box is 64 dims of the group's heads of nb tokens
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)a.T};
     const cuuint64_t strides[2] = {(cuuint64_t)p.q_head_stride * 2, (cuuint64_t)p.q_token_stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)(Hq / Hkv), (cuuint32_t)pl.nb}, estr[3] = {1, 1, 1};
-    if (encode(&tmQ, cache->dtype == TV_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-               3, const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint32_t box[3] = {64, (cuuint32_t)(a.Hq / Hkv), (cuuint32_t)pl.nb}, estr[3] = {1, 1, 1};
+    if (encode(&tmQ, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+               3, const_cast<void*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return TV_ERR_INVALID_ARG;
   } else {
     tmQ = tmK;  // not read
   }
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.part_bytes);
   p.desc = reinterpret_cast<int4*>(ws + pl.part_bytes + pl.ml_bytes);
-  p.late = reinterpret_cast<tv::paged::Late*>(ws + pl.part_bytes + pl.ml_bytes + pl.desc_bytes);
+  p.late = reinterpret_cast<Late*>(ws + pl.part_bytes + pl.ml_bytes + pl.desc_bytes);
   p.any_late = reinterpret_cast<unsigned long long*>(p.late + pl.ctas);
-  p.wait_limit = tv::paged::wait_limit();
-  p.q = static_cast<const uint16_t*>(q);
-  p.table = block_table;
-  p.q_start = q_start;
-  p.kv_len = kv_len;
-  p.anc = anc_mask;
-  p.slopes = slopes;
-  p.out = static_cast<uint16_t*>(out);
-  p.lse = lse;
-  p.status = status;
-  p.B = B;
-  p.T = T;
-  p.P = P;
-  p.Hq = Hq;
+  p.wait_limit = wait_limit();
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.k_scale = cache.k_scale;
+  p.v_scale = cache.v_scale;
+  p.f16 = f16;
+  p.table = a.block_table;
+  p.q_start = a.q_start;
+  p.kv_len = a.kv_len;
+  p.anc = a.anc_mask;
+  p.slopes = a.slopes;
+  p.out = static_cast<uint16_t*>(a.out);
+  p.lse = a.lse;
+  p.status = a.status;
+  p.B = a.B;
+  p.T = a.T;
+  p.P = a.P;
+  p.Hq = a.Hq;
   p.Hkv = Hkv;
-  p.G = Hq / Hkv;
-  p.W = (max_q + 63) / 64;
-  p.window = window;
+  p.G = a.Hq / Hkv;
+  p.W = (a.max_q + 63) / 64;
+  p.window = a.window;
   p.num_pages = c.num_pages;
   p.page_shift = c.page_shift;
   for (int i = 0; i < 3; ++i) {
@@ -355,19 +388,19 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   p.tq = pl.tq;
   p.min_share = pl.min_share;
   p.share_lanes = 0;  // (a lane per query tile of the largest chunk, where the kernels' threads suffice)
-  while (p.share_lanes < 5 && (pl.tq << p.share_lanes) < max_q && (B << (p.share_lanes + 1)) <= 192)
+  while (p.share_lanes < 5 && (pl.tq << p.share_lanes) < a.max_q && (a.B << (p.share_lanes + 1)) <= 192)
     ++p.share_lanes;
   p.whole = pl.whole;
-  p.out_sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+  p.out_sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   p.merge = pl.merge;
   p.ready = reinterpret_cast<unsigned long long*>(ws + pl.part_bytes + pl.ml_bytes + pl.desc_bytes +
                                                   pl.late_bytes);
-  p.token = tv::paged::next_token();
-  const float sc = scale == 0.0f ? 1.0f / sqrtf((float)D) : scale;
-  p.scale_log2 = sc * tv::paged::kLog2e;
+  p.token = next_token();
+  const float sc = a.scale == 0.0f ? 1.0f / sqrtf((float)D) : a.scale;
+  p.scale_log2 = sc * kLog2e;
   // (caps at the ends of the 32-bit range: a product of 0 has a score of 0 all the same)
-  p.softcap_log2 = fminf(softcap * tv::paged::kLog2e, FLT_MAX);
-  p.cap_in = softcap > 0.0f ? fminf(sc / softcap, 1e30f) : 0.0f;
+  p.softcap_log2 = fminf(a.softcap * kLog2e, FLT_MAX);
+  p.cap_in = a.softcap > 0.0f ? fminf(sc / a.softcap, 1e30f) : 0.0f;
   // The cubic's coefficients for products as they are, in the log2 domain.  For a large cap the higher
   // ones fade to 0 and nearly every score is taken by it: the function for the others is off by
   // some 2^-23 of the cap, not of the score.  For caps below 1e-5 of the scale, whose coefficients would
@@ -377,21 +410,82 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
   if (p.cap_in <= 1e5f) {
     const float a2 = p.cap_in * p.cap_in;
     float f = p.scale_log2;
-    for (int i = 0; i < 4; ++i, f *= a2) p.cap_q[i] = f * tv::paged::kTanhC[i];
-    p.cap_top = fminf(tv::paged::kTanhSmall * tv::paged::kTanhSmall / a2, 1e36f);  // (squares stay finite)
+    for (int i = 0; i < 4; ++i, f *= a2) p.cap_q[i] = f * kTanhC[i];
+    p.cap_top = fminf(kTanhSmall * kTanhSmall / a2, 1e36f);  // (squares stay finite)
   }
-  const bool bias = slopes || (anc_mask && window > 0 && window < 64 * p.W);
-  const bool f16 = cache->dtype == TV_FP16;
-  cudaError_t e = pl.small ? tv::paged::launch_rows(pl, D, f16, bias || softcap > 0.0f, tmK, tmV, p, stream)
-                        : tv::paged::launch_tc(pl, D, f16, bias, tmQ, tmK, tmV, p, stream);
+  const bool bias = a.slopes || (a.anc_mask && a.window > 0 && a.window < 64 * p.W);
+  const bool mod = bias || a.softcap > 0.0f;
+  cudaError_t e;
+  if (q8)
+    e = cache.format == TV_E4M3 ? launch_rows_e4m3(pl, D, mod, tmK, tmV, p, a.stream)
+                                : launch_rows_int8(pl, D, mod, tmK, tmV, p, a.stream);
+  else
+    e = pl.small ? launch_rows(pl, D, f16, mod, tmK, tmV, p, a.stream)
+                 : launch_tc(pl, D, f16, bias, tmQ, tmK, tmV, p, a.stream);
   if (e == cudaSuccess && pl.merge)
-    e = D == 128 ? (f16 ? tv::paged::launch_merge<128, true>(pl, p, stream)
-                        : tv::paged::launch_merge<128, false>(pl, p, stream))
-                 : (f16 ? tv::paged::launch_merge<64, true>(pl, p, stream)
-                        : tv::paged::launch_merge<64, false>(pl, p, stream));
+    e = D == 128 ? (f16 ? launch_merge<128, true>(pl, p, a.stream)
+                        : launch_merge<128, false>(pl, p, a.stream))
+                 : (f16 ? launch_merge<64, true>(pl, p, a.stream)
+                        : launch_merge<64, false>(pl, p, a.stream));
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return TV_ERR_CUDA;
   }
   return TV_OK;
+}
+
+}  // namespace
+}  // namespace paged
+}  // namespace tv
+
+extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                   const tv_paged_cache* cache, const int32_t* block_table,
+                                   const int32_t* q_start, const int32_t* kv_len,
+                                   const uint64_t* anc_mask, const float* slopes, int B, int T,
+                                   int P, int Hq, int max_q, float scale, float softcap, int window,
+                                   void* out, float* lse, int32_t* status, void* workspace,
+                                   size_t ws_bytes, cudaStream_t stream) {
+  TV_NVTX_RANGE("tv_attn_paged");
+  tv::paged::CacheArg c{};
+  const tv_status st = tv::check_cache(cache, &c.c);
+  if (st != TV_OK) return st;
+  c.k = cache->k;
+  c.v = cache->v;
+  c.Hkv = cache->Hkv;
+  c.D = cache->D;
+  c.dtype = cache->dtype;
+  c.format = -1;
+  return tv::paged::attend({q, q_token_stride, q_head_stride, block_table, q_start, kv_len, anc_mask, slopes, B, T, P,
+                            Hq, max_q, scale, softcap, window, out, lse, status, workspace, ws_bytes, stream}, c);
+}
+
+extern "C" size_t tv_attn_paged_q8_workspace_size(int max_q, int Hq, int Hkv, int D) {
+  if (max_q < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128))
+    return 0;
+  return tv::paged::paged_plan(max_q, Hkv, Hq / Hkv, D, 0, 0, 0, true).bytes();
+}
+
+extern "C" tv_status tv_attn_paged_q8(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                                      const tv_q8_cache* cache, const int32_t* block_table,
+                                      const int32_t* q_start, const int32_t* kv_len,
+                                      const uint64_t* anc_mask, const float* slopes, int B, int T,
+                                      int P, int Hq, int max_q, float scale, float softcap, int window,
+                                      void* out, float* lse, int32_t* status, void* workspace,
+                                      size_t ws_bytes, cudaStream_t stream) {
+  TV_NVTX_RANGE("tv_attn_paged_q8");
+  tv::paged::CacheArg c{};
+  tv::Q8Cache rows;
+  const tv_status st = tv::check_q8_cache(cache, &rows);
+  if (st != TV_OK) return st;
+  c.c = rows;
+  c.k = cache->k;
+  c.v = cache->v;
+  c.Hkv = cache->Hkv;
+  c.D = cache->D;
+  c.dtype = cache->dtype;
+  c.format = cache->format;
+  c.k_scale = cache->k_scale;
+  c.v_scale = cache->v_scale;
+  return tv::paged::attend({q, q_token_stride, q_head_stride, block_table, q_start, kv_len, anc_mask, slopes, B, T, P,
+                            Hq, max_q, scale, softcap, window, out, lse, status, workspace, ws_bytes, stream}, c);
 }

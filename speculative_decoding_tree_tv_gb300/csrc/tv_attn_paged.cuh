@@ -49,6 +49,8 @@ struct Late {
 struct PagedAttnParams {
   const uint16_t* q;
   long long q_token_stride, q_head_stride;
+  const uint8_t* k_scale;  // of an 8-bit cache: [pages, heads, rows]
+  const uint8_t* v_scale;
   const int32_t* table;
   const int32_t* q_start;
   const int32_t* kv_len;
@@ -70,6 +72,7 @@ struct PagedAttnParams {
   int min_share;    // least cost of a share
   int share_lanes;  // log2 of the lanes that look at one sequence (1 << share_lanes) * B threads at most
   int whole;        // one unit a CTA, none is split
+  int f16;          // 16-bit tensors are fp16 (the 8-bit cache's kernels)
   int out_sectors;  // out lies on a 32-byte boundary
   int merge;        // a merge kernel joins the parts of split units, else the CTA a unit begins in
   unsigned long long token;      // this call's mark in `ready`
@@ -159,6 +162,15 @@ __device__ __forceinline__ bool wait_within(uint64_t* bar, uint32_t parity, long
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long limit) {
   return __all_sync(0xffffffffu, wait_within(bar, parity, limit));
+}
+// Eight bytes to shared memory, zeros where `valid` is not set; they count on the barrier that
+// the thread arrives at next with cp_arrive.
+__device__ __forceinline__ void cp_async8(void* dst, const void* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 8 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -588,6 +600,14 @@ struct PageFeed {
   }
 };
 
+// The scale bytes of the eight rows from `row` of (page, head), zeros where there is no page.
+__device__ __forceinline__ void load_scales(const PagedAttnParams& p, uint8_t* dst, const uint8_t* src, int page,
+                                            int head, int row) {
+  const bool valid = TV_CHECK(page >= 0) && page < p.num_pages;
+  const long long at = valid ? (((long long)page * p.Hkv + head) << p.page_shift) + row : 0;
+  cp_async8(dst, src + at, valid);
+}
+
 // How a call runs: the kernel, its CTAs, and the layout of the workspace.
 struct PagedPlan {
   bool small;  // units of at most 16 rows: paged_rows_kernel
@@ -600,10 +620,15 @@ struct PagedPlan {
 };
 
 constexpr int kTcKeys = 128;  // keys of a tile of the tcgen05 kernel
+constexpr int kQ8Keys = 128;  // keys of a stage of the 8-bit cache's small kernel
 
 // bias: slopes, or tree distances that the window reaches (mod: those or a cap)
 cudaError_t launch_rows(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmK,
                         const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
+cudaError_t launch_rows_e4m3(const PagedPlan& pl, int D, bool mod, const CUtensorMap& tmK,
+                             const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
+cudaError_t launch_rows_int8(const PagedPlan& pl, int D, bool mod, const CUtensorMap& tmK,
+                             const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
 cudaError_t launch_tc(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
                       const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
                       cudaStream_t stream);

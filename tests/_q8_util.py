@@ -88,3 +88,45 @@ def make_q8(seed, lens, Hq, Hkv, D, page, fmt, dtype="bf16", layout="heads", spr
     c["q8"] = (moved[0], moved[1], sides[2].to(dev), sides[3].to(dev))
     c["fmt"] = fmt
     return c
+
+
+def check_attn_q8(got_out, got_lse, ref, case, dtype, Hkv, scale=0.0, what=""):
+    """Outputs against 64 bits (ref: attn_ref's).  Beside what attn_ref bounds:
+    q, scaled by a power of two to [1, 2) at its largest, is rounded to fp16 below 2^-14 of that (2^-25 of the
+    row's largest at most, times sum |k| in a score; elsewhere it is exact); a probability times its V row's scale is rounded
+    to fp16 (2^-11 of it) or, far below the largest V scale, to a multiple of 2^-30 of it, 2^-31 off: a row's
+    largest value is above half of what its scale can hold, the kept scale at most twice the largest and a row's
+    sum at least 1, so that is below 2^-29 of the largest |v| a row; and the output is rounded once."""
+    out, lse, spread, xerr, _ = ref
+    D = case["q"].shape[2]
+    u = torch.finfo(got_out.dtype).eps / 2
+    scale = scale or D**-0.5
+    qerr, far, at = [], [], 0
+    for b, (L, n) in enumerate(case["lens"]):
+        if n == 0:
+            continue
+        kr, vr = case["rows"][b]
+        q = case["q"][at:at + n].cpu().double()
+        ksum = kr.abs().nan_to_num(0.0).sum(2).amax(0).repeat_interleave(q.shape[1] // Hkv)
+        qerr.append(scale * 2.0**-25 * q.abs().nan_to_num(0.0).amax(2) * ksum)
+        vmax = vr.abs().nan_to_num(0.0).amax((0, 2)).repeat_interleave(q.shape[1] // Hkv)
+        far.append((2.0**-29 * (L + n) * vmax).expand(n, -1))
+        at += n
+    xerr = xerr + torch.cat(qerr)
+    got = got_out.cpu().double()
+    tol = (spread * (2.0**-11 + 2 * xerr[..., None] + 2.0**-19) + torch.cat(far)[..., None]
+           + u * (out.abs() + 2.0**-11 * spread) + 1e-30)
+    if got_out.dtype == torch.float16:
+        tol = tol + 2.0**-25
+    assert torch.isfinite(got).all(), f"{what}: non-finite output"
+    worst = ((got - out).abs() / tol).max().item() if got.numel() else 0.0
+    assert worst <= 1.0, f"{what}: output {worst:.3g} of its tolerance"
+    if got_lse is not None:
+        g = got_lse.cpu().double()
+        fin = torch.isfinite(lse)
+        assert torch.equal(fin, torch.isfinite(g)), f"{what}: lse finiteness"
+        assert bool((g[~fin] == -float("inf")).all()), f"{what}: lse of an empty row"
+        ltol = 2 * xerr + 2.0**-21 + 2.0**-21 * torch.where(fin, lse.abs(), torch.zeros_like(lse))
+        bad = ((g - lse).abs() / ltol)[fin]
+        assert bad.numel() == 0 or bad.max().item() <= 1.0, f"{what}: lse {bad.max().item():.3g}"
+    return worst
