@@ -30,6 +30,9 @@
  *   tv_attn_paged     attention of every new token over its sequence's pages
  *   tv_commit_paged   the accepted branch's K/V rows to consecutive positions
  *
+ *   tv_attn_paged_prefix  the same behind prefixes that sequences share, each
+ *                     read once for all of them
+ *
  * and over an 8-bit paged cache, which holds twice the tokens:
  *
  *   tv_paged_append_q8  new K/V rows, quantised, into their slots
@@ -360,7 +363,8 @@ tv_status tv_debug_set_wait_limit(long long cycles);
  *                       4 expand, 5 attention, 6 commit, 7 expected,
  *                       8 top-n selection, 9 library, 10 pages,
  *                       11 to 13 paged attention, 14 the 8-bit cache,
- *                       15 and 16 its attention.  Host call; it must not
+ *                       15 and 16 its attention, 17 and 18 attention
+ *                       behind shared prefixes.  Host call; it must not
  *                       overlap a launch of this library on the device.
  *                       TV_ERR_INVALID_ARG if site is NULL, TV_ERR_CUDA if
  *                       the device reports an error.
@@ -689,6 +693,39 @@ tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_st
                         const float* slopes, int B, int T, int P, int Hq, int max_q, float scale,
                         float softcap, int window, void* out, float* lse, int32_t* status,
                         void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * tv_attn_paged_prefix -- tv_attn_paged for sequences of which some share a long prefix (a system
+ * prompt, a document): the prefix's rows are read once for all tokens of its sequences.
+ *
+ * Group g is the sequences group_start[g] .. group_start[g + 1] - 1, which follow one another in the batch.  Its
+ * prefix is prefix_len[g] rows in the pages prefix_table[g, ..]; row j is at position j.  Sequence b of the
+ * group has its own kv_len[b] cached rows and its new tokens behind it, in its own block_table row: its
+ * row i is at position prefix_len[g] + i.  Tokens see the prefix (as far as the window reaches) and their own
+ * rows as in tv_attn_paged; out and lse are over both.  Sequences before the first group or behind the last
+ * have no prefix.  No page need be held twice: to tv_page_map a prefix is a sequence of its
+ * own, with its own table row, that grows once and is released when its last user is.
+ *
+ *   prefix_table int32 [groups, prefix_P]; prefix_len int32 [groups]; group_start int32 [groups + 1], ascending
+ *               from 0 or more to B or less.  groups = 0: as tv_attn_paged (the three are not read then).
+ *   status      as tv_attn_paged's, and TV_ERR_INVALID_ARG for the sequences of a malformed group, with a
+ *               prefix_len < 0 or past prefix_P * page_size (the prefix then counts as hidden), or with a
+ *               page id outside [0, num_pages) among the prefix's pages that the window reaches (its rows count
+ *               as hidden).
+ *   workspace   tv_attn_paged_prefix_workspace_size() bytes (32-bit rows of the prefixes' sums, and what both
+ *               passes need), otherwise as tv_attn_paged's.
+ * The other arguments, statuses and limits are tv_attn_paged's; groups <= 4096, groups * prefix_P and
+ * (P + prefix_P) * page_size + 512 below 2^31.
+ */
+size_t tv_attn_paged_prefix_workspace_size(int max_q, int T, int groups, int Hq, int Hkv, int D);
+tv_status tv_attn_paged_prefix(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                               const tv_paged_cache* cache, const int32_t* prefix_table,
+                               const int32_t* prefix_len, const int32_t* group_start, int groups,
+                               int prefix_P, const int32_t* block_table, const int32_t* q_start,
+                               const int32_t* kv_len, const uint64_t* anc_mask, const float* slopes,
+                               int B, int T, int P, int Hq, int max_q, float scale, float softcap,
+                               int window, void* out, float* lse, int32_t* status, void* workspace,
+                               size_t ws_bytes, cudaStream_t stream);
 
 /*
  * tv_commit_paged -- tv_commit_path over a paged cache: the accepted branch's

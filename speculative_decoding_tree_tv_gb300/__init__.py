@@ -17,5 +17,5 @@ from .api import (  # noqa: F401
     workspace, attn_workspace_size, attn_plan, greedy_workspace_size, sample_workspace_size,
     expand_workspace_size, page_map, paged_append, attn_paged, commit_paged,
     attn_paged_workspace_size, paged_append_q8, paged_read_q8, commit_paged_q8, attn_paged_q8,
-    attn_paged_q8_workspace_size,
+    attn_paged_q8_workspace_size, attn_paged_prefix, attn_paged_prefix_workspace_size,
 )

@@ -97,6 +97,9 @@ _SIGS = {
     "tv_attn_paged_q8_workspace_size": (_SZ, [_I, _I, _I, _I]),
     "tv_attn_paged_q8": (_I, [_P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _I,
                               _P, _P, _P, _P, _SZ, _P]),
+    "tv_attn_paged_prefix_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "tv_attn_paged_prefix": (_I, [_P, _I64, _I64, _P, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
+                                  _F, _F, _I, _P, _P, _P, _P, _SZ, _P]),
     "tv_commit_paged_q8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
     "tv_commit_paged": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P]),
 }

@@ -2,7 +2,6 @@
 from __future__ import annotations
 
 import ctypes
-import functools
 import struct
 from typing import Callable, Optional
 
@@ -15,7 +14,7 @@ __all__ = ["tree_build", "attn_verify", "accept_greedy", "accept_sample", "expan
            "expand_tree", "commit_path", "expected_accept", "build_spine_tree", "spine_ratio_update", "workspace", "attn_workspace_size", "attn_plan", "greedy_workspace_size",
            "sample_workspace_size", "expand_workspace_size", "page_map", "paged_append", "attn_paged",
            "commit_paged", "attn_paged_workspace_size", "paged_append_q8", "paged_read_q8", "commit_paged_q8",
-           "attn_paged_q8", "attn_paged_q8_workspace_size"]
+           "attn_paged_q8", "attn_paged_q8_workspace_size", "attn_paged_prefix", "attn_paged_prefix_workspace_size"]
 
 _workspaces: dict = {}
 
@@ -683,7 +682,7 @@ def attn_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
 
 
 def _attn(fn, name, ws_size, cache, k_pages, dtype, q, block_table, q_start, kv_len, max_q, anc_mask, scale, softcap,
-          window, slopes, out, lse, status, want_lse, ws):
+          window, slopes, out, lse, status, want_lse, ws, prefix=(), groups=None):
     dev = k_pages.device
     _, Hkv, _, Dc = k_pages.shape
     max_q = int(max_q)
@@ -730,16 +729,63 @@ def _attn(fn, name, ws_size, cache, k_pages, dtype, q, block_table, q_start, kv_
     else:
         _need(status, "status", _I32, (B,), dev)
     if ws is None:  # from torch's allocator: ordered by stream, and a captured graph's own
-        size = (ws_size if dev.index == _current_device() else functools.partial(_ws_size, ws_size, dev))(
-            max_q, Hq, Hkv, D)
+        sizes = (max_q, Hq, Hkv, D) if groups is None else (max_q, T, groups, Hq, Hkv, D)
+        size = ws_size(*sizes) if dev.index == _current_device() else _ws_size(ws_size, dev, *sizes)
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
     else:
         _need(ws, "ws", torch.uint8, None, dev)
     _call(fn, name, dev, q.data_ptr(), strides[0], strides[1], cache,
-          block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), _ptr(anc_mask),
+          *prefix, block_table.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), _ptr(anc_mask),
           _ptr(slopes), B, T, P, Hq, max_q, scale, softcap, window, out.data_ptr(), _ptr(lse),
           status.data_ptr(), ws.data_ptr(), ws.numel())
     return out, lse, status
+
+
+def attn_paged_prefix_workspace_size(max_q, T, groups, Hq, Hkv, D, device=None) -> int:
+    """Bytes of attn_paged_prefix's workspace on `device` (the current one)."""
+    return _ws_size(lib.tv_attn_paged_prefix_workspace_size, device, max_q, T, groups, Hq, Hkv, D)
+
+
+def _prefix(dev, prefix_table, prefix_len, group_start):
+    """The prefix arguments of a call: pointers, groups and table width."""
+    try:
+        groups, P = prefix_table.shape
+        good = (P <= _MOST
+                and prefix_table.dtype is _I32 and prefix_table.device == dev and prefix_table.is_contiguous()
+                and prefix_len.dtype is _I32 and prefix_len.shape == (groups,) and prefix_len.device == dev
+                and prefix_len.is_contiguous()
+                and group_start.dtype is _I32 and group_start.shape == (groups + 1,) and group_start.device == dev
+                and group_start.is_contiguous())
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        _need(prefix_table, "prefix_table", _I32, None, dev)
+        if prefix_table.dim() != 2:
+            raise ValueError("prefix_table must have shape [groups, prefix_P]")
+        groups, P = prefix_table.shape
+        _fits(prefix_P=P)
+        _need(prefix_len, "prefix_len", _I32, (groups,), dev)
+        _need(group_start, "group_start", _I32, (groups + 1,), dev)
+    return prefix_table.data_ptr(), prefix_len.data_ptr(), group_start.data_ptr(), groups, P
+
+
+def attn_paged_prefix(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, prefix_table: torch.Tensor,
+                      prefix_len: torch.Tensor, group_start: torch.Tensor, block_table: torch.Tensor,
+                      q_start: torch.Tensor, kv_len: torch.Tensor, max_q: int,
+                      anc_mask: Optional[torch.Tensor] = None, scale: float = 0.0, softcap: float = 0.0,
+                      window: int = 0, slopes: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                      want_lse: bool = True, ws: Optional[torch.Tensor] = None):
+    """attn_paged for sequences that share prefixes, each read once: sequences group_start[g] ..
+    group_start[g + 1] - 1 stand behind the prefix_len[g] rows in the pages prefix_table[g].
+    prefix_table int32 [groups, prefix_P]; prefix_len int32 [groups]; group_start int32 [groups+1];
+    block_table, kv_len and the other arguments as attn_paged's, of the sequences' own rows.
+    Returns (out [T, Hq, D], lse float32 [T, Hq], status int32 [B])."""
+    cache = _cache(k_pages, v_pages)
+    prefix = _prefix(k_pages.device, prefix_table, prefix_len, group_start)
+    return _attn(lib.tv_attn_paged_prefix, "tv_attn_paged_prefix", lib.tv_attn_paged_prefix_workspace_size, cache,
+                 k_pages, k_pages.dtype, q, block_table, q_start, kv_len, max_q, anc_mask, scale, softcap, window,
+                 slopes, out, lse, status, want_lse, ws, prefix, prefix[3])
 
 
 def commit_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,

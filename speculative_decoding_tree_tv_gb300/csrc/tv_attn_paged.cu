@@ -34,14 +34,17 @@ __device__ __forceinline__ void merge_status(const PagedAttnParams& p) {
 
 // A thread joins kC chunks (of four floats) of one row, all its loads of a batch of parts
 // in flight.
-template <int D, bool F16, bool TC>
+// PRE: of a pass of an attention with shared prefixes.
+template <int D, bool F16, bool TC, bool PRE>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnParams p, int nb) {
   constexpr int kChunks = D / 4, kRows = TC ? 256 : 16;
   constexpr int kC = TC ? 4 : kChunks * kRows / kMergeThreads;  // a small unit: one block
   pdl_trigger();
   pdl_wait();
   const int i = blockIdx.x;
-  const int4 d = p.desc[i];
+  int4 d = p.desc[i];
+  const bool joins = PRE && (d.w & kPartsPre);
+  if (PRE) d.w &= ~kPartsPre;
   merge_status(p);
   if (d.w == 0) return;
   const int row = TC ? threadIdx.x : threadIdx.x / (kChunks / kC);
@@ -100,6 +103,20 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
         a[c].w = fmaf(e, v[j][c].w, a[c].w);
       }
     }
+  }
+  if (PRE && p.pass == 1) {
+    float4* pre = reinterpret_cast<float4*>(p.pre + oidx * D) + c0;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) pre[c] = a[c];
+    if (c0 == 0) p.pre_ml[oidx] = make_float2(M, l);
+    return;
+  }
+  if (joins) {
+    float fo, fp;
+    join_factors(p.pre_ml[oidx], M, l, fo, fp);
+    const float4* pre = reinterpret_cast<const float4*>(p.pre + oidx * D) + c0;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) join_rows(a[c], pre[c], fo, fp);
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint2* out = reinterpret_cast<uint2*>(p.out + oidx * D) + c0;
@@ -247,13 +264,18 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
   return pl;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool PRE>
 cudaError_t launch_merge(const PagedPlan& pl, const PagedAttnParams& p, cudaStream_t stream) {
   if (pl.small)
-    return launch_pdl(paged_merge_kernel<D, F16, false>, dim3(pl.ctas, 1), dim3(kMergeThreads), 0,
+    return launch_pdl(paged_merge_kernel<D, F16, false, PRE>, dim3(pl.ctas, 1), dim3(kMergeThreads), 0,
                       stream, p, pl.nb);
-  return launch_pdl(paged_merge_kernel<D, F16, true>, dim3(pl.ctas, D / 16), dim3(kMergeThreads), 0,
+  return launch_pdl(paged_merge_kernel<D, F16, true, PRE>, dim3(pl.ctas, D / 16), dim3(kMergeThreads), 0,
                     stream, p, pl.nb);
+}
+template <bool PRE>
+cudaError_t launch_merge(const PagedPlan& pl, int D, bool f16, const PagedAttnParams& p, cudaStream_t stream) {
+  if (D == 128) return f16 ? launch_merge<128, true, PRE>(pl, p, stream) : launch_merge<128, false, PRE>(pl, p, stream);
+  return f16 ? launch_merge<64, true, PRE>(pl, p, stream) : launch_merge<64, false, PRE>(pl, p, stream);
 }
 
 }  // namespace
@@ -277,6 +299,18 @@ namespace tv {
 namespace paged {
 namespace {
 
+tv_status cache_arg(const tv_paged_cache* cache, CacheArg* c) {
+  const tv_status st = check_cache(cache, &c->c);
+  if (st != TV_OK) return st;
+  c->k = cache->k;
+  c->v = cache->v;
+  c->Hkv = cache->Hkv;
+  c->D = cache->D;
+  c->dtype = cache->dtype;
+  c->format = -1;
+  return TV_OK;
+}
+
 // What an attention call is given, whatever the cache.
 struct AttnArgs {
   const void* q;
@@ -297,23 +331,50 @@ struct AttnArgs {
   cudaStream_t stream;
 };
 
-tv_status attend(const AttnArgs& a, const CacheArg& cache) {
-  PagedAttnParams p;
-  const PagedCache& c = cache.c;
+// The prefixes that groups of sequences share.
+struct PrefixArgs {
+  const int32_t* table;
+  const int32_t* len;
+  const int32_t* group_start;
+  int groups, P;
+};
+
+tv_status check_attn(const AttnArgs& a, const CacheArg& cache) {
   const int Hkv = cache.Hkv, D = cache.D;
-  const bool q8 = cache.format >= 0, f16 = cache.dtype == TV_FP16;
   if (a.B < 0 || a.T < 0 || a.P < 1 || a.Hq < 1 || a.max_q < 1 || a.window < 0) return TV_ERR_INVALID_ARG;
   if (!(a.scale >= 0.0f) || !isfinite(a.scale) || !(a.softcap >= 0.0f) || !isfinite(a.softcap))
     return TV_ERR_INVALID_ARG;
   if (a.Hq % Hkv != 0) return TV_ERR_INVALID_ARG;
   if ((D != 64 && D != 128) || a.Hq / Hkv > 128 || a.B > kMaxSeqs) return TV_ERR_UNSUPPORTED;
-  if (q8 && a.Hq / Hkv > 16) return TV_ERR_UNSUPPORTED;
+  if (cache.format >= 0 && a.Hq / Hkv > 16) return TV_ERR_UNSUPPORTED;
   if (a.anc_mask && a.max_q > TV_MAX_NODES) return TV_ERR_UNSUPPORTED;
   if ((long long)a.T * a.Hq > 0x7fffffffll || (long long)a.B * a.P > 0x7fffffffll ||
-      ((long long)a.P << c.page_shift) > 0x7fffffffll - 512)
+      ((long long)a.P << cache.c.page_shift) > 0x7fffffffll - 512)
     return TV_ERR_UNSUPPORTED;
   if (a.B == 0) return TV_OK;
   if (!a.block_table || !a.q_start || !a.kv_len || (a.T > 0 && (!a.q || !a.out))) return TV_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.out)) & 15)
+    return TV_ERR_INVALID_ARG;
+  return TV_OK;
+}
+
+// One pass over a paged cache: a plan, the kernels' arguments and tensor maps.
+struct Pass {
+  PagedPlan pl;
+  PagedAttnParams p;
+  CUtensorMap tmQ, tmK, tmV;
+  bool bias;
+};
+
+// chunk: the tokens of a sequence, as far as the host knows them.
+tv_status make_pass(const AttnArgs& a, const CacheArg& cache, const PagedPlan& pl, int chunk, uint8_t* ws,
+                    Pass* out) {
+  out->pl = pl;
+  PagedAttnParams& p = out->p;
+  p = PagedAttnParams{};
+  const PagedCache& c = cache.c;
+  const int Hkv = cache.Hkv, D = cache.D;
+  const bool q8 = cache.format >= 0, f16 = cache.dtype == TV_FP16;
   p.q_head_stride = stride_or(a.q_head_stride, a.Hq, D);
   p.q_token_stride = stride_or(a.q_token_stride, a.T, a.Hq * p.q_head_stride);
   if (p.q_token_stride < 0 || p.q_head_stride < 0 || ((p.q_token_stride | p.q_head_stride) & 7))
@@ -326,15 +387,9 @@ tv_status attend(const AttnArgs& a, const CacheArg& cache) {
   long long stride[3] = {c.row_stride, c.head_stride, c.page_stride};
   int order[3];
   if (!order_strides(extent, stride, D, order)) return TV_ERR_UNSUPPORTED;
-  if ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.out)) & 15)
-    return TV_ERR_INVALID_ARG;
-  const PagedPlan pl =
-      paged_plan(a.max_q, Hkv, a.Hq / Hkv, D, a.B, a.T, (long long)a.P << c.page_shift, q8);
-  if (!a.workspace || a.ws_bytes < pl.bytes() || (reinterpret_cast<uintptr_t>(a.workspace) & 255))
-    return TV_ERR_WORKSPACE;
   auto encode = tensor_map_encoder();
   if (!encode) return TV_ERR_CUDA;
-  CUtensorMap tmQ, tmK, tmV;
+  CUtensorMap &tmQ = out->tmQ, &tmK = out->tmK, &tmV = out->tmV;
   const int rows = min(1 << c.page_shift, pl.small && !pl.whole && !q8 ? 64 : 128);
   if (!map_cache(encode, &tmK, cache.k, cache, stride, order, rows) ||
       !map_cache(encode, &tmV, cache.v, cache, stride, order, rows))
@@ -352,7 +407,6 @@ tv_status attend(const AttnArgs& a, const CacheArg& cache) {
   } else {
     tmQ = tmK;  // not read
   }
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.part_bytes);
   p.desc = reinterpret_cast<int4*>(ws + pl.part_bytes + pl.ml_bytes);
@@ -388,7 +442,7 @@ tv_status attend(const AttnArgs& a, const CacheArg& cache) {
   p.tq = pl.tq;
   p.min_share = pl.min_share;
   p.share_lanes = 0;  // (a lane per query tile of the largest chunk, where the kernels' threads suffice)
-  while (p.share_lanes < 5 && (pl.tq << p.share_lanes) < a.max_q && (a.B << (p.share_lanes + 1)) <= 192)
+  while (p.share_lanes < 5 && (pl.tq << p.share_lanes) < chunk && (a.B << (p.share_lanes + 1)) <= 192)
     ++p.share_lanes;
   p.whole = pl.whole;
   p.out_sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
@@ -413,25 +467,114 @@ tv_status attend(const AttnArgs& a, const CacheArg& cache) {
     for (int i = 0; i < 4; ++i, f *= a2) p.cap_q[i] = f * kTanhC[i];
     p.cap_top = fminf(kTanhSmall * kTanhSmall / a2, 1e36f);  // (squares stay finite)
   }
-  const bool bias = a.slopes || (a.anc_mask && a.window > 0 && a.window < 64 * p.W);
-  const bool mod = bias || a.softcap > 0.0f;
-  cudaError_t e;
-  if (q8)
-    e = cache.format == TV_E4M3 ? launch_rows_e4m3(pl, D, mod, tmK, tmV, p, a.stream)
-                                : launch_rows_int8(pl, D, mod, tmK, tmV, p, a.stream);
-  else
-    e = pl.small ? launch_rows(pl, D, f16, mod, tmK, tmV, p, a.stream)
-                 : launch_tc(pl, D, f16, bias, tmQ, tmK, tmV, p, a.stream);
-  if (e == cudaSuccess && pl.merge)
-    e = D == 128 ? (f16 ? launch_merge<128, true>(pl, p, a.stream)
-                        : launch_merge<128, false>(pl, p, a.stream))
-                 : (f16 ? launch_merge<64, true>(pl, p, a.stream)
-                        : launch_merge<64, false>(pl, p, a.stream));
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();
-    return TV_ERR_CUDA;
-  }
+  out->bias = a.slopes || (a.anc_mask && a.window > 0 && a.window < 64 * p.W);
   return TV_OK;
+}
+
+cudaError_t launch_pass(const Pass& s, const CacheArg& cache, cudaStream_t stream) {
+  const PagedPlan& pl = s.pl;
+  const PagedAttnParams& p = s.p;
+  const int D = cache.D;
+  const bool f16 = cache.dtype == TV_FP16, mod = s.bias || p.softcap_log2 > 0.0f, pre = p.pass != 0;
+  cudaError_t e;
+  if (cache.format >= 0)
+    e = cache.format == TV_E4M3 ? launch_rows_e4m3(pl, D, mod, s.tmK, s.tmV, p, stream)
+                                : launch_rows_int8(pl, D, mod, s.tmK, s.tmV, p, stream);
+  else if (pl.small)
+    e = (pre ? launch_rows_prefix : launch_rows)(pl, D, f16, mod, s.tmK, s.tmV, p, stream);
+  else
+    e = (pre ? launch_tc_prefix : launch_tc)(pl, D, f16, s.bias, s.tmQ, s.tmK, s.tmV, p, stream);
+  if (e == cudaSuccess && pl.merge)
+    e = pre ? launch_merge<true>(pl, D, f16, p, stream) : launch_merge<false>(pl, D, f16, p, stream);
+  return e;
+}
+
+tv_status launched(cudaError_t e) {
+  if (e == cudaSuccess) return TV_OK;
+  (void)cudaGetLastError();
+  return TV_ERR_CUDA;
+}
+
+tv_status attend(const AttnArgs& a, const CacheArg& cache) {
+  tv_status st = check_attn(a, cache);
+  if (st != TV_OK || a.B == 0) return st;
+  const PagedPlan pl = paged_plan(a.max_q, cache.Hkv, a.Hq / cache.Hkv, cache.D, a.B, a.T,
+                                  (long long)a.P << cache.c.page_shift, cache.format >= 0);
+  if (!a.workspace || a.ws_bytes < pl.bytes() || (reinterpret_cast<uintptr_t>(a.workspace) & 255))
+    return TV_ERR_WORKSPACE;
+  Pass s;
+  st = make_pass(a, cache, pl, a.max_q, static_cast<uint8_t*>(a.workspace), &s);
+  return st != TV_OK ? st : launched(launch_pass(s, cache, a.stream));
+}
+
+// The plans of the two passes, and where their parts of the workspace lie.
+struct PrefixPlan {
+  PagedPlan first, second;
+  size_t pre, pre_ml, bytes;  // offsets: behind both plans' parts
+};
+// (the host knows no groups' lengths)
+int per_group(int T, int groups) { return T > groups ? T / groups + (T % groups != 0) : 1; }
+PrefixPlan prefix_plan(int max_q, int T, int groups, int Hq, int Hkv, int D, int B, long long keys,
+                       long long prefix_keys) {
+  PrefixPlan pl;
+  pl.first = paged_plan(per_group(T, groups), Hkv, Hq / Hkv, D, groups, T, prefix_keys, false);
+  pl.second = paged_plan(max_q, Hkv, Hq / Hkv, D, B, T, keys, false);
+  pl.pre = pl.first.bytes() + pl.second.bytes();
+  pl.pre_ml = pl.pre + align_up((size_t)T * Hq * D * 4, 256);
+  pl.bytes = pl.pre_ml + align_up((size_t)T * Hq * 8, 256);
+  return pl;
+}
+
+tv_status attend_prefix(const AttnArgs& a, const PrefixArgs& f, const CacheArg& cache) {
+  if (f.groups < 0 || f.P < 1) return TV_ERR_INVALID_ARG;
+  tv_status st = check_attn(a, cache);
+  if (st != TV_OK) return st;
+  const int shift = cache.c.page_shift;
+  if (f.groups > kMaxSeqs || (long long)f.groups * f.P > 0x7fffffffll ||
+      ((long long)a.P + f.P) << shift > 0x7fffffffll - 512)
+    return TV_ERR_UNSUPPORTED;
+  if (a.B == 0) return TV_OK;
+  if (f.groups == 0) return attend(a, cache);
+  if (!f.table || !f.len || !f.group_start) return TV_ERR_INVALID_ARG;
+  const PrefixPlan pl = prefix_plan(a.max_q, a.T, f.groups, a.Hq, cache.Hkv, cache.D, a.B, (long long)a.P << shift,
+                                    (long long)f.P << shift);
+  if (!a.workspace || a.ws_bytes < pl.bytes || (reinterpret_cast<uintptr_t>(a.workspace) & 255))
+    return TV_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  AttnArgs g = a;
+  g.block_table = f.table;
+  g.kv_len = f.len;
+  g.B = f.groups;
+  g.P = f.P;
+  g.lse = nullptr;
+  g.status = nullptr;
+  Pass one, two;
+  if ((st = make_pass(g, cache, pl.first, per_group(a.T, f.groups), ws, &one)) != TV_OK ||
+      (st = make_pass(a, cache, pl.second, a.max_q, ws + pl.first.bytes(), &two)) != TV_OK)
+    return st;
+  one.p.anc = nullptr;
+  one.p.token = two.p.token;
+  one.p.pass = 1;
+  two.p.pass = 2;
+  for (Pass* s : {&one, &two}) {
+    PagedAttnParams& p = s->p;
+    p.group_start = f.group_start;
+    p.prefix_len = f.len;
+    p.prefix_table = f.table;
+    p.own_len = a.kv_len;
+    p.own_anc = a.anc_mask;
+    p.pre = reinterpret_cast<float*>(ws + pl.pre);
+    p.pre_ml = reinterpret_cast<float2*>(ws + pl.pre_ml);
+    p.pre_late = one.p.late;
+    p.pre_any_late = one.p.any_late;
+    p.pre_ctas = pl.first.ctas;
+    p.groups = f.groups;
+    p.seqs = a.B;
+    p.prefix_P = f.P;
+  }
+  cudaError_t e = launch_pass(one, cache, a.stream);
+  if (e == cudaSuccess) e = launch_pass(two, cache, a.stream);
+  return launched(e);
 }
 
 }  // namespace
@@ -447,14 +590,8 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
                                    size_t ws_bytes, cudaStream_t stream) {
   TV_NVTX_RANGE("tv_attn_paged");
   tv::paged::CacheArg c{};
-  const tv_status st = tv::check_cache(cache, &c.c);
+  const tv_status st = tv::paged::cache_arg(cache, &c);
   if (st != TV_OK) return st;
-  c.k = cache->k;
-  c.v = cache->v;
-  c.Hkv = cache->Hkv;
-  c.D = cache->D;
-  c.dtype = cache->dtype;
-  c.format = -1;
   return tv::paged::attend({q, q_token_stride, q_head_stride, block_table, q_start, kv_len, anc_mask, slopes, B, T, P,
                             Hq, max_q, scale, softcap, window, out, lse, status, workspace, ws_bytes, stream}, c);
 }
@@ -488,4 +625,28 @@ extern "C" tv_status tv_attn_paged_q8(const void* q, int64_t q_token_stride, int
   c.v_scale = cache->v_scale;
   return tv::paged::attend({q, q_token_stride, q_head_stride, block_table, q_start, kv_len, anc_mask, slopes, B, T, P,
                             Hq, max_q, scale, softcap, window, out, lse, status, workspace, ws_bytes, stream}, c);
+}
+
+extern "C" size_t tv_attn_paged_prefix_workspace_size(int max_q, int T, int groups, int Hq, int Hkv, int D) {
+  if (max_q < 1 || T < 0 || groups < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 128 ||
+      (D != 64 && D != 128) || (long long)T * Hq > 0x7fffffffll)
+    return 0;
+  if (groups == 0) return tv_attn_paged_workspace_size(max_q, Hq, Hkv, D);
+  return tv::paged::prefix_plan(max_q, T, groups, Hq, Hkv, D, 0, 0, 0).bytes;
+}
+
+extern "C" tv_status tv_attn_paged_prefix(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride, const tv_paged_cache* cache,
+    const int32_t* prefix_table, const int32_t* prefix_len, const int32_t* group_start, int groups, int prefix_P,
+    const int32_t* block_table, const int32_t* q_start, const int32_t* kv_len, const uint64_t* anc_mask,
+    const float* slopes, int B, int T, int P, int Hq, int max_q, float scale, float softcap, int window,
+    void* out, float* lse, int32_t* status, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  TV_NVTX_RANGE("tv_attn_paged_prefix");
+  tv::paged::CacheArg c{};
+  const tv_status st = tv::paged::cache_arg(cache, &c);
+  if (st != TV_OK) return st;
+  return tv::paged::attend_prefix(
+      {q, q_token_stride, q_head_stride, block_table, q_start, kv_len, anc_mask, slopes, B, T, P, Hq, max_q, scale,
+       softcap, window, out, lse, status, workspace, ws_bytes, stream},
+      {prefix_table, prefix_len, group_start, groups, prefix_P}, c);
 }

@@ -77,6 +77,20 @@ struct PagedAttnParams {
   int merge;        // a merge kernel joins the parts of split units, else the CTA a unit begins in
   unsigned long long token;      // this call's mark in `ready`
   unsigned long long* ready;     // [CTAs][8]: a warp of a share's first part has left its rows
+  // A shared prefix takes two passes.  In the first the groups are the sequences: table, kv_len, B and P are the
+  // prefixes', a group's tokens are its sequences', and rows go to pre and pre_ml as they are (not divided by
+  // their sums).  In the second the sequences' own rows are joined with those.
+  int pass;                    // 0: no shared prefix
+  const int32_t* group_start;  // [groups + 1] sequences
+  const int32_t* prefix_len;   // [groups]
+  const int32_t* prefix_table;
+  const int32_t* own_len;      // [seqs]
+  const uint64_t* own_anc;
+  float* pre;       // [T * Hq][D]
+  float2* pre_ml;   // [T * Hq]
+  Late* pre_late;   // the first pass's marks, [pre_ctas]
+  unsigned long long* pre_any_late;
+  int groups, seqs, prefix_P, pre_ctas;
   float scale_log2, softcap_log2, cap_in;  // cap_in: scale / softcap
   float cap_q[4], cap_top;  // capped scores s of s^2 <= cap_top: s (q0 + q1 s^2 + q2 s^4 + q3 s^6)
 };
@@ -214,10 +228,65 @@ __device__ __forceinline__ int anc_depth(const uint64_t* anc, int W) {
   return max(0, anc_count(anc, W, 64 * W) - 1);
 }
 
+// A row's sums joined with those of its prefix (pre: maximum and sum): fo and fp are the factors of the two.
+__device__ __forceinline__ void join_factors(float2 pre, float& m, float& l, float& fo, float& fp) {
+  const float top = fmaxf(m, pre.x);  // (maxima leave a NaN out, sums carry it)
+  fo = m == -INFINITY ? 0.0f : ex2(m - top);
+  fp = pre.x == -INFINITY ? 0.0f : ex2(pre.x - top);
+  l = fmaf(fo, l, fp * pre.y);
+  m = top;
+}
+__device__ __forceinline__ void join_rows(float4& a, const float4& v, float fo, float fp) {
+  if (fo != 1.0f) a = make_float4(a.x * fo, a.y * fo, a.z * fo, a.w * fo);
+  if (fp != 0.0f)
+    a = make_float4(fmaf(fp, v.x, a.x), fmaf(fp, v.y, a.y), fmaf(fp, v.z, a.z), fmaf(fp, v.w, a.w));
+}
+
 // ------------------------------------------------------- shares of the work
 // (16 trees of 64 nodes, a capped ragged batch and biased prompts of 200 to 1,500: 79.1, 64.2 and 29.5 us at 1;
 // 75.7, 63.8 and 28.7 us at 3; 80.3, 63.0 and 33.0 us at 8)
 constexpr int kUnitCost = 3;
+
+// Tokens of group g: false for a malformed group_start or q_start.
+__device__ __forceinline__ bool group_range(const PagedAttnParams& p, int g, int& t0, int& n) {
+  const int b0 = __ldg(p.group_start + g), b1 = __ldg(p.group_start + g + 1);
+  t0 = n = 0;
+  if (b0 < 0 || b1 < b0 || b1 > p.seqs) return false;
+  t0 = __ldg(p.q_start + b0);
+  const int t1 = __ldg(p.q_start + b1);
+  n = t1 - t0;
+  return t0 >= 0 && t1 >= t0 && t1 <= p.T;
+}
+// The group of sequence b whose rows the first pass has left, or -1.
+__device__ __forceinline__ int group_of(const PagedAttnParams& p, int b) {
+  int lo = 0, hi = p.groups;  // the last group that starts at or before b
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.group_start + mid) <= b) lo = mid + 1;
+    else hi = mid;
+  }
+  int t0, n, s0, sn;
+  if (lo == 0 || b >= __ldg(p.group_start + lo) || b < __ldg(p.group_start + lo - 1)) return -1;
+  // (a sequence whose tokens are not among its group's: starts that descend)
+  return group_range(p, lo - 1, t0, n) && seq_range(p.q_start, b, p.T, s0, sn) && s0 >= t0 && s0 + sn <= t0 + n
+             ? lo - 1 : -1;
+}
+// Tokens of the pass's sequence b.
+__device__ __forceinline__ bool token_range(const PagedAttnParams& p, int b, int& t0, int& n) {
+  return p.pass == 1 ? group_range(p, b, t0, n) : seq_range(p.q_start, b, p.T, t0, n);
+}
+// The position of a group's token t, behind a prefix of L rows.
+__device__ __forceinline__ int prefix_pos(const PagedAttnParams& p, int g, int t, int L) {
+  if (p.window == 0 && !p.slopes) return L;  // (not looked at)
+  int lo = __ldg(p.group_start + g), hi = __ldg(p.group_start + g + 1);
+  while (hi - lo > 1) {  // the last of its sequences that starts at or before t
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.q_start + mid) <= t) lo = mid;
+    else hi = mid;
+  }
+  return L + __ldg(p.own_len + lo) +
+         (p.own_anc ? anc_depth(p.own_anc + (size_t)t * p.W, p.W) : t - __ldg(p.q_start + lo));
+}
 
 struct Seq {
   int t0, n, L;
@@ -227,8 +296,8 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
   Seq s;
   s.L = __ldg(p.kv_len + b);
-  if (!seq_range(p.q_start, b, p.T, s.t0, s.n)) s.n = 0;
-  s.bad = s.L < 0 || (long long)s.L + s.n > ((long long)p.P << p.page_shift) ||
+  if (!token_range(p, b, s.t0, s.n)) s.n = 0;
+  s.bad = s.L < 0 || (long long)s.L + (p.pass == 1 ? 0 : s.n) > ((long long)p.P << p.page_shift) ||
           (p.anc && s.n > 64 * p.W);
   return s;
 }
@@ -237,6 +306,11 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
 __device__ __forceinline__ void key_range(const PagedAttnParams& p, const Seq& s, int qt, int& lo,
                                           int& hi) {
   const int first = qt * p.tq;
+  if (p.pass == 1) {  // (its tokens are all behind the prefix)
+    hi = s.L;
+    lo = p.window > 0 ? max(0, s.L - p.window + 1) : 0;
+    return;
+  }
   hi = p.anc ? s.L + s.n : s.L + min(s.n, first + p.tq);
   // (the root of a tree sees furthest back)
   lo = p.window > 0 ? max(0, (p.anc ? s.L : s.L + first) - p.window + 1) : 0;
@@ -262,7 +336,10 @@ struct Part {
   int begin, end;    // key tiles of this part
   int slot;          // partial slot, or -1: the whole unit is here
   int parts;         // a unit that this part begins: how many parts it has
+  int pre;           // (second pass) its rows are to be joined with the first pass's
 };
+// A split unit in `desc`: its parts, and a bit for Part::pre.
+constexpr int kPartsPre = 1 << 30;
 
 // (64-bit division costs some hundred cycles; the quotients here are small)
 __device__ __forceinline__ long long div_fast(long long a, long long b) {
@@ -277,6 +354,7 @@ struct Cursor {
   long long at;           // cost behind the share's start
   int b, kvh, qt, pos;    // unit, and cost of it that lies behind
   int last;               // the share's last sequence (or one behind it, where a thread looks at several)
+  int pre_of, pre;        // (second pass) the last sequence asked, and whether it has a prefix
   Seq s;
 
   __device__ __forceinline__ int cost_of(const PagedAttnParams& p, int tiles) const {
@@ -300,6 +378,11 @@ struct Cursor {
         o.begin = o.lo / KT + a;
         o.end = o.lo / KT + e;
         o.slot = (a == 0 && e == tiles) ? -1 : p.merge ? 2 * share_index() + (a == 0) : share_index();
+        if (p.pass == 2 && pre_of != b) {
+          pre = group_of(p, b) >= 0;
+          pre_of = b;
+        }
+        o.pre = p.pass == 2 && !s.bad ? pre : 0;
         o.parts = (o.slot >= 0 && a == 0) ? (int)div_fast(at - pos + cost - 1, share) + 1 : 0;
       }
       rest -= take;
@@ -417,6 +500,7 @@ __device__ __forceinline__ void find_share(const PagedAttnParams& p, Cursor<KT>&
         s_cur.kvh = c.kvh;
         s_cur.qt = c.qt;
         s_cur.pos = c.pos;
+        s_cur.pre_of = -1;
         s_cur.s = c.s;
         break;
       }
@@ -459,6 +543,30 @@ struct PartRing {
   __device__ __forceinline__ void done(uint32_t n) { mbar_arrive(&empty[n % kPartRing]); }  // one thread
 };
 
+// Whether the prefix of sequence b, if it has one, fits and its pages are pages, as far as the
+// sequence's window reaches.
+__device__ __forceinline__ bool prefix_ok(const PagedAttnParams& p, int b, int n, int own, int lane, int lanes) {
+  const int g = group_of(p, b);
+  if (g < 0) {  // outside the groups, or in one that is none
+    int lo = 0, hi = p.groups;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(p.group_start + mid) <= b) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo == 0 || (lo == p.groups && b >= __ldg(p.group_start + lo));
+  }
+  const int L = __ldg(p.prefix_len + g);
+  if (L < 0 || L > ((long long)p.prefix_P << p.page_shift)) return false;
+  if (n == 0) return true;
+  const long long lo = p.window > 0 ? max(0ll, (long long)L + own - p.window + 1) : 0;
+  int any = 0;
+  for (long long j = (lo >> p.page_shift) + lane; j << p.page_shift < L; j += lanes) {
+    const int page = TV_IN(j, p.prefix_P) ? __ldg(p.prefix_table + (size_t)g * p.prefix_P + j) : 0;
+    any |= page < 0 || page >= p.num_pages;
+  }
+  return any == 0;
+}
 // Whether sequence b's lengths fit and its pages are pages, as far as the window reaches;
 // `lane` of `lanes` threads looks at its share of the pages.
 __device__ __forceinline__ bool seq_ok(const PagedAttnParams& p, int b, int lane, int lanes) {
@@ -466,6 +574,7 @@ __device__ __forceinline__ bool seq_ok(const PagedAttnParams& p, int b, int lane
   if (!seq_range(p.q_start, b, p.T, t0, n)) return false;
   const Seq s = load_seq(p, b);
   if (s.bad) return false;
+  if (p.pass == 2 && !prefix_ok(p, b, n, s.L, lane, lanes)) return false;
   if (n == 0) return true;
   int lo, hi, any = 0;
   key_range(p, s, 0, lo, hi);
@@ -481,12 +590,22 @@ __device__ __forceinline__ bool seq_ok(const PagedAttnParams& p, int b, int lane
 // Whether a CTA that gave up may have left rows of sequence b undone; `lane` of `lanes` threads
 // looks at its share of the CTAs.
 __device__ __forceinline__ bool is_late(const PagedAttnParams& p, int b, int lane, int lanes) {
-  if (*(volatile unsigned long long*)p.any_late != p.token) return false;
+  const bool pre = p.pass == 2 && *(volatile unsigned long long*)p.pre_any_late == p.token;
+  const bool own = *(volatile unsigned long long*)p.any_late == p.token;
+  if (!pre && !own) return false;
   int t0, n;
   bool late = false;
-  for (int c = lane; c < gridDim.x; c += lanes) {
-    volatile Late* l = p.late + c;
-    late |= l->token == p.token && b >= l->first && b <= l->last;
+  if (own)
+    for (int c = lane; c < gridDim.x; c += lanes) {
+      volatile Late* l = p.late + c;
+      late |= l->token == p.token && b >= l->first && b <= l->last;
+    }
+  if (pre) {
+    const int g = group_of(p, b);
+    for (int c = lane; g >= 0 && c < p.pre_ctas; c += lanes) {
+      volatile Late* l = p.pre_late + c;
+      late |= l->token == p.token && g >= l->first && g <= l->last;
+    }
   }
   return late && seq_range(p.q_start, b, p.T, t0, n) && n > 0;
 }
@@ -629,6 +748,11 @@ cudaError_t launch_rows_e4m3(const PagedPlan& pl, int D, bool mod, const CUtenso
                              const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
 cudaError_t launch_rows_int8(const PagedPlan& pl, int D, bool mod, const CUtensorMap& tmK,
                              const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
+cudaError_t launch_rows_prefix(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmK,
+                               const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
+cudaError_t launch_tc_prefix(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
+                             const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
+                             cudaStream_t stream);
 cudaError_t launch_tc(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
                       const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
                       cudaStream_t stream);

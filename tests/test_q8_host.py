@@ -91,3 +91,70 @@ def test_plain_quantiser(fmt, dt):
     again = y.float().to(kind) if fmt == "e4m3" else torch.round(y.float())
     assert torch.equal(again.float().double(), codes)
     assert torch.equal(values_ref(codes, scale).bfloat16().double(), values_ref(codes, scale))
+
+
+def paged_cache(tv, **kw):
+    from speculative_decoding_tree_tv_gb300._lib import PAGED_CACHE_FORMAT
+    f = dict(k=0x1000, v=0x1000, page_stride=16 * 64 * 2, head_stride=16 * 64, row_stride=64, num_pages=10,
+             page_size=16, Hkv=2, D=64, dtype=0)
+    f.update(kw)
+    return struct.pack(PAGED_CACHE_FORMAT, *f.values())
+
+
+ATTN = [(dict(B=-1), 1), (dict(T=-1), 1), (dict(Pg=0), 1), (dict(Hq=0), 1), (dict(Hq=3), 1), (dict(max_q=0), 1),
+        (dict(window=-1), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1), (dict(softcap=-2.0), 1),
+        (dict(B=5000), 3), (dict(Hq=2 * 130), 3), (dict(T=2**30), 3), (dict(Pg=2**28), 3),
+        (dict(anc=P, max_q=513), 3), (dict(q=None), 1), (dict(out=None), 1), (dict(table=None), 1),
+        (dict(q_start=None), 1), (dict(kv_len=None), 1), (dict(q=ODD), 1), (dict(out=ODD), 1), (dict(qt=100), 1),
+        (dict(qh=-64), 1), (dict(n=0), 7), (dict(ws=None), 7), (dict(B=0), 0)]
+
+
+def args(**kw):
+    a = dict(q=P, qt=256, qh=64, table=P, q_start=P, kv_len=P, anc=None, slopes=None, B=1, T=4, Pg=4, Hq=4, max_q=4,
+             scale=0.0, softcap=0.0, window=0, out=P, lse=None, status=None, ws=P, n=0)
+    a.update(kw)
+    return a
+
+
+def tail(a):
+    return (a["table"], a["q_start"], a["kv_len"], a["anc"], a["slopes"], a["B"], a["T"], a["Pg"], a["Hq"], a["max_q"],
+            a["scale"], a["softcap"], a["window"], a["out"], a["lse"], a["status"], a["ws"], a["n"], None)
+
+
+@pytest.mark.parametrize("kw,code", ATTN)
+def test_attention_arguments_are_checked(tvlib, kw, code):
+    a = args(**kw)
+    assert tvlib.lib.tv_attn_paged_q8(a["q"], a["qt"], a["qh"], cache(tvlib), *tail(a)) == code
+    assert tvlib.lib.tv_attn_paged_prefix(a["q"], a["qt"], a["qh"], paged_cache(tvlib), P, P, P, 1, 4, *tail(a)) == code
+
+
+@pytest.mark.parametrize("d", [32, 48, 96, 256])
+def test_attention_head_sizes(tvlib, d):
+    a = args()
+    assert tvlib.lib.tv_attn_paged_q8(a["q"], a["qt"], a["qh"], cache(tvlib, D=d), *tail(a)) == 3
+    assert tvlib.lib.tv_attn_paged_prefix(a["q"], a["qt"], a["qh"], paged_cache(tvlib, D=d), P, P, P, 1, 4, *tail(a)) == 3
+
+
+def test_prefix_arguments_are_checked(tvlib):
+    def call(table=P, length=P, start=P, groups=1, prefix_P=4, **kw):
+        a = args(**kw)
+        return tvlib.lib.tv_attn_paged_prefix(a["q"], a["qt"], a["qh"], paged_cache(tvlib), table, length, start, groups,
+                                              prefix_P, *tail(a))
+    for kw in (dict(groups=-1), dict(prefix_P=0), dict(table=None), dict(length=None), dict(start=None)):
+        assert call(**kw) == tvlib.TV_ERR_INVALID_ARG, kw
+    for kw in (dict(groups=4097), dict(groups=4096, prefix_P=2**20), dict(prefix_P=2**27), dict(prefix_P=2**26, Pg=2**26)):
+        assert call(**kw) == tvlib.TV_ERR_UNSUPPORTED, kw
+    assert call(groups=0, table=None, length=None, start=None) == tvlib.TV_ERR_WORKSPACE  # (as tv_attn_paged)
+    assert call(B=0) == tvlib.TV_OK
+
+
+def test_workspace_sizes(tvlib):
+    f = tvlib.lib.tv_attn_paged_prefix_workspace_size
+    one = tvlib.lib.tv_attn_paged_workspace_size(1, 8, 2, 64)
+    assert f(1, 64, 0, 8, 2, 64) == one
+    # both passes' parts, and a 32-bit row with its maximum and sum for each query row
+    assert f(1, 64, 1, 8, 2, 64) >= one + 64 * 8 * (64 * 4 + 8)
+    for bad in ((0, 64, 1, 8, 2, 64), (1, -1, 1, 8, 2, 64), (1, 64, -1, 8, 2, 64), (1, 64, 1, 7, 2, 64), (1, 64, 1, 8, 2, 80)):
+        assert f(*bad) == 0
+    g = tvlib.lib.tv_attn_paged_q8_workspace_size
+    assert g(1, 8, 2, 64) > 0 and g(1, 8, 2, 80) == 0 and g(0, 8, 2, 64) == 0
