@@ -363,8 +363,8 @@ tv_status tv_debug_set_wait_limit(long long cycles);
  *                       4 expand, 5 attention, 6 commit, 7 expected,
  *                       8 top-n selection, 9 library, 10 pages,
  *                       11 to 13 paged attention, 14 the 8-bit cache,
- *                       15 and 16 its attention, 17 and 18 attention
- *                       behind shared prefixes.  Host call; it must not
+ *                       15 and 16 its attention, 17 attention behind
+ *                       shared prefixes.  Host call; it must not
  *                       overlap a launch of this library on the device.
  *                       TV_ERR_INVALID_ARG if site is NULL, TV_ERR_CUDA if
  *                       the device reports an error.
@@ -708,12 +708,13 @@ tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_st
  *
  *   prefix_table int32 [groups, prefix_P]; prefix_len int32 [groups]; group_start int32 [groups + 1], ascending
  *               from 0 or more to B or less.  groups = 0: as tv_attn_paged (the three are not read then).
- *   status      as tv_attn_paged's, and TV_ERR_INVALID_ARG for the sequences of a malformed group, with a
+ *   status      as tv_attn_paged's, and TV_ERR_INVALID_ARG for the sequences of a malformed group (where
+ *               group_start descends, for others behind it too), or one in which q_start descends, with a
  *               prefix_len < 0 or past prefix_P * page_size (the prefix then counts as hidden), or with a
  *               page id outside [0, num_pages) among the prefix's pages that the window reaches (its rows count
  *               as hidden).
- *   workspace   tv_attn_paged_prefix_workspace_size() bytes (32-bit rows of the prefixes' sums, and what both
- *               passes need), otherwise as tv_attn_paged's.
+ *   workspace   tv_attn_paged_prefix_workspace_size() bytes (32-bit rows of what a token sees in its prefix
+ *               and in its own rows, before they are joined, among it), otherwise as tv_attn_paged's.
  * The other arguments, statuses and limits are tv_attn_paged's; groups <= 4096, groups * prefix_P and
  * (P + prefix_P) * page_size + 512 below 2^31.
  */

@@ -34,17 +34,14 @@ __device__ __forceinline__ void merge_status(const PagedAttnParams& p) {
 
 // A thread joins kC chunks (of four floats) of one row, all its loads of a batch of parts
 // in flight.
-// PRE: of a pass of an attention with shared prefixes.
-template <int D, bool F16, bool TC, bool PRE>
+template <int D, bool F16, bool TC>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedAttnParams p, int nb) {
   constexpr int kChunks = D / 4, kRows = TC ? 256 : 16;
   constexpr int kC = TC ? 4 : kChunks * kRows / kMergeThreads;  // a small unit: one block
   pdl_trigger();
   pdl_wait();
   const int i = blockIdx.x;
-  int4 d = p.desc[i];
-  const bool joins = PRE && (d.w & kPartsPre);
-  if (PRE) d.w &= ~kPartsPre;
+  const int4 d = p.desc[i];
   merge_status(p);
   if (d.w == 0) return;
   const int row = TC ? threadIdx.x : threadIdx.x / (kChunks / kC);
@@ -103,20 +100,6 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
         a[c].w = fmaf(e, v[j][c].w, a[c].w);
       }
     }
-  }
-  if (PRE && p.pass == 1) {
-    float4* pre = reinterpret_cast<float4*>(p.pre + oidx * D) + c0;
-#pragma unroll
-    for (int c = 0; c < kC; ++c) pre[c] = a[c];
-    if (c0 == 0) p.pre_ml[oidx] = make_float2(M, l);
-    return;
-  }
-  if (joins) {
-    float fo, fp;
-    join_factors(p.pre_ml[oidx], M, l, fo, fp);
-    const float4* pre = reinterpret_cast<const float4*>(p.pre + oidx * D) + c0;
-#pragma unroll
-    for (int c = 0; c < kC; ++c) join_rows(a[c], pre[c], fo, fp);
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint2* out = reinterpret_cast<uint2*>(p.out + oidx * D) + c0;
@@ -264,18 +247,17 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
   return pl;
 }
 
-template <int D, bool F16, bool PRE>
+template <int D, bool F16>
 cudaError_t launch_merge(const PagedPlan& pl, const PagedAttnParams& p, cudaStream_t stream) {
   if (pl.small)
-    return launch_pdl(paged_merge_kernel<D, F16, false, PRE>, dim3(pl.ctas, 1), dim3(kMergeThreads), 0,
+    return launch_pdl(paged_merge_kernel<D, F16, false>, dim3(pl.ctas, 1), dim3(kMergeThreads), 0,
                       stream, p, pl.nb);
-  return launch_pdl(paged_merge_kernel<D, F16, true, PRE>, dim3(pl.ctas, D / 16), dim3(kMergeThreads), 0,
+  return launch_pdl(paged_merge_kernel<D, F16, true>, dim3(pl.ctas, D / 16), dim3(kMergeThreads), 0,
                     stream, p, pl.nb);
 }
-template <bool PRE>
 cudaError_t launch_merge(const PagedPlan& pl, int D, bool f16, const PagedAttnParams& p, cudaStream_t stream) {
-  if (D == 128) return f16 ? launch_merge<128, true, PRE>(pl, p, stream) : launch_merge<128, false, PRE>(pl, p, stream);
-  return f16 ? launch_merge<64, true, PRE>(pl, p, stream) : launch_merge<64, false, PRE>(pl, p, stream);
+  if (D == 128) return f16 ? launch_merge<128, true>(pl, p, stream) : launch_merge<128, false>(pl, p, stream);
+  return f16 ? launch_merge<64, true>(pl, p, stream) : launch_merge<64, false>(pl, p, stream);
 }
 
 }  // namespace
@@ -339,7 +321,8 @@ struct PrefixArgs {
   int groups, P;
 };
 
-tv_status check_attn(const AttnArgs& a, const CacheArg& cache) {
+// Checks what the host can see; strides of extent-one dimensions are set to ones that fit.
+tv_status check_attn(AttnArgs& a, const CacheArg& cache) {
   const int Hkv = cache.Hkv, D = cache.D;
   if (a.B < 0 || a.T < 0 || a.P < 1 || a.Hq < 1 || a.max_q < 1 || a.window < 0) return TV_ERR_INVALID_ARG;
   if (!(a.scale >= 0.0f) || !isfinite(a.scale) || !(a.softcap >= 0.0f) || !isfinite(a.softcap))
@@ -353,6 +336,14 @@ tv_status check_attn(const AttnArgs& a, const CacheArg& cache) {
     return TV_ERR_UNSUPPORTED;
   if (a.B == 0) return TV_OK;
   if (!a.block_table || !a.q_start || !a.kv_len || (a.T > 0 && (!a.q || !a.out))) return TV_ERR_INVALID_ARG;
+  a.q_head_stride = stride_or(a.q_head_stride, a.Hq, D);
+  a.q_token_stride = stride_or(a.q_token_stride, a.T, a.Hq * a.q_head_stride);
+  if (a.q_token_stride < 0 || a.q_head_stride < 0 || ((a.q_token_stride | a.q_head_stride) & 7))
+    return TV_ERR_INVALID_ARG;
+  if (a.q_head_stride == 0 || a.q_token_stride == 0) return TV_ERR_UNSUPPORTED;
+  if (a.Hq == 1) a.q_head_stride = a.q_token_stride;
+  if (a.q_token_stride % a.q_head_stride != 0 || a.q_token_stride >= (1ll << 39))
+    return TV_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.out)) & 15)
     return TV_ERR_INVALID_ARG;
   return TV_OK;
@@ -375,14 +366,8 @@ tv_status make_pass(const AttnArgs& a, const CacheArg& cache, const PagedPlan& p
   const PagedCache& c = cache.c;
   const int Hkv = cache.Hkv, D = cache.D;
   const bool q8 = cache.format >= 0, f16 = cache.dtype == TV_FP16;
-  p.q_head_stride = stride_or(a.q_head_stride, a.Hq, D);
-  p.q_token_stride = stride_or(a.q_token_stride, a.T, a.Hq * p.q_head_stride);
-  if (p.q_token_stride < 0 || p.q_head_stride < 0 || ((p.q_token_stride | p.q_head_stride) & 7))
-    return TV_ERR_INVALID_ARG;
-  if (p.q_head_stride == 0 || p.q_token_stride == 0) return TV_ERR_UNSUPPORTED;
-  if (a.Hq == 1) p.q_head_stride = p.q_token_stride;
-  if (p.q_token_stride % p.q_head_stride != 0 || p.q_token_stride >= (1ll << 39))
-    return TV_ERR_UNSUPPORTED;
+  p.q_head_stride = a.q_head_stride;
+  p.q_token_stride = a.q_token_stride;
   const long long extent[3] = {1ll << c.page_shift, Hkv, c.num_pages};
   long long stride[3] = {c.row_stride, c.head_stride, c.page_stride};
   int order[3];
@@ -440,6 +425,7 @@ tv_status make_pass(const AttnArgs& a, const CacheArg& cache, const PagedPlan& p
     if (order[i] == 1) p.head_dim = i + 1;
   }
   p.tq = pl.tq;
+  p.ctas = pl.ctas;
   p.min_share = pl.min_share;
   p.share_lanes = 0;  // (a lane per query tile of the largest chunk, where the kernels' threads suffice)
   while (p.share_lanes < 5 && (pl.tq << p.share_lanes) < chunk && (a.B << (p.share_lanes + 1)) <= 192)
@@ -475,17 +461,18 @@ cudaError_t launch_pass(const Pass& s, const CacheArg& cache, cudaStream_t strea
   const PagedPlan& pl = s.pl;
   const PagedAttnParams& p = s.p;
   const int D = cache.D;
-  const bool f16 = cache.dtype == TV_FP16, mod = s.bias || p.softcap_log2 > 0.0f, pre = p.pass != 0;
+  const bool f16 = cache.dtype == TV_FP16, mod = s.bias || p.softcap_log2 > 0.0f;
   cudaError_t e;
   if (cache.format >= 0)
     e = cache.format == TV_E4M3 ? launch_rows_e4m3(pl, D, mod, s.tmK, s.tmV, p, stream)
                                 : launch_rows_int8(pl, D, mod, s.tmK, s.tmV, p, stream);
+  else if (p.groups > 0)
+    return launch_prefix(pl, D, f16, s.bias, s.tmQ, s.tmK, s.tmV, p, stream);
   else if (pl.small)
-    e = (pre ? launch_rows_prefix : launch_rows)(pl, D, f16, mod, s.tmK, s.tmV, p, stream);
+    e = launch_rows(pl, D, f16, mod, s.tmK, s.tmV, p, stream);
   else
-    e = (pre ? launch_tc_prefix : launch_tc)(pl, D, f16, s.bias, s.tmQ, s.tmK, s.tmV, p, stream);
-  if (e == cudaSuccess && pl.merge)
-    e = pre ? launch_merge<true>(pl, D, f16, p, stream) : launch_merge<false>(pl, D, f16, p, stream);
+    e = launch_tc(pl, D, f16, s.bias, s.tmQ, s.tmK, s.tmV, p, stream);
+  if (e == cudaSuccess && pl.merge) e = launch_merge(pl, D, f16, p, stream);
   return e;
 }
 
@@ -495,7 +482,7 @@ tv_status launched(cudaError_t e) {
   return TV_ERR_CUDA;
 }
 
-tv_status attend(const AttnArgs& a, const CacheArg& cache) {
+tv_status attend(AttnArgs a, const CacheArg& cache) {
   tv_status st = check_attn(a, cache);
   if (st != TV_OK || a.B == 0) return st;
   const PagedPlan pl = paged_plan(a.max_q, cache.Hkv, a.Hq / cache.Hkv, cache.D, a.B, a.T,
@@ -507,25 +494,27 @@ tv_status attend(const AttnArgs& a, const CacheArg& cache) {
   return st != TV_OK ? st : launched(launch_pass(s, cache, a.stream));
 }
 
-// The plans of the two passes, and where their parts of the workspace lie.
+// The plan of a call with shared prefixes, and where the rows of units that are not split lie behind its workspace.
 struct PrefixPlan {
-  PagedPlan first, second;
-  size_t pre, pre_ml, bytes;  // offsets: behind both plans' parts
+  PagedPlan pl;
+  size_t raw, raw_ml, src, bytes;
 };
-// (the host knows no groups' lengths)
-int per_group(int T, int groups) { return T > groups ? T / groups + (T % groups != 0) : 1; }
-PrefixPlan prefix_plan(int max_q, int T, int groups, int Hq, int Hkv, int D, int B, long long keys,
-                       long long prefix_keys) {
-  PrefixPlan pl;
-  pl.first = paged_plan(per_group(T, groups), Hkv, Hq / Hkv, D, groups, T, prefix_keys, false);
-  pl.second = paged_plan(max_q, Hkv, Hq / Hkv, D, B, T, keys, false);
-  pl.pre = pl.first.bytes() + pl.second.bytes();
-  pl.pre_ml = pl.pre + align_up((size_t)T * Hq * D * 4, 256);
-  pl.bytes = pl.pre_ml + align_up((size_t)T * Hq * 8, 256);
-  return pl;
+PrefixPlan prefix_plan(int T, int groups, int Hq, int Hkv, int D, int B, long long keys) {
+  PrefixPlan f;
+  PagedPlan& pl = f.pl;
+  pl = paged_plan(TV_MAX_NODES, Hkv, Hq / Hkv, D, B, T, 1ll << 40, false);  // (the tcgen05 kernel's)
+  // (units of prefixes and of sequences)
+  pl.whole = keys <= kWholeTcKeys && (long long)Hkv * (2ll * (T / pl.tq) + groups + B) <= device_sm_count();
+  if (pl.whole) pl.min_share = 1;
+  pl.merge = true;  // split units' rows are left in slots
+  f.raw = pl.bytes();
+  f.raw_ml = f.raw + align_up(2 * (size_t)T * Hq * D * 4, 256);
+  f.src = f.raw_ml + align_up(2 * (size_t)T * Hq * 8, 256);
+  f.bytes = f.src + align_up(2 * (size_t)T * Hkv * 16, 256);
+  return f;
 }
 
-tv_status attend_prefix(const AttnArgs& a, const PrefixArgs& f, const CacheArg& cache) {
+tv_status attend_prefix(AttnArgs a, const PrefixArgs& f, const CacheArg& cache) {
   if (f.groups < 0 || f.P < 1) return TV_ERR_INVALID_ARG;
   tv_status st = check_attn(a, cache);
   if (st != TV_OK) return st;
@@ -536,45 +525,25 @@ tv_status attend_prefix(const AttnArgs& a, const PrefixArgs& f, const CacheArg& 
   if (a.B == 0) return TV_OK;
   if (f.groups == 0) return attend(a, cache);
   if (!f.table || !f.len || !f.group_start) return TV_ERR_INVALID_ARG;
-  const PrefixPlan pl = prefix_plan(a.max_q, a.T, f.groups, a.Hq, cache.Hkv, cache.D, a.B, (long long)a.P << shift,
-                                    (long long)f.P << shift);
+  const PrefixPlan pl = prefix_plan(a.T, f.groups, a.Hq, cache.Hkv, cache.D, a.B,
+                                    (long long)(a.P > f.P ? a.P : f.P) << shift);
   if (!a.workspace || a.ws_bytes < pl.bytes || (reinterpret_cast<uintptr_t>(a.workspace) & 255))
     return TV_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  AttnArgs g = a;
-  g.block_table = f.table;
-  g.kv_len = f.len;
-  g.B = f.groups;
-  g.P = f.P;
-  g.lse = nullptr;
-  g.status = nullptr;
-  Pass one, two;
-  if ((st = make_pass(g, cache, pl.first, per_group(a.T, f.groups), ws, &one)) != TV_OK ||
-      (st = make_pass(a, cache, pl.second, a.max_q, ws + pl.first.bytes(), &two)) != TV_OK)
-    return st;
-  one.p.anc = nullptr;
-  one.p.token = two.p.token;
-  one.p.pass = 1;
-  two.p.pass = 2;
-  for (Pass* s : {&one, &two}) {
-    PagedAttnParams& p = s->p;
-    p.group_start = f.group_start;
-    p.prefix_len = f.len;
-    p.prefix_table = f.table;
-    p.own_len = a.kv_len;
-    p.own_anc = a.anc_mask;
-    p.pre = reinterpret_cast<float*>(ws + pl.pre);
-    p.pre_ml = reinterpret_cast<float2*>(ws + pl.pre_ml);
-    p.pre_late = one.p.late;
-    p.pre_any_late = one.p.any_late;
-    p.pre_ctas = pl.first.ctas;
-    p.groups = f.groups;
-    p.seqs = a.B;
-    p.prefix_P = f.P;
-  }
-  cudaError_t e = launch_pass(one, cache, a.stream);
-  if (e == cudaSuccess) e = launch_pass(two, cache, a.stream);
-  return launched(e);
+  Pass s;
+  const int per_group = a.T / f.groups + 1;  // (the host knows no groups' lengths)
+  if ((st = make_pass(a, cache, pl.pl, per_group > a.max_q ? per_group : a.max_q, ws, &s)) != TV_OK) return st;
+  PagedAttnParams& p = s.p;
+  p.groups = f.groups;
+  p.prefix_P = f.P;
+  p.group_start = f.group_start;
+  p.prefix_len = f.len;
+  p.prefix_table = f.table;
+  p.raw = reinterpret_cast<float*>(ws + pl.raw);
+  p.raw_ml = reinterpret_cast<float2*>(ws + pl.raw_ml);
+  p.src = reinterpret_cast<int4*>(ws + pl.src);
+  while (p.share_lanes > 0 && (f.groups + a.B) << p.share_lanes > 384) --p.share_lanes;  // (a thread each at most)
+  return launched(launch_pass(s, cache, a.stream));
 }
 
 }  // namespace
@@ -632,7 +601,7 @@ extern "C" size_t tv_attn_paged_prefix_workspace_size(int max_q, int T, int grou
       (D != 64 && D != 128) || (long long)T * Hq > 0x7fffffffll)
     return 0;
   if (groups == 0) return tv_attn_paged_workspace_size(max_q, Hq, Hkv, D);
-  return tv::paged::prefix_plan(max_q, T, groups, Hq, Hkv, D, 0, 0, 0).bytes;
+  return tv::paged::prefix_plan(T, groups, Hq, Hkv, D, 0, 0).bytes;
 }
 
 extern "C" tv_status tv_attn_paged_prefix(

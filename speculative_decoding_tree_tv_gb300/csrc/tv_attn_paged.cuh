@@ -66,6 +66,7 @@ struct PagedAttnParams {
   unsigned long long* any_late;  // this call's token: some CTA is late
   long long wait_limit;          // SM cycles; 0: the producers of K and V give up before they load anything
   int B, T, P, Hq, Hkv, G, W, window;
+  int ctas;         // of the attention kernel
   int num_pages, page_shift;
   int row_dim, head_dim;  // which of a cache map's dimensions 1, 2, 3 they are (the pages: the third)
   int tq;           // tokens per query tile
@@ -77,20 +78,18 @@ struct PagedAttnParams {
   int merge;        // a merge kernel joins the parts of split units, else the CTA a unit begins in
   unsigned long long token;      // this call's mark in `ready`
   unsigned long long* ready;     // [CTAs][8]: a warp of a share's first part has left its rows
-  // A shared prefix takes two passes.  In the first the groups are the sequences: table, kv_len, B and P are the
-  // prefixes', a group's tokens are its sequences', and rows go to pre and pre_ml as they are (not divided by
-  // their sums).  In the second the sequences' own rows are joined with those.
-  int pass;                    // 0: no shared prefix
+  // Shared prefixes (tv_attn_prefix.cu): the line holds groups + B sequences, of which the first `groups` are the
+  // prefixes: a group's tokens are its sequences', its keys the prefix's rows.  Rows of either kind are left
+  // as they are (not divided by their sums) and joined by a kernel behind.
+  int groups;                  // 0: none
+  int prefix_P;
   const int32_t* group_start;  // [groups + 1] sequences
   const int32_t* prefix_len;   // [groups]
-  const int32_t* prefix_table;
-  const int32_t* own_len;      // [seqs]
-  const uint64_t* own_anc;
-  float* pre;       // [T * Hq][D]
-  float2* pre_ml;   // [T * Hq]
-  Late* pre_late;   // the first pass's marks, [pre_ctas]
-  unsigned long long* pre_any_late;
-  int groups, seqs, prefix_P, pre_ctas;
+  const int32_t* prefix_table; // [groups, prefix_P]
+  float* raw;                  // [2][T * Hq][D]: rows of units that are not split (0: prefixes', 1: own)
+  float2* raw_ml;              // [2][T * Hq]
+  int4* src;                   // [2][T * Hkv]: a token's unit: first slot (-1: in raw), parts, its first
+                               // token, its prefix or sequence
   float scale_log2, softcap_log2, cap_in;  // cap_in: scale / softcap
   float cap_q[4], cap_top;  // capped scores s of s^2 <= cap_top: s (q0 + q1 s^2 + q2 s^4 + q3 s^6)
 };
@@ -228,20 +227,6 @@ __device__ __forceinline__ int anc_depth(const uint64_t* anc, int W) {
   return max(0, anc_count(anc, W, 64 * W) - 1);
 }
 
-// A row's sums joined with those of its prefix (pre: maximum and sum): fo and fp are the factors of the two.
-__device__ __forceinline__ void join_factors(float2 pre, float& m, float& l, float& fo, float& fp) {
-  const float top = fmaxf(m, pre.x);  // (maxima leave a NaN out, sums carry it)
-  fo = m == -INFINITY ? 0.0f : ex2(m - top);
-  fp = pre.x == -INFINITY ? 0.0f : ex2(pre.x - top);
-  l = fmaf(fo, l, fp * pre.y);
-  m = top;
-}
-__device__ __forceinline__ void join_rows(float4& a, const float4& v, float fo, float fp) {
-  if (fo != 1.0f) a = make_float4(a.x * fo, a.y * fo, a.z * fo, a.w * fo);
-  if (fp != 0.0f)
-    a = make_float4(fmaf(fp, v.x, a.x), fmaf(fp, v.y, a.y), fmaf(fp, v.z, a.z), fmaf(fp, v.w, a.w));
-}
-
 // ------------------------------------------------------- shares of the work
 // (16 trees of 64 nodes, a capped ragged batch and biased prompts of 200 to 1,500: 79.1, 64.2 and 29.5 us at 1;
 // 75.7, 63.8 and 28.7 us at 3; 80.3, 63.0 and 33.0 us at 8)
@@ -251,53 +236,51 @@ constexpr int kUnitCost = 3;
 __device__ __forceinline__ bool group_range(const PagedAttnParams& p, int g, int& t0, int& n) {
   const int b0 = __ldg(p.group_start + g), b1 = __ldg(p.group_start + g + 1);
   t0 = n = 0;
-  if (b0 < 0 || b1 < b0 || b1 > p.seqs) return false;
+  if (b0 < 0 || b1 < b0 || b1 > p.B) return false;
   t0 = __ldg(p.q_start + b0);
   const int t1 = __ldg(p.q_start + b1);
   n = t1 - t0;
   return t0 >= 0 && t1 >= t0 && t1 <= p.T;
 }
-// The group of sequence b whose rows the first pass has left, or -1.
-__device__ __forceinline__ int group_of(const PagedAttnParams& p, int b) {
-  int lo = 0, hi = p.groups;  // the last group that starts at or before b
+// The last of `n` ascending values that is at most x, or -1.
+__device__ __forceinline__ int last_at_most(const int32_t* v, int n, int x) {
+  int lo = 0, hi = n;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(p.group_start + mid) <= b) lo = mid + 1;
+    if (__ldg(v + mid) <= x) lo = mid + 1;
     else hi = mid;
   }
-  int t0, n, s0, sn;
-  if (lo == 0 || b >= __ldg(p.group_start + lo) || b < __ldg(p.group_start + lo - 1)) return -1;
-  // (a sequence whose tokens are not among its group's: starts that descend)
-  return group_range(p, lo - 1, t0, n) && seq_range(p.q_start, b, p.T, s0, sn) && s0 >= t0 && s0 + sn <= t0 + n
-             ? lo - 1 : -1;
+  return lo - 1;
 }
-// Tokens of the pass's sequence b.
-__device__ __forceinline__ bool token_range(const PagedAttnParams& p, int b, int& t0, int& n) {
-  return p.pass == 1 ? group_range(p, b, t0, n) : seq_range(p.q_start, b, p.T, t0, n);
-}
-// The position of a group's token t, behind a prefix of L rows.
+// The position of token t of group g behind a prefix of L rows.
 __device__ __forceinline__ int prefix_pos(const PagedAttnParams& p, int g, int t, int L) {
   if (p.window == 0 && !p.slopes) return L;  // (not looked at)
-  int lo = __ldg(p.group_start + g), hi = __ldg(p.group_start + g + 1);
-  while (hi - lo > 1) {  // the last of its sequences that starts at or before t
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.q_start + mid) <= t) lo = mid;
-    else hi = mid;
-  }
-  return L + __ldg(p.own_len + lo) +
-         (p.own_anc ? anc_depth(p.own_anc + (size_t)t * p.W, p.W) : t - __ldg(p.q_start + lo));
+  const int b0 = __ldg(p.group_start + g), n = __ldg(p.group_start + g + 1) - b0;
+  const int b = b0 + max(0, last_at_most(p.q_start + b0, n, t));
+  return L + __ldg(p.kv_len + b) +
+         (p.anc ? anc_depth(p.anc + (size_t)t * p.W, p.W) : t - __ldg(p.q_start + b));
 }
 
 struct Seq {
   int t0, n, L;
   bool bad;  // rows are zeroed
+  bool shared;  // a prefix
 };
 
+// (b: on the line, prefixes ahead of sequences)
 __device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
   Seq s;
+  s.shared = b < p.groups;
+  if (s.shared) {
+    s.L = __ldg(p.prefix_len + b);
+    if (!group_range(p, b, s.t0, s.n)) s.n = 0;
+    s.bad = s.L < 0 || s.L > ((long long)p.prefix_P << p.page_shift);
+    return s;
+  }
+  b -= p.groups;
   s.L = __ldg(p.kv_len + b);
-  if (!token_range(p, b, s.t0, s.n)) s.n = 0;
-  s.bad = s.L < 0 || (long long)s.L + (p.pass == 1 ? 0 : s.n) > ((long long)p.P << p.page_shift) ||
+  if (!seq_range(p.q_start, b, p.T, s.t0, s.n)) s.n = 0;
+  s.bad = s.L < 0 || (long long)s.L + s.n > ((long long)p.P << p.page_shift) ||
           (p.anc && s.n > 64 * p.W);
   return s;
 }
@@ -306,7 +289,7 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
 __device__ __forceinline__ void key_range(const PagedAttnParams& p, const Seq& s, int qt, int& lo,
                                           int& hi) {
   const int first = qt * p.tq;
-  if (p.pass == 1) {  // (its tokens are all behind the prefix)
+  if (s.shared) {  // (its tokens are all behind the prefix)
     hi = s.L;
     lo = p.window > 0 ? max(0, s.L - p.window + 1) : 0;
     return;
@@ -336,10 +319,7 @@ struct Part {
   int begin, end;    // key tiles of this part
   int slot;          // partial slot, or -1: the whole unit is here
   int parts;         // a unit that this part begins: how many parts it has
-  int pre;           // (second pass) its rows are to be joined with the first pass's
 };
-// A split unit in `desc`: its parts, and a bit for Part::pre.
-constexpr int kPartsPre = 1 << 30;
 
 // (64-bit division costs some hundred cycles; the quotients here are small)
 __device__ __forceinline__ long long div_fast(long long a, long long b) {
@@ -354,7 +334,6 @@ struct Cursor {
   long long at;           // cost behind the share's start
   int b, kvh, qt, pos;    // unit, and cost of it that lies behind
   int last;               // the share's last sequence (or one behind it, where a thread looks at several)
-  int pre_of, pre;        // (second pass) the last sequence asked, and whether it has a prefix
   Seq s;
 
   __device__ __forceinline__ int cost_of(const PagedAttnParams& p, int tiles) const {
@@ -378,11 +357,6 @@ struct Cursor {
         o.begin = o.lo / KT + a;
         o.end = o.lo / KT + e;
         o.slot = (a == 0 && e == tiles) ? -1 : p.merge ? 2 * share_index() + (a == 0) : share_index();
-        if (p.pass == 2 && pre_of != b) {
-          pre = group_of(p, b) >= 0;
-          pre_of = b;
-        }
-        o.pre = p.pass == 2 && !s.bad ? pre : 0;
         o.parts = (o.slot >= 0 && a == 0) ? (int)div_fast(at - pos + cost - 1, share) + 1 : 0;
       }
       rest -= take;
@@ -395,10 +369,10 @@ struct Cursor {
           if (++kvh == p.Hkv) {
             kvh = 0;
             do {
-              if (++b >= p.B) break;
+              if (++b >= p.groups + p.B) break;
               s = load_seq(p, b);
             } while (s.n == 0);
-            if (b >= p.B) rest = 0;
+            if (b >= p.groups + p.B) rest = 0;
           }
         }
       }
@@ -430,8 +404,8 @@ __device__ __forceinline__ void find_share(const PagedAttnParams& p, Cursor<KT>&
   __shared__ long long s_warp[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lanes = 1 << p.share_lanes;
-  const int per = ceil_div(p.B, THREADS);  // (1 where lanes > 1)
-  const int own = tid >> p.share_lanes, b0 = min(p.B, own * per), b1 = min(p.B, b0 + per);
+  const int seqs = p.groups + p.B, per = ceil_div(seqs, THREADS);  // (1 where lanes > 1)
+  const int own = tid >> p.share_lanes, b0 = min(seqs, own * per), b1 = min(seqs, b0 + per);
   Cursor<KT> c;
   int qt0 = 0, qt1 = 0;  // this lane's query tiles
   auto tiles_cost = [&](const Seq& s) {  // of one kv head's units among them
@@ -500,7 +474,6 @@ __device__ __forceinline__ void find_share(const PagedAttnParams& p, Cursor<KT>&
         s_cur.kvh = c.kvh;
         s_cur.qt = c.qt;
         s_cur.pos = c.pos;
-        s_cur.pre_of = -1;
         s_cur.s = c.s;
         break;
       }
@@ -543,38 +516,13 @@ struct PartRing {
   __device__ __forceinline__ void done(uint32_t n) { mbar_arrive(&empty[n % kPartRing]); }  // one thread
 };
 
-// Whether the prefix of sequence b, if it has one, fits and its pages are pages, as far as the
-// sequence's window reaches.
-__device__ __forceinline__ bool prefix_ok(const PagedAttnParams& p, int b, int n, int own, int lane, int lanes) {
-  const int g = group_of(p, b);
-  if (g < 0) {  // outside the groups, or in one that is none
-    int lo = 0, hi = p.groups;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.group_start + mid) <= b) lo = mid + 1;
-      else hi = mid;
-    }
-    return lo == 0 || (lo == p.groups && b >= __ldg(p.group_start + lo));
-  }
-  const int L = __ldg(p.prefix_len + g);
-  if (L < 0 || L > ((long long)p.prefix_P << p.page_shift)) return false;
-  if (n == 0) return true;
-  const long long lo = p.window > 0 ? max(0ll, (long long)L + own - p.window + 1) : 0;
-  int any = 0;
-  for (long long j = (lo >> p.page_shift) + lane; j << p.page_shift < L; j += lanes) {
-    const int page = TV_IN(j, p.prefix_P) ? __ldg(p.prefix_table + (size_t)g * p.prefix_P + j) : 0;
-    any |= page < 0 || page >= p.num_pages;
-  }
-  return any == 0;
-}
 // Whether sequence b's lengths fit and its pages are pages, as far as the window reaches;
 // `lane` of `lanes` threads looks at its share of the pages.
 __device__ __forceinline__ bool seq_ok(const PagedAttnParams& p, int b, int lane, int lanes) {
   int t0, n;
   if (!seq_range(p.q_start, b, p.T, t0, n)) return false;
-  const Seq s = load_seq(p, b);
+  const Seq s = load_seq(p, p.groups + b);
   if (s.bad) return false;
-  if (p.pass == 2 && !prefix_ok(p, b, n, s.L, lane, lanes)) return false;
   if (n == 0) return true;
   int lo, hi, any = 0;
   key_range(p, s, 0, lo, hi);
@@ -587,25 +535,16 @@ __device__ __forceinline__ bool seq_ok(const PagedAttnParams& p, int b, int lane
   }
   return any == 0;
 }
-// Whether a CTA that gave up may have left rows of sequence b undone; `lane` of `lanes` threads
+// Whether a CTA that gave up may have left rows of sequence b (of group g) undone; `lane` of `lanes` threads
 // looks at its share of the CTAs.
-__device__ __forceinline__ bool is_late(const PagedAttnParams& p, int b, int lane, int lanes) {
-  const bool pre = p.pass == 2 && *(volatile unsigned long long*)p.pre_any_late == p.token;
-  const bool own = *(volatile unsigned long long*)p.any_late == p.token;
-  if (!pre && !own) return false;
+__device__ __forceinline__ bool is_late(const PagedAttnParams& p, int b, int lane, int lanes, int g = -1) {
+  if (*(volatile unsigned long long*)p.any_late != p.token) return false;
   int t0, n;
   bool late = false;
-  if (own)
-    for (int c = lane; c < gridDim.x; c += lanes) {
-      volatile Late* l = p.late + c;
-      late |= l->token == p.token && b >= l->first && b <= l->last;
-    }
-  if (pre) {
-    const int g = group_of(p, b);
-    for (int c = lane; g >= 0 && c < p.pre_ctas; c += lanes) {
-      volatile Late* l = p.pre_late + c;
-      late |= l->token == p.token && g >= l->first && g <= l->last;
-    }
+  for (int c = lane; c < p.ctas; c += lanes) {
+    volatile Late* l = p.late + c;
+    late |= l->token == p.token && ((b + p.groups >= l->first && b + p.groups <= l->last) ||
+                                    (g >= l->first && g <= l->last));
   }
   return late && seq_range(p.q_start, b, p.T, t0, n) && n > 0;
 }
@@ -688,7 +627,9 @@ struct PageFeed {
     const int lane = threadIdx.x & 31, back = lane / per_tile, t = t0 - back;
     const int key = t * KT + (lane - back * per_tile) * rows, j = key >> p.page_shift;
     next_needed = back < tiles && t >= w.begin && key < w.hi && key + rows > w.lo;
-    next = next_needed && TV_IN(j, p.P) ? __ldg(p.table + (size_t)w.b * p.P + j) : -1;
+    const int P = w.s.shared ? p.prefix_P : p.P;
+    const int32_t* row = w.s.shared ? p.prefix_table + (size_t)w.b * P : p.table + (size_t)(w.b - p.groups) * P;
+    next = next_needed && TV_IN(j, P) ? __ldg(row + j) : -1;
   }
   __device__ __forceinline__ void take(const PagedAttnParams& p) {
     const bool is_page = next >= 0 && next < p.num_pages;
@@ -748,11 +689,10 @@ cudaError_t launch_rows_e4m3(const PagedPlan& pl, int D, bool mod, const CUtenso
                              const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
 cudaError_t launch_rows_int8(const PagedPlan& pl, int D, bool mod, const CUtensorMap& tmK,
                              const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
-cudaError_t launch_rows_prefix(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmK,
-                               const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
-cudaError_t launch_tc_prefix(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
-                             const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
-                             cudaStream_t stream);
+// a call with shared prefixes: paged_tc_kernel and the kernel that joins the rows
+cudaError_t launch_prefix(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
+                          const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
+                          cudaStream_t stream);
 cudaError_t launch_tc(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
                       const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
                       cudaStream_t stream);

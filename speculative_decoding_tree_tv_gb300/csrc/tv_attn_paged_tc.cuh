@@ -125,10 +125,19 @@ __device__ __forceinline__ void tree_chunk(const PagedAttnParams& p, const Row& 
   }
 }
 
+// Where the kernel that joins rows finds those of a unit (its first part's warp).
+__device__ __forceinline__ void note_unit(const PagedAttnParams& p, const Part& w) {
+  int4* src = p.src + (w.s.shared ? 0 : (size_t)p.T * p.Hkv);
+  for (int i = threadIdx.x & 31; i < w.ntok; i += 32) {
+    const int t = w.s.t0 + w.first + i;
+    if (TV_IN(t, p.T)) src[(size_t)t * p.Hkv + w.kvh] = make_int4(w.slot, w.parts, w.s.t0 + w.first, w.s.shared ? w.b : w.b - p.groups);
+  }
+}
+
 // CAP: a softcap; BIAS: slopes, or tree distances that the window reaches.  Variants of
 // their own, and rolled loops wherever a warp does not wait for them: a loop over the tiles that is
 // larger than the instruction cache (some 32 KB) runs at half the speed.
-// PRE: a pass of an attention with shared prefixes (PagedAttnParams::pass).
+// PRE: of a call with shared prefixes: a part may be a prefix's, and rows are left as they are.
 template <int D, bool F16, bool CAP, bool BIAS, bool PRE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -273,14 +282,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint32_t parts = 0;
     Part w;
     Cursor<kTcKeys> cur = s_cur;
-    if (p.merge && lane == 0) p.desc[share_index()] = make_int4(0, 0, 0, 0);
+    if (!PRE && p.merge && lane == 0) p.desc[share_index()] = make_int4(0, 0, 0, 0);
     for (;; ++n) {
       const bool more = cur.next(p, w);
       ok = s_ring.publish(n, w, p.wait_limit);
       if (!ok || !more) break;
-      if (p.merge && w.parts && lane == 0)
-        p.desc[share_index()] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh,
-                                          PRE && w.pre ? w.parts | kPartsPre : w.parts);
+      if (!PRE && p.merge && w.parts && lane == 0)
+        p.desc[share_index()] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
+      if (PRE && (w.parts || w.slot < 0)) note_unit(p, w);
       if (w.begin == w.end) continue;
       ok = warp_wait(&bar_q_empty, (parts & 1) ^ 1, p.wait_limit) && !s_abort;
       if (!ok) break;
@@ -391,7 +400,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     ok = __all_sync(0xffffffffu, ok);
   } else {
     // -------------------------------------------------------------- softmax
-    const bool shared = PRE && p.pass == 1;  // rows of several sequences, behind all of the keys
     const int rb = warp >> 2, row = tid & (kRB - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128 * rb, tO = tmem + kOCol + 128 * rb;
@@ -419,13 +427,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const int tile_tok = rb * nb + tl;
         const bool mine = tl < nb && tile_tok < w.ntok;
         const size_t oidx = (size_t)(w.s.t0 + w.first + tile_tok) * p.Hq + w.kvh * p.G + h_in;
-        if (shared) {  // (or one without a prefix)
-          if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq)) {
-            float4* prow = reinterpret_cast<float4*>(p.pre + oidx * D);
-#pragma unroll 1
-            for (int c = 0; c < D / 4; ++c) prow[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-            p.pre_ml[oidx] = make_float2(-INFINITY, 0.0f);
-          }
+        if (PRE) {  // (or a prefix without rows)
+          if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq))
+            p.raw_ml[oidx + (w.s.shared ? 0 : (size_t)p.T * p.Hq)] = make_float2(-INFINITY, 0.0f);
         } else if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq)) {
           uint4* orow = reinterpret_cast<uint4*>(p.out + oidx * D);
 #pragma unroll
@@ -446,7 +450,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const int i = w.first + min(rb * nb + min(tl, nb - 1), w.ntok - 1);
       const bool warp_works = warp_in_block && rb * nb + (warp & 3) * 32 / p.G < w.ntok;
       Row r;
-      r.anc = p.anc ? p.anc + (size_t)(w.s.t0 + i) * p.W : nullptr;
+      r.anc = p.anc && !(PRE && w.s.shared) ? p.anc + (size_t)(w.s.t0 + i) * p.W : nullptr;
+      const bool shared = PRE && w.s.shared;  // (its rows are several sequences', behind all of the keys)
       r.pos = shared ? prefix_pos(p, w.b, w.s.t0 + i, w.s.L) : w.s.L + (p.anc ? anc_depth(r.anc, p.W) : i);
       r.limit = shared || p.anc ? w.s.L : w.s.L + i + 1;
       r.from = p.window > 0 ? r.pos - p.window + 1 : 0;
@@ -699,10 +704,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           m_all = top;
         }
         if (!ok) break;
-        // (second pass) the prefix's share of the row
-        const bool joins = PRE && w.pre && mine;
-        float fo = 1.0f, fp = 0.0f;
-        if (joins) join_factors(__ldcg(&p.pre_ml[oidx]), m_all, l_all, fo, fp);
         const float f0 = m_run == -INFINITY ? 0.0f : ex2(m_run - m_all);
         const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
         uint8_t* orow = reinterpret_cast<uint8_t*>(p.out + oidx * D);
@@ -712,7 +713,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           tmem_ld32(tO + lane_base + 64 * c, o[0]);
           tmem_ld32(tO + lane_base + 64 * c + 32, o[1]);
           tmem_wait_ld();
-          if ((more || (PRE && w.pre)) && mine) {
+          if (more && mine) {
 #pragma unroll
             for (int e = 0; e < 64; ++e)
               o[e >> 5][e & 31] = __float_as_uint(__uint_as_float(o[e >> 5][e & 31]) * f0);
@@ -735,23 +736,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               }
             }
           }
-          if (joins) {
-            const float4* prow = reinterpret_cast<const float4*>(p.pre + oidx * D) + 16 * c;
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              uint32_t* x = &o[q >> 3][4 * (q & 7)];
-              const float4 v = fp == 0.0f ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(prow + q);
-              x[0] = __float_as_uint(fmaf(fp, v.x, __uint_as_float(x[0])));
-              x[1] = __float_as_uint(fmaf(fp, v.y, __uint_as_float(x[1])));
-              x[2] = __float_as_uint(fmaf(fp, v.z, __uint_as_float(x[2])));
-              x[3] = __float_as_uint(fmaf(fp, v.w, __uint_as_float(x[3])));
-            }
-          }
-          if (shared) {
+          if (PRE) {
             if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq))
 #pragma unroll
               for (int q = 0; q < 8; ++q)  // 8 columns: a sector
-                store32(reinterpret_cast<uint8_t*>(p.pre + oidx * D + 64 * c + 8 * q),
+                store32(reinterpret_cast<uint8_t*>(p.raw + (oidx + (shared ? 0 : (size_t)p.T * p.Hq)) * D + 64 * c + 8 * q),
                         *reinterpret_cast<const uint32_t(*)[8]>(&o[q >> 2][8 * (q & 3)]), true);
           } else if (mine && TV_CHECK(oidx < (size_t)p.T * p.Hq))
 #pragma unroll
@@ -765,7 +754,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             }
           __syncwarp();
         }
-        if (shared && mine) p.pre_ml[oidx] = make_float2(m_all, l_all);
+        if (PRE && mine) p.raw_ml[oidx + (shared ? 0 : (size_t)p.T * p.Hq)] = make_float2(m_all, l_all);
         else if (mine && p.lse) p.lse[oidx] = l_all == 0.0f ? -INFINITY : (m_all + log2f(l_all)) * kLn2;
       }
       tc_fence_before();

@@ -106,7 +106,7 @@ ATTN = [(dict(B=-1), 1), (dict(T=-1), 1), (dict(Pg=0), 1), (dict(Hq=0), 1), (dic
         (dict(B=5000), 3), (dict(Hq=2 * 130), 3), (dict(T=2**30), 3), (dict(Pg=2**28), 3),
         (dict(anc=P, max_q=513), 3), (dict(q=None), 1), (dict(out=None), 1), (dict(table=None), 1),
         (dict(q_start=None), 1), (dict(kv_len=None), 1), (dict(q=ODD), 1), (dict(out=ODD), 1), (dict(qt=100), 1),
-        (dict(qh=-64), 1), (dict(n=0), 7), (dict(ws=None), 7), (dict(B=0), 0)]
+        (dict(qh=-64), 1), (dict(), 7), (dict(ws=None, n=2**30), 7), (dict(B=0), 0)]
 
 
 def args(**kw):
