@@ -73,6 +73,7 @@ struct PagedAttnParams {
   int min_share;    // least cost of a share
   int share_lanes;  // log2 of the lanes that look at one sequence (1 << share_lanes) * B threads at most
   int whole;        // one unit a CTA, none is split
+  int unit_cost;    // of starting and finishing a unit, in tiles
   int f16;          // 16-bit tensors are fp16 (the 8-bit cache's kernels)
   int out_sectors;  // out lies on a 32-byte boundary
   int merge;        // a merge kernel joins the parts of split units, else the CTA a unit begins in
@@ -337,14 +338,14 @@ struct Cursor {
   Seq s;
 
   __device__ __forceinline__ int cost_of(const PagedAttnParams& p, int tiles) const {
-    return p.whole ? 1 : tiles + kUnitCost;
+    return p.whole ? 1 : tiles + p.unit_cost;
   }
   __device__ __forceinline__ bool next(const PagedAttnParams& p, Part& o) {
     while (rest > 0) {
       const int tiles = key_tiles<KT>(p, s, qt), cost = cost_of(p, tiles);
       const int take = (int)min((long long)(cost - pos), rest);
-      const int a = p.whole ? 0 : max(0, pos - kUnitCost);
-      const int e = p.whole ? tiles : max(0, pos + take - kUnitCost);
+      const int a = p.whole ? 0 : max(0, pos - p.unit_cost);
+      const int e = p.whole ? tiles : max(0, pos + take - p.unit_cost);
       const bool ends = pos + take == cost;
       const bool emit = e > a || (tiles == 0 && ends);
       if (emit) {
@@ -394,6 +395,11 @@ __device__ __forceinline__ void prefetch_lengths(const PagedAttnParams& p) {
   }
   const long long words = min((long long)p.B * p.P, (long long)step);  // (one line a thread)
   if (first < words) line_prefetch_l2(p.table + first);
+  for (int i = first; i < p.groups; i += step) {
+    line_prefetch_l2(p.group_start + i);
+    line_prefetch_l2(p.prefix_len + i);
+  }
+  if (first < (long long)p.groups * p.prefix_P) line_prefetch_l2(p.prefix_table + first);
 }
 
 // Finds this CTA's share (s_cur: shared; rest is 0 where there is none).  All THREADS threads call it;

@@ -283,16 +283,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     Part w;
     Cursor<kTcKeys> cur = s_cur;
     if (!PRE && p.merge && lane == 0) p.desc[share_index()] = make_int4(0, 0, 0, 0);
-    for (;; ++n) {
-      const bool more = cur.next(p, w);
-      ok = s_ring.publish(n, w, p.wait_limit);
-      if (!ok || !more) break;
-      if (!PRE && p.merge && w.parts && lane == 0)
-        p.desc[share_index()] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
-      if (PRE && (w.parts || w.slot < 0)) note_unit(p, w);
-      if (w.begin == w.end) continue;
-      ok = warp_wait(&bar_q_empty, (parts & 1) ^ 1, p.wait_limit) && !s_abort;
-      if (!ok) break;
+    // One thread: a part's Q rows, as boxes of nb tokens.
+    auto load_q = [&](const Part& w) {
       if (lane == 0) {
         const int nrb = w.ntok > nb ? 2 : 1;
         mbar_expect_tx(&bar_q_full, (uint32_t)(nrb * A * 64 * p.G * nb * 2));
@@ -304,6 +296,47 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       }
       __syncwarp();
       ++parts;
+    };
+    if (PRE) {
+      // Many small units: parts are published ahead of the Q rows that they wait for, so that their K and V
+      // are on their way.
+      uint32_t nq = 0;  // parts whose Q rows are asked for
+      bool more = true;
+      for (;;) {
+        const bool behind = nq < n, full = n - nq == kPartRing - 1;
+        const bool free = behind && __all_sync(0xffffffffu, mbar_test(&bar_q_empty, (parts & 1) ^ 1));
+        if (behind && (full || !more || free)) {
+          const Part& q = s_ring.at(nq);
+          if (q.begin != q.end) {
+            ok = warp_wait(&bar_q_empty, (parts & 1) ^ 1, p.wait_limit) && !s_abort;
+            if (!ok) break;
+            load_q(q);
+          }
+          ++nq;
+        } else if (more) {
+          more = cur.next(p, w);
+          ok = s_ring.publish(n, w, p.wait_limit);
+          if (!ok) break;
+          if (more) {
+            ++n;
+            if (w.parts || w.slot < 0) note_unit(p, w);
+          }
+        } else {
+          break;
+        }
+      }
+    } else {
+      for (;; ++n) {
+        const bool more = cur.next(p, w);
+        ok = s_ring.publish(n, w, p.wait_limit);
+        if (!ok || !more) break;
+        if (p.merge && w.parts && lane == 0)
+          p.desc[share_index()] = make_int4(w.s.t0 + w.first, w.ntok, w.kvh, w.parts);
+        if (w.begin == w.end) continue;
+        ok = warp_wait(&bar_q_empty, (parts & 1) ^ 1, p.wait_limit) && !s_abort;
+        if (!ok) break;
+        load_q(w);
+      }
     }
     if (!p.merge) write_status(p);
     if (parts > 0) mbar_wait(&bar_q_full, (parts - 1) & 1);
