@@ -363,7 +363,7 @@ tv_status tv_debug_set_wait_limit(long long cycles);
  *                       4 expand, 5 attention, 6 commit, 7 expected,
  *                       8 top-n selection, 9 library, 10 pages,
  *                       11 to 13 paged attention, 14 the 8-bit cache,
- *                       15 and 16 its attention, 17 attention behind
+ *                       15, 16 and 18 its attention, 17 attention behind
  *                       shared prefixes.  Host call; it must not
  *                       overlap a launch of this library on the device.
  *                       TV_ERR_INVALID_ARG if site is NULL, TV_ERR_CUDA if
@@ -808,9 +808,9 @@ tv_status tv_paged_read_q8(const tv_q8_cache* cache, const int32_t* block_table,
  * sums as there (q and out of cache->dtype).  Arguments, statuses and limits are tv_attn_paged's, with these
  * differences:
  *   - the workspace is tv_attn_paged_q8_workspace_size() bytes;
- *   - Hq / Hkv is at most 16;
  *   - a row of V whose scale is 255 makes the outputs of the tokens that see it NaN, and no others';
- *     codes that tv_paged_append_q8 does not write (the NaNs of e4m3) count as V values that are not finite.
+ *   - codes are ones that tv_paged_append_q8 writes: what a token gets that sees one of e4m3's NaN codes is
+ *     undefined.
  */
 size_t tv_attn_paged_q8_workspace_size(int max_q, int Hq, int Hkv, int D);
 tv_status tv_attn_paged_q8(const void* q, int64_t q_token_stride, int64_t q_head_stride,

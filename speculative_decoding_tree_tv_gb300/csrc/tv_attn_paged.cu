@@ -160,9 +160,9 @@ struct CacheArg {
 };
 
 // A cache side: D by rows, heads and pages; a box is 64 dims (of codes: all) of `rows` rows of one
-// page and head.
+// page and head, for codes that go on as they are (plain) not swizzled.
 bool map_cache(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void* base, const CacheArg& a,
-               const long long (&stride)[3], const int (&order)[3], int rows) {
+               const long long (&stride)[3], const int (&order)[3], int rows, bool plain) {
   const cuuint64_t extent[3] = {(cuuint64_t)1 << a.c.page_shift, (cuuint64_t)a.Hkv, (cuuint64_t)a.c.num_pages};
   const bool codes = a.format >= 0;
   cuuint64_t dims[4] = {(cuuint64_t)a.D}, strides[3];
@@ -177,7 +177,9 @@ bool map_cache(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, void*
                 codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                       : a.dtype == TV_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                codes && a.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                plain                ? CU_TENSOR_MAP_SWIZZLE_NONE
+                : codes && a.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -201,13 +203,13 @@ long long wait_limit() {
 }
 
 // Which kernel runs, by the rows of the largest unit.
-PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long keys, bool q8) {
+PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long keys) {
   PagedPlan pl;
   const long long rows = (long long)max_q * G;
   // 64 decode sequences of 512 to 8,192 keys, 8 kv heads: 4 rows a unit 186 us here and 198 us on the
   // tcgen05 kernel (D 64: 102 and 149 us), 16 rows 171 and 180 us; 32 rows took 430 us with two row
   // tiles a warp here (its registers spill) and 185 us there.
-  pl.small = rows <= 16 || q8;
+  pl.small = rows <= 16;
   if (pl.small) {
     pl.rows = 16;
     pl.nb = pl.tq = (rows <= 8 ? 8 : 16) / G;
@@ -273,7 +275,7 @@ void set_wait_limit(long long cycles) {
 extern "C" size_t tv_attn_paged_workspace_size(int max_q, int Hq, int Hkv, int D) {
   if (max_q < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128))
     return 0;
-  return tv::paged::paged_plan(max_q, Hkv, Hq / Hkv, D, 0, 0, 0, false).bytes();  // (whatever B, T and keys are)
+  return tv::paged::paged_plan(max_q, Hkv, Hq / Hkv, D, 0, 0, 0).bytes();  // (whatever B, T and keys are)
 }
 
 
@@ -329,7 +331,6 @@ tv_status check_attn(AttnArgs& a, const CacheArg& cache) {
     return TV_ERR_INVALID_ARG;
   if (a.Hq % Hkv != 0) return TV_ERR_INVALID_ARG;
   if ((D != 64 && D != 128) || a.Hq / Hkv > 128 || a.B > kMaxSeqs) return TV_ERR_UNSUPPORTED;
-  if (cache.format >= 0 && a.Hq / Hkv > 16) return TV_ERR_UNSUPPORTED;
   if (a.anc_mask && a.max_q > TV_MAX_NODES) return TV_ERR_UNSUPPORTED;
   if ((long long)a.T * a.Hq > 0x7fffffffll || (long long)a.B * a.P > 0x7fffffffll ||
       ((long long)a.P << cache.c.page_shift) > 0x7fffffffll - 512)
@@ -376,8 +377,9 @@ tv_status make_pass(const AttnArgs& a, const CacheArg& cache, const PagedPlan& p
   if (!encode) return TV_ERR_CUDA;
   CUtensorMap &tmQ = out->tmQ, &tmK = out->tmK, &tmV = out->tmV;
   const int rows = min(1 << c.page_shift, pl.small && !pl.whole && !q8 ? 64 : 128);
-  if (!map_cache(encode, &tmK, cache.k, cache, stride, order, rows) ||
-      !map_cache(encode, &tmV, cache.v, cache, stride, order, rows))
+  const bool plain = q8 && !pl.small;  // (codes on their way to 16-bit tiles)
+  if (!map_cache(encode, &tmK, cache.k, cache, stride, order, rows, plain) ||
+      !map_cache(encode, &tmV, cache.v, cache, stride, order, rows, plain))
     return TV_ERR_INVALID_ARG;
   if (!pl.small && a.T > 0) {
     // q as [tokens][heads][D]; a box is 64 dims of the group's heads of nb tokens
@@ -402,6 +404,7 @@ tv_status make_pass(const AttnArgs& a, const CacheArg& cache, const PagedPlan& p
   p.k_scale = cache.k_scale;
   p.v_scale = cache.v_scale;
   p.f16 = f16;
+  p.e4m3 = cache.format == TV_E4M3;
   p.table = a.block_table;
   p.q_start = a.q_start;
   p.kv_len = a.kv_len;
@@ -464,7 +467,9 @@ cudaError_t launch_pass(const Pass& s, const CacheArg& cache, cudaStream_t strea
   const int D = cache.D;
   const bool f16 = cache.dtype == TV_FP16, mod = s.bias || p.softcap_log2 > 0.0f;
   cudaError_t e;
-  if (cache.format >= 0)
+  if (cache.format >= 0 && !pl.small)
+    e = launch_tc_q8(pl, D, f16, s.bias, s.tmQ, s.tmK, s.tmV, p, stream);
+  else if (cache.format >= 0)
     e = cache.format == TV_E4M3 ? launch_rows_e4m3(pl, D, mod, s.tmK, s.tmV, p, stream)
                                 : launch_rows_int8(pl, D, mod, s.tmK, s.tmV, p, stream);
   else if (p.groups > 0)
@@ -487,7 +492,7 @@ tv_status attend(AttnArgs a, const CacheArg& cache) {
   tv_status st = check_attn(a, cache);
   if (st != TV_OK || a.B == 0) return st;
   const PagedPlan pl = paged_plan(a.max_q, cache.Hkv, a.Hq / cache.Hkv, cache.D, a.B, a.T,
-                                  (long long)a.P << cache.c.page_shift, cache.format >= 0);
+                                  (long long)a.P << cache.c.page_shift);
   if (!a.workspace || a.ws_bytes < pl.bytes() || (reinterpret_cast<uintptr_t>(a.workspace) & 255))
     return TV_ERR_WORKSPACE;
   Pass s;
@@ -503,7 +508,7 @@ struct PrefixPlan {
 PrefixPlan prefix_plan(int T, int groups, int Hq, int Hkv, int D, int B, long long keys) {
   PrefixPlan f;
   PagedPlan& pl = f.pl;
-  pl = paged_plan(TV_MAX_NODES, Hkv, Hq / Hkv, D, B, T, 1ll << 40, false);  // (the tcgen05 kernel's)
+  pl = paged_plan(TV_MAX_NODES, Hkv, Hq / Hkv, D, B, T, 1ll << 40);  // (the tcgen05 kernel's)
   // (units of prefixes and of sequences)
   pl.whole = keys <= kWholeTcKeys && (long long)Hkv * (2ll * (T / pl.tq) + groups + B) <= device_sm_count();
   if (pl.whole) pl.min_share = 1;
@@ -573,7 +578,7 @@ extern "C" tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_
 extern "C" size_t tv_attn_paged_q8_workspace_size(int max_q, int Hq, int Hkv, int D) {
   if (max_q < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 128 || (D != 64 && D != 128))
     return 0;
-  return tv::paged::paged_plan(max_q, Hkv, Hq / Hkv, D, 0, 0, 0, true).bytes();
+  return tv::paged::paged_plan(max_q, Hkv, Hq / Hkv, D, 0, 0, 0).bytes();
 }
 
 extern "C" tv_status tv_attn_paged_q8(const void* q, int64_t q_token_stride, int64_t q_head_stride,

@@ -74,7 +74,8 @@ struct PagedAttnParams {
   int share_lanes;  // log2 of the lanes that look at one sequence (1 << share_lanes) * B threads at most
   int whole;        // one unit a CTA, none is split
   int unit_cost;    // of starting and finishing a unit, in tiles
-  int f16;          // 16-bit tensors are fp16 (the 8-bit cache's kernels)
+  int f16;          // 16-bit tensors are fp16 (the 8-bit cache's small units)
+  int e4m3;         // codes of an 8-bit cache are e4m3, else int8
   int out_sectors;  // out lies on a 32-byte boundary
   int merge;        // a merge kernel joins the parts of split units, else the CTA a unit begins in
   unsigned long long token;      // this call's mark in `ready`
@@ -691,6 +692,9 @@ constexpr int kQ8Keys = 128;  // keys of a stage of the 8-bit cache's small kern
 // bias: slopes, or tree distances that the window reaches (mod: those or a cap)
 cudaError_t launch_rows(const PagedPlan& pl, int D, bool f16, bool mod, const CUtensorMap& tmK,
                         const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
+cudaError_t launch_tc_q8(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
+                         const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
+                         cudaStream_t stream);
 cudaError_t launch_rows_e4m3(const PagedPlan& pl, int D, bool mod, const CUtensorMap& tmK,
                              const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream);
 cudaError_t launch_rows_int8(const PagedPlan& pl, int D, bool mod, const CUtensorMap& tmK,

@@ -8,7 +8,7 @@ namespace paged {
 cudaError_t launch_tc(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
                       const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
                       cudaStream_t stream) {
-  return launch_any<false>(pl, D, f16, bias, tmQ, tmK, tmV, p, stream);
+  return launch_any<false, false>(pl, D, f16, bias, tmQ, tmK, tmV, p, stream);
 }
 
 }  // namespace paged

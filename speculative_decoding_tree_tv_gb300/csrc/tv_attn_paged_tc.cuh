@@ -25,12 +25,13 @@
 #include <climits>
 
 #include "tv_attn_paged.cuh"
+#include "tv_quant.cuh"
 
 namespace tv {
 namespace paged {
 namespace {
 
-constexpr int kTcThreads = 384;
+constexpr int kTcThreads = 384, kConvertThreads = 128;  // (those: over an 8-bit cache)
 constexpr int kRB = 128;           // rows of a row block
 constexpr int kAtomBytes = 16384;  // 128 rows x 128 bytes
 constexpr int kKStages = 2, kVStages = 3;
@@ -134,17 +135,167 @@ __device__ __forceinline__ void note_unit(const PagedAttnParams& p, const Part& 
   }
 }
 
+// ------------------------------------------------------------- 8-bit tiles
+// A raw tile of 128 rows of D codes lands in the second half of its stage; 128 threads take it into registers,
+// and then write the 16-bit tile over the whole stage, in the layout that TMA gives a 16-bit cache's.  A thread
+// has 16 codes of D / 16 rows: chunk ctid % (D / 16), rows ctid / (D / 16) + i 2048 / D.
+constexpr float kTcPBias = 6.0f;
+
+// Registers of the threads of a warpgroup (Q8 kernels alone).
+template <bool MORE, int N, bool Q8>
+__device__ __forceinline__ void set_registers() {
+  if (Q8 && MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if (Q8 && !MORE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int D>
+__device__ __forceinline__ void load_raw(const uint8_t* tile, int ctid, uint4 (&x)[D / 16]) {
+  const uint4* raw = reinterpret_cast<const uint4*>(tile + TcLayout<D>::kTile / 2) + ctid;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) x[i] = raw[i * 128];
+}
+// The largest scale byte of rows z0 .. z1 - 1 that are numbers, at least 1 (by a whole warp).
+__device__ __forceinline__ int scale_top(const uint8_t* scale, int z0, int z1) {
+  const int r = (threadIdx.x & 31) * 4;
+  const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + r);
+  int top = 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int s = (s4 >> (8 * i)) & 255;
+    if (s != q8::kNaN && r + i >= z0 && r + i < z1) top = max(top, s);
+  }
+  return __reduce_max_sync(0xffffffffu, top);
+}
+// Notes which of rows z0 .. z1 - 1 are no numbers, if any is (by a whole warp).
+constexpr int kHasNaN = 1 << 16;
+__device__ __forceinline__ bool note_nan_rows(const uint8_t* scale, int z0, int z1, volatile uint32_t (&words)[4]) {
+  const int lane = threadIdx.x & 31, r = lane * 4;
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bits |= (uint32_t)(scale[r + i] == q8::kNaN && r + i >= z0 && r + i < z1) << i;
+  if (!__any_sync(0xffffffffu, bits != 0)) return false;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const uint32_t word = __reduce_or_sync(0xffffffffu, lane / 8 == w ? bits << (4 * (lane & 7)) : 0u);
+    if (lane == 0) words[w] = word;
+  }
+  return true;
+}
+// Pairs of 16-bit values of four codes, times a pair of equal factors (and `twice`, once more).
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t f) {
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&f));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t f) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(f));
+  return d;
+}
+__device__ __forceinline__ uint32_t sub_bf2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// The factor of a row with scale byte s, as a pair.  HALF: fp16 2^(s - over), over >= s - 1.  Else bf16, for
+// int8 2^(s - 127); for e4m3, whose bits are placed as a bf16's with an exponent too small by 120,
+// 2^(s - 7), in two steps where that is past the type.
+template <bool E4M3, bool HALF>
+__device__ __forceinline__ uint32_t row_factor(int s, int over, uint32_t& second) {
+  uint32_t f;
+  second = 0x3f803f80u;
+  if (s == q8::kNaN) {
+    f = 0x7fffu;
+  } else if (HALF) {
+    const int e = s - over + 15;
+    f = e > 0 ? (uint32_t)e << 10 : e > -10 ? 512u >> -e : 0u;
+  } else if (E4M3) {
+    const int e = s + 120;
+    f = (uint32_t)min(e, 254) << 7;
+    if (e > 254) second = (uint32_t)(e - 254 + 127) * 0x800080u;
+  } else {
+    f = s > 0 ? (uint32_t)s << 7 : 0x40u;
+  }
+  return f * 0x10001u;
+}
+template <bool E4M3, bool HALF>
+__device__ __forceinline__ void widen4(uint32_t x, uint32_t f, uint32_t& lo, uint32_t& hi) {
+  if (HALF) {
+    if (E4M3) {
+      asm("{.reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+          : "=r"(lo), "=r"(hi)
+          : "r"(x));
+    } else {  // 1024 + (code + 128), less 1152
+      const uint32_t u = x ^ 0x80808080u, a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+      const __half2 off = __half2half2(__ushort_as_half(0x6480));
+      const __half2 v0 = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+      const __half2 v1 = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+      lo = *reinterpret_cast<const uint32_t*>(&v0);
+      hi = *reinterpret_cast<const uint32_t*>(&v1);
+    }
+    lo = mul_half2(lo, f);
+    hi = mul_half2(hi, f);
+  } else {
+    if (E4M3) {  // sign, and the other seven bits four places down
+      const uint32_t a = __byte_perm(x, 0, 0x1404), b = __byte_perm(x, 0, 0x3424);
+      lo = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
+      hi = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
+    } else {  // 128 + the last seven bits, less 128 or, of a negative code, 256
+      const uint32_t a = __byte_perm(x, 0x43434343u, 0x4140), b = __byte_perm(x, 0x43434343u, 0x4342);
+      lo = sub_bf2(a & 0xff7fff7fu, a & 0xff80ff80u);
+      hi = sub_bf2(b & 0xff7fff7fu, b & 0xff80ff80u);
+    }
+    lo = mul_bf2(lo, f);
+    hi = mul_bf2(hi, f);
+  }
+}
+// Rows outside of [z0, z1) become zeros (their codes and scales may be anything), and so do V's rows that are no
+// numbers: a probability of 0 would meet them in the product.  The softmax threads that see one know of it.
+template <int D, bool E4M3, bool HALF>
+__device__ __forceinline__ void convert_tile(uint8_t* tile, const uint8_t* scale, int ctid, const uint4 (&x)[D / 16],
+                                             int over, int z0, int z1, bool drop_nan) {
+  constexpr int kChunks = D / 16, kRowStep = 128 / kChunks;
+  const int c = ctid % kChunks, r0 = ctid / kChunks;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const int r = r0 + i * kRowStep;
+    uint32_t second;
+    const uint32_t f = row_factor<E4M3, HALF>(scale[r], over, second);
+    const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) widen4<E4M3, HALF>(in[q], f, o[2 * q], o[2 * q + 1]);
+    if (!HALF && E4M3 && second != 0x3f803f80u) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) o[q] = mul_bf2(o[q], second);
+    }
+    if (r < z0 || r >= z1 || (drop_nan && scale[r] == q8::kNaN)) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) o[q] = 0;
+    }
+    uint8_t* row = tile + (c >> 2) * kAtomBytes + r * 128;
+    const int ch = 2 * (c & 3), sw = r & 7;
+    // (threads of the second atom write their halves the other way round: 128 bytes of the two atoms lie in the same banks)
+    const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
+    const bool turn = c >= 4;
+    *reinterpret_cast<uint4*>(row + (((ch + turn) ^ sw) << 4)) = turn ? b : a;
+    *reinterpret_cast<uint4*>(row + (((ch + !turn) ^ sw) << 4)) = turn ? a : b;
+  }
+}
+
 // CAP: a softcap; BIAS: slopes, or tree distances that the window reaches.  Variants of
 // their own, and rolled loops wherever a warp does not wait for them: a loop over the tiles that is
 // larger than the instruction cache (some 32 KB) runs at half the speed.
 // PRE: of a call with shared prefixes: a part may be a prefix's, and rows are left as they are.
-template <int D, bool F16, bool CAP, bool BIAS, bool PRE>
-__global__ void __launch_bounds__(kTcThreads, 1)
+// Q8: over an 8-bit cache: warps 12-15 convert tiles (see convert_tile).  K becomes bf16 values (F16: fp16 values
+// over a power of two of the tile's), V fp16 values over a power of two that grows with the unit's scales; P
+// is fp16 with six more bits of range below, and the accumulators take up the powers of two.
+template <int D, bool F16, bool CAP, bool BIAS, bool PRE, bool Q8>
+__global__ void __launch_bounds__(Q8 ? kTcThreads + kConvertThreads : kTcThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const PagedAttnParams p, const int nb) {
   using Lay = TcLayout<D>;
   constexpr int A = Lay::A;
   constexpr uint32_t kTmemCols = 512, kOCol = 256;
+  constexpr int kThreads = Q8 ? kTcThreads + kConvertThreads : kTcThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -161,6 +312,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_bad_pages[kBadRing];  // bit g: keys 8 g .. 8 g + 7 have no page
   __shared__ volatile int s_abort;
+  // (8-bit cache) raw tiles have landed; scales; the powers of two that a tile's K and V are held over; a
+  // converter's wait ran out
+  __shared__ __align__(8) uint64_t bar_k_raw[Q8 ? kKStages : 1], bar_v_raw[Q8 ? kVStages : 1];
+  __shared__ __align__(16) uint8_t s_kscale[Q8 ? kKStages : 1][kTcKeys], s_vscale[Q8 ? kVStages : 1][kTcKeys];
+  __shared__ volatile int s_kexp[kBadRing], s_vexp[kBadRing];
+  __shared__ volatile uint32_t s_vnan[Q8 ? kBadRing : 1][4];  // keys whose V row is no number, where s_vexp says so
+  __shared__ volatile int s_late_step[2];
   __shared__ PartRing s_ring;
   __shared__ Cursor<kTcKeys> s_cur;
   __shared__ int s_late;  // the first sequence that a softmax warp gave up in
@@ -171,11 +329,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     mbar_init(&bar_q_empty, 1);
     mbar_init(&bar_drain, 1);
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(&bar_k_full[i], 1);
+      mbar_init(&bar_k_full[i], Q8 ? 4 : 1);
       mbar_init(&bar_k_empty[i], 1);
+      if (Q8) mbar_init(&bar_k_raw[Q8 ? i : 0], 1 + 32);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(&bar_v_full[i], 1);
+      mbar_init(&bar_v_full[i], Q8 ? 4 : 1);
+      if (Q8) mbar_init(&bar_v_raw[Q8 ? i : 0], 1 + 32);
       mbar_init(&bar_v_empty[i], 1);
       mbar_init(&bar_v_zero[i], 1);
     }
@@ -188,32 +348,101 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     mbar_fence_init();
     s_abort = 0;
     s_late = INT_MAX;
-    s_ring.init(11);  // K, V, products, eight softmax warps
+    s_late_step[0] = s_late_step[1] = 0;
+    s_ring.init(Q8 ? 15 : 11);  // K, V, products, eight softmax warps (, four that convert)
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
   if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
-  prefetch_lengths<kTcThreads>(p);
+  prefetch_lengths<kThreads>(p);
   pdl_wait();
   tc_fence_before();
-  find_share<kTcKeys, kTcThreads>(p, s_cur);
+  find_share<kTcKeys, kThreads>(p, s_cur);
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   uint32_t n = 0;  // parts so far
   bool ok = true;
+  // (8-bit cache) the launch's 128 registers a thread are shared out: 184 to a softmax thread, 72 to the others
+  if (Q8 && warp >= 12) {
+    // ------------------------------------------- raw tiles to 16-bit operands
+    set_registers<false, 72, Q8>();
+    const int ctid = tid - kTcThreads;
+    // The warps go step by step (a part, a K tile, a V tile), with a barrier in each.  A warp that gives up still joins
+    // the others there, and all see it behind: its mark has the step's parity, as a warp may already be in the next.
+    uint32_t it = 0, step = 0;  // tiles, steps so far
+    auto joined = [&](bool good) {
+      if (!good) s_late_step[step & 1] = 1;
+      named_sync(2, kConvertThreads);
+      return !s_late_step[step++ & 1];
+    };
+    for (; ok; ++n) {
+      ok = __all_sync(0xffffffffu, s_ring.ready(n, p.wait_limit));
+      int lo = 0, hi = 0, begin = 0, end = 0;
+      bool over = true;
+      if (ok) {
+        const Part& w = s_ring.at(n);
+        over = w.b < 0;
+        lo = w.lo;
+        hi = w.hi;
+        begin = w.begin;
+        end = w.end;
+      }
+      ok = joined(ok);
+      if (!ok || over) break;
+      int vexp = -1;
+      for (int t = end - 1; ok && t >= begin; --t, ++it) {
+        const int z0 = max(0, lo - t * kTcKeys), z1 = min(kTcKeys, hi - t * kTcKeys);
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+          const uint32_t stages = side ? kVStages : kKStages, st = it % stages;
+          uint64_t* raw = side ? &bar_v_raw[Q8 ? st : 0] : &bar_k_raw[Q8 ? st : 0];
+          const bool landed = warp_wait(raw, (it / stages) & 1, p.wait_limit);
+          uint8_t* tile = (side ? sV : sK) + st * Lay::kTile;
+          const uint8_t* scale = side ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0];
+          uint4 x[D / 16];
+          load_raw<D>(tile, ctid, x);
+          const int top = scale_top(scale, z0, z1);
+          int over_exp = top;
+          if (side) {
+            if (top > vexp + 1 || vexp < 0) vexp = top;
+            over_exp = vexp;
+          }
+          ok = joined(landed);  // (every code is in registers before its place is written)
+          if (!ok) break;
+          if (warp == 12) {
+            const bool nan = side && note_nan_rows(scale, z0, z1, s_vnan[Q8 ? it % kBadRing : 0]);
+            if (lane == 0) (side ? s_vexp : s_kexp)[it % kBadRing] = nan ? over_exp | kHasNaN : over_exp;
+          }
+          if (side || F16)
+            p.e4m3 ? convert_tile<D, true, true>(tile, scale, ctid, x, over_exp, side ? z0 : 0, side ? z1 : kTcKeys, side)
+                   : convert_tile<D, false, true>(tile, scale, ctid, x, over_exp, side ? z0 : 0, side ? z1 : kTcKeys, side);
+          else
+            p.e4m3 ? convert_tile<D, true, false>(tile, scale, ctid, x, 0, 0, kTcKeys, false)
+                   : convert_tile<D, false, false>(tile, scale, ctid, x, 0, 0, kTcKeys, false);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(side ? &bar_v_full[st] : &bar_k_full[st]);
+        }
+      }
+      if (lane == 0) s_ring.done(n);
+    }
+  } else if (warp >= 8) {
+  set_registers<false, 72, Q8>();
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------------- K, V producers
     const bool isV = warp == 10;
     const CUtensorMap* map = isV ? &tmV : &tmK;
     uint8_t* ring = isV ? sV : sK;
-    uint64_t* full = isV ? bar_v_full : bar_k_full;
+    uint64_t* full = Q8 ? (isV ? bar_v_raw : bar_k_raw) : isV ? bar_v_full : bar_k_full;
     uint64_t* empty = isV ? bar_v_empty : bar_k_empty;
     const uint32_t stages = isV ? kVStages : kKStages;
     PageFeed<kTcKeys> feed;
     const int rows_page = min(1 << p.page_shift, kTcKeys), npg = kTcKeys / rows_page;
-    const int pg = lane % npg, atom = lane / npg, row0 = pg * rows_page;
-    const bool issues = atom < A;
+    // (8-bit cache: lane l < 16 has the keys 8 l .. 8 l + 7, their scales and, if they are its first, their page's box)
+    const int pg = Q8 ? (lane & 15) * 8 / rows_page : lane % npg, atom = lane / npg;
+    const int row0 = Q8 ? (lane & 15) * 8 : pg * rows_page;
+    const bool issues = Q8 ? lane < 16 && (lane * 8) % rows_page == 0 : atom < A;
     uint32_t it = 0;
     // Rows of V before lo and from hi on may hold anything (NaN times a probability of 0 is
     // NaN): cleared in the tiles that have them (a unit's first and last at most), once the
@@ -243,7 +472,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (!ok) break;
       const Part w = s_ring.at(n);
       if (w.b < 0) break;
-      if (isV && w.begin == w.end) clear_rows();
+      if (!Q8 && isV && w.begin == w.end) clear_rows();
       feed.start(p, w);
       for (int t = w.end - 1; t >= w.begin; --t, ++it) {
         const uint32_t st = it % stages;
@@ -254,13 +483,22 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (!ok) break;
         if (lane == 0) {
           if (!isV) s_bad_pages[it % kBadRing] = bad8;
-          mbar_expect_tx(&full[st], Lay::kTile);
+          mbar_expect_tx(&full[st], Q8 ? Lay::kTile / 2 : Lay::kTile);
         }
         __syncwarp();
-        if (issues)
+        if (Q8) {
+          const int row = key & ((1 << p.page_shift) - 1);
+          if (issues)
+            tma_load_rows(ring + st * Lay::kTile + Lay::kTile / 2 + row0 * D, map, &full[st], 0, row, w.kvh, page, p.row_dim,
+                          p.head_dim);
+          if (lane < 16)
+            load_scales(p, (isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0]) + row0, isV ? p.v_scale : p.k_scale, page,
+                        w.kvh, row);
+          cp_arrive(&full[st]);
+        } else if (issues)
           tma_load_rows(ring + st * Lay::kTile + atom * kAtomBytes + row0 * 128, map, &full[st],
                         atom * 64, key & ((1 << p.page_shift) - 1), w.kvh, page, p.row_dim, p.head_dim);
-        if (isV) {
+        if (!Q8 && isV) {
           clear_rows();
           if (!ok) {
             ++it;  // (this tile's copy is on its way)
@@ -273,7 +511,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       }
       if (lane == 0) s_ring.done(n);
     }
-    if (isV && ok) clear_rows();
+    if (!Q8 && isV && ok) clear_rows();
+    if (Q8) asm volatile("cp.async.wait_all;" ::: "memory");
     // no copy may be in flight when the CTA leaves
     for (uint32_t i = it > stages ? it - stages : 0; i < it; ++i)
       mbar_wait(&full[i % stages], (i / stages) & 1);
@@ -346,7 +585,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     // path of both row blocks (with the whole warp waiting and voting, a barrier that
     // had completed already cost some 150 cycles).
     if (elect_one()) {
-      constexpr uint32_t idS = idesc(F16, kTcKeys, 0), idO = idesc(F16, D, 1);
+      constexpr uint32_t idS = idesc(F16, kTcKeys, 0), idO = idesc(F16 || Q8, D, 1);
       const uint64_t dQ = sw128_desc(smem_u32(sQ), 16, 1024);
       const uint64_t dK = sw128_desc(smem_u32(sK), 16, 1024);
       const uint64_t dV = sw128_desc(smem_u32(sV), kAtomBytes, 1024);
@@ -394,7 +633,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           const int j0 = (w.end - 1 - t) * kTcKeys;
           const bool more = t + 1 < T;
           ok = wait_within(&bar_v_full[vst], vph, p.wait_limit);
-          if (w.lo > j0 || w.hi < j0 + kTcKeys) {  // the V producer clears rows of this tile
+          if (!Q8 && (w.lo > j0 || w.hi < j0 + kTcKeys)) {  // the V producer clears rows of this tile
             ok = ok && wait_within(&bar_v_zero[vst], (zph >> vst) & 1, p.wait_limit);
             zph ^= 1u << vst;
           }
@@ -431,8 +670,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (!mbar_wait(&bar_drain, 0)) s_abort = 1;
     }
     ok = __all_sync(0xffffffffu, ok);
+  }
   } else {
     // -------------------------------------------------------------- softmax
+    set_registers<true, 184, Q8>();
     const int rb = warp >> 2, row = tid & (kRB - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128 * rb, tO = tmem + kOCol + 128 * rb;
@@ -491,9 +732,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const float slope = (BIAS && p.slopes) ? __ldg(p.slopes + w.kvh * p.G + h_in) * kLog2e : 0.0f;
       // what turns a score into the log2 domain; capped scores are there already, and with
       // slopes it comes with the bias
-      const float in_scale = CAP ? 1.0f : p.scale_log2;
-      const float scale = (BIAS && p.slopes) ? 1.0f : in_scale;
+      const float in_scale0 = CAP ? 1.0f : p.scale_log2;
       float m_run = -INFINITY, l_run = 0.0f;
+      int vexp = -1;  // (8-bit cache) O is held over 2^(vexp - 127)
+      bool vnan = false;  // (8-bit cache) it sees a V row that is no number
       for (int t = 0; t < T; ++t, ++kt, ++sc) {
         const int j0 = j_last - t * kTcKeys;
         uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
@@ -517,6 +759,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           continue;
         }
         const uint32_t bad = s_bad_pages[kt % kBadRing];
+        // (8-bit cache, fp16) what the tile's K is held over
+        const float kf = Q8 && F16 ? __int_as_float(max(s_kexp[kt % kBadRing], 1) << 23) : 1.0f;
+        const float in_scale = CAP ? 1.0f : in_scale0 * kf, scale = (BIAS && p.slopes) ? 1.0f : in_scale;
         tc_fence_after();
         uint32_t sr[4][32];
 #pragma unroll
@@ -541,6 +786,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
               for (int b = 0; b < 4; ++b) {
                 s[b] = make_float2(__uint_as_float(sr[c][e + 2 * b]), __uint_as_float(sr[c][e + 2 * b + 1]));
+                if (Q8 && F16) s[b] = fmul2(s[b], make_float2(kf, kf));
                 w[b] = fmul2(s[b], s[b]);
               }
 #pragma unroll
@@ -571,14 +817,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float y = __uint_as_float(x[e]);
+                const float y = __uint_as_float(x[e]) * kf;
                 if (j0 + c + e >= w.lo && j0 + c + e < hi) top = fmaxf(top, y * y);
               }
             }
             far = __any_sync(0xffffffffu, top > p.cap_top && is_row);
           }
           if (far) {
-            const float in = 2.0f * kLog2e * p.cap_in;
+            const float in = 2.0f * kLog2e * p.cap_in * kf;
 #pragma unroll 1
             for (int c = 0; c < 128; c += 8) {
               uint32_t x[8];
@@ -631,7 +877,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         __syncwarp();
         // Probabilities of 32 keys against the maximum m: their sums into ps, packed pairs to pw.
         float2 ps[4] = {};
-        const float2 sc2 = make_float2(scale, scale);
+        float2 sc2 = make_float2(scale, scale);
         auto probs = [&](int c, float m, uint32_t (&pw)[16]) {
           const float2 nm2 = make_float2(-m, -m);
 #pragma unroll
@@ -640,7 +886,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
                                                __uint_as_float(sr[c][2 * e + 1])), sc2, nm2);
             const float2 x = make_float2(ex2(y.x), ex2(y.y));
             ps[e & 3] = fadd2(ps[e & 3], x);
-            pw[e] = pack2<F16>(x.x, x.y);
+            pw[e] = pack2<F16 || Q8>(x.x, x.y);
           }
         };
         float mx[4];
@@ -653,8 +899,33 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           mx[c] = fmaxf(mx[c], __uint_as_float(sr[c][31]));
         }
         const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+        const float tmag = fabsf(tmax);
+        if ((Q8 || PRE) && !CAP && __any_sync(0xffffffffu, tmag > 0x1p22f && tmag < INFINITY)) {
+          // Scores so large that a rounding of the maximum is a power of two or more: the products are rounded
+          // like it, ahead of the difference (fused, the largest could end far above 0).
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sr[c][e] = __float_as_uint(__uint_as_float(sr[c][e]) * scale);
+          sc2 = make_float2(1.0f, 1.0f);
+        }
         const bool moves = m_run == -INFINITY || tmax > m_run + kRescaleLog2;
-        if (__any_sync(0xffffffffu, moves)) {
+        bool vmoves = false;
+        float vcorr = 1.0f;
+        if (Q8) {  // (V's scales are known; it has landed long before, as a rule)
+          ok = warp_wait(&bar_v_full[kt % kVStages], (kt / kVStages) & 1, p.wait_limit);
+          if (!ok) break;
+          int v = s_vexp[kt % kBadRing];
+          if (v & kHasNaN) {
+            v &= ~kHasNaN;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) vnan |= (vis[c] & s_vnan[Q8 ? kt % kBadRing : 0][c]) != 0;
+          }
+          vmoves = vexp >= 0 && v != vexp;
+          if (vmoves) vcorr = v - vexp > 126 ? 0.0f : __int_as_float((127 + vexp - v) << 23);
+          vexp = v;
+        }
+        if (__any_sync(0xffffffffu, moves) || vmoves) {
           const float m_new = moves ? tmax : m_run;
           const float corr = moves && m_run != -INFINITY ? ex2(m_run - m_new) : 1.0f;
           m_run = m_new;
@@ -667,12 +938,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               tmem_ld8(tO + lane_base + c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * (Q8 ? corr * vcorr : corr));
               tmem_st8(tO + lane_base + c, o);
             }
           }
         }
-        const float mm = m_run == -INFINITY ? 0.0f : m_run;  // nothing seen yet: 2^-inf = 0
+        // (nothing seen yet: 2^-inf = 0; an fp16 P reaches up to 2^14 and six bits further down)
+        const float mm = (m_run == -INFINITY ? 0.0f : m_run) - (Q8 ? kTcPBias : 0.0f);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           // (rounded to the cache's type, the product's operand: half a step, 2^-8 or 2^-11 of a
@@ -704,6 +976,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const bool mine = tl < nb && tile_tok < w.ntok;
       const size_t oidx = (size_t)(w.s.t0 + w.first + tile_tok) * p.Hq + w.kvh * p.G + h_in;
       const int crow = rb * kRB + row;
+      // (8-bit cache) O's own power of two; the sums are held over the maximum less the bias
+      const float vf = Q8 ? __int_as_float(vnan ? 0x7fffffff : max(vexp, 1) << 23) : 1.0f;
+      if (Q8) m_run -= kTcPBias;
       const bool leaves = w.slot >= 0 && (p.merge || w.parts == 0);  // rows for another to join
       float4* part = reinterpret_cast<float4*>(p.part) + crow;       // [slot][D / 4][256]
       if (leaves) {
@@ -717,8 +992,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               part[((size_t)w.slot * (D / 4) + 8 * c + q) * 256] =
-                  make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
-                              __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+                  Q8 ? make_float4(__uint_as_float(o[4 * q]) * vf, __uint_as_float(o[4 * q + 1]) * vf,
+                                   __uint_as_float(o[4 * q + 2]) * vf, __uint_as_float(o[4 * q + 3]) * vf)
+                     : make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                   __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
           __syncwarp();
         }
         if (!p.merge) left = w.slot;
@@ -746,6 +1023,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           tmem_ld32(tO + lane_base + 64 * c, o[0]);
           tmem_ld32(tO + lane_base + 64 * c + 32, o[1]);
           tmem_wait_ld();
+          if (Q8 && mine) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = __float_as_uint(__uint_as_float(o[e >> 5][e & 31]) * vf);
+          }
           if (more && mine) {
 #pragma unroll
             for (int e = 0; e < 64; ++e)
@@ -758,7 +1039,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               for (int q = 0; q < 16; ++q)
                 v[q] = __ldcg(&part[((size_t)(w.slot + k) * (D / 4) + 16 * c + q) * 256]);
               const float f = m == -INFINITY ? 0.0f : ex2(m - m_all);
-              if (f == 0.0f) continue;  // (a part whose keys are all hidden: select, do not multiply)
+              if (f == 0.0f && (!Q8 || m == -INFINITY)) continue;  // (a part whose keys are all hidden: select, do not multiply)
 #pragma unroll
               for (int q = 0; q < 16; ++q) {
                 uint32_t* x = &o[q >> 3][4 * (q & 7)];
@@ -804,31 +1085,31 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   if (warp == 0) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool F16, bool CAP, bool BIAS, bool PRE>
+template <int D, bool F16, bool CAP, bool BIAS, bool PRE, bool Q8>
 cudaError_t launch(const PagedPlan& pl, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                    const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream) {
-  if (!set_dyn_smem(paged_tc_kernel<D, F16, CAP, BIAS, PRE>, TcLayout<D>::kDyn)) return cudaErrorUnknown;
-  return launch_pdl(paged_tc_kernel<D, F16, CAP, BIAS, PRE>, dim3(pl.ctas), dim3(kTcThreads),
+  if (!set_dyn_smem(paged_tc_kernel<D, F16, CAP, BIAS, PRE, Q8>, TcLayout<D>::kDyn)) return cudaErrorUnknown;
+  return launch_pdl(paged_tc_kernel<D, F16, CAP, BIAS, PRE, Q8>, dim3(pl.ctas), dim3(Q8 ? kTcThreads + kConvertThreads : kTcThreads),
                     (size_t)TcLayout<D>::kDyn, stream, tmQ, tmK, tmV, p, pl.nb);
 }
-template <int D, bool F16, bool PRE>
+template <int D, bool F16, bool PRE, bool Q8>
 cudaError_t launch_kind(const PagedPlan& pl, bool bias, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                         const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream) {
   if (p.softcap_log2 > 0.0f)
-    return bias ? launch<D, F16, true, true, PRE>(pl, tmQ, tmK, tmV, p, stream)
-                : launch<D, F16, true, false, PRE>(pl, tmQ, tmK, tmV, p, stream);
-  return bias ? launch<D, F16, false, true, PRE>(pl, tmQ, tmK, tmV, p, stream)
-              : launch<D, F16, false, false, PRE>(pl, tmQ, tmK, tmV, p, stream);
+    return bias ? launch<D, F16, true, true, PRE, Q8>(pl, tmQ, tmK, tmV, p, stream)
+                : launch<D, F16, true, false, PRE, Q8>(pl, tmQ, tmK, tmV, p, stream);
+  return bias ? launch<D, F16, false, true, PRE, Q8>(pl, tmQ, tmK, tmV, p, stream)
+              : launch<D, F16, false, false, PRE, Q8>(pl, tmQ, tmK, tmV, p, stream);
 }
-template <bool PRE>
+template <bool PRE, bool Q8>
 cudaError_t launch_any(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
                        const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
                        cudaStream_t stream) {
   if (D == 128)
-    return f16 ? launch_kind<128, true, PRE>(pl, bias, tmQ, tmK, tmV, p, stream)
-               : launch_kind<128, false, PRE>(pl, bias, tmQ, tmK, tmV, p, stream);
-  return f16 ? launch_kind<64, true, PRE>(pl, bias, tmQ, tmK, tmV, p, stream)
-             : launch_kind<64, false, PRE>(pl, bias, tmQ, tmK, tmV, p, stream);
+    return f16 ? launch_kind<128, true, PRE, Q8>(pl, bias, tmQ, tmK, tmV, p, stream)
+               : launch_kind<128, false, PRE, Q8>(pl, bias, tmQ, tmK, tmV, p, stream);
+  return f16 ? launch_kind<64, true, PRE, Q8>(pl, bias, tmQ, tmK, tmV, p, stream)
+             : launch_kind<64, false, PRE, Q8>(pl, bias, tmQ, tmK, tmV, p, stream);
 }
 
 }  // namespace

@@ -165,7 +165,7 @@ cudaError_t launch_size(const PagedPlan& pl, const PagedAttnParams& p, cudaStrea
 cudaError_t launch_prefix(const PagedPlan& pl, int D, bool f16, bool bias, const CUtensorMap& tmQ,
                           const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedAttnParams& p,
                           cudaStream_t stream) {
-  const cudaError_t e = launch_any<true>(pl, D, f16, bias, tmQ, tmK, tmV, p, stream);
+  const cudaError_t e = launch_any<true, false>(pl, D, f16, bias, tmQ, tmK, tmV, p, stream);
   if (e != cudaSuccess) return e;
   if (D == 128) return f16 ? launch_size<128, true>(pl, p, stream) : launch_size<128, false>(pl, p, stream);
   return f16 ? launch_size<64, true>(pl, p, stream) : launch_size<64, false>(pl, p, stream);

@@ -49,7 +49,8 @@ def agree(tv, c, Hq, Hkv, D, dtype, **kw):
 
 SHAPES = [(8, 2, 128, 16, "e4m3", "bf16", "heads"), (4, 4, 64, 8, "int8", "fp16", "rows"),
           (7, 1, 128, 256, "int8", "bf16", "both"), (10, 2, 64, 64, "e4m3", "bf16", "rows"),
-          (16, 1, 128, 32, "e4m3", "fp16", "heads"), (3, 3, 64, 128, "e4m3", "bf16", "both")]
+          (16, 1, 128, 32, "e4m3", "fp16", "heads"), (3, 3, 64, 128, "e4m3", "bf16", "both"),
+          (64, 1, 128, 32, "int8", "bf16", "rows"), (8, 2, 64, 16, "e4m3", "fp16", "rows")]
 DECODE = [[(0, 1)], [(1, 1)], [(63, 1), (64, 1), (127, 1), (0, 1), (128, 1)], [(1500, 1), (3, 1), (0, 1), (700, 1)]]
 CHUNKS = [[(0, 2)], [(0, 129)], [(200, 33), (0, 0), (5, 64), (130, 1)], [(64, 200), (700, 3)],
           [(1000, 5), (1, 4), (33, 8)]]
@@ -172,6 +173,11 @@ def test_many_short_sequences(tv, B, new):
 def test_long_contexts(tv, lens):
     c = make_q8(2, lens, 4, 1, 64, 64, "int8")
     agree(tv, c, 4, 1, 64, "bf16")
+
+
+def test_the_widest_group(tv):
+    c = make_q8(3, [(150, 5), (0, 2), (300, 1)], 128, 1, 64, 32, "e4m3")
+    agree(tv, c, 128, 1, 64, "bf16")
 
 
 def test_offsets_past_32_bits(tv):
