@@ -31,11 +31,12 @@ namespace tv {
 namespace paged {
 namespace {
 
-constexpr int kTcThreads = 384, kConvertThreads = 128;  // (those: over an 8-bit cache)
+constexpr int kTcThreads = 384, kConvertThreads = 256;  // (those: over an 8-bit cache)
 constexpr int kRB = 128;           // rows of a row block
 constexpr int kAtomBytes = 16384;  // 128 rows x 128 bytes
 constexpr int kKStages = 2, kVStages = 3;
 constexpr int kBadRing = 8;        // page flags outlive their K stage by two tiles at most
+constexpr int kExpRing = 4;        // and what an 8-bit tile's K and V are held over, V's stage by none
 
 template <int D>
 struct TcLayout {
@@ -136,9 +137,13 @@ __device__ __forceinline__ void note_unit(const PagedAttnParams& p, const Part& 
 }
 
 // ------------------------------------------------------------- 8-bit tiles
-// A raw tile of 128 rows of D codes lands in the second half of its stage; 128 threads take it into registers,
+// A raw tile of 128 rows of D codes lands in the second half of its stage; 256 threads take it into registers,
 // and then write the 16-bit tile over the whole stage, in the layout that TMA gives a 16-bit cache's.  A thread
-// has 16 codes of D / 16 rows: chunk ctid % (D / 16), rows ctid / (D / 16) + i 2048 / D.
+// has the 16 codes of chunk ctid % (D / 16) of rows ctid / (D / 16) + i 4096 / D, whose places
+// differ by a multiple of the swizzle's period.  (With four warps in place of eight, and factors and places found anew
+// for each 16 codes: 16 trees of 64 174 us, a chunk of 2,048 behind 6,100 458 us.)
+template <int D>
+constexpr int kUnits = 128 * (D / 16) / kConvertThreads;
 constexpr float kTcPBias = 6.0f;
 
 // Registers of the threads of a warpgroup (Q8 kernels alone).
@@ -148,10 +153,10 @@ __device__ __forceinline__ void set_registers() {
   if (Q8 && !MORE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 template <int D>
-__device__ __forceinline__ void load_raw(const uint8_t* tile, int ctid, uint4 (&x)[D / 16]) {
+__device__ __forceinline__ void load_raw(const uint8_t* tile, int ctid, uint4 (&x)[kUnits<D>]) {
   const uint4* raw = reinterpret_cast<const uint4*>(tile + TcLayout<D>::kTile / 2) + ctid;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) x[i] = raw[i * 128];
+  for (int i = 0; i < kUnits<D>; ++i) x[i] = raw[i * kConvertThreads];
 }
 // The largest scale byte of rows z0 .. z1 - 1 that are numbers, at least 1 (by a whole warp).
 __device__ __forceinline__ int scale_top(const uint8_t* scale, int z0, int z1) {
@@ -195,26 +200,24 @@ __device__ __forceinline__ uint32_t sub_bf2(uint32_t a, uint32_t b) {
   asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// The factor of a row with scale byte s, as a pair.  HALF: fp16 2^(s - over), over >= s - 1.  Else bf16, for
+// The factor of a row with scale byte s.  half: fp16 2^(s - over), over >= s - 1.  Else bf16, for
 // int8 2^(s - 127); for e4m3, whose bits are placed as a bf16's with an exponent too small by 120,
-// 2^(s - 7), in two steps where that is past the type.
-template <bool E4M3, bool HALF>
-__device__ __forceinline__ uint32_t row_factor(int s, int over, uint32_t& second) {
+// 2^(s - 7), the rest of it behind (far_rows) where that is past the type.  V's rows that are no numbers become
+// zeros: a probability of 0 would meet them in the product (the softmax threads that see one know of it).
+constexpr int kFarScale = 254 - 120;
+__device__ __forceinline__ uint32_t row_factor(bool e4m3, bool half, bool is_v, int s, int over) {
   uint32_t f;
-  second = 0x3f803f80u;
   if (s == q8::kNaN) {
-    f = 0x7fffu;
-  } else if (HALF) {
+    f = is_v ? 0u : 0x7fffu;
+  } else if (half) {
     const int e = s - over + 15;
-    f = e > 0 ? (uint32_t)e << 10 : e > -10 ? 512u >> -e : 0u;
-  } else if (E4M3) {
-    const int e = s + 120;
-    f = (uint32_t)min(e, 254) << 7;
-    if (e > 254) second = (uint32_t)(e - 254 + 127) * 0x800080u;
+    f = e > 30 ? 0u : e > 0 ? (uint32_t)e << 10 : e > -10 ? 512u >> -e : 0u;  // (past 30: a row that nobody sees)
+  } else if (e4m3) {
+    f = (uint32_t)min(s + 120, 254) << 7;
   } else {
     f = s > 0 ? (uint32_t)s << 7 : 0x40u;
   }
-  return f * 0x10001u;
+  return f;
 }
 template <bool E4M3, bool HALF>
 __device__ __forceinline__ void widen4(uint32_t x, uint32_t f, uint32_t& lo, uint32_t& hi) {
@@ -247,37 +250,58 @@ __device__ __forceinline__ void widen4(uint32_t x, uint32_t f, uint32_t& lo, uin
     hi = mul_bf2(hi, f);
   }
 }
-// Rows outside of [z0, z1) become zeros (their codes and scales may be anything), and so do V's rows that are no
-// numbers: a probability of 0 would meet them in the product.  The softmax threads that see one know of it.
 template <int D, bool E4M3, bool HALF>
-__device__ __forceinline__ void convert_tile(uint8_t* tile, const uint8_t* scale, int ctid, const uint4 (&x)[D / 16],
-                                             int over, int z0, int z1, bool drop_nan) {
-  constexpr int kChunks = D / 16, kRowStep = 128 / kChunks;
+__device__ __forceinline__ void convert_tile(uint8_t* tile, const uint16_t* factor, int ctid,
+                                             const uint4 (&x)[kUnits<D>]) {
+  constexpr int kChunks = D / 16, kRowStep = kConvertThreads / kChunks;
   const int c = ctid % kChunks, r0 = ctid / kChunks;
+  // (threads of the second atom write their halves the other way round: 128 bytes of the two atoms lie in the same banks)
+  const int ch = 2 * (c & 3), sw = r0 & 7, turn = c >> 2;
+  uint8_t* row = tile + (c >> 2) * kAtomBytes + r0 * 128;
+  uint8_t *first = row + (((ch + turn) ^ sw) << 4), *second = row + (((ch + 1 - turn) ^ sw) << 4);
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    const int r = r0 + i * kRowStep;
-    uint32_t second;
-    const uint32_t f = row_factor<E4M3, HALF>(scale[r], over, second);
+  for (int i = 0; i < kUnits<D>; ++i) {
+    const uint32_t f = factor[r0 + i * kRowStep] * 0x10001u;
     const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     uint32_t o[8];
 #pragma unroll
     for (int q = 0; q < 4; ++q) widen4<E4M3, HALF>(in[q], f, o[2 * q], o[2 * q + 1]);
-    if (!HALF && E4M3 && second != 0x3f803f80u) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) o[q] = mul_bf2(o[q], second);
-    }
-    if (r < z0 || r >= z1 || (drop_nan && scale[r] == q8::kNaN)) {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) o[q] = 0;
-    }
-    uint8_t* row = tile + (c >> 2) * kAtomBytes + r * 128;
-    const int ch = 2 * (c & 3), sw = r & 7;
-    // (threads of the second atom write their halves the other way round: 128 bytes of the two atoms lie in the same banks)
     const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-    const bool turn = c >= 4;
-    *reinterpret_cast<uint4*>(row + (((ch + turn) ^ sw) << 4)) = turn ? b : a;
-    *reinterpret_cast<uint4*>(row + (((ch + !turn) ^ sw) << 4)) = turn ? a : b;
+    *reinterpret_cast<uint4*>(first + i * kRowStep * 128) = turn ? b : a;
+    *reinterpret_cast<uint4*>(second + i * kRowStep * 128) = turn ? a : b;
+  }
+}
+// The 32 bytes of a thread's unit i of a 16-bit tile: their place, for what follows the conversion (by the same thread).
+template <int D>
+__device__ __forceinline__ uint4* unit_at(uint8_t* tile, int ctid, int i, int half, int& r) {
+  constexpr int kChunks = D / 16;
+  const int c = ctid % kChunks;
+  r = ctid / kChunks + i * (kConvertThreads / kChunks);
+  return reinterpret_cast<uint4*>(tile + (c >> 2) * kAtomBytes + r * 128 + (((2 * (c & 3) + half) ^ (r & 7)) << 4));
+}
+// V rows outside of [z0, z1), whose codes and scales may be anything, become zeros.
+template <int D>
+__device__ __forceinline__ void clear_outside(uint8_t* tile, int ctid, int z0, int z1) {
+#pragma unroll 1
+  for (int i = 0; i < 2 * kUnits<D>; ++i) {
+    int r;
+    uint4* at = unit_at<D>(tile, ctid, i >> 1, i & 1, r);
+    if (r < z0 || r >= z1) *at = make_uint4(0, 0, 0, 0);
+  }
+}
+// The second step of e4m3 rows as bf16 whose factor is past the type.
+template <int D>
+__device__ __forceinline__ void far_rows(uint8_t* tile, const uint8_t* scale, int ctid) {
+#pragma unroll 1
+  for (int i = 0; i < 2 * kUnits<D>; ++i) {
+    int r;
+    uint4* at = unit_at<D>(tile, ctid, i >> 1, i & 1, r);
+    const int s = scale[r];
+    if (s <= kFarScale || s == q8::kNaN) continue;
+    const uint32_t f = (uint32_t)(s - kFarScale + 127) * 0x800080u;
+    uint4 v = *at;
+    v = make_uint4(mul_bf2(v.x, f), mul_bf2(v.y, f), mul_bf2(v.z, f), mul_bf2(v.w, f));
+    *at = v;
   }
 }
 
@@ -285,7 +309,7 @@ __device__ __forceinline__ void convert_tile(uint8_t* tile, const uint8_t* scale
 // their own, and rolled loops wherever a warp does not wait for them: a loop over the tiles that is
 // larger than the instruction cache (some 32 KB) runs at half the speed.
 // PRE: of a call with shared prefixes: a part may be a prefix's, and rows are left as they are.
-// Q8: over an 8-bit cache: warps 12-15 convert tiles (see convert_tile).  K becomes bf16 values (F16: fp16 values
+// Q8: over an 8-bit cache: warps 12-19 convert tiles (see convert_tile).  K becomes bf16 values (F16: fp16 values
 // over a power of two of the tile's), V fp16 values over a power of two that grows with the unit's scales; P
 // is fp16 with six more bits of range below, and the accumulators take up the powers of two.
 template <int D, bool F16, bool CAP, bool BIAS, bool PRE, bool Q8>
@@ -316,9 +340,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   // converter's wait ran out
   __shared__ __align__(8) uint64_t bar_k_raw[Q8 ? kKStages : 1], bar_v_raw[Q8 ? kVStages : 1];
   __shared__ __align__(16) uint8_t s_kscale[Q8 ? kKStages : 1][kTcKeys], s_vscale[Q8 ? kVStages : 1][kTcKeys];
-  __shared__ volatile int s_kexp[kBadRing], s_vexp[kBadRing];
-  __shared__ volatile uint32_t s_vnan[Q8 ? kBadRing : 1][4];  // keys whose V row is no number, where s_vexp says so
+  __shared__ volatile int s_kexp[Q8 ? kExpRing : 1], s_vexp[Q8 ? kExpRing : 1];
+  __shared__ volatile uint32_t s_vnan[Q8 ? kExpRing : 1][4];  // keys whose V row is no number, where s_vexp says so
   __shared__ volatile int s_late_step[2];
+  __shared__ uint16_t s_factor[2][Q8 ? kTcKeys : 1];  // of a tile's rows, by a step's parity
   __shared__ PartRing s_ring;
   __shared__ Cursor<kTcKeys> s_cur;
   __shared__ int s_late;  // the first sequence that a softmax warp gave up in
@@ -329,12 +354,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     mbar_init(&bar_q_empty, 1);
     mbar_init(&bar_drain, 1);
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(&bar_k_full[i], Q8 ? 4 : 1);
+      mbar_init(&bar_k_full[i], Q8 ? kConvertThreads / 32 : 1);
       mbar_init(&bar_k_empty[i], 1);
       if (Q8) mbar_init(&bar_k_raw[Q8 ? i : 0], 1 + 32);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(&bar_v_full[i], Q8 ? 4 : 1);
+      mbar_init(&bar_v_full[i], Q8 ? kConvertThreads / 32 : 1);
       if (Q8) mbar_init(&bar_v_raw[Q8 ? i : 0], 1 + 32);
       mbar_init(&bar_v_empty[i], 1);
       mbar_init(&bar_v_zero[i], 1);
@@ -349,7 +374,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     s_abort = 0;
     s_late = INT_MAX;
     s_late_step[0] = s_late_step[1] = 0;
-    s_ring.init(Q8 ? 15 : 11);  // K, V, products, eight softmax warps (, four that convert)
+    s_ring.init(Q8 ? 11 + kConvertThreads / 32 : 11);  // K, V, products, eight softmax warps (, those that convert)
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -363,10 +388,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   const uint32_t tmem = s_tmem;
   uint32_t n = 0;  // parts so far
   bool ok = true;
-  // (8-bit cache) the launch's 128 registers a thread are shared out: 184 to a softmax thread, 72 to the others
+  // (8-bit cache) the launch's 96 registers a thread are shared out: 168 to a softmax thread, 48 to the others
   if (Q8 && warp >= 12) {
     // ------------------------------------------- raw tiles to 16-bit operands
-    set_registers<false, 72, Q8>();
+    set_registers<false, 48, Q8>();
     const int ctid = tid - kTcThreads;
     // The warps go step by step (a part, a K tile, a V tile), with a barrier in each.  A warp that gives up still joins
     // the others there, and all see it behind: its mark has the step's parity, as a warp may already be in the next.
@@ -400,7 +425,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           const bool landed = warp_wait(raw, (it / stages) & 1, p.wait_limit);
           uint8_t* tile = (side ? sV : sK) + st * Lay::kTile;
           const uint8_t* scale = side ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0];
-          uint4 x[D / 16];
+          uint4 x[kUnits<D>];
           load_raw<D>(tile, ctid, x);
           const int top = scale_top(scale, z0, z1);
           int over_exp = top;
@@ -408,18 +433,21 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (top > vexp + 1 || vexp < 0) vexp = top;
             over_exp = vexp;
           }
+          const bool half = side || F16;
+          uint16_t* factor = s_factor[Q8 ? step & 1 : 0];
+          if (ctid < kTcKeys) factor[Q8 ? ctid : 0] = (uint16_t)row_factor(p.e4m3, half, side, scale[ctid], over_exp);
           ok = joined(landed);  // (every code is in registers before its place is written)
           if (!ok) break;
           if (warp == 12) {
-            const bool nan = side && note_nan_rows(scale, z0, z1, s_vnan[Q8 ? it % kBadRing : 0]);
-            if (lane == 0) (side ? s_vexp : s_kexp)[it % kBadRing] = nan ? over_exp | kHasNaN : over_exp;
+            const bool nan = side && note_nan_rows(scale, z0, z1, s_vnan[Q8 ? it % kExpRing : 0]);
+            if (lane == 0) (side ? s_vexp : s_kexp)[Q8 ? it % kExpRing : 0] = nan ? over_exp | kHasNaN : over_exp;
           }
-          if (side || F16)
-            p.e4m3 ? convert_tile<D, true, true>(tile, scale, ctid, x, over_exp, side ? z0 : 0, side ? z1 : kTcKeys, side)
-                   : convert_tile<D, false, true>(tile, scale, ctid, x, over_exp, side ? z0 : 0, side ? z1 : kTcKeys, side);
+          if (half)
+            p.e4m3 ? convert_tile<D, true, true>(tile, factor, ctid, x) : convert_tile<D, false, true>(tile, factor, ctid, x);
           else
-            p.e4m3 ? convert_tile<D, true, false>(tile, scale, ctid, x, 0, 0, kTcKeys, false)
-                   : convert_tile<D, false, false>(tile, scale, ctid, x, 0, 0, kTcKeys, false);
+            p.e4m3 ? convert_tile<D, true, false>(tile, factor, ctid, x) : convert_tile<D, false, false>(tile, factor, ctid, x);
+          if (!half && p.e4m3 && top > kFarScale) far_rows<D>(tile, scale, ctid);
+          if (side && (z0 > 0 || z1 < kTcKeys)) clear_outside<D>(tile, ctid, z0, z1);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(side ? &bar_v_full[st] : &bar_k_full[st]);
@@ -428,7 +456,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (lane == 0) s_ring.done(n);
     }
   } else if (warp >= 8) {
-  set_registers<false, 72, Q8>();
+  set_registers<false, 48, Q8>();
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------------- K, V producers
     const bool isV = warp == 10;
@@ -673,7 +701,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   }
   } else {
     // -------------------------------------------------------------- softmax
-    set_registers<true, 184, Q8>();
+    set_registers<true, 168, Q8>();
     const int rb = warp >> 2, row = tid & (kRB - 1);
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + 128 * rb, tO = tmem + kOCol + 128 * rb;
@@ -760,7 +788,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         }
         const uint32_t bad = s_bad_pages[kt % kBadRing];
         // (8-bit cache, fp16) what the tile's K is held over
-        const float kf = Q8 && F16 ? __int_as_float(max(s_kexp[kt % kBadRing], 1) << 23) : 1.0f;
+        const float kf = Q8 && F16 ? __int_as_float(max(s_kexp[Q8 ? kt % kExpRing : 0], 1) << 23) : 1.0f;
         const float in_scale = CAP ? 1.0f : in_scale0 * kf, scale = (BIAS && p.slopes) ? 1.0f : in_scale;
         tc_fence_after();
         uint32_t sr[4][32];
@@ -915,11 +943,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (Q8) {  // (V's scales are known; it has landed long before, as a rule)
           ok = warp_wait(&bar_v_full[kt % kVStages], (kt / kVStages) & 1, p.wait_limit);
           if (!ok) break;
-          int v = s_vexp[kt % kBadRing];
+          int v = s_vexp[Q8 ? kt % kExpRing : 0];
           if (v & kHasNaN) {
             v &= ~kHasNaN;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) vnan |= (vis[c] & s_vnan[Q8 ? kt % kBadRing : 0][c]) != 0;
+            for (int c = 0; c < 4; ++c) vnan |= (vis[c] & s_vnan[Q8 ? kt % kExpRing : 0][c]) != 0;
           }
           vmoves = vexp >= 0 && v != vexp;
           if (vmoves) vcorr = v - vexp > 126 ? 0.0f : __int_as_float((127 + vexp - v) << 23);
