@@ -139,7 +139,7 @@ __device__ __forceinline__ void note_unit(const PagedAttnParams& p, const Part& 
 // ------------------------------------------------------------- 8-bit tiles
 // A raw tile of 128 rows of D codes lands in the second half of its stage; 256 threads take it into registers,
 // and then write the 16-bit tile over the whole stage, in the layout that TMA gives a 16-bit cache's.  A thread
-// has the 16 codes of chunk ctid % (D / 16) of rows ctid / (D / 16) + i 4096 / D, whose places
+// has the 16 codes of chunk ctid % (D / 16) of rows unit_row + i 4096 / D, whose places
 // differ by a multiple of the swizzle's period.  (With four warps in place of eight, and factors and places found anew
 // for each 16 codes: 16 trees of 64 174 us, a chunk of 2,048 behind 6,100 458 us.)
 template <int D>
@@ -152,9 +152,17 @@ __device__ __forceinline__ void set_registers() {
   if (Q8 && MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
   if (Q8 && !MORE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+// A thread's row of a step of rows: the two 64-dim atoms of a row lie in the same banks, so of eight threads with
+// a row's chunks the four of the second atom take its neighbour.
+template <int D>
+__device__ __forceinline__ int unit_row(int ctid) {
+  const int c = ctid % (D / 16);
+  return (ctid / (D / 16)) ^ (c >> 2);
+}
 template <int D>
 __device__ __forceinline__ void load_raw(const uint8_t* tile, int ctid, uint4 (&x)[kUnits<D>]) {
-  const uint4* raw = reinterpret_cast<const uint4*>(tile + TcLayout<D>::kTile / 2) + ctid;
+  const uint4* raw = reinterpret_cast<const uint4*>(tile + TcLayout<D>::kTile / 2) + unit_row<D>(ctid) * (D / 16) +
+                     ctid % (D / 16);
 #pragma unroll
   for (int i = 0; i < kUnits<D>; ++i) x[i] = raw[i * kConvertThreads];
 }
@@ -185,90 +193,52 @@ __device__ __forceinline__ bool note_nan_rows(const uint8_t* scale, int z0, int 
   }
   return true;
 }
-// Pairs of 16-bit values of four codes, times a pair of equal factors (and `twice`, once more).
-__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t f) {
-  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&f));
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t mul_bf2(uint32_t a, uint32_t f) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(f));
-  return d;
-}
-__device__ __forceinline__ uint32_t sub_bf2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// The factor of a row with scale byte s.  half: fp16 2^(s - over), over >= s - 1.  Else bf16, for
-// int8 2^(s - 127); for e4m3, whose bits are placed as a bf16's with an exponent too small by 120,
-// 2^(s - 7), the rest of it behind (far_rows) where that is past the type.  V's rows that are no numbers become
+// The factor of a row with scale byte s, fp16 2^(s - over), over >= s - 1.  V's rows that are no numbers become
 // zeros: a probability of 0 would meet them in the product (the softmax threads that see one know of it).
-constexpr int kFarScale = 254 - 120;
-__device__ __forceinline__ uint32_t row_factor(bool e4m3, bool half, bool is_v, int s, int over) {
-  uint32_t f;
-  if (s == q8::kNaN) {
-    f = is_v ? 0u : 0x7fffu;
-  } else if (half) {
-    const int e = s - over + 15;
-    f = e > 30 ? 0u : e > 0 ? (uint32_t)e << 10 : e > -10 ? 512u >> -e : 0u;  // (past 30: a row that nobody sees)
-  } else if (e4m3) {
-    f = (uint32_t)min(s + 120, 254) << 7;
-  } else {
-    f = s > 0 ? (uint32_t)s << 7 : 0x40u;
-  }
-  return f;
+__device__ __forceinline__ uint32_t row_factor(bool is_v, int s, int over) {
+  if (s == q8::kNaN) return is_v ? 0u : 0x7fffu;
+  const int e = s - over + 15;
+  return e > 30 ? 0u : e > 0 ? (uint32_t)e << 10 : e > -10 ? 512u >> -e : 0u;  // (past 30: a row that nobody sees)
 }
-template <bool E4M3, bool HALF>
-__device__ __forceinline__ void widen4(uint32_t x, uint32_t f, uint32_t& lo, uint32_t& hi) {
-  if (HALF) {
-    if (E4M3) {
-      asm("{.reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-          : "=r"(lo), "=r"(hi)
-          : "r"(x));
-    } else {  // 1024 + (code + 128), less 1152
-      const uint32_t u = x ^ 0x80808080u, a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-      const __half2 off = __half2half2(__ushort_as_half(0x6480));
-      const __half2 v0 = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
-      const __half2 v1 = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
-      lo = *reinterpret_cast<const uint32_t*>(&v0);
-      hi = *reinterpret_cast<const uint32_t*>(&v1);
-    }
-    lo = mul_half2(lo, f);
-    hi = mul_half2(hi, f);
-  } else {
-    if (E4M3) {  // sign, and the other seven bits four places down
-      const uint32_t a = __byte_perm(x, 0, 0x1404), b = __byte_perm(x, 0, 0x3424);
-      lo = (a & 0x80008000u) | ((a >> 4) & 0x07f007f0u);
-      hi = (b & 0x80008000u) | ((b >> 4) & 0x07f007f0u);
-    } else {  // 128 + the last seven bits, less 128 or, of a negative code, 256
-      const uint32_t a = __byte_perm(x, 0x43434343u, 0x4140), b = __byte_perm(x, 0x43434343u, 0x4342);
-      lo = sub_bf2(a & 0xff7fff7fu, a & 0xff80ff80u);
-      hi = sub_bf2(b & 0xff7fff7fu, b & 0xff80ff80u);
-    }
-    lo = mul_bf2(lo, f);
-    hi = mul_bf2(hi, f);
+// Pairs of fp16 values of four codes, times a pair of equal factors f; g = -1152 f.
+template <bool E4M3>
+__device__ __forceinline__ void widen4(uint32_t x, __half2 f, __half2 g, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  __half2 v0, v1;
+  if (E4M3) {
+    asm("{.reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(a), "=r"(b)
+        : "r"(x));
+    v0 = __hmul2(*reinterpret_cast<const __half2*>(&a), f);
+    v1 = __hmul2(*reinterpret_cast<const __half2*>(&b), f);
+  } else {  // 1024 + (code + 128), less 1152 (exact ahead of the sum's one rounding)
+    const uint32_t u = x ^ 0x80808080u;
+    a = __byte_perm(u, 0x64646464u, 0x4140);
+    b = __byte_perm(u, 0x64646464u, 0x4342);
+    v0 = __hfma2(*reinterpret_cast<const __half2*>(&a), f, g);
+    v1 = __hfma2(*reinterpret_cast<const __half2*>(&b), f, g);
   }
+  lo = *reinterpret_cast<const uint32_t*>(&v0);
+  hi = *reinterpret_cast<const uint32_t*>(&v1);
 }
-template <int D, bool E4M3, bool HALF>
+template <int D, bool E4M3>
 __device__ __forceinline__ void convert_tile(uint8_t* tile, const uint16_t* factor, int ctid,
                                              const uint4 (&x)[kUnits<D>]) {
-  constexpr int kChunks = D / 16, kRowStep = kConvertThreads / kChunks;
-  const int c = ctid % kChunks, r0 = ctid / kChunks;
-  // (threads of the second atom write their halves the other way round: 128 bytes of the two atoms lie in the same banks)
-  const int ch = 2 * (c & 3), sw = r0 & 7, turn = c >> 2;
+  constexpr int kRowStep = kConvertThreads / (D / 16);
+  const int c = ctid % (D / 16), r0 = unit_row<D>(ctid), ch = 2 * (c & 3), sw = r0 & 7;
   uint8_t* row = tile + (c >> 2) * kAtomBytes + r0 * 128;
-  uint8_t *first = row + (((ch + turn) ^ sw) << 4), *second = row + (((ch + 1 - turn) ^ sw) << 4);
+  uint8_t *first = row + ((ch ^ sw) << 4), *second = row + (((ch + 1) ^ sw) << 4);
 #pragma unroll
   for (int i = 0; i < kUnits<D>; ++i) {
-    const uint32_t f = factor[r0 + i * kRowStep] * 0x10001u;
-    const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    const __half2 f = __half2half2(__ushort_as_half(factor[r0 + i * kRowStep]));
+    const __half2 g = E4M3 ? f : __hmul2(f, __half2half2(__ushort_as_half(0xe480)));  // (-1152)
     uint32_t o[8];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) widen4<E4M3, HALF>(in[q], f, o[2 * q], o[2 * q + 1]);
-    const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-    *reinterpret_cast<uint4*>(first + i * kRowStep * 128) = turn ? b : a;
-    *reinterpret_cast<uint4*>(second + i * kRowStep * 128) = turn ? a : b;
+    widen4<E4M3>(x[i].x, f, g, o[0], o[1]);
+    widen4<E4M3>(x[i].y, f, g, o[2], o[3]);
+    widen4<E4M3>(x[i].z, f, g, o[4], o[5]);
+    widen4<E4M3>(x[i].w, f, g, o[6], o[7]);
+    *reinterpret_cast<uint4*>(first + i * kRowStep * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(second + i * kRowStep * 128) = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 // The 32 bytes of a thread's unit i of a 16-bit tile: their place, for what follows the conversion (by the same thread).
@@ -276,7 +246,7 @@ template <int D>
 __device__ __forceinline__ uint4* unit_at(uint8_t* tile, int ctid, int i, int half, int& r) {
   constexpr int kChunks = D / 16;
   const int c = ctid % kChunks;
-  r = ctid / kChunks + i * (kConvertThreads / kChunks);
+  r = unit_row<D>(ctid) + i * (kConvertThreads / kChunks);
   return reinterpret_cast<uint4*>(tile + (c >> 2) * kAtomBytes + r * 128 + (((2 * (c & 3) + half) ^ (r & 7)) << 4));
 }
 // V rows outside of [z0, z1), whose codes and scales may be anything, become zeros.
@@ -289,29 +259,40 @@ __device__ __forceinline__ void clear_outside(uint8_t* tile, int ctid, int z0, i
     if (r < z0 || r >= z1) *at = make_uint4(0, 0, 0, 0);
   }
 }
-// The second step of e4m3 rows as bf16 whose factor is past the type.
+// A row of bf16 queries in shared memory becomes fp16, over the power of two of its largest; returns that.
+// Elements below 2^-14 of the largest lose bits (to 2^-25 of it), the others none.
 template <int D>
-__device__ __forceinline__ void far_rows(uint8_t* tile, const uint8_t* scale, int ctid) {
-#pragma unroll 1
-  for (int i = 0; i < 2 * kUnits<D>; ++i) {
-    int r;
-    uint4* at = unit_at<D>(tile, ctid, i >> 1, i & 1, r);
-    const int s = scale[r];
-    if (s <= kFarScale || s == q8::kNaN) continue;
-    const uint32_t f = (uint32_t)(s - kFarScale + 127) * 0x800080u;
-    uint4 v = *at;
-    v = make_uint4(mul_bf2(v.x, f), mul_bf2(v.y, f), mul_bf2(v.z, f), mul_bf2(v.w, f));
-    *at = v;
+__device__ __forceinline__ float as_halves(uint8_t* block, int row) {
+  uint8_t* at = block + row * 128;
+  const int sw = row & 7;
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at + (c >> 3) * kAtomBytes + (((c & 7) ^ sw) << 4));
+    const uint32_t m = 0x7fff7fffu;
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m)));
   }
+  const int e = min(max((int)(max(top & 0xffffu, top >> 16) >> 7), 1), 253);
+  const float f = __int_as_float((254 - e) << 23);
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    uint4* p = reinterpret_cast<uint4*>(at + (c >> 3) * kAtomBytes + (((c & 7) ^ sw) << 4));
+    const uint4 v = *p;
+    const float2 a = q8::unpack<false>(v.x), b = q8::unpack<false>(v.y), d = q8::unpack<false>(v.z), g = q8::unpack<false>(v.w);
+    *p = make_uint4(pack2<true>(a.x * f, a.y * f), pack2<true>(b.x * f, b.y * f), pack2<true>(d.x * f, d.y * f),
+                    pack2<true>(g.x * f, g.y * f));
+  }
+  return __int_as_float(e << 23);
 }
 
 // CAP: a softcap; BIAS: slopes, or tree distances that the window reaches.  Variants of
 // their own, and rolled loops wherever a warp does not wait for them: a loop over the tiles that is
 // larger than the instruction cache (some 32 KB) runs at half the speed.
 // PRE: of a call with shared prefixes: a part may be a prefix's, and rows are left as they are.
-// Q8: over an 8-bit cache: warps 12-19 convert tiles (see convert_tile).  K becomes bf16 values (F16: fp16 values
-// over a power of two of the tile's), V fp16 values over a power of two that grows with the unit's scales; P
-// is fp16 with six more bits of range below, and the accumulators take up the powers of two.
+// Q8: over an 8-bit cache: warps 12-19 convert tiles (convert_tile) to fp16: K's over a power of two of the tile's, V's
+// over one that grows with the unit's scales.  bf16 queries become fp16 over a power of two of their row
+// (as_halves).  Scores take the powers of two of q and K with their scale, O's is V's, and P is fp16 with six more bits
+// of range below.
 template <int D, bool F16, bool CAP, bool BIAS, bool PRE, bool Q8>
 __global__ void __launch_bounds__(Q8 ? kTcThreads + kConvertThreads : kTcThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -338,6 +319,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   __shared__ volatile int s_abort;
   // (8-bit cache) raw tiles have landed; scales; the powers of two that a tile's K and V are held over; a
   // converter's wait ran out
+  __shared__ __align__(8) uint64_t bar_q_raw;  // (bf16 queries, ahead of as_halves)
   __shared__ __align__(8) uint64_t bar_k_raw[Q8 ? kKStages : 1], bar_v_raw[Q8 ? kVStages : 1];
   __shared__ __align__(16) uint8_t s_kscale[Q8 ? kKStages : 1][kTcKeys], s_vscale[Q8 ? kVStages : 1][kTcKeys];
   __shared__ volatile int s_kexp[Q8 ? kExpRing : 1], s_vexp[Q8 ? kExpRing : 1];
@@ -350,7 +332,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
   if (tid == 0) {
-    mbar_init(&bar_q_full, 1);
+    mbar_init(&bar_q_full, Q8 && !F16 ? 8 : 1);
+    mbar_init(&bar_q_raw, 1);
     mbar_init(&bar_q_empty, 1);
     mbar_init(&bar_drain, 1);
     for (int i = 0; i < kKStages; ++i) {
@@ -433,20 +416,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             if (top > vexp + 1 || vexp < 0) vexp = top;
             over_exp = vexp;
           }
-          const bool half = side || F16;
           uint16_t* factor = s_factor[Q8 ? step & 1 : 0];
-          if (ctid < kTcKeys) factor[Q8 ? ctid : 0] = (uint16_t)row_factor(p.e4m3, half, side, scale[ctid], over_exp);
+          if (ctid < kTcKeys) factor[Q8 ? ctid : 0] = (uint16_t)row_factor(side, scale[ctid], over_exp);
           ok = joined(landed);  // (every code is in registers before its place is written)
           if (!ok) break;
           if (warp == 12) {
             const bool nan = side && note_nan_rows(scale, z0, z1, s_vnan[Q8 ? it % kExpRing : 0]);
             if (lane == 0) (side ? s_vexp : s_kexp)[Q8 ? it % kExpRing : 0] = nan ? over_exp | kHasNaN : over_exp;
           }
-          if (half)
-            p.e4m3 ? convert_tile<D, true, true>(tile, factor, ctid, x) : convert_tile<D, false, true>(tile, factor, ctid, x);
-          else
-            p.e4m3 ? convert_tile<D, true, false>(tile, factor, ctid, x) : convert_tile<D, false, false>(tile, factor, ctid, x);
-          if (!half && p.e4m3 && top > kFarScale) far_rows<D>(tile, scale, ctid);
+          if (p.e4m3) convert_tile<D, true>(tile, factor, ctid, x);
+          else convert_tile<D, false>(tile, factor, ctid, x);
           if (side && (z0 > 0 || z1 < kTcKeys)) clear_outside<D>(tile, ctid, z0, z1);
           fence_async_smem();
           __syncwarp();
@@ -550,15 +529,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     Part w;
     Cursor<kTcKeys> cur = s_cur;
     if (!PRE && p.merge && lane == 0) p.desc[share_index()] = make_int4(0, 0, 0, 0);
+    uint64_t& bar_q_land = Q8 && !F16 ? bar_q_raw : bar_q_full;
     // One thread: a part's Q rows, as boxes of nb tokens.
     auto load_q = [&](const Part& w) {
       if (lane == 0) {
         const int nrb = w.ntok > nb ? 2 : 1;
-        mbar_expect_tx(&bar_q_full, (uint32_t)(nrb * A * 64 * p.G * nb * 2));
+        mbar_expect_tx(&bar_q_land, (uint32_t)(nrb * A * 64 * p.G * nb * 2));
         for (int r = 0; r < nrb; ++r)
 #pragma unroll
           for (int a = 0; a < A; ++a)
-            tma_load_3d(sQ + (r * A + a) * kAtomBytes, &tmQ, &bar_q_full, a * 64, w.kvh * p.G,
+            tma_load_3d(sQ + (r * A + a) * kAtomBytes, &tmQ, &bar_q_land, a * 64, w.kvh * p.G,
                         w.s.t0 + w.first + r * nb);
       }
       __syncwarp();
@@ -606,14 +586,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       }
     }
     if (!p.merge) write_status(p);
-    if (parts > 0) mbar_wait(&bar_q_full, (parts - 1) & 1);
+    if (parts > 0) mbar_wait(&bar_q_land, (parts - 1) & 1);
   } else if (warp == 9) {
     // ------------------------------------------------------------- products
     // One thread waits and issues: what it does between two products is on the critical
     // path of both row blocks (with the whole warp waiting and voting, a barrier that
     // had completed already cost some 150 cycles).
     if (elect_one()) {
-      constexpr uint32_t idS = idesc(F16, kTcKeys, 0), idO = idesc(F16 || Q8, D, 1);
+      constexpr uint32_t idS = idesc(F16 || Q8, kTcKeys, 0), idO = idesc(F16 || Q8, D, 1);
       const uint64_t dQ = sw128_desc(smem_u32(sQ), 16, 1024);
       const uint64_t dK = sw128_desc(smem_u32(sK), 16, 1024);
       const uint64_t dV = sw128_desc(smem_u32(sV), kAtomBytes, 1024);
@@ -707,7 +687,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     const uint32_t tS = tmem + 128 * rb, tO = tmem + kOCol + 128 * rb;
     const int tl = row / p.G, h_in = row % p.G;
     const bool warp_in_block = (warp & 3) * 32 < nb * p.G;
-    uint32_t sc = 0, oc = 0, kt = 0;
+    uint32_t sc = 0, oc = 0, kt = 0, qn = 0;
     // Rows left for an earlier share are announced while the next part's first tile is under way:
     // the fence before the announcement waits for their stores, some 4,000 cycles right behind them.
     int left = -1;
@@ -741,6 +721,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         __syncwarp();
         if (lane == 0) s_ring.done(n);
         continue;
+      }
+      float qf = 1.0f;  // (8-bit cache, bf16) what the row of q is held over
+      if (Q8 && !F16) {
+        ok = warp_wait(&bar_q_raw, qn++ & 1, p.wait_limit);
+        if (!ok) break;
+        if (rb * nb < w.ntok) qf = as_halves<D>(sQ + rb * Lay::kTile, row);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_q_full);
       }
       if (rb * nb >= w.ntok) {  // no second row block
         kt += T;
@@ -787,8 +776,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           continue;
         }
         const uint32_t bad = s_bad_pages[kt % kBadRing];
-        // (8-bit cache, fp16) what the tile's K is held over
-        const float kf = Q8 && F16 ? __int_as_float(max(s_kexp[Q8 ? kt % kExpRing : 0], 1) << 23) : 1.0f;
+        // (8-bit cache) what the tile's scores are held over
+        const float kf = Q8 ? qf * __int_as_float(max(s_kexp[Q8 ? kt % kExpRing : 0], 1) << 23) : 1.0f;
         const float in_scale = CAP ? 1.0f : in_scale0 * kf, scale = (BIAS && p.slopes) ? 1.0f : in_scale;
         tc_fence_after();
         uint32_t sr[4][32];
@@ -814,7 +803,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
               for (int b = 0; b < 4; ++b) {
                 s[b] = make_float2(__uint_as_float(sr[c][e + 2 * b]), __uint_as_float(sr[c][e + 2 * b + 1]));
-                if (Q8 && F16) s[b] = fmul2(s[b], make_float2(kf, kf));
+                if (Q8) s[b] = fmul2(s[b], make_float2(kf, kf));
                 w[b] = fmul2(s[b], s[b]);
               }
 #pragma unroll

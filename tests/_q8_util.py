@@ -96,8 +96,8 @@ def check_attn_q8(got_out, got_lse, ref, case, dtype, Hkv, scale=0.0, what=""):
     row's largest at most, times sum |k| in a score; elsewhere it is exact); a probability times its V row's scale is rounded
     to fp16 (2^-11 of it) or, far below the largest V scale, to a multiple of 2^-30 of it, 2^-31 off: a row's
     largest value is above half of what its scale can hold, the kept scale at most twice the largest and a row's
-    sum at least 1, so that is below 2^-29 of the largest |v| a row; and the output is rounded once.  Tiles of an fp16
-    call hold K over the power of two of their largest row, so an element is off by 2^-25 of that, which is below 2^-30
+    sum at least 1, so that is below 2^-29 of the largest |v| a row; and the output is rounded once.  Larger units
+    hold a tile's K over the power of two of its largest row, so an element is off by 2^-25 of that, which is below 2^-30
     of the largest |k| (127 codes are the fewest that reach half of a scale), and V likewise, in the bound above."""
     out, lse, spread, xerr, _ = ref
     D = case["q"].shape[2]
@@ -112,7 +112,7 @@ def check_attn_q8(got_out, got_lse, ref, case, dtype, Hkv, scale=0.0, what=""):
         ksum = kr.abs().nan_to_num(0.0).sum(2).amax(0).repeat_interleave(q.shape[1] // Hkv)
         kmax = kr.abs().nan_to_num(0.0).amax((0, 2)).repeat_interleave(q.shape[1] // Hkv)
         qerr.append(scale * (2.0**-25 * q.abs().nan_to_num(0.0).amax(2) * ksum
-                             + (2.0**-30 * q.abs().nan_to_num(0.0).sum(2) * kmax if dtype == "fp16" else 0.0)))
+                             + 2.0**-30 * q.abs().nan_to_num(0.0).sum(2) * kmax))
         vmax = vr.abs().nan_to_num(0.0).amax((0, 2)).repeat_interleave(q.shape[1] // Hkv)
         far.append((2.0**-29 * (L + n) * vmax).expand(n, -1))
         at += n
