@@ -144,6 +144,8 @@ __device__ __forceinline__ void note_unit(const PagedAttnParams& p, const Part& 
 // for each 16 codes: 16 trees of 64 174 us, a chunk of 2,048 behind 6,100 458 us.)
 template <int D>
 constexpr int kUnits = 128 * (D / 16) / kConvertThreads;
+template <int D>
+constexpr int kRowStep = kConvertThreads / (D / 16);
 constexpr float kTcPBias = 6.0f;
 
 // Registers of the threads of a warpgroup (Q8 kernels alone).
@@ -166,39 +168,42 @@ __device__ __forceinline__ void load_raw(const uint8_t* tile, int ctid, uint4 (&
 #pragma unroll
   for (int i = 0; i < kUnits<D>; ++i) x[i] = raw[i * kConvertThreads];
 }
-// The largest scale byte of rows z0 .. z1 - 1 that are numbers, at least 1 (by a whole warp).
-__device__ __forceinline__ int scale_top(const uint8_t* scale, int z0, int z1) {
-  const int r = (threadIdx.x & 31) * 4;
-  const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + r);
-  int top = 1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int s = (s4 >> (8 * i)) & 255;
-    if (s != q8::kNaN && r + i >= z0 && r + i < z1) top = max(top, s);
-  }
-  return __reduce_max_sync(0xffffffffu, top);
+// Whether a predicate holds in all threads of a named barrier, which they all come to.
+template <int ID, int THREADS>
+__device__ __forceinline__ bool all_threads(bool good) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.and.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(all)
+      : "r"((uint32_t)good), "n"(ID), "n"(THREADS)
+      : "memory");
+  return all != 0;
 }
-// Notes which of rows z0 .. z1 - 1 are no numbers, if any is (by a whole warp).
+// The largest scale byte of rows z0 .. z1 - 1 that are numbers, at least 1, and which of a lane's four rows (bytes
+// 0xff) are not (by a whole warp).
+__device__ __forceinline__ int scale_top(const uint8_t* scale, int z0, int z1, uint32_t& nan4) {
+  const int r = (threadIdx.x & 31) * 4;
+  uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + r);
+  if (z0 > 0 || z1 < kTcKeys)
+    s4 &= (r >= z0 && r < z1 ? 0xffu : 0u) | (r + 1 >= z0 && r + 1 < z1 ? 0xff00u : 0u) |
+          (r + 2 >= z0 && r + 2 < z1 ? 0xff0000u : 0u) | (r + 3 >= z0 && r + 3 < z1 ? 0xff000000u : 0u);
+  nan4 = __vcmpeq4(s4, 0xffffffffu);
+  s4 &= ~nan4;
+  s4 = __vmaxu4(s4, s4 >> 16);
+  return __reduce_max_sync(0xffffffffu, max(max(s4 & 255u, (s4 >> 8) & 255u), 1u));
+}
+// Notes the rows that are no numbers, if there is one (by a whole warp).
 constexpr int kHasNaN = 1 << 16;
-__device__ __forceinline__ bool note_nan_rows(const uint8_t* scale, int z0, int z1, volatile uint32_t (&words)[4]) {
-  const int lane = threadIdx.x & 31, r = lane * 4;
-  uint32_t bits = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) bits |= (uint32_t)(scale[r + i] == q8::kNaN && r + i >= z0 && r + i < z1) << i;
-  if (!__any_sync(0xffffffffu, bits != 0)) return false;
+__device__ __forceinline__ bool note_nan_rows(uint32_t nan4, volatile uint32_t (&words)[4]) {
+  if (!__any_sync(0xffffffffu, nan4 != 0)) return false;
+  const int lane = threadIdx.x & 31;
+  const uint32_t bits = (nan4 & 1) | (nan4 >> 7 & 2) | (nan4 >> 14 & 4) | (nan4 >> 21 & 8);
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     const uint32_t word = __reduce_or_sync(0xffffffffu, lane / 8 == w ? bits << (4 * (lane & 7)) : 0u);
     if (lane == 0) words[w] = word;
   }
   return true;
-}
-// The factor of a row with scale byte s, fp16 2^(s - over), over >= s - 1.  V's rows that are no numbers become
-// zeros: a probability of 0 would meet them in the product (the softmax threads that see one know of it).
-__device__ __forceinline__ uint32_t row_factor(bool is_v, int s, int over) {
-  if (s == q8::kNaN) return is_v ? 0u : 0x7fffu;
-  const int e = s - over + 15;
-  return e > 30 ? 0u : e > 0 ? (uint32_t)e << 10 : e > -10 ? 512u >> -e : 0u;  // (past 30: a row that nobody sees)
 }
 // Pairs of fp16 values of four codes, times a pair of equal factors f; g = -1152 f.
 template <bool E4M3>
@@ -222,43 +227,39 @@ __device__ __forceinline__ void widen4(uint32_t x, __half2 f, __half2 g, uint32_
   hi = *reinterpret_cast<const uint32_t*>(&v1);
 }
 template <int D, bool E4M3>
-__device__ __forceinline__ void convert_tile(uint8_t* tile, const uint16_t* factor, int ctid,
+__device__ __forceinline__ void convert_tile(uint8_t* tile, const int (&e)[kUnits<D>], int ctid,
                                              const uint4 (&x)[kUnits<D>]) {
-  constexpr int kRowStep = kConvertThreads / (D / 16);
   const int c = ctid % (D / 16), r0 = unit_row<D>(ctid), ch = 2 * (c & 3), sw = r0 & 7;
   uint8_t* row = tile + (c >> 2) * kAtomBytes + r0 * 128;
   uint8_t *first = row + ((ch ^ sw) << 4), *second = row + (((ch + 1) ^ sw) << 4);
 #pragma unroll
   for (int i = 0; i < kUnits<D>; ++i) {
-    const __half2 f = __half2half2(__ushort_as_half(factor[r0 + i * kRowStep]));
+    // (a row that is no number, s = 255: infinity, which its codes of 0 make NaN)
+    const float f32 = __int_as_float(min(max(e[i], 0), 255) << 23);
+    const __half2 f = __floats2half2_rn(f32, f32);
     const __half2 g = E4M3 ? f : __hmul2(f, __half2half2(__ushort_as_half(0xe480)));  // (-1152)
     uint32_t o[8];
     widen4<E4M3>(x[i].x, f, g, o[0], o[1]);
     widen4<E4M3>(x[i].y, f, g, o[2], o[3]);
     widen4<E4M3>(x[i].z, f, g, o[4], o[5]);
     widen4<E4M3>(x[i].w, f, g, o[6], o[7]);
-    *reinterpret_cast<uint4*>(first + i * kRowStep * 128) = make_uint4(o[0], o[1], o[2], o[3]);
-    *reinterpret_cast<uint4*>(second + i * kRowStep * 128) = make_uint4(o[4], o[5], o[6], o[7]);
+    *reinterpret_cast<uint4*>(first + i * kRowStep<D> * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4*>(second + i * kRowStep<D> * 128) = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
-// The 32 bytes of a thread's unit i of a 16-bit tile: their place, for what follows the conversion (by the same thread).
-template <int D>
-__device__ __forceinline__ uint4* unit_at(uint8_t* tile, int ctid, int i, int half, int& r) {
-  constexpr int kChunks = D / 16;
-  const int c = ctid % kChunks;
-  r = unit_row<D>(ctid) + i * (kConvertThreads / kChunks);
-  return reinterpret_cast<uint4*>(tile + (c >> 2) * kAtomBytes + r * 128 + (((2 * (c & 3) + half) ^ (r & 7)) << 4));
-}
-// V rows outside of [z0, z1), whose codes and scales may be anything, become zeros.
+// V rows outside of [z0, z1), whose codes and scales may be anything, become zeros (by the threads that wrote them).
 template <int D>
 __device__ __forceinline__ void clear_outside(uint8_t* tile, int ctid, int z0, int z1) {
+  const int c = ctid % (D / 16);
 #pragma unroll 1
   for (int i = 0; i < 2 * kUnits<D>; ++i) {
-    int r;
-    uint4* at = unit_at<D>(tile, ctid, i >> 1, i & 1, r);
-    if (r < z0 || r >= z1) *at = make_uint4(0, 0, 0, 0);
+    const int r = unit_row<D>(ctid) + (i >> 1) * kRowStep<D>;
+    if (r < z0 || r >= z1)
+      *reinterpret_cast<uint4*>(tile + (c >> 2) * kAtomBytes + r * 128 + (((2 * (c & 3) + (i & 1)) ^ (r & 7)) << 4)) =
+          make_uint4(0, 0, 0, 0);
   }
 }
+
 // A row of bf16 queries in shared memory becomes fp16, over the power of two of its largest; returns that.
 // Elements below 2^-14 of the largest lose bits (to 2^-25 of it), the others none.
 template <int D>
@@ -317,15 +318,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_bad_pages[kBadRing];  // bit g: keys 8 g .. 8 g + 7 have no page
   __shared__ volatile int s_abort;
-  // (8-bit cache) raw tiles have landed; scales; the powers of two that a tile's K and V are held over; a
-  // converter's wait ran out
+  // (8-bit cache) raw tiles have landed; their scales have been looked at; scales; the powers of two that a tile's K
+  // and V are held over
   __shared__ __align__(8) uint64_t bar_q_raw;  // (bf16 queries, ahead of as_halves)
   __shared__ __align__(8) uint64_t bar_k_raw[Q8 ? kKStages : 1], bar_v_raw[Q8 ? kVStages : 1];
+  __shared__ __align__(8) uint64_t bar_k_scale[Q8 ? kKStages : 1], bar_v_scale[Q8 ? kVStages : 1];
   __shared__ __align__(16) uint8_t s_kscale[Q8 ? kKStages : 1][kTcKeys], s_vscale[Q8 ? kVStages : 1][kTcKeys];
   __shared__ volatile int s_kexp[Q8 ? kExpRing : 1], s_vexp[Q8 ? kExpRing : 1];
   __shared__ volatile uint32_t s_vnan[Q8 ? kExpRing : 1][4];  // keys whose V row is no number, where s_vexp says so
-  __shared__ volatile int s_late_step[2];
-  __shared__ uint16_t s_factor[2][Q8 ? kTcKeys : 1];  // of a tile's rows, by a step's parity
   __shared__ PartRing s_ring;
   __shared__ Cursor<kTcKeys> s_cur;
   __shared__ int s_late;  // the first sequence that a softmax warp gave up in
@@ -340,10 +340,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       mbar_init(&bar_k_full[i], Q8 ? kConvertThreads / 32 : 1);
       mbar_init(&bar_k_empty[i], 1);
       if (Q8) mbar_init(&bar_k_raw[Q8 ? i : 0], 1 + 32);
+      if (Q8) mbar_init(&bar_k_scale[Q8 ? i : 0], 1);
     }
     for (int i = 0; i < kVStages; ++i) {
       mbar_init(&bar_v_full[i], Q8 ? kConvertThreads / 32 : 1);
       if (Q8) mbar_init(&bar_v_raw[Q8 ? i : 0], 1 + 32);
+      if (Q8) mbar_init(&bar_v_scale[Q8 ? i : 0], 1);
       mbar_init(&bar_v_empty[i], 1);
       mbar_init(&bar_v_zero[i], 1);
     }
@@ -356,7 +358,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     mbar_fence_init();
     s_abort = 0;
     s_late = INT_MAX;
-    s_late_step[0] = s_late_step[1] = 0;
     s_ring.init(Q8 ? 11 + kConvertThreads / 32 : 11);  // K, V, products, eight softmax warps (, those that convert)
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
@@ -376,61 +377,42 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     // ------------------------------------------- raw tiles to 16-bit operands
     set_registers<false, 48, Q8>();
     const int ctid = tid - kTcThreads;
-    // The warps go step by step (a part, a K tile, a V tile), with a barrier in each.  A warp that gives up still joins
-    // the others there, and all see it behind: its mark has the step's parity, as a warp may already be in the next.
-    uint32_t it = 0, step = 0;  // tiles, steps so far
-    auto joined = [&](bool good) {
-      if (!good) s_late_step[step & 1] = 1;
-      named_sync(2, kConvertThreads);
-      return !s_late_step[step++ & 1];
-    };
+    uint32_t it = 0, kst = 0, kph = 0, vst = 0, vph = 0;  // tiles so far
     for (; ok; ++n) {
-      ok = __all_sync(0xffffffffu, s_ring.ready(n, p.wait_limit));
-      int lo = 0, hi = 0, begin = 0, end = 0;
-      bool over = true;
-      if (ok) {
-        const Part& w = s_ring.at(n);
-        over = w.b < 0;
-        lo = w.lo;
-        hi = w.hi;
-        begin = w.begin;
-        end = w.end;
-      }
-      ok = joined(ok);
-      if (!ok || over) break;
-      int vexp = -1;
-      for (int t = end - 1; ok && t >= begin; --t, ++it) {
-        const int z0 = max(0, lo - t * kTcKeys), z1 = min(kTcKeys, hi - t * kTcKeys);
+      ok = all_threads<2, kConvertThreads>(__all_sync(0xffffffffu, s_ring.ready(n, p.wait_limit)));
+      if (!ok) break;
+      const Part& w = s_ring.at(n);
+      if (w.b < 0) break;
+      const int lo = w.lo, hi = w.hi, begin = w.begin;
+      for (int t = w.end - 1; ok && t >= begin; --t, ++it) {
 #pragma unroll 1
         for (int side = 0; side < 2; ++side) {
-          const uint32_t stages = side ? kVStages : kKStages, st = it % stages;
-          uint64_t* raw = side ? &bar_v_raw[Q8 ? st : 0] : &bar_k_raw[Q8 ? st : 0];
-          const bool landed = warp_wait(raw, (it / stages) & 1, p.wait_limit);
+          const uint32_t st = side ? vst : kst, ph = side ? vph : kph;
+          bool landed = warp_wait((side ? bar_v_scale : bar_k_scale) + (Q8 ? st : 0), ph, p.wait_limit);
+          landed = warp_wait((side ? bar_v_raw : bar_k_raw) + (Q8 ? st : 0), ph, p.wait_limit) && landed;  // (it has)
           uint8_t* tile = (side ? sV : sK) + st * Lay::kTile;
           const uint8_t* scale = side ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0];
           uint4 x[kUnits<D>];
           load_raw<D>(tile, ctid, x);
-          const int top = scale_top(scale, z0, z1);
-          int over_exp = top;
-          if (side) {
-            if (top > vexp + 1 || vexp < 0) vexp = top;
-            over_exp = vexp;
-          }
-          uint16_t* factor = s_factor[Q8 ? step & 1 : 0];
-          if (ctid < kTcKeys) factor[Q8 ? ctid : 0] = (uint16_t)row_factor(side, scale[ctid], over_exp);
-          ok = joined(landed);  // (every code is in registers before its place is written)
+          int e[kUnits<D>];  // exponents of the rows' factors, as floats have them
+          const int over = (side ? s_vexp : s_kexp)[Q8 ? it % kExpRing : 0] & ~kHasNaN;
+#pragma unroll
+          for (int i = 0; i < kUnits<D>; ++i) e[i] = scale[unit_row<D>(ctid) + i * kRowStep<D>] + 127 - over;
+          // (every code is in registers before its place is written; a warp that gave up joins the others here)
+          ok = all_threads<2, kConvertThreads>(landed);
           if (!ok) break;
-          if (warp == 12) {
-            const bool nan = side && note_nan_rows(scale, z0, z1, s_vnan[Q8 ? it % kExpRing : 0]);
-            if (lane == 0) (side ? s_vexp : s_kexp)[Q8 ? it % kExpRing : 0] = nan ? over_exp | kHasNaN : over_exp;
-          }
-          if (p.e4m3) convert_tile<D, true>(tile, factor, ctid, x);
-          else convert_tile<D, false>(tile, factor, ctid, x);
+          if (p.e4m3) convert_tile<D, true>(tile, e, ctid, x);
+          else convert_tile<D, false>(tile, e, ctid, x);
+          const int z0 = lo - t * kTcKeys, z1 = hi - t * kTcKeys;
           if (side && (z0 > 0 || z1 < kTcKeys)) clear_outside<D>(tile, ctid, z0, z1);
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(side ? &bar_v_full[st] : &bar_k_full[st]);
+          if (lane == 0) mbar_arrive((side ? bar_v_full : bar_k_full) + st);
         }
+        kph ^= kst == kKStages - 1;
+        kst = kst == kKStages - 1 ? 0 : kst + 1;
+        vph ^= vst == kVStages - 1;
+        vst = vst == kVStages - 1 ? 0 : vst + 1;
       }
       if (lane == 0) s_ring.done(n);
     }
@@ -473,6 +455,31 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       z0 = 0;
       z1 = kTcKeys;
     };
+    // (8-bit cache) The scales of a tile that has landed: what its K or V is held over, and V's rows that are no
+    // numbers, which are noted and taken for zeros.  One tile at most is pending.
+    bool pending = false, part_first = false;
+    int p0 = 0, p1 = 0, vexp = -1;
+    uint32_t pit = 0;
+    auto look_at_scales = [&]() {
+      pending = false;
+      const uint32_t st = pit % stages;
+      if (!warp_wait(&full[st], (pit / stages) & 1, p.wait_limit)) return false;
+      uint8_t* scale = isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0];
+      uint32_t nan4;
+      int over = scale_top(scale, p0, p1, nan4);
+      if (isV) {
+        if (part_first || over > vexp + 1) vexp = over;
+        over = vexp;
+        if (note_nan_rows(nan4, s_vnan[Q8 ? pit % kExpRing : 0])) {
+          over |= kHasNaN;
+          *reinterpret_cast<uint32_t*>(scale + 4 * lane) &= ~nan4;
+        }
+      }
+      if (lane == 0) (isV ? s_vexp : s_kexp)[Q8 ? pit % kExpRing : 0] = over;
+      __syncwarp();
+      if (lane == 0) mbar_arrive((isV ? bar_v_scale : bar_k_scale) + st);
+      return true;
+    };
     ok = p.wait_limit > 0;
     for (; ok; ++n) {
       ok = __all_sync(0xffffffffu, s_ring.ready(n, p.wait_limit));
@@ -486,7 +493,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const int key = t * kTcKeys + row0;
         uint32_t bad8;
         const int page = feed.get(p, w, t, pg, bad8);
-        ok = warp_wait(&empty[st], ((it / stages) & 1) ^ 1, p.wait_limit) && !s_abort;
+        if (Q8 && pending && !__all_sync(0xffffffffu, mbar_test(&empty[st], ((it / stages) & 1) ^ 1))) ok = look_at_scales();
+        ok = ok && warp_wait(&empty[st], ((it / stages) & 1) ^ 1, p.wait_limit) && !s_abort;
         if (!ok) break;
         if (lane == 0) {
           if (!isV) s_bad_pages[it % kBadRing] = bad8;
@@ -502,6 +510,18 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             load_scales(p, (isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0]) + row0, isV ? p.v_scale : p.k_scale, page,
                         w.kvh, row);
           cp_arrive(&full[st]);
+          if (pending) {
+            ok = look_at_scales();
+            if (!ok) {
+              ++it;  // (this tile's copy is on its way)
+              break;
+            }
+          }
+          pending = true;
+          part_first = t == w.end - 1;
+          pit = it;
+          p0 = w.lo - t * kTcKeys;
+          p1 = w.hi - t * kTcKeys;
         } else if (issues)
           tma_load_rows(ring + st * Lay::kTile + atom * kAtomBytes + row0 * 128, map, &full[st],
                         atom * 64, key & ((1 << p.page_shift) - 1), w.kvh, page, p.row_dim, p.head_dim);
@@ -516,6 +536,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           z1 = min(kTcKeys, w.hi - t * kTcKeys);
         }
       }
+      if (Q8 && ok && pending) ok = look_at_scales();
       if (lane == 0) s_ring.done(n);
     }
     if (!Q8 && isV && ok) clear_rows();
@@ -645,7 +666,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             ok = ok && wait_within(&bar_v_zero[vst], (zph >> vst) & 1, p.wait_limit);
             zph ^= 1u << vst;
           }
-          if (more) ok = ok && wait_within(&bar_k_full[kst], kph, p.wait_limit);
+          // (the next K, of an 8-bit cache, is waited for where it is needed: it is converted meanwhile)
+          if (!Q8 && more) ok = ok && wait_within(&bar_k_full[kst], kph, p.wait_limit);
           for (int r = 0; ok && r < nrb; ++r) {
             ok = wait_within(&bar_p_full[r][0], pph[r], p.wait_limit);
             if (!ok) break;
@@ -656,6 +678,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             pph[r] ^= 1;
             tc_fence_after();
             issue_pv(r, 1, false);
+            if (Q8 && more && r == 0) {
+              ok = wait_within(&bar_k_full[kst], kph, p.wait_limit);
+              if (!ok) break;
+              tc_fence_after();
+            }
             if (more) issue_s(r);
             else mma_commit(&bar_o_done[r]);
           }
