@@ -137,13 +137,19 @@ __device__ __forceinline__ void note_unit(const PagedAttnParams& p, const Part& 
 }
 
 // ------------------------------------------------------------- 8-bit tiles
-// A raw tile of 128 rows of D codes lands in the second half of its stage; 256 threads take it into registers,
-// and then write the 16-bit tile over the whole stage, in the layout that TMA gives a 16-bit cache's.  A thread
-// has the 16 codes of chunk ctid % (D / 16) of rows unit_row + i 4096 / D, whose places
-// differ by a multiple of the swizzle's period.  (With four warps in place of eight, and factors and places found anew
-// for each 16 codes: 16 trees of 64 174 us, a chunk of 2,048 behind 6,100 458 us.)
+// A raw tile of 128 rows of D codes lands in the second half of its stage, and the 16-bit tile is written over the
+// whole stage, in the layout that TMA gives a 16-bit cache's: 64 rows a pass, whose place holds no codes but their own
+// and ones that have been taken.  256 threads take a pass's codes into registers, and then write them; a thread has the
+// 16 codes of chunk ctid % (D / 16) of rows unit_row + i kRowStep, whose places differ by a multiple of the swizzle's
+// period.  What bounds it is the SM's instruction cache: the roles' code does not fit (94.6 % of the fetches hit, 98 % without
+// this role), every warp waits for instructions, and a tile of 256 rows takes 4,400 cycles instead of 2,850.  So K and V share their
+// code, and a pass is half a tile.  16 trees of 64 at 4 warps 174 us, at 8 146, with K in fp16 like V 108, with
+// the scales looked at by the warps that load 105, two passes 103 (a chunk of 2,048 behind 6,100: 458, 323, 247, 226, 226).
+// Four warps a side, codes in places of their own with one tile ahead, or a pass of a whole tile twice unrolled: 128, 121,
+// 109 us.
+constexpr int kPasses = 2;
 template <int D>
-constexpr int kUnits = 128 * (D / 16) / kConvertThreads;
+constexpr int kUnits = kTcKeys / kPasses * (D / 16) / kConvertThreads;
 template <int D>
 constexpr int kRowStep = kConvertThreads / (D / 16);
 constexpr float kTcPBias = 6.0f;
@@ -162,8 +168,9 @@ __device__ __forceinline__ int unit_row(int ctid) {
   return (ctid / (D / 16)) ^ (c >> 2);
 }
 template <int D>
-__device__ __forceinline__ void load_raw(const uint8_t* tile, int ctid, uint4 (&x)[kUnits<D>]) {
-  const uint4* raw = reinterpret_cast<const uint4*>(tile + TcLayout<D>::kTile / 2) + unit_row<D>(ctid) * (D / 16) +
+__device__ __forceinline__ void load_raw(const uint8_t* tile, int ctid, int row0, uint4 (&x)[kUnits<D>]) {
+  const uint4* raw = reinterpret_cast<const uint4*>(tile + TcLayout<D>::kTile / 2) +
+                     (row0 + unit_row<D>(ctid)) * (D / 16) +
                      ctid % (D / 16);
 #pragma unroll
   for (int i = 0; i < kUnits<D>; ++i) x[i] = raw[i * kConvertThreads];
@@ -227,10 +234,10 @@ __device__ __forceinline__ void widen4(uint32_t x, __half2 f, __half2 g, uint32_
   hi = *reinterpret_cast<const uint32_t*>(&v1);
 }
 template <int D, bool E4M3>
-__device__ __forceinline__ void convert_tile(uint8_t* tile, const int (&e)[kUnits<D>], int ctid,
+__device__ __forceinline__ void convert_rows(uint8_t* tile, const int (&e)[kUnits<D>], int ctid, int row0,
                                              const uint4 (&x)[kUnits<D>]) {
   const int c = ctid % (D / 16), r0 = unit_row<D>(ctid), ch = 2 * (c & 3), sw = r0 & 7;
-  uint8_t* row = tile + (c >> 2) * kAtomBytes + r0 * 128;
+  uint8_t* row = tile + (c >> 2) * kAtomBytes + (row0 + r0) * 128;
   uint8_t *first = row + ((ch ^ sw) << 4), *second = row + (((ch + 1) ^ sw) << 4);
 #pragma unroll
   for (int i = 0; i < kUnits<D>; ++i) {
@@ -252,7 +259,7 @@ template <int D>
 __device__ __forceinline__ void clear_outside(uint8_t* tile, int ctid, int z0, int z1) {
   const int c = ctid % (D / 16);
 #pragma unroll 1
-  for (int i = 0; i < 2 * kUnits<D>; ++i) {
+  for (int i = 0; i < 2 * kPasses * kUnits<D>; ++i) {
     const int r = unit_row<D>(ctid) + (i >> 1) * kRowStep<D>;
     if (r < z0 || r >= z1)
       *reinterpret_cast<uint4*>(tile + (c >> 2) * kAtomBytes + r * 128 + (((2 * (c & 3) + (i & 1)) ^ (r & 7)) << 4)) =
@@ -290,7 +297,7 @@ __device__ __forceinline__ float as_halves(uint8_t* block, int row) {
 // their own, and rolled loops wherever a warp does not wait for them: a loop over the tiles that is
 // larger than the instruction cache (some 32 KB) runs at half the speed.
 // PRE: of a call with shared prefixes: a part may be a prefix's, and rows are left as they are.
-// Q8: over an 8-bit cache: warps 12-19 convert tiles (convert_tile) to fp16: K's over a power of two of the tile's, V's
+// Q8: over an 8-bit cache: warps 12-19 convert tiles (convert_rows) to fp16: K's over a power of two of the tile's, V's
 // over one that grows with the unit's scales.  bf16 queries become fp16 over a power of two of their row
 // (as_halves).  Scores take the powers of two of q and K with their scale, O's is V's, and P is fp16 with six more bits
 // of range below.
@@ -385,25 +392,30 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (w.b < 0) break;
       const int lo = w.lo, hi = w.hi, begin = w.begin;
       for (int t = w.end - 1; ok && t >= begin; --t, ++it) {
+        const int z0 = lo - t * kTcKeys, z1 = hi - t * kTcKeys;
 #pragma unroll 1
-        for (int side = 0; side < 2; ++side) {
+        for (int side = 0; ok && side < 2; ++side) {
           const uint32_t st = side ? vst : kst, ph = side ? vph : kph;
           bool landed = warp_wait((side ? bar_v_scale : bar_k_scale) + (Q8 ? st : 0), ph, p.wait_limit);
           landed = warp_wait((side ? bar_v_raw : bar_k_raw) + (Q8 ? st : 0), ph, p.wait_limit) && landed;  // (it has)
           uint8_t* tile = (side ? sV : sK) + st * Lay::kTile;
           const uint8_t* scale = side ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0];
-          uint4 x[kUnits<D>];
-          load_raw<D>(tile, ctid, x);
-          int e[kUnits<D>];  // exponents of the rows' factors, as floats have them
           const int over = (side ? s_vexp : s_kexp)[Q8 ? it % kExpRing : 0] & ~kHasNaN;
+#pragma unroll 1
+          for (int pass = 0; ok && pass < kPasses; ++pass) {
+            const int row0 = pass * (kTcKeys / kPasses);
+            uint4 x[kUnits<D>];
+            load_raw<D>(tile, ctid, row0, x);
+            int e[kUnits<D>];  // exponents of the rows' factors, as floats have them
 #pragma unroll
-          for (int i = 0; i < kUnits<D>; ++i) e[i] = scale[unit_row<D>(ctid) + i * kRowStep<D>] + 127 - over;
-          // (every code is in registers before its place is written; a warp that gave up joins the others here)
-          ok = all_threads<2, kConvertThreads>(landed);
+            for (int i = 0; i < kUnits<D>; ++i) e[i] = scale[row0 + unit_row<D>(ctid) + i * kRowStep<D>] + 127 - over;
+            // (the pass's codes are in registers before their place is written; a warp that gave up joins the others here)
+            ok = all_threads<2, kConvertThreads>(landed);
+            if (!ok) break;
+            if (p.e4m3) convert_rows<D, true>(tile, e, ctid, row0, x);
+            else convert_rows<D, false>(tile, e, ctid, row0, x);
+          }
           if (!ok) break;
-          if (p.e4m3) convert_tile<D, true>(tile, e, ctid, x);
-          else convert_tile<D, false>(tile, e, ctid, x);
-          const int z0 = lo - t * kTcKeys, z1 = hi - t * kTcKeys;
           if (side && (z0 > 0 || z1 < kTcKeys)) clear_outside<D>(tile, ctid, z0, z1);
           fence_async_smem();
           __syncwarp();
@@ -455,27 +467,24 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       z0 = 0;
       z1 = kTcKeys;
     };
-    // (8-bit cache) The scales of a tile that has landed: what its K or V is held over, and V's rows that are no
-    // numbers, which are noted and taken for zeros.  One tile at most is pending.
-    bool pending = false, part_first = false;
-    int p0 = 0, p1 = 0, vexp = -1;
-    uint32_t pit = 0;
-    auto look_at_scales = [&]() {
-      pending = false;
-      const uint32_t st = pit % stages;
-      if (!warp_wait(&full[st], (pit / stages) & 1, p.wait_limit)) return false;
+    // (8-bit cache) The scales of tile j, once it has landed: what its K or V is held over, and V's rows that are no
+    // numbers, which are noted and taken for zeros.
+    int vexp = -1;
+    auto look_at_scales = [&](uint32_t j, int z0, int z1, bool first) {
+      const uint32_t st = isV ? j % kVStages : j % kKStages, ph = (isV ? j / kVStages : j / kKStages) & 1;
+      if (!warp_wait(&full[st], ph, p.wait_limit)) return false;
       uint8_t* scale = isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0];
       uint32_t nan4;
-      int over = scale_top(scale, p0, p1, nan4);
+      int over = scale_top(scale, z0, z1, nan4);
       if (isV) {
-        if (part_first || over > vexp + 1) vexp = over;
+        if (first || over > vexp + 1) vexp = over;
         over = vexp;
-        if (note_nan_rows(nan4, s_vnan[Q8 ? pit % kExpRing : 0])) {
+        if (note_nan_rows(nan4, s_vnan[Q8 ? j % kExpRing : 0])) {
           over |= kHasNaN;
           *reinterpret_cast<uint32_t*>(scale + 4 * lane) &= ~nan4;
         }
       }
-      if (lane == 0) (isV ? s_vexp : s_kexp)[Q8 ? pit % kExpRing : 0] = over;
+      if (lane == 0) (isV ? s_vexp : s_kexp)[Q8 ? j % kExpRing : 0] = over;
       __syncwarp();
       if (lane == 0) mbar_arrive((isV ? bar_v_scale : bar_k_scale) + st);
       return true;
@@ -488,44 +497,56 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       if (w.b < 0) break;
       if (!Q8 && isV && w.begin == w.end) clear_rows();
       feed.start(p, w);
+      if (Q8) {
+        // Loads go first, as far as there is room; else the scales of the next tile that lands are looked at.
+        const uint32_t it0 = it, it1 = it + (w.end - w.begin);
+        for (uint32_t seen = it; seen < it1;) {
+          const uint32_t st = isV ? it % kVStages : it % kKStages, ph = ((isV ? it / kVStages : it / kKStages) & 1) ^ 1;
+          if (it < it1 && (seen == it || __all_sync(0xffffffffu, mbar_test(&empty[st], ph)))) {
+            const int t = w.end - 1 - (int)(it - it0), row = (t * kTcKeys + row0) & ((1 << p.page_shift) - 1);
+            uint32_t bad8;
+            const int page = feed.get(p, w, t, pg, bad8);
+            ok = warp_wait(&empty[st], ph, p.wait_limit) && !s_abort;
+            if (!ok) break;
+            if (lane == 0) {
+              if (!isV) s_bad_pages[it % kBadRing] = bad8;
+              mbar_expect_tx(&full[st], Lay::kTile / 2);
+            }
+            __syncwarp();
+            if (issues)
+              tma_load_rows(ring + st * Lay::kTile + Lay::kTile / 2 + row0 * D, map, &full[st], 0, row, w.kvh, page,
+                            p.row_dim, p.head_dim);
+            if (lane < 16)
+              load_scales(p, (isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0]) + row0, isV ? p.v_scale : p.k_scale,
+                          page, w.kvh, row);
+            cp_arrive(&full[st]);
+            ++it;
+          } else {
+            const int j0 = (w.end - 1 - (int)(seen - it0)) * kTcKeys;
+            ok = look_at_scales(seen, w.lo - j0, w.hi - j0, seen == it0);
+            if (!ok) break;
+            ++seen;
+          }
+        }
+        if (lane == 0) s_ring.done(n);
+        continue;
+      }
       for (int t = w.end - 1; t >= w.begin; --t, ++it) {
         const uint32_t st = it % stages;
         const int key = t * kTcKeys + row0;
         uint32_t bad8;
         const int page = feed.get(p, w, t, pg, bad8);
-        if (Q8 && pending && !__all_sync(0xffffffffu, mbar_test(&empty[st], ((it / stages) & 1) ^ 1))) ok = look_at_scales();
-        ok = ok && warp_wait(&empty[st], ((it / stages) & 1) ^ 1, p.wait_limit) && !s_abort;
+        ok = warp_wait(&empty[st], ((it / stages) & 1) ^ 1, p.wait_limit) && !s_abort;
         if (!ok) break;
         if (lane == 0) {
           if (!isV) s_bad_pages[it % kBadRing] = bad8;
-          mbar_expect_tx(&full[st], Q8 ? Lay::kTile / 2 : Lay::kTile);
+          mbar_expect_tx(&full[st], Lay::kTile);
         }
         __syncwarp();
-        if (Q8) {
-          const int row = key & ((1 << p.page_shift) - 1);
-          if (issues)
-            tma_load_rows(ring + st * Lay::kTile + Lay::kTile / 2 + row0 * D, map, &full[st], 0, row, w.kvh, page, p.row_dim,
-                          p.head_dim);
-          if (lane < 16)
-            load_scales(p, (isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0]) + row0, isV ? p.v_scale : p.k_scale, page,
-                        w.kvh, row);
-          cp_arrive(&full[st]);
-          if (pending) {
-            ok = look_at_scales();
-            if (!ok) {
-              ++it;  // (this tile's copy is on its way)
-              break;
-            }
-          }
-          pending = true;
-          part_first = t == w.end - 1;
-          pit = it;
-          p0 = w.lo - t * kTcKeys;
-          p1 = w.hi - t * kTcKeys;
-        } else if (issues)
+        if (issues)
           tma_load_rows(ring + st * Lay::kTile + atom * kAtomBytes + row0 * 128, map, &full[st],
                         atom * 64, key & ((1 << p.page_shift) - 1), w.kvh, page, p.row_dim, p.head_dim);
-        if (!Q8 && isV) {
+        if (isV) {
           clear_rows();
           if (!ok) {
             ++it;  // (this tile's copy is on its way)
@@ -536,7 +557,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           z1 = min(kTcKeys, w.hi - t * kTcKeys);
         }
       }
-      if (Q8 && ok && pending) ok = look_at_scales();
       if (lane == 0) s_ring.done(n);
     }
     if (!Q8 && isV && ok) clear_rows();
