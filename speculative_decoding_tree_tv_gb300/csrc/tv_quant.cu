@@ -22,8 +22,10 @@ tv_status launched(cudaError_t e) {
 }
 
 // ------------------------------------------------------------------- append
-// A row goes to 1 << row_lanes lanes, C chunks of eight values each, all loads in flight ahead of the
-// row's maximum, which takes row_lanes shuffles.  Bound by HBM (3 D + 1 bytes a row).
+// A row goes to 1 << row_lanes lanes, U units of 16 values each, all loads in flight ahead of the
+// row's maximum, which takes row_lanes shuffles.  Bound by HBM (3 D + 1 bytes a row): 8,192 tokens of 8 heads of 128
+// take 9.6 us, 73 % of the copy rate (10.4 us when a lane stored 8 codes at a time); 64 tokens 1.6 us, a launch's
+// latency.
 constexpr int kRowThreads = 256;
 
 struct AppendQ8Params {
@@ -33,10 +35,10 @@ struct AppendQ8Params {
   int32_t* status;
   long long token_stride, head_stride;
   Q8Cache c;
-  int T, chunks, row_lanes;
+  int T, units, row_lanes;  // units: of 16 values in a row
 };
 
-template <bool E4M3, bool F16, int C>
+template <bool E4M3, bool F16, int U>
 __global__ void __launch_bounds__(kRowThreads) append_q8_kernel(const AppendQ8Params p) {
   pdl_trigger();
   pdl_wait();
@@ -50,20 +52,21 @@ __global__ void __launch_bounds__(kRowThreads) append_q8_kernel(const AppendQ8Pa
   const long long limit = (long long)p.c.num_pages << p.c.page_shift;
   const bool in = slot >= 0 && slot < limit;
   if (is_row && w == 0 && lane == 0 && p.status) p.status[t] = slot >= limit ? TV_ERR_INVALID_ARG : TV_OK;
-  uint4 x[C];
+  uint4 x[U][2];
   const uint4* src = reinterpret_cast<const uint4*>((side ? p.v : p.k) + (long long)t * p.token_stride +
                                                     h * p.head_stride);
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int at = lane + c * lanes;
-    x[c] = in && at < p.chunks ? __ldg(src + at) : make_uint4(0, 0, 0, 0);
+  for (int c = 0; c < 2 * U; ++c) {
+    const int at = lane + (c >> 1) * lanes;
+    x[c >> 1][c & 1] = in && at < p.units ? __ldg(src + 2 * at + (c & 1)) : make_uint4(0, 0, 0, 0);
   }
   // the largest magnitude: 16-bit floats without their sign are in the order of their bits
   uint32_t top = 0;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
+  for (int c = 0; c < 2 * U; ++c) {
     const uint32_t m = 0x7fff7fffu;
-    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[c].x & m, x[c].y & m), __vmaxu2(x[c].z & m, x[c].w & m)));
+    const uint4 v = x[c >> 1][c & 1];
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m)));
   }
   top = max(top & 0xffffu, top >> 16);
   for (int o = 1; o < (int)lanes; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -73,33 +76,40 @@ __global__ void __launch_bounds__(kRowThreads) append_q8_kernel(const AppendQ8Pa
   const float f = s == q8::kNaN ? 0.0f : __int_as_float((254 - s) << 23);
   const long long page = slot >> p.c.page_shift;
   const int row = (int)(slot & ((1ll << p.c.page_shift) - 1));
-  uint2* dst = reinterpret_cast<uint2*>((side ? p.c.v : p.c.k) + p.c.code_at(page, h, row));
+  uint4* dst = reinterpret_cast<uint4*>((side ? p.c.v : p.c.k) + p.c.code_at(page, h, row));
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int at = lane + c * lanes;
-    const uint32_t in4[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-    float2 y[4];
+  for (int c = 0; c < U; ++c) {
+    const uint32_t in8[8] = {x[c][0].x, x[c][0].y, x[c][0].z, x[c][0].w, x[c][1].x, x[c][1].y, x[c][1].z, x[c][1].w};
+    uint32_t out4[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      y[i] = q8::unpack<F16>(s == q8::kNaN ? 0u : in4[i]);
-      y[i].x *= f;
-      y[i].y *= f;
+      float2 y[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        y[k] = q8::unpack<F16>(s == q8::kNaN ? 0u : in8[2 * i + k]);
+        y[k].x *= f;
+        y[k].y *= f;
+      }
+      out4[i] = q8::encode4<E4M3>(y[0], y[1]);
     }
-    if (at < p.chunks) dst[at] = make_uint2(q8::encode4<E4M3>(y[0], y[1]), q8::encode4<E4M3>(y[2], y[3]));
+    const int at = lane + c * lanes;
+    if (at < p.units) dst[at] = make_uint4(out4[0], out4[1], out4[2], out4[3]);
   }
   if (lane == 0) (side ? p.c.vs : p.c.ks)[p.c.scale_at(page, h, row)] = (uint8_t)s;
 }
 
 template <bool E4M3, bool F16>
-cudaError_t launch_append(const AppendQ8Params& p, int C, unsigned blocks, cudaStream_t stream) {
-  if (C == 1) return launch_pdl(append_q8_kernel<E4M3, F16, 1>, dim3(blocks), dim3(kRowThreads), 0, stream, p);
-  if (C == 2) return launch_pdl(append_q8_kernel<E4M3, F16, 2>, dim3(blocks), dim3(kRowThreads), 0, stream, p);
-  return launch_pdl(append_q8_kernel<E4M3, F16, 4>, dim3(blocks), dim3(kRowThreads), 0, stream, p);
+cudaError_t launch_append(const AppendQ8Params& p, int U, unsigned blocks, cudaStream_t stream) {
+  if (U == 1) return launch_pdl(append_q8_kernel<E4M3, F16, 1>, dim3(blocks), dim3(kRowThreads), 0, stream, p);
+  return launch_pdl(append_q8_kernel<E4M3, F16, 2>, dim3(blocks), dim3(kRowThreads), 0, stream, p);
 }
 
 // --------------------------------------------------------------------- read
 // A CTA takes `tokens` consecutive tokens: a thread each finds its token's sequence (a binary search of
-// the starts) and row, then all stream the rows, 16 codes a step, four steps in flight.
+// the starts) and row, then all stream the rows, 16 codes a step, four steps in flight (two take as long, eight
+// 103 us for the 85 that four took then: fewer warps).  Bound by HBM (3 D + 1 bytes a row): 16 sequences of 512 to 8,192
+// tokens, 8 heads of 128, take 73 us, 87 % of the copy rate; 84.5 us while each step divided for its place and
+// every value was held against the type's largest.
 constexpr int kReadTokens = 32, kReadFlight = 4;
 
 struct ReadQ8Params {
@@ -111,6 +121,7 @@ struct ReadQ8Params {
   uint16_t* v;
   int32_t* status;
   int B, T, P, tokens, units;  // units: of 16 codes in a row
+  int step_c, step_w, step_t;  // kRowThreads units as units of a row, rows of a token and tokens
   int blocks;                  // CTAs of tokens; those behind them write the sequences' status
 };
 
@@ -119,13 +130,19 @@ __device__ __forceinline__ bool read_fits(const ReadQ8Params& p, int start, int 
   return start >= 0 && (long long)start + n <= ((long long)p.P << p.c.page_shift);
 }
 
+// Scale bytes up to this one give no value (448 2^e or 128 2^e at most) past the type's largest.
+template <bool E4M3, bool F16>
+constexpr int kSafeScale = 127 + (E4M3 ? (F16 ? 7 : 119) : (F16 ? 8 : 120));
+
 template <bool F16>
-__device__ __forceinline__ uint32_t narrow(float2 y, float f) {
+__device__ __forceinline__ uint32_t narrow(float2 y, float f, bool safe) {
   y.x *= f;
   y.y *= f;
-  const float most = F16 ? 65504.0f : 3.38953139e38f;  // (a code's value may be past it; a NaN stays)
-  if (fabsf(y.x) > most) y.x = copysignf(most, y.x);
-  if (fabsf(y.y) > most) y.y = copysignf(most, y.y);
+  if (!safe) {
+    const float most = F16 ? 65504.0f : 3.38953139e38f;  // (a code's value may be past it; a NaN stays)
+    if (fabsf(y.x) > most) y.x = copysignf(most, y.x);
+    if (fabsf(y.y) > most) y.y = copysignf(most, y.y);
+  }
   if (F16) {
     const __half2 o = __floats2half2_rn(y.x, y.y);
     return *reinterpret_cast<const uint32_t*>(&o);
@@ -181,42 +198,53 @@ __global__ void __launch_bounds__(kRowThreads) read_q8_kernel(const ReadQ8Params
     s_row[tid] = row;
   }
   __syncthreads();
-  const int per_side = p.c.Hkv * p.units, per_token = 2 * per_side, items = count * per_token;
-  for (int i0 = tid; i0 < items; i0 += kRowThreads * kReadFlight) {
+  const int rows = 2 * p.c.Hkv;  // of a token, K's ahead of V's
+  int c = tid % p.units, w = tid / p.units % rows, t = tid / p.units / rows;
+  while (t < count) {
     uint4 x[kReadFlight], *dst[kReadFlight];
     int s[kReadFlight];
 #pragma unroll
     for (int u = 0; u < kReadFlight; ++u) {
-      const int i = i0 + u * kRowThreads;
       dst[u] = nullptr;
-      if (i < items) {
-        const int t = i / per_token, w = i - t * per_token;
-        const bool side = w >= per_side;
-        const int r = side ? w - per_side : w, h = r / p.units, c = r - h * p.units;
-        const int page = s_page[t];
+      if (t < count) {
+        const bool side = w >= p.c.Hkv;
+        const int h = side ? w - p.c.Hkv : w, page = s_page[t];
         x[u] = make_uint4(0, 0, 0, 0);
         s[u] = 1;
         if (page >= -1)
-          dst[u] = reinterpret_cast<uint4*>((side ? p.v : p.k) +
-                                            ((long long)(first + t) * per_side + r) * 16);
+          dst[u] = reinterpret_cast<uint4*>(
+              (side ? p.v : p.k) + (((long long)(first + t) * p.c.Hkv + h) * p.units + c) * 16);
         if (page >= 0) {
           x[u] = __ldg(reinterpret_cast<const uint4*>((side ? p.c.v : p.c.k) + p.c.code_at(page, h, s_row[t])) + c);
           s[u] = __ldg((side ? p.c.vs : p.c.ks) + p.c.scale_at(page, h, s_row[t]));
         }
+      }
+      // kRowThreads units of 16 codes on
+      c += p.step_c;
+      w += p.step_w;
+      t += p.step_t;
+      if (c >= p.units) {
+        c -= p.units;
+        ++w;
+      }
+      if (w >= rows) {
+        w -= rows;
+        ++t;
       }
     }
 #pragma unroll
     for (int u = 0; u < kReadFlight; ++u) {
       if (!dst[u]) continue;
       const float f = q8::factor(s[u]);
+      const bool safe = s[u] <= kSafeScale<E4M3, F16>;
       const uint32_t c4[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
       uint32_t o[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float2 a, b;
         q8::decode4<E4M3>(c4[i], a, b);
-        o[2 * i] = narrow<F16>(a, f);
-        o[2 * i + 1] = narrow<F16>(b, f);
+        o[2 * i] = narrow<F16>(a, f, safe);
+        o[2 * i + 1] = narrow<F16>(b, f, safe);
       }
       dst[u][0] = make_uint4(o[0], o[1], o[2], o[3]);
       dst[u][1] = make_uint4(o[4], o[5], o[6], o[7]);
@@ -251,18 +279,21 @@ extern "C" tv_status tv_paged_append_q8(const void* k, const void* v, int64_t to
   p.slots = slots;
   p.status = status;
   p.T = T;
-  p.chunks = D / 8;
-  const int C = p.chunks > 64 ? 4 : p.chunks >= 4 ? 2 : 1;
+  p.units = D / 16;
+  // Half the threads where a unit each would be more than half as many again as the GPU holds (8 CTAs an SM): 8,192,
+  // 4,096 and 2,048 tokens of 8 heads of 128 take 9.6, 6.1 and 4.4 us with two units, 10.3, 6.2 and 4.1 us with one.
+  const bool many = 2ll * T * Hkv * p.units > 12ll * tv::kRowThreads * tv::device_sm_count();
+  const int U = p.units > 32 || (p.units > 1 && many) ? 2 : 1;
   p.row_lanes = 0;
-  while (p.row_lanes < 5 && (C << p.row_lanes) < p.chunks) ++p.row_lanes;
+  while (p.row_lanes < 5 && (U << p.row_lanes) < p.units) ++p.row_lanes;
   const long long threads = (2ll * T * Hkv) << p.row_lanes;
   const unsigned blocks = (unsigned)((threads + tv::kRowThreads - 1) / tv::kRowThreads);
   const bool f16 = cache->dtype == TV_FP16;
   if (cache->format == TV_E4M3)
-    return tv::launched(f16 ? tv::launch_append<true, true>(p, C, blocks, stream)
-                            : tv::launch_append<true, false>(p, C, blocks, stream));
-  return tv::launched(f16 ? tv::launch_append<false, true>(p, C, blocks, stream)
-                          : tv::launch_append<false, false>(p, C, blocks, stream));
+    return tv::launched(f16 ? tv::launch_append<true, true>(p, U, blocks, stream)
+                            : tv::launch_append<true, false>(p, U, blocks, stream));
+  return tv::launched(f16 ? tv::launch_append<false, true>(p, U, blocks, stream)
+                          : tv::launch_append<false, false>(p, U, blocks, stream));
 }
 
 extern "C" tv_status tv_paged_read_q8(const tv_q8_cache* cache, const int32_t* block_table,
@@ -291,6 +322,9 @@ extern "C" tv_status tv_paged_read_q8(const tv_q8_cache* cache, const int32_t* b
   p.T = T;
   p.P = P;
   p.units = D / 16;
+  p.step_c = tv::kRowThreads % p.units;
+  p.step_w = tv::kRowThreads / p.units % (2 * Hkv);
+  p.step_t = tv::kRowThreads / p.units / (2 * Hkv);
   p.tokens = tv::kReadTokens;
   while (p.tokens > 1 && T / p.tokens < 4 * tv::device_sm_count()) p.tokens /= 2;
   p.blocks = T / p.tokens + (T % p.tokens != 0);
