@@ -203,7 +203,7 @@ long long wait_limit() {
 }
 
 // Which kernel runs, by the rows of the largest unit.
-PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long keys) {
+PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long keys, bool q8 = false) {
   PagedPlan pl;
   const long long rows = (long long)max_q * G;
   // 64 decode sequences of 512 to 8,192 keys, 8 kv heads: 4 rows a unit 186 us here and 198 us on the
@@ -215,8 +215,9 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
     pl.nb = pl.tq = (rows <= 8 ? 8 : 16) / G;
     pl.ctas = 2 * device_sm_count();
     // (4 sequences of 1,000 keys 11.4, 12.0 and 13.9 us at 5, 6 and 9; one of 10,000, whose parts are many,
-    // 20.7, 19.4 and 18.6 us)
-    pl.min_share = 6;
+    // 20.7, 19.4 and 18.6 us.  Tiles of 8-bit codes have 128 keys: 4 sequences of 1,500 keys 14, 14 to 15, 18 and 22 us
+    // at 3, 4, 6 and 9, one of 10,000 19.0, 18.9, 20.0 and 23.4 us)
+    pl.min_share = q8 ? 4 : 6;
   } else {
     pl.rows = 256;
     pl.nb = 128 / G;
@@ -229,7 +230,9 @@ PagedPlan paged_plan(int max_q, int Hkv, int G, int D, int B, int T, long long k
   // host knows no lengths; short sequences in a wide table are split) are not split, and
   // the merge is not launched: decode of 4 sequences of 500, 1,000 and 1,500 keys 8.9, 12.6 and 16.2 us,
   // split 11.2, 11.8 and 12.2 us (D 64: 1,000 keys 9.9 and 10.5 us; 16 rows: 13.5 and 14.1 us); 2 trees of 64
-  // behind 200, 440 and 900 keys 14.3, 14.7 and 20.3 us, split 18.1, 18.9 and 19.5 us.
+  // behind 200, 440 and 900 keys 14.3, 14.7 and 20.3 us, split 18.1, 18.9 and 19.5 us.  8-bit caches: decode of 4
+  // sequences of 500, 940 and 1,500 keys 10.4, 14.0 and 18.3 us, split 14.5, 16.9 and 17.9 us (at shares of 6; 14 to 15
+  // at 4); 2 trees of 64 behind 200, 440 and 900 keys 19.6, 20.4 and 30.9 us, split 25.1, 26.2 and 27.6 us.
   pl.whole = keys <= (pl.small ? kWholeRowsKeys : kWholeTcKeys) &&
              (long long)Hkv * (T / pl.tq + B) <= device_sm_count();
   if (pl.whole) pl.min_share = 1;
@@ -492,7 +495,7 @@ tv_status attend(AttnArgs a, const CacheArg& cache) {
   tv_status st = check_attn(a, cache);
   if (st != TV_OK || a.B == 0) return st;
   const PagedPlan pl = paged_plan(a.max_q, cache.Hkv, a.Hq / cache.Hkv, cache.D, a.B, a.T,
-                                  (long long)a.P << cache.c.page_shift);
+                                  (long long)a.P << cache.c.page_shift, cache.format >= 0);
   if (!a.workspace || a.ws_bytes < pl.bytes() || (reinterpret_cast<uintptr_t>(a.workspace) & 255))
     return TV_ERR_WORKSPACE;
   Pass s;
