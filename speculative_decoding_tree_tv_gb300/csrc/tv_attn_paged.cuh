@@ -20,7 +20,9 @@
 //
 // Two kernels take units: paged_rows_kernel (tv_attn_paged_rows.cu) those of at most 16 rows
 // (decode tokens and small trees: HBM-bound, warp-level mma), and
-// paged_tc_kernel (tv_attn_paged_tc.cu, tcgen05) larger ones.
+// paged_tc_kernel (tv_attn_paged_tc.cuh, tcgen05) larger ones.  Over an 8-bit cache the former has a twin,
+// paged_rows_q8_kernel (tv_attn_q8_rows.cuh), the latter a variant.  With shared prefixes (tv_attn_prefix.cu) the line
+// holds the groups' prefixes, as sequences whose rows are all their group's tokens, ahead of the sequences.
 #pragma once
 
 #include <cuda.h>

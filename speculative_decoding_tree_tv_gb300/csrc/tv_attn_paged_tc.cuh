@@ -14,7 +14,11 @@
 //                   one page), each into a ring of its own;
 //   warp 9          the products: S_r = Q_r K^T and O_r += P_r V (tcgen05.mma, operands in
 //                   shared memory but P, which is read from TMEM where it overlays S_r);
-//   warp 11         walks the share and publishes its parts; the parts' Q rows.
+//   warp 11         walks the share and publishes its parts; the parts' Q rows;
+//   warps 12-19     over an 8-bit cache: tiles of codes, which land in the second half of their
+//                   stage, become fp16 tiles in place (warps 8 and 10 look at their scales ahead of that).
+// 8-bit tiles take 4,400 cycles (the section on them tells why): 16 trees of 64 nodes 101 us with e4m3 and 103 with int8, a
+// chunk of 2,048 behind 6,100 keys 226 and 235 us.
 // The products are issued in the order PV_0(t), S_0(t + 1), PV_1(t), S_1(t + 1): while one row
 // block's softmax runs, the tensor core works on the other's.  S_r(t + 1) may
 // overwrite P_r(t), as products retire in issue order.  The next unit's first S
@@ -132,7 +136,9 @@ __device__ __forceinline__ void note_unit(const PagedAttnParams& p, const Part& 
   int4* src = p.src + (w.s.shared ? 0 : (size_t)p.T * p.Hkv);
   for (int i = threadIdx.x & 31; i < w.ntok; i += 32) {
     const int t = w.s.t0 + w.first + i;
-    if (TV_IN(t, p.T)) src[(size_t)t * p.Hkv + w.kvh] = make_int4(w.slot, w.parts, w.s.t0 + w.first, w.s.shared ? w.b : w.b - p.groups);
+    if (TV_IN(t, p.T))
+      src[(size_t)t * p.Hkv + w.kvh] =
+          make_int4(w.slot, w.parts, w.s.t0 + w.first, w.s.shared ? w.b : w.b - p.groups);
   }
 }
 
@@ -141,12 +147,12 @@ __device__ __forceinline__ void note_unit(const PagedAttnParams& p, const Part& 
 // whole stage, in the layout that TMA gives a 16-bit cache's: 64 rows a pass, whose place holds no codes but their own
 // and ones that have been taken.  256 threads take a pass's codes into registers, and then write them; a thread has the
 // 16 codes of chunk ctid % (D / 16) of rows unit_row + i kRowStep, whose places differ by a multiple of the swizzle's
-// period.  What bounds it is the SM's instruction cache: the roles' code does not fit (94.6 % of the fetches hit, 98 % without
-// this role), every warp waits for instructions, and a tile of 256 rows takes 4,400 cycles instead of 2,850.  So K and V share their
-// code, and a pass is half a tile.  16 trees of 64 at 4 warps 174 us, at 8 146, with K in fp16 like V 108, with
-// the scales looked at by the warps that load 105, two passes 103 (a chunk of 2,048 behind 6,100: 458, 323, 247, 226, 226).
-// Four warps a side, codes in places of their own with one tile ahead, or a pass of a whole tile twice unrolled: 128, 121,
-// 109 us.
+// period.  What bounds it is the SM's instruction cache: the roles' code does not fit (92 to 95 % of the fetches hit,
+// 98 % without this role), every warp waits for instructions, and a tile of 256 rows takes 4,400 cycles instead of
+// 2,850.  So K and V share their code, and a pass is half a tile.  16 trees of 64 at 4 warps 174 us, at 8 146, with K
+// in fp16 like V 108, with the scales looked at by the warps that load 105, two passes 103 (a chunk of 2,048 behind
+// 6,100: 458, 323, 247, 226, 226).  Four warps a side, codes in places of their own with one tile ahead, or a pass of a
+// whole tile twice unrolled: 128, 121, 109 us.
 constexpr int kPasses = 2;
 template <int D>
 constexpr int kUnits = kTcKeys / kPasses * (D / 16) / kConvertThreads;
@@ -286,7 +292,8 @@ __device__ __forceinline__ float as_halves(uint8_t* block, int row) {
   for (int c = 0; c < D / 8; ++c) {
     uint4* p = reinterpret_cast<uint4*>(at + (c >> 3) * kAtomBytes + (((c & 7) ^ sw) << 4));
     const uint4 v = *p;
-    const float2 a = q8::unpack<false>(v.x), b = q8::unpack<false>(v.y), d = q8::unpack<false>(v.z), g = q8::unpack<false>(v.w);
+    const float2 a = q8::unpack<false>(v.x), b = q8::unpack<false>(v.y);
+    const float2 d = q8::unpack<false>(v.z), g = q8::unpack<false>(v.w);
     *p = make_uint4(pack2<true>(a.x * f, a.y * f), pack2<true>(b.x * f, b.y * f), pack2<true>(d.x * f, d.y * f),
                     pack2<true>(g.x * f, g.y * f));
   }
@@ -1103,7 +1110,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               for (int q = 0; q < 16; ++q)
                 v[q] = __ldcg(&part[((size_t)(w.slot + k) * (D / 4) + 16 * c + q) * 256]);
               const float f = m == -INFINITY ? 0.0f : ex2(m - m_all);
-              if (f == 0.0f && (!Q8 || m == -INFINITY)) continue;  // (a part whose keys are all hidden: select, do not multiply)
+              // (a part whose keys are all hidden: select, do not multiply)
+              if (f == 0.0f && (!Q8 || m == -INFINITY)) continue;
 #pragma unroll
               for (int q = 0; q < 16; ++q) {
                 uint32_t* x = &o[q >> 3][4 * (q & 7)];
@@ -1153,7 +1161,8 @@ template <int D, bool F16, bool CAP, bool BIAS, bool PRE, bool Q8>
 cudaError_t launch(const PagedPlan& pl, const CUtensorMap& tmQ, const CUtensorMap& tmK,
                    const CUtensorMap& tmV, const PagedAttnParams& p, cudaStream_t stream) {
   if (!set_dyn_smem(paged_tc_kernel<D, F16, CAP, BIAS, PRE, Q8>, TcLayout<D>::kDyn)) return cudaErrorUnknown;
-  return launch_pdl(paged_tc_kernel<D, F16, CAP, BIAS, PRE, Q8>, dim3(pl.ctas), dim3(Q8 ? kTcThreads + kConvertThreads : kTcThreads),
+  return launch_pdl(paged_tc_kernel<D, F16, CAP, BIAS, PRE, Q8>, dim3(pl.ctas),
+                    dim3(Q8 ? kTcThreads + kConvertThreads : kTcThreads),
                     (size_t)TcLayout<D>::kDyn, stream, tmQ, tmK, tmV, p, pl.nb);
 }
 template <int D, bool F16, bool PRE, bool Q8>

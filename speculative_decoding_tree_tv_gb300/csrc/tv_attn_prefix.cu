@@ -5,7 +5,13 @@
 // read once for them; a sequence's own units follow on the same line, and the line is cut into equal shares as
 // always: prefixes and own rows are worked on side by side in one launch.  Small own units (decode tokens)
 // stay on this kernel too: it streams their pages at 94 % of the small kernel's rate (64 decode
-// sequences 198 and 186 us), and a launch of their own would wait for the prefixes' one.
+// sequences 198 and 186 us), and a launch of their own waits for the prefixes' one (52 for 46.5 us, 64 sequences behind
+// 8,000 rows).  As two passes, own rows behind the prefixes' joined ones, that took 71 us.
+//
+// Bound by latency: a prefix has few bytes when it is read once.  64 decode tokens behind 8,000 rows with 30 to 600 of
+// their own take 45 us (floor 16): the share is known at 3.4 us, the first product issued at 8, the first tile done at
+// 12.5 (its code is new to the SM), then 1.9 us a tile, and 9 us for the rows' stores and their joining.  Trees of 16 to
+// 48 nodes behind four prompts take 27 us, three short sequences 17.
 #define TV_UNIT 17
 #include "tv_attn_paged_tc.cuh"
 
