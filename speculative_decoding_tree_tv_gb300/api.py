@@ -913,6 +913,8 @@ def paged_read_q8(k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.T
     [B+1]; start int32 [B]; tokens = rows of the outputs.
     Returns (k, v [tokens, Hkv, D], status int32 [B])."""
     if k is not None:
+        if not isinstance(k, torch.Tensor):
+            raise TypeError("k must be a torch.Tensor")
         dtype = k.dtype
     cache = _q8_cache(k_codes, v_codes, k_scale, v_scale, dtype)
     dev = k_codes.device

@@ -357,3 +357,18 @@ def test_refusals_of_the_binding(tv):
         tv.paged_append_q8(x, x, slots, wide[0], wide[1], ks, vs)
     with pytest.raises(tv.TVError):
         tv.paged_append_q8(x, x, slots, *cache("int8", 3, 2, 24, 64))
+
+
+def test_outputs_that_do_not_fit_are_refused(tv):
+    c = cache("int8", 3, 2, 16, 64)
+    table, q_start, start = i32([[0, 1]]), i32([0, 4]), i32([0])
+    x = torch.zeros(4, 2, 64, dtype=torch.float16, device="cuda:0")
+    for kw in (dict(k=[0.0]), dict(v=[0.0]), dict(v=x), dict(k=x.float()), dict(k=x, v=x.bfloat16()),
+               dict(status=x)):
+        with pytest.raises(TypeError):
+            tv.paged_read_q8(*c, table, q_start, start, 4, **kw)
+    for kw in (dict(k=x.cpu()), dict(k=x[:, :1]), dict(k=x, v=x.transpose(0, 1)), dict(status=i32([0, 0]))):
+        with pytest.raises(ValueError):
+            tv.paged_read_q8(*c, table, q_start, start, 4, **kw)
+    k, v, _ = tv.paged_read_q8(*c, table, q_start, start, 4, k=x)
+    assert k is x and v.dtype == torch.float16
