@@ -26,6 +26,7 @@
 // threads write after the epilogue.  Every wait is bounded.
 #pragma once
 
+#include <cfloat>
 #include <climits>
 
 #include "tv_attn_paged.cuh"
@@ -830,9 +831,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           continue;
         }
         const uint32_t bad = s_bad_pages[kt % kBadRing];
-        // (8-bit cache) what the tile's scores are held over
-        const float kf = Q8 ? qf * __int_as_float(max(s_kexp[Q8 ? kt % kExpRing : 0], 1) << 23) : 1.0f;
-        const float in_scale = CAP ? 1.0f : in_scale0 * kf, scale = (BIAS && p.slopes) ? 1.0f : in_scale;
+        // (8-bit cache) what the tile's scores are held over, as a 32-bit number: a row of zeros over a tile of tiny
+        // keys would make it 0, and hidden keys are at -inf ahead of it; nor is 0 times it to be anything else
+        const float kf = Q8 ? fminf(qf * __int_as_float(max(s_kexp[Q8 ? kt % kExpRing : 0], 1) << 23), FLT_MAX) : 1.0f;
+        const float in_scale = CAP ? 1.0f : Q8 ? fminf(fmaxf(in_scale0 * kf, FLT_MIN), FLT_MAX) : in_scale0;
+        const float scale = (BIAS && p.slopes) ? 1.0f : in_scale;
         tc_fence_after();
         uint32_t sr[4][32];
 #pragma unroll

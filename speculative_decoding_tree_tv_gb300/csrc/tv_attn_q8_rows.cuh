@@ -20,6 +20,8 @@
 // same scores to turn into probabilities, 91 us (51 %).
 #pragma once
 
+#include <cfloat>
+
 #include "tv_quant.cuh"
 #include "tv_warp_mma.cuh"
 
@@ -66,6 +68,14 @@ __device__ __forceinline__ void halves(uint32_t x, uint32_t& lo, uint32_t& hi) {
 template <bool E4M3>
 __device__ __forceinline__ void halves_t(uint32_t x, uint32_t& even, uint32_t& odd) {
   halves<E4M3>(__byte_perm(x, 0, 0x3120), even, odd);
+}
+
+// The smaller of two numbers, NaN if x is (a row that is no number has that factor; 0 times a factor past the 32-bit
+// range is 0 all the same).
+__device__ __forceinline__ float at_most(float x, float top) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(top));
+  return y;
 }
 
 // Q's and the outputs' type makes no variant: it matters at a unit's ends alone.
@@ -337,7 +347,7 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int i = 0; i < kAll; ++i) s[at(r, i)] *= in_scale[r] * kf[i];
+          for (int i = 0; i < kAll; ++i) s[at(r, i)] *= at_most(in_scale[r] * kf[i], FLT_MAX);
         if (MOD && p.softcap_log2 > 0.0f) {
           float f[KB * 8], top = 0.0f;
 #pragma unroll

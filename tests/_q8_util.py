@@ -134,3 +134,95 @@ def check_attn_q8(got_out, got_lse, ref, case, dtype, Hkv, scale=0.0, what=""):
         bad = ((g - lse).abs() / ltol)[fin]
         assert bad.numel() == 0 or bad.max().item() <= 1.0, f"{what}: lse {bad.max().item():.3g}"
     return worst
+
+
+def set_rows(c, b, j, k=None, v=None):
+    """Rows j, j + 1, .. of sequence b of a make_q8 case become the quantised rows of k, v [n, Hkv, D]."""
+    table, page = c["table"].cpu().tolist(), c["page"]
+    for side, x in enumerate((k, v)):
+        if x is None:
+            continue
+        codes, scale = quantise_ref(x, c["fmt"])
+        raw8 = codes.float().to(FORMATS[c["fmt"]][0]).view(torch.uint8)
+        pos = np.arange(j, j + len(x))
+        at, row = torch.tensor(np.array(table[b])[pos // page]), torch.from_numpy(pos % page)
+        c["q8"][side].view(torch.uint8)[at, :, row] = raw8.to(c["q"].device)
+        c["q8"][2 + side][at, :, row] = scale.to(torch.uint8).to(c["q"].device)
+        c["rows"][b][side][j:j + len(x)] = values_ref(codes, scale)
+
+
+def visible(c, b, at, window=0, hidden=None):
+    """Which rows [n, L + n] the tokens of sequence b (the first is token `at`) see."""
+    L, n = c["lens"][b]
+    slot = torch.arange(L + n)
+    if c["anc"] is None:
+        qpos, kpos = torch.arange(L, L + n), slot.clone()
+        see = slot[None] <= qpos[:, None]
+    else:
+        see = torch.ones(n, L + n, dtype=torch.bool)
+        see[:, L:] = False
+        for i in range(n):
+            j = i
+            while j >= 0:
+                see[i, L + j] = True
+                j = c["parents"][b][j]
+        dep = torch.tensor(c["depth"][at:at + n])
+        qpos, kpos = L + dep, slot.clone()
+        kpos[L:] = L + dep
+    if window:
+        see &= qpos[:, None] - kpos[None] < window
+    for j in (hidden or {}).get(b, ()):
+        see[:, j] = False
+    return see
+
+
+def check_seen(got_out, got_lse, c, Hkv, window=0, softcap=0.0, scale=0.0, hidden=None, weighed=False, what=""):
+    """Outputs against 64 bits, held to what each token sees: rows that it does not see have no say in its bound,
+    whatever their size.  As check_attn_q8 has it, with keys exact (a key is held over no other's size), and
+    a probability p_j (at most 2^8 against the running maximum, a row's sum at least 1) times its V row's power of two t_j,
+    which is rounded to fp16, so far below what it is held over to a multiple of 2^-24, 2^-25 off:
+    - rows within 2^8 of one another are held over one power of two, at most 2^9 of the token's own largest row,
+      and p over 2^-6, so that is 2^-31 2^9 = 2^-22 of the largest |v| a row;
+    - else (`weighed`) p_j 2^t_j is held over the largest of the token's: that is 2^-31, times 2 for a power of two that is
+      rounded up, 2 for a row's largest value above half of what its scale can hold and 2 for probabilities rounded up
+      alike: 2^-28 of the largest p_j |v_j|."""
+    Hq, D = c["q"].shape[1:]
+    scale = scale or D**-0.5
+    u = torch.finfo(got_out.dtype).eps / 2
+    heads = torch.arange(Hq) // (Hq // Hkv)
+    at, worst = 0, 0.0
+    for b, (L, n) in enumerate(c["lens"]):
+        if n == 0:
+            continue
+        see = visible(c, b, at, window, hidden)
+        kh, vh = (r.double()[:, heads].transpose(0, 1) for r in c["rows"][b])
+        q = c["q"][at:at + n].cpu().double().transpose(0, 1)
+        x = scale * q @ kh.transpose(1, 2)
+        mag = (see * (scale * q.abs() @ kh.abs().transpose(1, 2))).amax(2)
+        if softcap:
+            x = softcap * torch.tanh(x / softcap)
+        x = torch.where(see, x, torch.full_like(x, -float("inf")))
+        lse = torch.logsumexp(x, 2)
+        p = torch.exp(x - torch.where(torch.isfinite(lse), lse, torch.zeros_like(lse))[..., None])
+        out, spread = p @ vh, p @ vh.abs()
+        top = torch.where(see, x.abs(), torch.zeros_like(x)).amax(2)
+        xerr = (2.0**-23 * ((D + 4) * mag + 4 * torch.minimum(top, 2 * mag + 40) + 8 * softcap)
+                + scale * 2.0**-25 * q.abs().amax(2) * (see * kh.abs().sum(2)[:, None]).amax(2))
+        vmax = vh.abs().amax(2)[:, None]
+        far = see.sum(1) * (2.0**-28 * (p * vmax).amax(2) if weighed else 2.0**-22 * (see * vmax).amax(2))
+        tol = (spread * (2.0**-11 + 2 * xerr[..., None] + 2.0**-19) + far[..., None]
+               + u * (out.abs() + 2.0**-11 * spread) + 1e-30)
+        if got_out.dtype == torch.float16:
+            tol = tol + 2.0**-25
+        got = got_out[at:at + n].cpu().double().transpose(0, 1)
+        assert torch.isfinite(got).all(), f"{what}: non-finite output"
+        worst = max(worst, ((got - out).abs() / tol).max().item())
+        assert worst <= 1.0, f"{what}: output {worst:.3g} of its tolerance"
+        fin = torch.isfinite(lse)
+        g = got_lse[at:at + n].cpu().double().T
+        assert torch.equal(fin, torch.isfinite(g)), f"{what}: lse finiteness"
+        ltol = 2 * xerr + 2.0**-21 + 2.0**-21 * torch.where(fin, lse.abs(), torch.zeros_like(lse))
+        bad = ((g - lse).abs() / ltol)[fin]
+        assert bad.numel() == 0 or bad.max().item() <= 1.0, f"{what}: lse {bad.max().item():.3g}"
+        at += n
+    return worst

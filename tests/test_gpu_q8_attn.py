@@ -9,7 +9,7 @@ import torch
 
 from _gpu_util import i32, np_
 from _paged_util import attn_ref
-from _q8_util import cache, check_attn_q8, make_q8, quantise_ref, raw, values_ref
+from _q8_util import cache, check_attn_q8, check_seen, make_q8, quantise_ref, raw, set_rows, values_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -470,3 +470,69 @@ def test_steps_of_a_serving_loop(tv, fmt, N):
     for i, got in enumerate((k, v)):
         assert torch.equal(got.cpu().double(), torch.cat([s[i] for s in kept]))
     assert raw(q8[0]).numel() == pool * Hkv * page * D
+
+
+ZERO_LENS = [([(300, 1), (40, 1)], False), ([(300, 60), (0, 40)], False), ([(190, 60), (5, 40)], True),
+             ([(1500, 40)], False)]
+
+
+@pytest.mark.parametrize("lens,tree", ZERO_LENS)
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", "bf16"), ("int8", "bf16"), ("e4m3", "fp16")])
+@pytest.mark.parametrize("kw", [{}, dict(window=33), dict(softcap=7.0)])
+def test_zero_and_tiny_rows(tv, lens, tree, fmt, dtype, kw):
+    """Queries of zeros and tiny ones, keys of zeros, small ones and both: scores of 0, no less finite for that."""
+    for zero_q, zero_k, size in ((True, False, 1.0), (False, True, 1.0), (True, True, 1.0), (True, False, 2.0**-30),
+                                 (False, True, 2.0**-22)):
+        c = make_q8(7, lens, 8, 2, 128, 16, fmt, dtype, tree=tree)
+        c["q"] = c["q"].clone() * (size if not zero_q else 1.0)
+        if zero_q:
+            c["q"][::2] = 0
+        for b, (L, n) in enumerate(lens):
+            if zero_k:  # (whole tiles of them, and the new tokens)
+                set_rows(c, b, 0, k=torch.zeros(min(L + n, 256), 2, 128))
+                set_rows(c, b, L, k=torch.zeros(n, 2, 128))
+            elif size != 1.0:
+                set_rows(c, b, 0, k=c["rows"][b][0] * size)
+        out, lse, status = run(tv, c, **kw)
+        assert not any(status)
+        check_seen(out, lse, c, 2, what=f"{zero_q} {zero_k} {size}", **kw)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_tiny_queries_beside_pages_that_are_none(tv, new):
+    c = make_q8(3, [(600, new), (300, new)], 8, 2, 128, 128, "e4m3")
+    c["q"] = c["q"].clone() * 2.0**-22
+    c["q"][::3] = 0
+    c["table"][0, 1] = -5
+    hidden = {0: set(range(128, 256))}
+    out, lse, status = run(tv, c)
+    assert status == [1, 0]
+    check_seen(out, lse, c, 2, hidden=hidden)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("scale_byte", [0, 1])
+def test_a_call_on_zeros_gives_the_mean_of_v(tv, new, scale_byte):
+    c = make_q8(3, [(300, new), (0, new)], 8, 2, 64, 16, "int8")
+    c["q"] = torch.zeros_like(c["q"])
+    c["q8"][0].view(torch.uint8).zero_()
+    c["q8"][2].fill_(scale_byte)
+    c["rows"] = [(torch.zeros_like(k), v) for k, v in c["rows"]]
+    out, lse, status = run(tv, c)
+    assert status == [0, 0]
+    check_seen(out, lse, c, 2)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_large_rows_at_right_angles(tv, new):
+    """Products of 0 between rows whose sizes' product is past the 32-bit range are scores of 0."""
+    c = make_q8(3, [(300, new)], 8, 2, 128, 16, "e4m3")
+    c["q"] = torch.zeros_like(c["q"])
+    c["q"][..., 0] = 2.0**100
+    k = torch.zeros(300 + new, 2, 128)
+    k[..., 1] = 2.0**60
+    set_rows(c, 0, 0, k=k)
+    out, lse, status = run(tv, c)
+    assert not any(status)
+    same = dict(c, q=torch.zeros_like(c["q"]))  # (what a score may be off by goes by the sizes: none here)
+    check_seen(out, lse, same, 2)
