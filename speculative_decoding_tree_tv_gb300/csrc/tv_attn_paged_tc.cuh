@@ -248,8 +248,8 @@ __device__ __forceinline__ void convert_rows(uint8_t* tile, const int (&e)[kUnit
   uint8_t *first = row + ((ch ^ sw) << 4), *second = row + (((ch + 1) ^ sw) << 4);
 #pragma unroll
   for (int i = 0; i < kUnits<D>; ++i) {
-    // (a row that is no number, s = 255: infinity, which its codes of 0 make NaN)
-    const float f32 = __int_as_float(min(max(e[i], 0), 255) << 23);
+    // (255, a row that is no number: infinity, which its codes of 0 make NaN)
+    const float f32 = __int_as_float(e[i] << 23);
     const __half2 f = __floats2half2_rn(f32, f32);
     const __half2 g = E4M3 ? f : __hmul2(f, __half2half2(__ushort_as_half(0xe480)));  // (-1152)
     uint32_t o[8];
@@ -416,7 +416,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             load_raw<D>(tile, ctid, row0, x);
             int e[kUnits<D>];  // exponents of the rows' factors, as floats have them
 #pragma unroll
-            for (int i = 0; i < kUnits<D>; ++i) e[i] = scale[row0 + unit_row<D>(ctid) + i * kRowStep<D>] + 127 - over;
+            for (int i = 0; i < kUnits<D>; ++i) {
+              const int s = scale[row0 + unit_row<D>(ctid) + i * kRowStep<D>];
+              e[i] = s == q8::kNaN ? 255 : min(max(s + 127 - over, 0), 254);
+            }
             // (the pass's codes are in registers before their place is written; a warp that gave up joins the others here)
             ok = all_threads<2, kConvertThreads>(landed);
             if (!ok) break;

@@ -536,3 +536,26 @@ def test_large_rows_at_right_angles(tv, new):
     assert not any(status)
     same = dict(c, q=torch.zeros_like(c["q"]))  # (what a score may be off by goes by the sizes: none here)
     check_seen(out, lse, same, 2)
+
+
+@pytest.mark.parametrize("lens", [[(90, 1), (300, 1)], [(70, 30), (300, 40)]])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_a_key_that_is_no_number_beside_the_largest_ones(tv, lens, fmt):
+    """Tokens that see it get NaN, whatever the size of the keys beside it."""
+    c = make_q8(4, lens, 8, 2, 128, 16, fmt, spread=0.5, q_mag=2.0**-118)
+    c["q8"][2].copy_((c["q8"][2].int() + 122).clamp(0, 247).to(torch.uint8))
+    c["rows"] = [(k * 2.0**122, v) for k, v in c["rows"]]
+    out, lse, status = run(tv, c)
+    assert not any(status)
+    check_seen(out, lse, c, 2)
+    want, sees = (out, lse), []
+    table = np_(c["table"])
+    for b, (L, n) in enumerate(lens):
+        j = L + n // 2
+        c["q8"][0].view(torch.uint8)[table[b, j // 16], :, j % 16] = 0
+        c["q8"][2][table[b, j // 16], :, j % 16] = 255
+        sees += [L + i >= j for i in range(n)]
+    out, lse, status = run(tv, c)
+    sees = torch.tensor(sees, device="cuda:0")
+    assert not any(status) and bool(out[sees].isnan().all()) and bool(lse[sees].isnan().all())
+    assert torch.equal(lse[~sees], want[1][~sees]) and same_bits(out[~sees], want[0][~sees])
