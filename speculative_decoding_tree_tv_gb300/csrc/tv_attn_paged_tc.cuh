@@ -159,7 +159,7 @@ template <int D>
 constexpr int kUnits = kTcKeys / kPasses * (D / 16) / kConvertThreads;
 template <int D>
 constexpr int kRowStep = kConvertThreads / (D / 16);
-constexpr float kTcPBias = 6.0f;
+constexpr int kTcPBias = 6;
 
 // Registers of the threads of a warpgroup (Q8 kernels alone).
 template <bool MORE, int N, bool Q8>
@@ -182,6 +182,8 @@ __device__ __forceinline__ void load_raw(const uint8_t* tile, int ctid, int row0
 #pragma unroll
   for (int i = 0; i < kUnits<D>; ++i) x[i] = raw[i * kConvertThreads];
 }
+// 2^e of a whole number, as far as normal 32-bit floats reach.
+__device__ __forceinline__ float exp2_whole(int e) { return __int_as_float(min(max(e + 127, 1), 254) << 23); }
 // Whether a predicate holds in all threads of a named barrier, which they all come to.
 template <int ID, int THREADS>
 __device__ __forceinline__ bool all_threads(bool good) {
@@ -1021,7 +1023,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           }
         }
         // (nothing seen yet: 2^-inf = 0; an fp16 P reaches up to 2^14 and six bits further down)
-        const float mm = (m_run == -INFINITY ? 0.0f : m_run) - (Q8 ? kTcPBias : 0.0f);
+        const float mm = (m_run == -INFINITY ? 0.0f : m_run) - (Q8 ? (float)kTcPBias : 0.0f);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           // (rounded to the cache's type, the product's operand: half a step, 2^-8 or 2^-11 of a
@@ -1053,9 +1055,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const bool mine = tl < nb && tile_tok < w.ntok;
       const size_t oidx = (size_t)(w.s.t0 + w.first + tile_tok) * p.Hq + w.kvh * p.G + h_in;
       const int crow = rb * kRB + row;
-      // (8-bit cache) O's own power of two; the sums are held over the maximum less the bias
-      const float vf = Q8 ? __int_as_float(vnan ? 0x7fffffff : max(vexp, 1) << 23) : 1.0f;
-      if (Q8) m_run -= kTcPBias;
+      // (8-bit cache) O's own power of two less the bias, which the sums have too, as two factors: O times one
+      // of them may leave the 32-bit range where the result does not
+      const int ve = max(vexp, 0) - 127 - kTcPBias;
+      const float v1 = Q8 && vnan ? __int_as_float(0x7fffffff) : exp2_whole(ve >> 1), v2 = exp2_whole(ve - (ve >> 1));
+      if (Q8) l_run *= exp2_whole(-kTcPBias);
       const bool leaves = w.slot >= 0 && (p.merge || w.parts == 0);  // rows for another to join
       float4* part = reinterpret_cast<float4*>(p.part) + crow;       // [slot][D / 4][256]
       if (leaves) {
@@ -1069,8 +1073,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
             for (int q = 0; q < 8; ++q)
               part[((size_t)w.slot * (D / 4) + 8 * c + q) * 256] =
-                  Q8 ? make_float4(__uint_as_float(o[4 * q]) * vf, __uint_as_float(o[4 * q + 1]) * vf,
-                                   __uint_as_float(o[4 * q + 2]) * vf, __uint_as_float(o[4 * q + 3]) * vf)
+                  Q8 ? make_float4(__uint_as_float(o[4 * q]) * v1 * v2, __uint_as_float(o[4 * q + 1]) * v1 * v2,
+                                   __uint_as_float(o[4 * q + 2]) * v1 * v2, __uint_as_float(o[4 * q + 3]) * v1 * v2)
                      : make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
                                    __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
           __syncwarp();
@@ -1091,8 +1095,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           m_all = top;
         }
         if (!ok) break;
-        const float f0 = m_run == -INFINITY ? 0.0f : ex2(m_run - m_all);
-        const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+        const float f0 = (m_run == -INFINITY ? 0.0f : ex2(m_run - m_all)) * (Q8 ? v2 : 1.0f);
+        const float by_sum = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+        // (8-bit cache: rows that are joined take v2 with f0, others the sum first)
+        const float first = more ? v1 : v1 * by_sum, inv = Q8 && !more ? v2 : by_sum;
         uint8_t* orow = reinterpret_cast<uint8_t*>(p.out + oidx * D);
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
@@ -1102,7 +1108,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           tmem_wait_ld();
           if (Q8 && mine) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = __float_as_uint(__uint_as_float(o[e >> 5][e & 31]) * vf);
+            for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = __float_as_uint(__uint_as_float(o[e >> 5][e & 31]) * first);
           }
           if (more && mine) {
 #pragma unroll

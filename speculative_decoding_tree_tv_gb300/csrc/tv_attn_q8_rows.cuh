@@ -86,6 +86,11 @@ __device__ __forceinline__ uint32_t pack16(int f16, float lo, float hi) {
   return f16 ? pack2<true>(lo, hi) : pack2<false>(lo, hi);
 }
 
+// A row's sum with that of a warp's (maximum, sum) on top (a NaN stays: maxima leave it out, sums do not).
+__device__ __forceinline__ float row_sum(float2 v, float top, float sum) {
+  return fmaf(v.x == -INFINITY ? 0.0f : ex2(v.x - top), v.y, sum);
+}
+
 // NR: the most rows of a unit.  16: S = Q K^T and O = P V.  8: S^T = K Q^T and O^T = V^T P^T, keys and
 // dims in the mma's 16 and rows in its 8.
 template <int D, bool E4M3, bool MOD, int NW, int NR>
@@ -507,24 +512,26 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     const float vf = __int_as_float(max(ve, 1) << 23), vf2 = ve < 1 ? __int_as_float((126 + ve) << 23) : 1.0f;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      float mm = -INFINITY;
+      float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
       for (int x = 0; x < NW; ++x) mm = fmaxf(mm, s_ml[x][row_of(r)].x);
       f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mm) * vf2;  // (0: nothing seen by this warp, its sums are 0)
+      // (a whole unit's rows are divided by their sums ahead of vf: their own sums may pass the 32-bit range)
+      if (w.slot < 0) {
+#pragma unroll
+        for (int x = 0; x < NW; ++x) ll = row_sum(s_ml[x][row_of(r)], mm, ll);
+        f[r] *= ll == 0.0f ? 0.0f : 1.0f / ll;
+      }
     }
     const int row = (tid >> 3) & (NR - 1), od = (tid & 7) * 4;  // this thread's row and dims of a joined piece
     float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
     for (int x = 0; x < NW; ++x) mm = fmaxf(mm, s_ml[x][row].x);
 #pragma unroll
-    for (int x = 0; x < NW; ++x) {
-      const float2 v = s_ml[x][row];
-      ll = fmaf(v.x == -INFINITY ? 0.0f : ex2(v.x - mm), v.y, ll);  // (a NaN stays: maxima leave it out, sums do not)
-    }
+    for (int x = 0; x < NW; ++x) ll = row_sum(s_ml[x][row], mm, ll);
     const bool mine = tid < 8 * NR && row < rows;
     const int out_tok = w.s.t0 + w.first + row / p.G, h = w.kvh * p.G + row % p.G;
     const size_t oidx = (size_t)out_tok * p.Hq + h;
-    const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
     auto swz = [](int r) { return NR == 16 ? (r & 1) << 4 : ((r & 6) << 2) | ((r & 1) << 2); };
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) {
@@ -560,7 +567,7 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           *reinterpret_cast<float4*>(p.part + ((size_t)w.slot * kUnitRows + row) * D + 32 * d + od) = a;
         else if (TV_CHECK(out_tok < p.T && h < p.Hq))
           *reinterpret_cast<uint2*>(p.out + oidx * D + 32 * d + od) =
-              make_uint2(pack16(p.f16, a.x * inv, a.y * inv), pack16(p.f16, a.z * inv, a.w * inv));
+              make_uint2(pack16(p.f16, a.x, a.y), pack16(p.f16, a.z, a.w));
       }
       named_sync(1, NW * 32);
     }

@@ -559,3 +559,19 @@ def test_a_key_that_is_no_number_beside_the_largest_ones(tv, lens, fmt):
     sees = torch.tensor(sees, device="cuda:0")
     assert not any(status) and bool(out[sees].isnan().all()) and bool(lse[sees].isnan().all())
     assert torch.equal(lse[~sees], want[1][~sees]) and same_bits(out[~sees], want[0][~sees])
+
+
+@pytest.mark.parametrize("lens", [[(0, 1), (2, 1), (6, 1)], [(0, 20)], [(3, 30), (0, 40)]])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_values_up_to_the_largest_bf16_number(tv, lens, fmt):
+    """Means of values near 2^128, which are bf16 numbers, are finite."""
+    c = make_q8(6, lens, 8, 2, 64, 16, fmt)
+    g = torch.Generator().manual_seed(3)
+    for b, (L, n) in enumerate(lens):
+        big = (1.0 + 0.9 * torch.rand(L + n, 2, 64, generator=g)) * 2.0**127
+        big[..., ::3] *= -0.5
+        set_rows(c, b, 0, v=big.bfloat16())
+        assert bool((c["rows"][b][1].abs() < 2.0**128).all())
+    out, lse, status = run(tv, c)
+    assert not any(status)
+    check_seen(out, lse, c, 2)
