@@ -91,6 +91,16 @@ struct Row {
   int pos;
 };
 
+// Row of token i (of the sequence) of a part; `shared`: of a prefix, whose rows are several sequences', behind all keys.
+__device__ __forceinline__ Row row_of(const PagedAttnParams& p, const Part& w, int i, bool shared) {
+  Row r;
+  r.anc = p.anc && !shared ? p.anc + (size_t)(w.s.t0 + i) * p.W : nullptr;
+  r.pos = shared ? prefix_pos(p, w.b, w.s.t0 + i, w.s.L) : w.s.L + (p.anc ? anc_depth(r.anc, p.W) : i);
+  r.limit = shared || p.anc ? w.s.L : w.s.L + i + 1;
+  r.from = p.window > 0 ? r.pos - p.window + 1 : 0;
+  return r;
+}
+
 // The row's mask for keys j .. j + 31.
 __device__ __forceinline__ uint32_t tree32(const PagedAttnParams& p, const Row& r, int j, int L, int hi) {
   const int x = j - L;  // tree index of the first key
@@ -182,8 +192,6 @@ __device__ __forceinline__ void load_raw(const uint8_t* tile, int ctid, int row0
 #pragma unroll
   for (int i = 0; i < kUnits<D>; ++i) x[i] = raw[i * kConvertThreads];
 }
-// 2^e of a whole number, as far as normal 32-bit floats reach.
-__device__ __forceinline__ float exp2_whole(int e) { return __int_as_float(min(max(e + 127, 1), 254) << 23); }
 // Whether a predicate holds in all threads of a named barrier, which they all come to.
 template <int ID, int THREADS>
 __device__ __forceinline__ bool all_threads(bool good) {
@@ -195,21 +203,26 @@ __device__ __forceinline__ bool all_threads(bool good) {
       : "memory");
   return all != 0;
 }
-// The largest scale byte of rows z0 .. z1 - 1 that are numbers, at least 1, and which of a lane's four rows (bytes
-// 0xff) are not (by a whole warp).
-__device__ __forceinline__ int scale_top(const uint8_t* scale, int z0, int z1, uint32_t& nan4) {
+// The largest and the smallest scale byte of rows z0 .. z1 - 1 that are numbers (0 and 255 if none is), and which of a
+// lane's four rows (bytes 0xff) are not (by a whole warp).
+__device__ __forceinline__ int2 scale_range(const uint8_t* scale, int z0, int z1, uint32_t& nan4) {
   const int r = (threadIdx.x & 31) * 4;
-  uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + r);
+  const uint32_t s4 = *reinterpret_cast<const uint32_t*>(scale + r);
+  uint32_t out4 = 0;
   if (z0 > 0 || z1 < kTcKeys)
-    s4 &= (r >= z0 && r < z1 ? 0xffu : 0u) | (r + 1 >= z0 && r + 1 < z1 ? 0xff00u : 0u) |
-          (r + 2 >= z0 && r + 2 < z1 ? 0xff0000u : 0u) | (r + 3 >= z0 && r + 3 < z1 ? 0xff000000u : 0u);
-  nan4 = __vcmpeq4(s4, 0xffffffffu);
-  s4 &= ~nan4;
-  s4 = __vmaxu4(s4, s4 >> 16);
-  return __reduce_max_sync(0xffffffffu, max(max(s4 & 255u, (s4 >> 8) & 255u), 1u));
+    out4 = (r >= z0 && r < z1 ? 0u : 0xffu) | (r + 1 >= z0 && r + 1 < z1 ? 0u : 0xff00u) |
+           (r + 2 >= z0 && r + 2 < z1 ? 0u : 0xff0000u) | (r + 3 >= z0 && r + 3 < z1 ? 0u : 0xff000000u);
+  nan4 = __vcmpeq4(s4, 0xffffffffu) & ~out4;
+  out4 |= nan4;
+  const uint32_t hi = __vmaxu4(s4 & ~out4, (s4 & ~out4) >> 16), lo = __vminu4(s4 | out4, (s4 | out4) >> 16);
+  return make_int2(__reduce_max_sync(0xffffffffu, max(hi & 255u, (hi >> 8) & 255u)),
+                   __reduce_min_sync(0xffffffffu, min(lo & 255u, (lo >> 8) & 255u)));
 }
 // Notes the rows that are no numbers, if there is one (by a whole warp).
 constexpr int kHasNaN = 1 << 16;
+// Or that the rows are too far apart to be held over one power of two: their codes go on as they are, and a row of
+// the unit takes their powers of two itself (apart_tile).  K rows of up to 15 apart lose no bit in fp16.
+constexpr int kApart = 1 << 17, kExpMask = 0xffff, kKeysNear = 15;
 __device__ __forceinline__ bool note_nan_rows(uint32_t nan4, volatile uint32_t (&words)[4]) {
   if (!__any_sync(0xffffffffu, nan4 != 0)) return false;
   const int lane = threadIdx.x & 31;
@@ -303,6 +316,159 @@ __device__ __forceinline__ float as_halves(uint8_t* block, int row) {
   return __int_as_float(e << 23);
 }
 
+// What an 8-bit cache's tiles are held over, and their scales (K's outlive their stage).
+template <bool Q8>
+struct Held {
+  __align__(16) uint8_t kscale[Q8 ? kExpRing : 1][kTcKeys];
+  uint8_t vscale[Q8 ? kVStages : 1][kTcKeys];
+  volatile int kexp[Q8 ? kExpRing : 1], vexp[Q8 ? kExpRing : 1];  // a scale byte, kHasNaN, kApart
+  volatile uint32_t vnan[Q8 ? kExpRing : 1][4];                   // keys whose V row is no number, where vexp says so
+};
+
+// A row's tile of an 8-bit cache whose K or V rows are far apart: a key's power of two goes on its score, a V row's on its
+// probability, and O is held over the row's largest p_j 2^t_j.  Otherwise as the loop of paged_tc_kernel, bit for bit
+// where sums and maxima are concerned.  By a whole warp, 32 keys at a time through TMEM.  A function, and called from a loop
+// of its own behind that one: in it the tiles that need none of this pay for it (16 trees of 64 104 us, 106 to 109 with the
+// call there, 119 with its code there; 103 without any).
+struct ApartRow {
+  float m_run, l_run;
+  int vexp, vnan;
+};
+template <int D, bool CAP, bool BIAS>
+__device__ __noinline__ ApartRow apart_tile(const PagedAttnParams& p, const Part& w, const Held<true>& held,
+                                            uint64_t* p_full, int nb, int t, uint32_t kt, uint32_t bad, uint32_t tmem,
+                                            float qf, ApartRow a) {
+  const int rb = threadIdx.x >> 7, row = threadIdx.x & (kRB - 1), tl = row / p.G;
+  const uint32_t lane_base = (uint32_t)(((threadIdx.x >> 5) & 3) * 32) << 16;
+  const uint32_t tS = tmem + 128 * rb + lane_base, tO = tmem + 256 + 128 * rb + lane_base;
+  const int j0 = (w.end - 1 - t) * kTcKeys, L = w.s.L, lo = w.lo, hi = w.hi;
+  const Row r = row_of(p, w, w.first + min(rb * nb + min(tl, nb - 1), w.ntok - 1), false);
+  const float slope = (BIAS && p.slopes) ? __ldg(p.slopes + w.kvh * p.G + row % p.G) * kLog2e : 0.0f;
+  const int k_held = held.kexp[kt % kExpRing], v_held = held.vexp[kt % kExpRing];
+  const uint8_t *ks = held.kscale[kt % kExpRing], *vs = held.vscale[kt % kVStages];
+  const bool k_apart = k_held & kApart, v_apart = v_held & kApart;
+  const float kf = fminf(qf * __int_as_float((k_held & kExpMask) << 23), FLT_MAX);  // (0 where K is apart)
+  auto key_factor = [&](int j) { return k_apart ? fminf(qf * q8::factor(ks[j]), FLT_MAX) : kf; };
+  const float in_scale = CAP ? 1.0f : k_apart ? p.scale_log2 : fminf(fmaxf(p.scale_log2 * kf, FLT_MIN), FLT_MAX);
+  const float scale = (BIAS && p.slopes) ? 1.0f : in_scale;
+  uint32_t x[32];
+  bool far = false;
+  if (CAP) {
+    float top = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      tmem_ld32(tS + 32 * c, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const int j = 32 * c + e;
+        const float y = __uint_as_float(x[e]) * key_factor(j);
+        if (j0 + j >= lo && j0 + j < hi) top = fmaxf(top, y * y);
+      }
+    }
+    far = __any_sync(0xffffffffu, top > p.cap_top && tl < nb && rb * nb + tl < w.ntok);
+  }
+  float tmax = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int j = j0 + 32 * c;
+    uint32_t v = see32(p, r, j, L, hi);
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      if ((bad >> (4 * c + g)) & 1u) v &= ~(0xffu << (8 * g));
+    tmem_ld32(tS + 32 * c, x);
+    tmem_wait_ld();
+    if (CAP || k_apart) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        float s = __uint_as_float(x[e]) * key_factor(32 * c + e);
+        if (CAP && far) s = p.softcap_log2 * tanh_any(s * (2.0f * kLog2e * p.cap_in));
+        else if (CAP) {
+          const float y = s * s;
+          s *= fmaf(fmaf(fmaf(p.cap_q[3], y, p.cap_q[2]), y, p.cap_q[1]), y, p.cap_q[0]);
+        }
+        x[e] = __float_as_uint(s);
+      }
+    }
+    if (BIAS && r.anc && j0 + kTcKeys > L)
+      tree_chunk(p, r, j, L, hi, in_scale, slope, v, x);
+    else if (BIAS && p.slopes)
+      bias_chunk(fmaf(slope, 32.0f * c, slope * (float)(j0 - r.pos)), slope, in_scale, x);
+    if ((v_held & kHasNaN) && (v & held.vnan[kt % kExpRing][c])) a.vnan = 1;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      if (!((v >> e) & 1u)) x[e] = __float_as_uint(-INFINITY);
+      tmax = fmaxf(tmax, __uint_as_float(x[e]));
+    }
+    tmem_st32(tS + 32 * c, x);
+  }
+  tmem_wait_st();
+  tmax *= scale;
+  // (scores so large that a rounding of the maximum is a power of two or more: see paged_tc_kernel)
+  const bool big = !CAP && __any_sync(0xffffffffu, fabsf(tmax) > 0x1p22f && fabsf(tmax) < INFINITY);
+  auto score = [&](uint32_t y) { return big ? __fmul_rn(__uint_as_float(y), scale) : __uint_as_float(y); };
+  const float sc = big ? 1.0f : scale;
+  const bool moves = a.m_run == -INFINITY || tmax > a.m_run + kRescaleLog2, fresh = a.m_run == -INFINITY;
+  const float m_new = moves ? tmax : a.m_run, nm = m_new == -INFINITY ? 0.0f : -m_new;
+  int vexp = v_held & kExpMask;
+  if (v_apart) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      tmem_ld32(tS + 32 * c, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) top = fmaxf(top, fmaf(score(x[e]), sc, nm) + (float)vs[32 * c + e]);
+    }
+    vexp = q8::held_over(a.vexp, top > -INFINITY ? (int)ceilf(fminf(fmaxf(top, -1e4f), 1e4f)) : q8::kNone,
+                         m_new - a.m_run, fresh);
+  }
+  const float corr = moves && !fresh ? ex2(a.m_run - m_new) : 1.0f;
+  a.l_run *= corr;
+  if (t > 0 && __any_sync(0xffffffffu, moves || vexp != a.vexp)) {
+    // (the two powers of two may each be past the 32-bit range; O of a fresh row is 0)
+    const float o_corr = moves && !fresh ? ex2(a.m_run - m_new + (float)(a.vexp - vexp)) : q8::exp2_whole(a.vexp - vexp);
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      tmem_ld32(tO + c, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * o_corr);
+      tmem_st32(tO + c, x);
+    }
+  }
+  a.m_run = m_new;
+  a.vexp = vexp;
+  const float mm = (m_new == -INFINITY ? 0.0f : m_new) - (float)kTcPBias;
+  const float2 sc2 = make_float2(sc, sc), nm2 = make_float2(-mm, -mm);
+  float2 ps[4] = {};
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    tmem_ld32(tS + 32 * c, x);
+    tmem_wait_ld();
+    uint32_t pw[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float2 y = ffma2(make_float2(score(x[2 * e]), score(x[2 * e + 1])), sc2, nm2);
+      const float2 f = make_float2(ex2(y.x), ex2(y.y));
+      ps[e & 3] = fadd2(ps[e & 3], f);
+      const int j = 32 * c + 2 * e;
+      pw[e] = pack2<true>(v_apart ? q8::times_exp2(f.x, vs[j] - vexp) : f.x,
+                          v_apart ? q8::times_exp2(f.y, vs[j + 1] - vexp) : f.y);
+    }
+    tmem_st16(tS + 16 * c, pw);
+    if (c & 1) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&p_full[c >> 1]);
+    }
+  }
+  const float2 pa = fadd2(fadd2(ps[0], ps[1]), fadd2(ps[2], ps[3]));
+  a.l_run += pa.x + pa.y;
+  return a;
+}
+
 // CAP: a softcap; BIAS: slopes, or tree distances that the window reaches.  Variants of
 // their own, and rolled loops wherever a warp does not wait for them: a loop over the tiles that is
 // larger than the instruction cache (some 32 KB) runs at half the speed.
@@ -314,7 +480,7 @@ __device__ __forceinline__ float as_halves(uint8_t* block, int row) {
 template <int D, bool F16, bool CAP, bool BIAS, bool PRE, bool Q8>
 __global__ void __launch_bounds__(Q8 ? kTcThreads + kConvertThreads : kTcThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                const __grid_constant__ CUtensorMap tmV, const PagedAttnParams p, const int nb) {
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PagedAttnParams p, const int nb) {
   using Lay = TcLayout<D>;
   constexpr int A = Lay::A;
   constexpr uint32_t kTmemCols = 512, kOCol = 256;
@@ -335,14 +501,15 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_bad_pages[kBadRing];  // bit g: keys 8 g .. 8 g + 7 have no page
   __shared__ volatile int s_abort;
-  // (8-bit cache) raw tiles have landed; their scales have been looked at; scales; the powers of two that a tile's K
-  // and V are held over
+  // (8-bit cache) raw tiles have landed; their scales have been looked at
   __shared__ __align__(8) uint64_t bar_q_raw;  // (bf16 queries, ahead of as_halves)
   __shared__ __align__(8) uint64_t bar_k_raw[Q8 ? kKStages : 1], bar_v_raw[Q8 ? kVStages : 1];
   __shared__ __align__(8) uint64_t bar_k_scale[Q8 ? kKStages : 1], bar_v_scale[Q8 ? kVStages : 1];
-  __shared__ __align__(16) uint8_t s_kscale[Q8 ? kKStages : 1][kTcKeys], s_vscale[Q8 ? kVStages : 1][kTcKeys];
-  __shared__ volatile int s_kexp[Q8 ? kExpRing : 1], s_vexp[Q8 ? kExpRing : 1];
-  __shared__ volatile uint32_t s_vnan[Q8 ? kExpRing : 1][4];  // keys whose V row is no number, where s_vexp says so
+  __shared__ Held<Q8> s_held;
+  auto& s_kscale = s_held.kscale;
+  auto& s_vscale = s_held.vscale;
+  auto& s_vnan = s_held.vnan;
+  volatile int *s_kexp = s_held.kexp, *s_vexp = s_held.vexp;
   __shared__ PartRing s_ring;
   __shared__ Cursor<kTcKeys> s_cur;
   __shared__ int s_late;  // the first sequence that a softmax warp gave up in
@@ -409,19 +576,22 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           bool landed = warp_wait((side ? bar_v_scale : bar_k_scale) + (Q8 ? st : 0), ph, p.wait_limit);
           landed = warp_wait((side ? bar_v_raw : bar_k_raw) + (Q8 ? st : 0), ph, p.wait_limit) && landed;  // (it has)
           uint8_t* tile = (side ? sV : sK) + st * Lay::kTile;
-          const uint8_t* scale = side ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0];
-          const int over = (side ? s_vexp : s_kexp)[Q8 ? it % kExpRing : 0] & ~kHasNaN;
+          const uint8_t* scale = side ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? it % kExpRing : 0];
+          const int held = (side ? s_vexp : s_kexp)[Q8 ? it % kExpRing : 0], over = held & kExpMask;
 #pragma unroll 1
           for (int pass = 0; ok && pass < kPasses; ++pass) {
             const int row0 = pass * (kTcKeys / kPasses);
             uint4 x[kUnits<D>];
             load_raw<D>(tile, ctid, row0, x);
-            int e[kUnits<D>];  // exponents of the rows' factors, as floats have them
+            int e[kUnits<D>];  // exponents of the rows' factors, as floats have them (outside of the unit's range: anything)
 #pragma unroll
-            for (int i = 0; i < kUnits<D>; ++i) {
-              const int s = scale[row0 + unit_row<D>(ctid) + i * kRowStep<D>];
-              e[i] = s == q8::kNaN ? 255 : min(max(s + 127 - over, 0), 254);
-            }
+            for (int i = 0; i < kUnits<D>; ++i) e[i] = scale[row0 + unit_row<D>(ctid) + i * kRowStep<D>] + 127 - over;
+            if (held & (kApart | kHasNaN))
+#pragma unroll
+              for (int i = 0; i < kUnits<D>; ++i) {
+                const int s = e[i] - 127 + over;
+                e[i] = s == q8::kNaN ? 255 : held & kApart ? 127 : e[i];
+              }
             // (the pass's codes are in registers before their place is written; a warp that gave up joins the others here)
             ok = all_threads<2, kConvertThreads>(landed);
             if (!ok) break;
@@ -482,20 +652,25 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     };
     // (8-bit cache) The scales of tile j, once it has landed: what its K or V is held over, and V's rows that are no
     // numbers, which are noted and taken for zeros.
-    int vexp = -1;
+    int vexp = -1, vlo = 255, vhi = 0;  // (the part's scales so far lie within vlo .. vhi)
     auto look_at_scales = [&](uint32_t j, int z0, int z1, bool first) {
       const uint32_t st = isV ? j % kVStages : j % kKStages, ph = (isV ? j / kVStages : j / kKStages) & 1;
       if (!warp_wait(&full[st], ph, p.wait_limit)) return false;
-      uint8_t* scale = isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0];
+      uint8_t* scale = isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? j % kExpRing : 0];
       uint32_t nan4;
-      int over = scale_top(scale, z0, z1, nan4);
+      const int2 range = scale_range(scale, z0, z1, nan4);
+      int over = range.x - range.y > kKeysNear ? kApart : max(range.x, 1);
       if (isV) {
-        if (first || over > vexp + 1) vexp = over;
-        over = vexp;
+        vhi = first ? range.x : max(vhi, range.x);
+        vlo = first ? range.y : min(vlo, range.y);
+        if (first || vhi > vexp + 1) vexp = vhi;
+        over = vhi - vlo > q8::kNear ? kApart : vexp;
         if (note_nan_rows(nan4, s_vnan[Q8 ? j % kExpRing : 0])) {
           over |= kHasNaN;
           *reinterpret_cast<uint32_t*>(scale + 4 * lane) &= ~nan4;
         }
+      } else if (__any_sync(0xffffffffu, nan4 != 0)) {
+        over |= kHasNaN;
       }
       if (lane == 0) (isV ? s_vexp : s_kexp)[Q8 ? j % kExpRing : 0] = over;
       __syncwarp();
@@ -530,7 +705,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
               tma_load_rows(ring + st * Lay::kTile + Lay::kTile / 2 + row0 * D, map, &full[st], 0, row, w.kvh, page,
                             p.row_dim, p.head_dim);
             if (lane < 16)
-              load_scales(p, (isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? st : 0]) + row0, isV ? p.v_scale : p.k_scale,
+              load_scales(p, (isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? it % kExpRing : 0]) + row0, isV ? p.v_scale : p.k_scale,
                           page, w.kvh, row);
             cp_arrive(&full[st]);
             ++it;
@@ -800,20 +975,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       // rows past the unit take the last token's mask: computed, never written
       const int i = w.first + min(rb * nb + min(tl, nb - 1), w.ntok - 1);
       const bool warp_works = warp_in_block && rb * nb + (warp & 3) * 32 / p.G < w.ntok;
-      Row r;
-      r.anc = p.anc && !(PRE && w.s.shared) ? p.anc + (size_t)(w.s.t0 + i) * p.W : nullptr;
-      const bool shared = PRE && w.s.shared;  // (its rows are several sequences', behind all of the keys)
-      r.pos = shared ? prefix_pos(p, w.b, w.s.t0 + i, w.s.L) : w.s.L + (p.anc ? anc_depth(r.anc, p.W) : i);
-      r.limit = shared || p.anc ? w.s.L : w.s.L + i + 1;
-      r.from = p.window > 0 ? r.pos - p.window + 1 : 0;
+      const bool shared = PRE && w.s.shared;
+      const Row r = row_of(p, w, i, shared);
       const float slope = (BIAS && p.slopes) ? __ldg(p.slopes + w.kvh * p.G + h_in) * kLog2e : 0.0f;
       // what turns a score into the log2 domain; capped scores are there already, and with
       // slopes it comes with the bias
       const float in_scale0 = CAP ? 1.0f : p.scale_log2;
       float m_run = -INFINITY, l_run = 0.0f;
-      int vexp = -1;  // (8-bit cache) O is held over 2^(vexp - 127)
+      int vexp = -1;  // (8-bit cache) O is held over 2^(vexp - 127); no row yet: -1
       bool vnan = false;  // (8-bit cache) it sees a V row that is no number
-      for (int t = 0; t < T; ++t, ++kt, ++sc) {
+      int t = 0;
+      for (; t < T; ++t, ++kt, ++sc) {
         const int j0 = j_last - t * kTcKeys;
         uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         if (j0 + kTcKeys > r.limit || j0 < r.from) {
@@ -838,7 +1010,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const uint32_t bad = s_bad_pages[kt % kBadRing];
         // (8-bit cache) what the tile's scores are held over, as a 32-bit number: a row of zeros over a tile of tiny
         // keys would make it 0, and hidden keys are at -inf ahead of it; nor is 0 times it to be anything else
-        const float kf = Q8 ? fminf(qf * __int_as_float(max(s_kexp[Q8 ? kt % kExpRing : 0], 1) << 23), FLT_MAX) : 1.0f;
+        const float kf = Q8 ? fminf(qf * __int_as_float((s_kexp[Q8 ? kt % kExpRing : 0] & kExpMask) << 23), FLT_MAX) : 1.0f;
         const float in_scale = CAP ? 1.0f : Q8 ? fminf(fmaxf(in_scale0 * kf, FLT_MIN), FLT_MAX) : in_scale0;
         const float scale = (BIAS && p.slopes) ? 1.0f : in_scale;
         tc_fence_after();
@@ -846,6 +1018,13 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(tS + lane_base + 32 * c, sr[c]);
         tmem_wait_ld();
+        int v_held = 0;
+        if (Q8) {  // (V's scales are known long before, as a rule)
+          ok = warp_wait(&bar_v_scale[Q8 ? kt % kVStages : 0], (kt / kVStages) & 1, p.wait_limit);
+          if (!ok) break;
+          v_held = s_vexp[Q8 ? kt % kExpRing : 0];
+          if ((v_held | s_kexp[Q8 ? kt % kExpRing : 0]) & kApart) break;
+        }
         if (bad) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -991,17 +1170,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const bool moves = m_run == -INFINITY || tmax > m_run + kRescaleLog2;
         bool vmoves = false;
         float vcorr = 1.0f;
-        if (Q8) {  // (V's scales are known; it has landed long before, as a rule)
-          ok = warp_wait(&bar_v_full[kt % kVStages], (kt / kVStages) & 1, p.wait_limit);
-          if (!ok) break;
-          int v = s_vexp[Q8 ? kt % kExpRing : 0];
-          if (v & kHasNaN) {
-            v &= ~kHasNaN;
+        if (Q8) {
+          const int v = v_held & ~kHasNaN;
+          if (v_held & kHasNaN) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) vnan |= (vis[c] & s_vnan[Q8 ? kt % kExpRing : 0][c]) != 0;
           }
           vmoves = vexp >= 0 && v != vexp;
-          if (vmoves) vcorr = v - vexp > 126 ? 0.0f : __int_as_float((127 + vexp - v) << 23);
+          if (vmoves) vcorr = q8::exp2_whole(vexp - v);
           vexp = v;
         }
         if (__any_sync(0xffffffffu, moves) || vmoves) {
@@ -1042,6 +1218,21 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const float2 pa = fadd2(fadd2(ps[0], ps[1]), fadd2(ps[2], ps[3]));
         l_run += pa.x + pa.y;
       }
+      if constexpr (Q8) {  // from the first tile of K or V rows far apart on
+        for (; ok && t < T; ++t, ++kt, ++sc) {
+          ok = warp_wait(&bar_s_full[rb], sc & 1, p.wait_limit) &&
+               warp_wait(&bar_v_scale[kt % kVStages], (kt / kVStages) & 1, p.wait_limit);
+          if (!ok) break;
+          tc_fence_after();
+          const ApartRow a = apart_tile<D, CAP, BIAS>(p, w, s_held, bar_p_full[rb], nb, t, kt, s_bad_pages[kt % kBadRing],
+                                                      tmem, qf, {m_run, l_run, vexp, vnan});
+          m_run = a.m_run;
+          l_run = a.l_run;
+          vexp = a.vexp;
+          vnan = a.vnan;
+          announce();
+        }
+      }
       if (ok) ok = warp_wait(&bar_o_done[rb], oc & 1, p.wait_limit);
       if (!ok) break;
       ++oc;
@@ -1057,9 +1248,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const int crow = rb * kRB + row;
       // (8-bit cache) O's own power of two less the bias, which the sums have too, as two factors: O times one
       // of them may leave the 32-bit range where the result does not
-      const int ve = max(vexp, 0) - 127 - kTcPBias;
-      const float v1 = Q8 && vnan ? __int_as_float(0x7fffffff) : exp2_whole(ve >> 1), v2 = exp2_whole(ve - (ve >> 1));
-      if (Q8) l_run *= exp2_whole(-kTcPBias);
+      const int ve = vexp - 127 - kTcPBias;
+      const float v1 = Q8 && vnan ? __int_as_float(0x7fffffff) : q8::exp2_whole(ve >> 1), v2 = q8::exp2_whole(ve - (ve >> 1));
+      if (Q8) l_run *= q8::exp2_whole(-kTcPBias);
       const bool leaves = w.slot >= 0 && (p.merge || w.parts == 0);  // rows for another to join
       float4* part = reinterpret_cast<float4*>(p.part) + crow;       // [slot][D / 4][256]
       if (leaves) {

@@ -7,8 +7,10 @@
 // them: with q_r = 2^a_r q'_r (a row's largest |q'| in [1, 2)), k_j = 2^s_j k'_j, v_j = 2^t_j v'_j,
 //   x_rj = 2^(a_r + s_j) q'_r . k'_j,   O_r = sum_j (p_rj 2^t_j) v'_j,
 // a score takes its key's factor behind the first product, a probability its row's ahead of the second.
-// p_rj 2^t_j is rounded to fp16 (half a step: 2^-11 of it) as p 2^(t_j - c + 6), c the warp's largest t so far,
-// less one at most: from 2^-20 of the largest on with all its bits, below that to multiples of 2^-30.
+// p_rj 2^t_j is rounded to fp16 (half a step: 2^-11 of it) as p 2^(t_j - c + 6), c about the warp's largest t: from
+// 2^-20 of that on with all its bits, below to multiples of 2^-30.  Where the warp's t differ by more
+// than kNear allows, c is the row's own, that of its largest p_rj 2^t_j: a row that it does not see, or hardly, has no say
+// in its bits.
 //
 // An operand's 16 dims (or rows) are in the order in which the bytes lie: ldmatrix takes byte
 // pairs for 16-bit values, so a lane gets dims 4c .. 4c + 3 of a key, which serve as the mma's k = 2c, 2c + 1,
@@ -267,7 +269,7 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       for (int k = 0; k < kSteps; ++k)
         qf[h][k] = *reinterpret_cast<const uint2*>(s_q + (8 * h + g) * (D * 2) +
                                                    (((2 * k + (c >> 1)) ^ g) << 4) + (c & 1) * 8);
-    int pos[2], tok[2];
+    int ve[2] = {-1, -1}, pos[2], tok[2];  // (ve: the power of two of a row's outputs, where V rows are far apart)
     float slope[2], in_scale[2];
     float m[2], l[2], o[kAcc][4];
 #pragma unroll
@@ -282,7 +284,11 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       m[r] = -INFINITY;
       l[r] = 0.0f;
     }
-    int vtop = -1;  // the outputs are held as O 2^(kPBias + 127 - vtop), vtop from the scale bytes; -1: no row yet
+    // The outputs are held as O 2^(kPBias + 127 - vtop), vtop from the scale bytes (-1: no row yet): one above the first
+    // tile's largest, for tiles from vtop - kNear + 1 to vtop + 1.  From the first that is not on, they are held over a
+    // power of two of each row.
+    int vtop = -1;
+    bool apart = false;
 #pragma unroll
     for (int n = 0; n < kAcc; ++n)
 #pragma unroll
@@ -336,16 +342,15 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
         const bool plain = j0 + kWarpKeys <= all_below && j0 > all_from && j0 >= w.lo && bad8 == 0;
         // the keys' scales: factors of K, bytes of V
         float kf[kAll];
-        int vb[kAll], vmax = 0;
+        int vb[kAll];
+        unsigned off = 0;  // how far the bytes of V are from what the outputs are held over
         const uint8_t* ks = s_ks + st * kQ8Keys + kWarpKeys * warp;
         const uint8_t* vs = s_vs + st * kQ8Keys + kWarpKeys * warp;
 #pragma unroll
         for (int i = 0; i < kAll; ++i) {
-          const int j = j0 + key_of(i);
           kf[i] = q8::factor(ks[key_of(i)]);
           vb[i] = vs[key_of(i)];
-          if (!plain && (j < w.lo || j >= w.hi)) vb[i] = 0;  // (keys outside of the unit's range hold anything)
-          if (vb[i] != q8::kNaN) vmax = max(vmax, vb[i]);
+          off = max(off, (unsigned)(vb[i] - (vtop + 1 - q8::kNear)));
         }
         uint32_t hidden = 0;  // bits by s's index
         // scores in the log2 domain, hidden keys at -inf
@@ -399,7 +404,7 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
             }
           }
         // running maximum (lazily moved), probabilities, sums
-        float corr[2];
+        float corr[2], before[2];
         bool move = false;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -408,6 +413,7 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           for (int i = 1; i < kAll; ++i) mx = fmaxf(mx, s[at(r, i)]);
           mx = reduce(mx, [](float a, float b) { return fmaxf(a, b); });
           corr[r] = 1.0f;
+          before[r] = m[r];
           if (m[r] == -INFINITY) {
             m[r] = mx;
           } else if (mx > m[r] + kRescaleLog2) {
@@ -421,15 +427,43 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
           for (int i = 0; i < kAll; ++i) sum += s[at(r, i)] = ex2(s[at(r, i)] - mm);
           l[r] = fmaf(l[r], corr[r], sum);
         }
-        vmax = __reduce_max_sync(0xffffffffu, vmax);
-        if (vmax > vtop + 1 || vtop < 0) {
-          if (vtop >= 0) {
-            const float f = vmax - vtop > 126 ? 0.0f : __int_as_float((127 + vtop - vmax) << 23);
-            corr[0] *= f;
-            corr[1] *= f;
-            move = true;
+        if (!apart && __any_sync(0xffffffffu, off > q8::kNear)) {
+          // (keys outside of the unit's range hold anything; rows that are no numbers count for none)
+          int lo = 255, hi = -1;
+#pragma unroll
+          for (int i = 0; i < kAll; ++i) {
+            const int j = j0 + key_of(i);
+            if (vb[i] == q8::kNaN || j < w.lo || j >= w.hi) continue;
+            lo = min(lo, vb[i]);
+            hi = max(hi, vb[i]);
           }
-          vtop = vmax;
+          hi = __reduce_max_sync(0xffffffffu, hi);
+          lo = __reduce_min_sync(0xffffffffu, lo);
+          const int top = vtop < 0 ? hi + 1 : vtop;
+          if (hi >= 0 && hi <= top + 1 && lo > top - q8::kNear) {
+            vtop = top;  // (if these are the first rows, the outputs are 0 so far)
+          } else if (hi >= 0) {
+            apart = true;
+            ve[0] = ve[1] = vtop;
+          }
+        }
+        if (apart) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            int want = q8::kNone;
+#pragma unroll
+            for (int i = 0; i < kAll; ++i) {
+              const float x = s[at(r, i)];
+              if (x > 0.0f && vb[i] != q8::kNaN) want = max(want, (__float_as_int(x) >> 23) - 126 + vb[i]);
+            }
+            want = (int)reduce((float)want, [](float a, float b) { return fmaxf(a, b); });
+            const bool fresh = before[r] == -INFINITY;
+            const int e = q8::held_over(ve[r], want, m[r] - before[r], fresh);
+            move |= e != ve[r];
+            // (fresh: outputs of 0)
+            corr[r] = fresh || m[r] == before[r] ? q8::exp2_whole(ve[r] - e) : ex2(before[r] - m[r] + (float)(ve[r] - e));
+            ve[r] = e;
+          }
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -437,14 +471,25 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][e] *= corr[NR == 16 ? e >> 1 : e & 1];
         }
+        if (apart) {
 #pragma unroll
-        for (int i = 0; i < kAll; ++i) {
-          const int e = vb[i] - vtop + 127 + kPBias;
-          const float f = vb[i] == q8::kNaN ? q8::factor(q8::kNaN) : e > 0 ? __int_as_float(e << 23) : 0.0f;
+          for (int i = 0; i < kAll; ++i)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float& x = s[at(r, i)];
-            x = (hidden >> at(r, i)) & 1 ? 0.0f : x * f;  // (a hidden row's scale may say NaN)
+            for (int r = 0; r < 2; ++r) {
+              float& x = s[at(r, i)];
+              const float y = vb[i] == q8::kNaN ? q8::factor(q8::kNaN) : q8::times_exp2(x, vb[i] - ve[r] + kPBias);
+              x = (hidden >> at(r, i)) & 1 ? 0.0f : y;
+            }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kAll; ++i) {
+            // (of a key that no row sees it may be anything)
+            const float f = vb[i] == q8::kNaN ? q8::factor(q8::kNaN) : __int_as_float((vb[i] - vtop + 127 + kPBias) << 23);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float& x = s[at(r, i)];
+              x = (hidden >> at(r, i)) & 1 ? 0.0f : x * f;  // (a hidden row's scale may say NaN)
+            }
           }
         }
 #pragma unroll
@@ -506,16 +551,16 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
     }
     named_sync(1, NW * 32);
     const bool abort = s_abort;
-    float f[2];
-    // (the outputs' own factor is 2^(vtop - 127 - kPBias), in two steps where that is below the floats')
-    const int ve = max(vtop, 0) - kPBias;
-    const float vf = __int_as_float(max(ve, 1) << 23), vf2 = ve < 1 ? __int_as_float((126 + ve) << 23) : 1.0f;
+    float f[2], vf[2];  // (vf: the second of the outputs' own factor's two)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
       for (int x = 0; x < NW; ++x) mm = fmaxf(mm, s_ml[x][row_of(r)].x);
-      f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mm) * vf2;  // (0: nothing seen by this warp, its sums are 0)
+      f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mm) ;  // (0: nothing seen by this warp, its sums are 0)
+      const int e = (apart ? ve[r] : vtop) - 127 - kPBias;
+      f[r] *= q8::exp2_whole(e >> 1);
+      vf[r] = q8::exp2_whole(e - (e >> 1));
       // (a whole unit's rows are divided by their sums ahead of vf: their own sums may pass the 32-bit range)
       if (w.slot < 0) {
 #pragma unroll
@@ -542,14 +587,14 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 #pragma unroll
           for (int r = 0; r < 2; ++r)
             *reinterpret_cast<float4*>(s_acc + (warp * 16 + r * 8 + g) * 32 + ((16 * x + 4 * c) ^ swz(g))) =
-                make_float4(ev[2 * r] * f[r] * vf, odd[2 * r] * f[r] * vf, ev[2 * r + 1] * f[r] * vf,
-                            odd[2 * r + 1] * f[r] * vf);
+                make_float4(ev[2 * r] * f[r] * vf[r], odd[2 * r] * f[r] * vf[r], ev[2 * r + 1] * f[r] * vf[r],
+                            odd[2 * r + 1] * f[r] * vf[r]);
         } else {
           const float(&v)[4] = o[(2 * d + x) % kAcc];
 #pragma unroll
           for (int r = 0; r < 2; ++r)
             *reinterpret_cast<float2*>(s_acc + (warp * 16 + c2 + r) * 32 + ((16 * x + 2 * g) ^ swz(c2 + r))) =
-                make_float2(v[r] * f[r] * vf, v[2 + r] * f[r] * vf);
+                make_float2(v[r] * f[r] * vf[r], v[2 + r] * f[r] * vf[r]);
         }
       }
       named_sync(1, NW * 32);

@@ -59,6 +59,25 @@ __device__ __forceinline__ float factor(int s) {
   return __int_as_float(s == kNaN ? 0x7fffffff : s == 0 ? 0x00400000 : s << 23);  // (0: 2^-127)
 }
 
+// 2^e of a whole number, as far as normal 32-bit floats reach.
+__device__ __forceinline__ float exp2_whole(int e) { return __int_as_float(min(max(e + 127, 1), 254) << 23); }
+// x 2^e, where 2^e alone may be past that.
+__device__ __forceinline__ float times_exp2(float x, int e) { return x * exp2_whole(e >> 1) * exp2_whole(e - (e >> 1)); }
+
+// While the scale bytes t_j of the V rows that a part has met lie within this of one another, all rows of the unit
+// hold their outputs over one power of two.  Beyond it each row has its own, that of its
+// largest p_j 2^t_j so far, so that V rows that it does not see, or hardly, cost it no bits.  Either way
+// p_j 2^t_j, rounded to fp16 times 2^6, is off by 2^-21 of the row's largest p_j |v_j| at most where it is too small for
+// half a step of its own.
+constexpr int kNear = 9;
+// A row's power of two, as a scale byte's: `e` so far, `want` that of the largest p_j 2^t_j at hand (kNone: it sees none),
+// after its maximum went up by `up` (in the log2 domain); `fresh`: it saw nothing before.
+constexpr int kNone = -(1 << 20);
+__device__ __forceinline__ int held_over(int e, int want, float up, bool fresh) {
+  if (!fresh) e -= (int)ceilf(fminf(up, 1e4f));
+  return want > kNone && (fresh || want > e + 8) ? want : e;
+}
+
 // The scale byte of a row whose largest magnitude is `top` (>= 0): the least e >= -126 with
 // top <= M 2^e, M = 448 = 1.75 * 2^8 or 127 = 1.984375 * 2^6, plus 127.
 template <bool E4M3>

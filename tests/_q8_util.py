@@ -176,16 +176,14 @@ def visible(c, b, at, window=0, hidden=None):
     return see
 
 
-def check_seen(got_out, got_lse, c, Hkv, window=0, softcap=0.0, scale=0.0, hidden=None, weighed=False, what=""):
+def check_seen(got_out, got_lse, c, Hkv, window=0, softcap=0.0, scale=0.0, hidden=None, what=""):
     """Outputs against 64 bits, held to what each token sees: rows that it does not see have no say in its bound,
     whatever their size.  As check_attn_q8 has it, with keys exact (a key is held over no other's size), and
-    a probability p_j (at most 2^8 against the running maximum, a row's sum at least 1) times its V row's power of two t_j,
-    which is rounded to fp16, so far below what it is held over to a multiple of 2^-24, 2^-25 off:
-    - rows within 2^8 of one another are held over one power of two, at most 2^9 of the token's own largest row,
-      and p over 2^-6, so that is 2^-31 2^9 = 2^-22 of the largest |v| a row;
-    - else (`weighed`) p_j 2^t_j is held over the largest of the token's: that is 2^-31, times 2 for a power of two that is
-      rounded up, 2 for a row's largest value above half of what its scale can hold and 2 for probabilities rounded up
-      alike: 2^-28 of the largest p_j |v_j|."""
+    p_j 2^t_j, a probability (its row's largest is 1) times its V row's power of two, is rounded to fp16 times 2^6, so
+    far below what it is held over to a multiple of 2^-30 of that, 2^-31 off.  V rows within 2^9 of one another are held over
+    the largest's power of two, so over 2^9 of that of the row whose probability is 1, at most; others over the largest
+    p_j 2^t_j, rounded up.  A row's largest value is above half of what its scale can hold: 2^-21 of the largest p_j |v_j|
+    for each visible row."""
     Hq, D = c["q"].shape[1:]
     scale = scale or D**-0.5
     u = torch.finfo(got_out.dtype).eps / 2
@@ -209,7 +207,7 @@ def check_seen(got_out, got_lse, c, Hkv, window=0, softcap=0.0, scale=0.0, hidde
         xerr = (2.0**-23 * ((D + 4) * mag + 4 * torch.minimum(top, 2 * mag + 40) + 8 * softcap)
                 + scale * 2.0**-25 * q.abs().amax(2) * (see * kh.abs().sum(2)[:, None]).amax(2))
         vmax = vh.abs().amax(2)[:, None]
-        far = see.sum(1) * (2.0**-28 * (p * vmax).amax(2) if weighed else 2.0**-22 * (see * vmax).amax(2))
+        far = see.sum(1) * 2.0**-21 * (p * vmax).amax(2)
         tol = (spread * (2.0**-11 + 2 * xerr[..., None] + 2.0**-19) + far[..., None]
                + u * (out.abs() + 2.0**-11 * spread) + 1e-30)
         if got_out.dtype == torch.float16:

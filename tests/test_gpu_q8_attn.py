@@ -575,3 +575,72 @@ def test_values_up_to_the_largest_bf16_number(tv, lens, fmt):
     out, lse, status = run(tv, c)
     assert not any(status)
     check_seen(out, lse, c, 2)
+
+
+APART = [([(60, 4), (1500, 3)], True), ([(60, 40), (700, 64)], True), ([(60, 4), (1500, 3)], False),
+         ([(60, 40), (700, 64)], False), ([(2000, 70)] * 3, True)]
+
+
+@pytest.mark.parametrize("lens,tree", APART)
+@pytest.mark.parametrize("Hq,D,fmt", [(8, 128, "e4m3"), (4, 64, "int8"), (2, 128, "int8")])
+@pytest.mark.parametrize("bits", [12, 28, 100])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_large_rows_that_a_token_does_not_see(tv, lens, tree, Hq, D, fmt, bits, side):
+    """A rejected node's or a later token's row, far larger than the others, costs those that do not see it nothing."""
+    for where in ("last", "middle"):
+        c = make_q8(5, lens, Hq, 2, D, 16, fmt, tree=tree, spread=0.7)
+        for b, (L, n) in enumerate(lens):
+            i = n - 1 if where == "last" else n // 2
+            row = c["rows"][b][0 if side == "k" else 1][L + i:L + i + 1] * 2.0**bits
+            set_rows(c, b, L + i, **{side: row})
+        out, lse, status = run(tv, c)
+        assert not any(status)
+        check_seen(out, lse, c, 2, what=where)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("bits", [28, 100])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_large_rows_that_the_window_left(tv, n, bits, side):
+    lens = [(300, n), (77, n)]
+    c = make_q8(5, lens, 8, 2, 128, 16, "e4m3", spread=0.7)
+    for b, (L, _) in enumerate(lens):
+        j = L - 40 + n // 2 + 1  # (seen by about half of the tokens)
+        row = c["rows"][b][0 if side == "k" else 1][j:j + 1] * 2.0**bits
+        set_rows(c, b, j, **{side: row})
+    out, lse, status = run(tv, c, window=40)
+    assert not any(status)
+    check_seen(out, lse, c, 2, window=40)
+
+
+@pytest.mark.parametrize("lens", [[(40, 1)], [(900, 1), (300, 2)], [(40, 40)], [(900, 33)], [(3000, 64)]])
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("nats,bits", [(10.0, 15), (30.0, 44), (60.0, 90)])
+@pytest.mark.parametrize("at", [0, -1, 3])
+def test_values_of_all_sizes_with_weights_that_make_up_for_them(tv, lens, fmt, nats, bits, at):
+    """A key whose probability is e^-nats of the others' and whose value is 2^bits of theirs counts like them."""
+    H, D = 2, 128
+    c = make_q8(5, lens, H, H, D, 16, fmt, spread=0.5)
+    q = c["q"][:1].clone()
+    c["q"] = q.expand(c["T"], H, D).contiguous()
+    for b, (L, n) in enumerate(lens):
+        j = at % L if at < 0 else at  # (the last row that all tokens see, or one of the first)
+        k = -nats * D**0.5 * q.cpu().double() / (q.cpu().double()**2).sum(2, keepdim=True)
+        set_rows(c, b, j, k=k, v=c["rows"][b][1][j:j + 1] * 2.0**bits)
+    out, lse, status = run(tv, c)
+    assert not any(status)
+    check_seen(out, lse, c, H)
+
+
+@pytest.mark.parametrize("lens", [[(600, 1)], [(900, 40)]])
+@pytest.mark.parametrize("spread,kw", [(2.5, {}), (12.0, {}), (25.0, dict(window=300)), (12.0, dict(softcap=9.0))])
+@pytest.mark.parametrize("fmt,D", [("e4m3", 128), ("int8", 64)])
+def test_values_many_powers_of_two_apart(tv, lens, spread, kw, fmt, D):
+    """Each output is off by little of what its token's largest weighed value is."""
+    c = make_q8(6, lens, 4, 1, D, 16, fmt, spread=0.5)
+    g = torch.Generator().manual_seed(2)
+    for b, (L, n) in enumerate(lens):
+        set_rows(c, b, 0, v=c["rows"][b][1] * torch.exp2(torch.randn(L + n, 1, 1, generator=g) * spread))
+    out, lse, status = run(tv, c, **kw)
+    assert not any(status)
+    check_seen(out, lse, c, 1, **kw)
