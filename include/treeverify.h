@@ -796,7 +796,8 @@ tv_status tv_paged_append_q8(const void* k, const void* v, int64_t token_stride,
  *               number that number.  Rows of tokens outside every sequence are left as they were.
  *   status      int32 [B] out, may be NULL: 0, or TV_ERR_INVALID_ARG for a malformed q_start (the
  *               sequence's rows are left as they were), start[b] < 0 or start[b] + n_b > P * page_size
- *               (its rows are zeroed), or a page id outside [0, num_pages) (that page's rows are zeroed).
+ *               (its rows are zeroed), a page id outside [0, num_pages) (that page's rows are zeroed), or, where
+ *               q_start descends elsewhere, tokens that another sequence has too (either's rows).
  * Requires B <= 4096; B * P below 2^31 and P * page_size at most 2^31 - 1; Hkv * D / 16 at most 2^20.
  */
 tv_status tv_paged_read_q8(const tv_q8_cache* cache, const int32_t* block_table,

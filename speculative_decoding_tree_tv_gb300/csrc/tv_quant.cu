@@ -125,6 +125,17 @@ struct ReadQ8Params {
   int blocks;                  // CTAs of tokens; those behind them write the sequences' status
 };
 
+// The last sequence that starts at or before token t, or -1, if the starts ascend.
+__device__ __forceinline__ int seq_of(const ReadQ8Params& p, int t) {
+  int lo = 0, hi = p.B;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.q_start + mid) <= t) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo - 1;
+}
+
 // Whether a sequence's rows lie within the table.
 __device__ __forceinline__ bool read_fits(const ReadQ8Params& p, int start, int n) {
   return start >= 0 && (long long)start + n <= ((long long)p.P << p.c.page_shift);
@@ -154,6 +165,7 @@ __device__ __forceinline__ uint32_t narrow(float2 y, float f, bool safe) {
 template <bool E4M3, bool F16>
 __global__ void __launch_bounds__(kRowThreads) read_q8_kernel(const ReadQ8Params p) {
   __shared__ int s_page[kReadTokens], s_row[kReadTokens];  // page -1: zeros, -2: nobody's token
+  __shared__ int s_owner[kReadTokens];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
@@ -169,26 +181,44 @@ __global__ void __launch_bounds__(kRowThreads) read_q8_kernel(const ReadQ8Params
         const int page = TV_IN(j, p.P) ? __ldg(p.table + (size_t)b * p.P + j) : -1;
         ok = ok && page >= 0 && page < p.c.num_pages;
       }
+    // (a search that finds its first and last token finds those between, as one path through the starts does.  One that
+    // does not means starts that descend: its rows are its own then if no other sequence has tokens of it)
+    if (seq_range(p.q_start, b, p.T, t0, n) && n > 0 && (seq_of(p, t0) != b || seq_of(p, t0 + n - 1) != b))
+      for (int o = tid & 31; o < p.B; o += 32) {
+        int s0, sn;
+        if (o != b && seq_range(p.q_start, o, p.T, s0, sn)) ok = ok && (s0 >= t0 + n || s0 + sn <= t0 || sn == 0);
+      }
     ok = __all_sync(0xffffffffu, ok);
     if ((tid & 31) == 0 && p.status) p.status[b] = ok ? TV_OK : TV_ERR_INVALID_ARG;
     return;
   }
   const int first = blockIdx.x * p.tokens, count = min(p.tokens, p.T - first);
+  const int token = first + tid;
+  int b = -1, t0 = 0, n = 0;
   if (tid < count) {
-    const int t = first + tid;
-    int lo = 0, hi = p.B;  // the last sequence that starts at or before t
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldg(p.q_start + mid) <= t) lo = mid + 1;
-      else hi = mid;
+    b = seq_of(p, token);
+    if (b >= 0 && !(seq_range(p.q_start, b, p.T, t0, n) && token >= t0 && token - t0 < n)) b = -1;
+    s_owner[tid] = p.B;
+  }
+  if (__syncthreads_or(tid < count && b < 0)) {  // nobody's tokens, or starts that descend: the first that has them
+    for (int o = tid; o < p.B; o += kRowThreads) {
+      int s0, sn;
+      if (seq_range(p.q_start, o, p.T, s0, sn))
+        for (int i = max(s0 - first, 0); i < min(s0 + sn - first, count); ++i) atomicMin(&s_owner[i], o);
     }
-    const int b = lo - 1;
-    int page = -2, row = 0, t0, n;
-    if (b >= 0 && seq_range(p.q_start, b, p.T, t0, n) && t >= t0 && t - t0 < n) {
+    __syncthreads();
+    if (tid < count && b < 0 && s_owner[tid] < p.B) {
+      b = s_owner[tid];
+      seq_range(p.q_start, b, p.T, t0, n);
+    }
+  }
+  if (tid < count) {
+    int page = -2, row = 0;
+    if (b >= 0) {
       const int start = __ldg(p.start + b);
       page = -1;
       if (read_fits(p, start, n)) {
-        const int pos = start + t - t0, j = pos >> p.c.page_shift;
+        const int pos = start + token - t0, j = pos >> p.c.page_shift;
         page = TV_IN(j, p.P) ? __ldg(p.table + (size_t)b * p.P + j) : -1;
         if (page < 0 || page >= p.c.num_pages) page = -1;
         row = pos & ((1 << p.c.page_shift) - 1);

@@ -372,3 +372,38 @@ def test_outputs_that_do_not_fit_are_refused(tv):
             tv.paged_read_q8(*c, table, q_start, start, 4, **kw)
     k, v, _ = tv.paged_read_q8(*c, table, q_start, start, 4, k=x)
     assert k is x and v.dtype == torch.float16
+
+
+def test_read_beside_malformed_starts(tv):
+    """Sequences are judged by their own starts, wherever others' lie: rows of one with status 0 are there."""
+    page, D, T = 8, 64, 40
+    c = cache("e4m3", 20, 2, page, D)
+    c[2].clamp_(0, 250)
+    c[3].clamp_(0, 250)
+    for side in c[:2]:
+        side.view(torch.uint8).bitwise_and_(0x3f)  # (codes that are numbers)
+    for q_start in ([0, 2, 100, 4, 6], [6, 7, 0, 4, 4], [30, 31, 5, 9, 9], [-3, 2, 5, 30, 30], [0, 9, 4, 9, 12],
+                    [0, 50, 50, 3, 8]):
+        B = len(q_start) - 1
+        table = torch.arange(20, dtype=torch.int32).view(5, 4)[:B].to("cuda:0")
+        start = [3, 0, 7, 2][:B]
+        k, v = (torch.full((T, 2, D), 7.0, dtype=torch.bfloat16, device="cuda:0") for _ in range(2))
+        _, _, status = tv.paged_read_q8(*c, table, i32(q_start), i32(start), T, k=k, v=v)
+        status = np_(status).tolist()
+        val = [values_ref(c[i], c[2 + i]) for i in range(2)]
+        written = torch.zeros(T, dtype=torch.bool)
+        spans = [range(a, b) if 0 <= a <= b <= T else range(0) for a, b in zip(q_start, q_start[1:])]
+        for b in range(B):
+            a, e = q_start[b], q_start[b + 1]
+            if not 0 <= a <= e <= T:
+                assert status[b] == 1, (q_start, status)
+                continue
+            alone = not any(set(spans[b]) & set(spans[o]) for o in range(B) if o != b)
+            assert status[b] == 0 or not alone, (q_start, status)
+            written[a:e] = True
+            if status[b] == 0:
+                pos = np.arange(start[b], start[b] + e - a)
+                pages = np_(table)[b][pos // page]
+                for got, w in ((k, val[0]), (v, val[1])):
+                    check_read(got[a:e], w[pages, :, pos % page], torch.bfloat16)
+        assert bool((k[~written.cuda()] == 7).all()) and bool((v[~written.cuda()] == 7).all())
