@@ -702,7 +702,8 @@ tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_st
  * prefix is prefix_len[g] rows in the pages prefix_table[g, ..]; row j is at position j.  Sequence b of the
  * group has its own kv_len[b] cached rows and its new tokens behind it, in its own block_table row: its
  * row i is at position prefix_len[g] + i.  Tokens see the prefix (as far as the window reaches) and their own
- * rows as in tv_attn_paged; out and lse are over both.  Sequences before the first group or behind the last
+ * rows as in tv_attn_paged; out and lse are over both.  Rows of a prefix that no token of its group sees may hold
+ * anything; a row of V that one of them sees and another does not must be finite.  Sequences before the first group or behind the last
  * have no prefix.  No page need be held twice: to tv_page_map a prefix is a sequence of its
  * own, with its own table row, that grows once and is released when its last user is.
  *

@@ -29,6 +29,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
+
 #include "tv_paged.cuh"
 #include "tv_sm100.cuh"
 
@@ -267,9 +269,23 @@ __device__ __forceinline__ int prefix_pos(const PagedAttnParams& p, int g, int t
 
 struct Seq {
   int t0, n, L;
-  bool bad;  // rows are zeroed
+  int lo;       // a prefix: the first row that a window reaches
+  bool bad;     // rows are zeroed
   bool shared;  // a prefix
 };
+
+// The first row of a prefix of L that the window of some token of group g reaches: the sequence with the fewest
+// rows of its own reaches back furthest.
+__device__ __forceinline__ int prefix_reach(const PagedAttnParams& p, int g, int L) {
+  const int b1 = __ldg(p.group_start + g + 1);
+  int least = INT_MAX;
+#pragma unroll 8
+  for (int b = __ldg(p.group_start + g); b < b1; ++b) {
+    const int own = __ldg(p.kv_len + b);
+    if (__ldg(p.q_start + b + 1) > __ldg(p.q_start + b)) least = min(least, own);
+  }
+  return (int)min((long long)L, max(0ll, (long long)L + max(least, 0) - p.window + 1));
+}
 
 // (b: on the line, prefixes ahead of sequences)
 __device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
@@ -279,6 +295,7 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
     s.L = __ldg(p.prefix_len + b);
     if (!group_range(p, b, s.t0, s.n)) s.n = 0;
     s.bad = s.L < 0 || s.L > ((long long)p.prefix_P << p.page_shift);
+    s.lo = p.window > 0 && s.n > 0 && !s.bad ? prefix_reach(p, b, s.L) : 0;
     return s;
   }
   b -= p.groups;
@@ -293,9 +310,9 @@ __device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
 __device__ __forceinline__ void key_range(const PagedAttnParams& p, const Seq& s, int qt, int& lo,
                                           int& hi) {
   const int first = qt * p.tq;
-  if (s.shared) {  // (its tokens are all behind the prefix)
-    hi = s.L;
-    lo = p.window > 0 ? max(0, s.L - p.window + 1) : 0;
+  if (s.shared) {  // (its tokens are all behind the prefix; no tiles where no window reaches it)
+    lo = s.lo < s.L ? s.lo : 0;
+    hi = s.lo < s.L ? s.L : 0;
     return;
   }
   hi = p.anc ? s.L + s.n : s.L + min(s.n, first + p.tq);

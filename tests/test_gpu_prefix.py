@@ -398,3 +398,21 @@ def test_a_serving_loop_behind_one_prompt(tv):
     zero = i32([0] * (B + 2))
     tv.page_map(zero, zero[1:], table, held, free, n_free, page, 0)
     assert int(n_free) == pool and sorted(np_(free).tolist()) == list(range(pool))
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("own", [(10, 30), (120, 150), (99, 300), (98, 0)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_prefix_rows_that_no_window_reaches_may_hold_anything(tv, n, own, tree):
+    """The window reaches back from a sequence's own rows: what is ahead of all of a group's is not read."""
+    window, S = 100, 500
+    c = shared(3, [(S, [(own[0], n), (2, 0), (own[1], n)])], 4, 2, 64, 16, tree=tree)
+    ref = attn_ref(c["full"], 4, 2, 64, window=window)
+    for fill in (float("nan"), float("inf")):
+        for j in range(min(S, S + min(own) - window + 1)):
+            page = int(c["pre_table"][0, j // 16])
+            c["k"][page, :, j % 16] = fill
+            c["v"][page, :, j % 16] = fill
+        out, lse, status = run(tv, c, window=window)
+        assert status == [0, 0, 0]
+        check_attn(out, lse, ref, "bf16")
