@@ -709,8 +709,9 @@ tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_st
  *
  *   prefix_table int32 [groups, prefix_P]; prefix_len int32 [groups]; group_start int32 [groups + 1], ascending
  *               from 0 or more to B or less.  groups = 0: as tv_attn_paged (the three are not read then).
- *   status      as tv_attn_paged's, and TV_ERR_INVALID_ARG for the sequences of a malformed group (where
- *               group_start descends, for others behind it too), or one in which q_start descends, with a
+ *   status      as tv_attn_paged's, and TV_ERR_INVALID_ARG for the sequences from group_start[g] on, g the first
+ *               malformed group (one that descends or leaves 0 .. B; it and the groups behind it count for none; all
+ *               sequences if g is 0), and for those of a group in which q_start descends, with a
  *               prefix_len < 0 or past prefix_P * page_size (the prefix then counts as hidden), or with a
  *               page id outside [0, num_pages) among the prefix's pages that the window reaches (its rows count
  *               as hidden).

@@ -65,7 +65,8 @@ struct PagedAttnParams {
   int32_t* status;
   float* part;      // [2 * CTAs] slots of partial rows
   float2* part_ml;  // their (running maximum, log2 domain; running sum)
-  int4* desc;       // [CTAs]: the unit a CTA's share ends inside (first token, tokens, kv head, parts)
+  int4* desc;       // [CTAs]: the unit a CTA's share ends inside (first token, tokens, kv head, parts);
+                    // with shared prefixes [0].x: the groups that count
   Late* late;       // [CTAs]
   unsigned long long* any_late;  // this call's token: some CTA is late
   long long wait_limit;          // SM cycles; 0: the producers of K and V give up before they load anything
@@ -238,6 +239,12 @@ __device__ __forceinline__ int anc_depth(const uint64_t* anc, int W) {
 // 75.7, 63.8 and 28.7 us at 3; 80.3, 63.0 and 33.0 us at 8)
 constexpr int kUnitCost = 3;
 
+// Whether group g's sequences are none.  The first such group and those behind it do not count (they may name
+// sequences of the ones ahead).
+__device__ __forceinline__ bool group_malformed(const PagedAttnParams& p, int g) {
+  const int b0 = __ldg(p.group_start + g), b1 = __ldg(p.group_start + g + 1);
+  return b0 < 0 || b1 < b0 || b1 > p.B;
+}
 // Tokens of group g: false for a malformed group_start or q_start.
 __device__ __forceinline__ bool group_range(const PagedAttnParams& p, int g, int& t0, int& n) {
   const int b0 = __ldg(p.group_start + g), b1 = __ldg(p.group_start + g + 1);
@@ -287,14 +294,15 @@ __device__ __forceinline__ int prefix_reach(const PagedAttnParams& p, int g, int
   return (int)min((long long)L, max(0ll, (long long)L + max(least, 0) - p.window + 1));
 }
 
-// (b: on the line, prefixes ahead of sequences)
-__device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b) {
+// (b: on the line, prefixes ahead of sequences; good: the groups that count)
+__device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b, int good) {
   Seq s;
   s.shared = b < p.groups;
   if (s.shared) {
     s.L = __ldg(p.prefix_len + b);
-    if (!group_range(p, b, s.t0, s.n)) s.n = 0;
-    s.bad = s.L < 0 || s.L > ((long long)p.prefix_P << p.page_shift);
+    const bool is_group = group_range(p, b, s.t0, s.n);
+    if (b >= good || !is_group) s.n = 0;
+    s.bad = !is_group || s.L < 0 || s.L > ((long long)p.prefix_P << p.page_shift);
     s.lo = p.window > 0 && s.n > 0 && !s.bad ? prefix_reach(p, b, s.L) : 0;
     return s;
   }
@@ -355,6 +363,7 @@ struct Cursor {
   long long at;           // cost behind the share's start
   int b, kvh, qt, pos;    // unit, and cost of it that lies behind
   int last;               // the share's last sequence (or one behind it, where a thread looks at several)
+  int good;               // groups that count
   Seq s;
 
   __device__ __forceinline__ int cost_of(const PagedAttnParams& p, int tiles) const {
@@ -391,7 +400,7 @@ struct Cursor {
             kvh = 0;
             do {
               if (++b >= p.groups + p.B) break;
-              s = load_seq(p, b);
+              s = load_seq(p, b, good);
             } while (s.n == 0);
             if (b >= p.groups + p.B) rest = 0;
           }
@@ -422,17 +431,33 @@ __device__ __forceinline__ void prefetch_lengths(const PagedAttnParams& p) {
   if (first < (long long)p.groups * p.prefix_P) line_prefetch_l2(p.prefix_table + first);
 }
 
+// The first malformed group, or p.groups (all THREADS threads; a function of its own, as hardly any call needs it and code
+// at a kernel's start is new to the SM: the three cases of shared prefixes took 0.5 to 1.5 us longer with it in find_share).
+template <int THREADS>
+__device__ __noinline__ int first_malformed(const PagedAttnParams& p) {
+  __shared__ int s_first;
+  __syncthreads();
+  if (threadIdx.x == 0) s_first = p.groups;
+  __syncthreads();
+  for (int g = threadIdx.x; g < p.groups; g += THREADS)
+    if (group_malformed(p, g)) atomicMin(&s_first, g);
+  __syncthreads();
+  return s_first;
+}
+
 // Finds this CTA's share (s_cur: shared; rest is 0 where there is none).  All THREADS threads call it;
-// ends with a barrier.  Where sequences are few and chunks long, 2^share_lanes lanes share one's query tiles
+// ends with a barrier; returns the groups that count.  Where sequences are few and chunks long, 2^share_lanes lanes share one's query tiles
 // (a lane that walked the 32 of a chunk of 2048 alone held up the first tile by some 3,000 cycles).
-template <int KT, int THREADS>
-__device__ __forceinline__ void find_share(const PagedAttnParams& p, Cursor<KT>& s_cur) {
+// PRE: of a call with shared prefixes.
+template <int KT, int THREADS, bool PRE = false>
+__device__ __forceinline__ int find_share(const PagedAttnParams& p, Cursor<KT>& s_cur) {
   __shared__ long long s_warp[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lanes = 1 << p.share_lanes;
   const int seqs = p.groups + p.B, per = ceil_div(seqs, THREADS);  // (1 where lanes > 1)
   const int own = tid >> p.share_lanes, b0 = min(seqs, own * per), b1 = min(seqs, b0 + per);
   Cursor<KT> c;
+  c.good = p.groups;
   int qt0 = 0, qt1 = 0;  // this lane's query tiles
   auto tiles_cost = [&](const Seq& s) {  // of one kv head's units among them
     const int nq = s.n > 0 ? (s.n - 1) / p.tq + 1 : 0, each = (nq + lanes - 1) >> p.share_lanes;
@@ -442,21 +467,33 @@ __device__ __forceinline__ void find_share(const PagedAttnParams& p, Cursor<KT>&
     for (int qt = qt0; qt < qt1; ++qt) v += c.cost_of(p, key_tiles<KT>(p, s, qt));
     return v;
   };
-  long long sum = 0, one = 0, before = 0;  // (before: of the head's units ahead of this lane's)
-  for (int b = b0; b < b1; ++b) {
-    c.s = load_seq(p, b);
-    one = tiles_cost(c.s);
-    sum += one * p.Hkv;
-  }
-  long long inc = sum;
+  long long sum, one, before = 0, inc;  // (before: of the head's units ahead of this lane's)
+  for (;;) {
+    bool look = false;
+    sum = one = 0;
+    for (int b = b0; b < b1; ++b) {
+      c.s = load_seq(p, b, c.good);
+      look |= c.s.bad && b < c.good;
+      one = tiles_cost(c.s);
+      sum += one * p.Hkv;
+    }
+    inc = sum;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    if (tid == 0) s_cur.rest = 0;
+    if (!PRE) {
+      __syncthreads();
+      break;
+    }
+    if (!__syncthreads_or(look)) break;
+    const int good = first_malformed<THREADS>(p);
+    if (good == c.good) break;
+    c.good = good;  // (the lengths anew)
   }
-  if (lane == 31) s_warp[warp] = inc;
-  if (tid == 0) s_cur.rest = 0;
-  __syncthreads();
   long long base = inc - sum, total = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
@@ -480,7 +517,7 @@ __device__ __forceinline__ void find_share(const PagedAttnParams& p, Cursor<KT>&
     c.b = b0;
     if (per > 1) {
       for (;; ++c.b) {
-        c.s = load_seq(p, c.b);
+        c.s = load_seq(p, c.b, c.good);
         one = tiles_cost(c.s);
         if (x0 < base + one * p.Hkv) break;
         base += one * p.Hkv;
@@ -501,6 +538,7 @@ __device__ __forceinline__ void find_share(const PagedAttnParams& p, Cursor<KT>&
         s_cur.qt = c.qt;
         s_cur.pos = c.pos;
         s_cur.s = c.s;
+        s_cur.good = c.good;
         break;
       }
       left -= cost;
@@ -509,6 +547,7 @@ __device__ __forceinline__ void find_share(const PagedAttnParams& p, Cursor<KT>&
   const long long x1 = x0 + c.rest;  // the share's end, among this lane's sequences?
   if (c.rest > 0 && x1 > base0 && x1 <= base0 + sum) s_cur.last = b1 - 1;
   __syncthreads();
+  return c.good;
 }
 
 // The parts of a CTA's share, published by the one warp that walks it: the other
@@ -547,7 +586,7 @@ struct PartRing {
 __device__ __forceinline__ bool seq_ok(const PagedAttnParams& p, int b, int lane, int lanes) {
   int t0, n;
   if (!seq_range(p.q_start, b, p.T, t0, n)) return false;
-  const Seq s = load_seq(p, p.groups + b);
+  const Seq s = load_seq(p, p.groups + b, 0);
   if (s.bad) return false;
   if (n == 0) return true;
   int lo, hi, any = 0;

@@ -551,7 +551,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   prefetch_lengths<kThreads>(p);
   pdl_wait();
   tc_fence_before();
-  find_share<kTcKeys, kThreads>(p, s_cur);
+  const int good = find_share<kTcKeys, kThreads, PRE>(p, s_cur);
+  if (PRE && blockIdx.x == 0 && tid == 0) p.desc[0] = make_int4(good, 0, 0, 0);
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   uint32_t n = 0;  // parts so far

@@ -21,13 +21,13 @@ namespace {
 
 constexpr int kJoinThreads = 128;
 
-// The status of the sequence of a block.  Beside tv_attn_paged's reasons: a malformed group (or one with starts that
-// descend), a prefix that
-// does not fit, and a page of it that is none, as far as the sequence's window reaches.
+// The status of the sequence of a block.  Beside tv_attn_paged's reasons: a malformed group at or ahead of it, a group with
+// starts that descend, a prefix that does not fit, and a page of it that is none, as far as the sequence's window reaches.
 __device__ __forceinline__ void prefix_status(const PagedAttnParams& p, int b) {
   const int lane = threadIdx.x, lanes = kJoinThreads;
   bool bad = !seq_ok(p, b, lane, lanes);
-  const int g = last_at_most(p.group_start, p.groups, b);
+  const int good = p.desc[0].x;  // (their starts ascend)
+  const int g = last_at_most(p.group_start, good, b);
   const int next = __ldg(p.group_start + g + 1);
   int t0, n, s0, sn, of = -1;
   if (g >= 0 && b < next) {
@@ -46,7 +46,7 @@ __device__ __forceinline__ void prefix_status(const PagedAttnParams& p, int b) {
       }
     }
   } else {  // behind the last group or ahead of the first
-    bad |= g >= 0 && g != p.groups - 1;
+    bad |= good < p.groups && (good == 0 || b >= __ldg(p.group_start + good));
   }
   const bool late = is_late(p, b, lane, lanes, of);
   const int any_late = __syncthreads_or(late), any_bad = __syncthreads_or(bad);
@@ -74,11 +74,12 @@ prefix_join_kernel(const PagedAttnParams p, int nb, int row_blocks) {
   // that is known.
   const int4 mine = p.src[((size_t)p.T + t) * p.Hkv + kvh], pfx = p.src[(size_t)t * p.Hkv + kvh];
   const int b = min(max(mine.w, 0), p.B - 1), g = min(max(pfx.w, 0), p.groups - 1);
-  const Seq s_own = load_seq(p, p.groups + b);
+  const Seq s_own = load_seq(p, p.groups + b, 0);
+  const int good = p.desc[0].x;
   int gt, gn;
   const bool is_group = group_range(p, g, gt, gn);
   const bool is_own = mine.w == b && t >= s_own.t0 && t - s_own.t0 < s_own.n;
-  const bool pre = pfx.w == g && is_group && t >= gt && t - gt < gn && b >= __ldg(p.group_start + g) &&
+  const bool pre = pfx.w == g && g < good && is_group && t >= gt && t - gt < gn && b >= __ldg(p.group_start + g) &&
                    b < __ldg(p.group_start + g + 1);
   const size_t oidx = (size_t)t * p.Hq + kvh * p.G + h_in, rows = (size_t)p.T * p.Hq;
   uint2* out = reinterpret_cast<uint2*>(p.out + oidx * D) + c0;

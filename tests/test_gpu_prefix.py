@@ -416,3 +416,27 @@ def test_prefix_rows_that_no_window_reaches_may_hold_anything(tv, n, own, tree):
         out, lse, status = run(tv, c, window=window)
         assert status == [0, 0, 0]
         check_attn(out, lse, ref, "bf16")
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_groups_that_descend(tv, n):
+    """The first malformed group and those behind it have no prefix, and sequences from its start on say so."""
+    groups = [(200, [(10, n), (20, n)]), (100, [(5, n)]), (60, [(60, n)])]
+    for bounds, good, status in (([0, 3, 2, 4], 1, [0, 0, 0, 1]), ([0, 2, 1, 4], 1, [0, 0, 1, 1]),
+                                 ([2, 1, 3, 4], 0, [1, 1, 1, 1]), ([0, 1, 9, 4], 1, [0, 1, 1, 1]),
+                                 ([0, 1, 3, 1], 2, [0, 0, 0, 1]), ([1, 2, 3, 4], 3, [0, 0, 0, 0]),
+                                 ([0, 3, 2], 1, [0, 0, 0, 1]), ([5, 6, 7, 8], 0, [1, 1, 1, 1])):
+        c = shared(2, groups, 8, 2, 128, 16)
+        c["group_start"] = i32(bounds)
+        c["pre_table"], c["pre_len"] = c["pre_table"][:len(bounds) - 1], c["pre_len"][:len(bounds) - 1]
+        # the groups that count, and what their sequences see
+        of = [max([g for g in range(good) if bounds[g] <= b < bounds[g + 1]], default=-1) for b in range(4)]
+        full = dict(c["full"])
+        full["lens"] = [(L + (groups[g][0] if g >= 0 else 0), m) for g, (L, m) in zip(of, c["own"])]
+        full["rows"] = [tuple(torch.cat([c["rows"][g][i], c["rows"][3 + b][i]]) if g >= 0 else c["rows"][3 + b][i]
+                              for i in range(2)) for b, g in enumerate(of)]
+        out, lse, got = run(tv, c)
+        assert got == status, bounds
+        check_attn(out, lse, attn_ref(full, 8, 2, 128), "bf16", f"{bounds}")
+        again = run(tv, c)
+        assert same_bits(again[0], out) and torch.equal(again[1], lse)
