@@ -92,10 +92,10 @@ prefix_join_kernel(const PagedAttnParams p, int nb, int row_blocks) {
     if (side == 0 && !pre) break;
     const int4 s = side ? mine : pfx;
     // a part's rows lie chunk by chunk ([D / 4][256]): two row blocks of nb tokens in 128 each
-    const int parts = s.x < 0 ? 1 : min(s.y, p.ctas), tl = t - s.z, rb = tl >= nb;
+    const int parts = s.x < 0 ? 1 : min(s.y, p.ctas), tl = (int)((unsigned)t - (unsigned)s.z), rb = tl >= nb;
+    // (what nobody noted, of nobody's token or where a CTA gave up, may be anything)
+    if (s.x >= 0 && (tl < 0 || tl >= 2 * nb || s.x >= 2 * p.ctas)) continue;
     const int crow = rb * 128 + (tl - rb * nb) * p.G + h_in;
-    // (where a CTA gave up, what it would have noted may be anything)
-    if (s.x >= 0 && (tl < 0 || crow >= 256 || crow < 0)) continue;
     for (int j0 = 0; j0 < parts; j0 += kBatch) {
       float2 ml[kBatch];
       float4 v[kBatch][kC];

@@ -440,3 +440,21 @@ def test_groups_that_descend(tv, n):
         check_attn(out, lse, attn_ref(full, 8, 2, 128), "bf16", f"{bounds}")
         again = run(tv, c)
         assert same_bits(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("first", [2**31 - 1, 2**31 - 2, 2**31 - 300, -2**31, 303, 304])
+def test_whatever_the_workspace_held(tv, n, first):
+    """Tokens of nobody, whose entries in the workspace are old or anything."""
+    groups = [(3000, [(50, n)] * 20)]
+    c = shared(8, groups, 8, 2, 128, 64, pad=40)
+    want = run(tv, c)
+    T, Hq, D = c["q"].shape
+    size = tv.attn_paged_prefix_workspace_size(c["max_q"], T, 1, Hq, 2, D)
+    for parts, token, of in ((3, c["T"], 0), (2**31 - 1, c["T"] - 1, 0), (2, 2**31 - 1, 2**31 - 1),
+                             (2, -2**31, -1), (9, c["T"] + 39, 19)):
+        words = torch.tensor([first, parts, token, of], dtype=torch.int64).to(torch.int32)
+        ws = words.repeat(-(-size // 16)).to("cuda:0").view(torch.uint8)[:size]
+        out, lse, status = run(tv, c, ws=ws)
+        assert not any(status)
+        assert same_bits(out, want[0]) and torch.equal(lse, want[1])
