@@ -294,31 +294,36 @@ __device__ __forceinline__ int prefix_reach(const PagedAttnParams& p, int g, int
   return (int)min((long long)L, max(0ll, (long long)L + max(least, 0) - p.window + 1));
 }
 
-// (b: on the line, prefixes ahead of sequences; good: the groups that count)
-__device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b, int good) {
+__device__ __forceinline__ Seq load_own(const PagedAttnParams& p, int b) {
   Seq s;
-  s.shared = b < p.groups;
-  if (s.shared) {
-    s.L = __ldg(p.prefix_len + b);
-    const bool is_group = group_range(p, b, s.t0, s.n);
-    if (b >= good || !is_group) s.n = 0;
-    s.bad = !is_group || s.L < 0 || s.L > ((long long)p.prefix_P << p.page_shift);
-    s.lo = p.window > 0 && s.n > 0 && !s.bad ? prefix_reach(p, b, s.L) : 0;
-    return s;
-  }
-  b -= p.groups;
+  s.shared = false;
   s.L = __ldg(p.kv_len + b);
   if (!seq_range(p.q_start, b, p.T, s.t0, s.n)) s.n = 0;
   s.bad = s.L < 0 || (long long)s.L + s.n > ((long long)p.P << p.page_shift) ||
           (p.anc && s.n > 64 * p.W);
   return s;
 }
+// PRE: with shared prefixes, which lie on the line (b) ahead of the sequences (a variant of its own: 4 short sequences
+// took 11.6 us for 11.3 with groups looked for at run time).  good: the groups that count.
+template <bool PRE>
+__device__ __forceinline__ Seq load_seq(const PagedAttnParams& p, int b, int good) {
+  if (!PRE || b >= p.groups) return load_own(p, PRE ? b - p.groups : b);
+  Seq s;
+  s.shared = true;
+  s.L = __ldg(p.prefix_len + b);
+  const bool is_group = group_range(p, b, s.t0, s.n);
+  if (b >= good || !is_group) s.n = 0;
+  s.bad = !is_group || s.L < 0 || s.L > ((long long)p.prefix_P << p.page_shift);
+  s.lo = p.window > 0 && s.n > 0 && !s.bad ? prefix_reach(p, b, s.L) : 0;
+  return s;
+}
 
 // Keys [lo, hi) that some token of query tile qt sees.
+template <bool PRE>
 __device__ __forceinline__ void key_range(const PagedAttnParams& p, const Seq& s, int qt, int& lo,
                                           int& hi) {
   const int first = qt * p.tq;
-  if (s.shared) {  // (its tokens are all behind the prefix; no tiles where no window reaches it)
+  if (PRE && s.shared) {  // (its tokens are all behind the prefix; no tiles where no window reaches it)
     lo = s.lo < s.L ? s.lo : 0;
     hi = s.lo < s.L ? s.L : 0;
     return;
@@ -327,11 +332,11 @@ __device__ __forceinline__ void key_range(const PagedAttnParams& p, const Seq& s
   // (the root of a tree sees furthest back)
   lo = p.window > 0 ? max(0, (p.anc ? s.L : s.L + first) - p.window + 1) : 0;
 }
-template <int KT>
+template <int KT, bool PRE>
 __device__ __forceinline__ int key_tiles(const PagedAttnParams& p, const Seq& s, int qt) {
   if (s.bad) return 0;
   int lo, hi;
-  key_range(p, s, qt, lo, hi);
+  key_range<PRE>(p, s, qt, lo, hi);
   return (hi + KT - 1) / KT - lo / KT;
 }
 
@@ -357,7 +362,7 @@ __device__ __forceinline__ long long div_fast(long long a, long long b) {
 }
 
 // A CTA's walk over its share of the line.
-template <int KT>
+template <int KT, bool PRE = false>
 struct Cursor {
   long long rest, share;  // cost left, cost of a share
   long long at;           // cost behind the share's start
@@ -366,19 +371,21 @@ struct Cursor {
   int good;               // groups that count
   Seq s;
 
+  static __device__ __forceinline__ int line(const PagedAttnParams& p) { return PRE ? p.groups + p.B : p.B; }
+  __device__ __forceinline__ int unit_cost(const PagedAttnParams& p) const { return PRE ? p.unit_cost : kUnitCost; }
   __device__ __forceinline__ int cost_of(const PagedAttnParams& p, int tiles) const {
-    return p.whole ? 1 : tiles + p.unit_cost;
+    return p.whole ? 1 : tiles + unit_cost(p);
   }
   __device__ __forceinline__ bool next(const PagedAttnParams& p, Part& o) {
     while (rest > 0) {
-      const int tiles = key_tiles<KT>(p, s, qt), cost = cost_of(p, tiles);
+      const int tiles = key_tiles<KT, PRE>(p, s, qt), cost = cost_of(p, tiles);
       const int take = (int)min((long long)(cost - pos), rest);
-      const int a = p.whole ? 0 : max(0, pos - p.unit_cost);
-      const int e = p.whole ? tiles : max(0, pos + take - p.unit_cost);
+      const int a = p.whole ? 0 : max(0, pos - unit_cost(p));
+      const int e = p.whole ? tiles : max(0, pos + take - unit_cost(p));
       const bool ends = pos + take == cost;
       const bool emit = e > a || (tiles == 0 && ends);
       if (emit) {
-        key_range(p, s, qt, o.lo, o.hi);
+        key_range<PRE>(p, s, qt, o.lo, o.hi);
         o.s = s;
         o.b = b;
         o.kvh = kvh;
@@ -399,10 +406,10 @@ struct Cursor {
           if (++kvh == p.Hkv) {
             kvh = 0;
             do {
-              if (++b >= p.groups + p.B) break;
-              s = load_seq(p, b, good);
+              if (++b >= line(p)) break;
+              s = load_seq<PRE>(p, b, good);
             } while (s.n == 0);
-            if (b >= p.groups + p.B) rest = 0;
+            if (b >= line(p)) rest = 0;
           }
         }
       }
@@ -415,7 +422,7 @@ struct Cursor {
 
 // Lines of the lengths and of the block table into the L2, shared out over the CTAs, while
 // the previous kernel finishes: a hint, which changes no result if that kernel writes them.
-template <int THREADS>
+template <int THREADS, bool PRE = false>
 __device__ __forceinline__ void prefetch_lengths(const PagedAttnParams& p) {
   const int first = (blockIdx.x * THREADS + threadIdx.x) * 32, step = gridDim.x * THREADS * 32;
   for (int i = first; i < p.B; i += step) {
@@ -424,6 +431,7 @@ __device__ __forceinline__ void prefetch_lengths(const PagedAttnParams& p) {
   }
   const long long words = min((long long)p.B * p.P, (long long)step);  // (one line a thread)
   if (first < words) line_prefetch_l2(p.table + first);
+  if (!PRE) return;
   for (int i = first; i < p.groups; i += step) {
     line_prefetch_l2(p.group_start + i);
     line_prefetch_l2(p.prefix_len + i);
@@ -448,23 +456,22 @@ __device__ __noinline__ int first_malformed(const PagedAttnParams& p) {
 // Finds this CTA's share (s_cur: shared; rest is 0 where there is none).  All THREADS threads call it;
 // ends with a barrier; returns the groups that count.  Where sequences are few and chunks long, 2^share_lanes lanes share one's query tiles
 // (a lane that walked the 32 of a chunk of 2048 alone held up the first tile by some 3,000 cycles).
-// PRE: of a call with shared prefixes.
-template <int KT, int THREADS, bool PRE = false>
-__device__ __forceinline__ int find_share(const PagedAttnParams& p, Cursor<KT>& s_cur) {
+template <int KT, int THREADS, bool PRE>
+__device__ __forceinline__ int find_share(const PagedAttnParams& p, Cursor<KT, PRE>& s_cur) {
   __shared__ long long s_warp[THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lanes = 1 << p.share_lanes;
-  const int seqs = p.groups + p.B, per = ceil_div(seqs, THREADS);  // (1 where lanes > 1)
+  const int seqs = Cursor<KT, PRE>::line(p), per = ceil_div(seqs, THREADS);  // (1 where lanes > 1)
   const int own = tid >> p.share_lanes, b0 = min(seqs, own * per), b1 = min(seqs, b0 + per);
-  Cursor<KT> c;
-  c.good = p.groups;
+  Cursor<KT, PRE> c;
+  c.good = PRE ? p.groups : 0;
   int qt0 = 0, qt1 = 0;  // this lane's query tiles
   auto tiles_cost = [&](const Seq& s) {  // of one kv head's units among them
     const int nq = s.n > 0 ? (s.n - 1) / p.tq + 1 : 0, each = (nq + lanes - 1) >> p.share_lanes;
     qt0 = min(nq, (tid & (lanes - 1)) * each);
     qt1 = min(nq, qt0 + each);
     long long v = 0;
-    for (int qt = qt0; qt < qt1; ++qt) v += c.cost_of(p, key_tiles<KT>(p, s, qt));
+    for (int qt = qt0; qt < qt1; ++qt) v += c.cost_of(p, key_tiles<KT, PRE>(p, s, qt));
     return v;
   };
   long long sum, one, before = 0, inc;  // (before: of the head's units ahead of this lane's)
@@ -472,7 +479,7 @@ __device__ __forceinline__ int find_share(const PagedAttnParams& p, Cursor<KT>& 
     bool look = false;
     sum = one = 0;
     for (int b = b0; b < b1; ++b) {
-      c.s = load_seq(p, b, c.good);
+      c.s = load_seq<PRE>(p, b, c.good);
       look |= c.s.bad && b < c.good;
       one = tiles_cost(c.s);
       sum += one * p.Hkv;
@@ -517,7 +524,7 @@ __device__ __forceinline__ int find_share(const PagedAttnParams& p, Cursor<KT>& 
     c.b = b0;
     if (per > 1) {
       for (;; ++c.b) {
-        c.s = load_seq(p, c.b, c.good);
+        c.s = load_seq<PRE>(p, c.b, c.good);
         one = tiles_cost(c.s);
         if (x0 < base + one * p.Hkv) break;
         base += one * p.Hkv;
@@ -527,7 +534,7 @@ __device__ __forceinline__ int find_share(const PagedAttnParams& p, Cursor<KT>& 
     c.kvh = (int)div_fast(x0 - base, one);
     long long left = x0 - base - c.kvh * one - before;
     for (c.qt = qt0; left >= 0 && c.qt < qt1; ++c.qt) {
-      const int cost = c.cost_of(p, key_tiles<KT>(p, c.s, c.qt));
+      const int cost = c.cost_of(p, key_tiles<KT, PRE>(p, c.s, c.qt));
       if (left < cost) {
         c.pos = (int)left;
         s_cur.rest = c.rest;
@@ -586,11 +593,11 @@ struct PartRing {
 __device__ __forceinline__ bool seq_ok(const PagedAttnParams& p, int b, int lane, int lanes) {
   int t0, n;
   if (!seq_range(p.q_start, b, p.T, t0, n)) return false;
-  const Seq s = load_seq(p, p.groups + b, 0);
+  const Seq s = load_own(p, b);
   if (s.bad) return false;
   if (n == 0) return true;
   int lo, hi, any = 0;
-  key_range(p, s, 0, lo, hi);
+  key_range<false>(p, s, 0, lo, hi);
   hi = s.L + n;
   const int32_t* row = p.table + (size_t)b * p.P;
 #pragma unroll 8
@@ -630,8 +637,8 @@ __device__ __forceinline__ void write_status(const PagedAttnParams& p) {
       *(volatile int32_t*)(p.status + b) = TV_ERR_TIMEOUT;
 }
 // A wait of this CTA gave up: the sequences of its share from `first` on may lack rows (one thread).
-template <int KT>
-__device__ __forceinline__ void report_late(const PagedAttnParams& p, const Cursor<KT>& share, int first) {
+template <int KT, bool PRE>
+__device__ __forceinline__ void report_late(const PagedAttnParams& p, const Cursor<KT, PRE>& share, int first) {
   if (share.rest <= 0) return;
   volatile Late* l = p.late + blockIdx.x;
   l->first = first;
@@ -680,7 +687,7 @@ __device__ __forceinline__ bool await_rows(const PagedAttnParams& p, int share, 
 // The page ids of a part's tiles, last tile first, for a warp that issues their loads: one
 // coalesced read of the block table covers 32 pages, and the next is on its way
 // (a read per tile held the loads to a tile per memory latency).
-template <int KT>
+template <int KT, bool PRE = false>
 struct PageFeed {
   int rows, per_tile, tiles;  // rows of a box; pages of a tile; tiles of a read
   int page, next;             // this lane's page, and what the table says of the next read's
@@ -692,8 +699,9 @@ struct PageFeed {
     const int lane = threadIdx.x & 31, back = lane / per_tile, t = t0 - back;
     const int key = t * KT + (lane - back * per_tile) * rows, j = key >> p.page_shift;
     next_needed = back < tiles && t >= w.begin && key < w.hi && key + rows > w.lo;
-    const int P = w.s.shared ? p.prefix_P : p.P;
-    const int32_t* row = w.s.shared ? p.prefix_table + (size_t)w.b * P : p.table + (size_t)(w.b - p.groups) * P;
+    const bool shared = PRE && w.s.shared;
+    const int P = shared ? p.prefix_P : p.P;
+    const int32_t* row = (shared ? p.prefix_table : p.table) + (size_t)(PRE && !shared ? w.b - p.groups : w.b) * P;
     next = next_needed && TV_IN(j, P) ? __ldg(row + j) : -1;
   }
   __device__ __forceinline__ void take(const PagedAttnParams& p) {

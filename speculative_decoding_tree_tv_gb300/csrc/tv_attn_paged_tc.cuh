@@ -511,7 +511,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
   auto& s_vnan = s_held.vnan;
   volatile int *s_kexp = s_held.kexp, *s_vexp = s_held.vexp;
   __shared__ PartRing s_ring;
-  __shared__ Cursor<kTcKeys> s_cur;
+  __shared__ Cursor<kTcKeys, PRE> s_cur;
   __shared__ int s_late;  // the first sequence that a softmax warp gave up in
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_trigger();
@@ -548,10 +548,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     tma_prefetch_desc(&tmV);
   }
   if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
-  prefetch_lengths<kThreads>(p);
+  prefetch_lengths<kThreads, PRE>(p);
   pdl_wait();
   tc_fence_before();
-  const int good = find_share<kTcKeys, kThreads, PRE>(p, s_cur);
+  const int good = find_share<kTcKeys, kThreads>(p, s_cur);
   if (PRE && blockIdx.x == 0 && tid == 0) p.desc[0] = make_int4(good, 0, 0, 0);
   tc_fence_after();
   const uint32_t tmem = s_tmem;
@@ -622,7 +622,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     uint64_t* full = Q8 ? (isV ? bar_v_raw : bar_k_raw) : isV ? bar_v_full : bar_k_full;
     uint64_t* empty = isV ? bar_v_empty : bar_k_empty;
     const uint32_t stages = isV ? kVStages : kKStages;
-    PageFeed<kTcKeys> feed;
+    PageFeed<kTcKeys, PRE> feed;
     const int rows_page = min(1 << p.page_shift, kTcKeys), npg = kTcKeys / rows_page;
     // (8-bit cache: lane l < 16 has the keys 8 l .. 8 l + 7, their scales and, if they are its first, their page's box)
     const int pg = Q8 ? (lane & 15) * 8 / rows_page : lane % npg, atom = lane / npg;
@@ -757,7 +757,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     // ------------------------------ the share's parts, and their Q rows
     uint32_t parts = 0;
     Part w;
-    Cursor<kTcKeys> cur = s_cur;
+    Cursor<kTcKeys, PRE> cur = s_cur;
     if (!PRE && p.merge && lane == 0) p.desc[share_index()] = make_int4(0, 0, 0, 0);
     uint64_t& bar_q_land = Q8 && !F16 ? bar_q_raw : bar_q_full;
     // One thread: a part's Q rows, as boxes of nb tokens.

@@ -74,7 +74,7 @@ prefix_join_kernel(const PagedAttnParams p, int nb, int row_blocks) {
   // that is known.
   const int4 mine = p.src[((size_t)p.T + t) * p.Hkv + kvh], pfx = p.src[(size_t)t * p.Hkv + kvh];
   const int b = min(max(mine.w, 0), p.B - 1), g = min(max(pfx.w, 0), p.groups - 1);
-  const Seq s_own = load_seq(p, p.groups + b, 0);
+  const Seq s_own = load_own(p, b);
   const int good = p.desc[0].x;
   int gt, gn;
   const bool is_group = group_range(p, g, gt, gn);
