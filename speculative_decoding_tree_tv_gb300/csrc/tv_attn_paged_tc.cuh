@@ -218,21 +218,50 @@ __device__ __forceinline__ int2 scale_range(const uint8_t* scale, int z0, int z1
   return make_int2(__reduce_max_sync(0xffffffffu, max(hi & 255u, (hi >> 8) & 255u)),
                    __reduce_min_sync(0xffffffffu, min(lo & 255u, (lo >> 8) & 255u)));
 }
-// Notes the rows that are no numbers, if there is one (by a whole warp).
-constexpr int kHasNaN = 1 << 16;
-// Or that the rows are too far apart to be held over one power of two: their codes go on as they are, and a row of
-// the unit takes their powers of two itself (apart_tile).  K rows of up to 15 apart lose no bit in fp16.
-constexpr int kApart = 1 << 17, kExpMask = 0xffff, kKeysNear = 15;
-__device__ __forceinline__ bool note_nan_rows(uint32_t nan4, volatile uint32_t (&words)[4]) {
-  if (!__any_sync(0xffffffffu, nan4 != 0)) return false;
-  const int lane = threadIdx.x & 31;
-  const uint32_t bits = (nan4 & 1) | (nan4 >> 7 & 2) | (nan4 >> 14 & 4) | (nan4 >> 21 & 8);
+// What a tile is held over: a scale byte, ref, one above the largest of the part's first tile, for rows of up to one above
+// it and kSpan below: V rows as far as a unit's rows share a power of two, K rows as far as they lose no bit in fp16.
+// Or the tile is apart: codes go on as they are, and a row of the unit takes their powers of two itself (apart_tile): where K
+// rows are further apart or one is no number, and where V rows are, then to the part's end.  kHasNaN: V rows of the tile
+// are no numbers, which are noted and taken for the zeros that their codes are.
+constexpr int kHasNaN = 1 << 16, kApart = 1 << 17, kExpMask = 0xffff;
+constexpr int kNoRef = -1, kFarRef = -2;  // no row yet; apart to the part's end
+__device__ __forceinline__ int span_of(bool v) { return v ? q8::kNear - 1 : 15; }
+// Whether all rows of a tile are within the reach of ref (by a whole warp).
+__device__ __forceinline__ bool near_ref(const uint8_t* scale, int ref, bool v) {
+  const uint32_t s4 = reinterpret_cast<const uint32_t*>(scale)[threadIdx.x & 31];
+  const int low = ref - span_of(v);
+  unsigned off = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const uint32_t word = __reduce_or_sync(0xffffffffu, lane / 8 == w ? bits << (4 * (lane & 7)) : 0u);
-    if (lane == 0) words[w] = word;
+  for (int i = 0; i < 4; ++i) off = max(off, (unsigned)((int)__byte_perm(s4, 0, 0x4440 + i) - low));
+  return __all_sync(0xffffffffu, off <= (unsigned)(ref + 1 - low) && ref < 254);
+}
+// What a tile is held over, and ref from then on (by a whole warp; a function of its own, as few tiles need it: with
+// the largest and the smallest scale of every tile looked for in the loop 16 trees of 64 took 106 to 108 us).
+__device__ __noinline__ int2 look_closer(uint8_t* scale, int z0, int z1, bool v, int ref, volatile uint32_t* words) {
+  uint32_t nan4;
+  const int2 range = scale_range(scale, z0, z1, nan4);  // (0, 255): no row is a number
+  const int to = ref == kNoRef ? min(range.x + 1, 254) : ref;
+  int over = kApart | 1;
+  if (ref != kFarRef && range.x <= to + 1 && range.y >= to - span_of(v)) {
+    over = to;
+    if (range.x > 0) ref = to;
+  } else if (v) {
+    ref = kFarRef;
   }
-  return true;
+  if (__any_sync(0xffffffffu, nan4 != 0)) {
+    if (!v) return make_int2(kApart | 1, ref);
+    const int lane = threadIdx.x & 31;
+    const uint32_t bits = (nan4 & 1) | (nan4 >> 7 & 2) | (nan4 >> 14 & 4) | (nan4 >> 21 & 8);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t word = __reduce_or_sync(0xffffffffu, lane / 8 == w ? bits << (4 * (lane & 7)) : 0u);
+      if (lane == 0) words[w] = word;
+    }
+    uint32_t* s4 = reinterpret_cast<uint32_t*>(scale + 4 * lane);
+    *s4 = (*s4 & ~nan4) | (nan4 & (uint32_t)(over & 255) * 0x01010101u);
+    over |= kHasNaN;
+  }
+  return make_int2(over, ref);
 }
 // Pairs of fp16 values of four codes, times a pair of equal factors f; g = -1152 f.
 template <bool E4M3>
@@ -263,7 +292,6 @@ __device__ __forceinline__ void convert_rows(uint8_t* tile, const int (&e)[kUnit
   uint8_t *first = row + ((ch ^ sw) << 4), *second = row + (((ch + 1) ^ sw) << 4);
 #pragma unroll
   for (int i = 0; i < kUnits<D>; ++i) {
-    // (255, a row that is no number: infinity, which its codes of 0 make NaN)
     const float f32 = __int_as_float(e[i] << 23);
     const __half2 f = __floats2half2_rn(f32, f32);
     const __half2 g = E4M3 ? f : __hmul2(f, __half2half2(__ushort_as_half(0xe480)));  // (-1152)
@@ -321,6 +349,7 @@ template <bool Q8>
 struct Held {
   __align__(16) uint8_t kscale[Q8 ? kExpRing : 1][kTcKeys];
   uint8_t vscale[Q8 ? kVStages : 1][kTcKeys];
+  uint8_t flat[Q8 ? kTcKeys : 1];                                 // of tiles whose codes go on as they are
   volatile int kexp[Q8 ? kExpRing : 1], vexp[Q8 ? kExpRing : 1];  // a scale byte, kHasNaN, kApart
   volatile uint32_t vnan[Q8 ? kExpRing : 1][4];                   // keys whose V row is no number, where vexp says so
 };
@@ -344,11 +373,12 @@ __device__ __noinline__ ApartRow apart_tile(const PagedAttnParams& p, const Part
   const int j0 = (w.end - 1 - t) * kTcKeys, L = w.s.L, lo = w.lo, hi = w.hi;
   const Row r = row_of(p, w, w.first + min(rb * nb + min(tl, nb - 1), w.ntok - 1), false);
   const float slope = (BIAS && p.slopes) ? __ldg(p.slopes + w.kvh * p.G + row % p.G) * kLog2e : 0.0f;
+  tc_fence_after();
   const int k_held = held.kexp[kt % kExpRing], v_held = held.vexp[kt % kExpRing];
   const uint8_t *ks = held.kscale[kt % kExpRing], *vs = held.vscale[kt % kVStages];
   const bool k_apart = k_held & kApart, v_apart = v_held & kApart;
   const float kf = fminf(qf * __int_as_float((k_held & kExpMask) << 23), FLT_MAX);  // (0 where K is apart)
-  auto key_factor = [&](int j) { return k_apart ? fminf(qf * q8::factor(ks[j]), FLT_MAX) : kf; };
+  auto key_factor = [&](int j) { return k_apart ? q8::at_most(qf * q8::factor(ks[j]), FLT_MAX) : kf; };
   const float in_scale = CAP ? 1.0f : k_apart ? p.scale_log2 : fminf(fmaxf(p.scale_log2 * kf, FLT_MIN), FLT_MAX);
   const float scale = (BIAS && p.slopes) ? 1.0f : in_scale;
   uint32_t x[32];
@@ -547,6 +577,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
+  if (Q8 && tid < kTcKeys) s_held.flat[Q8 ? tid : 0] = 1;
   if (warp == 0) tmem_alloc(&s_tmem, kTmemCols);
   prefetch_lengths<kThreads, PRE>(p);
   pdl_wait();
@@ -577,8 +608,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
           bool landed = warp_wait((side ? bar_v_scale : bar_k_scale) + (Q8 ? st : 0), ph, p.wait_limit);
           landed = warp_wait((side ? bar_v_raw : bar_k_raw) + (Q8 ? st : 0), ph, p.wait_limit) && landed;  // (it has)
           uint8_t* tile = (side ? sV : sK) + st * Lay::kTile;
-          const uint8_t* scale = side ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? it % kExpRing : 0];
           const int held = (side ? s_vexp : s_kexp)[Q8 ? it % kExpRing : 0], over = held & kExpMask;
+          const uint8_t* scale = held & kApart ? s_held.flat : side ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? it % kExpRing : 0];
 #pragma unroll 1
           for (int pass = 0; ok && pass < kPasses; ++pass) {
             const int row0 = pass * (kTcKeys / kPasses);
@@ -587,12 +618,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
             int e[kUnits<D>];  // exponents of the rows' factors, as floats have them (outside of the unit's range: anything)
 #pragma unroll
             for (int i = 0; i < kUnits<D>; ++i) e[i] = scale[row0 + unit_row<D>(ctid) + i * kRowStep<D>] + 127 - over;
-            if (held & (kApart | kHasNaN))
-#pragma unroll
-              for (int i = 0; i < kUnits<D>; ++i) {
-                const int s = e[i] - 127 + over;
-                e[i] = s == q8::kNaN ? 255 : held & kApart ? 127 : e[i];
-              }
             // (the pass's codes are in registers before their place is written; a warp that gave up joins the others here)
             ok = all_threads<2, kConvertThreads>(landed);
             if (!ok) break;
@@ -651,27 +676,18 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       z0 = 0;
       z1 = kTcKeys;
     };
-    // (8-bit cache) The scales of tile j, once it has landed: what its K or V is held over, and V's rows that are no
-    // numbers, which are noted and taken for zeros.
-    int vexp = -1, vlo = 255, vhi = 0;  // (the part's scales so far lie within vlo .. vhi)
+    // (8-bit cache) The scales of tile j, once it has landed: what its K or V is held over.
+    int ref = kNoRef;
     auto look_at_scales = [&](uint32_t j, int z0, int z1, bool first) {
       const uint32_t st = isV ? j % kVStages : j % kKStages, ph = (isV ? j / kVStages : j / kKStages) & 1;
       if (!warp_wait(&full[st], ph, p.wait_limit)) return false;
       uint8_t* scale = isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? j % kExpRing : 0];
-      uint32_t nan4;
-      const int2 range = scale_range(scale, z0, z1, nan4);
-      int over = range.x - range.y > kKeysNear ? kApart : max(range.x, 1);
-      if (isV) {
-        vhi = first ? range.x : max(vhi, range.x);
-        vlo = first ? range.y : min(vlo, range.y);
-        if (first || vhi > vexp + 1) vexp = vhi;
-        over = vhi - vlo > q8::kNear ? kApart : vexp;
-        if (note_nan_rows(nan4, s_vnan[Q8 ? j % kExpRing : 0])) {
-          over |= kHasNaN;
-          *reinterpret_cast<uint32_t*>(scale + 4 * lane) &= ~nan4;
-        }
-      } else if (__any_sync(0xffffffffu, nan4 != 0)) {
-        over |= kHasNaN;
+      if (first) ref = kNoRef;
+      int over = ref;
+      if (z0 > 0 || z1 < kTcKeys || ref < 0 || !near_ref(scale, ref, isV)) {
+        const int2 at = look_closer(scale, z0, z1, isV, ref, s_vnan[Q8 ? j % kExpRing : 0]);
+        over = at.x;
+        ref = at.y;
       }
       if (lane == 0) (isV ? s_vexp : s_kexp)[Q8 ? j % kExpRing : 0] = over;
       __syncwarp();
@@ -1161,7 +1177,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         const float tmag = fabsf(tmax);
         if ((Q8 || PRE) && !CAP && __any_sync(0xffffffffu, tmag > 0x1p22f && tmag < INFINITY)) {
           // Scores so large that a rounding of the maximum is a power of two or more: the products are rounded
-          // like it, ahead of the difference (fused, the largest could end far above 0).
+          // like it, ahead of the difference (fused, the largest could end far above 0).  (Of an 8-bit cache
+          // apart_tile does, while TMEM still has them as they were.)
+          if (Q8 && !BIAS) break;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll

@@ -72,14 +72,6 @@ __device__ __forceinline__ void halves_t(uint32_t x, uint32_t& even, uint32_t& o
   halves<E4M3>(__byte_perm(x, 0, 0x3120), even, odd);
 }
 
-// The smaller of two numbers, NaN if x is (a row that is no number has that factor; 0 times a factor past the 32-bit
-// range is 0 all the same).
-__device__ __forceinline__ float at_most(float x, float top) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(top));
-  return y;
-}
-
 // Q's and the outputs' type makes no variant: it matters at a unit's ends alone.
 __device__ __forceinline__ float2 unpack16(int f16, uint32_t x) {
   return f16 ? q8::unpack<true>(x) : q8::unpack<false>(x);
@@ -357,7 +349,7 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int i = 0; i < kAll; ++i) s[at(r, i)] *= at_most(in_scale[r] * kf[i], FLT_MAX);
+          for (int i = 0; i < kAll; ++i) s[at(r, i)] *= q8::at_most(in_scale[r] * kf[i], FLT_MAX);
         if (MOD && p.softcap_log2 > 0.0f) {
           float f[KB * 8], top = 0.0f;
 #pragma unroll

@@ -64,6 +64,14 @@ __device__ __forceinline__ float exp2_whole(int e) { return __int_as_float(min(m
 // x 2^e, where 2^e alone may be past that.
 __device__ __forceinline__ float times_exp2(float x, int e) { return x * exp2_whole(e >> 1) * exp2_whole(e - (e >> 1)); }
 
+// The smaller of two numbers, NaN if x is (a row that is no number has that factor; 0 times a factor past the 32-bit
+// range is 0 all the same).
+__device__ __forceinline__ float at_most(float x, float top) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(top));
+  return y;
+}
+
 // While the scale bytes t_j of the V rows that a part has met lie within this of one another, all rows of the unit
 // hold their outputs over one power of two.  Beyond it each row has its own, that of its
 // largest p_j 2^t_j so far, so that V rows that it does not see, or hardly, cost it no bits.  Either way

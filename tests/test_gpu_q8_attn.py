@@ -644,3 +644,23 @@ def test_values_many_powers_of_two_apart(tv, lens, spread, kw, fmt, D):
     out, lse, status = run(tv, c, **kw)
     assert not any(status)
     check_seen(out, lse, c, 1, **kw)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_a_value_that_is_no_number_beside_scales_of_any_size(tv, fmt, n):
+    """A V row that is no number has no say in the outputs of tokens that do not see it."""
+    for byte in [1, 2, 60] + list(range(120, 136)) + [200, 240]:
+        c = make_q8(4, [(300, n), (70, n)], 4, 2, 64, 16, fmt, spread=0.0)
+        c["q8"][3].fill_(byte)
+        want, sees = run(tv, c), []
+        table = np_(c["table"])
+        for b, (L, _) in enumerate(c["lens"]):
+            j = L + n // 2
+            c["q8"][1].view(torch.uint8)[table[b, j // 16], :, j % 16] = 0
+            c["q8"][3][table[b, j // 16], :, j % 16] = 255
+            sees += [L + i >= j for i in range(n)]
+        out, lse, status = run(tv, c)
+        sees = torch.tensor(sees, device="cuda:0")
+        assert not any(status) and torch.equal(lse, want[1])
+        assert bool(out[sees].isnan().all()) and same_bits(out[~sees], want[0][~sees]), byte
