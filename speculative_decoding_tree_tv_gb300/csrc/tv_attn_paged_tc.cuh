@@ -219,7 +219,7 @@ __device__ __forceinline__ int2 scale_range(const uint8_t* scale, int z0, int z1
                    __reduce_min_sync(0xffffffffu, min(lo & 255u, (lo >> 8) & 255u)));
 }
 // What a tile is held over: a scale byte, ref, one above the largest of the part's first tile, for rows of up to one above
-// it and kSpan below: V rows as far as a unit's rows share a power of two, K rows as far as they lose no bit in fp16.
+// it and span_of below: V rows as far as a unit's rows share a power of two, K rows as far as they lose no bit in fp16.
 // Or the tile is apart: codes go on as they are, and a row of the unit takes their powers of two itself (apart_tile): where K
 // rows are further apart or one is no number, and where V rows are, then to the part's end.  kHasNaN: V rows of the tile
 // are no numbers, which are noted and taken for the zeros that their codes are.
@@ -244,7 +244,7 @@ __device__ __noinline__ int2 look_closer(uint8_t* scale, int z0, int z1, bool v,
   int over = kApart | 1;
   if (ref != kFarRef && range.x <= to + 1 && range.y >= to - span_of(v)) {
     over = to;
-    if (range.x > 0) ref = to;
+    if (range.y < q8::kNaN) ref = to;
   } else if (v) {
     ref = kFarRef;
   }

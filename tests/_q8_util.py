@@ -152,7 +152,7 @@ def set_rows(c, b, j, k=None, v=None):
 
 
 def visible(c, b, at, window=0, hidden=None):
-    """Which rows [n, L + n] the tokens of sequence b (the first is token `at`) see."""
+    """Which rows [n, L + n] the tokens of sequence b (the first is token `at`) see, and how far they are."""
     L, n = c["lens"][b]
     slot = torch.arange(L + n)
     if c["anc"] is None:
@@ -173,10 +173,10 @@ def visible(c, b, at, window=0, hidden=None):
         see &= qpos[:, None] - kpos[None] < window
     for j in (hidden or {}).get(b, ()):
         see[:, j] = False
-    return see
+    return see, qpos[:, None] - kpos[None]
 
 
-def check_seen(got_out, got_lse, c, Hkv, window=0, softcap=0.0, scale=0.0, hidden=None, what=""):
+def check_seen(got_out, got_lse, c, Hkv, window=0, softcap=0.0, slopes=None, scale=0.0, hidden=None, what=""):
     """Outputs against 64 bits, held to what each token sees: rows that it does not see have no say in its bound,
     whatever their size.  As check_attn_q8 has it, with keys exact (a key is held over no other's size), and
     p_j 2^t_j, a probability (its row's largest is 1) times its V row's power of two, is rounded to fp16 times 2^6, so
@@ -192,13 +192,15 @@ def check_seen(got_out, got_lse, c, Hkv, window=0, softcap=0.0, scale=0.0, hidde
     for b, (L, n) in enumerate(c["lens"]):
         if n == 0:
             continue
-        see = visible(c, b, at, window, hidden)
+        see, dist = visible(c, b, at, window, hidden)
         kh, vh = (r.double()[:, heads].transpose(0, 1) for r in c["rows"][b])
         q = c["q"][at:at + n].cpu().double().transpose(0, 1)
         x = scale * q @ kh.transpose(1, 2)
         mag = (see * (scale * q.abs() @ kh.abs().transpose(1, 2))).amax(2)
         if softcap:
             x = softcap * torch.tanh(x / softcap)
+        if slopes is not None:
+            x = x - slopes.double().cpu()[:, None, None] * dist.double()
         x = torch.where(see, x, torch.full_like(x, -float("inf")))
         lse = torch.logsumexp(x, 2)
         p = torch.exp(x - torch.where(torch.isfinite(lse), lse, torch.zeros_like(lse))[..., None])

@@ -664,3 +664,23 @@ def test_a_value_that_is_no_number_beside_scales_of_any_size(tv, fmt, n):
         sees = torch.tensor(sees, device="cuda:0")
         assert not any(status) and torch.equal(lse, want[1])
         assert bool(out[sees].isnan().all()) and same_bits(out[~sees], want[0][~sees]), byte
+
+
+@pytest.mark.parametrize("kw", KINDS)
+@pytest.mark.parametrize("lens,tree", [([(200, 1), (0, 1), (150, 4)], False), ([(300, 90), (0, 40), (77, 1)], False),
+                                       ([(260, 70), (0, 9), (129, 1)], True), ([(500, 3), (64, 4)], True)])
+@pytest.mark.parametrize("Hq,Hkv,D,fmt,dtype", [(8, 2, 128, "e4m3", "bf16"), (4, 4, 64, "int8", "bf16")])
+@pytest.mark.parametrize("side", ["k", "v", "both"])
+def test_score_kinds_over_rows_of_all_sizes(tv, kw, lens, tree, Hq, Hkv, D, fmt, dtype, side):
+    """Rows that some tokens see and others do not, 2^40 of the others, and tiny ones among them."""
+    kw = dict(kw)
+    if kw.get("slopes"):
+        kw["slopes"] = slopes_of(Hq)
+    c = make_q8(9, lens, Hq, Hkv, D, 16, fmt, dtype, tree=tree, spread=0.7)
+    for b, (L, n) in enumerate(lens):
+        for j, bits in ((L + n - 1, 40), (max(0, L - 60), 40), (L // 2, -30), (L // 3, -30)):
+            k, v = (r[j:j + 1] * 2.0**bits for r in c["rows"][b])
+            set_rows(c, b, j, k=k if side != "v" else None, v=v if side != "k" else None)
+    out, lse, status = run(tv, c, **kw)
+    assert not any(status)
+    check_seen(out, lse, c, Hkv, **kw)
