@@ -226,18 +226,8 @@ __device__ __forceinline__ int2 scale_range(const uint8_t* scale, int z0, int z1
 constexpr int kHasNaN = 1 << 16, kApart = 1 << 17, kExpMask = 0xffff;
 constexpr int kNoRef = -1, kFarRef = -2;  // no row yet; apart to the part's end
 __device__ __forceinline__ int span_of(bool v) { return v ? q8::kNear - 1 : 15; }
-// Whether all rows of a tile are within the reach of ref (by a whole warp).
-__device__ __forceinline__ bool near_ref(const uint8_t* scale, int ref, bool v) {
-  const uint32_t s4 = reinterpret_cast<const uint32_t*>(scale)[threadIdx.x & 31];
-  const int low = ref - span_of(v);
-  unsigned off = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) off = max(off, (unsigned)((int)__byte_perm(s4, 0, 0x4440 + i) - low));
-  return __all_sync(0xffffffffu, off <= (unsigned)(ref + 1 - low) && ref < 254);
-}
-// What a tile is held over, and ref from then on (by a whole warp; a function of its own, as few tiles need it: with
-// the largest and the smallest scale of every tile looked for in the loop 16 trees of 64 took 106 to 108 us).
-__device__ __noinline__ int2 look_closer(uint8_t* scale, int z0, int z1, bool v, int ref, volatile uint32_t* words) {
+// What a tile is held over, and ref from then on (by a whole warp).
+__device__ __forceinline__ int2 held_at(uint8_t* scale, int z0, int z1, bool v, int ref, volatile uint32_t* words) {
   uint32_t nan4;
   const int2 range = scale_range(scale, z0, z1, nan4);  // (0, 255): no row is a number
   const int to = ref == kNoRef ? min(range.x + 1, 254) : ref;
@@ -682,14 +672,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
       const uint32_t st = isV ? j % kVStages : j % kKStages, ph = (isV ? j / kVStages : j / kKStages) & 1;
       if (!warp_wait(&full[st], ph, p.wait_limit)) return false;
       uint8_t* scale = isV ? s_vscale[Q8 ? st : 0] : s_kscale[Q8 ? j % kExpRing : 0];
-      if (first) ref = kNoRef;
-      int over = ref;
-      if (z0 > 0 || z1 < kTcKeys || ref < 0 || !near_ref(scale, ref, isV)) {
-        const int2 at = look_closer(scale, z0, z1, isV, ref, s_vnan[Q8 ? j % kExpRing : 0]);
-        over = at.x;
-        ref = at.y;
-      }
-      if (lane == 0) (isV ? s_vexp : s_kexp)[Q8 ? j % kExpRing : 0] = over;
+      const int2 at = held_at(scale, z0, z1, isV, first ? kNoRef : ref, s_vnan[Q8 ? j % kExpRing : 0]);
+      ref = at.y;
+      if (lane == 0) (isV ? s_vexp : s_kexp)[Q8 ? j % kExpRing : 0] = at.x;
       __syncwarp();
       if (lane == 0) mbar_arrive((isV ? bar_v_scale : bar_k_scale) + st);
       return true;
