@@ -218,21 +218,21 @@ __device__ __forceinline__ int2 scale_range(const uint8_t* scale, int z0, int z1
   return make_int2(__reduce_max_sync(0xffffffffu, max(hi & 255u, (hi >> 8) & 255u)),
                    __reduce_min_sync(0xffffffffu, min(lo & 255u, (lo >> 8) & 255u)));
 }
-// What a tile is held over: a scale byte, ref, one above the largest of the part's first tile, for rows of up to one above
-// it and span_of below: V rows as far as a unit's rows share a power of two, K rows as far as they lose no bit in fp16.
-// Or the tile is apart: codes go on as they are, and a row of the unit takes their powers of two itself (apart_tile): where K
-// rows are further apart or one is no number, and where V rows are, then to the part's end.  kHasNaN: V rows of the tile
-// are no numbers, which are noted and taken for the zeros that their codes are.
+// What a tile is held over: a scale byte, ref, the largest of the part's first tile, for rows up to kUp above it, and
+// below it for K rows as far as they lose no bit in fp16 (15; kUp: int8's -1152 f has to be a half), for V rows as far as
+// a unit's rows share a power of two.  Or the tile is apart: codes go on as they are, and a row of the unit takes their powers
+// of two itself (apart_tile): where K rows are further apart or one is no number, and where V rows are, then to the part's
+// end.  kHasNaN: V rows of the tile are no numbers, which are noted and taken for the zeros that their codes are.
+constexpr int kUp = 4;
 constexpr int kHasNaN = 1 << 16, kApart = 1 << 17, kExpMask = 0xffff;
 constexpr int kNoRef = -1, kFarRef = -2;  // no row yet; apart to the part's end
-__device__ __forceinline__ int span_of(bool v) { return v ? q8::kNear - 1 : 15; }
 // What a tile is held over, and ref from then on (by a whole warp).
 __device__ __forceinline__ int2 held_at(uint8_t* scale, int z0, int z1, bool v, int ref, volatile uint32_t* words) {
   uint32_t nan4;
   const int2 range = scale_range(scale, z0, z1, nan4);  // (0, 255): no row is a number
-  const int to = ref == kNoRef ? min(range.x + 1, 254) : ref;
+  const int to = ref == kNoRef ? max(range.x, 1) : ref;
   int over = kApart | 1;
-  if (ref != kFarRef && range.x <= to + 1 && range.y >= to - span_of(v)) {
+  if (ref != kFarRef && range.x <= to + kUp && range.y >= to - (v ? q8::kNear - kUp : 15)) {
     over = to;
     if (range.y < q8::kNaN) ref = to;
   } else if (v) {

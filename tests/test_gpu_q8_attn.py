@@ -684,3 +684,18 @@ def test_score_kinds_over_rows_of_all_sizes(tv, kw, lens, tree, Hq, Hkv, D, fmt,
     out, lse, status = run(tv, c, **kw)
     assert not any(status)
     check_seen(out, lse, c, Hkv, **kw)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("side", ["k", "v"])
+def test_rows_at_the_ends_of_what_shares_a_power_of_two(tv, fmt, n, side):
+    """Rows of the other tiles some powers of two above or below those of the last."""
+    for bits in (-17, -16, -15, -14, -10, -9, -8, -7, -6, -5, -4, 1, 2, 3, 4, 5, 6, 8, 9, 10, 12):
+        c = make_q8(5, [(700, n), (390, n)], 4, 2, 128, 16, fmt, spread=0.0, q_mag=0.1 if bits < 6 else 2.0**-bits)
+        for b, (L, _) in enumerate(c["lens"]):
+            r = c["rows"][b][0 if side == "k" else 1]
+            set_rows(c, b, 0, **{side: torch.cat([r[:L - 200] * 2.0**bits, r[L - 200:]])})
+        out, lse, status = run(tv, c)
+        assert not any(status)
+        check_seen(out, lse, c, 2, what=f"{bits}")
