@@ -705,7 +705,8 @@ tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_st
  * rows as in tv_attn_paged; out and lse are over both.  Rows of a prefix that no token of its group sees may hold
  * anything; a row of V that one of them sees and another does not must be finite.  Sequences before the first group or behind the last
  * have no prefix.  No page need be held twice: to tv_page_map a prefix is a sequence of its
- * own, with its own table row, that grows once and is released when its last user is.
+ * own, with its own table row, that grows once and is released when its last user is.  For few short sequences
+ * (three behind 500 rows 16.4 us, 10.5 over rows of their own) it saves pages, not time.
  *
  *   prefix_table int32 [groups, prefix_P]; prefix_len int32 [groups]; group_start int32 [groups + 1], ascending
  *               from 0 or more to B or less.  groups = 0: as tv_attn_paged (the three are not read then).
@@ -715,8 +716,9 @@ tv_status tv_attn_paged(const void* q, int64_t q_token_stride, int64_t q_head_st
  *               prefix_len < 0 or past prefix_P * page_size (the prefix then counts as hidden), or with a
  *               page id outside [0, num_pages) among the prefix's pages that the window reaches (its rows count
  *               as hidden).
- *   workspace   tv_attn_paged_prefix_workspace_size() bytes (32-bit rows of what a token sees in its prefix
- *               and in its own rows, before they are joined, among it), otherwise as tv_attn_paged's.
+ *   workspace   tv_attn_paged_prefix_workspace_size() bytes (beside what tv_attn_paged takes for large chunks,
+ *               8 T Hq (D + 2) for 32-bit rows of what a token sees in its prefix and in its own rows, before
+ *               they are joined, and 32 T Hkv; 8,192 tokens of 32 heads of 128: 275 MB), otherwise as tv_attn_paged's.
  * The other arguments, statuses and limits are tv_attn_paged's; groups <= 4096, groups * prefix_P and
  * (P + prefix_P) * page_size + 512 below 2^31.
  */
@@ -813,7 +815,14 @@ tv_status tv_paged_read_q8(const tv_q8_cache* cache, const int32_t* block_table,
  *   - the workspace is tv_attn_paged_q8_workspace_size() bytes;
  *   - a row of V whose scale is 255 makes the outputs of the tokens that see it NaN, and no others';
  *   - codes are ones that tv_paged_append_q8 writes: what a token gets that sees one of e4m3's NaN codes is
- *     undefined.
+ *     undefined;
+ *   - what is rounded: a query row to fp16 over a power of two of its largest element (a bf16 element below 2^-14
+ *     of that is off by up to 2^-25 of it, the others are exact), and each probability times its V row's power of two
+ *     to fp16 (by 2^-11 of it, or, where that is more, by 2^-21 of the token's largest probability times |v|).  Rows
+ *     that a token does not see have no say in it, and codes and scales are exact whatever the rows' sizes;
+ *   - time: in units of more than 16 rows (new tokens of a sequence times Hq / Hkv) a tile of 128 keys takes longer than
+ *     over a 16-bit cache (a chunk of 2,048 behind 6,100 keys 234 us for 157), and 3 to 4 times that where V rows are
+ *     more than 2^4 above or 2^5 below the largest of a share's last tile, or K rows 2^4 above or 2^15 below.
  */
 size_t tv_attn_paged_q8_workspace_size(int max_q, int Hq, int Hkv, int D);
 tv_status tv_attn_paged_q8(const void* q, int64_t q_token_stride, int64_t q_head_stride,

@@ -17,8 +17,8 @@
 //   warp 11         walks the share and publishes its parts; the parts' Q rows;
 //   warps 12-19     over an 8-bit cache: tiles of codes, which land in the second half of their
 //                   stage, become fp16 tiles in place (warps 8 and 10 look at their scales ahead of that).
-// 8-bit tiles take 4,400 cycles (the section on them tells why): 16 trees of 64 nodes 101 us with e4m3 and 103 with int8, a
-// chunk of 2,048 behind 6,100 keys 226 and 235 us.
+// 8-bit tiles take 4,400 cycles (the section on them tells why): 16 trees of 64 nodes 102 us with e4m3 and 104 with int8, a
+// chunk of 2,048 behind 6,100 keys 234 and 241 us, where a 16-bit cache takes 76 and 157.
 // The products are issued in the order PV_0(t), S_0(t + 1), PV_1(t), S_1(t + 1): while one row
 // block's softmax runs, the tensor core works on the other's.  S_r(t + 1) may
 // overwrite P_r(t), as products retire in issue order.  The next unit's first S
@@ -493,10 +493,10 @@ __device__ __noinline__ ApartRow apart_tile(const PagedAttnParams& p, const Part
 // their own, and rolled loops wherever a warp does not wait for them: a loop over the tiles that is
 // larger than the instruction cache (some 32 KB) runs at half the speed.
 // PRE: of a call with shared prefixes: a part may be a prefix's, and rows are left as they are.
-// Q8: over an 8-bit cache: warps 12-19 convert tiles (convert_rows) to fp16: K's over a power of two of the tile's, V's
-// over one that grows with the unit's scales.  bf16 queries become fp16 over a power of two of their row
-// (as_halves).  Scores take the powers of two of q and K with their scale, O's is V's, and P is fp16 with six more bits
-// of range below.
+// Q8: over an 8-bit cache: warps 12-19 convert tiles (convert_rows) to fp16, over a power of two of the part's K or V rows
+// (held_at); from a tile on whose rows are too far apart for one, apart_tile takes the softmax.  bf16 queries become fp16
+// over a power of two of their row (as_halves).  Scores take the powers of two of q and K with their scale, O's is V's, and P
+// is fp16 with six more bits of range below.
 template <int D, bool F16, bool CAP, bool BIAS, bool PRE, bool Q8>
 __global__ void __launch_bounds__(Q8 ? kTcThreads + kConvertThreads : kTcThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,

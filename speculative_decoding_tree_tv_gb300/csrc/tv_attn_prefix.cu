@@ -9,9 +9,9 @@
 // 8,000 rows).  As two passes, own rows behind the prefixes' joined ones, that took 71 us.
 //
 // Bound by latency: a prefix has few bytes when it is read once.  64 decode tokens behind 8,000 rows with 30 to 600 of
-// their own take 45 us (floor 16): the share is known at 3.4 us, the first product issued at 8, the first tile done at
+// their own take 46 us (floor 16): the share is known at 3.4 us, the first product issued at 8, the first tile done at
 // 12.5 (its code is new to the SM), then 1.9 us a tile, and 9 us for the rows' stores and their joining.  Trees of 16 to
-// 48 nodes behind four prompts take 27 us, three short sequences 17.
+// 48 nodes behind four prompts take 27 us, three short sequences 16.5.
 #define TV_UNIT 17
 #include "tv_attn_paged_tc.cuh"
 

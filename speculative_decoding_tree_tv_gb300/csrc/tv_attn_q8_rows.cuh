@@ -16,10 +16,10 @@
 // pairs for 16-bit values, so a lane gets dims 4c .. 4c + 3 of a key, which serve as the mma's k = 2c, 2c + 1,
 // 2c + 8, 2c + 9 (q' in the same order), and of V, transposed, dims 2g and 2g + 1 of keys 2c and 2c + 1.
 //
-// Bound by HBM, 2 D + 2 bytes a key: a decode of 64 sequences of 512 to 8,192 keys (8 kv heads, D 128) takes 110 us
-// with e4m3, 84 % of the copy rate (7 us of it the merge, some 8 the start and the drain; 186 us over 16 bits), and 125 us
+// Bound by HBM, 2 D + 2 bytes a key: a decode of 64 sequences of 512 to 8,192 keys (8 kv heads, D 128) takes 108 us
+// with e4m3, 85 % of the copy rate (7 us of it the merge, some 8 the start and the drain; 186 us over 16 bits), and 121 us
 // with int8, whose codes take more instructions on their way to fp16.  At D 64, where a key has half the bytes and the
-// same scores to turn into probabilities, 91 us (51 %).
+// same scores to turn into probabilities, 89 us (52 %).  V rows too far apart for one power of two: 134 us.
 #pragma once
 
 #include <cfloat>

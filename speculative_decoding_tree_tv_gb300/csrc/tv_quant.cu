@@ -108,7 +108,7 @@ cudaError_t launch_append(const AppendQ8Params& p, int U, unsigned blocks, cudaS
 // A CTA takes `tokens` consecutive tokens: a thread each finds its token's sequence (a binary search of
 // the starts) and row, then all stream the rows, 16 codes a step, four steps in flight (two take as long, eight
 // 103 us for the 85 that four took then: fewer warps).  Bound by HBM (3 D + 1 bytes a row): 16 sequences of 512 to 8,192
-// tokens, 8 heads of 128, take 73 us, 87 % of the copy rate; 84.5 us while each step divided for its place and
+// tokens, 8 heads of 128, take 73 us, 86 % of the copy rate; 84.5 us while each step divided for its place and
 // every value was held against the type's largest.
 constexpr int kReadTokens = 32, kReadFlight = 4;
 
