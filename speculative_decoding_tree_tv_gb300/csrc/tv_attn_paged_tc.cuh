@@ -974,6 +974,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         if (lane == 0) s_ring.done(n);
         continue;
       }
+      if (Q8 && (tl >= nb || rb * nb + tl >= w.ntok)) qf = FLT_MIN;  // (its scores are not to be large ones, see below)
       // rows past the unit take the last token's mask: computed, never written
       const int i = w.first + min(rb * nb + min(tl, nb - 1), w.ntok - 1);
       const bool warp_works = warp_in_block && rb * nb + (warp & 3) * 32 / p.G < w.ntok;
@@ -1160,7 +1161,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__
         }
         const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
         const float tmag = fabsf(tmax);
-        if ((Q8 || PRE) && !CAP && __any_sync(0xffffffffu, tmag > 0x1p22f && tmag < INFINITY)) {
+        if ((Q8 || PRE) && !CAP &&
+            __any_sync(0xffffffffu, tmag > 0x1p22f && tmag < INFINITY && (Q8 || (tl < nb && rb * nb + tl < w.ntok)))) {
           // Scores so large that a rounding of the maximum is a power of two or more: the products are rounded
           // like it, ahead of the difference (fused, the largest could end far above 0).  (Of an 8-bit cache
           // apart_tile does, while TMEM still has them as they were.)

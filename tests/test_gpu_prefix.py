@@ -458,3 +458,17 @@ def test_whatever_the_workspace_held(tv, n, first):
         out, lse, status = run(tv, c, ws=ws)
         assert not any(status)
         assert same_bits(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (7, 1)])
+def test_other_groups_queries_change_no_bit(tv, Hq, Hkv):
+    """Rows of a block that are another group's or sequence's, whatever their size."""
+    groups = [(300, [(40, 20), (7, 3)]), (500, [(20, 30)])]
+    c = shared(3, groups, Hq, Hkv, 128, 16)
+    want = run(tv, c)
+    c["q"] = c["q"].clone()
+    for size in (2.0**30, 2.0**100):
+        c["q"][23:] = torch.randn(c["q"][23:].shape, generator=torch.Generator().manual_seed(1)).to(c["q"]) * size
+        out, lse, status = run(tv, c)
+        assert not any(status)
+        assert same_bits(out[:23], want[0][:23]) and torch.equal(lse[:23], want[1][:23])

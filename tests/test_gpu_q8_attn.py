@@ -699,3 +699,21 @@ def test_rows_at_the_ends_of_what_shares_a_power_of_two(tv, fmt, n, side):
         out, lse, status = run(tv, c)
         assert not any(status)
         check_seen(out, lse, c, 2, what=f"{bits}")
+
+
+@pytest.mark.parametrize("lens", [[(300, 40), (50, 30)], [(300, 70), (700, 9), (20, 33)]])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (7, 1)])
+def test_other_sequences_queries_change_no_bit(tv, lens, dtype, Hq, Hkv):
+    """Rows of a block that are another sequence's, whatever their size."""
+    c = make_q8(3, lens, Hq, Hkv, 128, 16, "e4m3", dtype)
+    want = run(tv, c)
+    n = lens[0][1]
+    c["q"] = c["q"].clone()
+    for size in (2.0**30, 2.0**100) if dtype == "bf16" else (2.0**13,):
+        c["q"][n:] = torch.randn(c["q"][n:].shape, generator=torch.Generator().manual_seed(1)).to(c["q"]) * size
+        if dtype == "fp16":
+            c["q"][n:] = c["q"][n:].clamp(-6e4, 6e4)
+        out, lse, status = run(tv, c, scale=0.0)
+        assert not any(status)
+        assert same_bits(out[:n], want[0][:n]) and torch.equal(lse[:n], want[1][:n])
