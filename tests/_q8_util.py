@@ -208,6 +208,8 @@ def check_seen(got_out, got_lse, c, Hkv, window=0, softcap=0.0, slopes=None, sca
         top = torch.where(see, x.abs(), torch.zeros_like(x)).amax(2)
         xerr = (2.0**-23 * ((D + 4) * mag + 4 * torch.minimum(top, 2 * mag + 40) + 8 * softcap)
                 + scale * 2.0**-25 * q.abs().amax(2) * (see * kh.abs().sum(2)[:, None]).amax(2))
+        if slopes is not None:  # (a key's bias is counted on from its tile's first key, up to 127 on: three roundings of that)
+            xerr = xerr + 3 * 2.0**-24 * 128 * slopes.double().cpu()[:, None]
         vmax = vh.abs().amax(2)[:, None]
         far = see.sum(1) * 2.0**-21 * (p * vmax).amax(2)
         tol = (spread * (2.0**-11 + 2 * xerr[..., None] + 2.0**-19) + far[..., None]

@@ -717,3 +717,15 @@ def test_other_sequences_queries_change_no_bit(tv, lens, dtype, Hq, Hkv):
         out, lse, status = run(tv, c, scale=0.0)
         assert not any(status)
         assert same_bits(out[:n], want[0][:n]) and torch.equal(lse[:n], want[1][:n])
+
+
+def test_rows_of_all_sizes_where_ctas_join_units_themselves(tv):
+    lens = [(500 + 23 * i, 64) for i in range(45)]
+    c = make_q8(5, lens, 8, 2, 64, 64, "e4m3", tree=True, spread=0.7)
+    for b, (L, n) in enumerate(lens):
+        k, v = c["rows"][b]
+        set_rows(c, b, L + n - 1, v=v[L + n - 1:] * 2.0**40)
+        set_rows(c, b, L // 2, k=k[L // 2:L // 2 + 1] * 2.0**-30, v=v[L // 2:L // 2 + 1] * 2.0**-30)
+    out, lse, status = run(tv, c)
+    assert not any(status)
+    check_seen(out, lse, c, 2)
