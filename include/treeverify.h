@@ -821,7 +821,7 @@ tv_status tv_paged_read_q8(const tv_q8_cache* cache, const int32_t* block_table,
  *     to fp16 (by 2^-11 of it, or, where that is more, by 2^-21 of the token's largest probability times |v|).  Rows
  *     that a token does not see have no say in it, and codes and scales are exact whatever the rows' sizes;
  *   - time: in units of more than 16 rows (new tokens of a sequence times Hq / Hkv) a tile of 128 keys takes longer than
- *     over a 16-bit cache (a chunk of 2,048 behind 6,100 keys 234 us for 157), and 3 to 4 times that where V rows are
+ *     over a 16-bit cache (a chunk of 2,048 behind 6,100 keys 236 us for 157), and 3 to 4 times that where V rows are
  *     more than 2^4 above or 2^5 below the largest of a share's last tile, or K rows 2^4 above or 2^15 below.
  */
 size_t tv_attn_paged_q8_workspace_size(int max_q, int Hq, int Hkv, int D);

@@ -297,6 +297,7 @@ __device__ __forceinline__ int prefix_reach(const PagedAttnParams& p, int g, int
 __device__ __forceinline__ Seq load_own(const PagedAttnParams& p, int b) {
   Seq s;
   s.shared = false;
+  s.lo = 0;
   s.L = __ldg(p.kv_len + b);
   if (!seq_range(p.q_start, b, p.T, s.t0, s.n)) s.n = 0;
   s.bad = s.L < 0 || (long long)s.L + s.n > ((long long)p.P << p.page_shift) ||
@@ -453,8 +454,8 @@ __device__ __noinline__ int first_malformed(const PagedAttnParams& p) {
   return s_first;
 }
 
-// Finds this CTA's share (s_cur: shared; rest is 0 where there is none).  All THREADS threads call it;
-// ends with a barrier; returns the groups that count.  Where sequences are few and chunks long, 2^share_lanes lanes share one's query tiles
+// Finds this CTA's share (s_cur: shared; rest is 0 where there is none); returns the groups that count.  All THREADS
+// threads call it; ends with a barrier.  Where sequences are few and chunks long, 2^share_lanes lanes share one's query tiles
 // (a lane that walked the 32 of a chunk of 2048 alone held up the first tile by some 3,000 cycles).
 template <int KT, int THREADS, bool PRE>
 __device__ __forceinline__ int find_share(const PagedAttnParams& p, Cursor<KT, PRE>& s_cur) {

@@ -17,8 +17,8 @@
 //   warp 11         walks the share and publishes its parts; the parts' Q rows;
 //   warps 12-19     over an 8-bit cache: tiles of codes, which land in the second half of their
 //                   stage, become fp16 tiles in place (warps 8 and 10 look at their scales ahead of that).
-// 8-bit tiles take 4,400 cycles (the section on them tells why): 16 trees of 64 nodes 102 us with e4m3 and 104 with int8, a
-// chunk of 2,048 behind 6,100 keys 234 and 241 us, where a 16-bit cache takes 76 and 157.
+// 8-bit tiles take 4,400 cycles (the section on them tells why): 16 trees of 64 nodes 103 us with e4m3 and 104 with int8, a
+// chunk of 2,048 behind 6,100 keys 236 and 242 us, where a 16-bit cache takes 76 and 157.
 // The products are issued in the order PV_0(t), S_0(t + 1), PV_1(t), S_1(t + 1): while one row
 // block's softmax runs, the tensor core works on the other's.  S_r(t + 1) may
 // overwrite P_r(t), as products retire in issue order.  The next unit's first S

@@ -549,7 +549,7 @@ paged_rows_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_const
       float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
       for (int x = 0; x < NW; ++x) mm = fmaxf(mm, s_ml[x][row_of(r)].x);
-      f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mm) ;  // (0: nothing seen by this warp, its sums are 0)
+      f[r] = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mm);  // (0: nothing seen by this warp, its sums are 0)
       const int e = (apart ? ve[r] : vtop) - 127 - kPBias;
       f[r] *= q8::exp2_whole(e >> 1);
       vf[r] = q8::exp2_whole(e - (e >> 1));

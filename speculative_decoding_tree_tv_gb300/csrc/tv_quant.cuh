@@ -73,8 +73,8 @@ __device__ __forceinline__ float at_most(float x, float top) {
 }
 
 // While the scale bytes t_j of the V rows that a part has met lie within this of one another, all rows of the unit
-// hold their outputs over one power of two.  Beyond it each row has its own, that of its
-// largest p_j 2^t_j so far, so that V rows that it does not see, or hardly, cost it no bits.  Either way
+// hold their outputs over one power of two.  Beyond it each row has its own, that of its largest p_j 2^t_j so far, so
+// that V rows that it does not see, or hardly, cost it no bits.  Either way
 // p_j 2^t_j, rounded to fp16 times 2^6, is off by 2^-21 of the row's largest p_j |v_j| at most where it is too small for
 // half a step of its own.
 constexpr int kNear = 9;
